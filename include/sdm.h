@@ -1,7 +1,9 @@
 /*
  * sdm.h -- C ABI of the GB300 (sm_103a) hot path of the chunked sparse-delta-memory (SDM)
  * recurrence: the forward's Phase 1 and Phase-2 decay-and-write (DW), the saving forward's dense
- * snapshot, and the deterministic backward's step kernels (Phase A, GWR, GDS).
+ * snapshot, and the deterministic backward's step kernels (Phase A, GWR, GDS); and of the operators a model
+ * needs around that layer (gated linear recurrence, norm and rotation of queries and keys, token log
+ * probabilities; from their own section on).
  *
  * Definitions followed (sparse-delta-memory 2.0.0):
  *   phase1_cuda.py, module docstring ........ the Phase-1 outputs and the determinism contract
@@ -69,6 +71,9 @@ typedef enum { SDM_F32 = 0, SDM_BF16 = 1 } sdm_dtype;
 
 /* Bits of the device status word (sdm_device_status). */
 #define SDM_DEV_BAD_SLOT 0x1u /* a valid entry's slot id was outside [0, S): the entry is dropped */
+#define SDM_DEV_BAD_OFFSET 0x2u   /* sequence offsets not ascending within [0, rows]: cut to it */
+#define SDM_DEV_BAD_POSITION 0x4u /* a position at or above max_pos: treated as padding */
+#define SDM_DEV_BAD_TARGET 0x8u   /* a target at or above V: treated as ignored */
 
 typedef struct {
     int32_t P;              /* streams */
@@ -354,6 +359,159 @@ sdm_status sdm_gwr(const sdm_shape* shape, int32_t grad_dtype, const int32_t* k_
 sdm_status sdm_gds(const sdm_shape* shape, int32_t grad_dtype, const int32_t* sorted_q, const int32_t* q_idx,
                    const void* q_val, const float* log_q, const float* gr, const void* bank, void* grad, float* d_q_w,
                    int64_t step_begin, int64_t step_end, uint32_t* status, sdm_stream_t stream);
+
+/* ================================================================================================
+ * The operators around the memory: the gated linear recurrence, the norm and rotation of query and
+ * key heads, and log probabilities of tokens. They share the conventions above (caller-owned device
+ * pointers, no allocation, no synchronization, checks before any launch, every output bitwise
+ * reproducible) and differ in these:
+ *   - Row arrays take the distance between rows in elements (`*_ld`), so that a slice of a wider row
+ *     can be passed. Inputs may repeat a row (ld 0). A base and its ld are aligned to 4 elements of the
+ *     array's type unless said otherwise; small float arrays (weights, states, tables) to 16 bytes.
+ *   - An output overlaps no input unless said otherwise.
+ *   - Row counts may be 0: nothing is read or written but what is said to be.
+ *   - status (nullable): a device word to which SDM_DEV_* bits are OR-ed.
+ *   - Errors: SDM_ERR_DTYPE / SHAPE / ALIGN for the shape, SDM_ERR_ARG for a NULL array or an ld below
+ *     the row's length, SDM_ERR_ALIGN for a misaligned array or ld, SDM_ERR_WORKSPACE, SDM_ERR_CUDA.
+ * ================================================================================================ */
+
+/* Rows between two saved states of the recurrence. */
+#define SDM_GLR_CHUNK 64
+
+typedef struct {
+    int32_t P;          /* sequences */
+    int32_t D;          /* channels of a row, a multiple of 4, up to 2^20 */
+    int32_t gate_width; /* channels that share a gate: 1 (a gate per channel), or a multiple of 4 that
+                         * divides D (a gate per head of that many channels; D: one per row) */
+    int32_t x_dtype;    /* sdm_dtype of x, y and their gradients */
+    int32_t g_dtype;    /* sdm_dtype of g and dg */
+    int64_t rows;       /* rows of all sequences together */
+} sdm_glr_shape;
+
+/*
+ * The gated linear recurrence (the dense, per-channel counterpart of the memory's decay and write):
+ *   h_t = exp(g_t) h_{t-1} + x_t,   y_t = h_t rounded to x_dtype,
+ * for the rows of each sequence in order, in float32.
+ *   x, y [rows, D]; g [rows, D / gate_width]: log gates, at most 0 (a gate of -inf starts anew; with gates
+ *   above 0 the product of a span's gates may overflow). A row of per-head gates has no alignment rule.
+ *   offsets: int64 [P + 1] on the device, sequence p owns rows [offsets[p], offsets[p+1]), empty ones
+ *   allowed; or NULL: P sequences of rows / P rows each (rows a multiple of P).
+ *   h0 (nullable: zeros) and hT (nullable) float32 [P, D]: the states before and after; hT may be h0; an
+ *   empty sequence hands its state on.
+ *   states (nullable) float32, sdm_glr_states_bytes: the state before every SDM_GLR_CHUNK-th row of each
+ *   sequence, for the backward (row offsets[p] / SDM_GLR_CHUNK + p + j holds sequence p's j-th).
+ * Spans of rows are computed apart and joined in a fixed order, so a sequence cut in two calls agrees with one
+ * call to rounding, not bit for bit.
+ */
+size_t sdm_glr_states_bytes(const sdm_glr_shape* shape);
+sdm_status sdm_glr_forward(const sdm_glr_shape* shape, const void* x, int64_t x_ld, const void* g, int64_t g_ld,
+                           const int64_t* offsets, const float* h0, void* y, int64_t y_ld, float* hT, float* states,
+                           uint32_t* status, sdm_stream_t stream);
+
+/*
+ * Its backward: with l_t = dy_t + exp(g_{t+1}) l_{t+1} (past a sequence's end: dhT, or 0 where NULL),
+ *   dx_t = l_t,   dg_t = exp(g_t) l_t h_{t-1} (summed over the gate's channels),   dh0 = exp(g_1) l_1
+ * (dhT for an empty sequence). h_{t-1} is computed again from x and the forward's states, so the rounding of
+ * y enters no gradient. x, g, offsets as the forward had them; dy, dx [rows, D]; dg [rows, D / gate_width];
+ * dhT, dh0 (nullable) float32 [P, D]. ws: sdm_glr_workspace_bytes, 16-byte aligned (used where gate_width >
+ * 128; may be NULL otherwise).
+ */
+size_t sdm_glr_workspace_bytes(const sdm_glr_shape* shape);
+sdm_status sdm_glr_backward(const sdm_glr_shape* shape, const void* x, int64_t x_ld, const void* g, int64_t g_ld,
+                            const void* dy, int64_t dy_ld, const int64_t* offsets, const float* states,
+                            const float* dhT, void* dx, int64_t dx_ld, void* dg, int64_t dg_ld, float* dh0, void* ws,
+                            size_t ws_bytes, uint32_t* status, sdm_stream_t stream);
+
+/*
+ * One token of each of `rows` requests (P is not used): state[s] = exp(g_i) state[s] + x_i, y_i = state[s], with
+ * s = slots[i] (int32 [rows], distinct), or i where slots is NULL. state float32 [states, D] with rows state_ld
+ * apart. A row with a slot below 0 is padding: y_i = 0 and no state changes; so too one at or above `states`,
+ * which sets SDM_DEV_BAD_SLOT.
+ */
+sdm_status sdm_glr_step(const sdm_glr_shape* shape, const void* x, int64_t x_ld, const void* g, int64_t g_ld,
+                        const int32_t* slots, float* state, int64_t state_ld, int64_t states, void* y, int64_t y_ld,
+                        uint32_t* status, sdm_stream_t stream);
+
+typedef struct {
+    int64_t tokens;
+    int32_t q_heads;    /* heads of q and of k (either may be 0, not both) */
+    int32_t k_heads;
+    int32_t hd;         /* columns of a head, a multiple of 8, up to 1024 */
+    int32_t rot_dim;    /* the first columns that turn, a multiple of 8, 0 .. hd */
+    int32_t max_pos;    /* positions of the table */
+    int32_t layout;     /* pairs that turn together: 0 half (i, i + rot_dim / 2), 1 interleaved (2i, 2i + 1) */
+    int32_t dtype;      /* sdm_dtype of q, k, their outputs and gradients */
+    int32_t norm;       /* 1: RMS norm of each head first; 0: the rotation alone (weights unused) */
+    float eps;
+} sdm_rope_shape;
+
+/*
+ * table [max_pos, rot_dim] float32: row m holds scale cos(m f_i) for i < rot_dim / 2, then scale sin(m f_i).
+ * inv_freq: the rot_dim / 2 angles f_i of one position in radians, a HOST array read during the call. Angles are
+ * reduced exactly for every position.
+ */
+sdm_status sdm_rope_table(const sdm_rope_shape* shape, const double* inv_freq, float scale, float* table,
+                          sdm_stream_t stream);
+
+/*
+ * Per token t and head, x its row of hd columns and w the weights of its kind (float32 [hd], NULL: ones):
+ *   n = x rsqrt(mean x^2 + eps) w   (norm 0: n = x),
+ *   out_a = n_a c_i - n_b s_i, out_b = n_b c_i + n_a s_i for pair i = (a, b), c, s from the table's row
+ * positions[t]; columns from rot_dim on are n. float32 throughout, rounded once. q, q_out [tokens, q_heads, hd],
+ * k, k_out [tokens, k_heads, hd], a token's heads contiguous, tokens `*_ld` apart. positions int32 [tokens]: below 0
+ * is a padding token (its outputs are 0); at or above max_pos likewise, and sets SDM_DEV_BAD_POSITION. q_out
+ * may be q and k_out may be k (same ld).
+ */
+sdm_status sdm_qk_norm_rope(const sdm_rope_shape* shape, const void* q, int64_t q_ld, const void* k, int64_t k_ld,
+                            const int32_t* positions, const float* table, const float* wq, const float* wk, void* q_out,
+                            int64_t qo_ld, void* k_out, int64_t ko_ld, uint32_t* status, sdm_stream_t stream);
+
+/*
+ * Its backward, from the outputs' gradients and the forward's inputs: e = the gradient turned back by the angle,
+ * dw += e x r over tokens and heads (r the row's rsqrt), and with u = e w: dx = r (u - x r^2 mean(u x)). Padding
+ * tokens get zeros and add nothing. dwq, dwk float32 [hd] (nullable), written; ws: sdm_rope_workspace_bytes,
+ * 16-byte aligned (may be NULL with norm 0 or where neither is asked for). dq may be dq_out, dk may be dk_out
+ * (same ld).
+ */
+size_t sdm_rope_workspace_bytes(const sdm_rope_shape* shape);
+sdm_status sdm_qk_norm_rope_backward(const sdm_rope_shape* shape, const void* dq_out, int64_t dqo_ld,
+                                     const void* dk_out, int64_t dko_ld, const void* q, int64_t q_ld, const void* k,
+                                     int64_t k_ld, const int32_t* positions, const float* table, const float* wq,
+                                     const float* wk, void* dq, int64_t dq_ld, void* dk, int64_t dk_ld, float* dwq,
+                                     float* dwk, void* ws, size_t ws_bytes, uint32_t* status, sdm_stream_t stream);
+
+typedef struct {
+    int64_t rows;       /* tokens, below 2^31 */
+    int32_t V;          /* logits of a row, up to 2^28 */
+    int32_t K;          /* top alternatives of a row, 0 .. min(32, V) */
+    int32_t dtype;      /* sdm_dtype of logits and dlogits */
+    float scale;        /* logits are multiplied by it first (1 / temperature), 1e-3 .. 1e3 */
+} sdm_logprob_shape;
+
+/*
+ * Per row x [V] of logits (rows ld apart, no alignment rule but the element's), z = scale x:
+ *   lse = log sum exp z, logp = z_target - lse, entropy = -sum p log p with p = exp(z - lse) (0 log 0 = 0),
+ *   top_vals, top_idx [rows, K]: log probabilities and ids of the K largest logits, descending, the lower id first
+ *   among equal logits.
+ * targets int32 [rows]: below 0 is ignored (logp 0); at or above V likewise, and sets SDM_DEV_BAD_TARGET. logp
+ * float32 [rows]; entropy, lse, top_vals, top_idx nullable. A row whose logits are all -inf has lse = -inf, log
+ * probabilities -inf and entropy 0. A row that holds NaN or +inf (or a finite logit whose product with
+ * scale log2(e) overflows) has NaN for its float outputs; NaN counts as the largest logit in top_idx.
+ */
+sdm_status sdm_token_logprobs(const sdm_logprob_shape* shape, const void* logits, int64_t ld, const int32_t* targets,
+                              float* logp, float* entropy, float* lse, float* top_vals, int32_t* top_idx,
+                              uint32_t* status, sdm_stream_t stream);
+
+/*
+ * The gradient of the logits, from the forward's lse and entropy:
+ *   dlogits_v = scale (d_logp (1[v = target] - p_v) - d_entropy p_v (log p_v + entropy)),
+ * d_logp float32 [rows] (taken as 0 where the target is ignored), d_entropy float32 [rows] (nullable: zeros). In a
+ * row whose logits are all -inf every p is 0. K is not used.
+ */
+sdm_status sdm_token_logprobs_backward(const sdm_logprob_shape* shape, const void* logits, int64_t ld,
+                                       const int32_t* targets, const float* lse, const float* entropy,
+                                       const float* d_logp, const float* d_entropy, void* dlogits, int64_t d_ld,
+                                       uint32_t* status, sdm_stream_t stream);
 
 /*
  * Synchronizes `stream`, reads the workspace's device status word into *code_out (0 = fine,

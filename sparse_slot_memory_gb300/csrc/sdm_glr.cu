@@ -1,0 +1,516 @@
+// sdm_glr.cu -- the gated linear recurrence: forward, backward and the single-token step behind
+// sdm_glr_forward / sdm_glr_backward / sdm_glr_step (include/sdm.h).
+//
+// Mathematics. h_t = a_t h_{t-1} + x_t with a_t = exp(g_t). A span of rows acts on the state as the pair
+// (A, B): h_out = A h_in + B with A the product of its gates and B its result from a zero state; spans join as
+// (A2 A1, A2 B1 + B2). The backward runs the same way from the end: with l_t the gradient of h_t and
+// m_t = a_t l_t what flows to h_{t-1}, l_t = dy_t + m_{t+1}, dx_t = l_t, dg_t = m_t h_{t-1}. States, products
+// and sums are float32.
+//
+// Layout. A block owns a tile of at most 128 channels (4 per lane) of one sequence and walks it in steps of
+// kWarps * kRows rows: each warp holds kRows consecutive rows in registers, forms its pair, the warps exchange
+// pairs through shared memory and each then runs its rows from its own starting state. One pass over the data.
+#include <cuda_bf16.h>
+
+#include <algorithm>
+#include <cstring>
+#include <type_traits>
+
+#include "sdm_checks.cuh"
+#include "sdm_internal.cuh"
+#include "sdm_rows.cuh"
+
+namespace sdm {
+namespace {
+
+using namespace rows;
+
+constexpr int kRows = 8;        // rows of a warp in one step
+constexpr int kWarps = 8;       // warps of a block: kWarps * kRows rows in one step
+constexpr int kTileCols = 128;  // channels of a tile
+static_assert(kWarps * kRows == SDM_GLR_CHUNK, "a block's step is one saved state");
+
+struct GlrArgs {
+    const void* x;
+    const void* g;
+    const void* dy;
+    const int64_t* offsets;   // nullable: equal lengths
+    const float* h0;          // nullable
+    const float* dhT;         // nullable
+    float* states;            // forward: nullable
+    void* y;
+    float* hT;                // nullable
+    void* dx;
+    void* dg;
+    float* part;              // [tiles per head][rows][heads] gate gradients of a tile
+    float* dh0;               // nullable
+    uint32_t* status;         // nullable
+    int64_t rows, len;        // len: rows of every sequence where offsets is null
+    int64_t x_ld, g_ld, y_ld, dy_ld, dx_ld, dg_ld;
+    int P, D, H, gw;
+    int tiles, tile_cols, tiles_per_head, heads_per_tile;
+};
+
+// A tile's columns and this lane's place in it.
+struct Tile {
+    int col;      // the lane's first channel
+    bool on;      // whether the lane has channels
+    int gate;     // the lane's gate (head)
+    int seg;      // lanes from this one to the end of its head's part in the tile
+    int sub;      // which of its head's tiles this is
+    bool lead;    // the first lane of its head in the tile
+};
+
+template <bool PERCH>
+__device__ __forceinline__ Tile tile_of(const GlrArgs& a, int tile, int lane) {
+    Tile t;
+    int c0, n;
+    if (PERCH || a.tiles_per_head == 1) {
+        c0 = tile * a.tile_cols;
+        n = min(a.tile_cols, a.D - c0);
+        t.sub = 0;
+    } else {
+        const int head = tile / a.tiles_per_head;
+        t.sub = tile - head * a.tiles_per_head;
+        c0 = head * a.gw + t.sub * a.tile_cols;
+        n = min(a.tile_cols, (head + 1) * a.gw - c0);
+    }
+    t.on = lane * 4 < n;
+    t.col = c0 + (t.on ? lane * 4 : 0);
+    if (PERCH) {
+        t.gate = t.col;
+        t.seg = 1;
+        t.lead = false;
+    } else {
+        t.gate = t.col / a.gw;
+        const int end = min(c0 + n, (t.gate + 1) * a.gw);
+        t.seg = t.on ? (end - t.col) / 4 : 1;
+        t.lead = t.on && (t.col == c0 || t.col % a.gw == 0);
+    }
+    return t;
+}
+
+// The rows [b, b + n) of sequence p. Offsets that are not ascending within [0, rows] are cut to it and reported.
+__device__ __forceinline__ void sequence(const GlrArgs& a, int p, int64_t& b, int64_t& n) {
+    if (a.offsets == nullptr) {
+        b = p * a.len;
+        n = a.len;
+        return;
+    }
+    const int64_t lo = __ldg(a.offsets + p), hi = __ldg(a.offsets + p + 1);
+    b = min(max(lo, int64_t(0)), a.rows);
+    n = max(min(hi, a.rows) - b, int64_t(0));
+    if ((lo < 0 || hi > a.rows || lo > hi) && a.status != nullptr && threadIdx.x == 0) atomicOr(a.status, SDM_DEV_BAD_OFFSET);
+}
+
+// exp of the lane's gates of one row
+template <bool PERCH, typename GT>
+__device__ __forceinline__ void gates(const GT* g, float (&o)[4]) {
+    if constexpr (PERCH) {
+        ld4(g, o);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] = expf(o[i]);
+    } else {
+        o[0] = o[1] = o[2] = o[3] = expf(widen(__ldg(g)));
+    }
+}
+
+__device__ __forceinline__ void set4(float (&o)[4], float v) { o[0] = o[1] = o[2] = o[3] = v; }
+
+// h = A h + B from a warp's pair in shared memory
+__device__ __forceinline__ void join(float (&h)[4], const float* A, const float* B) {
+    float p[4], q[4];
+    get4(A, p);
+    get4(B, q);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) h[i] = fmaf(p[i], h[i], q[i]);
+}
+
+template <typename XT, typename GT, bool PERCH>
+__global__ void __launch_bounds__(kWarps * 32) glr_fwd_kernel(const GlrArgs a) {
+    __shared__ __align__(16) float sA[2][kWarps][kTileCols], sB[2][kWarps][kTileCols];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    const int p = blockIdx.x / a.tiles;
+    const Tile tl = tile_of<PERCH>(a, blockIdx.x - p * a.tiles, lane);
+    int64_t b, n;
+    sequence(a, p, b, n);
+    float h[4] = {0.f, 0.f, 0.f, 0.f};   // the state before the step's rows
+    if (a.h0 != nullptr) ld4(a.h0 + static_cast<int64_t>(p) * a.D + tl.col, h);
+    const XT* const x = static_cast<const XT*>(a.x) + b * a.x_ld + tl.col;
+    const GT* const g = static_cast<const GT*>(a.g) + b * a.g_ld + tl.gate;
+    XT* const y = static_cast<XT*>(a.y) + b * a.y_ld + tl.col;
+    float* const st = a.states == nullptr ? nullptr : a.states + (b / SDM_GLR_CHUNK + p) * a.D + tl.col;
+    int buf = 0;
+    for (int64_t t0 = 0; t0 < n; t0 += kWarps * kRows, buf ^= 1) {
+        if (st != nullptr && w == 0 && tl.on) st4(st + t0 / SDM_GLR_CHUNK * a.D, h);
+        const int64_t t = t0 + w * kRows;
+        float ga[kRows][4], xv[kRows][4], A[4], B[4];
+        set4(A, 1.f);
+        set4(B, 0.f);
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+            if (t + i < n) {
+                gates<PERCH>(g + (t + i) * a.g_ld, ga[i]);
+                ld4(x + (t + i) * a.x_ld, xv[i]);
+            } else {   // past the end: the identity
+                set4(ga[i], 1.f);
+                set4(xv[i], 0.f);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kRows; ++i)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                A[c] *= ga[i][c];
+                B[c] = fmaf(ga[i][c], B[c], xv[i][c]);
+            }
+        st4(&sA[buf][w][lane * 4], A);
+        st4(&sB[buf][w][lane * 4], B);
+        __syncthreads();   // the other buffer is written next: one barrier a step
+        float hw[4];
+        for (int j = 0; j < kWarps; ++j) {
+            if (j == w)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) hw[c] = h[c];
+            join(h, &sA[buf][j][lane * 4], &sB[buf][j][lane * 4]);
+        }
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) hw[c] = fmaf(ga[i][c], hw[c], xv[i][c]);
+            if (tl.on && t + i < n) st4(y + (t + i) * a.y_ld, hw);
+        }
+    }
+    if (a.hT != nullptr && w == 0 && tl.on) st4(a.hT + static_cast<int64_t>(p) * a.D + tl.col, h);
+}
+
+// The sum of v over the lanes of its head in the tile, in the head's first lane.
+__device__ __forceinline__ float head_sum(float v, int seg) {
+#pragma unroll
+    for (int k = 1; k < 32; k <<= 1) {
+        const float o = __shfl_down_sync(kFull, v, k);
+        if (k < seg) v += o;   // lane + k lies in the same head
+    }
+    return v;
+}
+
+template <typename XT, typename GT, bool PERCH>
+__global__ void __launch_bounds__(kWarps * 32) glr_bwd_kernel(const GlrArgs a) {
+    __shared__ __align__(16) float sA[2][kWarps][kTileCols], sF[2][kWarps][kTileCols], sR[2][kWarps][kTileCols];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    const int p = blockIdx.x / a.tiles;
+    const Tile tl = tile_of<PERCH>(a, blockIdx.x - p * a.tiles, lane);
+    int64_t b, n;
+    sequence(a, p, b, n);
+    float m[4] = {0.f, 0.f, 0.f, 0.f};   // the gradient of the state after the step's rows
+    if (a.dhT != nullptr) ld4(a.dhT + static_cast<int64_t>(p) * a.D + tl.col, m);
+    const XT* const x = static_cast<const XT*>(a.x) + b * a.x_ld + tl.col;
+    const GT* const g = static_cast<const GT*>(a.g) + b * a.g_ld + tl.gate;
+    const XT* const dy = static_cast<const XT*>(a.dy) + b * a.dy_ld + tl.col;
+    XT* const dx = static_cast<XT*>(a.dx) + b * a.dx_ld + tl.col;
+    GT* const dg = static_cast<GT*>(a.dg) + b * a.dg_ld + tl.gate;
+    const float* const st = a.states + (b / SDM_GLR_CHUNK + p) * a.D + tl.col;
+    int buf = 0;
+    for (int64_t k = (n + SDM_GLR_CHUNK - 1) / SDM_GLR_CHUNK - 1; k >= 0; --k, buf ^= 1) {
+        const int64_t t = k * SDM_GLR_CHUNK + w * kRows;
+        float ga[kRows][4], xv[kRows][4], dv[kRows][4], A[4], F[4], R[4], h[4];
+        ld4(st + k * a.D, h);
+        set4(A, 1.f);
+        set4(F, 0.f);
+        set4(R, 0.f);
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+            if (t + i < n) {
+                gates<PERCH>(g + (t + i) * a.g_ld, ga[i]);
+                ld4(x + (t + i) * a.x_ld, xv[i]);
+                ld4(dy + (t + i) * a.dy_ld, dv[i]);
+            } else {
+                set4(ga[i], 1.f);
+                set4(xv[i], 0.f);
+                set4(dv[i], 0.f);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kRows; ++i)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                A[c] *= ga[i][c];
+                F[c] = fmaf(ga[i][c], F[c], xv[i][c]);
+                R[c] = ga[kRows - 1 - i][c] * (dv[kRows - 1 - i][c] + R[c]);
+            }
+        st4(&sA[buf][w][lane * 4], A);
+        st4(&sF[buf][w][lane * 4], F);
+        st4(&sR[buf][w][lane * 4], R);
+        __syncthreads();
+        float mw[4];
+        for (int j = 0; j < w; ++j) join(h, &sA[buf][j][lane * 4], &sF[buf][j][lane * 4]);
+        for (int j = kWarps - 1; j >= 0; --j) {
+            if (j == w)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) mw[c] = m[c];
+            join(m, &sA[buf][j][lane * 4], &sR[buf][j][lane * 4]);
+        }
+        // xv becomes the state before each row
+#pragma unroll
+        for (int i = 0; i < kRows; ++i)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                const float next = fmaf(ga[i][c], h[c], xv[i][c]);
+                xv[i][c] = h[c];
+                h[c] = next;
+            }
+#pragma unroll
+        for (int i = kRows - 1; i >= 0; --i) {
+            float l[4], d[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                l[c] = dv[i][c] + mw[c];
+                mw[c] = ga[i][c] * l[c];
+                d[c] = mw[c] * xv[i][c];
+            }
+            const bool live = t + i < n;
+            if (tl.on && live) st4(dx + (t + i) * a.dx_ld, l);
+            if constexpr (PERCH) {
+                if (tl.on && live) st4(dg + (t + i) * a.dg_ld, d);
+            } else {
+                const float s = head_sum(tl.on ? (d[0] + d[1]) + (d[2] + d[3]) : 0.f, tl.seg);
+                if (tl.lead && live) {
+                    if (a.tiles_per_head == 1)
+                        st1(dg + (t + i) * a.dg_ld, s);
+                    else
+                        a.part[(tl.sub * a.rows + b + t + i) * a.H + tl.gate] = s;
+                }
+            }
+        }
+    }
+    if (a.dh0 != nullptr && w == 0 && tl.on) st4(a.dh0 + static_cast<int64_t>(p) * a.D + tl.col, m);
+}
+
+// dg of a head wider than a tile: the sum of its tiles' parts, in tile order.
+template <typename GT>
+__global__ void __launch_bounds__(256) glr_dg_kernel(const GlrArgs a) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int64_t n = a.rows * a.H;
+    for (int64_t i = blockIdx.x * int64_t(256) + threadIdx.x; i < n; i += gridDim.x * int64_t(256)) {
+        float s = a.part[i];
+        for (int k = 1; k < a.tiles_per_head; ++k) s += a.part[k * n + i];
+        st1(static_cast<GT*>(a.dg) + i / a.H * a.dg_ld + i % a.H, s);
+    }
+}
+
+struct StepArgs {
+    const void* x;
+    const void* g;
+    const int32_t* slots;   // nullable: row i uses state i
+    float* state;
+    void* y;
+    uint32_t* status;
+    int64_t x_ld, g_ld, y_ld, s_ld;
+    int64_t units;          // rows * (D / 4)
+    int64_t states;
+    int D, gw;
+};
+
+template <typename XT, typename GT, bool PERCH>
+__global__ void __launch_bounds__(256) glr_step_kernel(const StepArgs a) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int64_t u = blockIdx.x * int64_t(256) + threadIdx.x;
+    if (u >= a.units) return;
+    const int quads = a.D / 4;
+    const int64_t r = u / quads;
+    const int col = static_cast<int>(u - r * quads) * 4;
+    const int64_t s = a.slots == nullptr ? r : static_cast<int64_t>(__ldg(a.slots + r));
+    float x[4], ga[4], h[4];
+    XT* const y = static_cast<XT*>(a.y) + r * a.y_ld + col;
+    if (s < 0 || s >= a.states) {   // a padding row, or an id that names no state
+        if (s >= a.states && a.status != nullptr) atomicOr(a.status, kDevBadSlot);
+        set4(h, 0.f);
+        st4(y, h);
+        return;
+    }
+    float* const st = a.state + s * a.s_ld + col;
+    ld4cg(st, h);
+    ld4(static_cast<const XT*>(a.x) + r * a.x_ld + col, x);
+    gates<PERCH>(static_cast<const GT*>(a.g) + r * a.g_ld + (PERCH ? col : col / a.gw), ga);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) h[c] = fmaf(ga[c], h[c], x[c]);
+    st4(st, h);
+    st4(y, h);
+}
+
+// ---- host side ------------------------------------------------------------------------------------
+using checks::aligned16;
+
+int elem(int dtype) { return dtype == SDM_BF16 ? 2 : 4; }
+
+sdm_status check(const sdm_glr_shape* s) {
+    if (s == nullptr) return SDM_ERR_ARG;
+    if (s->x_dtype < 0 || s->x_dtype > 1 || s->g_dtype < 0 || s->g_dtype > 1) return SDM_ERR_DTYPE;
+    if (s->P < 1 || s->D < 1 || s->D > (1 << 20) || s->rows < 0 || s->rows > (int64_t(1) << 40) || s->gate_width < 1)
+        return SDM_ERR_SHAPE;
+    if (s->D % 4 != 0 || (s->gate_width != 1 && s->gate_width % 4 != 0)) return SDM_ERR_ALIGN;
+    if (s->D % s->gate_width != 0) return SDM_ERR_SHAPE;
+    return SDM_OK;
+}
+
+// A row array of `cols` columns: present, aligned to 4 elements (one where `vec` is false), its rows too.
+sdm_status check_rows(const void* p, int64_t ld, int64_t cols, int dtype, bool vec, bool out) {
+    if (p == nullptr) return SDM_ERR_ARG;
+    const int v = vec ? 4 : 1;
+    if (reinterpret_cast<uintptr_t>(p) % (v * elem(dtype)) != 0 || ld % v != 0) return SDM_ERR_ALIGN;
+    if (ld < (out ? cols : 0) || ld > (int64_t(1) << 40)) return SDM_ERR_ARG;
+    return SDM_OK;
+}
+
+void geometry(const sdm_glr_shape* s, GlrArgs* a) {
+    memset(a, 0, sizeof(*a));
+    a->P = s->P;
+    a->D = s->D;
+    a->gw = s->gate_width;
+    a->H = s->D / s->gate_width;
+    a->rows = s->rows;
+    a->len = s->rows / s->P;
+    a->tiles_per_head = 1;
+    if (s->gate_width == 1) {
+        a->tile_cols = kTileCols;
+        a->tiles = (s->D + kTileCols - 1) / kTileCols;
+    } else if (s->gate_width <= kTileCols) {   // whole heads
+        a->tile_cols = kTileCols / s->gate_width * s->gate_width;
+        a->tiles = (s->D + a->tile_cols - 1) / a->tile_cols;
+    } else {   // equal parts of a head, in multiples of 4 channels
+        const int k = (s->gate_width + kTileCols - 1) / kTileCols;
+        a->tile_cols = ((s->gate_width + k - 1) / k + 3) / 4 * 4;
+        a->tiles_per_head = (s->gate_width + a->tile_cols - 1) / a->tile_cols;
+        a->tiles = a->H * a->tiles_per_head;
+    }
+}
+
+size_t part_bytes(const GlrArgs& a) {
+    return a.tiles_per_head == 1 ? 0 : static_cast<size_t>(a.tiles_per_head) * a.rows * a.H * sizeof(float);
+}
+
+// Calls f(x type, g type, per-channel gates) with the shape's types.
+template <typename F>
+cudaError_t by_type(const sdm_glr_shape* s, F f) {
+    const bool xb = s->x_dtype == SDM_BF16, gb = s->g_dtype == SDM_BF16, pc = s->gate_width == 1;
+    auto with = [&](auto x, auto g) { return pc ? f(x, g, std::true_type{}) : f(x, g, std::false_type{}); };
+    const __nv_bfloat16 b{};
+    if (xb) return gb ? with(b, b) : with(b, 0.f);
+    return gb ? with(0.f, b) : with(0.f, 0.f);
+}
+
+}  // namespace
+}  // namespace sdm
+
+using namespace sdm;
+
+extern "C" size_t sdm_glr_states_bytes(const sdm_glr_shape* shape) {
+    if (check(shape) != SDM_OK) return 0;
+    return static_cast<size_t>(shape->rows / SDM_GLR_CHUNK + shape->P) * shape->D * sizeof(float);
+}
+
+extern "C" size_t sdm_glr_workspace_bytes(const sdm_glr_shape* shape) {
+    if (check(shape) != SDM_OK) return 0;
+    GlrArgs a;
+    geometry(shape, &a);
+    return std::max<size_t>(part_bytes(a), 256);
+}
+
+extern "C" sdm_status sdm_glr_forward(const sdm_glr_shape* shape, const void* x, int64_t x_ld, const void* g,
+                                      int64_t g_ld, const int64_t* offsets, const float* h0, void* y, int64_t y_ld,
+                                      float* hT, float* states, uint32_t* status, sdm_stream_t stream) {
+    sdm_status st = check(shape);
+    if (st != SDM_OK) return st;
+    if (offsets == nullptr && shape->rows % shape->P != 0) return SDM_ERR_SHAPE;
+    const bool pc = shape->gate_width == 1;
+    if (shape->rows > 0) {
+        if ((st = check_rows(x, x_ld, shape->D, shape->x_dtype, true, false)) != SDM_OK) return st;
+        if ((st = check_rows(g, g_ld, shape->D / shape->gate_width, shape->g_dtype, pc, false)) != SDM_OK) return st;
+        if ((st = check_rows(y, y_ld, shape->D, shape->x_dtype, true, true)) != SDM_OK) return st;
+    }
+    for (const void* p : {static_cast<const void*>(h0), static_cast<const void*>(hT), static_cast<const void*>(states)})
+        if (!aligned16(p)) return SDM_ERR_ALIGN;
+    GlrArgs a;
+    geometry(shape, &a);
+    if (static_cast<int64_t>(a.tiles) * a.P > 0x7FFFFFFF) return SDM_ERR_SHAPE;
+    a.x = x; a.x_ld = x_ld; a.g = g; a.g_ld = g_ld; a.y = y; a.y_ld = y_ld;
+    a.offsets = offsets; a.h0 = h0; a.hT = hT; a.states = states; a.status = status;
+    const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+    const cudaError_t e = by_type(shape, [&](auto xt, auto gt, auto perch) {
+        return launch_dependent(glr_fwd_kernel<decltype(xt), decltype(gt), decltype(perch)::value>,
+                                dim3(static_cast<unsigned>(a.tiles * a.P)), dim3(kWarps * 32), 0, cs, a);
+    });
+    return e == cudaSuccess ? SDM_OK : SDM_ERR_CUDA;
+}
+
+extern "C" sdm_status sdm_glr_backward(const sdm_glr_shape* shape, const void* x, int64_t x_ld, const void* g,
+                                       int64_t g_ld, const void* dy, int64_t dy_ld, const int64_t* offsets,
+                                       const float* states, const float* dhT, void* dx, int64_t dx_ld, void* dg,
+                                       int64_t dg_ld, float* dh0, void* ws, size_t ws_bytes, uint32_t* status,
+                                       sdm_stream_t stream) {
+    sdm_status st = check(shape);
+    if (st != SDM_OK) return st;
+    if (offsets == nullptr && shape->rows % shape->P != 0) return SDM_ERR_SHAPE;
+    const bool pc = shape->gate_width == 1;
+    const int H = shape->D / shape->gate_width;
+    if (shape->rows > 0) {
+        if ((st = check_rows(x, x_ld, shape->D, shape->x_dtype, true, false)) != SDM_OK) return st;
+        if ((st = check_rows(g, g_ld, H, shape->g_dtype, pc, false)) != SDM_OK) return st;
+        if ((st = check_rows(dy, dy_ld, shape->D, shape->x_dtype, true, false)) != SDM_OK) return st;
+        if ((st = check_rows(dx, dx_ld, shape->D, shape->x_dtype, true, true)) != SDM_OK) return st;
+        if ((st = check_rows(dg, dg_ld, H, shape->g_dtype, pc, true)) != SDM_OK) return st;
+        if (states == nullptr) return SDM_ERR_ARG;
+    }
+    for (const void* p : {static_cast<const void*>(states), static_cast<const void*>(dhT), static_cast<const void*>(dh0)})
+        if (!aligned16(p)) return SDM_ERR_ALIGN;
+    GlrArgs a;
+    geometry(shape, &a);
+    if (static_cast<int64_t>(a.tiles) * a.P > 0x7FFFFFFF) return SDM_ERR_SHAPE;
+    if (part_bytes(a) > 0 && (ws == nullptr || !aligned16(ws) || ws_bytes < part_bytes(a))) return SDM_ERR_WORKSPACE;
+    a.x = x; a.x_ld = x_ld; a.g = g; a.g_ld = g_ld; a.dy = dy; a.dy_ld = dy_ld;
+    a.dx = dx; a.dx_ld = dx_ld; a.dg = dg; a.dg_ld = dg_ld;
+    a.offsets = offsets; a.dhT = dhT; a.dh0 = dh0; a.states = const_cast<float*>(states); a.status = status;
+    a.part = static_cast<float*>(ws);
+    const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+    cudaError_t e = by_type(shape, [&](auto xt, auto gt, auto perch) {
+        return launch_dependent(glr_bwd_kernel<decltype(xt), decltype(gt), decltype(perch)::value>,
+                                dim3(static_cast<unsigned>(a.tiles * a.P)), dim3(kWarps * 32), 0, cs, a);
+    });
+    if (e == cudaSuccess && part_bytes(a) > 0) {
+        const int64_t blocks = std::min<int64_t>((a.rows * a.H + 255) / 256, 4096);
+        e = launch_dependent(shape->g_dtype == SDM_BF16 ? glr_dg_kernel<__nv_bfloat16> : glr_dg_kernel<float>,
+                             dim3(static_cast<unsigned>(blocks)), dim3(256), 0, cs, a);
+    }
+    return e == cudaSuccess ? SDM_OK : SDM_ERR_CUDA;
+}
+
+extern "C" sdm_status sdm_glr_step(const sdm_glr_shape* shape, const void* x, int64_t x_ld, const void* g, int64_t g_ld,
+                                   const int32_t* slots, float* state, int64_t state_ld, int64_t states, void* y,
+                                   int64_t y_ld, uint32_t* status, sdm_stream_t stream) {
+    sdm_status st = check(shape);
+    if (st != SDM_OK) return st;
+    if (states < 0 || (slots == nullptr && states < shape->rows)) return SDM_ERR_SHAPE;
+    if (shape->rows == 0) return SDM_OK;
+    if ((st = check_rows(x, x_ld, shape->D, shape->x_dtype, true, false)) != SDM_OK) return st;
+    if ((st = check_rows(g, g_ld, shape->D / shape->gate_width, shape->g_dtype, shape->gate_width == 1, false)) != SDM_OK)
+        return st;
+    if ((st = check_rows(y, y_ld, shape->D, shape->x_dtype, true, true)) != SDM_OK) return st;
+    if (states > 0 && (st = check_rows(state, state_ld, shape->D, SDM_F32, true, true)) != SDM_OK) return st;
+    StepArgs a;
+    memset(&a, 0, sizeof(a));
+    a.x = x; a.x_ld = x_ld; a.g = g; a.g_ld = g_ld; a.slots = slots; a.state = state; a.s_ld = state_ld;
+    a.states = states; a.y = y; a.y_ld = y_ld; a.status = status;
+    a.D = shape->D;
+    a.gw = shape->gate_width;
+    a.units = shape->rows * (shape->D / 4);
+    const int64_t blocks = (a.units + 255) / 256;
+    if (blocks > 0x7FFFFFFF) return SDM_ERR_SHAPE;
+    const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+    const cudaError_t e = by_type(shape, [&](auto xt, auto gt, auto perch) {
+        return launch_dependent(glr_step_kernel<decltype(xt), decltype(gt), decltype(perch)::value>,
+                                dim3(static_cast<unsigned>(blocks)), dim3(256), 0, cs, a);
+    });
+    return e == cudaSuccess ? SDM_OK : SDM_ERR_CUDA;
+}

@@ -1,0 +1,443 @@
+// sdm_logprob.cu -- log probabilities of given tokens with entropy and top alternatives, and the gradient of the
+// logits: sdm_token_logprobs / sdm_token_logprobs_backward (include/sdm.h).
+//
+// Mathematics. For a row x of V logits, z = scale x, lse = log sum exp z, p = exp(z - lse), H = lse - sum p z.
+// One pass keeps, per thread, a reference M, s = sum 2^t and u = sum t 2^t with t = x scale log2(e) - M, moved to a
+// new M when a larger logit comes; the threads' triples join the same way. log p(target) = (t_target - log2 s) ln 2,
+// H = (log2 s - u / s) ln 2. Backward: dz_v = dlogp (1[v = target] - p_v) - dH p_v (log p_v + H).
+//
+// The top alternatives are kept in the same pass: every warp holds its K <= 32 largest (value, id) so far, one in a
+// lane, and looks only at vectors that hold a logit above the last of them.
+//
+// A row whose largest logit lies under -1e30 / scale (everything masked, by -inf or by a type's lowest value)
+// leaves s = 0 and takes a second, plain look; so does the backward of a row whose lse is too large for float32
+// differences.
+#include <cuda_bf16.h>
+
+#include <algorithm>
+#include <cstring>
+
+#include "sdm_checks.cuh"
+#include "sdm_internal.cuh"
+#include "sdm_rows.cuh"
+
+namespace sdm {
+namespace {
+
+using namespace rows;
+
+constexpr int kThreads = 512;
+constexpr int kWarps = kThreads / 32;
+constexpr int kMaxK = 32;
+constexpr float kLog2e = 1.44269504088896341f;
+constexpr float kLn2 = 0.69314718055994531f;
+constexpr float kFloor = -1e35f;      // what a masked logit counts as in the sums: its term is 0 beside any M
+constexpr float kStart = -1e30f;      // the first M
+constexpr float kFarLse = 1024.f;     // |lse| from which float32 z - lse is too coarse
+
+struct LpArgs {
+    const void* logits;
+    const int32_t* targets;
+    float* logp;
+    float* entropy;        // nullable
+    float* lse;            // nullable
+    float* top_vals;       // nullable [rows, K]
+    int32_t* top_idx;      // nullable
+    const float* lse_in;
+    const float* ent_in;
+    const float* d_logp;
+    const float* d_entropy;   // nullable
+    void* dlogits;
+    uint32_t* status;      // nullable
+    int64_t rows, ld, d_ld;
+    int V, K;
+    float scale;
+};
+
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float o;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(o) : "f"(a), "f"(b));
+    return o;
+}
+
+// A float's place in the order of the reals as an unsigned number (0 is no value's); -0 is +0, NaN is above all.
+__device__ __forceinline__ uint32_t order_of(float x) {
+    if (x != x) return 0xFFFFFFFFu;
+    const uint32_t b = __float_as_uint(x + 0.f);
+    return (b & 0x80000000u) ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float value_of(uint32_t o) {
+    return o == 0xFFFFFFFFu ? __uint_as_float(0x7FC00000u) : __uint_as_float((o & 0x80000000u) ? o & 0x7FFFFFFFu : ~o);
+}
+
+template <typename T>
+struct Vec;   // 16 bytes of logits
+template <>
+struct Vec<float> {
+    static constexpr int n = 4;
+    float4 v;
+    __device__ __forceinline__ void ld(const float* p) { v = __ldg(reinterpret_cast<const float4*>(p)); }
+    __device__ __forceinline__ void get(float (&o)[4]) const { o[0] = v.x; o[1] = v.y; o[2] = v.z; o[3] = v.w; }
+    __device__ __forceinline__ static void st(float* p, const float (&o)[4]) { st4(p, o); }
+};
+template <>
+struct Vec<__nv_bfloat16> {
+    static constexpr int n = 8;
+    uint4 v;
+    __device__ __forceinline__ void ld(const __nv_bfloat16* p) { v = __ldg(reinterpret_cast<const uint4*>(p)); }
+    __device__ __forceinline__ void get(float (&o)[8]) const {
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            o[2 * i] = __uint_as_float(w[i] << 16);
+            o[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+        }
+    }
+    __device__ __forceinline__ static void st(__nv_bfloat16* p, const float (&o)[8]) { st8(p, o); }
+};
+
+// The online sums of some of a row's logits, in units of log2.
+struct Sums {
+    float M, s, u;
+    __device__ __forceinline__ void clear() {
+        M = kStart;
+        s = u = 0.f;
+    }
+    __device__ __forceinline__ void raise(float m) {
+        const float d = M - m, f = exp2f(d);   // d <= 0
+        u = f * fmaf(d, s, u);
+        s *= f;
+        M = m;
+    }
+    __device__ __forceinline__ void add(float x, float c) {   // M is at least x c
+        const float t = fmaf(max_nan(x, kFloor), c, -M), e = exp2f(t);
+        s += e;
+        u = fmaf(e, t, u);
+    }
+    __device__ __forceinline__ void join(float oM, float os, float ou) {
+        const float m = fmaxf(M, oM), d = M - m, od = oM - m, f = exp2f(d), of = exp2f(od);
+        u = f * fmaf(d, s, u) + of * fmaf(od, os, ou);
+        s = f * s + of * os;
+        M = m;
+    }
+};
+
+// A warp's K largest (order, ~id) so far, the i-th in lane i.
+struct TopList {
+    uint64_t key;
+    int K, lane;
+    uint32_t pass;   // a logit enters only if its order is at least this
+    __device__ __forceinline__ void clear(int k, int l) {
+        key = 0;
+        K = k;
+        lane = l;
+        pass = 0;
+    }
+    __device__ __forceinline__ void insert(uint64_t c) {   // warp-uniform c
+        const uint64_t last = __shfl_sync(kFull, key, K - 1);
+        if (c <= last) return;
+        const int at = __popc(__ballot_sync(kFull, lane < K && key > c));
+        const uint64_t up = __shfl_up_sync(kFull, key, 1);
+        if (lane < K && lane >= at) key = lane == at ? c : up;
+        const uint32_t k = static_cast<uint32_t>(__shfl_sync(kFull, key, K - 1) >> 32);
+        // once K are held, an equal logit of a later vector has a higher id and stays out
+        pass = k == 0 ? 0 : k == 0xFFFFFFFFu ? k : k + 1;
+    }
+    // N logits of each lane, ids id .. id + N - 1 (those from `end` on are none)
+    template <int N>
+    __device__ __forceinline__ void offer(const float (&x)[N], float most, int id, int end) {
+        const bool want = id < end && order_of(most) >= pass;
+        if (!__any_sync(kFull, want)) return;
+        const uint32_t bar = pass;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const uint32_t o = order_of(x[i]);
+            uint32_t b = __ballot_sync(kFull, id + i < end && o >= bar);
+            while (b) {
+                const int l = __ffs(b) - 1;
+                b &= b - 1;
+                const uint32_t oc = __shfl_sync(kFull, o, l);
+                const uint32_t ic = static_cast<uint32_t>(__shfl_sync(kFull, id, l) + i);
+                insert(static_cast<uint64_t>(oc) << 32 | static_cast<uint32_t>(~ic));
+            }
+        }
+    }
+};
+
+struct Shared {
+    float M[kWarps], s[kWarps], u[kWarps];
+    uint64_t top[kWarps][kMaxK];
+    float red[kWarps];
+};
+
+// The row's largest logit, then sum exp(z - z_max), sum exp(z - z_max) (z - z_max), from differences that hold for
+// any finite logits. Block-wide; every thread gets them.
+template <typename T>
+__device__ void plain_stats(const T* x, int V, float scale, Shared& sh, float& m, float& s, float& u) {
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    auto block = [&](float v, bool sum) {
+#pragma unroll
+        for (int k = 16; k; k >>= 1) {
+            const float o = __shfl_xor_sync(kFull, v, k);
+            v = sum ? v + o : max_nan(v, o);
+        }
+        __syncthreads();
+        if (lane == 0) sh.red[w] = v;
+        __syncthreads();
+        v = sh.red[0];
+        for (int k = 1; k < static_cast<int>(blockDim.x) / 32; ++k) v = sum ? v + sh.red[k] : max_nan(v, sh.red[k]);
+        return v;
+    };
+    float most = -INFINITY;
+    for (int i = threadIdx.x; i < V; i += blockDim.x) most = max_nan(most, widen(x[i]));
+    m = block(most, false);
+    float a = 0.f, b = 0.f;
+    for (int i = threadIdx.x; i < V; i += blockDim.x) {
+        const float d = (widen(x[i]) - m) * scale, e = expf(d);
+        a += e;
+        b += e > 0.f ? e * d : e;   // NaN stays
+    }
+    s = block(a, true);
+    u = block(b, true);
+}
+
+template <typename T, bool TOP>
+__global__ void __launch_bounds__(kThreads) lp_fwd_kernel(const LpArgs a) {
+    __shared__ Shared sh;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    constexpr int N = Vec<T>::n;
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    const int64_t row = blockIdx.x;
+    const T* const x = static_cast<const T*>(a.logits) + row * a.ld;
+    const float c = a.scale * kLog2e;
+    Sums acc;
+    acc.clear();
+    TopList top;
+    top.clear(a.K, lane);
+    // vectors start at the row's first 16-byte boundary; the logits before it and behind the last vector are
+    // taken one by one, the former as the first step's (ids ascend over the steps of a warp)
+    const int head = min(a.V, static_cast<int>((16 - (reinterpret_cast<uintptr_t>(x) & 15)) % 16 / sizeof(T)));
+    const int nvec = (a.V - head) / N;
+    auto scalars = [&](int b, int e) {   // at most 32 logits, by warp 0
+        const int i = b + lane;
+        float v[1] = {i < e ? widen(__ldg(x + i)) : -INFINITY};
+        if (i < e) {
+            if (!(v[0] * c <= acc.M)) acc.raise(v[0] * c);
+            acc.add(v[0], c);
+        }
+        if (TOP) top.offer<1>(v, v[0], i, e);
+    };
+    if (w == 0) scalars(0, head);
+    for (int v0 = 0; v0 < nvec; v0 += kThreads) {
+        const int v = v0 + threadIdx.x;
+        const bool on = v < nvec;
+        float f[N];
+        if (on) {
+            Vec<T> r;
+            r.ld(x + head + static_cast<int64_t>(v) * N);
+            r.get(f);
+        } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i) f[i] = -INFINITY;
+        }
+        float most = f[0];
+#pragma unroll
+        for (int i = 1; i < N; ++i) most = max_nan(most, f[i]);
+        if (on) {
+            if (!(most * c <= acc.M)) acc.raise(most * c);
+#pragma unroll
+            for (int i = 0; i < N; ++i) acc.add(f[i], c);
+        }
+        if (TOP) top.offer<N>(f, most, on ? head + v * N : a.V, head + nvec * N);
+    }
+    if (w == 0) scalars(head + nvec * N, a.V);
+#pragma unroll
+    for (int k = 16; k; k >>= 1) {
+        const float M = __shfl_xor_sync(kFull, acc.M, k), s = __shfl_xor_sync(kFull, acc.s, k),
+                    u = __shfl_xor_sync(kFull, acc.u, k);
+        acc.join(M, s, u);
+    }
+    if (lane == 0) {
+        sh.M[w] = acc.M;
+        sh.s[w] = acc.s;
+        sh.u[w] = acc.u;
+    }
+    if (TOP) sh.top[w][lane] = lane < a.K ? top.key : 0;
+    __syncthreads();
+    acc.clear();
+    for (int k = 0; k < kWarps; ++k) acc.join(sh.M[k], sh.s[k], sh.u[k]);
+    // z - lse = (x - ref) mul - sub for the row's logits
+    float ref = 0.f, sub, lse, H, mul = 0.f;
+    bool empty = false;
+    if (acc.s == 0.f) {   // block-uniform
+        float m, s, u;
+        plain_stats(x, a.V, a.scale, sh, m, s, u);
+        empty = m == -INFINITY;
+        ref = m;
+        mul = a.scale;
+        sub = logf(s);
+        lse = empty ? -INFINITY : m * a.scale + sub;
+        H = empty ? 0.f : sub - u / s;
+    } else {
+        const float l2 = log2f(acc.s);
+        sub = l2;
+        lse = (acc.M + l2) * kLn2;
+        H = (l2 - acc.u / acc.s) * kLn2;
+    }
+    auto logp_of = [&](float v) {
+        if (empty) return -INFINITY;
+        if (mul != 0.f) return (v - ref) * mul - sub;
+        const float t = fmaf(v, c, -acc.M) - sub;
+        return t < kStart ? v * a.scale - lse : t * kLn2;   // a masked logit's t may have overflowed
+    };
+    if (threadIdx.x == 0) {
+        const int t = __ldg(a.targets + row);
+        if (t >= a.V && a.status != nullptr) atomicOr(a.status, SDM_DEV_BAD_TARGET);
+        a.logp[row] = t >= 0 && t < a.V ? logp_of(widen(__ldg(x + t))) : 0.f;
+        if (a.entropy != nullptr) a.entropy[row] = H;
+        if (a.lse != nullptr) a.lse[row] = lse;
+    }
+    if (TOP && w == 0) {
+        for (int k = 1; k < kWarps; ++k) {
+            const uint64_t cand = sh.top[k][lane];
+            for (int i = 0; i < a.K; ++i) {   // descending: the first that fails ends the list
+                const uint64_t cc = __shfl_sync(kFull, cand, i);
+                if (cc <= __shfl_sync(kFull, top.key, a.K - 1)) break;
+                top.insert(cc);
+            }
+        }
+        if (lane < a.K) {
+            const uint32_t o = static_cast<uint32_t>(top.key >> 32);
+            if (a.top_vals != nullptr) a.top_vals[row * a.K + lane] = logp_of(value_of(o));
+            if (a.top_idx != nullptr) a.top_idx[row * a.K + lane] = static_cast<int32_t>(~static_cast<uint32_t>(top.key));
+        }
+    }
+}
+
+constexpr int kBwdThreads = 256;
+constexpr int kBwdVecs = 4;   // vectors of a thread
+
+template <typename T>
+__global__ void __launch_bounds__(kBwdThreads) lp_bwd_kernel(const LpArgs a, int parts) {
+    __shared__ Shared sh;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    constexpr int N = Vec<T>::n;
+    const int64_t row = blockIdx.x / parts;
+    const int part = static_cast<int>(blockIdx.x - row * parts);
+    const T* const x = static_cast<const T*>(a.logits) + row * a.ld;
+    T* const o = static_cast<T*>(a.dlogits) + row * a.d_ld;
+    const int t = __ldg(a.targets + row);
+    const float dl = t >= 0 && t < a.V ? __ldg(a.d_logp + row) : 0.f;
+    const float dh = a.d_entropy != nullptr ? __ldg(a.d_entropy + row) : 0.f;
+    const float H = __ldg(a.ent_in + row);
+    float lse = __ldg(a.lse_in + row), ref = 0.f;
+    if (part == 0 && threadIdx.x == 0 && t >= a.V && a.status != nullptr) atomicOr(a.status, SDM_DEV_BAD_TARGET);
+    if (fabsf(lse) >= kFarLse && !isinf(lse)) {   // block-uniform: z - lse from z - z_max, log s
+        float m, s, u;
+        plain_stats(x, a.V, a.scale, sh, m, s, u);
+        ref = m;
+        lse = logf(s);
+    }
+    const bool empty = lse == -INFINITY;
+    auto grad = [&](float v, int id) {
+        const float d = max_nan((v - ref) * a.scale - lse, kFloor);   // log p; its product with p = 0 stays 0
+        const float p = empty ? 0.f : expf(d);
+        const float g = -p * (dl + dh * (empty ? 0.f : d + H)) + (id == t ? dl : 0.f);
+        return a.scale * g;
+    };
+    const bool same = ((reinterpret_cast<uintptr_t>(x) ^ reinterpret_cast<uintptr_t>(o)) & 15) == 0;
+    const int head = same ? min(a.V, static_cast<int>((16 - (reinterpret_cast<uintptr_t>(x) & 15)) % 16 / sizeof(T))) : a.V;
+    const int nvec = (a.V - head) / N;
+    // the logits outside the vectors: all of them where the two rows lie differently on 16 bytes
+    for (int i = part * kBwdThreads + threadIdx.x; i < head; i += parts * kBwdThreads) st1(o + i, grad(widen(x[i]), i));
+    for (int i = head + nvec * N + part * kBwdThreads + threadIdx.x; i < a.V; i += parts * kBwdThreads)
+        st1(o + i, grad(widen(x[i]), i));
+    for (int v0 = part * kBwdThreads * kBwdVecs; v0 < nvec; v0 += parts * kBwdThreads * kBwdVecs) {
+        Vec<T> r[kBwdVecs];
+#pragma unroll
+        for (int k = 0; k < kBwdVecs; ++k) {
+            const int v = v0 + k * kBwdThreads + threadIdx.x;
+            if (v < nvec) r[k].ld(x + head + static_cast<int64_t>(v) * N);
+        }
+#pragma unroll
+        for (int k = 0; k < kBwdVecs; ++k) {
+            const int v = v0 + k * kBwdThreads + threadIdx.x;
+            if (v >= nvec) continue;
+            float f[N];
+            r[k].get(f);
+#pragma unroll
+            for (int i = 0; i < N; ++i) f[i] = grad(f[i], head + v * N + i);
+            Vec<T>::st(o + head + static_cast<int64_t>(v) * N, f);
+        }
+    }
+}
+
+// ---- host side ------------------------------------------------------------------------------------
+sdm_status check(const sdm_logprob_shape* s) {
+    if (s == nullptr) return SDM_ERR_ARG;
+    if (s->dtype < 0 || s->dtype > 1) return SDM_ERR_DTYPE;
+    if (s->rows < 0 || s->rows > (int64_t(1) << 31) - 1 || s->V < 1 || s->V > (1 << 28) || s->K < 0 || s->K > kMaxK ||
+        s->K > s->V || !(s->scale >= 1e-3f && s->scale <= 1e3f))
+        return SDM_ERR_SHAPE;
+    return SDM_OK;
+}
+
+sdm_status check_logits(const sdm_logprob_shape* s, const void* p, int64_t ld, bool out) {
+    if (p == nullptr) return SDM_ERR_ARG;
+    if (reinterpret_cast<uintptr_t>(p) % (s->dtype == SDM_BF16 ? 2 : 4) != 0) return SDM_ERR_ALIGN;
+    if (ld < (out ? s->V : 0) || ld > (int64_t(1) << 40)) return SDM_ERR_ARG;
+    return SDM_OK;
+}
+
+}  // namespace
+}  // namespace sdm
+
+using namespace sdm;
+
+extern "C" sdm_status sdm_token_logprobs(const sdm_logprob_shape* shape, const void* logits, int64_t ld,
+                                         const int32_t* targets, float* logp, float* entropy, float* lse,
+                                         float* top_vals, int32_t* top_idx, uint32_t* status, sdm_stream_t stream) {
+    sdm_status st = check(shape);
+    if (st != SDM_OK) return st;
+    if (shape->rows == 0) return SDM_OK;
+    if ((st = check_logits(shape, logits, ld, false)) != SDM_OK) return st;
+    if (targets == nullptr || logp == nullptr) return SDM_ERR_ARG;
+    LpArgs a;
+    memset(&a, 0, sizeof(a));
+    a.logits = logits; a.ld = ld; a.targets = targets; a.logp = logp; a.entropy = entropy; a.lse = lse;
+    a.top_vals = top_vals; a.top_idx = top_idx; a.status = status;
+    a.rows = shape->rows; a.V = shape->V; a.K = shape->K; a.scale = shape->scale;
+    const bool top = shape->K > 0 && (top_vals != nullptr || top_idx != nullptr);
+    const bool bf = shape->dtype == SDM_BF16;
+    const auto kernel = bf ? (top ? lp_fwd_kernel<__nv_bfloat16, true> : lp_fwd_kernel<__nv_bfloat16, false>)
+                           : (top ? lp_fwd_kernel<float, true> : lp_fwd_kernel<float, false>);
+    const cudaError_t e = launch_dependent(kernel, dim3(static_cast<unsigned>(shape->rows)), dim3(kThreads), 0,
+                                           reinterpret_cast<cudaStream_t>(stream), a);
+    return e == cudaSuccess ? SDM_OK : SDM_ERR_CUDA;
+}
+
+extern "C" sdm_status sdm_token_logprobs_backward(const sdm_logprob_shape* shape, const void* logits, int64_t ld,
+                                                  const int32_t* targets, const float* lse, const float* entropy,
+                                                  const float* d_logp, const float* d_entropy, void* dlogits,
+                                                  int64_t d_ld, uint32_t* status, sdm_stream_t stream) {
+    sdm_status st = check(shape);
+    if (st != SDM_OK) return st;
+    if (shape->rows == 0) return SDM_OK;
+    if ((st = check_logits(shape, logits, ld, false)) != SDM_OK) return st;
+    if ((st = check_logits(shape, dlogits, d_ld, true)) != SDM_OK) return st;
+    if (targets == nullptr || lse == nullptr || entropy == nullptr || d_logp == nullptr) return SDM_ERR_ARG;
+    LpArgs a;
+    memset(&a, 0, sizeof(a));
+    a.logits = logits; a.ld = ld; a.targets = targets; a.lse_in = lse; a.ent_in = entropy; a.d_logp = d_logp;
+    a.d_entropy = d_entropy; a.dlogits = dlogits; a.d_ld = d_ld; a.status = status;
+    a.rows = shape->rows; a.V = shape->V; a.scale = shape->scale;
+    const bool bf = shape->dtype == SDM_BF16;
+    const int per = kBwdThreads * kBwdVecs * (bf ? 8 : 4);
+    const int parts = (shape->V + per - 1) / per;
+    const int64_t blocks = shape->rows * parts;
+    if (blocks > 0x7FFFFFFF) return SDM_ERR_SHAPE;
+    const cudaError_t e = launch_dependent(bf ? lp_bwd_kernel<__nv_bfloat16> : lp_bwd_kernel<float>,
+                                           dim3(static_cast<unsigned>(blocks)), dim3(kBwdThreads), 0,
+                                           reinterpret_cast<cudaStream_t>(stream), a, parts);
+    return e == cudaSuccess ? SDM_OK : SDM_ERR_CUDA;
+}

@@ -1,0 +1,467 @@
+// sdm_rope.cu -- the norm of every query and key head with the position rotation in the same pass, its
+// backward, and the table of the rotation: sdm_qk_norm_rope / sdm_qk_norm_rope_backward / sdm_rope_table
+// (include/sdm.h).
+//
+// Mathematics. A head's row x [hd] with r = rsqrt(mean x^2 + eps): n = x r w, then every pair (a, b) of the
+// first rot_dim columns turns by its angle: a' = a c - b s, b' = b c + a s. Backward: e = the gradient turned
+// back; dw += e x r; with t = e w: dx = r (t - x r^2 mean(t x)). Everything between the load and the store is
+// float32; each output is rounded once.
+//
+// Layout. A head's columns are taken in units of 8 that hold whole pairs: interleaved, columns 8u .. 8u + 7;
+// half, columns 4u .. and rot_dim / 2 + 4u ..; behind rot_dim, 8 columns in a row. A unit's four pairs have the
+// frequencies 4u .. 4u + 3 in either layout. A lane owns the same units of every head it meets, so a token's
+// cosines and sines and the weights stay in registers over the heads of the token.
+#include <cuda_bf16.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstring>
+
+#include "sdm_checks.cuh"
+#include "sdm_internal.cuh"
+#include "sdm_rows.cuh"
+
+namespace sdm {
+namespace {
+
+using namespace rows;
+
+constexpr int kThreads = 256;
+constexpr int kMaxHd = 1024;
+constexpr int kMaxFreq = kMaxHd / 2;
+constexpr int kPartBlocks = 512;   // blocks of the backward at most: a row of weight gradients each
+
+struct RopeArgs {
+    const void* q;
+    const void* k;
+    const void* dqo;
+    const void* dko;
+    const int32_t* pos;
+    const float* table;   // [max_pos, rot_dim]: cosines, then sines
+    const float* wq;      // nullable: ones
+    const float* wk;
+    void* qo;
+    void* ko;
+    float* part;          // backward: [blocks][2][hd] weight gradients
+    uint32_t* status;
+    int64_t q_ld, k_ld, dqo_ld, dko_ld, qo_ld, ko_ld;
+    int64_t tokens;
+    int Hq, Hk, hd, rd, max_pos, interleaved, norm;
+    float eps;
+};
+
+// A lane's place: `lanes` lanes hold a head, each `U` units of 8 columns (unit sub + i * lanes).
+template <int U>
+struct Place {
+    int a[U], b[U];       // first columns of the unit's two halves of 4
+    int f[U];             // its first frequency, or -1 behind rot_dim
+    bool on[U];
+    __device__ __forceinline__ void set(const RopeArgs& s, int sub, int lanes) {
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const int u = sub + i * lanes;
+            on[i] = u * 8 < s.hd;
+            const int v = on[i] ? u : 0;
+            const bool turned = v * 8 < s.rd;
+            f[i] = turned ? 4 * v : -1;
+            a[i] = turned && !s.interleaved ? 4 * v : 8 * v;
+            b[i] = turned && !s.interleaved ? s.rd / 2 + 4 * v : 8 * v + 4;
+        }
+    }
+};
+
+// The unit's cosines and sines of a position (1 and 0 behind rot_dim)
+__device__ __forceinline__ void turns(const RopeArgs& s, int64_t pos, int f, float (&c)[4], float (&sn)[4]) {
+    if (f >= 0) {
+        ld4(s.table + pos * s.rd + f, c);
+        ld4(s.table + pos * s.rd + s.rd / 2 + f, sn);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            c[j] = 1.f;
+            sn[j] = 0.f;
+        }
+    }
+}
+
+// The unit's pairs turned by `sign` times the angle: pairs (a[j], b[j]) in the half layout and behind rot_dim,
+// neighbours in the interleaved one.
+__device__ __forceinline__ void turn(float (&a)[4], float (&b)[4], const float (&c)[4], const float (&s)[4], float sign,
+                                     bool inter) {
+    if (inter) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const float x = a[2 * j], y = a[2 * j + 1], z = b[2 * j], w = b[2 * j + 1];
+            a[2 * j] = x * c[j] - sign * y * s[j];
+            a[2 * j + 1] = y * c[j] + sign * x * s[j];
+            b[2 * j] = z * c[2 + j] - sign * w * s[2 + j];
+            b[2 * j + 1] = w * c[2 + j] + sign * z * s[2 + j];
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float x = a[j], y = b[j];
+            a[j] = x * c[j] - sign * y * s[j];
+            b[j] = y * c[j] + sign * x * s[j];
+        }
+    }
+}
+
+__device__ __forceinline__ float lanes_sum(float v, int lanes) {
+    for (int k = 1; k < lanes; k <<= 1) v += __shfl_xor_sync(kFull, v, k);
+    return v;
+}
+
+__device__ __forceinline__ void weights(const float* w, int a, int b, float (&o)[4], float (&p)[4]) {
+    if (w != nullptr) {
+        ld4(w + a, o);
+        ld4(w + b, p);
+    } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[j] = p[j] = 1.f;
+    }
+}
+
+// One group of `lanes` lanes a (token, head); heads 0 .. Hq - 1 are queries, then the keys.
+template <typename T, int U>
+__global__ void __launch_bounds__(kThreads) rope_fwd_kernel(const RopeArgs s, int lanes) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int per = kThreads / lanes, H = s.Hq + s.Hk;
+    const int64_t unit = blockIdx.x * static_cast<int64_t>(per) + threadIdx.x / lanes;
+    const bool live = unit < s.tokens * H;
+    const int64_t t = live ? unit / H : 0;
+    const int head = static_cast<int>(live ? unit - t * H : 0);
+    Place<U> pl;
+    pl.set(s, threadIdx.x % lanes, lanes);
+    const bool isq = head < s.Hq;
+    const T* const x = isq ? static_cast<const T*>(s.q) + t * s.q_ld + head * s.hd
+                           : static_cast<const T*>(s.k) + t * s.k_ld + (head - s.Hq) * s.hd;
+    T* const y = isq ? static_cast<T*>(s.qo) + t * s.qo_ld + head * s.hd
+                     : static_cast<T*>(s.ko) + t * s.ko_ld + (head - s.Hq) * s.hd;
+    int64_t pos = __ldg(s.pos + t);
+    if (pos >= s.max_pos) {
+        if (live && s.status != nullptr) atomicOr(s.status, SDM_DEV_BAD_POSITION);
+        pos = -1;
+    }
+    float a[U][4], b[U][4], ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+        ld4(x + pl.a[i], a[i]);
+        ld4(x + pl.b[i], b[i]);
+        if (pl.on[i]) ss += dot4(a[i], a[i]) + dot4(b[i], b[i]);
+    }
+    const float r = s.norm ? rsqrtf(lanes_sum(ss, lanes) / s.hd + s.eps) : 1.f;
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+        float c[4], sn[4], wa[4], wb[4];
+        turns(s, pos < 0 ? 0 : pos, pl.f[i], c, sn);
+        weights(s.norm ? (isq ? s.wq : s.wk) : nullptr, pl.a[i], pl.b[i], wa, wb);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            a[i][j] = a[i][j] * r * wa[j];
+            b[i][j] = b[i][j] * r * wb[j];
+        }
+        if (pl.f[i] >= 0) turn(a[i], b[i], c, sn, 1.f, s.interleaved);
+        if (pos < 0)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) a[i][j] = b[i][j] = 0.f;
+        if (live && pl.on[i]) {
+            st4(y + pl.a[i], a[i]);
+            st4(y + pl.b[i], b[i]);
+        }
+    }
+}
+
+// Groups of lanes walk the tokens' heads, queries first, then keys; a lane's weight gradients stay in registers,
+// are joined over the block in a fixed order and written as the block's row of `part`.
+template <typename T, int U>
+__global__ void __launch_bounds__(kThreads) rope_bwd_kernel(const RopeArgs s, int lanes) {
+    extern __shared__ float sm[];   // [groups][hd]
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int per = kThreads / lanes, group = threadIdx.x / lanes;
+    Place<U> pl;
+    pl.set(s, threadIdx.x % lanes, lanes);
+    for (int side = 0; side < 2; ++side) {
+        const int H = side ? s.Hk : s.Hq;
+        const T* const X = static_cast<const T*>(side ? s.k : s.q);
+        const T* const G = static_cast<const T*>(side ? s.dko : s.dqo);
+        T* const Y = static_cast<T*>(side ? s.ko : s.qo);
+        const int64_t x_ld = side ? s.k_ld : s.q_ld, g_ld = side ? s.dko_ld : s.dqo_ld, y_ld = side ? s.ko_ld : s.qo_ld;
+        const float* const w = s.norm ? (side ? s.wk : s.wq) : nullptr;
+        float da[U][4], db[U][4];
+#pragma unroll
+        for (int i = 0; i < U; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) da[i][j] = db[i][j] = 0.f;
+        const int64_t units = s.tokens * H;
+        const int64_t step = static_cast<int64_t>(gridDim.x) * per;
+        for (int64_t u0 = blockIdx.x * static_cast<int64_t>(per); u0 < units; u0 += step) {   // block-uniform
+            const int64_t u = u0 + group;
+            const bool live = u < units;
+            const int64_t t = live ? u / H : 0;
+            const int head = static_cast<int>(live ? u - t * H : 0);
+            int64_t pos = __ldg(s.pos + t);
+            if (pos >= s.max_pos) {
+                if (live && s.status != nullptr) atomicOr(s.status, SDM_DEV_BAD_POSITION);
+                pos = -1;
+            }
+            float a[U][4], b[U][4], ea[U][4], eb[U][4], ss = 0.f, tx = 0.f;
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                ld4(X + t * x_ld + head * s.hd + pl.a[i], a[i]);
+                ld4(X + t * x_ld + head * s.hd + pl.b[i], b[i]);
+                ld4(G + t * g_ld + head * s.hd + pl.a[i], ea[i]);
+                ld4(G + t * g_ld + head * s.hd + pl.b[i], eb[i]);
+                if (pl.on[i]) ss += dot4(a[i], a[i]) + dot4(b[i], b[i]);
+            }
+            const float r = s.norm ? rsqrtf(lanes_sum(ss, lanes) / s.hd + s.eps) : 1.f;
+            const bool use = live && pos >= 0;
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                float c[4], sn[4], wa[4], wb[4];
+                turns(s, pos < 0 ? 0 : pos, pl.f[i], c, sn);
+                weights(w, pl.a[i], pl.b[i], wa, wb);
+                if (pl.f[i] >= 0) turn(ea[i], eb[i], c, sn, -1.f, s.interleaved);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    if (use) {
+                        da[i][j] = fmaf(ea[i][j], a[i][j] * r, da[i][j]);
+                        db[i][j] = fmaf(eb[i][j], b[i][j] * r, db[i][j]);
+                    }
+                    ea[i][j] *= wa[j];
+                    eb[i][j] *= wb[j];
+                }
+                if (pl.on[i]) tx += dot4(ea[i], a[i]) + dot4(eb[i], b[i]);
+            }
+            const float k = s.norm ? lanes_sum(tx, lanes) / s.hd * r * r : 0.f;
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    ea[i][j] = pos < 0 ? 0.f : r * (ea[i][j] - a[i][j] * k);
+                    eb[i][j] = pos < 0 ? 0.f : r * (eb[i][j] - b[i][j] * k);
+                }
+                if (live && pl.on[i]) {
+                    st4(Y + t * y_ld + head * s.hd + pl.a[i], ea[i]);
+                    st4(Y + t * y_ld + head * s.hd + pl.b[i], eb[i]);
+                }
+            }
+        }
+        if (s.part == nullptr) continue;
+#pragma unroll
+        for (int i = 0; i < U; ++i)
+            if (pl.on[i]) {
+                st4(sm + group * s.hd + pl.a[i], da[i]);
+                st4(sm + group * s.hd + pl.b[i], db[i]);
+            }
+        __syncthreads();
+        for (int c = threadIdx.x; c < s.hd; c += kThreads) {
+            float v = 0.f;
+            for (int k = 0; k < per; ++k) v += sm[k * s.hd + c];
+            s.part[(static_cast<int64_t>(blockIdx.x) * 2 + side) * s.hd + c] = v;
+        }
+        __syncthreads();
+    }
+}
+
+// The weight gradients: the blocks' rows summed in a fixed order. A block a column group of 32, its 32 rows of
+// threads each a strided share of the partial rows.
+__global__ void __launch_bounds__(1024) rope_dw_kernel(const float* part, int blocks, int hd, float* dwq, float* dwk) {
+    __shared__ float sm[32][33];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int c = blockIdx.x * 32 + threadIdx.x;   // of 2 * hd columns
+    float v = 0.f;
+    if (c < 2 * hd)
+        for (int k = threadIdx.y; k < blocks; k += 32) v += part[static_cast<int64_t>(k) * 2 * hd + c];
+    sm[threadIdx.y][threadIdx.x] = v;
+    __syncthreads();
+    v = allsum(sm[threadIdx.x][threadIdx.y]);
+    const int o = blockIdx.x * 32 + threadIdx.y;
+    if (threadIdx.x == 0 && o < 2 * hd) {
+        float* const d = o < hd ? dwq : dwk;
+        if (d != nullptr) d[o < hd ? o : o - hd] = v;
+    }
+}
+
+struct TableArgs {
+    uint64_t turns[kMaxFreq];   // a position's turn in units of 2^-64
+    float* table;
+    float scale;
+    int n, max_pos;
+};
+
+// cos and sin of pos * f: the whole turns drop out of the 64-bit product exactly, whatever the position.
+__global__ void __launch_bounds__(256) rope_table_kernel(const __grid_constant__ TableArgs a) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int64_t i = blockIdx.x * int64_t(256) + threadIdx.x;
+    if (i >= static_cast<int64_t>(a.n) * a.max_pos) return;
+    const int64_t pos = i / a.n;
+    const int f = static_cast<int>(i - pos * a.n);
+    const int64_t phase = static_cast<int64_t>(static_cast<uint64_t>(pos) * a.turns[f]);   // [-1/2, 1/2) turns
+    float s, c;
+    sincospif(static_cast<float>(phase) * 0x1p-63f, &s, &c);
+    a.table[pos * 2 * a.n + f] = c * a.scale;
+    a.table[pos * 2 * a.n + a.n + f] = s * a.scale;
+}
+
+// ---- host side ------------------------------------------------------------------------------------
+using checks::aligned16;
+
+sdm_status check(const sdm_rope_shape* s) {
+    if (s == nullptr) return SDM_ERR_ARG;
+    if (s->dtype < 0 || s->dtype > 1) return SDM_ERR_DTYPE;
+    if (s->tokens < 0 || s->tokens > (int64_t(1) << 31) || s->q_heads < 0 || s->k_heads < 0 || s->q_heads > 65536 ||
+        s->k_heads > 65536 || s->q_heads + s->k_heads < 1 || s->hd < 1 || s->hd > kMaxHd || s->rot_dim < 0 ||
+        s->rot_dim > s->hd || s->max_pos < 1 || s->layout < 0 || s->layout > 1 || s->norm < 0 || s->norm > 1 ||
+        !(s->eps >= 0.f))
+        return SDM_ERR_SHAPE;
+    if (s->hd % 8 != 0 || s->rot_dim % 8 != 0) return SDM_ERR_ALIGN;
+    return SDM_OK;
+}
+
+sdm_status check_heads(const sdm_rope_shape* s, const void* p, int64_t ld, int heads, bool out) {
+    if (heads == 0) return SDM_OK;
+    if (p == nullptr) return SDM_ERR_ARG;
+    const int e = s->dtype == SDM_BF16 ? 2 : 4;
+    if (reinterpret_cast<uintptr_t>(p) % (4 * e) != 0 || ld % 4 != 0) return SDM_ERR_ALIGN;
+    if (ld < (out ? static_cast<int64_t>(heads) * s->hd : 0) || ld > (int64_t(1) << 40)) return SDM_ERR_ARG;
+    return SDM_OK;
+}
+
+void fill(const sdm_rope_shape* s, RopeArgs* a) {
+    memset(a, 0, sizeof(*a));
+    a->tokens = s->tokens;
+    a->Hq = s->q_heads;
+    a->Hk = s->k_heads;
+    a->hd = s->hd;
+    a->rd = s->rot_dim;
+    a->max_pos = s->max_pos;
+    a->interleaved = s->layout;
+    a->norm = s->norm;
+    a->eps = s->eps;
+}
+
+int head_lanes(int hd) {
+    int lanes = 1;
+    while (lanes < 32 && lanes * 8 < hd) lanes *= 2;
+    return lanes;
+}
+
+int bwd_blocks(const sdm_rope_shape* s) {
+    const int64_t units = s->tokens * std::max(s->q_heads, s->k_heads), per = kThreads / head_lanes(s->hd);
+    return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(kPartBlocks, (units + per - 1) / per)));
+}
+
+template <typename F>
+cudaError_t by_type(const sdm_rope_shape* s, F f) {
+    const int u = (s->hd / 8 + 31) / 32;
+    auto with = [&](auto t) {
+        return u == 1 ? f(t, std::integral_constant<int, 1>{})
+               : u == 2 ? f(t, std::integral_constant<int, 2>{}) : f(t, std::integral_constant<int, 4>{});
+    };
+    return s->dtype == SDM_BF16 ? with(__nv_bfloat16{}) : with(0.f);
+}
+
+}  // namespace
+}  // namespace sdm
+
+using namespace sdm;
+
+extern "C" size_t sdm_rope_workspace_bytes(const sdm_rope_shape* shape) {
+    if (check(shape) != SDM_OK) return 0;
+    return static_cast<size_t>(bwd_blocks(shape)) * 2 * shape->hd * sizeof(float);
+}
+
+extern "C" sdm_status sdm_rope_table(const sdm_rope_shape* shape, const double* inv_freq, float scale, float* table,
+                                     sdm_stream_t stream) {
+    const sdm_status st = check(shape);
+    if (st != SDM_OK) return st;
+    if (shape->rot_dim == 0) return SDM_OK;
+    if (inv_freq == nullptr || table == nullptr) return SDM_ERR_ARG;
+    if (!aligned16(table)) return SDM_ERR_ALIGN;
+    TableArgs a;
+    memset(&a, 0, sizeof(a));
+    a.n = shape->rot_dim / 2;
+    a.max_pos = shape->max_pos;
+    a.scale = scale;
+    a.table = table;
+    for (int i = 0; i < a.n; ++i) {
+        if (!std::isfinite(inv_freq[i])) return SDM_ERR_ARG;
+        double turn = inv_freq[i] / 6.283185307179586476925;
+        turn -= std::floor(turn);
+        // two parts of 32 bits: a double holds either exactly
+        const double hi = std::floor(std::ldexp(turn, 32));
+        a.turns[i] = (static_cast<uint64_t>(hi) << 32) + static_cast<uint64_t>(std::ldexp(std::ldexp(turn, 32) - hi, 32));
+    }
+    const int64_t blocks = (static_cast<int64_t>(a.n) * a.max_pos + 255) / 256;
+    if (blocks > 0x7FFFFFFF) return SDM_ERR_SHAPE;
+    const cudaError_t e = launch_dependent(rope_table_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0,
+                                           reinterpret_cast<cudaStream_t>(stream), a);
+    return e == cudaSuccess ? SDM_OK : SDM_ERR_CUDA;
+}
+
+extern "C" sdm_status sdm_qk_norm_rope(const sdm_rope_shape* shape, const void* q, int64_t q_ld, const void* k,
+                                       int64_t k_ld, const int32_t* positions, const float* table, const float* wq,
+                                       const float* wk, void* q_out, int64_t qo_ld, void* k_out, int64_t ko_ld,
+                                       uint32_t* status, sdm_stream_t stream) {
+    sdm_status st = check(shape);
+    if (st != SDM_OK) return st;
+    if (shape->tokens == 0) return SDM_OK;
+    if (positions == nullptr || (shape->rot_dim > 0 && table == nullptr)) return SDM_ERR_ARG;
+    if ((st = check_heads(shape, q, q_ld, shape->q_heads, false)) != SDM_OK) return st;
+    if ((st = check_heads(shape, k, k_ld, shape->k_heads, false)) != SDM_OK) return st;
+    if ((st = check_heads(shape, q_out, qo_ld, shape->q_heads, true)) != SDM_OK) return st;
+    if ((st = check_heads(shape, k_out, ko_ld, shape->k_heads, true)) != SDM_OK) return st;
+    if (!aligned16(table) || !aligned16(wq) || !aligned16(wk)) return SDM_ERR_ALIGN;
+    RopeArgs a;
+    fill(shape, &a);
+    a.q = q; a.q_ld = q_ld; a.k = k; a.k_ld = k_ld; a.pos = positions; a.table = table; a.wq = wq; a.wk = wk;
+    a.qo = q_out; a.qo_ld = qo_ld; a.ko = k_out; a.ko_ld = ko_ld; a.status = status;
+    const int lanes = head_lanes(shape->hd);
+    const int64_t blocks = (shape->tokens * (a.Hq + a.Hk) * lanes + kThreads - 1) / kThreads;
+    if (blocks > 0x7FFFFFFF) return SDM_ERR_SHAPE;
+    const cudaError_t e = by_type(shape, [&](auto t, auto u) {
+        return launch_dependent(rope_fwd_kernel<decltype(t), decltype(u)::value>, dim3(static_cast<unsigned>(blocks)),
+                                dim3(kThreads), 0, reinterpret_cast<cudaStream_t>(stream), a, lanes);
+    });
+    return e == cudaSuccess ? SDM_OK : SDM_ERR_CUDA;
+}
+
+extern "C" sdm_status sdm_qk_norm_rope_backward(const sdm_rope_shape* shape, const void* dq_out, int64_t dqo_ld,
+                                                const void* dk_out, int64_t dko_ld, const void* q, int64_t q_ld,
+                                                const void* k, int64_t k_ld, const int32_t* positions,
+                                                const float* table, const float* wq, const float* wk, void* dq,
+                                                int64_t dq_ld, void* dk, int64_t dk_ld, float* dwq, float* dwk,
+                                                void* ws, size_t ws_bytes, uint32_t* status, sdm_stream_t stream) {
+    sdm_status st = check(shape);
+    if (st != SDM_OK) return st;
+    if (shape->tokens > 0) {
+        if (positions == nullptr || (shape->rot_dim > 0 && table == nullptr)) return SDM_ERR_ARG;
+        if ((st = check_heads(shape, dq_out, dqo_ld, shape->q_heads, false)) != SDM_OK) return st;
+        if ((st = check_heads(shape, dk_out, dko_ld, shape->k_heads, false)) != SDM_OK) return st;
+        if ((st = check_heads(shape, q, q_ld, shape->q_heads, false)) != SDM_OK) return st;
+        if ((st = check_heads(shape, k, k_ld, shape->k_heads, false)) != SDM_OK) return st;
+        if ((st = check_heads(shape, dq, dq_ld, shape->q_heads, true)) != SDM_OK) return st;
+        if ((st = check_heads(shape, dk, dk_ld, shape->k_heads, true)) != SDM_OK) return st;
+    }
+    if (!aligned16(table) || !aligned16(wq) || !aligned16(wk)) return SDM_ERR_ALIGN;
+    const bool sums = shape->norm && (dwq != nullptr || dwk != nullptr);
+    if (sums && (ws == nullptr || !aligned16(ws) || ws_bytes < sdm_rope_workspace_bytes(shape))) return SDM_ERR_WORKSPACE;
+    RopeArgs a;
+    fill(shape, &a);
+    a.dqo = dq_out; a.dqo_ld = dqo_ld; a.dko = dk_out; a.dko_ld = dko_ld;
+    a.q = q; a.q_ld = q_ld; a.k = k; a.k_ld = k_ld; a.pos = positions; a.table = table; a.wq = wq; a.wk = wk;
+    a.qo = dq; a.qo_ld = dq_ld; a.ko = dk; a.ko_ld = dk_ld; a.status = status;
+    a.part = sums ? static_cast<float*>(ws) : nullptr;
+    const int lanes = head_lanes(shape->hd), blocks = bwd_blocks(shape);
+    const size_t smem = static_cast<size_t>(kThreads / lanes) * shape->hd * sizeof(float);
+    const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+    cudaError_t e = by_type(shape, [&](auto t, auto u) {
+        return launch_dependent(rope_bwd_kernel<decltype(t), decltype(u)::value>, dim3(static_cast<unsigned>(blocks)),
+                                dim3(kThreads), smem, cs, a, lanes);
+    });
+    if (e == cudaSuccess && sums)
+        e = launch_dependent(rope_dw_kernel, dim3(static_cast<unsigned>((2 * shape->hd + 31) / 32)), dim3(32, 32), 0, cs,
+                             static_cast<const float*>(ws), blocks, shape->hd, dwq, dwk);
+    return e == cudaSuccess ? SDM_OK : SDM_ERR_CUDA;
+}
