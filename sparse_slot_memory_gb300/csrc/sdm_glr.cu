@@ -48,7 +48,8 @@ struct GlrArgs {
     int64_t rows, len;        // len: rows of every sequence where offsets is null
     int64_t x_ld, g_ld, y_ld, dy_ld, dx_ld, dg_ld;
     int P, D, H, gw;
-    int tiles, tile_cols, tiles_per_head, heads_per_tile;
+    int tiles, tile_cols, tiles_per_head;
+    int cluster;              // blocks that walk a sequence together
 };
 
 // A tile's columns and this lane's place in it.
@@ -103,16 +104,66 @@ __device__ __forceinline__ void sequence(const GlrArgs& a, int p, int64_t& b, in
     if ((lo < 0 || hi > a.rows || lo > hi) && a.status != nullptr && threadIdx.x == 0) atomicOr(a.status, SDM_DEV_BAD_OFFSET);
 }
 
-// exp of the lane's gates of one row
-template <bool PERCH, typename GT>
-__device__ __forceinline__ void gates(const GT* g, float (&o)[4]) {
-    if constexpr (PERCH) {
-        ld4(g, o);
+// The gates of one row as they lie in memory: the lane's four, or its head's one.
+template <typename GT, bool PERCH>
+struct RawGate;
+template <typename GT>
+struct RawGate<GT, true> {
+    static constexpr int n = 4;
+    Raw4<GT> v;
+    __device__ __forceinline__ void ld(const GT* p) { v.ld(p); }
+    __device__ __forceinline__ void zero() { v.zero(); }
+    __device__ __forceinline__ void exps(float (&o)[4]) const {
+        v.get(o);
 #pragma unroll
         for (int i = 0; i < 4; ++i) o[i] = expf(o[i]);
-    } else {
-        o[0] = o[1] = o[2] = o[3] = expf(widen(__ldg(g)));
     }
+};
+template <typename GT>
+struct RawGate<GT, false> {
+    static constexpr int n = 1;
+    GT v;
+    __device__ __forceinline__ void ld(const GT* p) { v = __ldg(p); }
+    __device__ __forceinline__ void zero() { v = GT(0.f); }
+    __device__ __forceinline__ void exps(float (&o)[1]) const { o[0] = expf(widen(v)); }
+};
+
+// kRows rows of a warp; those from `live` on are the identity (gate 1, nothing added)
+template <typename XT, typename GT, bool PERCH>
+struct Span {
+    Raw4<XT> x[kRows];
+    RawGate<GT, PERCH> g[kRows];
+    __device__ __forceinline__ void ld(const XT* xp, int64_t x_ld, const GT* gp, int64_t g_ld, int live) {
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+            if (i < live) {
+                g[i].ld(gp + i * g_ld);
+                x[i].ld(xp + i * x_ld);
+            } else {
+                g[i].zero();
+                x[i].zero();
+            }
+        }
+    }
+};
+
+// How many of the kRows rows from t on lie before n.
+__device__ __forceinline__ int live_rows(int64_t t, int64_t n) {
+    return static_cast<int>(min(max(n - t, int64_t(0)), int64_t(kRows)));
+}
+
+// The blocks of a cluster: this one's rank, and stores into another's shared memory.
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+__device__ __forceinline__ void st_remote(const float* p, uint32_t rank, float v) {
+    uint32_t a = static_cast<uint32_t>(__cvta_generic_to_shared(p));
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(a), "r"(rank));
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory");
 }
 
 __device__ __forceinline__ void set4(float (&o)[4], float v) { o[0] = o[1] = o[2] = o[3] = v; }
@@ -126,63 +177,112 @@ __device__ __forceinline__ void join(float (&h)[4], const float* A, const float*
     for (int i = 0; i < 4; ++i) h[i] = fmaf(p[i], h[i], q[i]);
 }
 
-template <typename XT, typename GT, bool PERCH>
-__global__ void __launch_bounds__(kWarps * 32) glr_fwd_kernel(const GlrArgs a) {
+// Joins the block's warps' pairs and writes the block's pair into every block of the cluster, at its own rank.
+__device__ __forceinline__ void share_pair(const float (*A)[kTileCols], const float (*B)[kTileCols], float (*cA)[kTileCols],
+                                           float (*cB)[kTileCols], uint32_t rank, int K, bool reverse) {
+    if (threadIdx.x >= kTileCols) return;
+    const int c = threadIdx.x;
+    float pa = 1.f, pb = 0.f;
+#pragma unroll
+    for (int j = 0; j < kWarps; ++j) {
+        const int k = reverse ? kWarps - 1 - j : j;
+        pb = fmaf(A[k][c], pb, B[k][c]);
+        pa *= A[k][c];
+    }
+    for (int k = 0; k < K; ++k) {
+        st_remote(&cA[rank][c], k, pa);
+        st_remote(&cB[rank][c], k, pb);
+    }
+}
+
+constexpr int kMaxCluster = 8;
+
+template <typename XT, typename GT, bool PERCH, bool CLUSTER>
+__global__ void __launch_bounds__(kWarps * 32, 2) glr_fwd_kernel(const GlrArgs a) {
     __shared__ __align__(16) float sA[2][kWarps][kTileCols], sB[2][kWarps][kTileCols];
+    __shared__ __align__(16) float cA[2][CLUSTER ? kMaxCluster : 1][kTileCols], cB[2][CLUSTER ? kMaxCluster : 1][kTileCols];
+    if (CLUSTER) cluster_arrive();
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-    const int p = blockIdx.x / a.tiles;
-    const Tile tl = tile_of<PERCH>(a, blockIdx.x - p * a.tiles, lane);
+    const int K = CLUSTER ? a.cluster : 1, rank = CLUSTER ? cluster_rank() : 0;
+    const int unit = blockIdx.x / K;
+    const int p = unit / a.tiles;
+    const Tile tl = tile_of<PERCH>(a, unit - p * a.tiles, lane);
     int64_t b, n;
     sequence(a, p, b, n);
     float h[4] = {0.f, 0.f, 0.f, 0.f};   // the state before the step's rows
     if (a.h0 != nullptr) ld4(a.h0 + static_cast<int64_t>(p) * a.D + tl.col, h);
-    const XT* const x = static_cast<const XT*>(a.x) + b * a.x_ld + tl.col;
-    const GT* const g = static_cast<const GT*>(a.g) + b * a.g_ld + tl.gate;
-    XT* const y = static_cast<XT*>(a.y) + b * a.y_ld + tl.col;
+    const int64_t step = static_cast<int64_t>(K) * SDM_GLR_CHUNK;
+    int64_t t = rank * SDM_GLR_CHUNK + w * kRows;   // the warp's first row of the step
+    const XT* x = static_cast<const XT*>(a.x) + (b + t) * a.x_ld + tl.col;
+    const GT* g = static_cast<const GT*>(a.g) + (b + t) * a.g_ld + tl.gate;
+    XT* y = static_cast<XT*>(a.y) + (b + t) * a.y_ld + tl.col;
     float* const st = a.states == nullptr ? nullptr : a.states + (b / SDM_GLR_CHUNK + p) * a.D + tl.col;
+    Span<XT, GT, PERCH> next;
+    int live = live_rows(t, n);
+    next.ld(x, a.x_ld, g, a.g_ld, live);
+    if (CLUSTER) cluster_wait();   // every block of the cluster runs
     int buf = 0;
-    for (int64_t t0 = 0; t0 < n; t0 += kWarps * kRows, buf ^= 1) {
-        if (st != nullptr && w == 0 && tl.on) st4(st + t0 / SDM_GLR_CHUNK * a.D, h);
-        const int64_t t = t0 + w * kRows;
-        float ga[kRows][4], xv[kRows][4], A[4], B[4];
+    for (int64_t t0 = 0; t0 < n; t0 += step, t += step, buf ^= 1) {
+        float ga[kRows][RawGate<GT, PERCH>::n], A[4], B[4];
+        Raw4<XT> xr[kRows];
         set4(A, 1.f);
         set4(B, 0.f);
 #pragma unroll
         for (int i = 0; i < kRows; ++i) {
-            if (t + i < n) {
-                gates<PERCH>(g + (t + i) * a.g_ld, ga[i]);
-                ld4(x + (t + i) * a.x_ld, xv[i]);
-            } else {   // past the end: the identity
-                set4(ga[i], 1.f);
-                set4(xv[i], 0.f);
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < kRows; ++i)
+            next.g[i].exps(ga[i]);
+            xr[i] = next.x[i];
+            float xv[4];
+            xr[i].get(xv);
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-                A[c] *= ga[i][c];
-                B[c] = fmaf(ga[i][c], B[c], xv[i][c]);
+                const float e = ga[i][PERCH ? c : 0];
+                A[c] *= e;
+                B[c] = fmaf(e, B[c], xv[c]);
             }
+        }
         st4(&sA[buf][w][lane * 4], A);
         st4(&sB[buf][w][lane * 4], B);
+        x += step * a.x_ld;
+        g += step * a.g_ld;
+        const int nlive = live_rows(t + step, n);
+        next.ld(x, a.x_ld, g, a.g_ld, nlive);   // in flight over the exchange
         __syncthreads();   // the other buffer is written next: one barrier a step
         float hw[4];
-        for (int j = 0; j < kWarps; ++j) {
-            if (j == w)
+        if (CLUSTER) {
+            share_pair(sA[buf], sB[buf], cA[buf], cB[buf], rank, K, false);
+            cluster_arrive();
+            cluster_wait();
+            for (int k = 0; k < K; ++k) {
+                if (k == rank)
 #pragma unroll
-                for (int c = 0; c < 4; ++c) hw[c] = h[c];
-            join(h, &sA[buf][j][lane * 4], &sB[buf][j][lane * 4]);
+                    for (int c = 0; c < 4; ++c) hw[c] = h[c];
+                join(h, &cA[buf][k][lane * 4], &cB[buf][k][lane * 4]);
+            }
+            if (st != nullptr && w == 0 && tl.on && t < n) st4(st + t / SDM_GLR_CHUNK * a.D, hw);
+            for (int j = 0; j < w; ++j) join(hw, &sA[buf][j][lane * 4], &sB[buf][j][lane * 4]);
+        } else {
+            if (st != nullptr && w == 0 && tl.on) st4(st + t0 / SDM_GLR_CHUNK * a.D, h);
+#pragma unroll
+            for (int j = 0; j < kWarps; ++j) {
+                if (j == w)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) hw[c] = h[c];
+                join(h, &sA[buf][j][lane * 4], &sB[buf][j][lane * 4]);
+            }
         }
 #pragma unroll
         for (int i = 0; i < kRows; ++i) {
+            float xv[4];
+            xr[i].get(xv);
 #pragma unroll
-            for (int c = 0; c < 4; ++c) hw[c] = fmaf(ga[i][c], hw[c], xv[i][c]);
-            if (tl.on && t + i < n) st4(y + (t + i) * a.y_ld, hw);
+            for (int c = 0; c < 4; ++c) hw[c] = fmaf(ga[i][PERCH ? c : 0], hw[c], xv[c]);
+            if (tl.on && i < live) st4(y + i * a.y_ld, hw);
         }
+        y += step * a.y_ld;
+        live = nlive;
     }
-    if (a.hT != nullptr && w == 0 && tl.on) st4(a.hT + static_cast<int64_t>(p) * a.D + tl.col, h);
+    if (a.hT != nullptr && rank == 0 && w == 0 && tl.on) st4(a.hT + static_cast<int64_t>(p) * a.D + tl.col, h);
 }
 
 // The sum of v over the lanes of its head in the tile, in the head's first lane.
@@ -195,97 +295,131 @@ __device__ __forceinline__ float head_sum(float v, int seg) {
     return v;
 }
 
-template <typename XT, typename GT, bool PERCH>
-__global__ void __launch_bounds__(kWarps * 32) glr_bwd_kernel(const GlrArgs a) {
+template <typename XT, typename GT, bool PERCH, bool CLUSTER>
+__global__ void __launch_bounds__(kWarps * 32, 2) glr_bwd_kernel(const GlrArgs a) {
     __shared__ __align__(16) float sA[2][kWarps][kTileCols], sF[2][kWarps][kTileCols], sR[2][kWarps][kTileCols];
+    __shared__ __align__(16) float cA[2][CLUSTER ? kMaxCluster : 1][kTileCols], cR[2][CLUSTER ? kMaxCluster : 1][kTileCols];
+    if (CLUSTER) cluster_arrive();
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-    const int p = blockIdx.x / a.tiles;
-    const Tile tl = tile_of<PERCH>(a, blockIdx.x - p * a.tiles, lane);
+    const int K = CLUSTER ? a.cluster : 1, rank = CLUSTER ? cluster_rank() : 0;
+    const int unit = blockIdx.x / K;
+    const int p = unit / a.tiles;
+    const Tile tl = tile_of<PERCH>(a, unit - p * a.tiles, lane);
     int64_t b, n;
     sequence(a, p, b, n);
     float m[4] = {0.f, 0.f, 0.f, 0.f};   // the gradient of the state after the step's rows
     if (a.dhT != nullptr) ld4(a.dhT + static_cast<int64_t>(p) * a.D + tl.col, m);
-    const XT* const x = static_cast<const XT*>(a.x) + b * a.x_ld + tl.col;
-    const GT* const g = static_cast<const GT*>(a.g) + b * a.g_ld + tl.gate;
-    const XT* const dy = static_cast<const XT*>(a.dy) + b * a.dy_ld + tl.col;
-    XT* const dx = static_cast<XT*>(a.dx) + b * a.dx_ld + tl.col;
-    GT* const dg = static_cast<GT*>(a.dg) + b * a.dg_ld + tl.gate;
     const float* const st = a.states + (b / SDM_GLR_CHUNK + p) * a.D + tl.col;
+    const int64_t step = static_cast<int64_t>(K) * SDM_GLR_CHUNK;
+    if (CLUSTER) cluster_wait();
     int buf = 0;
-    for (int64_t k = (n + SDM_GLR_CHUNK - 1) / SDM_GLR_CHUNK - 1; k >= 0; --k, buf ^= 1) {
-        const int64_t t = k * SDM_GLR_CHUNK + w * kRows;
-        float ga[kRows][4], xv[kRows][4], dv[kRows][4], A[4], F[4], R[4], h[4];
-        ld4(st + k * a.D, h);
+    for (int64_t t0 = (n + step - 1) / step * step - step; t0 >= 0; t0 -= step, buf ^= 1) {
+        const int64_t tc = t0 + rank * SDM_GLR_CHUNK, t = tc + w * kRows;
+        const int live = live_rows(t, n);
+        const XT* const x = static_cast<const XT*>(a.x) + (b + t) * a.x_ld + tl.col;
+        const GT* const g = static_cast<const GT*>(a.g) + (b + t) * a.g_ld + tl.gate;
+        const XT* const dy = static_cast<const XT*>(a.dy) + (b + t) * a.dy_ld + tl.col;
+        XT* const dx = static_cast<XT*>(a.dx) + (b + t) * a.dx_ld + tl.col;
+        GT* const dg = static_cast<GT*>(a.dg) + (b + t) * a.dg_ld + tl.gate;
+        float ga[kRows][RawGate<GT, PERCH>::n], A[4], F[4], R[4], h[4] = {0.f, 0.f, 0.f, 0.f};
+        Raw4<XT> xr[kRows], dr[kRows];
+        {
+            Span<XT, GT, PERCH> s;
+            s.ld(x, a.x_ld, g, a.g_ld, live);
+#pragma unroll
+            for (int i = 0; i < kRows; ++i) {
+                if (i < live)
+                    dr[i].ld(dy + i * a.dy_ld);
+                else
+                    dr[i].zero();
+            }
+            if (tc < n) ld4(st + tc / SDM_GLR_CHUNK * a.D, h);
+#pragma unroll
+            for (int i = 0; i < kRows; ++i) {
+                s.g[i].exps(ga[i]);
+                xr[i] = s.x[i];
+            }
+        }
         set4(A, 1.f);
         set4(F, 0.f);
         set4(R, 0.f);
 #pragma unroll
         for (int i = 0; i < kRows; ++i) {
-            if (t + i < n) {
-                gates<PERCH>(g + (t + i) * a.g_ld, ga[i]);
-                ld4(x + (t + i) * a.x_ld, xv[i]);
-                ld4(dy + (t + i) * a.dy_ld, dv[i]);
-            } else {
-                set4(ga[i], 1.f);
-                set4(xv[i], 0.f);
-                set4(dv[i], 0.f);
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < kRows; ++i)
+            float xv[4], dv[4];
+            xr[i].get(xv);
+            dr[kRows - 1 - i].get(dv);
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-                A[c] *= ga[i][c];
-                F[c] = fmaf(ga[i][c], F[c], xv[i][c]);
-                R[c] = ga[kRows - 1 - i][c] * (dv[kRows - 1 - i][c] + R[c]);
+                const float e = ga[i][PERCH ? c : 0];
+                A[c] *= e;
+                F[c] = fmaf(e, F[c], xv[c]);
+                R[c] = ga[kRows - 1 - i][PERCH ? c : 0] * (dv[c] + R[c]);
             }
+        }
         st4(&sA[buf][w][lane * 4], A);
         st4(&sF[buf][w][lane * 4], F);
         st4(&sR[buf][w][lane * 4], R);
         __syncthreads();
         float mw[4];
-        for (int j = 0; j < w; ++j) join(h, &sA[buf][j][lane * 4], &sF[buf][j][lane * 4]);
-        for (int j = kWarps - 1; j >= 0; --j) {
-            if (j == w)
+        if (CLUSTER) {
+            share_pair(sA[buf], sR[buf], cA[buf], cR[buf], rank, K, true);
+            cluster_arrive();
+            for (int j = 0; j < w; ++j) join(h, &sA[buf][j][lane * 4], &sF[buf][j][lane * 4]);
+            cluster_wait();
+            for (int k = K - 1; k >= 0; --k) {
+                if (k == rank)
 #pragma unroll
-                for (int c = 0; c < 4; ++c) mw[c] = m[c];
-            join(m, &sA[buf][j][lane * 4], &sR[buf][j][lane * 4]);
+                    for (int c = 0; c < 4; ++c) mw[c] = m[c];
+                join(m, &cA[buf][k][lane * 4], &cR[buf][k][lane * 4]);
+            }
+            for (int j = kWarps - 1; j > w; --j) join(mw, &sA[buf][j][lane * 4], &sR[buf][j][lane * 4]);
+        } else {
+            for (int j = 0; j < w; ++j) join(h, &sA[buf][j][lane * 4], &sF[buf][j][lane * 4]);
+#pragma unroll
+            for (int j = kWarps - 1; j >= 0; --j) {
+                if (j == w)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) mw[c] = m[c];
+                join(m, &sA[buf][j][lane * 4], &sR[buf][j][lane * 4]);
+            }
         }
-        // xv becomes the state before each row
+        float hp[kRows][4];   // the state before each row
 #pragma unroll
-        for (int i = 0; i < kRows; ++i)
+        for (int i = 0; i < kRows; ++i) {
+            float xv[4];
+            xr[i].get(xv);
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-                const float next = fmaf(ga[i][c], h[c], xv[i][c]);
-                xv[i][c] = h[c];
-                h[c] = next;
+                hp[i][c] = h[c];
+                h[c] = fmaf(ga[i][PERCH ? c : 0], h[c], xv[c]);
             }
+        }
 #pragma unroll
         for (int i = kRows - 1; i >= 0; --i) {
-            float l[4], d[4];
+            float l[4], d[4], dv[4];
+            dr[i].get(dv);
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-                l[c] = dv[i][c] + mw[c];
-                mw[c] = ga[i][c] * l[c];
-                d[c] = mw[c] * xv[i][c];
+                l[c] = dv[c] + mw[c];
+                mw[c] = ga[i][PERCH ? c : 0] * l[c];
+                d[c] = mw[c] * hp[i][c];
             }
-            const bool live = t + i < n;
-            if (tl.on && live) st4(dx + (t + i) * a.dx_ld, l);
+            if (tl.on && i < live) st4(dx + i * a.dx_ld, l);
             if constexpr (PERCH) {
-                if (tl.on && live) st4(dg + (t + i) * a.dg_ld, d);
+                if (tl.on && i < live) st4(dg + i * a.dg_ld, d);
             } else {
                 const float s = head_sum(tl.on ? (d[0] + d[1]) + (d[2] + d[3]) : 0.f, tl.seg);
-                if (tl.lead && live) {
+                if (tl.lead && i < live) {
                     if (a.tiles_per_head == 1)
-                        st1(dg + (t + i) * a.dg_ld, s);
+                        st1(dg + i * a.dg_ld, s);
                     else
                         a.part[(tl.sub * a.rows + b + t + i) * a.H + tl.gate] = s;
                 }
             }
         }
     }
-    if (a.dh0 != nullptr && w == 0 && tl.on) st4(a.dh0 + static_cast<int64_t>(p) * a.D + tl.col, m);
+    if (a.dh0 != nullptr && rank == 0 && w == 0 && tl.on) st4(a.dh0 + static_cast<int64_t>(p) * a.D + tl.col, m);
 }
 
 // dg of a head wider than a tile: the sum of its tiles' parts, in tile order.
@@ -322,7 +456,7 @@ __global__ void __launch_bounds__(256) glr_step_kernel(const StepArgs a) {
     const int64_t r = u / quads;
     const int col = static_cast<int>(u - r * quads) * 4;
     const int64_t s = a.slots == nullptr ? r : static_cast<int64_t>(__ldg(a.slots + r));
-    float x[4], ga[4], h[4];
+    float x[4], ga[RawGate<GT, PERCH>::n], h[4];
     XT* const y = static_cast<XT*>(a.y) + r * a.y_ld + col;
     if (s < 0 || s >= a.states) {   // a padding row, or an id that names no state
         if (s >= a.states && a.status != nullptr) atomicOr(a.status, kDevBadSlot);
@@ -333,9 +467,11 @@ __global__ void __launch_bounds__(256) glr_step_kernel(const StepArgs a) {
     float* const st = a.state + s * a.s_ld + col;
     ld4cg(st, h);
     ld4(static_cast<const XT*>(a.x) + r * a.x_ld + col, x);
-    gates<PERCH>(static_cast<const GT*>(a.g) + r * a.g_ld + (PERCH ? col : col / a.gw), ga);
+    RawGate<GT, PERCH> gr;
+    gr.ld(static_cast<const GT*>(a.g) + r * a.g_ld + (PERCH ? col : col / a.gw));
+    gr.exps(ga);
 #pragma unroll
-    for (int c = 0; c < 4; ++c) h[c] = fmaf(ga[c], h[c], x[c]);
+    for (int c = 0; c < 4; ++c) h[c] = fmaf(ga[PERCH ? c : 0], h[c], x[c]);
     st4(st, h);
     st4(y, h);
 }
@@ -391,6 +527,36 @@ size_t part_bytes(const GlrArgs& a) {
     return a.tiles_per_head == 1 ? 0 : static_cast<size_t>(a.tiles_per_head) * a.rows * a.H * sizeof(float);
 }
 
+// Blocks that share a sequence's rows: enough of them that the SMs are full, and no more than the sequences have
+// steps of SDM_GLR_CHUNK rows.
+int cluster_of(const sdm_glr_shape* s, const GlrArgs& a) {
+    if (const char* e = getenv("GLR_K")) return atoi(e);
+    const int64_t units = static_cast<int64_t>(a.tiles) * a.P, steps = (a.len + SDM_GLR_CHUNK - 1) / SDM_GLR_CHUNK;
+    int k = 1;
+    while (k < kMaxCluster && units * k < 304 && k < steps) k *= 2;
+    return k;
+}
+
+// A launch of clusters of `cluster` blocks (a multiple of them), as a programmatic dependent.
+template <typename... Params, typename... Args>
+cudaError_t launch_cluster(void (*kernel)(Params...), dim3 grid, dim3 block, int cluster, cudaStream_t stream,
+                           Args&&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
+
 // Calls f(x type, g type, per-channel gates) with the shape's types.
 template <typename F>
 cudaError_t by_type(const sdm_glr_shape* s, F f) {
@@ -434,13 +600,17 @@ extern "C" sdm_status sdm_glr_forward(const sdm_glr_shape* shape, const void* x,
         if (!aligned16(p)) return SDM_ERR_ALIGN;
     GlrArgs a;
     geometry(shape, &a);
-    if (static_cast<int64_t>(a.tiles) * a.P > 0x7FFFFFFF) return SDM_ERR_SHAPE;
+    if (static_cast<int64_t>(a.tiles) * a.P > 0x7FFFFFFF / kMaxCluster) return SDM_ERR_SHAPE;
+    a.cluster = cluster_of(shape, a);
     a.x = x; a.x_ld = x_ld; a.g = g; a.g_ld = g_ld; a.y = y; a.y_ld = y_ld;
     a.offsets = offsets; a.h0 = h0; a.hT = hT; a.states = states; a.status = status;
     const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
     const cudaError_t e = by_type(shape, [&](auto xt, auto gt, auto perch) {
-        return launch_dependent(glr_fwd_kernel<decltype(xt), decltype(gt), decltype(perch)::value>,
-                                dim3(static_cast<unsigned>(a.tiles * a.P)), dim3(kWarps * 32), 0, cs, a);
+        constexpr bool PC = decltype(perch)::value;
+        const dim3 grid(static_cast<unsigned>(a.tiles) * a.P * a.cluster), block(kWarps * 32);
+        if (a.cluster > 1)
+            return launch_cluster(glr_fwd_kernel<decltype(xt), decltype(gt), PC, true>, grid, block, a.cluster, cs, a);
+        return launch_dependent(glr_fwd_kernel<decltype(xt), decltype(gt), PC, false>, grid, block, 0, cs, a);
     });
     return e == cudaSuccess ? SDM_OK : SDM_ERR_CUDA;
 }
@@ -467,7 +637,8 @@ extern "C" sdm_status sdm_glr_backward(const sdm_glr_shape* shape, const void* x
         if (!aligned16(p)) return SDM_ERR_ALIGN;
     GlrArgs a;
     geometry(shape, &a);
-    if (static_cast<int64_t>(a.tiles) * a.P > 0x7FFFFFFF) return SDM_ERR_SHAPE;
+    if (static_cast<int64_t>(a.tiles) * a.P > 0x7FFFFFFF / kMaxCluster) return SDM_ERR_SHAPE;
+    a.cluster = cluster_of(shape, a);
     if (part_bytes(a) > 0 && (ws == nullptr || !aligned16(ws) || ws_bytes < part_bytes(a))) return SDM_ERR_WORKSPACE;
     a.x = x; a.x_ld = x_ld; a.g = g; a.g_ld = g_ld; a.dy = dy; a.dy_ld = dy_ld;
     a.dx = dx; a.dx_ld = dx_ld; a.dg = dg; a.dg_ld = dg_ld;
@@ -475,8 +646,11 @@ extern "C" sdm_status sdm_glr_backward(const sdm_glr_shape* shape, const void* x
     a.part = static_cast<float*>(ws);
     const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t e = by_type(shape, [&](auto xt, auto gt, auto perch) {
-        return launch_dependent(glr_bwd_kernel<decltype(xt), decltype(gt), decltype(perch)::value>,
-                                dim3(static_cast<unsigned>(a.tiles * a.P)), dim3(kWarps * 32), 0, cs, a);
+        constexpr bool PC = decltype(perch)::value;
+        const dim3 grid(static_cast<unsigned>(a.tiles) * a.P * a.cluster), block(kWarps * 32);
+        if (a.cluster > 1)
+            return launch_cluster(glr_bwd_kernel<decltype(xt), decltype(gt), PC, true>, grid, block, a.cluster, cs, a);
+        return launch_dependent(glr_bwd_kernel<decltype(xt), decltype(gt), PC, false>, grid, block, 0, cs, a);
     });
     if (e == cudaSuccess && part_bytes(a) > 0) {
         const int64_t blocks = std::min<int64_t>((a.rows * a.H + 255) / 256, 4096);
