@@ -104,28 +104,93 @@ __device__ __forceinline__ void sequence(const GlrArgs& a, int p, int64_t& b, in
     if ((lo < 0 || hi > a.rows || lo > hi) && a.status != nullptr && threadIdx.x == 0) atomicOr(a.status, SDM_DEV_BAD_OFFSET);
 }
 
+// Four channels as two pairs of float32: one instruction multiplies or multiply-adds a pair (each half rounded as
+// the scalar instruction rounds it).
+struct Quad {
+    uint64_t lo, hi;
+};
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+    uint64_t o;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(o) : "f"(a), "f"(b));
+    return o;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t o;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(o) : "l"(a), "l"(b), "l"(c));
+    return o;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t o;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(o) : "l"(a), "l"(b));
+    return o;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t o;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(o) : "l"(a), "l"(b));
+    return o;
+}
+__device__ __forceinline__ Quad quad(const float (&v)[4]) { return {pack2(v[0], v[1]), pack2(v[2], v[3])}; }
+__device__ __forceinline__ Quad quad(float v) { return {pack2(v, v), pack2(v, v)}; }
+__device__ __forceinline__ void floats(const Quad& q, float (&v)[4]) {
+    unpack2(q.lo, v[0], v[1]);
+    unpack2(q.hi, v[2], v[3]);
+}
+__device__ __forceinline__ Quad fma4(const Quad& a, const Quad& b, const Quad& c) { return {fma2(a.lo, b.lo, c.lo), fma2(a.hi, b.hi, c.hi)}; }
+__device__ __forceinline__ Quad mul4(const Quad& a, const Quad& b) { return {mul2(a.lo, b.lo), mul2(a.hi, b.hi)}; }
+__device__ __forceinline__ Quad add4(const Quad& a, const Quad& b) { return {add2(a.lo, b.lo), add2(a.hi, b.hi)}; }
+template <typename T>
+__device__ __forceinline__ Quad quad(const Raw4<T>& r) {
+    float v[4];
+    r.get(v);
+    return quad(v);
+}
+__device__ __forceinline__ Raw4<float> load4(const float* p) {
+    Raw4<float> r;
+    r.ld(p);
+    return r;
+}
+__device__ __forceinline__ Quad quad(const float* p) {   // 16 bytes of shared memory
+    float v[4];
+    get4(p, v);
+    return quad(v);
+}
+template <typename T>
+__device__ __forceinline__ void st4(T* p, const Quad& q) {
+    float v[4];
+    floats(q, v);
+    rows::st4(p, v);
+}
+
+// exp of a gate as 2^(g log2 e): within 4 u + |g| u (u = 2^-24), and exactly 0 and 1 at -inf and 0
+__device__ __forceinline__ float exp_gate(float g) {
+    float o;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(o) : "f"(g * 1.44269504088896341f));
+    return o;
+}
+
 // The gates of one row as they lie in memory: the lane's four, or its head's one.
 template <typename GT, bool PERCH>
 struct RawGate;
 template <typename GT>
 struct RawGate<GT, true> {
-    static constexpr int n = 4;
     Raw4<GT> v;
     __device__ __forceinline__ void ld(const GT* p) { v.ld(p); }
     __device__ __forceinline__ void zero() { v.zero(); }
-    __device__ __forceinline__ void exps(float (&o)[4]) const {
+    __device__ __forceinline__ Quad exps() const {
+        float o[4];
         v.get(o);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) o[i] = expf(o[i]);
+        for (int i = 0; i < 4; ++i) o[i] = exp_gate(o[i]);
+        return quad(o);
     }
 };
 template <typename GT>
 struct RawGate<GT, false> {
-    static constexpr int n = 1;
     GT v;
     __device__ __forceinline__ void ld(const GT* p) { v = __ldg(p); }
     __device__ __forceinline__ void zero() { v = GT(0.f); }
-    __device__ __forceinline__ void exps(float (&o)[1]) const { o[0] = expf(widen(v)); }
+    __device__ __forceinline__ Quad exps() const { return quad(exp_gate(widen(v))); }
 };
 
 // kRows rows of a warp; those from `live` on are the identity (gate 1, nothing added)
@@ -166,16 +231,8 @@ __device__ __forceinline__ void st_remote(const float* p, uint32_t rank, float v
     asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory");
 }
 
-__device__ __forceinline__ void set4(float (&o)[4], float v) { o[0] = o[1] = o[2] = o[3] = v; }
-
-// h = A h + B from a warp's pair in shared memory
-__device__ __forceinline__ void join(float (&h)[4], const float* A, const float* B) {
-    float p[4], q[4];
-    get4(A, p);
-    get4(B, q);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) h[i] = fmaf(p[i], h[i], q[i]);
-}
+// h = A h + B from a pair in shared memory
+__device__ __forceinline__ void join(Quad& h, const float* A, const float* B) { h = fma4(quad(A), h, quad(B)); }
 
 // Joins the block's warps' pairs and writes the block's pair into every block of the cluster, at its own rank.
 __device__ __forceinline__ void share_pair(const float (*A)[kTileCols], const float (*B)[kTileCols], float (*cA)[kTileCols],
@@ -210,8 +267,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2) glr_fwd_kernel(const GlrArgs a
     const Tile tl = tile_of<PERCH>(a, unit - p * a.tiles, lane);
     int64_t b, n;
     sequence(a, p, b, n);
-    float h[4] = {0.f, 0.f, 0.f, 0.f};   // the state before the step's rows
-    if (a.h0 != nullptr) ld4(a.h0 + static_cast<int64_t>(p) * a.D + tl.col, h);
+    Quad h = quad(0.f);   // the state before the step's rows
+    if (a.h0 != nullptr) h = quad(load4(a.h0 + static_cast<int64_t>(p) * a.D + tl.col));
     const int64_t step = static_cast<int64_t>(K) * SDM_GLR_CHUNK;
     int64_t t = rank * SDM_GLR_CHUNK + w * kRows;   // the warp's first row of the step
     const XT* x = static_cast<const XT*>(a.x) + (b + t) * a.x_ld + tl.col;
@@ -224,22 +281,14 @@ __global__ void __launch_bounds__(kWarps * 32, 2) glr_fwd_kernel(const GlrArgs a
     if (CLUSTER) cluster_wait();   // every block of the cluster runs
     int buf = 0;
     for (int64_t t0 = 0; t0 < n; t0 += step, t += step, buf ^= 1) {
-        float ga[kRows][RawGate<GT, PERCH>::n], A[4], B[4];
+        Quad ga[kRows], A = quad(1.f), B = quad(0.f);
         Raw4<XT> xr[kRows];
-        set4(A, 1.f);
-        set4(B, 0.f);
 #pragma unroll
         for (int i = 0; i < kRows; ++i) {
-            next.g[i].exps(ga[i]);
+            ga[i] = next.g[i].exps();
             xr[i] = next.x[i];
-            float xv[4];
-            xr[i].get(xv);
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const float e = ga[i][PERCH ? c : 0];
-                A[c] *= e;
-                B[c] = fmaf(e, B[c], xv[c]);
-            }
+            A = mul4(A, ga[i]);
+            B = fma4(ga[i], B, quad(xr[i]));
         }
         st4(&sA[buf][w][lane * 4], A);
         st4(&sB[buf][w][lane * 4], B);
@@ -248,15 +297,13 @@ __global__ void __launch_bounds__(kWarps * 32, 2) glr_fwd_kernel(const GlrArgs a
         const int nlive = live_rows(t + step, n);
         next.ld(x, a.x_ld, g, a.g_ld, nlive);   // in flight over the exchange
         __syncthreads();   // the other buffer is written next: one barrier a step
-        float hw[4];
+        Quad hw = h;
         if (CLUSTER) {
             share_pair(sA[buf], sB[buf], cA[buf], cB[buf], rank, K, false);
             cluster_arrive();
             cluster_wait();
             for (int k = 0; k < K; ++k) {
-                if (k == rank)
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) hw[c] = h[c];
+                if (k == rank) hw = h;
                 join(h, &cA[buf][k][lane * 4], &cB[buf][k][lane * 4]);
             }
             if (st != nullptr && w == 0 && tl.on && t < n) st4(st + t / SDM_GLR_CHUNK * a.D, hw);
@@ -265,18 +312,13 @@ __global__ void __launch_bounds__(kWarps * 32, 2) glr_fwd_kernel(const GlrArgs a
             if (st != nullptr && w == 0 && tl.on) st4(st + t0 / SDM_GLR_CHUNK * a.D, h);
 #pragma unroll
             for (int j = 0; j < kWarps; ++j) {
-                if (j == w)
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) hw[c] = h[c];
+                if (j == w) hw = h;
                 join(h, &sA[buf][j][lane * 4], &sB[buf][j][lane * 4]);
             }
         }
 #pragma unroll
         for (int i = 0; i < kRows; ++i) {
-            float xv[4];
-            xr[i].get(xv);
-#pragma unroll
-            for (int c = 0; c < 4; ++c) hw[c] = fmaf(ga[i][PERCH ? c : 0], hw[c], xv[c]);
+            hw = fma4(ga[i], hw, quad(xr[i]));
             if (tl.on && i < live) st4(y + i * a.y_ld, hw);
         }
         y += step * a.y_ld;
@@ -308,8 +350,8 @@ __global__ void __launch_bounds__(kWarps * 32, 2) glr_bwd_kernel(const GlrArgs a
     const Tile tl = tile_of<PERCH>(a, unit - p * a.tiles, lane);
     int64_t b, n;
     sequence(a, p, b, n);
-    float m[4] = {0.f, 0.f, 0.f, 0.f};   // the gradient of the state after the step's rows
-    if (a.dhT != nullptr) ld4(a.dhT + static_cast<int64_t>(p) * a.D + tl.col, m);
+    Quad m = quad(0.f);   // the gradient of the state after the step's rows
+    if (a.dhT != nullptr) m = quad(load4(a.dhT + static_cast<int64_t>(p) * a.D + tl.col));
     const float* const st = a.states + (b / SDM_GLR_CHUNK + p) * a.D + tl.col;
     const int64_t step = static_cast<int64_t>(K) * SDM_GLR_CHUNK;
     if (CLUSTER) cluster_wait();
@@ -322,7 +364,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) glr_bwd_kernel(const GlrArgs a
         const XT* const dy = static_cast<const XT*>(a.dy) + (b + t) * a.dy_ld + tl.col;
         XT* const dx = static_cast<XT*>(a.dx) + (b + t) * a.dx_ld + tl.col;
         GT* const dg = static_cast<GT*>(a.dg) + (b + t) * a.dg_ld + tl.gate;
-        float ga[kRows][RawGate<GT, PERCH>::n], A[4], F[4], R[4], h[4] = {0.f, 0.f, 0.f, 0.f};
+        Quad ga[kRows], A = quad(1.f), F = quad(0.f), R = quad(0.f), h = quad(0.f);
         Raw4<XT> xr[kRows], dr[kRows];
         {
             Span<XT, GT, PERCH> s;
@@ -334,43 +376,32 @@ __global__ void __launch_bounds__(kWarps * 32, 2) glr_bwd_kernel(const GlrArgs a
                 else
                     dr[i].zero();
             }
-            if (tc < n) ld4(st + tc / SDM_GLR_CHUNK * a.D, h);
+            if (tc < n) h = quad(load4(st + tc / SDM_GLR_CHUNK * a.D));
 #pragma unroll
             for (int i = 0; i < kRows; ++i) {
-                s.g[i].exps(ga[i]);
+                ga[i] = s.g[i].exps();
                 xr[i] = s.x[i];
             }
         }
-        set4(A, 1.f);
-        set4(F, 0.f);
-        set4(R, 0.f);
 #pragma unroll
         for (int i = 0; i < kRows; ++i) {
-            float xv[4], dv[4];
-            xr[i].get(xv);
-            dr[kRows - 1 - i].get(dv);
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                const float e = ga[i][PERCH ? c : 0];
-                A[c] *= e;
-                F[c] = fmaf(e, F[c], xv[c]);
-                R[c] = ga[kRows - 1 - i][PERCH ? c : 0] * (dv[c] + R[c]);
-            }
+            const int r = kRows - 1 - i;
+            A = mul4(A, ga[i]);
+            F = fma4(ga[i], F, quad(xr[i]));
+            R = mul4(ga[r], add4(quad(dr[r]), R));
         }
         st4(&sA[buf][w][lane * 4], A);
         st4(&sF[buf][w][lane * 4], F);
         st4(&sR[buf][w][lane * 4], R);
         __syncthreads();
-        float mw[4];
+        Quad mw = m;
         if (CLUSTER) {
             share_pair(sA[buf], sR[buf], cA[buf], cR[buf], rank, K, true);
             cluster_arrive();
             for (int j = 0; j < w; ++j) join(h, &sA[buf][j][lane * 4], &sF[buf][j][lane * 4]);
             cluster_wait();
             for (int k = K - 1; k >= 0; --k) {
-                if (k == rank)
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) mw[c] = m[c];
+                if (k == rank) mw = m;
                 join(m, &cA[buf][k][lane * 4], &cR[buf][k][lane * 4]);
             }
             for (int j = kWarps - 1; j > w; --j) join(mw, &sA[buf][j][lane * 4], &sR[buf][j][lane * 4]);
@@ -378,37 +409,27 @@ __global__ void __launch_bounds__(kWarps * 32, 2) glr_bwd_kernel(const GlrArgs a
             for (int j = 0; j < w; ++j) join(h, &sA[buf][j][lane * 4], &sF[buf][j][lane * 4]);
 #pragma unroll
             for (int j = kWarps - 1; j >= 0; --j) {
-                if (j == w)
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) mw[c] = m[c];
+                if (j == w) mw = m;
                 join(m, &sA[buf][j][lane * 4], &sR[buf][j][lane * 4]);
             }
         }
-        float hp[kRows][4];   // the state before each row
+        Quad hp[kRows];   // the state before each row
 #pragma unroll
         for (int i = 0; i < kRows; ++i) {
-            float xv[4];
-            xr[i].get(xv);
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                hp[i][c] = h[c];
-                h[c] = fmaf(ga[i][PERCH ? c : 0], h[c], xv[c]);
-            }
+            hp[i] = h;
+            h = fma4(ga[i], h, quad(xr[i]));
         }
 #pragma unroll
         for (int i = kRows - 1; i >= 0; --i) {
-            float l[4], d[4], dv[4];
-            dr[i].get(dv);
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                l[c] = dv[c] + mw[c];
-                mw[c] = ga[i][PERCH ? c : 0] * l[c];
-                d[c] = mw[c] * hp[i][c];
-            }
+            const Quad l = add4(quad(dr[i]), mw);
+            mw = mul4(ga[i], l);
+            const Quad q = mul4(mw, hp[i]);
             if (tl.on && i < live) st4(dx + i * a.dx_ld, l);
             if constexpr (PERCH) {
-                if (tl.on && i < live) st4(dg + i * a.dg_ld, d);
+                if (tl.on && i < live) st4(dg + i * a.dg_ld, q);
             } else {
+                float d[4];
+                floats(q, d);
                 const float s = head_sum(tl.on ? (d[0] + d[1]) + (d[2] + d[3]) : 0.f, tl.seg);
                 if (tl.lead && i < live) {
                     if (a.tiles_per_head == 1)
@@ -456,12 +477,11 @@ __global__ void __launch_bounds__(256) glr_step_kernel(const StepArgs a) {
     const int64_t r = u / quads;
     const int col = static_cast<int>(u - r * quads) * 4;
     const int64_t s = a.slots == nullptr ? r : static_cast<int64_t>(__ldg(a.slots + r));
-    float x[4], ga[RawGate<GT, PERCH>::n], h[4];
+    float x[4], h[4];
     XT* const y = static_cast<XT*>(a.y) + r * a.y_ld + col;
     if (s < 0 || s >= a.states) {   // a padding row, or an id that names no state
         if (s >= a.states && a.status != nullptr) atomicOr(a.status, kDevBadSlot);
-        set4(h, 0.f);
-        st4(y, h);
+        st4(y, quad(0.f));
         return;
     }
     float* const st = a.state + s * a.s_ld + col;
@@ -469,11 +489,9 @@ __global__ void __launch_bounds__(256) glr_step_kernel(const StepArgs a) {
     ld4(static_cast<const XT*>(a.x) + r * a.x_ld + col, x);
     RawGate<GT, PERCH> gr;
     gr.ld(static_cast<const GT*>(a.g) + r * a.g_ld + (PERCH ? col : col / a.gw));
-    gr.exps(ga);
-#pragma unroll
-    for (int c = 0; c < 4; ++c) h[c] = fmaf(ga[PERCH ? c : 0], h[c], x[c]);
-    st4(st, h);
-    st4(y, h);
+    const Quad o = fma4(gr.exps(), quad(h), quad(x));
+    st4(st, o);
+    st4(y, o);
 }
 
 // ---- host side ------------------------------------------------------------------------------------
