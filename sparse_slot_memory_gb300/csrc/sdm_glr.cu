@@ -25,10 +25,14 @@ namespace {
 
 using namespace rows;
 
-constexpr int kRows = 8;        // rows of a warp in one step
-constexpr int kWarps = 8;       // warps of a block: kWarps * kRows rows in one step
-constexpr int kTileCols = 128;  // channels of a tile
-static_assert(kWarps * kRows == SDM_GLR_CHUNK, "a block's step is one saved state");
+constexpr int kTileCols = 128;   // channels of a tile
+constexpr int kMaxCluster = 8;
+
+// How a block divides its step of SDM_GLR_CHUNK rows: kRows rows to each of kWarps warps.
+template <int ROWS>
+struct Split {
+    static constexpr int kWarps = SDM_GLR_CHUNK / ROWS, kThreads = kWarps * 32;
+};
 
 struct GlrArgs {
     const void* x;
@@ -54,6 +58,7 @@ struct GlrArgs {
 
 // A tile's columns and this lane's place in it.
 struct Tile {
+    int col0, n;  // the tile's first channel and its channels
     int col;      // the lane's first channel
     bool on;      // whether the lane has channels
     int gate;     // the lane's gate (head)
@@ -76,6 +81,8 @@ __device__ __forceinline__ Tile tile_of(const GlrArgs& a, int tile, int lane) {
         c0 = head * a.gw + t.sub * a.tile_cols;
         n = min(a.tile_cols, (head + 1) * a.gw - c0);
     }
+    t.col0 = c0;
+    t.n = n;
     t.on = lane * 4 < n;
     t.col = c0 + (t.on ? lane * 4 : 0);
     if (PERCH) {
@@ -104,32 +111,10 @@ __device__ __forceinline__ void sequence(const GlrArgs& a, int p, int64_t& b, in
     if ((lo < 0 || hi > a.rows || lo > hi) && a.status != nullptr && threadIdx.x == 0) atomicOr(a.status, SDM_DEV_BAD_OFFSET);
 }
 
-// Four channels as two pairs of float32: one instruction multiplies or multiply-adds a pair (each half rounded as
-// the scalar instruction rounds it).
+// Four channels as two pairs of float32.
 struct Quad {
     uint64_t lo, hi;
 };
-__device__ __forceinline__ uint64_t pack2(float a, float b) {
-    uint64_t o;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(o) : "f"(a), "f"(b));
-    return o;
-}
-__device__ __forceinline__ void unpack2(uint64_t v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t o;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(o) : "l"(a), "l"(b), "l"(c));
-    return o;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-    uint64_t o;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(o) : "l"(a), "l"(b));
-    return o;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-    uint64_t o;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(o) : "l"(a), "l"(b));
-    return o;
-}
 __device__ __forceinline__ Quad quad(const float (&v)[4]) { return {pack2(v[0], v[1]), pack2(v[2], v[3])}; }
 __device__ __forceinline__ Quad quad(float v) { return {pack2(v, v), pack2(v, v)}; }
 __device__ __forceinline__ void floats(const Quad& q, float (&v)[4]) {
@@ -162,10 +147,11 @@ __device__ __forceinline__ void st4(T* p, const Quad& q) {
     rows::st4(p, v);
 }
 
-// exp of a gate as 2^(g log2 e): within 4 u + |g| u (u = 2^-24), and exactly 0 and 1 at -inf and 0
-__device__ __forceinline__ float exp_gate(float g) {
+// A gate's exp is 2^(g log2 e): within 4 u + |g| u (u = 2^-24), and exactly 0 and 1 at -inf and 0.
+constexpr float kLog2e = 1.44269504088896341f;
+__device__ __forceinline__ float exp2_gate(float t) {
     float o;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(o) : "f"(g * 1.44269504088896341f));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(o) : "f"(t));
     return o;
 }
 
@@ -179,9 +165,9 @@ struct RawGate<GT, true> {
     __device__ __forceinline__ void zero() { v.zero(); }
     __device__ __forceinline__ Quad exps() const {
         float o[4];
-        v.get(o);
+        floats(mul4(quad(v), quad(kLog2e)), o);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) o[i] = exp_gate(o[i]);
+        for (int i = 0; i < 4; ++i) o[i] = exp2_gate(o[i]);
         return quad(o);
     }
 };
@@ -190,75 +176,94 @@ struct RawGate<GT, false> {
     GT v;
     __device__ __forceinline__ void ld(const GT* p) { v = __ldg(p); }
     __device__ __forceinline__ void zero() { v = GT(0.f); }
-    __device__ __forceinline__ Quad exps() const { return quad(exp_gate(widen(v))); }
+    __device__ __forceinline__ Quad exps() const { return quad(exp2_gate(widen(v) * kLog2e)); }
 };
 
-// kRows rows of a warp; those from `live` on are the identity (gate 1, nothing added)
-template <typename XT, typename GT, bool PERCH>
-struct Span {
-    Raw4<XT> x[kRows];
-    RawGate<GT, PERCH> g[kRows];
-    __device__ __forceinline__ void ld(const XT* xp, int64_t x_ld, const GT* gp, int64_t g_ld, int live) {
+// ROWS rows of a lane's columns; those from `live` on are zeros (the identity: gate 1, nothing added).
+template <int ROWS, typename Row, typename T>
+__device__ __forceinline__ void load_rows(Row (&r)[ROWS], const T* p, int64_t ld, int live) {
+    if (live == ROWS) {   // warp-uniform
 #pragma unroll
-        for (int i = 0; i < kRows; ++i) {
-            if (i < live) {
-                g[i].ld(gp + i * g_ld);
-                x[i].ld(xp + i * x_ld);
-            } else {
-                g[i].zero();
-                x[i].zero();
-            }
+        for (int i = 0; i < ROWS; ++i) r[i].ld(p + i * ld);
+    } else {
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i) {
+            r[i].zero();
+            if (i < live) r[i].ld(p + i * ld);
         }
     }
-};
-
-// How many of the kRows rows from t on lie before n.
-__device__ __forceinline__ int live_rows(int64_t t, int64_t n) {
-    return static_cast<int>(min(max(n - t, int64_t(0)), int64_t(kRows)));
 }
 
-// The blocks of a cluster: this one's rank, and stores into another's shared memory.
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
+// Asks for a warp's rows of its next step in the L2, from the tile's first column p on: lane l its lines l, l + 32, ..
+// of ROWS rows of up to 128 columns.
+template <int ROWS, typename T>
+__device__ __forceinline__ void prefetch_rows(const T* p, int64_t ld, int live, int cols, int lane) {
+    constexpr int kLines = kTileCols * sizeof(T) / 128;
+#pragma unroll
+    for (int k = 0; k < (ROWS * kLines + 31) / 32; ++k) {
+        const int l = lane + 32 * k, i = l / kLines, c = l % kLines * static_cast<int>(128 / sizeof(T));
+        if (i < live && c < cols) asm volatile("prefetch.global.L2 [%0];" ::"l"(p + i * ld + c));
+    }
 }
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
-__device__ __forceinline__ void st_remote(const float* p, uint32_t rank, float v) {
-    uint32_t a = static_cast<uint32_t>(__cvta_generic_to_shared(p));
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(a), "r"(rank));
-    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(a), "f"(v) : "memory");
+
+// Hides from the compiler that loaded rows are unchanged: what was widened or raised from them before an exchange is
+// computed again behind it, where keeping it would take twice the registers of the rows themselves.
+__device__ __forceinline__ void forget(float& v) { asm volatile("" : "+f"(v)); }
+__device__ __forceinline__ void forget(__nv_bfloat16& v) {
+    uint16_t u = __bfloat16_as_ushort(v);
+    asm volatile("" : "+h"(u));
+    v = __ushort_as_bfloat16(u);
+}
+__device__ __forceinline__ void forget(Raw4<float>& r) {
+    asm volatile("" : "+f"(r.v.x), "+f"(r.v.y), "+f"(r.v.z), "+f"(r.v.w));
+}
+__device__ __forceinline__ void forget(Raw4<__nv_bfloat16>& r) { asm volatile("" : "+r"(r.v.x), "+r"(r.v.y)); }
+template <typename GT, bool PERCH>
+__device__ __forceinline__ void forget(RawGate<GT, PERCH>& r) { forget(r.v); }
+template <typename Row, int ROWS>
+__device__ __forceinline__ void forget(Row (&r)[ROWS]) {
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) forget(r[i]);
+}
+
+// How many of the `rows` rows from t on lie before n.
+__device__ __forceinline__ int live_rows(int64_t t, int64_t n, int rows) {
+    return static_cast<int>(min(max(n - t, int64_t(0)), static_cast<int64_t>(rows)));
+}
+
+// A store into the shared memory of another block of the cluster.
+__device__ __forceinline__ void st_remote(const float* p, uint32_t rank, const Quad& q) {
+    const uint32_t a = remote_address(p, rank);
+    asm volatile("st.shared::cluster.v2.b64 [%0], {%1, %2};" ::"r"(a), "l"(q.lo), "l"(q.hi) : "memory");
 }
 
 // h = A h + B from a pair in shared memory
 __device__ __forceinline__ void join(Quad& h, const float* A, const float* B) { h = fma4(quad(A), h, quad(B)); }
 
-// Joins the block's warps' pairs and writes the block's pair into every block of the cluster, at its own rank.
+// One warp joins the block's warps' pairs and writes the block's pair into every block of the cluster, at its own rank.
+template <int WARPS, bool REVERSE>
 __device__ __forceinline__ void share_pair(const float (*A)[kTileCols], const float (*B)[kTileCols], float (*cA)[kTileCols],
-                                           float (*cB)[kTileCols], uint32_t rank, int K, bool reverse) {
-    if (threadIdx.x >= kTileCols) return;
-    const int c = threadIdx.x;
-    float pa = 1.f, pb = 0.f;
+                                           float (*cB)[kTileCols], uint32_t rank, int K, int lane) {
+    Quad pa = quad(1.f), pb = quad(0.f);
 #pragma unroll
-    for (int j = 0; j < kWarps; ++j) {
-        const int k = reverse ? kWarps - 1 - j : j;
-        pb = fmaf(A[k][c], pb, B[k][c]);
-        pa *= A[k][c];
+    for (int j = 0; j < WARPS; ++j) {
+        const int k = REVERSE ? WARPS - 1 - j : j;
+        const Quad ak = quad(&A[k][lane * 4]);
+        pb = fma4(ak, pb, quad(&B[k][lane * 4]));
+        pa = mul4(ak, pa);
     }
     for (int k = 0; k < K; ++k) {
-        st_remote(&cA[rank][c], k, pa);
-        st_remote(&cB[rank][c], k, pb);
+        st_remote(&cA[rank][lane * 4], k, pa);
+        st_remote(&cB[rank][lane * 4], k, pb);
     }
 }
 
-constexpr int kMaxCluster = 8;
-
-template <typename XT, typename GT, bool PERCH, bool CLUSTER>
-__global__ void __launch_bounds__(kWarps * 32, 2) glr_fwd_kernel(const GlrArgs a) {
+template <typename XT, typename GT, bool PERCH, bool CLUSTER, int ROWS>
+__global__ void __launch_bounds__(Split<ROWS>::kThreads, 2) glr_fwd_kernel(const GlrArgs a) {
+    constexpr int kWarps = Split<ROWS>::kWarps;
     __shared__ __align__(16) float sA[2][kWarps][kTileCols], sB[2][kWarps][kTileCols];
     __shared__ __align__(16) float cA[2][CLUSTER ? kMaxCluster : 1][kTileCols], cB[2][CLUSTER ? kMaxCluster : 1][kTileCols];
-    if (CLUSTER) cluster_arrive();
+    if (CLUSTER) cluster_arrive_relaxed();
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     const int K = CLUSTER ? a.cluster : 1, rank = CLUSTER ? cluster_rank() : 0;
@@ -270,37 +275,42 @@ __global__ void __launch_bounds__(kWarps * 32, 2) glr_fwd_kernel(const GlrArgs a
     Quad h = quad(0.f);   // the state before the step's rows
     if (a.h0 != nullptr) h = quad(load4(a.h0 + static_cast<int64_t>(p) * a.D + tl.col));
     const int64_t step = static_cast<int64_t>(K) * SDM_GLR_CHUNK;
-    int64_t t = rank * SDM_GLR_CHUNK + w * kRows;   // the warp's first row of the step
-    const XT* x = static_cast<const XT*>(a.x) + (b + t) * a.x_ld + tl.col;
-    const GT* g = static_cast<const GT*>(a.g) + (b + t) * a.g_ld + tl.gate;
+    int64_t t = rank * SDM_GLR_CHUNK + w * ROWS;   // the warp's first row of the step
+    const XT* x = static_cast<const XT*>(a.x) + (b + t) * a.x_ld;
+    const GT* g = static_cast<const GT*>(a.g) + (b + t) * a.g_ld;
     XT* y = static_cast<XT*>(a.y) + (b + t) * a.y_ld + tl.col;
     float* const st = a.states == nullptr ? nullptr : a.states + (b / SDM_GLR_CHUNK + p) * a.D + tl.col;
-    Span<XT, GT, PERCH> next;
-    int live = live_rows(t, n);
-    next.ld(x, a.x_ld, g, a.g_ld, live);
     if (CLUSTER) cluster_wait();   // every block of the cluster runs
     int buf = 0;
     for (int64_t t0 = 0; t0 < n; t0 += step, t += step, buf ^= 1) {
-        Quad ga[kRows], A = quad(1.f), B = quad(0.f);
-        Raw4<XT> xr[kRows];
+        const int live = live_rows(t, n, ROWS);
+        Raw4<XT> xr[ROWS];
+        RawGate<GT, PERCH> gr[ROWS];
+        load_rows(gr, g + tl.gate, a.g_ld, live);
+        load_rows(xr, x + tl.col, a.x_ld, live);
+        x += step * a.x_ld;
+        g += step * a.g_ld;
+        const int more = live_rows(t + step, n, ROWS);
+        prefetch_rows<ROWS>(x + tl.col0, a.x_ld, more, tl.n, lane);
+        if (PERCH) prefetch_rows<ROWS>(g + tl.col0, a.g_ld, more, tl.n, lane);
+        Quad A = quad(1.f), B = quad(0.f);
 #pragma unroll
-        for (int i = 0; i < kRows; ++i) {
-            ga[i] = next.g[i].exps();
-            xr[i] = next.x[i];
-            A = mul4(A, ga[i]);
-            B = fma4(ga[i], B, quad(xr[i]));
+        for (int i = 0; i < ROWS; ++i) {
+            const Quad e = gr[i].exps();
+            A = mul4(A, e);
+            B = fma4(e, B, quad(xr[i]));
         }
         st4(&sA[buf][w][lane * 4], A);
         st4(&sB[buf][w][lane * 4], B);
-        x += step * a.x_ld;
-        g += step * a.g_ld;
-        const int nlive = live_rows(t + step, n);
-        next.ld(x, a.x_ld, g, a.g_ld, nlive);   // in flight over the exchange
         __syncthreads();   // the other buffer is written next: one barrier a step
         Quad hw = h;
         if (CLUSTER) {
-            share_pair(sA[buf], sB[buf], cA[buf], cB[buf], rank, K, false);
-            cluster_arrive();
+            if (w == 0) {
+                share_pair<kWarps, false>(sA[buf], sB[buf], cA[buf], cB[buf], rank, K, lane);
+                cluster_arrive();
+            } else {
+                cluster_arrive_relaxed();
+            }
             cluster_wait();
             for (int k = 0; k < K; ++k) {
                 if (k == rank) hw = h;
@@ -317,12 +327,11 @@ __global__ void __launch_bounds__(kWarps * 32, 2) glr_fwd_kernel(const GlrArgs a
             }
         }
 #pragma unroll
-        for (int i = 0; i < kRows; ++i) {
-            hw = fma4(ga[i], hw, quad(xr[i]));
+        for (int i = 0; i < ROWS; ++i) {
+            hw = fma4(gr[i].exps(), hw, quad(xr[i]));
             if (tl.on && i < live) st4(y + i * a.y_ld, hw);
         }
         y += step * a.y_ld;
-        live = nlive;
     }
     if (a.hT != nullptr && rank == 0 && w == 0 && tl.on) st4(a.hT + static_cast<int64_t>(p) * a.D + tl.col, h);
 }
@@ -337,11 +346,12 @@ __device__ __forceinline__ float head_sum(float v, int seg) {
     return v;
 }
 
-template <typename XT, typename GT, bool PERCH, bool CLUSTER>
-__global__ void __launch_bounds__(kWarps * 32, 2) glr_bwd_kernel(const GlrArgs a) {
+template <typename XT, typename GT, bool PERCH, bool CLUSTER, int ROWS>
+__global__ void __launch_bounds__(Split<ROWS>::kThreads, 2) glr_bwd_kernel(const GlrArgs a) {
+    constexpr int kWarps = Split<ROWS>::kWarps;
     __shared__ __align__(16) float sA[2][kWarps][kTileCols], sF[2][kWarps][kTileCols], sR[2][kWarps][kTileCols];
     __shared__ __align__(16) float cA[2][CLUSTER ? kMaxCluster : 1][kTileCols], cR[2][CLUSTER ? kMaxCluster : 1][kTileCols];
-    if (CLUSTER) cluster_arrive();
+    if (CLUSTER) cluster_arrive_relaxed();
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     const int K = CLUSTER ? a.cluster : 1, rank = CLUSTER ? cluster_rank() : 0;
@@ -357,47 +367,46 @@ __global__ void __launch_bounds__(kWarps * 32, 2) glr_bwd_kernel(const GlrArgs a
     if (CLUSTER) cluster_wait();
     int buf = 0;
     for (int64_t t0 = (n + step - 1) / step * step - step; t0 >= 0; t0 -= step, buf ^= 1) {
-        const int64_t tc = t0 + rank * SDM_GLR_CHUNK, t = tc + w * kRows;
-        const int live = live_rows(t, n);
-        const XT* const x = static_cast<const XT*>(a.x) + (b + t) * a.x_ld + tl.col;
-        const GT* const g = static_cast<const GT*>(a.g) + (b + t) * a.g_ld + tl.gate;
-        const XT* const dy = static_cast<const XT*>(a.dy) + (b + t) * a.dy_ld + tl.col;
+        const int64_t tc = t0 + rank * SDM_GLR_CHUNK, t = tc + w * ROWS;
+        const int live = live_rows(t, n, ROWS);
+        const XT* const x = static_cast<const XT*>(a.x) + (b + t) * a.x_ld;
+        const GT* const g = static_cast<const GT*>(a.g) + (b + t) * a.g_ld;
+        const XT* const dy = static_cast<const XT*>(a.dy) + (b + t) * a.dy_ld;
         XT* const dx = static_cast<XT*>(a.dx) + (b + t) * a.dx_ld + tl.col;
         GT* const dg = static_cast<GT*>(a.dg) + (b + t) * a.dg_ld + tl.gate;
-        Quad ga[kRows], A = quad(1.f), F = quad(0.f), R = quad(0.f), h = quad(0.f);
-        Raw4<XT> xr[kRows], dr[kRows];
-        {
-            Span<XT, GT, PERCH> s;
-            s.ld(x, a.x_ld, g, a.g_ld, live);
+        Raw4<XT> xr[ROWS], dr[ROWS];
+        RawGate<GT, PERCH> gr[ROWS];
+        load_rows(gr, g + tl.gate, a.g_ld, live);
+        load_rows(dr, dy + tl.col, a.dy_ld, live);
+        load_rows(xr, x + tl.col, a.x_ld, live);
+        Quad h = quad(0.f);
+        if (tc < n) h = quad(load4(st + tc / SDM_GLR_CHUNK * a.D));
+        if (t0 > 0) {
+            prefetch_rows<ROWS>(x - step * a.x_ld + tl.col0, a.x_ld, ROWS, tl.n, lane);
+            prefetch_rows<ROWS>(dy - step * a.dy_ld + tl.col0, a.dy_ld, ROWS, tl.n, lane);
+            if (PERCH) prefetch_rows<ROWS>(g - step * a.g_ld + tl.col0, a.g_ld, ROWS, tl.n, lane);
+        }
+        Quad A = quad(1.f), F = quad(0.f), R = quad(0.f);
 #pragma unroll
-            for (int i = 0; i < kRows; ++i) {
-                if (i < live)
-                    dr[i].ld(dy + i * a.dy_ld);
-                else
-                    dr[i].zero();
-            }
-            if (tc < n) h = quad(load4(st + tc / SDM_GLR_CHUNK * a.D));
-#pragma unroll
-            for (int i = 0; i < kRows; ++i) {
-                ga[i] = s.g[i].exps();
-                xr[i] = s.x[i];
-            }
+        for (int i = 0; i < ROWS; ++i) {
+            const Quad e = gr[i].exps();
+            A = mul4(A, e);
+            F = fma4(e, F, quad(xr[i]));
         }
 #pragma unroll
-        for (int i = 0; i < kRows; ++i) {
-            const int r = kRows - 1 - i;
-            A = mul4(A, ga[i]);
-            F = fma4(ga[i], F, quad(xr[i]));
-            R = mul4(ga[r], add4(quad(dr[r]), R));
-        }
+        for (int i = ROWS - 1; i >= 0; --i) R = mul4(gr[i].exps(), add4(quad(dr[i]), R));
         st4(&sA[buf][w][lane * 4], A);
         st4(&sF[buf][w][lane * 4], F);
         st4(&sR[buf][w][lane * 4], R);
         __syncthreads();
         Quad mw = m;
         if (CLUSTER) {
-            share_pair(sA[buf], sR[buf], cA[buf], cR[buf], rank, K, true);
-            cluster_arrive();
+            if (w == 0) {
+                share_pair<kWarps, true>(sA[buf], sR[buf], cA[buf], cR[buf], rank, K, lane);
+                cluster_arrive();
+            } else {
+                cluster_arrive_relaxed();
+            }
             for (int j = 0; j < w; ++j) join(h, &sA[buf][j][lane * 4], &sF[buf][j][lane * 4]);
             cluster_wait();
             for (int k = K - 1; k >= 0; --k) {
@@ -413,16 +422,19 @@ __global__ void __launch_bounds__(kWarps * 32, 2) glr_bwd_kernel(const GlrArgs a
                 join(m, &sA[buf][j][lane * 4], &sR[buf][j][lane * 4]);
             }
         }
-        Quad hp[kRows];   // the state before each row
+        forget(gr);
+        forget(xr);
+        forget(dr);
+        Quad hp[ROWS];   // the state before each row
 #pragma unroll
-        for (int i = 0; i < kRows; ++i) {
+        for (int i = 0; i < ROWS; ++i) {
             hp[i] = h;
-            h = fma4(ga[i], h, quad(xr[i]));
+            h = fma4(gr[i].exps(), h, quad(xr[i]));
         }
 #pragma unroll
-        for (int i = kRows - 1; i >= 0; --i) {
+        for (int i = ROWS - 1; i >= 0; --i) {
             const Quad l = add4(quad(dr[i]), mw);
-            mw = mul4(ga[i], l);
+            mw = mul4(gr[i].exps(), l);
             const Quad q = mul4(mw, hp[i]);
             if (tl.on && i < live) st4(dx + i * a.dx_ld, l);
             if constexpr (PERCH) {
@@ -551,28 +563,8 @@ int cluster_of(const sdm_glr_shape* s, const GlrArgs& a) {
     if (const char* e = getenv("GLR_K")) return atoi(e);
     const int64_t units = static_cast<int64_t>(a.tiles) * a.P, steps = (a.len + SDM_GLR_CHUNK - 1) / SDM_GLR_CHUNK;
     int k = 1;
-    while (k < kMaxCluster && units * k < 304 && k < steps) k *= 2;
+    while (k < kMaxCluster && units * k < 228 && k < steps) k *= 2;
     return k;
-}
-
-// A launch of clusters of `cluster` blocks (a multiple of them), as a programmatic dependent.
-template <typename... Params, typename... Args>
-cudaError_t launch_cluster(void (*kernel)(Params...), dim3 grid, dim3 block, int cluster, cudaStream_t stream,
-                           Args&&... args) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = block;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = cluster;
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
 }
 
 // Calls f(x type, g type, per-channel gates) with the shape's types.
@@ -625,10 +617,11 @@ extern "C" sdm_status sdm_glr_forward(const sdm_glr_shape* shape, const void* x,
     const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
     const cudaError_t e = by_type(shape, [&](auto xt, auto gt, auto perch) {
         constexpr bool PC = decltype(perch)::value;
-        const dim3 grid(static_cast<unsigned>(a.tiles) * a.P * a.cluster), block(kWarps * 32);
+        constexpr int R = 8;
+        const dim3 grid(static_cast<unsigned>(a.tiles) * a.P * a.cluster), block(Split<R>::kThreads);
         if (a.cluster > 1)
-            return launch_cluster(glr_fwd_kernel<decltype(xt), decltype(gt), PC, true>, grid, block, a.cluster, cs, a);
-        return launch_dependent(glr_fwd_kernel<decltype(xt), decltype(gt), PC, false>, grid, block, 0, cs, a);
+            return launch_cluster(glr_fwd_kernel<decltype(xt), decltype(gt), PC, true, R>, grid, block, a.cluster, cs, a);
+        return launch_dependent(glr_fwd_kernel<decltype(xt), decltype(gt), PC, false, R>, grid, block, 0, cs, a);
     });
     return e == cudaSuccess ? SDM_OK : SDM_ERR_CUDA;
 }
@@ -665,10 +658,11 @@ extern "C" sdm_status sdm_glr_backward(const sdm_glr_shape* shape, const void* x
     const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t e = by_type(shape, [&](auto xt, auto gt, auto perch) {
         constexpr bool PC = decltype(perch)::value;
-        const dim3 grid(static_cast<unsigned>(a.tiles) * a.P * a.cluster), block(kWarps * 32);
+        constexpr int R = 8;
+        const dim3 grid(static_cast<unsigned>(a.tiles) * a.P * a.cluster), block(Split<R>::kThreads);
         if (a.cluster > 1)
-            return launch_cluster(glr_bwd_kernel<decltype(xt), decltype(gt), PC, true>, grid, block, a.cluster, cs, a);
-        return launch_dependent(glr_bwd_kernel<decltype(xt), decltype(gt), PC, false>, grid, block, 0, cs, a);
+            return launch_cluster(glr_bwd_kernel<decltype(xt), decltype(gt), PC, true, R>, grid, block, a.cluster, cs, a);
+        return launch_dependent(glr_bwd_kernel<decltype(xt), decltype(gt), PC, false, R>, grid, block, 0, cs, a);
     });
     if (e == cudaSuccess && part_bytes(a) > 0) {
         const int64_t blocks = std::min<int64_t>((a.rows * a.H + 255) / 256, 4096);

@@ -7,7 +7,12 @@
 // H = (log2 s - u / s) ln 2. Backward: dz_v = dlogp (1[v = target] - p_v) - dH p_v (log p_v + H).
 //
 // The top alternatives are kept in the same pass: every warp holds its K <= 32 largest (value, id) so far, one in a
-// lane, and looks only at vectors that hold a logit above the last of them.
+// lane, and looks only at vectors that hold a logit above the last of them. Before the first is taken, the 32 half
+// warps' largest logits of the block's first batch bound the K-th largest from below: only logits at least as large
+// as the least of those 32 are ever looked at (in random rows about one of 150). Sorted lists join by halves.
+//
+// A row is one block's, or where there are fewer rows than the SMs hold blocks, a cluster's: each block takes a part
+// of the row and the first joins their triples and lists through its shared memory.
 //
 // A row whose largest logit lies under -1e30 / scale (everything masked, by -inf or by a type's lowest value)
 // leaves s = 0 and takes a second, plain look; so does the backward of a row whose lse is too large for float32
@@ -16,6 +21,7 @@
 
 #include <algorithm>
 #include <cstring>
+#include <type_traits>
 
 #include "sdm_checks.cuh"
 #include "sdm_internal.cuh"
@@ -28,11 +34,15 @@ using namespace rows;
 
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
+constexpr int kBatch = 4;             // vectors of a thread in flight
 constexpr int kMaxK = 32;
+constexpr int kMaxCluster = 8;
+static_assert(kThreads / 16 == kMaxK, "one half warp for each alternative bounds them from below");
 constexpr float kLog2e = 1.44269504088896341f;
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr float kFloor = -1e35f;      // what a masked logit counts as in the sums: its term is 0 beside any M
 constexpr float kStart = -1e30f;      // the first M
+constexpr float kGradFloor = -1e30f;  // the same in the gradient, where its products have to stay finite
 constexpr float kFarLse = 1024.f;     // |lse| from which float32 z - lse is too coarse
 
 struct LpArgs {
@@ -52,6 +62,7 @@ struct LpArgs {
     int64_t rows, ld, d_ld;
     int V, K;
     float scale;
+    int cluster;           // blocks of a row
 };
 
 __device__ __forceinline__ float max_nan(float a, float b) {
@@ -70,6 +81,12 @@ __device__ __forceinline__ float value_of(uint32_t o) {
     return o == 0xFFFFFFFFu ? __uint_as_float(0x7FC00000u) : __uint_as_float((o & 0x80000000u) ? o & 0x7FFFFFFFu : ~o);
 }
 
+__device__ __forceinline__ float ex2(float t) {   // 2^t, to 2 ulp; below 2^-126 it is 0
+    float o;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(o) : "f"(t));
+    return o;
+}
+
 template <typename T>
 struct Vec;   // 16 bytes of logits
 template <>
@@ -77,7 +94,13 @@ struct Vec<float> {
     static constexpr int n = 4;
     float4 v;
     __device__ __forceinline__ void ld(const float* p) { v = __ldg(reinterpret_cast<const float4*>(p)); }
+    __device__ __forceinline__ void none() { v = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY); }
     __device__ __forceinline__ void get(float (&o)[4]) const { o[0] = v.x; o[1] = v.y; o[2] = v.z; o[3] = v.w; }
+    __device__ __forceinline__ float most() const { return max_nan(max_nan(v.x, v.y), max_nan(v.z, v.w)); }
+    // the pair i, no element below `floor`
+    __device__ __forceinline__ uint64_t pair(int i, float floor) const {
+        return i ? pack2(max_nan(v.z, floor), max_nan(v.w, floor)) : pack2(max_nan(v.x, floor), max_nan(v.y, floor));
+    }
     __device__ __forceinline__ static void st(float* p, const float (&o)[4]) { st4(p, o); }
 };
 template <>
@@ -85,13 +108,27 @@ struct Vec<__nv_bfloat16> {
     static constexpr int n = 8;
     uint4 v;
     __device__ __forceinline__ void ld(const __nv_bfloat16* p) { v = __ldg(reinterpret_cast<const uint4*>(p)); }
+    __device__ __forceinline__ void none() { v = make_uint4(0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u); }
+    __device__ __forceinline__ uint32_t word(int i) const { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
+    __device__ __forceinline__ static uint32_t max2(uint32_t a, uint32_t b) {
+        uint32_t o;
+        asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(o) : "r"(a), "r"(b));
+        return o;
+    }
     __device__ __forceinline__ void get(float (&o)[8]) const {
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            o[2 * i] = __uint_as_float(w[i] << 16);
-            o[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+            o[2 * i] = __uint_as_float(word(i) << 16);
+            o[2 * i + 1] = __uint_as_float(word(i) & 0xFFFF0000u);
         }
+    }
+    __device__ __forceinline__ float most() const {
+        const uint32_t m = max2(max2(v.x, v.y), max2(v.z, v.w));
+        return max_nan(__uint_as_float(m << 16), __uint_as_float(m & 0xFFFF0000u));
+    }
+    __device__ __forceinline__ uint64_t pair(int i, float floor) const {
+        const uint32_t f = __float_as_uint(floor) >> 16, w = max2(word(i), f << 16 | f);
+        return pack2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
     }
     __device__ __forceinline__ static void st(__nv_bfloat16* p, const float (&o)[8]) { st8(p, o); }
 };
@@ -104,18 +141,39 @@ struct Sums {
         s = u = 0.f;
     }
     __device__ __forceinline__ void raise(float m) {
-        const float d = M - m, f = exp2f(d);   // d <= 0
+        const float d = M - m, f = ex2(d);   // d <= 0
         u = f * fmaf(d, s, u);
         s *= f;
         M = m;
     }
     __device__ __forceinline__ void add(float x, float c) {   // M is at least x c
-        const float t = fmaf(max_nan(x, kFloor), c, -M), e = exp2f(t);
+        const float t = fmaf(max_nan(x, kFloor), c, -M), e = ex2(t);
         s += e;
         u = fmaf(e, t, u);
     }
+    template <int VECS, typename T>
+    __device__ __forceinline__ void add(const Vec<T> (&r)[VECS], float c) {
+        const uint64_t c2 = pack2(c, c), m2 = pack2(-M, -M);
+        uint64_t s2 = pack2(s, 0.f), u2 = pack2(u, 0.f);
+#pragma unroll
+        for (int k = 0; k < VECS; ++k)
+#pragma unroll
+            for (int i = 0; i < Vec<T>::n / 2; ++i) {
+                const uint64_t t2 = fma2(r[k].pair(i, kFloor), c2, m2);
+                float a, b;
+                unpack2(t2, a, b);
+                const uint64_t e2 = pack2(ex2(a), ex2(b));
+                s2 = add2(s2, e2);
+                u2 = fma2(e2, t2, u2);
+            }
+        float a, b;
+        unpack2(s2, a, b);
+        s = a + b;
+        unpack2(u2, a, b);
+        u = a + b;
+    }
     __device__ __forceinline__ void join(float oM, float os, float ou) {
-        const float m = fmaxf(M, oM), d = M - m, od = oM - m, f = exp2f(d), of = exp2f(od);
+        const float m = fmaxf(M, oM), d = M - m, od = oM - m, f = ex2(d), of = ex2(od);
         u = f * fmaf(d, s, u) + of * fmaf(od, os, ou);
         s = f * s + of * os;
         M = m;
@@ -133,6 +191,18 @@ struct TopList {
         lane = l;
         pass = 0;
     }
+    // The 32 largest of this list and another, both descending over the lanes: the larger of lane i's and the other's
+    // lane 31 - i are those 32, and five exchanges bring them in order.
+    __device__ __forceinline__ void join(uint64_t other) {
+        const uint64_t o = __shfl_xor_sync(kFull, other, 31);
+        key = key > o ? key : o;
+#pragma unroll
+        for (int k = 16; k; k >>= 1) {
+            const uint64_t x = __shfl_xor_sync(kFull, key, k);
+            const bool up = (lane & k) == 0;
+            key = (key > x) == up ? key : x;
+        }
+    }
     __device__ __forceinline__ void insert(uint64_t c) {   // warp-uniform c
         const uint64_t last = __shfl_sync(kFull, key, K - 1);
         if (c <= last) return;
@@ -141,7 +211,7 @@ struct TopList {
         if (lane < K && lane >= at) key = lane == at ? c : up;
         const uint32_t k = static_cast<uint32_t>(__shfl_sync(kFull, key, K - 1) >> 32);
         // once K are held, an equal logit of a later vector has a higher id and stays out
-        pass = k == 0 ? 0 : k == 0xFFFFFFFFu ? k : k + 1;
+        if (k != 0) pass = max(pass, k == 0xFFFFFFFFu ? k : k + 1);
     }
     // N logits of each lane, ids id .. id + N - 1 (those from `end` on are none)
     template <int N>
@@ -168,7 +238,25 @@ struct Shared {
     float M[kWarps], s[kWarps], u[kWarps];
     uint64_t top[kWarps][kMaxK];
     float red[kWarps];
+    uint32_t bound[kMaxK];
+    // of the cluster's blocks, in the first one
+    float cM[kMaxCluster], cs[kMaxCluster], cu[kMaxCluster];
+    uint64_t ctop[kMaxCluster][kMaxK];
 };
+
+// The lists in rows 0 .. n - 1 (n a power of two, one row a warp) joined into row 0. Block-wide.
+__device__ __forceinline__ void join_lists(uint64_t (*top)[kMaxK], int n, int w, int lane) {
+    for (int h = n >> 1; h; h >>= 1) {
+        if (w < h) {
+            TopList l;
+            l.clear(kMaxK, lane);
+            l.key = top[w][lane];
+            l.join(top[w + h][lane]);
+            top[w][lane] = l.key;
+        }
+        __syncthreads();
+    }
+}
 
 // The row's largest logit, then sum exp(z - z_max), sum exp(z - z_max) (z - z_max), from differences that hold for
 // any finite logits. Block-wide; every thread gets them.
@@ -201,13 +289,15 @@ __device__ void plain_stats(const T* x, int V, float scale, Shared& sh, float& m
     u = block(b, true);
 }
 
-template <typename T, bool TOP>
-__global__ void __launch_bounds__(kThreads) lp_fwd_kernel(const LpArgs a) {
+template <typename T, bool TOP, bool CLUSTER>
+__global__ void __launch_bounds__(kThreads, 2) lp_fwd_kernel(const LpArgs a) {
     __shared__ Shared sh;
+    if (CLUSTER) cluster_arrive_relaxed();
     asm volatile("griddepcontrol.wait;" ::: "memory");
     constexpr int N = Vec<T>::n;
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-    const int64_t row = blockIdx.x;
+    const int C = CLUSTER ? a.cluster : 1, rank = CLUSTER ? cluster_rank() : 0;
+    const int64_t row = blockIdx.x / C;
     const T* const x = static_cast<const T*>(a.logits) + row * a.ld;
     const float c = a.scale * kLog2e;
     Sums acc;
@@ -215,9 +305,12 @@ __global__ void __launch_bounds__(kThreads) lp_fwd_kernel(const LpArgs a) {
     TopList top;
     top.clear(a.K, lane);
     // vectors start at the row's first 16-byte boundary; the logits before it and behind the last vector are
-    // taken one by one, the former as the first step's (ids ascend over the steps of a warp)
+    // taken one by one, by the first and the last block (ids ascend over what a warp sees)
     const int head = min(a.V, static_cast<int>((16 - (reinterpret_cast<uintptr_t>(x) & 15)) % 16 / sizeof(T)));
     const int nvec = (a.V - head) / N;
+    const int each = CLUSTER ? (nvec + C - 1) / C : nvec;
+    const int vb = rank * each, ve = CLUSTER ? min(nvec, vb + each) : nvec;   // this block's vectors
+    const T* const xv = x + head;
     auto scalars = [&](int b, int e) {   // at most 32 logits, by warp 0
         const int i = b + lane;
         float v[1] = {i < e ? widen(__ldg(x + i)) : -INFINITY};
@@ -227,30 +320,43 @@ __global__ void __launch_bounds__(kThreads) lp_fwd_kernel(const LpArgs a) {
         }
         if (TOP) top.offer<1>(v, v[0], i, e);
     };
-    if (w == 0) scalars(0, head);
-    for (int v0 = 0; v0 < nvec; v0 += kThreads) {
-        const int v = v0 + threadIdx.x;
-        const bool on = v < nvec;
-        float f[N];
-        if (on) {
-            Vec<T> r;
-            r.ld(x + head + static_cast<int64_t>(v) * N);
-            r.get(f);
-        } else {
+    if (w == 0 && rank == 0) scalars(0, head);
+    for (int v0 = vb; v0 < ve; v0 += kThreads * kBatch) {
+        Vec<T> r[kBatch];
+        float most = -INFINITY;
 #pragma unroll
-            for (int i = 0; i < N; ++i) f[i] = -INFINITY;
+        for (int k = 0; k < kBatch; ++k) {
+            const int v = v0 + k * kThreads + threadIdx.x;
+            if (v < ve)
+                r[k].ld(xv + static_cast<int64_t>(v) * N);
+            else
+                r[k].none();
         }
-        float most = f[0];
 #pragma unroll
-        for (int i = 1; i < N; ++i) most = max_nan(most, f[i]);
-        if (on) {
-            if (!(most * c <= acc.M)) acc.raise(most * c);
+        for (int k = 0; k < kBatch; ++k) most = max_nan(most, r[k].most());
+        if (!(most * c <= acc.M)) acc.raise(most * c);
+        acc.add(r, c);
+        if (TOP) {
+            if (v0 == vb) {   // block-uniform: the bound from the first batch
+                uint32_t o = order_of(most);
 #pragma unroll
-            for (int i = 0; i < N; ++i) acc.add(f[i], c);
+                for (int k = 8; k; k >>= 1) o = max(o, __shfl_xor_sync(kFull, o, k));
+                if ((lane & 15) == 0) sh.bound[threadIdx.x >> 4] = o;
+                __syncthreads();
+                top.pass = max(top.pass, __reduce_min_sync(kFull, sh.bound[lane]));
+            }
+            if (__any_sync(kFull, order_of(most) >= top.pass)) {
+#pragma unroll
+                for (int k = 0; k < kBatch; ++k) {
+                    const int v = v0 + k * kThreads + threadIdx.x;
+                    float f[N];
+                    r[k].get(f);
+                    top.offer<N>(f, r[k].most(), v < ve ? head + v * N : a.V, head + ve * N);
+                }
+            }
         }
-        if (TOP) top.offer<N>(f, most, on ? head + v * N : a.V, head + nvec * N);
     }
-    if (w == 0) scalars(head + nvec * N, a.V);
+    if (w == 0 && rank == C - 1) scalars(head + nvec * N, a.V);
 #pragma unroll
     for (int k = 16; k; k >>= 1) {
         const float M = __shfl_xor_sync(kFull, acc.M, k), s = __shfl_xor_sync(kFull, acc.s, k),
@@ -262,10 +368,30 @@ __global__ void __launch_bounds__(kThreads) lp_fwd_kernel(const LpArgs a) {
         sh.s[w] = acc.s;
         sh.u[w] = acc.u;
     }
-    if (TOP) sh.top[w][lane] = lane < a.K ? top.key : 0;
+    if (TOP) sh.top[w][lane] = top.key;
     __syncthreads();
+    if (TOP) join_lists(sh.top, kWarps, w, lane);
     acc.clear();
     for (int k = 0; k < kWarps; ++k) acc.join(sh.M[k], sh.s[k], sh.u[k]);
+    if (CLUSTER) {
+        cluster_wait();   // every block of the cluster runs
+        if (w == 0) {
+            if (lane == 0) {
+                asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(remote_address(&sh.cM[rank], 0)), "f"(acc.M) : "memory");
+                asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(remote_address(&sh.cs[rank], 0)), "f"(acc.s) : "memory");
+                asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(remote_address(&sh.cu[rank], 0)), "f"(acc.u) : "memory");
+            }
+            if (TOP)
+                asm volatile("st.shared::cluster.b64 [%0], %1;" ::"r"(remote_address(&sh.ctop[rank][lane], 0)),
+                             "l"(sh.top[0][lane]) : "memory");
+        }
+        cluster_arrive();
+        cluster_wait();
+        if (rank != 0) return;
+        acc.clear();
+        for (int k = 0; k < C; ++k) acc.join(sh.cM[k], sh.cs[k], sh.cu[k]);
+        if (TOP) join_lists(sh.ctop, C, w, lane);
+    }
     // z - lse = (x - ref) mul - sub for the row's logits
     float ref = 0.f, sub, lse, H, mul = 0.f;
     bool empty = false;
@@ -297,20 +423,10 @@ __global__ void __launch_bounds__(kThreads) lp_fwd_kernel(const LpArgs a) {
         if (a.entropy != nullptr) a.entropy[row] = H;
         if (a.lse != nullptr) a.lse[row] = lse;
     }
-    if (TOP && w == 0) {
-        for (int k = 1; k < kWarps; ++k) {
-            const uint64_t cand = sh.top[k][lane];
-            for (int i = 0; i < a.K; ++i) {   // descending: the first that fails ends the list
-                const uint64_t cc = __shfl_sync(kFull, cand, i);
-                if (cc <= __shfl_sync(kFull, top.key, a.K - 1)) break;
-                top.insert(cc);
-            }
-        }
-        if (lane < a.K) {
-            const uint32_t o = static_cast<uint32_t>(top.key >> 32);
-            if (a.top_vals != nullptr) a.top_vals[row * a.K + lane] = logp_of(value_of(o));
-            if (a.top_idx != nullptr) a.top_idx[row * a.K + lane] = static_cast<int32_t>(~static_cast<uint32_t>(top.key));
-        }
+    if (TOP && w == 0 && lane < a.K) {
+        const uint64_t key = CLUSTER ? sh.ctop[0][lane] : sh.top[0][lane];
+        if (a.top_vals != nullptr) a.top_vals[row * a.K + lane] = logp_of(value_of(static_cast<uint32_t>(key >> 32)));
+        if (a.top_idx != nullptr) a.top_idx[row * a.K + lane] = static_cast<int32_t>(~static_cast<uint32_t>(key));
     }
 }
 
@@ -326,48 +442,69 @@ __global__ void __launch_bounds__(kBwdThreads) lp_bwd_kernel(const LpArgs a, int
     const int part = static_cast<int>(blockIdx.x - row * parts);
     const T* const x = static_cast<const T*>(a.logits) + row * a.ld;
     T* const o = static_cast<T*>(a.dlogits) + row * a.d_ld;
+    const bool same = ((reinterpret_cast<uintptr_t>(x) ^ reinterpret_cast<uintptr_t>(o)) & 15) == 0;
+    const int head = min(a.V, static_cast<int>((16 - (reinterpret_cast<uintptr_t>(x) & 15)) % 16 / sizeof(T)));
+    const int nvec = (a.V - head) / N;
+    // this part's vectors, on their way while the row's scalars arrive
+    const int v0 = part * kBwdThreads * kBwdVecs + threadIdx.x;
+    Vec<T> r[kBwdVecs];
+#pragma unroll
+    for (int k = 0; k < kBwdVecs; ++k)
+        if (v0 + k * kBwdThreads < nvec) r[k].ld(x + head + static_cast<int64_t>(v0 + k * kBwdThreads) * N);
     const int t = __ldg(a.targets + row);
     const float dl = t >= 0 && t < a.V ? __ldg(a.d_logp + row) : 0.f;
     const float dh = a.d_entropy != nullptr ? __ldg(a.d_entropy + row) : 0.f;
-    const float H = __ldg(a.ent_in + row);
-    float lse = __ldg(a.lse_in + row), ref = 0.f;
+    const float H = __ldg(a.ent_in + row), lse = __ldg(a.lse_in + row);
     if (part == 0 && threadIdx.x == 0 && t >= a.V && a.status != nullptr) atomicOr(a.status, SDM_DEV_BAD_TARGET);
-    if (fabsf(lse) >= kFarLse && !isinf(lse)) {   // block-uniform: z - lse from z - z_max, log s
-        float m, s, u;
-        plain_stats(x, a.V, a.scale, sh, m, s, u);
-        ref = m;
-        lse = logf(s);
-    }
-    const bool empty = lse == -INFINITY;
-    auto grad = [&](float v, int id) {
-        const float d = max_nan((v - ref) * a.scale - lse, kFloor);   // log p; its product with p = 0 stays 0
-        const float p = empty ? 0.f : expf(d);
-        const float g = -p * (dl + dh * (empty ? 0.f : d + H)) + (id == t ? dl : 0.f);
-        return a.scale * g;
-    };
-    const bool same = ((reinterpret_cast<uintptr_t>(x) ^ reinterpret_cast<uintptr_t>(o)) & 15) == 0;
-    const int head = same ? min(a.V, static_cast<int>((16 - (reinterpret_cast<uintptr_t>(x) & 15)) % 16 / sizeof(T))) : a.V;
-    const int nvec = (a.V - head) / N;
-    // the logits outside the vectors: all of them where the two rows lie differently on 16 bytes
-    for (int i = part * kBwdThreads + threadIdx.x; i < head; i += parts * kBwdThreads) st1(o + i, grad(widen(x[i]), i));
-    for (int i = head + nvec * N + part * kBwdThreads + threadIdx.x; i < a.V; i += parts * kBwdThreads)
-        st1(o + i, grad(widen(x[i]), i));
-    for (int v0 = part * kBwdThreads * kBwdVecs; v0 < nvec; v0 += parts * kBwdThreads * kBwdVecs) {
-        Vec<T> r[kBwdVecs];
-#pragma unroll
-        for (int k = 0; k < kBwdVecs; ++k) {
-            const int v = v0 + k * kBwdThreads + threadIdx.x;
-            if (v < nvec) r[k].ld(x + head + static_cast<int64_t>(v) * N);
+    if (fabsf(lse) >= kFarLse) {
+        // block-uniform and rare: z - lse from differences to the largest logit, or (lse -inf) a row of zeros
+        const bool empty = lse == -INFINITY;
+        float m = 0.f, s = 1.f, u;
+        if (!isinf(lse)) plain_stats(x, a.V, a.scale, sh, m, s, u);
+        const float ls = logf(s);
+        const int per = kBwdThreads * kBwdVecs * N;
+        for (int i = part * per + threadIdx.x; i < (part + 1 == parts ? a.V : min(a.V, (part + 1) * per)); i += kBwdThreads) {
+            const float d = max_nan((widen(x[i]) - m) * a.scale - ls, kGradFloor), p = empty ? 0.f : expf(d);
+            const float g = -p * (dl + dh * (empty ? 0.f : d + H)) + (i == t ? dl : 0.f);
+            st1(o + i, a.scale * g);
         }
+        return;
+    }
+    // dlogits = p (k1 d + k0) with d = log p, and scale dl more at the target
+    const float k0 = -a.scale * (dl + dh * H), k1 = -a.scale * dh;
+    auto grad = [&](float v, int id) {
+        const float d = fmaf(max_nan(v, kGradFloor), a.scale, -lse);
+        return ex2(d * kLog2e) * fmaf(d, k1, k0) + (id == t ? a.scale * dl : 0.f);
+    };
+    if (part == 0) {   // the logits outside the vectors
+        const int tail = head + nvec * N, i = threadIdx.x < head ? threadIdx.x : tail + threadIdx.x - head;
+        if (i < a.V) st1(o + i, grad(widen(x[i]), i));
+    }
+    const uint64_t sc2 = pack2(a.scale, a.scale), ls2 = pack2(-lse, -lse), le2 = pack2(kLog2e, kLog2e),
+                   k02 = pack2(k0, k0), k12 = pack2(k1, k1);
 #pragma unroll
-        for (int k = 0; k < kBwdVecs; ++k) {
-            const int v = v0 + k * kBwdThreads + threadIdx.x;
-            if (v >= nvec) continue;
-            float f[N];
-            r[k].get(f);
+    for (int k = 0; k < kBwdVecs; ++k) {
+        const int v = v0 + k * kBwdThreads;
+        if (v >= nvec) continue;
+        float f[N];
 #pragma unroll
-            for (int i = 0; i < N; ++i) f[i] = grad(f[i], head + v * N + i);
-            Vec<T>::st(o + head + static_cast<int64_t>(v) * N, f);
+        for (int i = 0; i < N / 2; ++i) {
+            const uint64_t d2 = fma2(r[k].pair(i, kGradFloor), sc2, ls2);
+            float p, q;
+            unpack2(mul2(d2, le2), p, q);
+            unpack2(mul2(pack2(ex2(p), ex2(q)), fma2(d2, k12, k02)), f[2 * i], f[2 * i + 1]);
+        }
+        const int base = head + v * N, at = t - base;
+        if (at >= 0 && at < N) {
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                if (i == at) f[i] += a.scale * dl;
+        }
+        if (same) {
+            Vec<T>::st(o + base, f);
+        } else {   // the gradient's row lies differently on 16 bytes
+#pragma unroll
+            for (int i = 0; i < N; ++i) st1(o + base + i, f[i]);
         }
     }
 }
@@ -387,6 +524,14 @@ sdm_status check_logits(const sdm_logprob_shape* s, const void* p, int64_t ld, b
     if (reinterpret_cast<uintptr_t>(p) % (s->dtype == SDM_BF16 ? 2 : 4) != 0) return SDM_ERR_ALIGN;
     if (ld < (out ? s->V : 0) || ld > (int64_t(1) << 40)) return SDM_ERR_ARG;
     return SDM_OK;
+}
+
+// Blocks of a row: as many as leave each at least a batch, while the rows alone leave SMs idle.
+int cluster_of(const sdm_logprob_shape* s) {
+    const int64_t batch = kThreads * 16 / (s->dtype == SDM_BF16 ? 2 : 4);
+    int c = 1;
+    while (c < kMaxCluster && s->rows * c < 152 && s->V >= 2 * c * batch) c *= 2;
+    return c;
 }
 
 }  // namespace
@@ -409,10 +554,19 @@ extern "C" sdm_status sdm_token_logprobs(const sdm_logprob_shape* shape, const v
     a.rows = shape->rows; a.V = shape->V; a.K = shape->K; a.scale = shape->scale;
     const bool top = shape->K > 0 && (top_vals != nullptr || top_idx != nullptr);
     const bool bf = shape->dtype == SDM_BF16;
-    const auto kernel = bf ? (top ? lp_fwd_kernel<__nv_bfloat16, true> : lp_fwd_kernel<__nv_bfloat16, false>)
-                           : (top ? lp_fwd_kernel<float, true> : lp_fwd_kernel<float, false>);
-    const cudaError_t e = launch_dependent(kernel, dim3(static_cast<unsigned>(shape->rows)), dim3(kThreads), 0,
-                                           reinterpret_cast<cudaStream_t>(stream), a);
+    a.cluster = cluster_of(shape);
+    if (shape->rows * a.cluster > 0x7FFFFFFF) return SDM_ERR_SHAPE;
+    const dim3 grid(static_cast<unsigned>(shape->rows * a.cluster)), block(kThreads);
+    const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+    auto run = [&](auto t, auto with_top) {
+        using T = decltype(t);
+        constexpr bool TOP = decltype(with_top)::value;
+        return a.cluster > 1 ? launch_cluster(lp_fwd_kernel<T, TOP, true>, grid, block, a.cluster, cs, a)
+                             : launch_dependent(lp_fwd_kernel<T, TOP, false>, grid, block, 0, cs, a);
+    };
+    const std::true_type yes;
+    const std::false_type no;
+    const cudaError_t e = bf ? (top ? run(__nv_bfloat16{}, yes) : run(__nv_bfloat16{}, no)) : (top ? run(0.f, yes) : run(0.f, no));
     return e == cudaSuccess ? SDM_OK : SDM_ERR_CUDA;
 }
 

@@ -216,5 +216,45 @@ __device__ __forceinline__ float tsum16(const float (&v)[16], int lane) {
     return x;
 }
 
+// Two float32 in one 64-bit register pair: one instruction multiplies, adds or multiply-adds both (each rounded as the
+// scalar instruction rounds it).
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+    uint64_t o;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(o) : "f"(a), "f"(b));
+    return o;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t o;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(o) : "l"(a), "l"(b), "l"(c));
+    return o;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t o;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(o) : "l"(a), "l"(b));
+    return o;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t o;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(o) : "l"(a), "l"(b));
+    return o;
+}
+
+// The blocks of a cluster: this one's rank, the barrier in its two halves (release / acquire of every thread's accesses;
+// relaxed: the arrival alone), and the address of another block's copy of a shared variable.
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_arrive_relaxed() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+__device__ __forceinline__ uint32_t remote_address(const void* p, uint32_t rank) {
+    uint32_t a = static_cast<uint32_t>(__cvta_generic_to_shared(p));
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(a), "r"(rank));
+    return a;
+}
+
 }  // namespace rows
 }  // namespace sdm
