@@ -433,7 +433,7 @@ sdm_status sdm_glr_step(const sdm_glr_shape* shape, const void* x, int64_t x_ld,
                         uint32_t* status, sdm_stream_t stream);
 
 typedef struct {
-    int64_t tokens;
+    int64_t tokens;     /* tokens times heads: below about 2^31 */
     int32_t q_heads;    /* heads of q and of k (either may be 0, not both) */
     int32_t k_heads;
     int32_t hd;         /* columns of a head, a multiple of 8, up to 1024 */

@@ -29,7 +29,7 @@ using namespace rows;
 constexpr int kThreads = 256;
 constexpr int kMaxHd = 1024;
 constexpr int kMaxFreq = kMaxHd / 2;
-constexpr int kPartBlocks = 512;   // blocks of the backward at most: a row of weight gradients each
+constexpr int kPartBlocks = 304;   // blocks of the backward at most (two for each of 152 SMs): a row of weight gradients each
 
 struct RopeArgs {
     const void* q;
@@ -71,10 +71,10 @@ struct Place {
 };
 
 // The unit's cosines and sines of a position (1 and 0 behind rot_dim)
-__device__ __forceinline__ void turns(const RopeArgs& s, int64_t pos, int f, float (&c)[4], float (&sn)[4]) {
+__device__ __forceinline__ void turns(const RopeArgs& s, int pos, int f, float (&c)[4], float (&sn)[4]) {
     if (f >= 0) {
-        ld4(s.table + pos * s.rd + f, c);
-        ld4(s.table + pos * s.rd + s.rd / 2 + f, sn);
+        ld4(s.table + static_cast<int64_t>(pos) * s.rd + f, c);
+        ld4(s.table + static_cast<int64_t>(pos) * s.rd + s.rd / 2 + f, sn);
     } else {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -107,9 +107,15 @@ __device__ __forceinline__ void turn(float (&a)[4], float (&b)[4], const float (
     }
 }
 
-__device__ __forceinline__ float lanes_sum(float v, int lanes) {
-    for (int k = 1; k < lanes; k <<= 1) v += __shfl_xor_sync(kFull, v, k);
-    return v;
+// Each of the n values summed over the group's lanes, in every lane.
+template <int n>
+__device__ __forceinline__ void lanes_sum(float (&v)[n], int lanes) {
+#pragma unroll
+    for (int k = 1; k < 32; k <<= 1)
+        if (k < lanes) {
+#pragma unroll
+            for (int i = 0; i < n; ++i) v[i] += __shfl_xor_sync(kFull, v[i], k);
+        }
 }
 
 __device__ __forceinline__ void weights(const float* w, int a, int b, float (&o)[4], float (&p)[4]) {
@@ -122,128 +128,185 @@ __device__ __forceinline__ void weights(const float* w, int a, int b, float (&o)
     }
 }
 
-// One group of `lanes` lanes a (token, head); heads 0 .. Hq - 1 are queries, then the keys.
+// Heads that a group of lanes takes together (their loads in flight at once, one set of cosines and sines for all).
+template <typename T, int U>
+constexpr int heads_at_once() {
+    return U > 1 ? 1 : sizeof(T) == 2 ? 4 : 2;
+}
+
+// The token's position, or -1 for a padding token.
+__device__ __forceinline__ int position(const RopeArgs& s, int t, bool live) {
+    const int pos = __ldg(s.pos + t);
+    if (pos < s.max_pos) return pos < 0 ? -1 : pos;
+    if (live && s.status != nullptr) atomicOr(s.status, SDM_DEV_BAD_POSITION);
+    return -1;
+}
+
+// One group of `lanes` lanes takes up to HU heads of one kind of one token.
 template <typename T, int U>
 __global__ void __launch_bounds__(kThreads) rope_fwd_kernel(const RopeArgs s, int lanes) {
+    constexpr int HU = heads_at_once<T, U>();
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int per = kThreads / lanes, H = s.Hq + s.Hk;
-    const int64_t unit = blockIdx.x * static_cast<int64_t>(per) + threadIdx.x / lanes;
-    const bool live = unit < s.tokens * H;
-    const int64_t t = live ? unit / H : 0;
-    const int head = static_cast<int>(live ? unit - t * H : 0);
+    const int per = kThreads / lanes, cq = (s.Hq + HU - 1) / HU, ct = cq + (s.Hk + HU - 1) / HU;
+    const int units = static_cast<int>(s.tokens) * ct, unit = static_cast<int>(blockIdx.x) * per + threadIdx.x / lanes;
+    const bool live = unit < units;
+    const int t = live ? unit / ct : 0, ch = live ? unit - t * ct : 0;
+    const bool isq = ch < cq;
+    const int h0 = (isq ? ch : ch - cq) * HU, H = live ? (isq ? s.Hq : s.Hk) - h0 : 0;   // heads from h0 on
     Place<U> pl;
     pl.set(s, threadIdx.x % lanes, lanes);
-    const bool isq = head < s.Hq;
-    const T* const x = isq ? static_cast<const T*>(s.q) + t * s.q_ld + head * s.hd
-                           : static_cast<const T*>(s.k) + t * s.k_ld + (head - s.Hq) * s.hd;
-    T* const y = isq ? static_cast<T*>(s.qo) + t * s.qo_ld + head * s.hd
-                     : static_cast<T*>(s.ko) + t * s.ko_ld + (head - s.Hq) * s.hd;
-    int64_t pos = __ldg(s.pos + t);
-    if (pos >= s.max_pos) {
-        if (live && s.status != nullptr) atomicOr(s.status, SDM_DEV_BAD_POSITION);
-        pos = -1;
-    }
-    float a[U][4], b[U][4], ss = 0.f;
+    const T* const x = (isq ? static_cast<const T*>(s.q) + t * s.q_ld : static_cast<const T*>(s.k) + t * s.k_ld) + h0 * s.hd;
+    T* const y = (isq ? static_cast<T*>(s.qo) + t * s.qo_ld : static_cast<T*>(s.ko) + t * s.ko_ld) + h0 * s.hd;
+    Raw4<T> ra[HU][U], rb[HU][U];
 #pragma unroll
-    for (int i = 0; i < U; ++i) {
-        ld4(x + pl.a[i], a[i]);
-        ld4(x + pl.b[i], b[i]);
-        if (pl.on[i]) ss += dot4(a[i], a[i]) + dot4(b[i], b[i]);
-    }
-    const float r = s.norm ? rsqrtf(lanes_sum(ss, lanes) / s.hd + s.eps) : 1.f;
+    for (int h = 0; h < HU; ++h)
 #pragma unroll
-    for (int i = 0; i < U; ++i) {
-        float c[4], sn[4], wa[4], wb[4];
-        turns(s, pos < 0 ? 0 : pos, pl.f[i], c, sn);
-        weights(s.norm ? (isq ? s.wq : s.wk) : nullptr, pl.a[i], pl.b[i], wa, wb);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            a[i][j] = a[i][j] * r * wa[j];
-            b[i][j] = b[i][j] * r * wb[j];
+        for (int i = 0; i < U; ++i) {
+            ra[h][i].zero();
+            rb[h][i].zero();
+            if (h < H) {
+                ra[h][i].ld_cg(x + h * s.hd + pl.a[i]);
+                rb[h][i].ld_cg(x + h * s.hd + pl.b[i]);
+            }
         }
-        if (pl.f[i] >= 0) turn(a[i], b[i], c, sn, 1.f, s.interleaved);
-        if (pos < 0)
+    const int pos = position(s, t, live);
+    float c[U][4], sn[U][4], wa[U][4], wb[U][4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) a[i][j] = b[i][j] = 0.f;
-        if (live && pl.on[i]) {
-            st4(y + pl.a[i], a[i]);
-            st4(y + pl.b[i], b[i]);
+    for (int i = 0; i < U; ++i) {
+        turns(s, max(pos, 0), pl.f[i], c[i], sn[i]);
+        weights(s.norm ? (isq ? s.wq : s.wk) : nullptr, pl.a[i], pl.b[i], wa[i], wb[i]);
+    }
+    float ss[HU];
+#pragma unroll
+    for (int h = 0; h < HU; ++h) {
+        ss[h] = 0.f;
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            float a[4], b[4];
+            ra[h][i].get(a);
+            rb[h][i].get(b);
+            if (pl.on[i]) ss[h] += dot4(a, a) + dot4(b, b);
+        }
+    }
+    if (s.norm) lanes_sum(ss, lanes);
+#pragma unroll
+    for (int h = 0; h < HU; ++h) {
+        const float r = pos < 0 ? 0.f : s.norm ? rsqrtf(ss[h] / s.hd + s.eps) : 1.f;
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            float a[4], b[4];
+            ra[h][i].get(a);
+            rb[h][i].get(b);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                a[j] = pos < 0 ? 0.f : a[j] * r * wa[i][j];   // a padding token's outputs are 0 whatever it holds
+                b[j] = pos < 0 ? 0.f : b[j] * r * wb[i][j];
+            }
+            if (pl.f[i] >= 0) turn(a, b, c[i], sn[i], 1.f, s.interleaved);
+            if (h < H && pl.on[i]) {
+                st4(y + h * s.hd + pl.a[i], a);
+                st4(y + h * s.hd + pl.b[i], b);
+            }
         }
     }
 }
 
 // Groups of lanes walk the tokens' heads, queries first, then keys; a lane's weight gradients stay in registers,
-// are joined over the block in a fixed order and written as the block's row of `part`.
+// are joined over the block in a fixed order and written as the block's row of `part`. mean(t x) does not depend on
+// r, so both of a head's sums go over the lanes together.
 template <typename T, int U>
-__global__ void __launch_bounds__(kThreads) rope_bwd_kernel(const RopeArgs s, int lanes) {
+__global__ void __launch_bounds__(kThreads, U == 1 ? 2 : 1) rope_bwd_kernel(const RopeArgs s, int lanes) {
+    constexpr int HU = heads_at_once<T, U>();
     extern __shared__ float sm[];   // [groups][hd]
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int per = kThreads / lanes, group = threadIdx.x / lanes;
+    const float inv = 1.f / s.hd;
     Place<U> pl;
     pl.set(s, threadIdx.x % lanes, lanes);
     for (int side = 0; side < 2; ++side) {
-        const int H = side ? s.Hk : s.Hq;
+        const int H = side ? s.Hk : s.Hq, chunks = (H + HU - 1) / HU;
         const T* const X = static_cast<const T*>(side ? s.k : s.q);
         const T* const G = static_cast<const T*>(side ? s.dko : s.dqo);
         T* const Y = static_cast<T*>(side ? s.ko : s.qo);
         const int64_t x_ld = side ? s.k_ld : s.q_ld, g_ld = side ? s.dko_ld : s.dqo_ld, y_ld = side ? s.ko_ld : s.qo_ld;
-        const float* const w = s.norm ? (side ? s.wk : s.wq) : nullptr;
-        float da[U][4], db[U][4];
+        float wa[U][4], wb[U][4], da[U][4], db[U][4];
 #pragma unroll
-        for (int i = 0; i < U; ++i)
+        for (int i = 0; i < U; ++i) {
+            weights(s.norm ? (side ? s.wk : s.wq) : nullptr, pl.a[i], pl.b[i], wa[i], wb[i]);
 #pragma unroll
             for (int j = 0; j < 4; ++j) da[i][j] = db[i][j] = 0.f;
-        const int64_t units = s.tokens * H;
-        const int64_t step = static_cast<int64_t>(gridDim.x) * per;
-        for (int64_t u0 = blockIdx.x * static_cast<int64_t>(per); u0 < units; u0 += step) {   // block-uniform
-            const int64_t u = u0 + group;
+        }
+        const int units = static_cast<int>(s.tokens) * chunks;
+        for (int u0 = blockIdx.x * per; u0 < units; u0 += gridDim.x * per) {   // block-uniform
+            const int u = u0 + group;
             const bool live = u < units;
-            const int64_t t = live ? u / H : 0;
-            const int head = static_cast<int>(live ? u - t * H : 0);
-            int64_t pos = __ldg(s.pos + t);
-            if (pos >= s.max_pos) {
-                if (live && s.status != nullptr) atomicOr(s.status, SDM_DEV_BAD_POSITION);
-                pos = -1;
-            }
-            float a[U][4], b[U][4], ea[U][4], eb[U][4], ss = 0.f, tx = 0.f;
+            const int t = live ? u / chunks : 0, h0 = live ? (u - t * chunks) * HU : 0, n = live ? H - h0 : 0;
+            const T* const x = X + t * x_ld + h0 * s.hd;
+            const T* const g = G + t * g_ld + h0 * s.hd;
+            Raw4<T> ra[HU][U], rb[HU][U], ga[HU][U], gb[HU][U];
 #pragma unroll
-            for (int i = 0; i < U; ++i) {
-                ld4(X + t * x_ld + head * s.hd + pl.a[i], a[i]);
-                ld4(X + t * x_ld + head * s.hd + pl.b[i], b[i]);
-                ld4(G + t * g_ld + head * s.hd + pl.a[i], ea[i]);
-                ld4(G + t * g_ld + head * s.hd + pl.b[i], eb[i]);
-                if (pl.on[i]) ss += dot4(a[i], a[i]) + dot4(b[i], b[i]);
-            }
-            const float r = s.norm ? rsqrtf(lanes_sum(ss, lanes) / s.hd + s.eps) : 1.f;
-            const bool use = live && pos >= 0;
+            for (int h = 0; h < HU; ++h)
 #pragma unroll
-            for (int i = 0; i < U; ++i) {
-                float c[4], sn[4], wa[4], wb[4];
-                turns(s, pos < 0 ? 0 : pos, pl.f[i], c, sn);
-                weights(w, pl.a[i], pl.b[i], wa, wb);
-                if (pl.f[i] >= 0) turn(ea[i], eb[i], c, sn, -1.f, s.interleaved);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    if (use) {
-                        da[i][j] = fmaf(ea[i][j], a[i][j] * r, da[i][j]);
-                        db[i][j] = fmaf(eb[i][j], b[i][j] * r, db[i][j]);
+                for (int i = 0; i < U; ++i) {
+                    ra[h][i].zero();
+                    rb[h][i].zero();
+                    ga[h][i].zero();
+                    gb[h][i].zero();
+                    if (h < n && pl.on[i]) {
+                        ra[h][i].ld_cg(x + h * s.hd + pl.a[i]);
+                        rb[h][i].ld_cg(x + h * s.hd + pl.b[i]);
+                        ga[h][i].ld_cg(g + h * s.hd + pl.a[i]);
+                        gb[h][i].ld_cg(g + h * s.hd + pl.b[i]);
                     }
-                    ea[i][j] *= wa[j];
-                    eb[i][j] *= wb[j];
                 }
-                if (pl.on[i]) tx += dot4(ea[i], a[i]) + dot4(eb[i], b[i]);
+            const int pos = position(s, t, live);
+            float c[U][4], sn[U][4], sums[2 * HU];
+#pragma unroll
+            for (int i = 0; i < U; ++i) turns(s, max(pos, 0), pl.f[i], c[i], sn[i]);
+#pragma unroll
+            for (int h = 0; h < HU; ++h) {
+                sums[2 * h] = sums[2 * h + 1] = 0.f;
+#pragma unroll
+                for (int i = 0; i < U; ++i) {
+                    float a[4], b[4], ea[4], eb[4];
+                    ra[h][i].get(a);
+                    rb[h][i].get(b);
+                    ga[h][i].get(ea);
+                    gb[h][i].get(eb);
+                    if (pl.f[i] >= 0) turn(ea, eb, c[i], sn[i], -1.f, s.interleaved);
+                    sums[2 * h] += dot4(a, a) + dot4(b, b);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        sums[2 * h + 1] += ea[j] * wa[i][j] * a[j] + eb[j] * wb[i][j] * b[j];
+                }
             }
-            const float k = s.norm ? lanes_sum(tx, lanes) / s.hd * r * r : 0.f;
+            if (s.norm) lanes_sum(sums, lanes);
 #pragma unroll
-            for (int i = 0; i < U; ++i) {
+            for (int h = 0; h < HU; ++h) {
+                const float r = s.norm ? rsqrtf(sums[2 * h] * inv + s.eps) : 1.f;
+                const float k = s.norm ? sums[2 * h + 1] * inv * r * r : 0.f;
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    ea[i][j] = pos < 0 ? 0.f : r * (ea[i][j] - a[i][j] * k);
-                    eb[i][j] = pos < 0 ? 0.f : r * (eb[i][j] - b[i][j] * k);
-                }
-                if (live && pl.on[i]) {
-                    st4(Y + t * y_ld + head * s.hd + pl.a[i], ea[i]);
-                    st4(Y + t * y_ld + head * s.hd + pl.b[i], eb[i]);
+                for (int i = 0; i < U; ++i) {
+                    float a[4], b[4], ea[4], eb[4];
+                    ra[h][i].get(a);
+                    rb[h][i].get(b);
+                    ga[h][i].get(ea);
+                    gb[h][i].get(eb);
+                    if (pl.f[i] >= 0) turn(ea, eb, c[i], sn[i], -1.f, s.interleaved);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        if (pos >= 0 && h < n) {
+                            da[i][j] = fmaf(ea[j], a[j] * r, da[i][j]);
+                            db[i][j] = fmaf(eb[j], b[j] * r, db[i][j]);
+                        }
+                        ea[j] = pos < 0 ? 0.f : r * (ea[j] * wa[i][j] - a[j] * k);
+                        eb[j] = pos < 0 ? 0.f : r * (eb[j] * wb[i][j] - b[j] * k);
+                    }
+                    if (h < n && pl.on[i]) {
+                        T* const y = Y + t * y_ld + (h0 + h) * s.hd;
+                        st4(y + pl.a[i], ea);
+                        st4(y + pl.b[i], eb);
+                    }
                 }
             }
         }
@@ -316,6 +379,7 @@ sdm_status check(const sdm_rope_shape* s) {
         !(s->eps >= 0.f))
         return SDM_ERR_SHAPE;
     if (s->hd % 8 != 0 || s->rot_dim % 8 != 0) return SDM_ERR_ALIGN;
+    if (s->tokens * (s->q_heads + s->k_heads) >= (int64_t(1) << 31) - (1 << 20)) return SDM_ERR_SHAPE;
     return SDM_OK;
 }
 
@@ -347,8 +411,11 @@ int head_lanes(int hd) {
     return lanes;
 }
 
+int heads_together(const sdm_rope_shape* s) { return s->hd > 256 ? 1 : s->dtype == SDM_BF16 ? 4 : 2; }
+
 int bwd_blocks(const sdm_rope_shape* s) {
-    const int64_t units = s->tokens * std::max(s->q_heads, s->k_heads), per = kThreads / head_lanes(s->hd);
+    const int hu = heads_together(s);
+    const int64_t units = s->tokens * ((std::max(s->q_heads, s->k_heads) + hu - 1) / hu), per = kThreads / head_lanes(s->hd);
     return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(kPartBlocks, (units + per - 1) / per)));
 }
 
@@ -418,8 +485,9 @@ extern "C" sdm_status sdm_qk_norm_rope(const sdm_rope_shape* shape, const void* 
     a.q = q; a.q_ld = q_ld; a.k = k; a.k_ld = k_ld; a.pos = positions; a.table = table; a.wq = wq; a.wk = wk;
     a.qo = q_out; a.qo_ld = qo_ld; a.ko = k_out; a.ko_ld = ko_ld; a.status = status;
     const int lanes = head_lanes(shape->hd);
-    const int64_t blocks = (shape->tokens * (a.Hq + a.Hk) * lanes + kThreads - 1) / kThreads;
-    if (blocks > 0x7FFFFFFF) return SDM_ERR_SHAPE;
+    const int hu = heads_together(shape);
+    const int64_t units = shape->tokens * ((a.Hq + hu - 1) / hu + (a.Hk + hu - 1) / hu);
+    const int64_t blocks = (units * lanes + kThreads - 1) / kThreads;
     const cudaError_t e = by_type(shape, [&](auto t, auto u) {
         return launch_dependent(rope_fwd_kernel<decltype(t), decltype(u)::value>, dim3(static_cast<unsigned>(blocks)),
                                 dim3(kThreads), 0, reinterpret_cast<cudaStream_t>(stream), a, lanes);
