@@ -111,42 +111,6 @@ __device__ __forceinline__ void sequence(const GlrArgs& a, int p, int64_t& b, in
     if ((lo < 0 || hi > a.rows || lo > hi) && a.status != nullptr && threadIdx.x == 0) atomicOr(a.status, SDM_DEV_BAD_OFFSET);
 }
 
-// Four channels as two pairs of float32.
-struct Quad {
-    uint64_t lo, hi;
-};
-__device__ __forceinline__ Quad quad(const float (&v)[4]) { return {pack2(v[0], v[1]), pack2(v[2], v[3])}; }
-__device__ __forceinline__ Quad quad(float v) { return {pack2(v, v), pack2(v, v)}; }
-__device__ __forceinline__ void floats(const Quad& q, float (&v)[4]) {
-    unpack2(q.lo, v[0], v[1]);
-    unpack2(q.hi, v[2], v[3]);
-}
-__device__ __forceinline__ Quad fma4(const Quad& a, const Quad& b, const Quad& c) { return {fma2(a.lo, b.lo, c.lo), fma2(a.hi, b.hi, c.hi)}; }
-__device__ __forceinline__ Quad mul4(const Quad& a, const Quad& b) { return {mul2(a.lo, b.lo), mul2(a.hi, b.hi)}; }
-__device__ __forceinline__ Quad add4(const Quad& a, const Quad& b) { return {add2(a.lo, b.lo), add2(a.hi, b.hi)}; }
-template <typename T>
-__device__ __forceinline__ Quad quad(const Raw4<T>& r) {
-    float v[4];
-    r.get(v);
-    return quad(v);
-}
-__device__ __forceinline__ Raw4<float> load4(const float* p) {
-    Raw4<float> r;
-    r.ld(p);
-    return r;
-}
-__device__ __forceinline__ Quad quad(const float* p) {   // 16 bytes of shared memory
-    float v[4];
-    get4(p, v);
-    return quad(v);
-}
-template <typename T>
-__device__ __forceinline__ void st4(T* p, const Quad& q) {
-    float v[4];
-    floats(q, v);
-    rows::st4(p, v);
-}
-
 // A gate's exp is 2^(g log2 e): within 4 u + |g| u (u = 2^-24), and exactly 0 and 1 at -inf and 0.
 constexpr float kLog2e = 1.44269504088896341f;
 __device__ __forceinline__ float exp2_gate(float t) {
@@ -238,7 +202,7 @@ __device__ __forceinline__ void st_remote(const float* p, uint32_t rank, const Q
 }
 
 // h = A h + B from a pair in shared memory
-__device__ __forceinline__ void join(Quad& h, const float* A, const float* B) { h = fma4(quad(A), h, quad(B)); }
+__device__ __forceinline__ void join(Quad& h, const float* A, const float* B) { h = fma4(quad_at(A), h, quad_at(B)); }
 
 // One warp joins the block's warps' pairs and writes the block's pair into every block of the cluster, at its own rank.
 template <int WARPS, bool REVERSE>
@@ -248,8 +212,8 @@ __device__ __forceinline__ void share_pair(const float (*A)[kTileCols], const fl
 #pragma unroll
     for (int j = 0; j < WARPS; ++j) {
         const int k = REVERSE ? WARPS - 1 - j : j;
-        const Quad ak = quad(&A[k][lane * 4]);
-        pb = fma4(ak, pb, quad(&B[k][lane * 4]));
+        const Quad ak = quad_at(&A[k][lane * 4]);
+        pb = fma4(ak, pb, quad_at(&B[k][lane * 4]));
         pa = mul4(ak, pa);
     }
     for (int k = 0; k < K; ++k) {

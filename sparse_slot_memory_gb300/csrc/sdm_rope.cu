@@ -16,6 +16,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstring>
+#include <type_traits>
 
 #include "sdm_checks.cuh"
 #include "sdm_internal.cuh"
@@ -70,41 +71,73 @@ struct Place {
     }
 };
 
-// The unit's cosines and sines of a position (1 and 0 behind rot_dim)
-__device__ __forceinline__ void turns(const RopeArgs& s, int pos, int f, float (&c)[4], float (&sn)[4]) {
-    if (f >= 0) {
-        ld4(s.table + static_cast<int64_t>(pos) * s.rd + f, c);
-        ld4(s.table + static_cast<int64_t>(pos) * s.rd + s.rd / 2 + f, sn);
+// A unit's eight values as the first and the second ones of its four pairs. Behind rot_dim and in the half layout those
+// are its two halves; in the interleaved one its even and odd columns.
+struct Pairs {
+    Quad a, b;
+};
+template <bool INTER>
+__device__ __forceinline__ Pairs pairs(const float (&x)[4], const float (&y)[4]) {
+    if (INTER) return {{pack2(x[0], x[2]), pack2(y[0], y[2])}, {pack2(x[1], x[3]), pack2(y[1], y[3])}};
+    return {quad(x), quad(y)};
+}
+template <bool INTER, typename T>
+__device__ __forceinline__ Pairs pairs(const Raw4<T>& x, const Raw4<T>& y) {
+    float u[4], v[4];
+    x.get(u);
+    y.get(v);
+    return pairs<INTER>(u, v);
+}
+template <bool INTER, typename T>
+__device__ __forceinline__ void st_pairs(T* x, T* y, const Pairs& p) {
+    float u[4], v[4];
+    floats(p.a, u);
+    floats(p.b, v);
+    if (INTER) {
+        const float s[4] = {u[0], v[0], u[1], v[1]}, t[4] = {u[2], v[2], u[3], v[3]};
+        rows::st4(x, s);
+        rows::st4(y, t);
     } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            c[j] = 1.f;
-            sn[j] = 0.f;
-        }
+        rows::st4(x, u);
+        rows::st4(y, v);
     }
 }
 
-// The unit's pairs turned by `sign` times the angle: pairs (a[j], b[j]) in the half layout and behind rot_dim,
-// neighbours in the interleaved one.
-__device__ __forceinline__ void turn(float (&a)[4], float (&b)[4], const float (&c)[4], const float (&s)[4], float sign,
-                                     bool inter) {
-    if (inter) {
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const float x = a[2 * j], y = a[2 * j + 1], z = b[2 * j], w = b[2 * j + 1];
-            a[2 * j] = x * c[j] - sign * y * s[j];
-            a[2 * j + 1] = y * c[j] + sign * x * s[j];
-            b[2 * j] = z * c[2 + j] - sign * w * s[2 + j];
-            b[2 * j + 1] = w * c[2 + j] + sign * z * s[2 + j];
-        }
-    } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float x = a[j], y = b[j];
-            a[j] = x * c[j] - sign * y * s[j];
-            b[j] = y * c[j] + sign * x * s[j];
-        }
-    }
+// The cosines and sines of a unit's four pairs at a position
+struct Turn {
+    Quad c, s;
+};
+__device__ __forceinline__ Turn turn_of(const RopeArgs& s, int pos, int f) {
+    if (f < 0) return {quad(1.f), quad(0.f)};
+    const float* const t = s.table + static_cast<int64_t>(pos) * s.rd + f;
+    return {quad(load4(t)), quad(load4(t + s.rd / 2))};
+}
+__device__ __forceinline__ Quad negative(const Quad& q) {
+    return {q.lo ^ 0x8000000080000000ull, q.hi ^ 0x8000000080000000ull};
+}
+// Pairs turned by the angle (back: by its opposite); those behind rot_dim stay as they are, whatever they hold.
+template <bool BACK>
+__device__ __forceinline__ Pairs turned(const Pairs& p, const Turn& t, bool on) {
+    if (!on) return p;
+    const Quad n = negative(t.s);
+    return {fma4(p.a, t.c, mul4(p.b, BACK ? t.s : n)), fma4(p.b, t.c, mul4(p.a, BACK ? n : t.s))};
+}
+
+template <bool INTER>
+__device__ __forceinline__ Pairs weights(const float* w, int a, int b) {
+    if (w == nullptr) return {quad(1.f), quad(1.f)};
+    return pairs<INTER>(load4(w + a), load4(w + b));
+}
+__device__ __forceinline__ float sum4(const Quad& q) {
+    float a, b;
+    unpack2(add2(q.lo, q.hi), a, b);
+    return a + b;
+}
+__device__ __forceinline__ float dot(const Pairs& x, const Pairs& y) { return sum4(fma4(x.a, y.a, mul4(x.b, y.b))); }
+__device__ __forceinline__ Pairs times(const Pairs& x, const Pairs& y) { return {mul4(x.a, y.a), mul4(x.b, y.b)}; }
+__device__ __forceinline__ Pairs times(const Pairs& x, float f) {
+    const Quad q = quad(f);
+    return {mul4(x.a, q), mul4(x.b, q)};
 }
 
 // Each of the n values summed over the group's lanes, in every lane.
@@ -116,16 +149,6 @@ __device__ __forceinline__ void lanes_sum(float (&v)[n], int lanes) {
 #pragma unroll
             for (int i = 0; i < n; ++i) v[i] += __shfl_xor_sync(kFull, v[i], k);
         }
-}
-
-__device__ __forceinline__ void weights(const float* w, int a, int b, float (&o)[4], float (&p)[4]) {
-    if (w != nullptr) {
-        ld4(w + a, o);
-        ld4(w + b, p);
-    } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) o[j] = p[j] = 1.f;
-    }
 }
 
 // Heads that a group of lanes takes together (their loads in flight at once, one set of cosines and sines for all).
@@ -143,7 +166,7 @@ __device__ __forceinline__ int position(const RopeArgs& s, int t, bool live) {
 }
 
 // One group of `lanes` lanes takes up to HU heads of one kind of one token.
-template <typename T, int U>
+template <typename T, int U, bool INTER>
 __global__ void __launch_bounds__(kThreads) rope_fwd_kernel(const RopeArgs s, int lanes) {
     constexpr int HU = heads_at_once<T, U>();
     asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -170,11 +193,12 @@ __global__ void __launch_bounds__(kThreads) rope_fwd_kernel(const RopeArgs s, in
             }
         }
     const int pos = position(s, t, live);
-    float c[U][4], sn[U][4], wa[U][4], wb[U][4];
+    Turn turn[U];
+    Pairs wt[U];
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-        turns(s, max(pos, 0), pl.f[i], c[i], sn[i]);
-        weights(s.norm ? (isq ? s.wq : s.wk) : nullptr, pl.a[i], pl.b[i], wa[i], wb[i]);
+        turn[i] = turn_of(s, max(pos, 0), pl.f[i]);
+        wt[i] = weights<INTER>(s.norm ? (isq ? s.wq : s.wk) : nullptr, pl.a[i], pl.b[i]);
     }
     float ss[HU];
 #pragma unroll
@@ -182,31 +206,20 @@ __global__ void __launch_bounds__(kThreads) rope_fwd_kernel(const RopeArgs s, in
         ss[h] = 0.f;
 #pragma unroll
         for (int i = 0; i < U; ++i) {
-            float a[4], b[4];
-            ra[h][i].get(a);
-            rb[h][i].get(b);
-            if (pl.on[i]) ss[h] += dot4(a, a) + dot4(b, b);
+            const Pairs x = pairs<INTER>(ra[h][i], rb[h][i]);
+            if (pl.on[i]) ss[h] += dot(x, x);
         }
     }
     if (s.norm) lanes_sum(ss, lanes);
 #pragma unroll
     for (int h = 0; h < HU; ++h) {
-        const float r = pos < 0 ? 0.f : s.norm ? rsqrtf(ss[h] / s.hd + s.eps) : 1.f;
+        const float r = s.norm ? rsqrtf(ss[h] / s.hd + s.eps) : 1.f;
 #pragma unroll
         for (int i = 0; i < U; ++i) {
-            float a[4], b[4];
-            ra[h][i].get(a);
-            rb[h][i].get(b);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                a[j] = pos < 0 ? 0.f : a[j] * r * wa[i][j];   // a padding token's outputs are 0 whatever it holds
-                b[j] = pos < 0 ? 0.f : b[j] * r * wb[i][j];
-            }
-            if (pl.f[i] >= 0) turn(a, b, c[i], sn[i], 1.f, s.interleaved);
-            if (h < H && pl.on[i]) {
-                st4(y + h * s.hd + pl.a[i], a);
-                st4(y + h * s.hd + pl.b[i], b);
-            }
+            Pairs n = pairs<INTER>(ra[h][i], rb[h][i]);
+            n = turned<false>(times(times(n, r), wt[i]), turn[i], pl.f[i] >= 0);
+            if (pos < 0) n = {quad(0.f), quad(0.f)};   // a padding token's outputs are 0 whatever it holds
+            if (h < H && pl.on[i]) st_pairs<INTER>(y + h * s.hd + pl.a[i], y + h * s.hd + pl.b[i], n);
         }
     }
 }
@@ -214,7 +227,7 @@ __global__ void __launch_bounds__(kThreads) rope_fwd_kernel(const RopeArgs s, in
 // Groups of lanes walk the tokens' heads, queries first, then keys; a lane's weight gradients stay in registers,
 // are joined over the block in a fixed order and written as the block's row of `part`. mean(t x) does not depend on
 // r, so both of a head's sums go over the lanes together.
-template <typename T, int U>
+template <typename T, int U, bool INTER>
 __global__ void __launch_bounds__(kThreads, U == 1 ? 2 : 1) rope_bwd_kernel(const RopeArgs s, int lanes) {
     constexpr int HU = heads_at_once<T, U>();
     extern __shared__ float sm[];   // [groups][hd]
@@ -229,12 +242,11 @@ __global__ void __launch_bounds__(kThreads, U == 1 ? 2 : 1) rope_bwd_kernel(cons
         const T* const G = static_cast<const T*>(side ? s.dko : s.dqo);
         T* const Y = static_cast<T*>(side ? s.ko : s.qo);
         const int64_t x_ld = side ? s.k_ld : s.q_ld, g_ld = side ? s.dko_ld : s.dqo_ld, y_ld = side ? s.ko_ld : s.qo_ld;
-        float wa[U][4], wb[U][4], da[U][4], db[U][4];
+        Pairs wt[U], dw[U];
 #pragma unroll
         for (int i = 0; i < U; ++i) {
-            weights(s.norm ? (side ? s.wk : s.wq) : nullptr, pl.a[i], pl.b[i], wa[i], wb[i]);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) da[i][j] = db[i][j] = 0.f;
+            wt[i] = weights<INTER>(s.norm ? (side ? s.wk : s.wq) : nullptr, pl.a[i], pl.b[i]);
+            dw[i] = {quad(0.f), quad(0.f)};
         }
         const int units = static_cast<int>(s.tokens) * chunks;
         for (int u0 = blockIdx.x * per; u0 < units; u0 += gridDim.x * per) {   // block-uniform
@@ -260,63 +272,44 @@ __global__ void __launch_bounds__(kThreads, U == 1 ? 2 : 1) rope_bwd_kernel(cons
                     }
                 }
             const int pos = position(s, t, live);
-            float c[U][4], sn[U][4], sums[2 * HU];
+            Turn turn[U];
+            float sums[2 * HU];
 #pragma unroll
-            for (int i = 0; i < U; ++i) turns(s, max(pos, 0), pl.f[i], c[i], sn[i]);
+            for (int i = 0; i < U; ++i) turn[i] = turn_of(s, max(pos, 0), pl.f[i]);
 #pragma unroll
             for (int h = 0; h < HU; ++h) {
                 sums[2 * h] = sums[2 * h + 1] = 0.f;
 #pragma unroll
                 for (int i = 0; i < U; ++i) {
-                    float a[4], b[4], ea[4], eb[4];
-                    ra[h][i].get(a);
-                    rb[h][i].get(b);
-                    ga[h][i].get(ea);
-                    gb[h][i].get(eb);
-                    if (pl.f[i] >= 0) turn(ea, eb, c[i], sn[i], -1.f, s.interleaved);
-                    sums[2 * h] += dot4(a, a) + dot4(b, b);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        sums[2 * h + 1] += ea[j] * wa[i][j] * a[j] + eb[j] * wb[i][j] * b[j];
+                    const Pairs x = pairs<INTER>(ra[h][i], rb[h][i]);
+                    const Pairs e = turned<true>(pairs<INTER>(ga[h][i], gb[h][i]), turn[i], pl.f[i] >= 0);
+                    sums[2 * h] += dot(x, x);
+                    sums[2 * h + 1] += dot(times(e, wt[i]), x);
                 }
             }
             if (s.norm) lanes_sum(sums, lanes);
 #pragma unroll
             for (int h = 0; h < HU; ++h) {
                 const float r = s.norm ? rsqrtf(sums[2 * h] * inv + s.eps) : 1.f;
-                const float k = s.norm ? sums[2 * h + 1] * inv * r * r : 0.f;
+                const float k = s.norm ? -sums[2 * h + 1] * inv * r * r * r : 0.f;   // dx = r t + k x
 #pragma unroll
                 for (int i = 0; i < U; ++i) {
-                    float a[4], b[4], ea[4], eb[4];
-                    ra[h][i].get(a);
-                    rb[h][i].get(b);
-                    ga[h][i].get(ea);
-                    gb[h][i].get(eb);
-                    if (pl.f[i] >= 0) turn(ea, eb, c[i], sn[i], -1.f, s.interleaved);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        if (pos >= 0 && h < n) {
-                            da[i][j] = fmaf(ea[j], a[j] * r, da[i][j]);
-                            db[i][j] = fmaf(eb[j], b[j] * r, db[i][j]);
-                        }
-                        ea[j] = pos < 0 ? 0.f : r * (ea[j] * wa[i][j] - a[j] * k);
-                        eb[j] = pos < 0 ? 0.f : r * (eb[j] * wb[i][j] - b[j] * k);
-                    }
-                    if (h < n && pl.on[i]) {
-                        T* const y = Y + t * y_ld + (h0 + h) * s.hd;
-                        st4(y + pl.a[i], ea);
-                        st4(y + pl.b[i], eb);
-                    }
+                    const Pairs x = pairs<INTER>(ra[h][i], rb[h][i]);
+                    const Pairs e = times(turned<true>(pairs<INTER>(ga[h][i], gb[h][i]), turn[i], pl.f[i] >= 0), r);
+                    if (pos >= 0 && h < n) dw[i] = {fma4(e.a, x.a, dw[i].a), fma4(e.b, x.b, dw[i].b)};
+                    const Quad k4 = quad(k);
+                    Pairs d = s.norm ? times(e, wt[i]) : e;
+                    if (s.norm) d = {fma4(x.a, k4, d.a), fma4(x.b, k4, d.b)};
+                    if (pos < 0) d = {quad(0.f), quad(0.f)};
+                    T* const y = Y + t * y_ld + (h0 + h) * s.hd;
+                    if (h < n && pl.on[i]) st_pairs<INTER>(y + pl.a[i], y + pl.b[i], d);
                 }
             }
         }
         if (s.part == nullptr) continue;
 #pragma unroll
         for (int i = 0; i < U; ++i)
-            if (pl.on[i]) {
-                st4(sm + group * s.hd + pl.a[i], da[i]);
-                st4(sm + group * s.hd + pl.b[i], db[i]);
-            }
+            if (pl.on[i]) st_pairs<INTER>(sm + group * s.hd + pl.a[i], sm + group * s.hd + pl.b[i], dw[i]);
         __syncthreads();
         for (int c = threadIdx.x; c < s.hd; c += kThreads) {
             float v = 0.f;
@@ -422,10 +415,11 @@ int bwd_blocks(const sdm_rope_shape* s) {
 template <typename F>
 cudaError_t by_type(const sdm_rope_shape* s, F f) {
     const int u = (s->hd / 8 + 31) / 32;
-    auto with = [&](auto t) {
-        return u == 1 ? f(t, std::integral_constant<int, 1>{})
-               : u == 2 ? f(t, std::integral_constant<int, 2>{}) : f(t, std::integral_constant<int, 4>{});
+    auto units = [&](auto t, auto inter) {
+        return u == 1 ? f(t, std::integral_constant<int, 1>{}, inter)
+               : u == 2 ? f(t, std::integral_constant<int, 2>{}, inter) : f(t, std::integral_constant<int, 4>{}, inter);
     };
+    auto with = [&](auto t) { return s->layout ? units(t, std::true_type{}) : units(t, std::false_type{}); };
     return s->dtype == SDM_BF16 ? with(__nv_bfloat16{}) : with(0.f);
 }
 
@@ -488,8 +482,8 @@ extern "C" sdm_status sdm_qk_norm_rope(const sdm_rope_shape* shape, const void* 
     const int hu = heads_together(shape);
     const int64_t units = shape->tokens * ((a.Hq + hu - 1) / hu + (a.Hk + hu - 1) / hu);
     const int64_t blocks = (units * lanes + kThreads - 1) / kThreads;
-    const cudaError_t e = by_type(shape, [&](auto t, auto u) {
-        return launch_dependent(rope_fwd_kernel<decltype(t), decltype(u)::value>, dim3(static_cast<unsigned>(blocks)),
+    const cudaError_t e = by_type(shape, [&](auto t, auto u, auto inter) {
+        return launch_dependent(rope_fwd_kernel<decltype(t), decltype(u)::value, decltype(inter)::value>, dim3(static_cast<unsigned>(blocks)),
                                 dim3(kThreads), 0, reinterpret_cast<cudaStream_t>(stream), a, lanes);
     });
     return e == cudaSuccess ? SDM_OK : SDM_ERR_CUDA;
@@ -524,8 +518,8 @@ extern "C" sdm_status sdm_qk_norm_rope_backward(const sdm_rope_shape* shape, con
     const int lanes = head_lanes(shape->hd), blocks = bwd_blocks(shape);
     const size_t smem = static_cast<size_t>(kThreads / lanes) * shape->hd * sizeof(float);
     const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-    cudaError_t e = by_type(shape, [&](auto t, auto u) {
-        return launch_dependent(rope_bwd_kernel<decltype(t), decltype(u)::value>, dim3(static_cast<unsigned>(blocks)),
+    cudaError_t e = by_type(shape, [&](auto t, auto u, auto inter) {
+        return launch_dependent(rope_bwd_kernel<decltype(t), decltype(u)::value, decltype(inter)::value>, dim3(static_cast<unsigned>(blocks)),
                                 dim3(kThreads), smem, cs, a, lanes);
     });
     if (e == cudaSuccess && sums)

@@ -240,6 +240,42 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     return o;
 }
 
+// Four columns as two pairs of float32.
+struct Quad {
+    uint64_t lo, hi;
+};
+__device__ __forceinline__ Quad quad(const float (&v)[4]) { return {pack2(v[0], v[1]), pack2(v[2], v[3])}; }
+__device__ __forceinline__ Quad quad(float v) { return {pack2(v, v), pack2(v, v)}; }
+__device__ __forceinline__ void floats(const Quad& q, float (&v)[4]) {
+    unpack2(q.lo, v[0], v[1]);
+    unpack2(q.hi, v[2], v[3]);
+}
+__device__ __forceinline__ Quad fma4(const Quad& a, const Quad& b, const Quad& c) { return {fma2(a.lo, b.lo, c.lo), fma2(a.hi, b.hi, c.hi)}; }
+__device__ __forceinline__ Quad mul4(const Quad& a, const Quad& b) { return {mul2(a.lo, b.lo), mul2(a.hi, b.hi)}; }
+__device__ __forceinline__ Quad add4(const Quad& a, const Quad& b) { return {add2(a.lo, b.lo), add2(a.hi, b.hi)}; }
+template <typename T>
+__device__ __forceinline__ Quad quad(const Raw4<T>& r) {
+    float v[4];
+    r.get(v);
+    return quad(v);
+}
+__device__ __forceinline__ Raw4<float> load4(const float* p) {
+    Raw4<float> r;
+    r.ld(p);
+    return r;
+}
+__device__ __forceinline__ Quad quad_at(const float* p) {   // 16 bytes of shared memory
+    float v[4];
+    get4(p, v);
+    return quad(v);
+}
+template <typename T>
+__device__ __forceinline__ void st4(T* p, const Quad& q) {
+    float v[4];
+    floats(q, v);
+    st4(p, v);
+}
+
 // The blocks of a cluster: this one's rank, the barrier in its two halves (release / acquire of every thread's accesses;
 // relaxed: the arrival alone), and the address of another block's copy of a shared variable.
 __device__ __forceinline__ uint32_t cluster_rank() {
