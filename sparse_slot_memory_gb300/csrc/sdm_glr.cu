@@ -53,7 +53,8 @@ struct GlrArgs {
     int64_t x_ld, g_ld, y_ld, dy_ld, dx_ld, dg_ld;
     int P, D, H, gw;
     int tiles, tile_cols, tiles_per_head;
-    int cluster;              // blocks that walk a sequence together
+    int cluster;              // blocks that walk a span together
+    int64_t seg;              // rows of a segment (a multiple of SDM_GLR_CHUNK); 0: sequences are walked whole
 };
 
 // A tile's columns and this lane's place in it.
@@ -117,6 +118,84 @@ __device__ __forceinline__ float exp2_gate(float t) {
     float o;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(o) : "f"(t));
     return o;
+}
+
+// What a block (or cluster) walks: rows [b, b + n) of sequence p, segment k of `of`.
+struct Part {
+    int p, k, of;
+    int64_t b, n;
+    int64_t chunk;   // its first saved state
+};
+
+// Part number `id` of the launch. Without segments that is sequence id. With segments of L rows (the last of a sequence
+// takes the rest, L to 2 L - 1 rows) sequence p's parts have the numbers from offsets[p] / L + p on; numbers between
+// two sequences' name nothing (n < 0). Warp-wide; every block of a cluster finds the same.
+__device__ __forceinline__ Part part_of(const GlrArgs& a, int id) {
+    Part r;
+    const int lane = threadIdx.x & 31;
+    int64_t b, n;
+    r.k = 0;
+    r.of = 1;
+    if (a.seg == 0) {
+        r.p = id;
+    } else if (a.offsets == nullptr) {
+        r.of = static_cast<int>(max(a.len / a.seg, int64_t(1)));
+        r.p = id / r.of;
+        r.k = id - r.p * r.of;
+    } else {
+        // the last sequence whose first number is at most id: 32 probes a round
+        int lo = 0, hi = a.P;   // in [lo, hi)
+        while (hi - lo > 1) {
+            const int w = (hi - lo + 31) / 32, q = lo + (lane + 1) * w;
+            const bool le = q < hi && min(max(__ldg(a.offsets + q), int64_t(0)), a.rows) / a.seg + q <= id;
+            const int c = __popc(__ballot_sync(kFull, le));
+            lo += c * w;
+            hi = min(hi, lo + w);
+        }
+        r.p = lo;
+    }
+    if (r.p >= a.P) {
+        r.n = -1;
+        return r;
+    }
+    sequence(a, r.p, b, n);
+    if (a.seg != 0) {
+        if (a.offsets != nullptr) {
+            r.of = static_cast<int>(max(n / a.seg, int64_t(1)));
+            r.k = id - static_cast<int>(b / a.seg) - r.p;
+        }
+        if (r.k < 0 || r.k >= r.of) {
+            r.n = -1;
+            return r;
+        }
+    }
+    r.chunk = b / SDM_GLR_CHUNK + r.p + r.k * (a.seg / SDM_GLR_CHUNK);
+    r.b = b + r.k * a.seg;
+    r.n = r.k + 1 < r.of ? a.seg : n - r.k * a.seg;
+    return r;
+}
+
+// Between its passes a segmented walk keeps float32 values of a lane's columns in the first rows of the segment's own
+// output, which the last pass overwrites: value i in the rows from i * 4 / sizeof(T) on.
+template <typename T>
+__device__ __forceinline__ void keep(T* row, int64_t ld, int i, const Quad& q) {
+    if constexpr (sizeof(T) == 4) {
+        st4(row + i * ld, q);
+    } else {
+        *reinterpret_cast<uint64_t*>(row + 2 * i * ld) = q.lo;
+        *reinterpret_cast<uint64_t*>(row + (2 * i + 1) * ld) = q.hi;
+    }
+}
+template <typename T>
+__device__ __forceinline__ Quad kept(const T* row, int64_t ld, int i) {   // written by an earlier kernel
+    if constexpr (sizeof(T) == 4) {
+        float v[4];
+        ld4cg(row + i * ld, v);
+        return quad(v);
+    } else {
+        return {__ldcg(reinterpret_cast<const unsigned long long*>(row + 2 * i * ld)),
+                __ldcg(reinterpret_cast<const unsigned long long*>(row + (2 * i + 1) * ld))};
+    }
 }
 
 // The gates of one row as they lie in memory: the lane's four, or its head's one.
@@ -231,19 +310,23 @@ __global__ void __launch_bounds__(Split<ROWS>::kThreads, 2) glr_fwd_kernel(const
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     const int K = CLUSTER ? a.cluster : 1, rank = CLUSTER ? cluster_rank() : 0;
-    const int unit = blockIdx.x / K;
-    const int p = unit / a.tiles;
-    const Tile tl = tile_of<PERCH>(a, unit - p * a.tiles, lane);
-    int64_t b, n;
-    sequence(a, p, b, n);
+    const int unit = blockIdx.x / K, id = unit / a.tiles;
+    const Tile tl = tile_of<PERCH>(a, unit - id * a.tiles, lane);
+    const Part part = part_of(a, id);
+    if (part.n < 0) return;   // all of the cluster's blocks
+    const int p = part.p;
+    const int64_t b = part.b, n = part.n;
     Quad h = quad(0.f);   // the state before the step's rows
-    if (a.h0 != nullptr) h = quad(load4(a.h0 + static_cast<int64_t>(p) * a.D + tl.col));
+    if (part.k > 0)
+        h = kept(static_cast<const XT*>(a.y) + b * a.y_ld + tl.col, a.y_ld, 2);
+    else if (a.h0 != nullptr)
+        h = quad(load4(a.h0 + static_cast<int64_t>(p) * a.D + tl.col));
     const int64_t step = static_cast<int64_t>(K) * SDM_GLR_CHUNK;
     int64_t t = rank * SDM_GLR_CHUNK + w * ROWS;   // the warp's first row of the step
     const XT* x = static_cast<const XT*>(a.x) + (b + t) * a.x_ld;
     const GT* g = static_cast<const GT*>(a.g) + (b + t) * a.g_ld;
     XT* y = static_cast<XT*>(a.y) + (b + t) * a.y_ld + tl.col;
-    float* const st = a.states == nullptr ? nullptr : a.states + (b / SDM_GLR_CHUNK + p) * a.D + tl.col;
+    float* const st = a.states == nullptr ? nullptr : a.states + part.chunk * a.D + tl.col;
     if (CLUSTER) cluster_wait();   // every block of the cluster runs
     int buf = 0;
     for (int64_t t0 = 0; t0 < n; t0 += step, t += step, buf ^= 1) {
@@ -297,7 +380,8 @@ __global__ void __launch_bounds__(Split<ROWS>::kThreads, 2) glr_fwd_kernel(const
         }
         y += step * a.y_ld;
     }
-    if (a.hT != nullptr && rank == 0 && w == 0 && tl.on) st4(a.hT + static_cast<int64_t>(p) * a.D + tl.col, h);
+    if (a.hT != nullptr && part.k + 1 == part.of && rank == 0 && w == 0 && tl.on)
+        st4(a.hT + static_cast<int64_t>(p) * a.D + tl.col, h);
 }
 
 // The sum of v over the lanes of its head in the tile, in the head's first lane.
@@ -319,14 +403,18 @@ __global__ void __launch_bounds__(Split<ROWS>::kThreads, 2) glr_bwd_kernel(const
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     const int K = CLUSTER ? a.cluster : 1, rank = CLUSTER ? cluster_rank() : 0;
-    const int unit = blockIdx.x / K;
-    const int p = unit / a.tiles;
-    const Tile tl = tile_of<PERCH>(a, unit - p * a.tiles, lane);
-    int64_t b, n;
-    sequence(a, p, b, n);
+    const int unit = blockIdx.x / K, id = unit / a.tiles;
+    const Tile tl = tile_of<PERCH>(a, unit - id * a.tiles, lane);
+    const Part part = part_of(a, id);
+    if (part.n < 0) return;   // all of the cluster's blocks
+    const int p = part.p;
+    const int64_t b = part.b, n = part.n;
     Quad m = quad(0.f);   // the gradient of the state after the step's rows
-    if (a.dhT != nullptr) m = quad(load4(a.dhT + static_cast<int64_t>(p) * a.D + tl.col));
-    const float* const st = a.states + (b / SDM_GLR_CHUNK + p) * a.D + tl.col;
+    if (part.k + 1 < part.of)
+        m = kept(static_cast<const XT*>(a.dx) + b * a.dx_ld + tl.col, a.dx_ld, 2);
+    else if (a.dhT != nullptr)
+        m = quad(load4(a.dhT + static_cast<int64_t>(p) * a.D + tl.col));
+    const float* const st = a.states + part.chunk * a.D + tl.col;
     const int64_t step = static_cast<int64_t>(K) * SDM_GLR_CHUNK;
     if (CLUSTER) cluster_wait();
     int buf = 0;
@@ -416,7 +504,92 @@ __global__ void __launch_bounds__(Split<ROWS>::kThreads, 2) glr_bwd_kernel(const
             }
         }
     }
-    if (a.dh0 != nullptr && rank == 0 && w == 0 && tl.on) st4(a.dh0 + static_cast<int64_t>(p) * a.D + tl.col, m);
+    if (a.dh0 != nullptr && part.k == 0 && rank == 0 && w == 0 && tl.on)
+        st4(a.dh0 + static_cast<int64_t>(p) * a.D + tl.col, m);
+}
+
+// The segments' pairs, kept in their outputs' first rows: forward (A, B) of all but a sequence's last segment,
+// backward (A, R) of all but its first. A warp walks an eighth of the segment, and the first joins the eight.
+template <typename XT, typename GT, bool PERCH, bool REVERSE>
+__global__ void __launch_bounds__(256, 2) glr_pair_kernel(const GlrArgs a) {
+    __shared__ __align__(16) float sA[8][kTileCols], sB[8][kTileCols];
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    const int id = blockIdx.x / a.tiles;
+    const Tile tl = tile_of<PERCH>(a, blockIdx.x - id * a.tiles, lane);
+    const Part part = part_of(a, id);
+    if (part.n < 0 || (REVERSE ? part.k == 0 : part.k + 1 == part.of)) return;   // block-uniform
+    const int64_t each = (part.n + 63) / 64 * 8, t0 = w * each, n = min(each, part.n - t0);   // rows of the warp
+    const XT* const v = static_cast<const XT*>(REVERSE ? a.dy : a.x) + (part.b + t0) * (REVERSE ? a.dy_ld : a.x_ld) + tl.col;
+    const int64_t v_ld = REVERSE ? a.dy_ld : a.x_ld;
+    const GT* const g = static_cast<const GT*>(a.g) + (part.b + t0) * a.g_ld + tl.gate;
+    Quad A = quad(1.f), B = quad(0.f);
+    for (int64_t i0 = 0; i0 < n; i0 += 8) {
+        const int64_t t = REVERSE ? (n + 7) / 8 * 8 - 8 - i0 : i0;
+        const int live = live_rows(t, n, 8);
+        Raw4<XT> xr[8];
+        RawGate<GT, PERCH> gr[8];
+        load_rows(gr, g + t * a.g_ld, a.g_ld, live);
+        load_rows(xr, v + t * v_ld, v_ld, live);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int i = REVERSE ? 7 - j : j;
+            const Quad e = gr[i].exps();
+            A = mul4(A, e);
+            B = REVERSE ? mul4(e, add4(quad(xr[i]), B)) : fma4(e, B, quad(xr[i]));
+        }
+    }
+    st4(&sA[w][lane * 4], A);
+    st4(&sB[w][lane * 4], B);
+    __syncthreads();
+    if (w != 0 || !tl.on) return;
+    A = quad(1.f);
+    B = quad(0.f);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const int k = REVERSE ? 7 - j : j;
+        const Quad ak = quad_at(&sA[k][lane * 4]);
+        B = fma4(ak, B, quad_at(&sB[k][lane * 4]));
+        A = mul4(ak, A);
+    }
+    XT* const o = static_cast<XT*>(REVERSE ? a.dx : a.y) + part.b * (REVERSE ? a.dx_ld : a.y_ld) + tl.col;
+    keep(o, REVERSE ? a.dx_ld : a.y_ld, 0, A);
+    keep(o, REVERSE ? a.dx_ld : a.y_ld, 1, B);
+}
+
+// From the pairs, the state before (backward: the state's gradient behind) every segment, kept beside them. A thread
+// four channels of a sequence, kAhead segments' pairs on their way at once.
+template <typename XT, bool REVERSE>
+__global__ void __launch_bounds__(128) glr_chain_kernel(const GlrArgs a) {
+    constexpr int kAhead = 8;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const int quads = a.D / 4, blocks = (quads + 127) / 128, p = blockIdx.x / blocks;
+    const int q = (blockIdx.x - p * blocks) * 128 + threadIdx.x;
+    if (q >= quads) return;
+    int64_t b, n;
+    sequence(a, p, b, n);
+    const int of = static_cast<int>(max(n / a.seg, int64_t(1)));
+    const int64_t ld = REVERSE ? a.dx_ld : a.y_ld;
+    const float* const first = REVERSE ? a.dhT : a.h0;
+    XT* const o = static_cast<XT*>(REVERSE ? a.dx : a.y) + b * ld + q * 4;
+    auto segment = [&](int i) { return o + (REVERSE ? of - 1 - i : i) * a.seg * ld; };   // i-th in the walk's order
+    Quad h = quad(0.f);
+    if (first != nullptr) h = quad(load4(first + static_cast<int64_t>(p) * a.D + q * 4));
+    for (int i0 = 0; i0 + 1 < of; i0 += kAhead) {
+        Quad A[kAhead], B[kAhead];
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            if (i0 + i + 1 >= of) break;
+            A[i] = kept(segment(i0 + i), ld, 0);
+            B[i] = kept(segment(i0 + i), ld, 1);
+        }
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) {
+            if (i0 + i + 1 >= of) break;
+            h = fma4(A[i], h, B[i]);
+            keep(segment(i0 + i + 1), ld, 2, h);
+        }
+    }
 }
 
 // dg of a head wider than a tile: the sum of its tiles' parts, in tile order.
@@ -521,14 +694,22 @@ size_t part_bytes(const GlrArgs& a) {
     return a.tiles_per_head == 1 ? 0 : static_cast<size_t>(a.tiles_per_head) * a.rows * a.H * sizeof(float);
 }
 
-// Blocks that share a sequence's rows: enough of them that the SMs are full, and no more than the sequences have
-// steps of SDM_GLR_CHUNK rows.
-int cluster_of(const sdm_glr_shape* s, const GlrArgs& a) {
-    if (const char* e = getenv("GLR_K")) return atoi(e);
-    const int64_t units = static_cast<int64_t>(a.tiles) * a.P, steps = (a.len + SDM_GLR_CHUNK - 1) / SDM_GLR_CHUNK;
-    int k = 1;
-    while (k < kMaxCluster && units * k < 228 && k < steps) k *= 2;
-    return k;
+// How the rows are divided: `cluster` blocks walk a part together, and parts are whole sequences or segments of them.
+void divide(const sdm_glr_shape* s, GlrArgs* a) {
+    const int64_t units = static_cast<int64_t>(a->tiles) * a->P, steps = (a->len + SDM_GLR_CHUNK - 1) / SDM_GLR_CHUNK;
+    a->cluster = 1;
+    a->seg = 0;
+    int seg = 0;
+    if (const char* e = getenv("GLR_K")) a->cluster = atoi(e);
+    else while (a->cluster < kMaxCluster && units * a->cluster < 228 && a->cluster < steps) a->cluster *= 2;
+    if (const char* e = getenv("GLR_L")) seg = atoi(e);
+    a->seg = seg;
+}
+
+// Parts of the launch.
+int64_t parts_of(const GlrArgs& a) {
+    if (a.seg == 0) return a.P;
+    return a.offsets == nullptr ? a.P * std::max<int64_t>(a.len / a.seg, 1) : a.rows / a.seg + a.P;
 }
 
 // Calls f(x type, g type, per-channel gates) with the shape's types.
@@ -574,15 +755,24 @@ extern "C" sdm_status sdm_glr_forward(const sdm_glr_shape* shape, const void* x,
         if (!aligned16(p)) return SDM_ERR_ALIGN;
     GlrArgs a;
     geometry(shape, &a);
-    if (static_cast<int64_t>(a.tiles) * a.P > 0x7FFFFFFF / kMaxCluster) return SDM_ERR_SHAPE;
-    a.cluster = cluster_of(shape, a);
+    if (static_cast<int64_t>(a.tiles) * (a.P + a.rows / SDM_GLR_CHUNK) > 0x7FFFFFFF / kMaxCluster) return SDM_ERR_SHAPE;
+    divide(shape, &a);
     a.x = x; a.x_ld = x_ld; a.g = g; a.g_ld = g_ld; a.y = y; a.y_ld = y_ld;
     a.offsets = offsets; a.h0 = h0; a.hT = hT; a.states = states; a.status = status;
     const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
     const cudaError_t e = by_type(shape, [&](auto xt, auto gt, auto perch) {
         constexpr bool PC = decltype(perch)::value;
         constexpr int R = 8;
-        const dim3 grid(static_cast<unsigned>(a.tiles) * a.P * a.cluster), block(Split<R>::kThreads);
+        const unsigned units = static_cast<unsigned>(a.tiles * parts_of(a));
+        if (a.seg != 0) {
+            using X = decltype(xt);
+            cudaError_t e = launch_dependent(glr_pair_kernel<X, decltype(gt), PC, false>, dim3(units), dim3(256), 0, cs, a);
+            if (e == cudaSuccess)
+                e = launch_dependent(glr_chain_kernel<X, false>, dim3(static_cast<unsigned>(a.P) * ((a.D / 4 + 127) / 128)), dim3(128),
+                                     0, cs, a);
+            if (e != cudaSuccess) return e;
+        }
+        const dim3 grid(units * a.cluster), block(Split<R>::kThreads);
         if (a.cluster > 1)
             return launch_cluster(glr_fwd_kernel<decltype(xt), decltype(gt), PC, true, R>, grid, block, a.cluster, cs, a);
         return launch_dependent(glr_fwd_kernel<decltype(xt), decltype(gt), PC, false, R>, grid, block, 0, cs, a);
@@ -612,8 +802,8 @@ extern "C" sdm_status sdm_glr_backward(const sdm_glr_shape* shape, const void* x
         if (!aligned16(p)) return SDM_ERR_ALIGN;
     GlrArgs a;
     geometry(shape, &a);
-    if (static_cast<int64_t>(a.tiles) * a.P > 0x7FFFFFFF / kMaxCluster) return SDM_ERR_SHAPE;
-    a.cluster = cluster_of(shape, a);
+    if (static_cast<int64_t>(a.tiles) * (a.P + a.rows / SDM_GLR_CHUNK) > 0x7FFFFFFF / kMaxCluster) return SDM_ERR_SHAPE;
+    divide(shape, &a);
     if (part_bytes(a) > 0 && (ws == nullptr || !aligned16(ws) || ws_bytes < part_bytes(a))) return SDM_ERR_WORKSPACE;
     a.x = x; a.x_ld = x_ld; a.g = g; a.g_ld = g_ld; a.dy = dy; a.dy_ld = dy_ld;
     a.dx = dx; a.dx_ld = dx_ld; a.dg = dg; a.dg_ld = dg_ld;
@@ -623,7 +813,16 @@ extern "C" sdm_status sdm_glr_backward(const sdm_glr_shape* shape, const void* x
     cudaError_t e = by_type(shape, [&](auto xt, auto gt, auto perch) {
         constexpr bool PC = decltype(perch)::value;
         constexpr int R = 8;
-        const dim3 grid(static_cast<unsigned>(a.tiles) * a.P * a.cluster), block(Split<R>::kThreads);
+        const unsigned units = static_cast<unsigned>(a.tiles * parts_of(a));
+        if (a.seg != 0) {
+            using X = decltype(xt);
+            cudaError_t e = launch_dependent(glr_pair_kernel<X, decltype(gt), PC, true>, dim3(units), dim3(256), 0, cs, a);
+            if (e == cudaSuccess)
+                e = launch_dependent(glr_chain_kernel<X, true>, dim3(static_cast<unsigned>(a.P) * ((a.D / 4 + 127) / 128)), dim3(128),
+                                     0, cs, a);
+            if (e != cudaSuccess) return e;
+        }
+        const dim3 grid(units * a.cluster), block(Split<R>::kThreads);
         if (a.cluster > 1)
             return launch_cluster(glr_bwd_kernel<decltype(xt), decltype(gt), PC, true, R>, grid, block, a.cluster, cs, a);
         return launch_dependent(glr_bwd_kernel<decltype(xt), decltype(gt), PC, false, R>, grid, block, 0, cs, a);

@@ -28,6 +28,7 @@ namespace {
 using namespace rows;
 
 constexpr int kThreads = 256;
+constexpr int kFwdBlocks = 3;      // blocks of the forward on an SM
 constexpr int kMaxHd = 1024;
 constexpr int kMaxFreq = kMaxHd / 2;
 constexpr int kPartBlocks = 304;   // blocks of the backward at most (two for each of 152 SMs): a row of weight gradients each
@@ -115,12 +116,24 @@ __device__ __forceinline__ Turn turn_of(const RopeArgs& s, int pos, int f) {
 __device__ __forceinline__ Quad negative(const Quad& q) {
     return {q.lo ^ 0x8000000080000000ull, q.hi ^ 0x8000000080000000ull};
 }
-// Pairs turned by the angle (back: by its opposite); those behind rot_dim stay as they are, whatever they hold.
-template <bool BACK>
-__device__ __forceinline__ Pairs turned(const Pairs& p, const Turn& t, bool on) {
-    if (!on) return p;
-    const Quad n = negative(t.s);
-    return {fma4(p.a, t.c, mul4(p.b, BACK ? t.s : n)), fma4(p.b, t.c, mul4(p.a, BACK ? n : t.s))};
+// The gradient's pairs turned back by the angle; those behind rot_dim (cosine 1, sine 0) stay as they are, whatever they
+// hold: `all` says that there are none.
+__device__ __forceinline__ Pairs turned_back(const Pairs& p, const Turn& t, bool all, bool on) {
+    Pairs o = {fma4(p.a, t.c, mul4(p.b, t.s)), fma4(p.b, t.c, mul4(p.a, negative(t.s)))};
+    if (!all && !on) o = p;
+    return o;
+}
+// The forward's rotation with the weights in it: a' = a (wa c) - b (wb s), b' = b (wb c) + a (wa s)
+struct Weighted {
+    Quad ca, sb, cb, sa;
+};
+__device__ __forceinline__ Weighted weighted(const Turn& t, const Pairs& w) {
+    return {mul4(w.a, t.c), negative(mul4(w.b, t.s)), mul4(w.b, t.c), mul4(w.a, t.s)};
+}
+__device__ __forceinline__ Pairs turned(const Pairs& p, const Weighted& t, bool all, bool on) {
+    Pairs o = {fma4(p.a, t.ca, mul4(p.b, t.sb)), fma4(p.b, t.cb, mul4(p.a, t.sa))};
+    if (!all && !on) o = {mul4(p.a, t.ca), mul4(p.b, t.cb)};
+    return o;
 }
 
 template <bool INTER>
@@ -158,69 +171,98 @@ constexpr int heads_at_once() {
 }
 
 // The token's position, or -1 for a padding token.
-__device__ __forceinline__ int position(const RopeArgs& s, int t, bool live) {
+__device__ __forceinline__ int position(const RopeArgs& s, int t) {
     const int pos = __ldg(s.pos + t);
     if (pos < s.max_pos) return pos < 0 ? -1 : pos;
-    if (live && s.status != nullptr) atomicOr(s.status, SDM_DEV_BAD_POSITION);
+    if (s.status != nullptr) atomicOr(s.status, SDM_DEV_BAD_POSITION);
     return -1;
 }
 
-// One group of `lanes` lanes takes up to HU heads of one kind of one token.
+// A group's walk over units of up to HU heads of a token: unit u is token u / chunks, chunk u % chunks, and the
+// next is a fixed number of units on, so that no step divides.
+struct Walk {
+    int u, t, ch, dt, dch, du;
+    __device__ __forceinline__ Walk(int first, int step, int chunks) : u(first), t(first / chunks), ch(first % chunks), dt(step / chunks), dch(step % chunks), du(step) {}
+    __device__ __forceinline__ void next(int chunks) {
+        u += du;
+        t += dt;
+        ch += dch;
+        if (ch >= chunks) {
+            ch -= chunks;
+            ++t;
+        }
+    }
+};
+
+// Groups of `lanes` lanes walk the tokens' heads, up to HU heads of one kind of one token at a time.
 template <typename T, int U, bool INTER>
-__global__ void __launch_bounds__(kThreads) rope_fwd_kernel(const RopeArgs s, int lanes) {
+__global__ void __launch_bounds__(kThreads, U == 1 ? kFwdBlocks : 1) rope_fwd_kernel(const RopeArgs s, int lanes) {
     constexpr int HU = heads_at_once<T, U>();
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int per = kThreads / lanes, cq = (s.Hq + HU - 1) / HU, ct = cq + (s.Hk + HU - 1) / HU;
-    const int units = static_cast<int>(s.tokens) * ct, unit = static_cast<int>(blockIdx.x) * per + threadIdx.x / lanes;
-    const bool live = unit < units;
-    const int t = live ? unit / ct : 0, ch = live ? unit - t * ct : 0;
-    const bool isq = ch < cq;
-    const int h0 = (isq ? ch : ch - cq) * HU, H = live ? (isq ? s.Hq : s.Hk) - h0 : 0;   // heads from h0 on
+    const int units = static_cast<int>(s.tokens) * ct, sub = threadIdx.x % lanes;
+    const float inv = 1.f / s.hd;
     Place<U> pl;
-    pl.set(s, threadIdx.x % lanes, lanes);
-    const T* const x = (isq ? static_cast<const T*>(s.q) + t * s.q_ld : static_cast<const T*>(s.k) + t * s.k_ld) + h0 * s.hd;
-    T* const y = (isq ? static_cast<T*>(s.qo) + t * s.qo_ld : static_cast<T*>(s.ko) + t * s.ko_ld) + h0 * s.hd;
-    Raw4<T> ra[HU][U], rb[HU][U];
+    pl.set(s, sub, lanes);
+    Walk at(blockIdx.x * per + threadIdx.x / lanes, gridDim.x * per, ct);
+    int pos = at.u < units ? position(s, at.t) : -1;
+    for (int u0 = blockIdx.x * per; u0 < units; u0 += gridDim.x * per) {   // block-uniform
+        const bool live = at.u < units, isq = at.ch < cq && s.Hq > 0;
+        const int t = live ? at.t : 0, h0 = live ? (isq ? at.ch : at.ch - cq) * HU : 0;
+        const int n = live ? min(HU, (isq ? s.Hq : s.Hk) - h0) : 0;
+        const T* const x = (isq ? static_cast<const T*>(s.q) + t * s.q_ld : static_cast<const T*>(s.k) + t * s.k_ld) + h0 * s.hd;
+        T* const y = (isq ? static_cast<T*>(s.qo) + t * s.qo_ld : static_cast<T*>(s.ko) + t * s.ko_ld) + h0 * s.hd;
+        const int p = pos;
+        auto body = [&](auto full) {   // full: HU heads of a real token, every column turns
+            constexpr bool FULL = decltype(full)::value;
+            Raw4<T> ra[HU][U], rb[HU][U];
 #pragma unroll
-    for (int h = 0; h < HU; ++h)
+            for (int h = 0; h < HU; ++h)
 #pragma unroll
-        for (int i = 0; i < U; ++i) {
-            ra[h][i].zero();
-            rb[h][i].zero();
-            if (h < H) {
-                ra[h][i].ld_cg(x + h * s.hd + pl.a[i]);
-                rb[h][i].ld_cg(x + h * s.hd + pl.b[i]);
+                for (int i = 0; i < U; ++i) {
+                    if (!FULL) {
+                        ra[h][i].zero();
+                        rb[h][i].zero();
+                    }
+                    if (FULL || (h < n && p >= 0)) {
+                        ra[h][i].ld_cg(x + h * s.hd + pl.a[i]);
+                        rb[h][i].ld_cg(x + h * s.hd + pl.b[i]);
+                    }
+                }
+            Weighted wt[U];
+#pragma unroll
+            for (int i = 0; i < U; ++i)
+                wt[i] = weighted(turn_of(s, max(p, 0), pl.f[i]),
+                                 weights<INTER>(s.norm ? (isq ? s.wq : s.wk) : nullptr, pl.a[i], pl.b[i]));
+            at.next(ct);
+            pos = at.u < units ? position(s, at.t) : -1;
+            float ss[HU];
+#pragma unroll
+            for (int h = 0; h < HU; ++h) {
+                ss[h] = 0.f;
+#pragma unroll
+                for (int i = 0; i < U; ++i) {
+                    const Pairs v = pairs<INTER>(ra[h][i], rb[h][i]);
+                    const float d = dot(v, v);
+                    if (pl.on[i]) ss[h] += d;
+                }
             }
-        }
-    const int pos = position(s, t, live);
-    Turn turn[U];
-    Pairs wt[U];
+            if (s.norm) lanes_sum(ss, lanes);
 #pragma unroll
-    for (int i = 0; i < U; ++i) {
-        turn[i] = turn_of(s, max(pos, 0), pl.f[i]);
-        wt[i] = weights<INTER>(s.norm ? (isq ? s.wq : s.wk) : nullptr, pl.a[i], pl.b[i]);
-    }
-    float ss[HU];
+            for (int h = 0; h < HU; ++h) {
+                float r = s.norm ? rsqrtf(fmaf(ss[h], inv, s.eps)) : 1.f;
+                if (!FULL && p < 0) r = 0.f;   // a padding token, not read: zeros
 #pragma unroll
-    for (int h = 0; h < HU; ++h) {
-        ss[h] = 0.f;
-#pragma unroll
-        for (int i = 0; i < U; ++i) {
-            const Pairs x = pairs<INTER>(ra[h][i], rb[h][i]);
-            if (pl.on[i]) ss[h] += dot(x, x);
-        }
-    }
-    if (s.norm) lanes_sum(ss, lanes);
-#pragma unroll
-    for (int h = 0; h < HU; ++h) {
-        const float r = s.norm ? rsqrtf(ss[h] / s.hd + s.eps) : 1.f;
-#pragma unroll
-        for (int i = 0; i < U; ++i) {
-            Pairs n = pairs<INTER>(ra[h][i], rb[h][i]);
-            n = turned<false>(times(times(n, r), wt[i]), turn[i], pl.f[i] >= 0);
-            if (pos < 0) n = {quad(0.f), quad(0.f)};   // a padding token's outputs are 0 whatever it holds
-            if (h < H && pl.on[i]) st_pairs<INTER>(y + h * s.hd + pl.a[i], y + h * s.hd + pl.b[i], n);
-        }
+                for (int i = 0; i < U; ++i) {
+                    const Pairs o = times(turned(pairs<INTER>(ra[h][i], rb[h][i]), wt[i], FULL, pl.f[i] >= 0), r);
+                    if ((FULL || h < n) && pl.on[i]) st_pairs<INTER>(y + h * s.hd + pl.a[i], y + h * s.hd + pl.b[i], o);
+                }
+            }
+        };
+        if (__all_sync(kFull, n == HU && p >= 0 && s.rd == s.hd))
+            body(std::true_type{});
+        else
+            body(std::false_type{});
     }
 }
 
@@ -232,12 +274,12 @@ __global__ void __launch_bounds__(kThreads, U == 1 ? 2 : 1) rope_bwd_kernel(cons
     constexpr int HU = heads_at_once<T, U>();
     extern __shared__ float sm[];   // [groups][hd]
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const int per = kThreads / lanes, group = threadIdx.x / lanes;
+    const int per = kThreads / lanes, group = threadIdx.x / lanes, sub = threadIdx.x % lanes;
     const float inv = 1.f / s.hd;
     Place<U> pl;
-    pl.set(s, threadIdx.x % lanes, lanes);
+    pl.set(s, sub, lanes);
     for (int side = 0; side < 2; ++side) {
-        const int H = side ? s.Hk : s.Hq, chunks = (H + HU - 1) / HU;
+        const int H = side ? s.Hk : s.Hq, chunks = max(1, (H + HU - 1) / HU);
         const T* const X = static_cast<const T*>(side ? s.k : s.q);
         const T* const G = static_cast<const T*>(side ? s.dko : s.dqo);
         T* const Y = static_cast<T*>(side ? s.ko : s.qo);
@@ -248,63 +290,85 @@ __global__ void __launch_bounds__(kThreads, U == 1 ? 2 : 1) rope_bwd_kernel(cons
             wt[i] = weights<INTER>(s.norm ? (side ? s.wk : s.wq) : nullptr, pl.a[i], pl.b[i]);
             dw[i] = {quad(0.f), quad(0.f)};
         }
-        const int units = static_cast<int>(s.tokens) * chunks;
+        const int units = H == 0 ? 0 : static_cast<int>(s.tokens) * chunks;
+        Walk at(blockIdx.x * per + group, gridDim.x * per, chunks);
+        int pos = at.u < units ? position(s, at.t) : -1;
         for (int u0 = blockIdx.x * per; u0 < units; u0 += gridDim.x * per) {   // block-uniform
-            const int u = u0 + group;
-            const bool live = u < units;
-            const int t = live ? u / chunks : 0, h0 = live ? (u - t * chunks) * HU : 0, n = live ? H - h0 : 0;
+            const bool live = at.u < units;
+            const int t = live ? at.t : 0, h0 = live ? at.ch * HU : 0, n = live ? min(HU, H - h0) : 0;
             const T* const x = X + t * x_ld + h0 * s.hd;
             const T* const g = G + t * g_ld + h0 * s.hd;
-            Raw4<T> ra[HU][U], rb[HU][U], ga[HU][U], gb[HU][U];
+            T* const y = Y + t * y_ld + h0 * s.hd;
+            const int p = pos;
+            auto body = [&](auto full) {   // full: HU heads of a real token, every column turns
+                constexpr bool FULL = decltype(full)::value;
+                Raw4<T> ra[HU][U], rb[HU][U], ga[HU][U], gb[HU][U];
 #pragma unroll
-            for (int h = 0; h < HU; ++h)
+                for (int h = 0; h < HU; ++h)
 #pragma unroll
-                for (int i = 0; i < U; ++i) {
-                    ra[h][i].zero();
-                    rb[h][i].zero();
-                    ga[h][i].zero();
-                    gb[h][i].zero();
-                    if (h < n && pl.on[i]) {
-                        ra[h][i].ld_cg(x + h * s.hd + pl.a[i]);
-                        rb[h][i].ld_cg(x + h * s.hd + pl.b[i]);
-                        ga[h][i].ld_cg(g + h * s.hd + pl.a[i]);
-                        gb[h][i].ld_cg(g + h * s.hd + pl.b[i]);
+                    for (int i = 0; i < U; ++i) {
+                        if (!FULL) {
+                            ra[h][i].zero();
+                            rb[h][i].zero();
+                            ga[h][i].zero();
+                            gb[h][i].zero();
+                        }
+                        if (FULL || (h < n && p >= 0)) {
+                            ra[h][i].ld_cg(x + h * s.hd + pl.a[i]);
+                            rb[h][i].ld_cg(x + h * s.hd + pl.b[i]);
+                            ga[h][i].ld_cg(g + h * s.hd + pl.a[i]);
+                            gb[h][i].ld_cg(g + h * s.hd + pl.b[i]);
+                        }
+                    }
+                Turn turn[U];
+#pragma unroll
+                for (int i = 0; i < U; ++i) turn[i] = turn_of(s, max(p, 0), pl.f[i]);
+                at.next(chunks);
+                pos = at.u < units ? position(s, at.t) : -1;
+                float sums[2 * HU];
+#pragma unroll
+                for (int h = 0; h < HU; ++h) {
+                    sums[2 * h] = sums[2 * h + 1] = 0.f;
+#pragma unroll
+                    for (int i = 0; i < U; ++i) {
+                        const Pairs v = pairs<INTER>(ra[h][i], rb[h][i]);
+                        const Pairs e = turned_back(pairs<INTER>(ga[h][i], gb[h][i]), turn[i], FULL, pl.f[i] >= 0);
+                        const float vv = dot(v, v), ev = dot(times(e, wt[i]), v);
+                        if (pl.on[i]) {
+                            sums[2 * h] += vv;
+                            sums[2 * h + 1] += ev;
+                        }
                     }
                 }
-            const int pos = position(s, t, live);
-            Turn turn[U];
-            float sums[2 * HU];
+                if (s.norm) lanes_sum(sums, lanes);
 #pragma unroll
-            for (int i = 0; i < U; ++i) turn[i] = turn_of(s, max(pos, 0), pl.f[i]);
+                for (int h = 0; h < HU; ++h) {
+                    // dx = r (t + k x); a padding token or a head past the last was not read, r = 0 leaves zeros
+                    float r = 1.f, k = 0.f;
+                    if (s.norm) {
+                        r = rsqrtf(fmaf(sums[2 * h], inv, s.eps));
+                        k = -sums[2 * h + 1] * inv * r * r;
+                    }
+                    if (!FULL && (p < 0 || h >= n)) r = k = 0.f;
 #pragma unroll
-            for (int h = 0; h < HU; ++h) {
-                sums[2 * h] = sums[2 * h + 1] = 0.f;
-#pragma unroll
-                for (int i = 0; i < U; ++i) {
-                    const Pairs x = pairs<INTER>(ra[h][i], rb[h][i]);
-                    const Pairs e = turned<true>(pairs<INTER>(ga[h][i], gb[h][i]), turn[i], pl.f[i] >= 0);
-                    sums[2 * h] += dot(x, x);
-                    sums[2 * h + 1] += dot(times(e, wt[i]), x);
+                    for (int i = 0; i < U; ++i) {
+                        const Pairs v = pairs<INTER>(ra[h][i], rb[h][i]);
+                        const Pairs e = times(turned_back(pairs<INTER>(ga[h][i], gb[h][i]), turn[i], FULL, pl.f[i] >= 0), r);
+                        dw[i] = {fma4(e.a, v.a, dw[i].a), fma4(e.b, v.b, dw[i].b)};
+                        Pairs d = e;
+                        if (s.norm) {
+                            const Quad kr = quad(k * r);
+                            d = times(e, wt[i]);
+                            d = {fma4(v.a, kr, d.a), fma4(v.b, kr, d.b)};
+                        }
+                        if ((FULL || h < n) && pl.on[i]) st_pairs<INTER>(y + h * s.hd + pl.a[i], y + h * s.hd + pl.b[i], d);
+                    }
                 }
-            }
-            if (s.norm) lanes_sum(sums, lanes);
-#pragma unroll
-            for (int h = 0; h < HU; ++h) {
-                const float r = s.norm ? rsqrtf(sums[2 * h] * inv + s.eps) : 1.f;
-                const float k = s.norm ? -sums[2 * h + 1] * inv * r * r * r : 0.f;   // dx = r t + k x
-#pragma unroll
-                for (int i = 0; i < U; ++i) {
-                    const Pairs x = pairs<INTER>(ra[h][i], rb[h][i]);
-                    const Pairs e = times(turned<true>(pairs<INTER>(ga[h][i], gb[h][i]), turn[i], pl.f[i] >= 0), r);
-                    if (pos >= 0 && h < n) dw[i] = {fma4(e.a, x.a, dw[i].a), fma4(e.b, x.b, dw[i].b)};
-                    const Quad k4 = quad(k);
-                    Pairs d = s.norm ? times(e, wt[i]) : e;
-                    if (s.norm) d = {fma4(x.a, k4, d.a), fma4(x.b, k4, d.b)};
-                    if (pos < 0) d = {quad(0.f), quad(0.f)};
-                    T* const y = Y + t * y_ld + (h0 + h) * s.hd;
-                    if (h < n && pl.on[i]) st_pairs<INTER>(y + pl.a[i], y + pl.b[i], d);
-                }
-            }
+            };
+            if (__all_sync(kFull, n == HU && p >= 0 && s.rd == s.hd))
+                body(std::true_type{});
+            else
+                body(std::false_type{});
         }
         if (s.part == nullptr) continue;
 #pragma unroll
@@ -481,7 +545,7 @@ extern "C" sdm_status sdm_qk_norm_rope(const sdm_rope_shape* shape, const void* 
     const int lanes = head_lanes(shape->hd);
     const int hu = heads_together(shape);
     const int64_t units = shape->tokens * ((a.Hq + hu - 1) / hu + (a.Hk + hu - 1) / hu);
-    const int64_t blocks = (units * lanes + kThreads - 1) / kThreads;
+    const int64_t blocks = std::min<int64_t>((units * lanes + kThreads - 1) / kThreads, 152 * kFwdBlocks);
     const cudaError_t e = by_type(shape, [&](auto t, auto u, auto inter) {
         return launch_dependent(rope_fwd_kernel<decltype(t), decltype(u)::value, decltype(inter)::value>, dim3(static_cast<unsigned>(blocks)),
                                 dim3(kThreads), 0, reinterpret_cast<cudaStream_t>(stream), a, lanes);

@@ -98,6 +98,15 @@ def test_zero_rows_have_finite_results():
     assert bool((r["q_out"] == 0).all()) and bool(torch.isfinite(r["dq"]).all())
 
 
+def test_rotation_alone_does_not_look_at_the_inputs_in_its_backward():
+    c = case(30, 3, 1, 64, 48, norm=False)
+    want = run(c)
+    c["q"][5, 1, 3], c["k"][9] = float("nan"), float("inf")
+    r = run(c)
+    assert torch.equal(r["dq"], want["dq"]) and torch.equal(r["dk"], want["dk"])
+    assert bool(torch.isnan(r["q_out"][5, 1]).any()) and torch.equal(r["q_out"][5, 2], want["q_out"][5, 2])
+
+
 def test_in_place_and_repeated_calls():
     c = case(70, 8, 2, 128, 64, dtype="bf16", pad=8)
     s, want = c["spec"], run(c)
