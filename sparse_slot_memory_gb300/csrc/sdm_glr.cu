@@ -62,6 +62,7 @@ struct Tile {
     int col0, n;  // the tile's first channel and its channels
     int col;      // the lane's first channel
     bool on;      // whether the lane has channels
+    bool full;    // whether every lane has
     int gate;     // the lane's gate (head)
     int seg;      // lanes from this one to the end of its head's part in the tile
     int sub;      // which of its head's tiles this is
@@ -85,6 +86,7 @@ __device__ __forceinline__ Tile tile_of(const GlrArgs& a, int tile, int lane) {
     t.col0 = c0;
     t.n = n;
     t.on = lane * 4 < n;
+    t.full = n == kTileCols;
     t.col = c0 + (t.on ? lane * 4 : 0);
     if (PERCH) {
         t.gate = t.col;
@@ -306,6 +308,7 @@ __global__ void __launch_bounds__(Split<ROWS>::kThreads, 2) glr_fwd_kernel(const
     constexpr int kWarps = Split<ROWS>::kWarps;
     __shared__ __align__(16) float sA[2][kWarps][kTileCols], sB[2][kWarps][kTileCols];
     __shared__ __align__(16) float cA[2][CLUSTER ? kMaxCluster : 1][kTileCols], cB[2][CLUSTER ? kMaxCluster : 1][kTileCols];
+    __shared__ __align__(16) float carry[2][kTileCols];
     if (CLUSTER) cluster_arrive_relaxed();
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
@@ -327,19 +330,32 @@ __global__ void __launch_bounds__(Split<ROWS>::kThreads, 2) glr_fwd_kernel(const
     const GT* g = static_cast<const GT*>(a.g) + (b + t) * a.g_ld;
     XT* y = static_cast<XT*>(a.y) + (b + t) * a.y_ld + tl.col;
     float* const st = a.states == nullptr ? nullptr : a.states + part.chunk * a.D + tl.col;
+    // bfloat16 rows: the next step's are loaded into registers over this one; float32 rows: asked for in the L2
+    constexpr bool AHEAD = sizeof(XT) == 2;
+    Raw4<XT> xr[ROWS], xn[AHEAD ? ROWS : 1];
+    RawGate<GT, PERCH> gr[ROWS], gn[AHEAD ? ROWS : 1];
+    int live = live_rows(t, n, ROWS);
+    if (AHEAD) {
+        load_rows(gr, g + tl.gate, a.g_ld, live);
+        load_rows(xr, x + tl.col, a.x_ld, live);
+    }
     if (CLUSTER) cluster_wait();   // every block of the cluster runs
     int buf = 0;
     for (int64_t t0 = 0; t0 < n; t0 += step, t += step, buf ^= 1) {
-        const int live = live_rows(t, n, ROWS);
-        Raw4<XT> xr[ROWS];
-        RawGate<GT, PERCH> gr[ROWS];
-        load_rows(gr, g + tl.gate, a.g_ld, live);
-        load_rows(xr, x + tl.col, a.x_ld, live);
+        const int more = live_rows(t + step, n, ROWS);
+        if (!AHEAD) {
+            load_rows(gr, g + tl.gate, a.g_ld, live);
+            load_rows(xr, x + tl.col, a.x_ld, live);
+        }
         x += step * a.x_ld;
         g += step * a.g_ld;
-        const int more = live_rows(t + step, n, ROWS);
-        prefetch_rows<ROWS>(x + tl.col0, a.x_ld, more, tl.n, lane);
-        if (PERCH) prefetch_rows<ROWS>(g + tl.col0, a.g_ld, more, tl.n, lane);
+        if constexpr (AHEAD) {
+            load_rows(gn, g + tl.gate, a.g_ld, more);
+            load_rows(xn, x + tl.col, a.x_ld, more);
+        } else {
+            prefetch_rows<ROWS>(x + tl.col0, a.x_ld, more, tl.n, lane);
+            if (PERCH) prefetch_rows<ROWS>(g + tl.col0, a.g_ld, more, tl.n, lane);
+        }
         Quad A = quad(1.f), B = quad(0.f);
 #pragma unroll
         for (int i = 0; i < ROWS; ++i) {
@@ -364,23 +380,46 @@ __global__ void __launch_bounds__(Split<ROWS>::kThreads, 2) glr_fwd_kernel(const
                 join(h, &cA[buf][k][lane * 4], &cB[buf][k][lane * 4]);
             }
             if (st != nullptr && w == 0 && tl.on && t < n) st4(st + t / SDM_GLR_CHUNK * a.D, hw);
-            for (int j = 0; j < w; ++j) join(hw, &sA[buf][j][lane * 4], &sB[buf][j][lane * 4]);
         } else {
-            if (st != nullptr && w == 0 && tl.on) st4(st + t0 / SDM_GLR_CHUNK * a.D, h);
+            // the state behind the step before: that step's last warp left it in the shared memory
+            if (t0 > 0) hw = quad_at(&carry[buf][lane * 4]);
+            if (st != nullptr && w == 0 && tl.on) st4(st + t0 / SDM_GLR_CHUNK * a.D, hw);
+        }
+        for (int j = 0; j < w; ++j) join(hw, &sA[buf][j][lane * 4], &sB[buf][j][lane * 4]);
+        if (!CLUSTER && w == kWarps - 1) {
+            h = hw;
+            join(h, &sA[buf][w][lane * 4], &sB[buf][w][lane * 4]);
+            st4(&carry[buf ^ 1][lane * 4], h);
+        }
+        if (AHEAD && PERCH) {
+            forget(gr);
+            forget(xr);
+        }
+        if (live == ROWS && tl.full) {
 #pragma unroll
-            for (int j = 0; j < kWarps; ++j) {
-                if (j == w) hw = h;
-                join(h, &sA[buf][j][lane * 4], &sB[buf][j][lane * 4]);
+            for (int i = 0; i < ROWS; ++i) {
+                hw = fma4(gr[i].exps(), hw, quad(xr[i]));
+                st4(y + i * a.y_ld, hw);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < ROWS; ++i) {
+                hw = fma4(gr[i].exps(), hw, quad(xr[i]));
+                if (tl.on && i < live) st4(y + i * a.y_ld, hw);
             }
         }
-#pragma unroll
-        for (int i = 0; i < ROWS; ++i) {
-            hw = fma4(gr[i].exps(), hw, quad(xr[i]));
-            if (tl.on && i < live) st4(y + i * a.y_ld, hw);
-        }
         y += step * a.y_ld;
+        live = more;
+        if constexpr (AHEAD) {
+#pragma unroll
+            for (int i = 0; i < ROWS; ++i) {
+                gr[i] = gn[i];
+                xr[i] = xn[i];
+            }
+        }
     }
-    if (a.hT != nullptr && part.k + 1 == part.of && rank == 0 && w == 0 && tl.on)
+    // every thread of a cluster holds the state at the end; of a lone block, the last warp
+    if (a.hT != nullptr && part.k + 1 == part.of && tl.on && (CLUSTER ? rank == 0 && w == 0 : w == kWarps - 1))
         st4(a.hT + static_cast<int64_t>(p) * a.D + tl.col, h);
 }
 
@@ -399,6 +438,7 @@ __global__ void __launch_bounds__(Split<ROWS>::kThreads, 2) glr_bwd_kernel(const
     constexpr int kWarps = Split<ROWS>::kWarps;
     __shared__ __align__(16) float sA[2][kWarps][kTileCols], sF[2][kWarps][kTileCols], sR[2][kWarps][kTileCols];
     __shared__ __align__(16) float cA[2][CLUSTER ? kMaxCluster : 1][kTileCols], cR[2][CLUSTER ? kMaxCluster : 1][kTileCols];
+    __shared__ __align__(16) float carry[2][kTileCols];
     if (CLUSTER) cluster_arrive_relaxed();
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
@@ -418,6 +458,7 @@ __global__ void __launch_bounds__(Split<ROWS>::kThreads, 2) glr_bwd_kernel(const
     const int64_t step = static_cast<int64_t>(K) * SDM_GLR_CHUNK;
     if (CLUSTER) cluster_wait();
     int buf = 0;
+    bool first = true;
     for (int64_t t0 = (n + step - 1) / step * step - step; t0 >= 0; t0 -= step, buf ^= 1) {
         const int64_t tc = t0 + rank * SDM_GLR_CHUNK, t = tc + w * ROWS;
         const int live = live_rows(t, n, ROWS);
@@ -465,18 +506,21 @@ __global__ void __launch_bounds__(Split<ROWS>::kThreads, 2) glr_bwd_kernel(const
                 if (k == rank) mw = m;
                 join(m, &cA[buf][k][lane * 4], &cR[buf][k][lane * 4]);
             }
-            for (int j = kWarps - 1; j > w; --j) join(mw, &sA[buf][j][lane * 4], &sR[buf][j][lane * 4]);
         } else {
             for (int j = 0; j < w; ++j) join(h, &sA[buf][j][lane * 4], &sF[buf][j][lane * 4]);
-#pragma unroll
-            for (int j = kWarps - 1; j >= 0; --j) {
-                if (j == w) mw = m;
-                join(m, &sA[buf][j][lane * 4], &sR[buf][j][lane * 4]);
-            }
+            if (!first) mw = quad_at(&carry[buf][lane * 4]);
         }
+        for (int j = kWarps - 1; j > w; --j) join(mw, &sA[buf][j][lane * 4], &sR[buf][j][lane * 4]);
+        if (!CLUSTER && w == 0) {
+            m = mw;
+            join(m, &sA[buf][0][lane * 4], &sR[buf][0][lane * 4]);
+            st4(&carry[buf ^ 1][lane * 4], m);
+        }
+        first = false;
         forget(gr);
         forget(xr);
         forget(dr);
+        const bool all = live == ROWS && tl.full;   // warp-uniform
         Quad hp[ROWS];   // the state before each row
 #pragma unroll
         for (int i = 0; i < ROWS; ++i) {
@@ -488,9 +532,9 @@ __global__ void __launch_bounds__(Split<ROWS>::kThreads, 2) glr_bwd_kernel(const
             const Quad l = add4(quad(dr[i]), mw);
             mw = mul4(gr[i].exps(), l);
             const Quad q = mul4(mw, hp[i]);
-            if (tl.on && i < live) st4(dx + i * a.dx_ld, l);
+            if (all || (tl.on && i < live)) st4(dx + i * a.dx_ld, l);
             if constexpr (PERCH) {
-                if (tl.on && i < live) st4(dg + i * a.dg_ld, q);
+                if (all || (tl.on && i < live)) st4(dg + i * a.dg_ld, q);
             } else {
                 float d[4];
                 floats(q, d);
