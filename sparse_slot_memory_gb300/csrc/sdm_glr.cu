@@ -140,6 +140,16 @@ __device__ __forceinline__ Part part_of(const GlrArgs& a, int id) {
     r.of = 1;
     if (a.seg == 0) {
         r.p = id;
+        if (a.offsets != nullptr && a.P <= 32 && a.P > 1) {
+            // the longest sequences first: lane p counts those before sequence p
+            const int64_t mine = lane < a.P ? __ldg(a.offsets + lane + 1) - __ldg(a.offsets + lane) : -1;
+            int before = 0;
+            for (int q = 0; q < a.P; ++q) {
+                const int64_t other = __shfl_sync(kFull, mine, q);
+                before += other > mine || (other == mine && q < lane);
+            }
+            r.p = __ffs(__ballot_sync(kFull, before == id && lane < a.P)) - 1;
+        }
     } else if (a.offsets == nullptr) {
         r.of = static_cast<int>(max(a.len / a.seg, int64_t(1)));
         r.p = id / r.of;
@@ -375,6 +385,7 @@ __global__ void __launch_bounds__(Split<ROWS>::kThreads, 2) glr_fwd_kernel(const
                 cluster_arrive_relaxed();
             }
             cluster_wait();
+#pragma unroll 1
             for (int k = 0; k < K; ++k) {
                 if (k == rank) hw = h;
                 join(h, &cA[buf][k][lane * 4], &cB[buf][k][lane * 4]);
@@ -385,6 +396,7 @@ __global__ void __launch_bounds__(Split<ROWS>::kThreads, 2) glr_fwd_kernel(const
             if (t0 > 0) hw = quad_at(&carry[buf][lane * 4]);
             if (st != nullptr && w == 0 && tl.on) st4(st + t0 / SDM_GLR_CHUNK * a.D, hw);
         }
+#pragma unroll 1
         for (int j = 0; j < w; ++j) join(hw, &sA[buf][j][lane * 4], &sB[buf][j][lane * 4]);
         if (!CLUSTER && w == kWarps - 1) {
             h = hw;
@@ -500,16 +512,20 @@ __global__ void __launch_bounds__(Split<ROWS>::kThreads, 2) glr_bwd_kernel(const
             } else {
                 cluster_arrive_relaxed();
             }
-            for (int j = 0; j < w; ++j) join(h, &sA[buf][j][lane * 4], &sF[buf][j][lane * 4]);
+#pragma unroll 1
+        for (int j = 0; j < w; ++j) join(h, &sA[buf][j][lane * 4], &sF[buf][j][lane * 4]);
             cluster_wait();
+#pragma unroll 1
             for (int k = K - 1; k >= 0; --k) {
                 if (k == rank) mw = m;
                 join(m, &cA[buf][k][lane * 4], &cR[buf][k][lane * 4]);
             }
         } else {
-            for (int j = 0; j < w; ++j) join(h, &sA[buf][j][lane * 4], &sF[buf][j][lane * 4]);
+#pragma unroll 1
+        for (int j = 0; j < w; ++j) join(h, &sA[buf][j][lane * 4], &sF[buf][j][lane * 4]);
             if (!first) mw = quad_at(&carry[buf][lane * 4]);
         }
+#pragma unroll 1
         for (int j = kWarps - 1; j > w; --j) join(mw, &sA[buf][j][lane * 4], &sR[buf][j][lane * 4]);
         if (!CLUSTER && w == 0) {
             m = mw;
@@ -738,16 +754,26 @@ size_t part_bytes(const GlrArgs& a) {
     return a.tiles_per_head == 1 ? 0 : static_cast<size_t>(a.tiles_per_head) * a.rows * a.H * sizeof(float);
 }
 
-// How the rows are divided: `cluster` blocks walk a part together, and parts are whole sequences or segments of them.
-void divide(const sdm_glr_shape* s, GlrArgs* a) {
+// How the rows are divided. A block alone walks a part where the tiles and sequences give 1.5 blocks an SM (152 of
+// them, kBusy blocks); else clusters of up to 8 do, and sequences of unequal lengths get four times as many blocks,
+// because the longest decides (24 sequences of 0 to 5526 rows, 30011 x 1920: 91 us with 1 block, 85 with 4, 120
+// with 8; 8 x 8192 x 2048 bfloat16, forward and backward: 456 us with 1, 397 with 2, 444 with 4). Where 8 are too few
+// and the sequences long, they are cut into segments for two blocks an SM, at the price of reading the inputs twice
+// (1 x 8192 x 1024: 97 us with clusters, 50 with segments; 1 x 4096 x 256: 48 and 47; 65537 x 512 float32: 893 and 192).
+constexpr int64_t kBusy = 228, kSegmentRows = 256, kLong = 4096;
+
+void divide(GlrArgs* a) {
     const int64_t units = static_cast<int64_t>(a->tiles) * a->P, steps = (a->len + SDM_GLR_CHUNK - 1) / SDM_GLR_CHUNK;
+    const int64_t want = a->offsets == nullptr || a->P == 1 ? kBusy : 4 * kBusy;
     a->cluster = 1;
     a->seg = 0;
-    int seg = 0;
-    if (const char* e = getenv("GLR_K")) a->cluster = atoi(e);
-    else while (a->cluster < kMaxCluster && units * a->cluster < 228 && a->cluster < steps) a->cluster *= 2;
-    if (const char* e = getenv("GLR_L")) seg = atoi(e);
-    a->seg = seg;
+    if (units * kMaxCluster < kBusy && a->len > kLong) {
+        const int64_t cuts = 2 * 152 / units;   // of a sequence
+        a->seg = std::max(kSegmentRows, (a->len + cuts - 1) / cuts);
+        a->seg = (a->seg + SDM_GLR_CHUNK - 1) / SDM_GLR_CHUNK * SDM_GLR_CHUNK;
+        return;
+    }
+    while (a->cluster < kMaxCluster && units * a->cluster < want && a->cluster < steps) a->cluster *= 2;
 }
 
 // Parts of the launch.
@@ -800,9 +826,9 @@ extern "C" sdm_status sdm_glr_forward(const sdm_glr_shape* shape, const void* x,
     GlrArgs a;
     geometry(shape, &a);
     if (static_cast<int64_t>(a.tiles) * (a.P + a.rows / SDM_GLR_CHUNK) > 0x7FFFFFFF / kMaxCluster) return SDM_ERR_SHAPE;
-    divide(shape, &a);
     a.x = x; a.x_ld = x_ld; a.g = g; a.g_ld = g_ld; a.y = y; a.y_ld = y_ld;
     a.offsets = offsets; a.h0 = h0; a.hT = hT; a.states = states; a.status = status;
+    divide(&a);
     const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
     const cudaError_t e = by_type(shape, [&](auto xt, auto gt, auto perch) {
         constexpr bool PC = decltype(perch)::value;
@@ -847,12 +873,12 @@ extern "C" sdm_status sdm_glr_backward(const sdm_glr_shape* shape, const void* x
     GlrArgs a;
     geometry(shape, &a);
     if (static_cast<int64_t>(a.tiles) * (a.P + a.rows / SDM_GLR_CHUNK) > 0x7FFFFFFF / kMaxCluster) return SDM_ERR_SHAPE;
-    divide(shape, &a);
     if (part_bytes(a) > 0 && (ws == nullptr || !aligned16(ws) || ws_bytes < part_bytes(a))) return SDM_ERR_WORKSPACE;
     a.x = x; a.x_ld = x_ld; a.g = g; a.g_ld = g_ld; a.dy = dy; a.dy_ld = dy_ld;
     a.dx = dx; a.dx_ld = dx_ld; a.dg = dg; a.dg_ld = dg_ld;
     a.offsets = offsets; a.dhT = dhT; a.dh0 = dh0; a.states = const_cast<float*>(states); a.status = status;
     a.part = static_cast<float*>(ws);
+    divide(&a);
     const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t e = by_type(shape, [&](auto xt, auto gt, auto perch) {
         constexpr bool PC = decltype(perch)::value;

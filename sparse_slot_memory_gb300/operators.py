@@ -24,31 +24,37 @@ _LAYOUT = {"half": 0, "interleaved": 1}
 
 
 class _Spec:
-    """A frozen description with its C struct, built once (the library only reads it)."""
+    """A frozen description; what is derived from it is built once (the C struct is only read by the library)."""
+
+    def _keep(self, name, value):
+        object.__setattr__(self, name, value)
+        return value
 
     def c(self):
         cs = self.__dict__.get("_cref")
-        if cs is None:
-            cs = ctypes.byref(self._struct())
-            object.__setattr__(self, "_cref", cs)
-        return cs
+        return self._keep("_cref", ctypes.byref(self._struct())) if cs is None else cs
 
 
-def _rows(t, dtype, shape, name: str, out: bool = False):
-    """The address of a row array [rows, ...] and the distance between its rows in elements. The library reads
-    bare pointers, so type, shape, place and layout are checked here."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+_Tensor = torch.Tensor
+
+
+def _rows(t, dtype, shape, n, name: str, out: bool = False):
+    """The address of a row array [rows, ..] whose rows hold n elements, and the distance between its rows in elements.
+    The library reads bare pointers, so type, shape, place and layout are checked here."""
+    if t.__class__ is _Tensor and t.dtype is dtype and t.is_cuda and t.shape == shape and t.is_contiguous():
+        return t.data_ptr(), n
+    if not isinstance(t, _Tensor) or not t.is_cuda:
         raise TypeError(f"{name}: expected a CUDA tensor (the library runs on the GPU only)")
     if t.dtype != dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
     st = t.stride()
-    n = 1
+    m = 1
     for i in range(len(shape) - 1, 0, -1):   # every dimension but the rows' is contiguous
-        if st[i] != n and shape[i] > 1:
+        if st[i] != m and shape[i] > 1:
             raise ValueError(f"{name}: rows must be contiguous, got strides {st}")
-        n *= shape[i]
+        m *= shape[i]
     if shape[0] <= 1:
         return t.data_ptr(), n
     if out and st[0] < n:
@@ -60,12 +66,17 @@ def _small(t, dtype, numel: int, name: str):
     """The address of an optional contiguous array of at least ``numel`` elements."""
     if t is None:
         return None
+    if t.__class__ is _Tensor and t.dtype is dtype and t.is_cuda and t.numel() >= numel and t.is_contiguous():
+        return t.data_ptr()
     _need(t, dtype, numel, name)
     return _ptr(t)
 
 
 def _status(status):
-    return _small(status, torch.int32, 1, "status")
+    return None if status is None else _small(status, torch.int32, 1, "status")
+
+
+_F32, _I32 = torch.float32, torch.int32
 
 
 # ---- the gated linear recurrence -------------------------------------------------------------------
@@ -89,25 +100,36 @@ class GlrSpec(_Spec):
         return _abi.GlrShape(self.P, self.D, self.gate_width, _DT[self.x_dtype], _DT[self.g_dtype], self.rows)
 
 
-def _glr_bytes(spec: GlrSpec, fn: str) -> int:
-    n = getattr(_abi.load(), fn)(spec.c())
-    if n == 0:
-        raise ValueError(f"invalid shape {spec}")
-    return int(n)
+def _bytes(spec, fn: str) -> int:
+    n = spec.__dict__.get(fn)
+    if n is None:
+        n = spec._keep(fn, int(getattr(_abi.load(), fn)(spec.c())))
+        if n == 0:
+            raise ValueError(f"invalid shape {spec}")
+    return n
+
+
+def _glr_kinds(spec: GlrSpec):
+    """The tensors' types and shapes: x's, g's, rows of x, rows of g, and P * D."""
+    k = spec.__dict__.get("_kinds")
+    if k is None:
+        k = spec._keep("_kinds", (_TORCH_DT[spec.x_dtype], _TORCH_DT[spec.g_dtype], (spec.rows, spec.D),
+                                  (spec.rows, spec.gates), spec.P * spec.D))
+    return k
 
 
 def alloc_glr_states(spec: GlrSpec, device="cuda") -> torch.Tensor:
     """The float32 states [.., D] that the forward saves for the backward (one for every 64 rows)."""
-    n = _glr_bytes(spec, "sdm_glr_states_bytes")
+    n = _bytes(spec, "sdm_glr_states_bytes")
     return torch.empty((n // (4 * spec.D), spec.D), dtype=torch.float32, device=device)
 
 
 def alloc_glr_workspace(spec: GlrSpec, device="cuda") -> torch.Tensor:
-    return torch.empty(_glr_bytes(spec, "sdm_glr_workspace_bytes"), dtype=torch.uint8, device=device)
+    return torch.empty(_bytes(spec, "sdm_glr_workspace_bytes"), dtype=torch.uint8, device=device)
 
 
 def _glr_states(spec: GlrSpec, states):
-    return _small(states, torch.float32, (spec.rows // _abi.SDM_GLR_CHUNK + spec.P) * spec.D, "states")
+    return _small(states, _F32, (spec.rows // _abi.SDM_GLR_CHUNK + spec.P) * spec.D, "states")
 
 
 def glr_forward(spec: GlrSpec, x, g, y, offsets=None, h0=None, hT=None, states=None, status=None, stream=None):
@@ -116,11 +138,11 @@ def glr_forward(spec: GlrSpec, x, g, y, offsets=None, h0=None, hT=None, states=N
     [P + 1]: sequence p owns rows offsets[p] .. offsets[p+1] - 1, else all have rows / P rows; ``h0``, ``hT``
     (optional) float32 [P, D]: the states before and after (may be one tensor); ``states`` (optional, from
     ``alloc_glr_states``) receives what ``glr_backward`` needs."""
-    xt, gt, PD = _TORCH_DT[spec.x_dtype], _TORCH_DT[spec.g_dtype], spec.P * spec.D
+    xt, gt, xs, gs, PD = _glr_kinds(spec)
+    D, G = xs[1], gs[1]
     st = _abi.load().sdm_glr_forward(
-        spec.c(), *_rows(x, xt, (spec.rows, spec.D), "x"), *_rows(g, gt, (spec.rows, spec.gates), "g"),
-        _small(offsets, torch.int64, spec.P + 1, "offsets"), _small(h0, torch.float32, PD, "h0"),
-        *_rows(y, xt, (spec.rows, spec.D), "y", True), _small(hT, torch.float32, PD, "hT"),
+        spec.c(), *_rows(x, xt, xs, D, "x"), *_rows(g, gt, gs, G, "g"), _small(offsets, torch.int64, spec.P + 1, "offsets"),
+        _small(h0, _F32, PD, "h0"), *_rows(y, xt, xs, D, "y", True), _small(hT, _F32, PD, "hT"),
         _glr_states(spec, states), _status(status), _stream(stream))
     _check(st, "sdm_glr_forward")
 
@@ -130,31 +152,29 @@ def glr_backward(spec: GlrSpec, x, g, dy, states, dx, dg, ws=None, offsets=None,
     """sdm_glr_backward: the gradients ``dx`` [rows, D], ``dg`` [rows, D / gate_width] and ``dh0`` (optional,
     float32 [P, D]) from ``dy`` and ``dhT`` (optional: the gradient of the states after). ``x``, ``g``, ``offsets`` and
     ``states`` are those of the forward; ``ws`` (from ``alloc_glr_workspace``) is needed where gate_width > 128."""
-    xt, gt, PD = _TORCH_DT[spec.x_dtype], _TORCH_DT[spec.g_dtype], spec.P * spec.D
+    xt, gt, xs, gs, PD = _glr_kinds(spec)
+    D, G = xs[1], gs[1]
     if states is None:
         raise ValueError("states: the backward needs the states that the forward saved")
     st = _abi.load().sdm_glr_backward(
-        spec.c(), *_rows(x, xt, (spec.rows, spec.D), "x"), *_rows(g, gt, (spec.rows, spec.gates), "g"),
-        *_rows(dy, xt, (spec.rows, spec.D), "dy"), _small(offsets, torch.int64, spec.P + 1, "offsets"),
-        _glr_states(spec, states), _small(dhT, torch.float32, PD, "dhT"),
-        *_rows(dx, xt, (spec.rows, spec.D), "dx", True), *_rows(dg, gt, (spec.rows, spec.gates), "dg", True),
-        _small(dh0, torch.float32, PD, "dh0"), _small(ws, torch.uint8, 0, "ws"), 0 if ws is None else ws.numel(),
-        _status(status), _stream(stream))
+        spec.c(), *_rows(x, xt, xs, D, "x"), *_rows(g, gt, gs, G, "g"), *_rows(dy, xt, xs, D, "dy"),
+        _small(offsets, torch.int64, spec.P + 1, "offsets"), _glr_states(spec, states), _small(dhT, _F32, PD, "dhT"),
+        *_rows(dx, xt, xs, D, "dx", True), *_rows(dg, gt, gs, G, "dg", True), _small(dh0, _F32, PD, "dh0"),
+        _small(ws, torch.uint8, 0, "ws"), 0 if ws is None else ws.numel(), _status(status), _stream(stream))
     _check(st, "sdm_glr_backward")
 
 
 def glr_step(spec: GlrSpec, x, g, state, y, slots=None, status=None, stream=None):
     """sdm_glr_step: one token of each of ``spec.rows`` requests. ``state`` float32 [states, D] is updated in place:
     row ``slots[i]`` (int32, distinct; below 0: a padding row) for token i, or row i without ``slots``."""
-    xt = _TORCH_DT[spec.x_dtype]
-    if not isinstance(state, torch.Tensor) or state.dim() != 2:
+    xt, gt, xs, gs, _ = _glr_kinds(spec)
+    D = xs[1]
+    if not isinstance(state, _Tensor) or state.dim() != 2:
         raise ValueError("state: expected a float32 tensor [states, D]")
     n = state.shape[0]
     st = _abi.load().sdm_glr_step(
-        spec.c(), *_rows(x, xt, (spec.rows, spec.D), "x"),
-        *_rows(g, _TORCH_DT[spec.g_dtype], (spec.rows, spec.gates), "g"),
-        _small(slots, torch.int32, spec.rows, "slots"), *_rows(state, torch.float32, (n, spec.D), "state", True), n,
-        *_rows(y, xt, (spec.rows, spec.D), "y", True), _status(status), _stream(stream))
+        spec.c(), *_rows(x, xt, xs, D, "x"), *_rows(g, gt, gs, gs[1], "g"), _small(slots, _I32, xs[0], "slots"),
+        *_rows(state, _F32, (n, D), D, "state", True), n, *_rows(y, xt, xs, D, "y", True), _status(status), _stream(stream))
     _check(st, "sdm_glr_step")
 
 
@@ -215,33 +235,31 @@ def rope_table(spec: RopeSpec, inv_freq, table, scale: float = 1.0, stream=None)
 
 
 def alloc_rope_workspace(spec: RopeSpec, device="cuda") -> torch.Tensor:
-    n = _abi.load().sdm_rope_workspace_bytes(spec.c())
-    if n == 0:
-        raise ValueError(f"invalid shape {spec}")
-    return torch.empty(int(n), dtype=torch.uint8, device=device)
+    return torch.empty(_bytes(spec, "sdm_rope_workspace_bytes"), dtype=torch.uint8, device=device)
 
 
-def _heads(spec: RopeSpec, q, k, names, out=False):
-    dt, T = _TORCH_DT[spec.dtype], spec.tokens
-    none = (None, 0)
-    return (*(_rows(q, dt, (T, spec.q_heads, spec.hd), names[0], out) if spec.q_heads else none),
-            *(_rows(k, dt, (T, spec.k_heads, spec.hd), names[1], out) if spec.k_heads else none))
+def _heads(spec: RopeSpec, q, k, qname, kname, out=False):
+    kinds = spec.__dict__.get("_kinds")
+    if kinds is None:
+        kinds = spec._keep("_kinds", (_TORCH_DT[spec.dtype], (spec.tokens, spec.q_heads, spec.hd),
+                                      spec.q_heads * spec.hd, (spec.tokens, spec.k_heads, spec.hd), spec.k_heads * spec.hd))
+    dt, qs, qn, ks, kn = kinds
+    return (*(_rows(q, dt, qs, qn, qname, out) if qn else (None, 0)), *(_rows(k, dt, ks, kn, kname, out) if kn else (None, 0)))
 
 
 def _rope_small(spec: RopeSpec, positions, table, wq, wk):
-    f32 = torch.float32
-    return (_small(positions, torch.int32, spec.tokens, "positions"),
-            _small(table, f32, spec.max_pos * spec.rot_dim, "table"), _small(wq, f32, spec.hd, "wq"),
-            _small(wk, f32, spec.hd, "wk"))
+    hd = spec.hd
+    return (_small(positions, _I32, spec.tokens, "positions"), _small(table, _F32, spec.max_pos * spec.rot_dim, "table"),
+            _small(wq, _F32, hd, "wq"), _small(wk, _F32, hd, "wk"))
 
 
 def qk_norm_rope(spec: RopeSpec, q, k, positions, table, wq, wk, q_out, k_out, status=None, stream=None):
     """sdm_qk_norm_rope: the RMS norm of every head of ``q`` [tokens, q_heads, hd] and ``k`` [tokens, k_heads, hd]
     with the weights ``wq``, ``wk`` (float32 [hd], or None for ones), turned by the table's row of the token's position
     (int32 [tokens]; below 0: a padding token, whose outputs are 0). The outputs may be the inputs."""
-    st = _abi.load().sdm_qk_norm_rope(spec.c(), *_heads(spec, q, k, ("q", "k")),
+    st = _abi.load().sdm_qk_norm_rope(spec.c(), *_heads(spec, q, k, "q", "k"),
                                       *_rope_small(spec, positions, table, wq, wk),
-                                      *_heads(spec, q_out, k_out, ("q_out", "k_out"), True), _status(status),
+                                      *_heads(spec, q_out, k_out, "q_out", "k_out", True), _status(status),
                                       _stream(stream))
     _check(st, "sdm_qk_norm_rope")
 
@@ -250,11 +268,10 @@ def qk_norm_rope_backward(spec: RopeSpec, dq_out, dk_out, q, k, positions, table
                           ws=None, status=None, stream=None):
     """sdm_qk_norm_rope_backward: ``dq``, ``dk`` and the weights' gradients ``dwq``, ``dwk`` (optional, float32 [hd]) from
     the outputs' gradients and the forward's inputs. ``ws`` (from ``alloc_rope_workspace``) is needed for dwq, dwk."""
-    f32 = torch.float32
     st = _abi.load().sdm_qk_norm_rope_backward(
-        spec.c(), *_heads(spec, dq_out, dk_out, ("dq_out", "dk_out")), *_heads(spec, q, k, ("q", "k")),
-        *_rope_small(spec, positions, table, wq, wk), *_heads(spec, dq, dk, ("dq", "dk"), True),
-        _small(dwq, f32, spec.hd, "dwq"), _small(dwk, f32, spec.hd, "dwk"), _small(ws, torch.uint8, 0, "ws"),
+        spec.c(), *_heads(spec, dq_out, dk_out, "dq_out", "dk_out"), *_heads(spec, q, k, "q", "k"),
+        *_rope_small(spec, positions, table, wq, wk), *_heads(spec, dq, dk, "dq", "dk", True),
+        _small(dwq, _F32, spec.hd, "dwq"), _small(dwk, _F32, spec.hd, "dwk"), _small(ws, torch.uint8, 0, "ws"),
         0 if ws is None else ws.numel(), _status(status), _stream(stream))
     _check(st, "sdm_qk_norm_rope_backward")
 
@@ -279,12 +296,11 @@ def token_logprobs(spec: LogprobSpec, logits, targets, logp, entropy=None, lse=N
     """sdm_token_logprobs: of every row of ``logits`` [rows, V] the log probability of ``targets`` (int32; below 0:
     ignored, 0) and, where asked for, the entropy and log-sum-exp [rows] and the log probabilities and ids of the K
     largest logits [rows, K], the lower id first among equals (float32; ids int32)."""
-    f32, N = torch.float32, spec.rows
+    N, V, K = spec.rows, spec.V, spec.K
     st = _abi.load().sdm_token_logprobs(
-        spec.c(), *_rows(logits, _TORCH_DT[spec.dtype], (N, spec.V), "logits"),
-        _small(targets, torch.int32, N, "targets"), _small(logp, f32, N, "logp"), _small(entropy, f32, N, "entropy"),
-        _small(lse, f32, N, "lse"), _small(top_vals, f32, N * spec.K, "top_vals"),
-        _small(top_idx, torch.int32, N * spec.K, "top_idx"), _status(status), _stream(stream))
+        spec.c(), *_rows(logits, _TORCH_DT[spec.dtype], (N, V), V, "logits"), _small(targets, _I32, N, "targets"),
+        _small(logp, _F32, N, "logp"), _small(entropy, _F32, N, "entropy"), _small(lse, _F32, N, "lse"),
+        _small(top_vals, _F32, N * K, "top_vals"), _small(top_idx, _I32, N * K, "top_idx"), _status(status), _stream(stream))
     _check(st, "sdm_token_logprobs")
 
 
@@ -292,10 +308,9 @@ def token_logprobs_backward(spec: LogprobSpec, logits, targets, lse, entropy, d_
                             status=None, stream=None):
     """sdm_token_logprobs_backward: ``dlogits`` [rows, V] from the gradients of logp and (optional) of the entropy,
     with the forward's ``lse`` and ``entropy``."""
-    f32, N, dt = torch.float32, spec.rows, _TORCH_DT[spec.dtype]
+    N, V, dt = spec.rows, spec.V, _TORCH_DT[spec.dtype]
     st = _abi.load().sdm_token_logprobs_backward(
-        spec.c(), *_rows(logits, dt, (N, spec.V), "logits"), _small(targets, torch.int32, N, "targets"),
-        _small(lse, f32, N, "lse"), _small(entropy, f32, N, "entropy"), _small(d_logp, f32, N, "d_logp"),
-        _small(d_entropy, f32, N, "d_entropy"), *_rows(dlogits, dt, (N, spec.V), "dlogits", True), _status(status),
-        _stream(stream))
+        spec.c(), *_rows(logits, dt, (N, V), V, "logits"), _small(targets, _I32, N, "targets"), _small(lse, _F32, N, "lse"),
+        _small(entropy, _F32, N, "entropy"), _small(d_logp, _F32, N, "d_logp"), _small(d_entropy, _F32, N, "d_entropy"),
+        *_rows(dlogits, dt, (N, V), V, "dlogits", True), _status(status), _stream(stream))
     _check(st, "sdm_token_logprobs_backward")

@@ -87,6 +87,13 @@ CASES = {
     # ragged, with empty sequences first, last and between
     "ragged": dict(lens=[0, 5, 130, 0, 64, 1, 300, 0], D=132, gw=1),
     "ragged_heads": dict(lens=[70, 0, 0, 129, 3], D=384, gw=192, xt="f32"),
+    # few channels and many rows (segments), equal and ragged; many sequences (a block each) and fewer (small clusters)
+    "segments": dict(lens=[9001], D=12, gw=4, xt="f32"), "segments_bf16": dict(lens=[4200, 4200], D=132, gw=1),
+    "segments_ragged": dict(lens=[0, 9000, 3, 0, 13000, 255, 256, 511, 512, 20000], D=8, gw=1, xt="f32", gt="bf16"),
+    "segments_wide": dict(lens=[6000], D=320, gw=160, gt="bf16"),
+    "blocks": dict(lens=[130] * 240, D=8, gw=1), "blocks_ragged": dict(lens=[3, 200, 70] * 320, D=4, gw=4, xt="f32"),
+    "pairs": dict(lens=[300] * 120, D=4, gw=1, gt="bf16"), "fours": dict(lens=[700] * 60, D=8, gw=8),
+    "fours_ragged": dict(lens=[1000, 0, 64, 300] * 60, D=4, gw=1, xt="f32"),
     "all_empty": dict(lens=[0, 0], D=8, gw=1),
     # rows further apart than they are long; no states given
     "strided": dict(lens=[100, 100], D=132, gw=1, pad=12), "strided_heads": dict(lens=[9, 100], D=160, gw=40, pad=4, gt="bf16"),
