@@ -320,7 +320,7 @@ __global__ void __launch_bounds__(Split<ROWS>::kThreads, 2) glr_fwd_kernel(const
     __shared__ __align__(16) float cA[2][CLUSTER ? kMaxCluster : 1][kTileCols], cB[2][CLUSTER ? kMaxCluster : 1][kTileCols];
     __shared__ __align__(16) float carry[2][kTileCols];
     if (CLUSTER) cluster_arrive_relaxed();
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    start_dependent();
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     const int K = CLUSTER ? a.cluster : 1, rank = CLUSTER ? cluster_rank() : 0;
     const int unit = blockIdx.x / K, id = unit / a.tiles;
@@ -452,7 +452,7 @@ __global__ void __launch_bounds__(Split<ROWS>::kThreads, 2) glr_bwd_kernel(const
     __shared__ __align__(16) float cA[2][CLUSTER ? kMaxCluster : 1][kTileCols], cR[2][CLUSTER ? kMaxCluster : 1][kTileCols];
     __shared__ __align__(16) float carry[2][kTileCols];
     if (CLUSTER) cluster_arrive_relaxed();
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    start_dependent();
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     const int K = CLUSTER ? a.cluster : 1, rank = CLUSTER ? cluster_rank() : 0;
     const int unit = blockIdx.x / K, id = unit / a.tiles;
@@ -573,7 +573,7 @@ __global__ void __launch_bounds__(Split<ROWS>::kThreads, 2) glr_bwd_kernel(const
 template <typename XT, typename GT, bool PERCH, bool REVERSE>
 __global__ void __launch_bounds__(256, 2) glr_pair_kernel(const GlrArgs a) {
     __shared__ __align__(16) float sA[8][kTileCols], sB[8][kTileCols];
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    start_dependent();
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     const int id = blockIdx.x / a.tiles;
     const Tile tl = tile_of<PERCH>(a, blockIdx.x - id * a.tiles, lane);
@@ -621,8 +621,8 @@ __global__ void __launch_bounds__(256, 2) glr_pair_kernel(const GlrArgs a) {
 // four channels of a sequence, kAhead segments' pairs on their way at once.
 template <typename XT, bool REVERSE>
 __global__ void __launch_bounds__(128) glr_chain_kernel(const GlrArgs a) {
-    constexpr int kAhead = 8;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    constexpr int kAhead = 16;
+    start_dependent();
     const int quads = a.D / 4, blocks = (quads + 127) / 128, p = blockIdx.x / blocks;
     const int q = (blockIdx.x - p * blocks) * 128 + threadIdx.x;
     if (q >= quads) return;
@@ -655,7 +655,7 @@ __global__ void __launch_bounds__(128) glr_chain_kernel(const GlrArgs a) {
 // dg of a head wider than a tile: the sum of its tiles' parts, in tile order.
 template <typename GT>
 __global__ void __launch_bounds__(256) glr_dg_kernel(const GlrArgs a) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    start_dependent();
     const int64_t n = a.rows * a.H;
     for (int64_t i = blockIdx.x * int64_t(256) + threadIdx.x; i < n; i += gridDim.x * int64_t(256)) {
         float s = a.part[i];
@@ -679,7 +679,7 @@ struct StepArgs {
 
 template <typename XT, typename GT, bool PERCH>
 __global__ void __launch_bounds__(256) glr_step_kernel(const StepArgs a) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    start_dependent();
     const int64_t u = blockIdx.x * int64_t(256) + threadIdx.x;
     if (u >= a.units) return;
     const int quads = a.D / 4;

@@ -162,6 +162,13 @@ struct DWArgs {
     int64_t items;      // P * B * nsl
 };
 
+// The first instruction of a kernel that is launched as a programmatic dependent: lets the kernel behind it take up
+// free SMs once all of this one's blocks have started (it waits there in its turn), and waits for the kernel before.
+__device__ __forceinline__ void start_dependent() {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
 // A launch as a programmatic dependent of the previous kernel in the stream: its CTAs may be
 // scheduled before that kernel completes (onto SMs it leaves idle) and wait in the kernel
 // (griddepcontrol.wait) until it has completed and its memory is visible. Every kernel launched so

@@ -6,10 +6,9 @@
 // new M when a larger logit comes; the threads' triples join the same way. log p(target) = (t_target - log2 s) ln 2,
 // H = (log2 s - u / s) ln 2. Backward: dz_v = dlogp (1[v = target] - p_v) - dH p_v (log p_v + H).
 //
-// The top alternatives are kept in the same pass: every warp holds its K <= 32 largest (value, id) so far, one in a
-// lane, and looks only at vectors that hold a logit above the last of them. Before the first is taken, the 32 half
-// warps' largest logits of the block's first batch bound the K-th largest from below: only logits at least as large
-// as the least of those 32 are ever looked at (in random rows about one of 150). Sorted lists join by halves.
+// The top alternatives are kept in the same pass: every warp holds its 32 largest (value, id) so far, one in a lane.
+// The block's first batch bounds the K-th largest from below, and what a warp's list holds raises the bound; only
+// logits at least as large are looked at, wait in the shared memory, and join the list sorted, 32 at a time.
 //
 // A row is one block's, or where there are fewer rows than the SMs hold blocks, a cluster's: each block takes a part
 // of the row and the first joins their triples and lists through its shared memory.
@@ -32,12 +31,13 @@ namespace {
 
 using namespace rows;
 
-constexpr int kThreads = 512;
-constexpr int kWarps = kThreads / 32;
+constexpr int kRowThreads = 256;      // threads of a block that has a row to itself, and of one of a cluster
+constexpr int kClusterThreads = 512;
+constexpr int kMaxWarps = kClusterThreads / 32;
+constexpr int kRowBlocks = 4;         // blocks of kRowThreads on an SM
 constexpr int kBatch = 4;             // vectors of a thread in flight
 constexpr int kMaxK = 32;
 constexpr int kMaxCluster = 8;
-static_assert(kThreads / 16 == kMaxK, "one half warp for each alternative bounds them from below");
 constexpr float kLog2e = 1.44269504088896341f;
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr float kFloor = -1e35f;      // what a masked logit counts as in the sums: its term is 0 beside any M
@@ -180,16 +180,26 @@ struct Sums {
     }
 };
 
-// A warp's K largest (order, ~id) so far, the i-th in lane i.
+// A warp's 32 largest (order, ~id) so far, the i-th in lane i, and up to 63 logits that wait to join them.
 struct TopList {
     uint64_t key;
-    int K, lane;
-    uint32_t pass;   // a logit enters only if its order is at least this
-    __device__ __forceinline__ void clear(int k, int l) {
+    uint64_t* wait;   // [64] in shared memory
+    uint32_t* bound;  // the block's: K logits at least this large are known
+    int K, lane, n;   // n wait
+    uint32_t pass;    // a logit enters only if its order is at least this
+    __device__ __forceinline__ void clear(int k, int l, uint64_t* w, uint32_t* b) {
         key = 0;
+        wait = w;
+        bound = b;
         K = k;
         lane = l;
+        n = 0;
         pass = 0;
+    }
+    // A step of a sorting network: the lane pairs at distance d, the larger first where `down`
+    __device__ __forceinline__ static void step(uint64_t& k, int d, bool down, int lane) {
+        const uint64_t x = __shfl_xor_sync(kFull, k, d);
+        k = (k > x) == (((lane & d) == 0) == down) ? k : x;
     }
     // The 32 largest of this list and another, both descending over the lanes: the larger of lane i's and the other's
     // lane 31 - i are those 32, and five exchanges bring them in order.
@@ -197,21 +207,29 @@ struct TopList {
         const uint64_t o = __shfl_xor_sync(kFull, other, 31);
         key = key > o ? key : o;
 #pragma unroll
-        for (int k = 16; k; k >>= 1) {
-            const uint64_t x = __shfl_xor_sync(kFull, key, k);
-            const bool up = (lane & k) == 0;
-            key = (key > x) == up ? key : x;
-        }
+        for (int d = 16; d; d >>= 1) step(key, d, true, lane);
     }
-    __device__ __forceinline__ void insert(uint64_t c) {   // warp-uniform c
-        const uint64_t last = __shfl_sync(kFull, key, K - 1);
-        if (c <= last) return;
-        const int at = __popc(__ballot_sync(kFull, lane < K && key > c));
-        const uint64_t up = __shfl_up_sync(kFull, key, 1);
-        if (lane < K && lane >= at) key = lane == at ? c : up;
+    // The first 32 that wait are sorted and join the list.
+    __device__ __forceinline__ void flush() {
+        __syncwarp();
+        uint64_t c = lane < n ? wait[lane] : 0;
+        const uint64_t rest = lane + 32 < n ? wait[lane + 32] : 0;
+        __syncwarp();
+        wait[lane] = rest;
+        n = max(0, n - 32);
+#pragma unroll
+        for (int size = 2; size <= 32; size <<= 1)
+#pragma unroll
+            for (int d = size >> 1; d; d >>= 1) step(c, d, (lane & size) == 0, lane);
+        join(c);
         const uint32_t k = static_cast<uint32_t>(__shfl_sync(kFull, key, K - 1) >> 32);
-        // once K are held, an equal logit of a later vector has a higher id and stays out
-        if (k != 0) pass = max(pass, k == 0xFFFFFFFFu ? k : k + 1);
+        if (k != 0) {
+            // an equal logit of one of the warp's later vectors has a higher id and stays out; one of another warp
+            // may have a lower
+            pass = max(pass, k == 0xFFFFFFFFu ? k : k + 1);
+            if (lane == 0) atomicMax(bound, k);
+        }
+        __syncwarp();
     }
     // N logits of each lane, ids id .. id + N - 1 (those from `end` on are none)
     template <int N>
@@ -222,23 +240,22 @@ struct TopList {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             const uint32_t o = order_of(x[i]);
-            uint32_t b = __ballot_sync(kFull, id + i < end && o >= bar);
-            while (b) {
-                const int l = __ffs(b) - 1;
-                b &= b - 1;
-                const uint32_t oc = __shfl_sync(kFull, o, l);
-                const uint32_t ic = static_cast<uint32_t>(__shfl_sync(kFull, id, l) + i);
-                insert(static_cast<uint64_t>(oc) << 32 | static_cast<uint32_t>(~ic));
-            }
+            const bool in = want && id + i < end && o >= bar;
+            const uint32_t b = __ballot_sync(kFull, in);
+            if (b == 0) continue;
+            if (in) wait[n + __popc(b & ((1u << lane) - 1u))] = static_cast<uint64_t>(o) << 32 | static_cast<uint32_t>(~(id + i));
+            n += __popc(b);
+            if (n >= 32) flush();
         }
     }
 };
 
 struct Shared {
-    float M[kWarps], s[kWarps], u[kWarps];
-    uint64_t top[kWarps][kMaxK];
-    float red[kWarps];
-    uint32_t bound[kMaxK];
+    float M[kMaxWarps], s[kMaxWarps], u[kMaxWarps];
+    uint64_t top[kMaxWarps][kMaxK];
+    float red[kMaxWarps];
+    uint64_t wait[kMaxWarps][64];
+    uint32_t least[kMaxWarps], bound;
     // of the cluster's blocks, in the first one
     float cM[kMaxCluster], cs[kMaxCluster], cu[kMaxCluster];
     uint64_t ctop[kMaxCluster][kMaxK];
@@ -249,7 +266,7 @@ __device__ __forceinline__ void join_lists(uint64_t (*top)[kMaxK], int n, int w,
     for (int h = n >> 1; h; h >>= 1) {
         if (w < h) {
             TopList l;
-            l.clear(kMaxK, lane);
+            l.lane = lane;
             l.key = top[w][lane];
             l.join(top[w + h][lane]);
             top[w][lane] = l.key;
@@ -290,10 +307,11 @@ __device__ void plain_stats(const T* x, int V, float scale, Shared& sh, float& m
 }
 
 template <typename T, bool TOP, bool CLUSTER>
-__global__ void __launch_bounds__(kThreads, 2) lp_fwd_kernel(const LpArgs a) {
+__global__ void __launch_bounds__(CLUSTER ? kClusterThreads : kRowThreads, CLUSTER ? 2 : kRowBlocks) lp_fwd_kernel(const LpArgs a) {
+    constexpr int kThreads = CLUSTER ? kClusterThreads : kRowThreads, kWarps = kThreads / 32;
     __shared__ Shared sh;
     if (CLUSTER) cluster_arrive_relaxed();
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    start_dependent();
     constexpr int N = Vec<T>::n;
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     const int C = CLUSTER ? a.cluster : 1, rank = CLUSTER ? cluster_rank() : 0;
@@ -303,7 +321,11 @@ __global__ void __launch_bounds__(kThreads, 2) lp_fwd_kernel(const LpArgs a) {
     Sums acc;
     acc.clear();
     TopList top;
-    top.clear(a.K, lane);
+    top.clear(a.K, lane, sh.wait[w], &sh.bound);
+    if (TOP) {
+        if (threadIdx.x == 0) sh.bound = 0;
+        __syncthreads();
+    }
     // vectors start at the row's first 16-byte boundary; the logits before it and behind the last vector are
     // taken one by one, by the first and the last block (ids ascend over what a warp sees)
     const int head = min(a.V, static_cast<int>((16 - (reinterpret_cast<uintptr_t>(x) & 15)) % 16 / sizeof(T)));
@@ -337,14 +359,19 @@ __global__ void __launch_bounds__(kThreads, 2) lp_fwd_kernel(const LpArgs a) {
         if (!(most * c <= acc.M)) acc.raise(most * c);
         acc.add(r, c);
         if (TOP) {
-            if (v0 == vb) {   // block-uniform: the bound from the first batch
-                uint32_t o = order_of(most);
-#pragma unroll
-                for (int k = 8; k; k >>= 1) o = max(o, __shfl_xor_sync(kFull, o, k));
-                if ((lane & 15) == 0) sh.bound[threadIdx.x >> 4] = o;
+            if (v0 == vb) {
+                // block-uniform: the first batch bounds the K-th largest from below. Each of the warps has `r` threads
+                // whose largest logits are at least its r-th largest of those, together K or more
+                uint32_t o = order_of(most), m = 0;
+                for (int r = (a.K + kWarps - 1) / kWarps; r; --r) {
+                    m = __reduce_max_sync(kFull, o);
+                    if (__ffs(__ballot_sync(kFull, o == m)) - 1 == lane) o = 0;
+                }
+                if (lane == 0) sh.least[w] = m;
                 __syncthreads();
-                top.pass = max(top.pass, __reduce_min_sync(kFull, sh.bound[lane]));
+                top.pass = max(top.pass, __reduce_min_sync(kFull, sh.least[lane % kWarps]));
             }
+            top.pass = max(top.pass, *static_cast<volatile uint32_t*>(&sh.bound));
             if (__any_sync(kFull, order_of(most) >= top.pass)) {
 #pragma unroll
                 for (int k = 0; k < kBatch; ++k) {
@@ -368,7 +395,10 @@ __global__ void __launch_bounds__(kThreads, 2) lp_fwd_kernel(const LpArgs a) {
         sh.s[w] = acc.s;
         sh.u[w] = acc.u;
     }
-    if (TOP) sh.top[w][lane] = top.key;
+    if (TOP) {
+        while (top.n > 0) top.flush();
+        sh.top[w][lane] = top.key;
+    }
     __syncthreads();
     if (TOP) join_lists(sh.top, kWarps, w, lane);
     acc.clear();
@@ -436,7 +466,7 @@ constexpr int kBwdVecs = 4;   // vectors of a thread
 template <typename T>
 __global__ void __launch_bounds__(kBwdThreads) lp_bwd_kernel(const LpArgs a, int parts) {
     __shared__ Shared sh;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    start_dependent();
     constexpr int N = Vec<T>::n;
     const int64_t row = blockIdx.x / parts;
     const int part = static_cast<int>(blockIdx.x - row * parts);
@@ -528,7 +558,7 @@ sdm_status check_logits(const sdm_logprob_shape* s, const void* p, int64_t ld, b
 
 // Blocks of a row: as many as leave each at least a batch, while the rows alone leave SMs idle.
 int cluster_of(const sdm_logprob_shape* s) {
-    const int64_t batch = kThreads * 16 / (s->dtype == SDM_BF16 ? 2 : 4);
+    const int64_t batch = kClusterThreads * 16 / (s->dtype == SDM_BF16 ? 2 : 4);
     int c = 1;
     while (c < kMaxCluster && s->rows * c < 152 && s->V >= 2 * c * batch) c *= 2;
     return c;
@@ -556,7 +586,7 @@ extern "C" sdm_status sdm_token_logprobs(const sdm_logprob_shape* shape, const v
     const bool bf = shape->dtype == SDM_BF16;
     a.cluster = cluster_of(shape);
     if (shape->rows * a.cluster > 0x7FFFFFFF) return SDM_ERR_SHAPE;
-    const dim3 grid(static_cast<unsigned>(shape->rows * a.cluster)), block(kThreads);
+    const dim3 grid(static_cast<unsigned>(shape->rows * a.cluster)), block(a.cluster > 1 ? kClusterThreads : kRowThreads);
     const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
     auto run = [&](auto t, auto with_top) {
         using T = decltype(t);

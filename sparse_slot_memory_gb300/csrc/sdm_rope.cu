@@ -198,7 +198,7 @@ struct Walk {
 template <typename T, int U, bool INTER>
 __global__ void __launch_bounds__(kThreads, U == 1 ? kFwdBlocks : 1) rope_fwd_kernel(const RopeArgs s, int lanes) {
     constexpr int HU = heads_at_once<T, U>();
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    start_dependent();
     const int per = kThreads / lanes, cq = (s.Hq + HU - 1) / HU, ct = cq + (s.Hk + HU - 1) / HU;
     const int units = static_cast<int>(s.tokens) * ct, sub = threadIdx.x % lanes;
     const float inv = 1.f / s.hd;
@@ -273,7 +273,7 @@ template <typename T, int U, bool INTER>
 __global__ void __launch_bounds__(kThreads, U == 1 ? 2 : 1) rope_bwd_kernel(const RopeArgs s, int lanes) {
     constexpr int HU = heads_at_once<T, U>();
     extern __shared__ float sm[];   // [groups][hd]
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    start_dependent();
     const int per = kThreads / lanes, group = threadIdx.x / lanes, sub = threadIdx.x % lanes;
     const float inv = 1.f / s.hd;
     Place<U> pl;
@@ -388,7 +388,7 @@ __global__ void __launch_bounds__(kThreads, U == 1 ? 2 : 1) rope_bwd_kernel(cons
 // threads each a strided share of the partial rows.
 __global__ void __launch_bounds__(1024) rope_dw_kernel(const float* part, int blocks, int hd, float* dwq, float* dwk) {
     __shared__ float sm[32][33];
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    start_dependent();
     const int c = blockIdx.x * 32 + threadIdx.x;   // of 2 * hd columns
     float v = 0.f;
     if (c < 2 * hd)
@@ -412,7 +412,7 @@ struct TableArgs {
 
 // cos and sin of pos * f: the whole turns drop out of the 64-bit product exactly, whatever the position.
 __global__ void __launch_bounds__(256) rope_table_kernel(const __grid_constant__ TableArgs a) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    start_dependent();
     const int64_t i = blockIdx.x * int64_t(256) + threadIdx.x;
     if (i >= static_cast<int64_t>(a.n) * a.max_pos) return;
     const int64_t pos = i / a.n;
