@@ -34,6 +34,7 @@ using namespace rows;
 constexpr int kRowThreads = 256;      // threads of a block that has a row to itself, and of one of a cluster
 constexpr int kClusterThreads = 512;
 constexpr int kMaxWarps = kClusterThreads / 32;
+static_assert(kRowThreads <= 1024 && kClusterThreads <= 1024, "a warp gives at least one of the 32 logits that bound the alternatives");
 constexpr int kRowBlocks = 4;         // blocks of kRowThreads on an SM
 constexpr int kBatch = 4;             // vectors of a thread in flight
 constexpr int kMaxK = 32;
@@ -187,6 +188,13 @@ struct TopList {
     uint32_t* bound;  // the block's: K logits at least this large are known
     int K, lane, n;   // n wait
     uint32_t pass;    // a logit enters only if its order is at least this
+    float thr;        // the same as a value: logits below it do not enter (NaN: none is below)
+    __device__ __forceinline__ void raise(uint32_t p) {
+        if (p > pass) {
+            pass = p;
+            thr = value_of(p);
+        }
+    }
     __device__ __forceinline__ void clear(int k, int l, uint64_t* w, uint32_t* b) {
         key = 0;
         wait = w;
@@ -195,6 +203,7 @@ struct TopList {
         lane = l;
         n = 0;
         pass = 0;
+        thr = value_of(0);
     }
     // A step of a sorting network: the lane pairs at distance d, the larger first where `down`
     __device__ __forceinline__ static void step(uint64_t& k, int d, bool down, int lane) {
@@ -226,7 +235,7 @@ struct TopList {
         if (k != 0) {
             // an equal logit of one of the warp's later vectors has a higher id and stays out; one of another warp
             // may have a lower
-            pass = max(pass, k == 0xFFFFFFFFu ? k : k + 1);
+            raise(k == 0xFFFFFFFFu ? k : k + 1);
             if (lane == 0) atomicMax(bound, k);
         }
         __syncwarp();
@@ -234,16 +243,17 @@ struct TopList {
     // N logits of each lane, ids id .. id + N - 1 (those from `end` on are none)
     template <int N>
     __device__ __forceinline__ void offer(const float (&x)[N], float most, int id, int end) {
-        const bool want = id < end && order_of(most) >= pass;
+        const float bar = thr;
+        const bool want = id < end && !(most < bar);
         if (!__any_sync(kFull, want)) return;
-        const uint32_t bar = pass;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const uint32_t o = order_of(x[i]);
-            const bool in = want && id + i < end && o >= bar;
+            const bool in = want && id + i < end && !(x[i] < bar);
             const uint32_t b = __ballot_sync(kFull, in);
             if (b == 0) continue;
-            if (in) wait[n + __popc(b & ((1u << lane) - 1u))] = static_cast<uint64_t>(o) << 32 | static_cast<uint32_t>(~(id + i));
+            if (in)
+                wait[n + __popc(b & ((1u << lane) - 1u))] =
+                    static_cast<uint64_t>(order_of(x[i])) << 32 | static_cast<uint32_t>(~(id + i));
             n += __popc(b);
             if (n >= 32) flush();
         }
@@ -255,7 +265,7 @@ struct Shared {
     uint64_t top[kMaxWarps][kMaxK];
     float red[kMaxWarps];
     uint64_t wait[kMaxWarps][64];
-    uint32_t least[kMaxWarps], bound;
+    uint32_t least[kMaxK], bound;
     // of the cluster's blocks, in the first one
     float cM[kMaxCluster], cs[kMaxCluster], cu[kMaxCluster];
     uint64_t ctop[kMaxCluster][kMaxK];
@@ -360,19 +370,28 @@ __global__ void __launch_bounds__(CLUSTER ? kClusterThreads : kRowThreads, CLUST
         acc.add(r, c);
         if (TOP) {
             if (v0 == vb) {
-                // block-uniform: the first batch bounds the K-th largest from below. Each of the warps has `r` threads
-                // whose largest logits are at least its r-th largest of those, together K or more
-                uint32_t o = order_of(most), m = 0;
-                for (int r = (a.K + kWarps - 1) / kWarps; r; --r) {
-                    m = __reduce_max_sync(kFull, o);
+                // block-uniform: the first batch bounds the K-th largest from below by the K-th largest of 32 of its
+                // logits, the largest of those threads of each warp that hold the warp's largest
+                constexpr int kEach = kMaxK / kWarps;
+                uint32_t o = order_of(most);
+#pragma unroll
+                for (int r = 0; r < kEach; ++r) {
+                    const uint32_t m = __reduce_max_sync(kFull, o);
                     if (__ffs(__ballot_sync(kFull, o == m)) - 1 == lane) o = 0;
+                    if (lane == 0) sh.least[w * kEach + r] = m;
                 }
-                if (lane == 0) sh.least[w] = m;
                 __syncthreads();
-                top.pass = max(top.pass, __reduce_min_sync(kFull, sh.least[lane % kWarps]));
+                o = sh.least[lane];
+                int above = 0;   // of the 32, those in front of the lane's in descending order
+#pragma unroll
+                for (int l = 0; l < 32; ++l) {
+                    const uint32_t q = __shfl_sync(kFull, o, l);
+                    above += q > o || (q == o && l < lane);
+                }
+                top.raise(__shfl_sync(kFull, o, __ffs(__ballot_sync(kFull, above == a.K - 1)) - 1));
             }
-            top.pass = max(top.pass, *static_cast<volatile uint32_t*>(&sh.bound));
-            if (__any_sync(kFull, order_of(most) >= top.pass)) {
+            top.raise(*static_cast<volatile uint32_t*>(&sh.bound));
+            if (__any_sync(kFull, !(most < top.thr))) {
 #pragma unroll
                 for (int k = 0; k < kBatch; ++k) {
                     const int v = v0 + k * kThreads + threadIdx.x;
