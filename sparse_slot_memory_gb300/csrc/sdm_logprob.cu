@@ -458,12 +458,14 @@ __global__ void __launch_bounds__(CLUSTER ? kClusterThreads : kRowThreads, CLUST
         sub = l2;
         lse = (acc.M + l2) * kLn2;
         H = (l2 - acc.u / acc.s) * kLn2;
+        if (H < 0.f) H = 0.f;   // by rounding, where one logit holds everything
     }
     auto logp_of = [&](float v) {
         if (empty) return -INFINITY;
         if (mul != 0.f) return (v - ref) * mul - sub;
         const float t = fmaf(v, c, -acc.M) - sub;
-        return t < kStart ? v * a.scale - lse : t * kLn2;   // a masked logit's t may have overflowed
+        if (t < kStart) return v * a.scale - lse;   // a masked logit's t may have overflowed
+        return t > 0.f ? 0.f : t * kLn2;            // M and the logit's product round apart: never above 0
     };
     if (threadIdx.x == 0) {
         const int t = __ldg(a.targets + row);
