@@ -330,7 +330,7 @@ __global__ void __launch_bounds__(Split<ROWS>::kThreads, 2) glr_fwd_kernel(const
     const int p = part.p;
     const int64_t b = part.b, n = part.n;
     Quad h = quad(0.f);   // the state before the step's rows
-    if (part.k > 0)
+    if (part.of > 1)   // a segment's, its first one's too: h0 may be hT, which another block writes
         h = kept(static_cast<const XT*>(a.y) + b * a.y_ld + tl.col, a.y_ld, 2);
     else if (a.h0 != nullptr)
         h = quad(load4(a.h0 + static_cast<int64_t>(p) * a.D + tl.col));
@@ -462,7 +462,7 @@ __global__ void __launch_bounds__(Split<ROWS>::kThreads, 2) glr_bwd_kernel(const
     const int p = part.p;
     const int64_t b = part.b, n = part.n;
     Quad m = quad(0.f);   // the gradient of the state after the step's rows
-    if (part.k + 1 < part.of)
+    if (part.of > 1)
         m = kept(static_cast<const XT*>(a.dx) + b * a.dx_ld + tl.col, a.dx_ld, 2);
     else if (a.dhT != nullptr)
         m = quad(load4(a.dhT + static_cast<int64_t>(p) * a.D + tl.col));
@@ -635,6 +635,7 @@ __global__ void __launch_bounds__(128) glr_chain_kernel(const GlrArgs a) {
     auto segment = [&](int i) { return o + (REVERSE ? of - 1 - i : i) * a.seg * ld; };   // i-th in the walk's order
     Quad h = quad(0.f);
     if (first != nullptr) h = quad(load4(first + static_cast<int64_t>(p) * a.D + q * 4));
+    if (of > 1) keep(segment(0), ld, 2, h);
     for (int i0 = 0; i0 + 1 < of; i0 += kAhead) {
         Quad A[kAhead], B[kAhead];
 #pragma unroll

@@ -181,6 +181,42 @@ def test_two_calls_continue_one():
     check("hT", state, hT, hTe)
 
 
+def test_states_in_place_over_segments():
+    """hT may be h0 also where a sequence is cut into segments that run at once; dh0 in place of dhT likewise."""
+    c = case([9001, 9001], 36, 1, xt="f32")
+    want = run(c)
+    state = c["h0"].clone()
+    states, y, dx, dg = sdm.alloc_glr_states(c["spec"]), *(torch.empty_like(c["x"]) for _ in range(3))
+    sdm.glr_forward(c["spec"], c["x"], c["g"], y, h0=state, hT=state, states=states)
+    grad = c["dhT"].clone()
+    sdm.glr_backward(c["spec"], c["x"], c["g"], c["dy"], states, dx, dg, dhT=grad, dh0=grad)
+    for a, b in ((y, "y"), (state, "hT"), (dx, "dx"), (dg, "dg"), (grad, "dh0")):
+        assert torch.equal(a, want[b]), b
+
+
+def test_rows_past_32_bits():
+    """More than 2^31 elements: the last sequence's rows lie behind them."""
+    P, T, D = 2700, 100, 8192
+    spec = sdm.GlrSpec(P=P, rows=P * T, D=D, gate_width=D, x_dtype="bf16", g_dtype="f32")
+    x = torch.empty(P * T, D, dtype=torch.bfloat16, device="cuda").normal_()
+    g = torch.nn.functional.logsigmoid(torch.empty(P * T, 1, device="cuda").normal_() + 3)
+    y, hT, states = torch.empty_like(x), torch.empty(P, D, device="cuda"), sdm.alloc_glr_states(spec)
+    sdm.glr_forward(spec, x, g, y, hT=hT, states=states)
+    dx, dg = torch.empty_like(x), torch.empty_like(g)
+    sdm.glr_backward(spec, x, g, x, states, dx, dg, sdm.alloc_glr_workspace(spec))
+    for p in (0, P // 2, P - 1):
+        r = slice(p * T, (p + 1) * T)
+        cols = slice(D - 40, D)
+        xs, gs = f64(x[r]), f64(g[r])
+        zero, cuts = np.zeros((1, D)), np.array([0, T])
+        h, he, last, laste = glr_forward(xs, gs, cuts, zero, D)
+        ddx, ddxe, ddg, ddge, _, _ = glr_backward(xs, gs, cuts, zero, D, xs, zero)
+        check("y", y[r, cols], h[:, cols], he[:, cols], torch.bfloat16)
+        check("hT", hT[p:p + 1, cols], last[:, cols], laste[:, cols])
+        check("dx", dx[r, cols], ddx[:, cols], ddxe[:, cols], torch.bfloat16)
+        check("dg", dg[r], ddg, ddge)
+
+
 def test_offsets_beyond_the_rows_are_cut_and_reported():
     c = case([50, 60], 8, 1, xt="f32")
     c["offsets"] = torch.tensor([0, 50, 400], dtype=torch.int64, device="cuda")

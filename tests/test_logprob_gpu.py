@@ -178,6 +178,17 @@ def test_gradient_agrees_with_differences():
         assert abs(terms.sum() - want) <= 1e-5 * np.abs(terms).sum()
 
 
+def test_rows_past_32_bits():
+    """More than 2^31 logits: the last rows lie behind them."""
+    N, V = 34000, 65001
+    x = torch.empty(N, V, dtype=torch.bfloat16, device="cuda").normal_().mul_(2)
+    t = targets(N, V)
+    r = run(x, t, 3)
+    at = [0, N // 2, N - 2, N - 1]
+    part = {k: v[at] if isinstance(v, torch.Tensor) else v for k, v in r.items()}
+    compare(x[at], t[at], 3, 1.0, part)
+
+
 def test_rows_of_the_gradient_that_lie_differently():
     """The gradient's rows on another 16-byte offset than the logits'."""
     x, t = logits(5, 1001, "bf16", pad=7), targets(5, 1001)
