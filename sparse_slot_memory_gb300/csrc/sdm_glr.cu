@@ -407,11 +407,13 @@ __global__ void __launch_bounds__(Split<ROWS>::kThreads, 2) glr_fwd_kernel(const
             forget(gr);
             forget(xr);
         }
-        if (live == ROWS && tl.full) {
+        if (live == ROWS) {
+            if (tl.on) {
 #pragma unroll
-            for (int i = 0; i < ROWS; ++i) {
-                hw = fma4(gr[i].exps(), hw, quad(xr[i]));
-                st4(y + i * a.y_ld, hw);
+                for (int i = 0; i < ROWS; ++i) {
+                    hw = fma4(gr[i].exps(), hw, quad(xr[i]));
+                    st4(y + i * a.y_ld, hw);
+                }
             }
         } else {
 #pragma unroll
@@ -617,40 +619,59 @@ __global__ void __launch_bounds__(256, 2) glr_pair_kernel(const GlrArgs a) {
     keep(o, REVERSE ? a.dx_ld : a.y_ld, 1, B);
 }
 
-// From the pairs, the state before (backward: the state's gradient behind) every segment, kept beside them. A thread
-// four channels of a sequence, kAhead segments' pairs on their way at once.
+// From the pairs, the state before (backward: the state's gradient behind) every segment, kept beside them. A block has
+// 32 lanes of four channels of a sequence and kChain rows of threads that take a share of the segments each: they join
+// their share's pairs, meet, and walk it again from their own start.
+constexpr int kChain = 8;
+
 template <typename XT, bool REVERSE>
-__global__ void __launch_bounds__(128) glr_chain_kernel(const GlrArgs a) {
-    constexpr int kAhead = 16;
+__global__ void __launch_bounds__(32 * kChain) glr_chain_kernel(const GlrArgs a) {
+    constexpr int kAhead = 8;   // pairs on their way at once
+    __shared__ Quad sA[kChain][32], sB[kChain][32];
     start_dependent();
-    const int quads = a.D / 4, blocks = (quads + 127) / 128, p = blockIdx.x / blocks;
-    const int q = (blockIdx.x - p * blocks) * 128 + threadIdx.x;
-    if (q >= quads) return;
+    const int quads = a.D / 4, blocks = (quads + 31) / 32, p = blockIdx.x / blocks;
+    const int lane = threadIdx.x, share = threadIdx.y;
+    const int q = min((blockIdx.x - p * blocks) * 32 + lane, quads - 1);
+    const bool on = (blockIdx.x - p * blocks) * 32 + lane < quads;
     int64_t b, n;
     sequence(a, p, b, n);
     const int of = static_cast<int>(max(n / a.seg, int64_t(1)));
+    if (of == 1) return;   // block-uniform
     const int64_t ld = REVERSE ? a.dx_ld : a.y_ld;
     const float* const first = REVERSE ? a.dhT : a.h0;
     XT* const o = static_cast<XT*>(REVERSE ? a.dx : a.y) + b * ld + q * 4;
     auto segment = [&](int i) { return o + (REVERSE ? of - 1 - i : i) * a.seg * ld; };   // i-th in the walk's order
+    const int each = (of - 1 + kChain - 1) / kChain, from = share * each, to = min(of - 1, from + each);
+    auto walk = [&](auto use) {
+        for (int i0 = from; i0 < to; i0 += kAhead) {
+            Quad A[kAhead], B[kAhead];
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i)
+                if (i0 + i < to) {
+                    A[i] = kept(segment(i0 + i), ld, 0);
+                    B[i] = kept(segment(i0 + i), ld, 1);
+                }
+#pragma unroll
+            for (int i = 0; i < kAhead; ++i)
+                if (i0 + i < to) use(i0 + i, A[i], B[i]);
+        }
+    };
+    Quad A = quad(1.f), B = quad(0.f);
+    walk([&](int, const Quad& x, const Quad& y) {
+        B = fma4(x, B, y);
+        A = mul4(x, A);
+    });
+    sA[share][lane] = A;
+    sB[share][lane] = B;
+    __syncthreads();
     Quad h = quad(0.f);
     if (first != nullptr) h = quad(load4(first + static_cast<int64_t>(p) * a.D + q * 4));
-    if (of > 1) keep(segment(0), ld, 2, h);
-    for (int i0 = 0; i0 + 1 < of; i0 += kAhead) {
-        Quad A[kAhead], B[kAhead];
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-            if (i0 + i + 1 >= of) break;
-            A[i] = kept(segment(i0 + i), ld, 0);
-            B[i] = kept(segment(i0 + i), ld, 1);
-        }
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-            if (i0 + i + 1 >= of) break;
-            h = fma4(A[i], h, B[i]);
-            keep(segment(i0 + i + 1), ld, 2, h);
-        }
-    }
+    if (share == 0 && on) keep(segment(0), ld, 2, h);
+    for (int k = 0; k < share; ++k) h = fma4(sA[k][lane], h, sB[k][lane]);
+    walk([&](int i, const Quad& x, const Quad& y) {
+        h = fma4(x, h, y);
+        if (on) keep(segment(i + 1), ld, 2, h);
+    });
 }
 
 // dg of a head wider than a tile: the sum of its tiles' parts, in tile order.
@@ -839,8 +860,8 @@ extern "C" sdm_status sdm_glr_forward(const sdm_glr_shape* shape, const void* x,
             using X = decltype(xt);
             cudaError_t e = launch_dependent(glr_pair_kernel<X, decltype(gt), PC, false>, dim3(units), dim3(256), 0, cs, a);
             if (e == cudaSuccess)
-                e = launch_dependent(glr_chain_kernel<X, false>, dim3(static_cast<unsigned>(a.P) * ((a.D / 4 + 127) / 128)), dim3(128),
-                                     0, cs, a);
+                e = launch_dependent(glr_chain_kernel<X, false>, dim3(static_cast<unsigned>(a.P) * ((a.D / 4 + 31) / 32)), dim3(32, kChain), 0,
+                                     cs, a);
             if (e != cudaSuccess) return e;
         }
         const dim3 grid(units * a.cluster), block(Split<R>::kThreads);
@@ -889,8 +910,8 @@ extern "C" sdm_status sdm_glr_backward(const sdm_glr_shape* shape, const void* x
             using X = decltype(xt);
             cudaError_t e = launch_dependent(glr_pair_kernel<X, decltype(gt), PC, true>, dim3(units), dim3(256), 0, cs, a);
             if (e == cudaSuccess)
-                e = launch_dependent(glr_chain_kernel<X, true>, dim3(static_cast<unsigned>(a.P) * ((a.D / 4 + 127) / 128)), dim3(128),
-                                     0, cs, a);
+                e = launch_dependent(glr_chain_kernel<X, true>, dim3(static_cast<unsigned>(a.P) * ((a.D / 4 + 31) / 32)), dim3(32, kChain), 0,
+                                     cs, a);
             if (e != cudaSuccess) return e;
         }
         const dim3 grid(units * a.cluster), block(Split<R>::kThreads);
