@@ -367,7 +367,8 @@ sdm_status sdm_gds(const sdm_shape* shape, int32_t grad_dtype, const int32_t* so
  * reproducible) and differ in these:
  *   - Row arrays take the distance between rows in elements (`*_ld`), so that a slice of a wider row
  *     can be passed. Inputs may repeat a row (ld 0). A base and its ld are aligned to 4 elements of the
- *     array's type unless said otherwise; small float arrays (weights, states, tables) to 16 bytes.
+ *     array's type unless said otherwise; states, tables and head weights to 16 bytes; the other small arrays to
+ *     their elements.
  *   - An output overlaps no input unless said otherwise.
  *   - Row counts may be 0: nothing is read or written but what is said to be.
  *   - status (nullable): a device word to which SDM_DEV_* bits are OR-ed.

@@ -727,6 +727,7 @@ __global__ void __launch_bounds__(256) glr_step_kernel(const StepArgs a) {
 
 // ---- host side ------------------------------------------------------------------------------------
 using checks::aligned16;
+using checks::aligned_all;
 
 int elem(int dtype) { return dtype == SDM_BF16 ? 2 : 4; }
 
@@ -843,8 +844,7 @@ extern "C" sdm_status sdm_glr_forward(const sdm_glr_shape* shape, const void* x,
         if ((st = check_rows(g, g_ld, shape->D / shape->gate_width, shape->g_dtype, pc, false)) != SDM_OK) return st;
         if ((st = check_rows(y, y_ld, shape->D, shape->x_dtype, true, true)) != SDM_OK) return st;
     }
-    for (const void* p : {static_cast<const void*>(h0), static_cast<const void*>(hT), static_cast<const void*>(states)})
-        if (!aligned16(p)) return SDM_ERR_ALIGN;
+    if (!aligned_all(16, {h0, hT, states}) || !aligned_all(8, {offsets}) || !aligned_all(4, {status})) return SDM_ERR_ALIGN;
     GlrArgs a;
     geometry(shape, &a);
     if (static_cast<int64_t>(a.tiles) * (a.P + a.rows / SDM_GLR_CHUNK) > 0x7FFFFFFF / kMaxCluster) return SDM_ERR_SHAPE;
@@ -890,8 +890,7 @@ extern "C" sdm_status sdm_glr_backward(const sdm_glr_shape* shape, const void* x
         if ((st = check_rows(dg, dg_ld, H, shape->g_dtype, pc, true)) != SDM_OK) return st;
         if (states == nullptr) return SDM_ERR_ARG;
     }
-    for (const void* p : {static_cast<const void*>(states), static_cast<const void*>(dhT), static_cast<const void*>(dh0)})
-        if (!aligned16(p)) return SDM_ERR_ALIGN;
+    if (!aligned_all(16, {states, dhT, dh0}) || !aligned_all(8, {offsets}) || !aligned_all(4, {status})) return SDM_ERR_ALIGN;
     GlrArgs a;
     geometry(shape, &a);
     if (static_cast<int64_t>(a.tiles) * (a.P + a.rows / SDM_GLR_CHUNK) > 0x7FFFFFFF / kMaxCluster) return SDM_ERR_SHAPE;
@@ -934,6 +933,7 @@ extern "C" sdm_status sdm_glr_step(const sdm_glr_shape* shape, const void* x, in
     if (st != SDM_OK) return st;
     if (states < 0 || (slots == nullptr && states < shape->rows)) return SDM_ERR_SHAPE;
     if (shape->rows == 0) return SDM_OK;
+    if (!aligned_all(4, {slots, status})) return SDM_ERR_ALIGN;
     if ((st = check_rows(x, x_ld, shape->D, shape->x_dtype, true, false)) != SDM_OK) return st;
     if ((st = check_rows(g, g_ld, shape->D / shape->gate_width, shape->g_dtype, shape->gate_width == 1, false)) != SDM_OK)
         return st;

@@ -598,6 +598,7 @@ extern "C" sdm_status sdm_token_logprobs(const sdm_logprob_shape* shape, const v
     if (shape->rows == 0) return SDM_OK;
     if ((st = check_logits(shape, logits, ld, false)) != SDM_OK) return st;
     if (targets == nullptr || logp == nullptr) return SDM_ERR_ARG;
+    if (!checks::aligned_all(4, {targets, logp, entropy, lse, top_vals, top_idx, status})) return SDM_ERR_ALIGN;
     LpArgs a;
     memset(&a, 0, sizeof(a));
     a.logits = logits; a.ld = ld; a.targets = targets; a.logp = logp; a.entropy = entropy; a.lse = lse;
@@ -631,6 +632,7 @@ extern "C" sdm_status sdm_token_logprobs_backward(const sdm_logprob_shape* shape
     if ((st = check_logits(shape, logits, ld, false)) != SDM_OK) return st;
     if ((st = check_logits(shape, dlogits, d_ld, true)) != SDM_OK) return st;
     if (targets == nullptr || lse == nullptr || entropy == nullptr || d_logp == nullptr) return SDM_ERR_ARG;
+    if (!checks::aligned_all(4, {targets, lse, entropy, d_logp, d_entropy, status})) return SDM_ERR_ALIGN;
     LpArgs a;
     memset(&a, 0, sizeof(a));
     a.logits = logits; a.ld = ld; a.targets = targets; a.lse_in = lse; a.ent_in = entropy; a.d_logp = d_logp;

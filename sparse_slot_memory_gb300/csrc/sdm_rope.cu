@@ -426,6 +426,7 @@ __global__ void __launch_bounds__(256) rope_table_kernel(const __grid_constant__
 
 // ---- host side ------------------------------------------------------------------------------------
 using checks::aligned16;
+using checks::aligned_all;
 
 sdm_status check(const sdm_rope_shape* s) {
     if (s == nullptr) return SDM_ERR_ARG;
@@ -537,7 +538,7 @@ extern "C" sdm_status sdm_qk_norm_rope(const sdm_rope_shape* shape, const void* 
     if ((st = check_heads(shape, k, k_ld, shape->k_heads, false)) != SDM_OK) return st;
     if ((st = check_heads(shape, q_out, qo_ld, shape->q_heads, true)) != SDM_OK) return st;
     if ((st = check_heads(shape, k_out, ko_ld, shape->k_heads, true)) != SDM_OK) return st;
-    if (!aligned16(table) || !aligned16(wq) || !aligned16(wk)) return SDM_ERR_ALIGN;
+    if (!aligned_all(16, {table, wq, wk}) || !aligned_all(4, {positions, status})) return SDM_ERR_ALIGN;
     RopeArgs a;
     fill(shape, &a);
     a.q = q; a.q_ld = q_ld; a.k = k; a.k_ld = k_ld; a.pos = positions; a.table = table; a.wq = wq; a.wk = wk;
@@ -570,7 +571,7 @@ extern "C" sdm_status sdm_qk_norm_rope_backward(const sdm_rope_shape* shape, con
         if ((st = check_heads(shape, dq, dq_ld, shape->q_heads, true)) != SDM_OK) return st;
         if ((st = check_heads(shape, dk, dk_ld, shape->k_heads, true)) != SDM_OK) return st;
     }
-    if (!aligned16(table) || !aligned16(wq) || !aligned16(wk)) return SDM_ERR_ALIGN;
+    if (!aligned_all(16, {table, wq, wk}) || !aligned_all(4, {positions, status, dwq, dwk})) return SDM_ERR_ALIGN;
     const bool sums = shape->norm && (dwq != nullptr || dwk != nullptr);
     if (sums && (ws == nullptr || !aligned16(ws) || ws_bytes < sdm_rope_workspace_bytes(shape))) return SDM_ERR_WORKSPACE;
     RopeArgs a;

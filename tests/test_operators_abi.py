@@ -140,6 +140,31 @@ def test_logprob_arrays(lib):
     assert b(s, A, 100, A, A, A, A, None, A + 2, 100, None, None) == -4
 
 
+def test_misaligned_small_arrays(lib):
+    """Arrays of ids, offsets, scalars per row and the status word off their elements' alignment."""
+    f = lib.sdm_glr_forward
+    assert f(glr(), A, 256, A, 256, A + 4, None, A, 256, None, None, None, None) == -4
+    assert f(glr(), A, 256, A, 256, None, None, A, 256, None, None, A + 2, None) == -4
+    assert lib.sdm_glr_backward(glr(), A, 256, A, 256, A, 256, A + 4, A, None, A, 256, A, 256, None, None, 0, None, None) == -4
+    assert lib.sdm_glr_step(glr(), A, 256, A, 256, A + 2, A, 256, 100, A, 256, None, None) == -4
+    r = lib.sdm_qk_norm_rope
+    assert r(rope(), A, 256, A, 128, A + 2, A, A, A, A, 256, A, 128, None, None) == -4
+    assert r(rope(), A, 256, A, 128, A, A, A, A, A, 256, A, 128, A + 1, None) == -4
+    b = lib.sdm_qk_norm_rope_backward
+    assert b(rope(), A, 256, A, 128, A, 256, A, 128, A, A, A, A, A, 256, A, 128, A + 2, A, A, 1 << 20, None, None) == -4
+    p, q = lib.sdm_token_logprobs, lib.sdm_token_logprobs_backward
+    good = [A, A, A, A, A, A, None]   # targets, logp, entropy, lse, top_vals, top_idx, status
+    for i in range(7):
+        bad = list(good)
+        bad[i] = A + 2
+        assert p(lp(), A, 100, *bad, None) == -4, i
+    good = [A, A, A, A, A]   # targets, lse, entropy, d_logp, d_entropy
+    for i in range(5):
+        bad = list(good)
+        bad[i] = A + 2
+        assert q(lp(), A, 100, *bad, A, 100, None, None) == -4, i
+
+
 def test_structs_match_the_header(lib):
     """The binding's structs have the header's fields in its order."""
     import os
