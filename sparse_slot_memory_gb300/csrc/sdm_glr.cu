@@ -7,9 +7,25 @@
 // m_t = a_t l_t what flows to h_{t-1}, l_t = dy_t + m_{t+1}, dx_t = l_t, dg_t = m_t h_{t-1}. States, products
 // and sums are float32.
 //
-// Layout. A block owns a tile of at most 128 channels (4 per lane) of one sequence and walks it in steps of
-// kWarps * kRows rows: each warp holds kRows consecutive rows in registers, forms its pair, the warps exchange
-// pairs through shared memory and each then runs its rows from its own starting state. One pass over the data.
+// Layout. A block owns a tile of at most 128 channels (4 per lane; whole heads where gates are per head) of one
+// sequence and walks it in steps of 64 rows: each of its 8 warps holds 8 consecutive rows in registers, forms their
+// pair, the warps exchange pairs through shared memory and each then runs its rows again from its own starting state.
+// The data are read once. Sequences long against the number of tiles are walked by clusters of 2, 4 or 8 blocks, whose
+// pairs meet through each other's shared memory, one cluster barrier a step; and where even that leaves SMs idle they
+// are cut into segments (`divide` has the rule): one kernel forms the segments' pairs, one chains them, and then every
+// segment is walked on its own, the inputs read twice. The values between the three kernels lie in the first rows of
+// the segments' own outputs, so no workspace is needed.
+//
+// The backward walks the steps from the end. It computes the states inside a step again from the saved state at its
+// start, so it reads x instead of y: the same bytes, and no rounding of y in the gradients. A gate per head sums its
+// channels' products over the lanes (and, for heads wider than a tile, over tiles in order in a second kernel).
+//
+// Bound by HBM in principle (6 bytes a bfloat16 element forward, 10 backward, 2 flops a byte); in fact by the issue of
+// instructions at the 16 warps an SM that 128 registers allow: one pass holds 8 rows, their gates and the next step's
+// rows. Measured on a GB300 (6.7 TB/s copy): 8 x 8192 x 2048 bfloat16 with a gate per channel, forward 151 us (5.3 TB/s
+// of its bytes), forward and backward 399 us (5.4 TB/s); 1 x 65537 x 512 float32 with gates per head, both, 189 us
+// (671 MB of single reads: 3.5 TB/s; 940 MB moved); 24 ragged sequences, 30011 x 1920, forward 81 us (2.9 TB/s). One
+// token of 64 requests: 7.0 us a call, the host's time for it.
 #include <cuda_bf16.h>
 
 #include <algorithm>

@@ -13,6 +13,11 @@
 // A row is one block's, or where there are fewer rows than the SMs hold blocks, a cluster's: each block takes a part
 // of the row and the first joins their triples and lists through its shared memory.
 //
+// Bound by HBM: a read forward, a read and a write backward. Measured on a GB300 (6.7 TB/s copy): 4096 x 65536 bfloat16,
+// forward and backward 239 us (1.61 GB: 6.7 TB/s); 1000 x 50001 float32 forward 33 us without alternatives (6.0 TB/s), 47
+// with 5, about 85 with 32: more alternatives let more logits past the bound; 500 x 32000 bfloat16 with 20, 28 us. Eight rows of
+// 131072 with 20 alternatives: 11.4 us in clusters of 8 blocks, bound by latency (loads, two list sorts, barriers).
+//
 // A row whose largest logit lies under -1e30 / scale (everything masked, by -inf or by a type's lowest value)
 // leaves s = 0 and takes a second, plain look; so does the backward of a row whose lse is too large for float32
 // differences.

@@ -10,7 +10,13 @@
 // Layout. A head's columns are taken in units of 8 that hold whole pairs: interleaved, columns 8u .. 8u + 7;
 // half, columns 4u .. and rot_dim / 2 + 4u ..; behind rot_dim, 8 columns in a row. A unit's four pairs have the
 // frequencies 4u .. 4u + 3 in either layout. A lane owns the same units of every head it meets, so a token's
-// cosines and sines and the weights stay in registers over the heads of the token.
+// cosines and sines and the weights stay in registers over the heads of the token, up to four of which (two in float32)
+// are on their way at once. Resident blocks walk the tokens; the weights' gradients stay in registers to the end.
+//
+// Bound by HBM: 4 bytes a bfloat16 element forward, 6 backward; the table's 512 bytes a token of 128 columns count
+// little beside the heads. Measured on a GB300 (6.7 TB/s copy), 32768 tokens of 32 + 8 heads of 128 columns, bfloat16,
+// slices of a fused projection: forward 112 us (6.0 TB/s), forward and backward 284 us (5.9 TB/s); 32 tokens: 9.9 us a
+// call, the host's time for it.
 #include <cuda_bf16.h>
 
 #include <algorithm>
