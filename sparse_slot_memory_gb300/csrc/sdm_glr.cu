@@ -402,10 +402,10 @@ __global__ void __launch_bounds__(Split<ROWS>::kThreads, 2) glr_fwd_kernel(const
             }
             cluster_wait();
 #pragma unroll 1
-            for (int k = 0; k < K; ++k) {
-                if (k == rank) hw = h;
-                join(h, &cA[buf][k][lane * 4], &cB[buf][k][lane * 4]);
-            }
+            for (int k = 0; k < rank; ++k) join(h, &cA[buf][k][lane * 4], &cB[buf][k][lane * 4]);
+            hw = h;
+#pragma unroll 1
+            for (int k = rank; k < K; ++k) join(h, &cA[buf][k][lane * 4], &cB[buf][k][lane * 4]);
             if (st != nullptr && w == 0 && tl.on && t < n) st4(st + t / SDM_GLR_CHUNK * a.D, hw);
         } else {
             // the state behind the step before: that step's last warp left it in the shared memory
@@ -534,10 +534,10 @@ __global__ void __launch_bounds__(Split<ROWS>::kThreads, 2) glr_bwd_kernel(const
         for (int j = 0; j < w; ++j) join(h, &sA[buf][j][lane * 4], &sF[buf][j][lane * 4]);
             cluster_wait();
 #pragma unroll 1
-            for (int k = K - 1; k >= 0; --k) {
-                if (k == rank) mw = m;
-                join(m, &cA[buf][k][lane * 4], &cR[buf][k][lane * 4]);
-            }
+            for (int k = K - 1; k > rank; --k) join(m, &cA[buf][k][lane * 4], &cR[buf][k][lane * 4]);
+            mw = m;
+#pragma unroll 1
+            for (int k = rank; k >= 0; --k) join(m, &cA[buf][k][lane * 4], &cR[buf][k][lane * 4]);
         } else {
 #pragma unroll 1
         for (int j = 0; j < w; ++j) join(h, &sA[buf][j][lane * 4], &sF[buf][j][lane * 4]);
