@@ -245,20 +245,29 @@ struct TopList {
         }
         __syncwarp();
     }
-    // N logits of each lane, ids id .. id + N - 1 (those from `end` on are none)
+    // N logits of each lane, ids id .. id + N - 1 (a lane whose id lies at or past `end` has none)
     template <int N>
     __device__ __forceinline__ void offer(const float (&x)[N], float most, int id, int end) {
         const float bar = thr;
         const bool want = id < end && !(most < bar);
         if (!__any_sync(kFull, want)) return;
+        uint32_t mine = 0;   // the lane's logits that enter
+        if (want) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const bool in = want && id + i < end && !(x[i] < bar);
-            const uint32_t b = __ballot_sync(kFull, in);
-            if (b == 0) continue;
-            if (in)
+            for (int i = 0; i < N; ++i) mine |= !(x[i] < bar) ? 1u << i : 0u;
+        }
+        while (true) {   // one logit of each lane that has one left, room for 32 of them behind the 31 that may wait
+            const uint32_t b = __ballot_sync(kFull, mine != 0);
+            if (b == 0) break;
+            if (mine != 0) {
+                const int i = __ffs(mine) - 1;
+                mine &= mine - 1;
+                float v = x[0];
+#pragma unroll
+                for (int k = 1; k < N; ++k) v = i == k ? x[k] : v;
                 wait[n + __popc(b & ((1u << lane) - 1u))] =
-                    static_cast<uint64_t>(order_of(x[i])) << 32 | static_cast<uint32_t>(~(id + i));
+                    static_cast<uint64_t>(order_of(v)) << 32 | static_cast<uint32_t>(~(id + i));
+            }
             n += __popc(b);
             if (n >= 32) flush();
         }
