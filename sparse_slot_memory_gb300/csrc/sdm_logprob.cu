@@ -396,13 +396,19 @@ __global__ void __launch_bounds__(CLUSTER ? kClusterThreads : kRowThreads, CLUST
                 }
                 __syncthreads();
                 o = sh.least[lane];
-                int above = 0;   // of the 32, those in front of the lane's in descending order
-#pragma unroll
-                for (int l = 0; l < 32; ++l) {
-                    const uint32_t q = __shfl_sync(kFull, o, l);
-                    above += q > o || (q == o && l < lane);
+                uint32_t kth = 0;
+                if (a.K <= kMaxK / 2) {   // taken away from the top, or from the bottom
+                    for (int r = 0; r < a.K; ++r) {
+                        kth = __reduce_max_sync(kFull, o);
+                        if (__ffs(__ballot_sync(kFull, o == kth)) - 1 == lane) o = 0;
+                    }
+                } else {
+                    for (int r = kMaxK; r >= a.K; --r) {
+                        kth = __reduce_min_sync(kFull, o);
+                        if (__ffs(__ballot_sync(kFull, o == kth)) - 1 == lane) o = 0xFFFFFFFFu;
+                    }
                 }
-                top.raise(__shfl_sync(kFull, o, __ffs(__ballot_sync(kFull, above == a.K - 1)) - 1));
+                top.raise(kth);
             }
             top.raise(*static_cast<volatile uint32_t*>(&sh.bound));
             if (__any_sync(kFull, !(most < top.thr))) {
