@@ -34,7 +34,9 @@ namespace {
 using namespace rows;
 
 constexpr int kThreads = 256;
-constexpr int kFwdBlocks = 3;      // blocks of the forward on an SM
+// Blocks of the forward on an SM: 80 registers hold four bfloat16 heads, 64 two float32 ones (4099 tokens of 32 float32
+// heads of 64: 15.7 us with 3, 15.4 with 4; 32768 tokens of 40 bfloat16 heads of 128: 112 with 3, 115 with 4).
+constexpr int fwd_blocks(bool bf16) { return bf16 ? 3 : 4; }
 constexpr int kMaxHd = 1024;
 constexpr int kMaxFreq = kMaxHd / 2;
 constexpr int kPartBlocks = 304;   // blocks of the backward at most (two for each of 152 SMs): a row of weight gradients each
@@ -202,12 +204,13 @@ struct Walk {
 
 // Groups of `lanes` lanes walk the tokens' heads, up to HU heads of one kind of one token at a time.
 template <typename T, int U, bool INTER>
-__global__ void __launch_bounds__(kThreads, U == 1 ? kFwdBlocks : 1) rope_fwd_kernel(const RopeArgs s, int lanes) {
+__global__ void __launch_bounds__(kThreads, U == 1 ? fwd_blocks(sizeof(T) == 2) : 1) rope_fwd_kernel(const RopeArgs s, int lanes) {
     constexpr int HU = heads_at_once<T, U>();
     start_dependent();
     const int per = kThreads / lanes, cq = (s.Hq + HU - 1) / HU, ct = cq + (s.Hk + HU - 1) / HU;
     const int units = static_cast<int>(s.tokens) * ct, sub = threadIdx.x % lanes;
     const float inv = 1.f / s.hd;
+    const bool all = s.rd == s.hd;   // every column turns
     Place<U> pl;
     pl.set(s, sub, lanes);
     Walk at(blockIdx.x * per + threadIdx.x / lanes, gridDim.x * per, ct);
@@ -219,8 +222,8 @@ __global__ void __launch_bounds__(kThreads, U == 1 ? kFwdBlocks : 1) rope_fwd_ke
         const T* const x = (isq ? static_cast<const T*>(s.q) + t * s.q_ld : static_cast<const T*>(s.k) + t * s.k_ld) + h0 * s.hd;
         T* const y = (isq ? static_cast<T*>(s.qo) + t * s.qo_ld : static_cast<T*>(s.ko) + t * s.ko_ld) + h0 * s.hd;
         const int p = pos;
-        auto body = [&](auto full) {   // full: HU heads of a real token, every column turns
-            constexpr bool FULL = decltype(full)::value;
+        auto body = [&](auto full, auto whole) {   // full: HU heads of a real token; whole: every column turns
+            constexpr bool FULL = decltype(full)::value, WHOLE = decltype(whole)::value;
             Raw4<T> ra[HU][U], rb[HU][U];
 #pragma unroll
             for (int h = 0; h < HU; ++h)
@@ -260,15 +263,17 @@ __global__ void __launch_bounds__(kThreads, U == 1 ? kFwdBlocks : 1) rope_fwd_ke
                 if (!FULL && p < 0) r = 0.f;   // a padding token, not read: zeros
 #pragma unroll
                 for (int i = 0; i < U; ++i) {
-                    const Pairs o = times(turned(pairs<INTER>(ra[h][i], rb[h][i]), wt[i], FULL, pl.f[i] >= 0), r);
+                    const Pairs o = times(turned(pairs<INTER>(ra[h][i], rb[h][i]), wt[i], WHOLE, pl.f[i] >= 0), r);
                     if ((FULL || h < n) && pl.on[i]) st_pairs<INTER>(y + h * s.hd + pl.a[i], y + h * s.hd + pl.b[i], o);
                 }
             }
         };
-        if (__all_sync(kFull, n == HU && p >= 0 && s.rd == s.hd))
-            body(std::true_type{});
+        if (!__all_sync(kFull, n == HU && p >= 0))
+            body(std::false_type{}, std::false_type{});
+        else if (all)
+            body(std::true_type{}, std::true_type{});
         else
-            body(std::false_type{});
+            body(std::true_type{}, std::false_type{});
     }
 }
 
@@ -282,6 +287,7 @@ __global__ void __launch_bounds__(kThreads, U == 1 ? 2 : 1) rope_bwd_kernel(cons
     start_dependent();
     const int per = kThreads / lanes, group = threadIdx.x / lanes, sub = threadIdx.x % lanes;
     const float inv = 1.f / s.hd;
+    const bool all = s.rd == s.hd;   // every column turns
     Place<U> pl;
     pl.set(s, sub, lanes);
     for (int side = 0; side < 2; ++side) {
@@ -306,8 +312,8 @@ __global__ void __launch_bounds__(kThreads, U == 1 ? 2 : 1) rope_bwd_kernel(cons
             const T* const g = G + t * g_ld + h0 * s.hd;
             T* const y = Y + t * y_ld + h0 * s.hd;
             const int p = pos;
-            auto body = [&](auto full) {   // full: HU heads of a real token, every column turns
-                constexpr bool FULL = decltype(full)::value;
+            auto body = [&](auto full, auto whole) {   // full: HU heads of a real token; whole: every column turns
+                constexpr bool FULL = decltype(full)::value, WHOLE = decltype(whole)::value;
                 Raw4<T> ra[HU][U], rb[HU][U], ga[HU][U], gb[HU][U];
 #pragma unroll
                 for (int h = 0; h < HU; ++h)
@@ -338,7 +344,7 @@ __global__ void __launch_bounds__(kThreads, U == 1 ? 2 : 1) rope_bwd_kernel(cons
 #pragma unroll
                     for (int i = 0; i < U; ++i) {
                         const Pairs v = pairs<INTER>(ra[h][i], rb[h][i]);
-                        const Pairs e = turned_back(pairs<INTER>(ga[h][i], gb[h][i]), turn[i], FULL, pl.f[i] >= 0);
+                        const Pairs e = turned_back(pairs<INTER>(ga[h][i], gb[h][i]), turn[i], WHOLE, pl.f[i] >= 0);
                         const float vv = dot(v, v), ev = dot(times(e, wt[i]), v);
                         if (pl.on[i]) {
                             sums[2 * h] += vv;
@@ -359,7 +365,7 @@ __global__ void __launch_bounds__(kThreads, U == 1 ? 2 : 1) rope_bwd_kernel(cons
 #pragma unroll
                     for (int i = 0; i < U; ++i) {
                         const Pairs v = pairs<INTER>(ra[h][i], rb[h][i]);
-                        const Pairs e = times(turned_back(pairs<INTER>(ga[h][i], gb[h][i]), turn[i], FULL, pl.f[i] >= 0), r);
+                        const Pairs e = times(turned_back(pairs<INTER>(ga[h][i], gb[h][i]), turn[i], WHOLE, pl.f[i] >= 0), r);
                         dw[i] = {fma4(e.a, v.a, dw[i].a), fma4(e.b, v.b, dw[i].b)};
                         Pairs d = e;
                         if (s.norm) {
@@ -371,10 +377,12 @@ __global__ void __launch_bounds__(kThreads, U == 1 ? 2 : 1) rope_bwd_kernel(cons
                     }
                 }
             };
-            if (__all_sync(kFull, n == HU && p >= 0 && s.rd == s.hd))
-                body(std::true_type{});
+            if (!__all_sync(kFull, n == HU && p >= 0))
+                body(std::false_type{}, std::false_type{});
+            else if (all)
+                body(std::true_type{}, std::true_type{});
             else
-                body(std::false_type{});
+                body(std::true_type{}, std::false_type{});
         }
         if (s.part == nullptr) continue;
 #pragma unroll
@@ -552,7 +560,7 @@ extern "C" sdm_status sdm_qk_norm_rope(const sdm_rope_shape* shape, const void* 
     const int lanes = head_lanes(shape->hd);
     const int hu = heads_together(shape);
     const int64_t units = shape->tokens * ((a.Hq + hu - 1) / hu + (a.Hk + hu - 1) / hu);
-    const int64_t blocks = std::min<int64_t>((units * lanes + kThreads - 1) / kThreads, 152 * kFwdBlocks);
+    const int64_t blocks = std::min<int64_t>((units * lanes + kThreads - 1) / kThreads, 152 * fwd_blocks(shape->dtype == SDM_BF16));
     const cudaError_t e = by_type(shape, [&](auto t, auto u, auto inter) {
         return launch_dependent(rope_fwd_kernel<decltype(t), decltype(u)::value, decltype(inter)::value>, dim3(static_cast<unsigned>(blocks)),
                                 dim3(kThreads), 0, reinterpret_cast<cudaStream_t>(stream), a, lanes);
