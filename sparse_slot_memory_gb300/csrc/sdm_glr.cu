@@ -44,7 +44,7 @@ using namespace rows;
 constexpr int kTileCols = 128;   // channels of a tile
 constexpr int kMaxCluster = 8;
 
-// How a block divides its step of SDM_GLR_CHUNK rows: kRows rows to each of kWarps warps.
+// How a block divides its step of SDM_GLR_CHUNK rows: ROWS rows to each of kWarps warps.
 template <int ROWS>
 struct Split {
     static constexpr int kWarps = SDM_GLR_CHUNK / ROWS, kThreads = kWarps * 32;
@@ -124,7 +124,7 @@ __device__ __forceinline__ void sequence(const GlrArgs& a, int p, int64_t& b, in
         n = a.len;
         return;
     }
-    const int64_t lo = __ldg(a.offsets + p), hi = __ldg(a.offsets + p + 1);
+    const int64_t lo = a.offsets[p], hi = a.offsets[p + 1];
     b = min(max(lo, int64_t(0)), a.rows);
     n = max(min(hi, a.rows) - b, int64_t(0));
     if ((lo < 0 || hi > a.rows || lo > hi) && a.status != nullptr && threadIdx.x == 0) atomicOr(a.status, SDM_DEV_BAD_OFFSET);
@@ -158,7 +158,7 @@ __device__ __forceinline__ Part part_of(const GlrArgs& a, int id) {
         r.p = id;
         if (a.offsets != nullptr && a.P <= 32 && a.P > 1) {
             // the longest sequences first: lane p counts those before sequence p
-            const int64_t mine = lane < a.P ? __ldg(a.offsets + lane + 1) - __ldg(a.offsets + lane) : -1;
+            const int64_t mine = lane < a.P ? a.offsets[lane + 1] - a.offsets[lane] : -1;
             int before = 0;
             for (int q = 0; q < a.P; ++q) {
                 const int64_t other = __shfl_sync(kFull, mine, q);
@@ -175,7 +175,7 @@ __device__ __forceinline__ Part part_of(const GlrArgs& a, int id) {
         int lo = 0, hi = a.P;   // in [lo, hi)
         while (hi - lo > 1) {
             const int w = (hi - lo + 31) / 32, q = lo + (lane + 1) * w;
-            const bool le = q < hi && min(max(__ldg(a.offsets + q), int64_t(0)), a.rows) / a.seg + q <= id;
+            const bool le = q < hi && min(max(a.offsets[q], int64_t(0)), a.rows) / a.seg + q <= id;
             const int c = __popc(__ballot_sync(kFull, le));
             lo += c * w;
             hi = min(hi, lo + w);
@@ -232,7 +232,7 @@ struct RawGate;
 template <typename GT>
 struct RawGate<GT, true> {
     Raw4<GT> v;
-    __device__ __forceinline__ void ld(const GT* p) { v.ld(p); }
+    __device__ __forceinline__ void ld_plain(const GT* p) { v.ld_plain(p); }
     __device__ __forceinline__ void zero() { v.zero(); }
     __device__ __forceinline__ Quad exps() const {
         float o[4];
@@ -245,7 +245,7 @@ struct RawGate<GT, true> {
 template <typename GT>
 struct RawGate<GT, false> {
     GT v;
-    __device__ __forceinline__ void ld(const GT* p) { v = __ldg(p); }
+    __device__ __forceinline__ void ld_plain(const GT* p) { v = *p; }
     __device__ __forceinline__ void zero() { v = GT(0.f); }
     __device__ __forceinline__ Quad exps() const { return quad(exp2_gate(widen(v) * kLog2e)); }
 };
@@ -255,12 +255,12 @@ template <int ROWS, typename Row, typename T>
 __device__ __forceinline__ void load_rows(Row (&r)[ROWS], const T* p, int64_t ld, int live) {
     if (live == ROWS) {   // warp-uniform
 #pragma unroll
-        for (int i = 0; i < ROWS; ++i) r[i].ld(p + i * ld);
+        for (int i = 0; i < ROWS; ++i) r[i].ld_plain(p + i * ld);
     } else {
 #pragma unroll
         for (int i = 0; i < ROWS; ++i) {
             r[i].zero();
-            if (i < live) r[i].ld(p + i * ld);
+            if (i < live) r[i].ld_plain(p + i * ld);
         }
     }
 }
@@ -531,7 +531,7 @@ __global__ void __launch_bounds__(Split<ROWS>::kThreads, 2) glr_bwd_kernel(const
                 cluster_arrive_relaxed();
             }
 #pragma unroll 1
-        for (int j = 0; j < w; ++j) join(h, &sA[buf][j][lane * 4], &sF[buf][j][lane * 4]);
+            for (int j = 0; j < w; ++j) join(h, &sA[buf][j][lane * 4], &sF[buf][j][lane * 4]);
             cluster_wait();
 #pragma unroll 1
             for (int k = K - 1; k > rank; --k) join(m, &cA[buf][k][lane * 4], &cR[buf][k][lane * 4]);
@@ -540,7 +540,7 @@ __global__ void __launch_bounds__(Split<ROWS>::kThreads, 2) glr_bwd_kernel(const
             for (int k = rank; k >= 0; --k) join(m, &cA[buf][k][lane * 4], &cR[buf][k][lane * 4]);
         } else {
 #pragma unroll 1
-        for (int j = 0; j < w; ++j) join(h, &sA[buf][j][lane * 4], &sF[buf][j][lane * 4]);
+            for (int j = 0; j < w; ++j) join(h, &sA[buf][j][lane * 4], &sF[buf][j][lane * 4]);
             if (!first) mw = quad_at(&carry[buf][lane * 4]);
         }
 #pragma unroll 1
@@ -723,8 +723,9 @@ __global__ void __launch_bounds__(256) glr_step_kernel(const StepArgs a) {
     const int quads = a.D / 4;
     const int64_t r = u / quads;
     const int col = static_cast<int>(u - r * quads) * 4;
-    const int64_t s = a.slots == nullptr ? r : static_cast<int64_t>(__ldg(a.slots + r));
-    float x[4], h[4];
+    const int64_t s = a.slots == nullptr ? r : static_cast<int64_t>(a.slots[r]);
+    float h[4];
+    Raw4<XT> x;
     XT* const y = static_cast<XT*>(a.y) + r * a.y_ld + col;
     if (s < 0 || s >= a.states) {   // a padding row, or an id that names no state
         if (s >= a.states && a.status != nullptr) atomicOr(a.status, kDevBadSlot);
@@ -733,9 +734,9 @@ __global__ void __launch_bounds__(256) glr_step_kernel(const StepArgs a) {
     }
     float* const st = a.state + s * a.s_ld + col;
     ld4cg(st, h);
-    ld4(static_cast<const XT*>(a.x) + r * a.x_ld + col, x);
+    x.ld_plain(static_cast<const XT*>(a.x) + r * a.x_ld + col);
     RawGate<GT, PERCH> gr;
-    gr.ld(static_cast<const GT*>(a.g) + r * a.g_ld + (PERCH ? col : col / a.gw));
+    gr.ld_plain(static_cast<const GT*>(a.g) + r * a.g_ld + (PERCH ? col : col / a.gw));
     const Quad o = fma4(gr.exps(), quad(h), quad(x));
     st4(st, o);
     st4(y, o);

@@ -99,7 +99,7 @@ template <>
 struct Vec<float> {
     static constexpr int n = 4;
     float4 v;
-    __device__ __forceinline__ void ld(const float* p) { v = __ldg(reinterpret_cast<const float4*>(p)); }
+    __device__ __forceinline__ void ld(const float* p) { v = *reinterpret_cast<const float4*>(p); }
     __device__ __forceinline__ void none() { v = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY); }
     __device__ __forceinline__ void get(float (&o)[4]) const { o[0] = v.x; o[1] = v.y; o[2] = v.z; o[3] = v.w; }
     __device__ __forceinline__ float most() const { return max_nan(max_nan(v.x, v.y), max_nan(v.z, v.w)); }
@@ -113,7 +113,7 @@ template <>
 struct Vec<__nv_bfloat16> {
     static constexpr int n = 8;
     uint4 v;
-    __device__ __forceinline__ void ld(const __nv_bfloat16* p) { v = __ldg(reinterpret_cast<const uint4*>(p)); }
+    __device__ __forceinline__ void ld(const __nv_bfloat16* p) { v = *reinterpret_cast<const uint4*>(p); }
     __device__ __forceinline__ void none() { v = make_uint4(0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u, 0xFF80FF80u); }
     __device__ __forceinline__ uint32_t word(int i) const { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
     __device__ __forceinline__ static uint32_t max2(uint32_t a, uint32_t b) {
@@ -359,7 +359,7 @@ __global__ void __launch_bounds__(CLUSTER ? kClusterThreads : kRowThreads, CLUST
     const T* const xv = x + head;
     auto scalars = [&](int b, int e) {   // at most 32 logits, by warp 0
         const int i = b + lane;
-        float v[1] = {i < e ? widen(__ldg(x + i)) : -INFINITY};
+        float v[1] = {i < e ? widen(x[i]) : -INFINITY};
         if (i < e) {
             if (!(v[0] * c <= acc.M)) acc.raise(v[0] * c);
             acc.add(v[0], c);
@@ -488,9 +488,9 @@ __global__ void __launch_bounds__(CLUSTER ? kClusterThreads : kRowThreads, CLUST
         return t > 0.f ? 0.f : t * kLn2;            // M and the logit's product round apart: never above 0
     };
     if (threadIdx.x == 0) {
-        const int t = __ldg(a.targets + row);
+        const int t = a.targets[row];
         if (t >= a.V && a.status != nullptr) atomicOr(a.status, SDM_DEV_BAD_TARGET);
-        a.logp[row] = t >= 0 && t < a.V ? logp_of(widen(__ldg(x + t))) : 0.f;
+        a.logp[row] = t >= 0 && t < a.V ? logp_of(widen(x[t])) : 0.f;
         if (a.entropy != nullptr) a.entropy[row] = H;
         if (a.lse != nullptr) a.lse[row] = lse;
     }
@@ -522,10 +522,10 @@ __global__ void __launch_bounds__(kBwdThreads) lp_bwd_kernel(const LpArgs a, int
 #pragma unroll
     for (int k = 0; k < kBwdVecs; ++k)
         if (v0 + k * kBwdThreads < nvec) r[k].ld(x + head + static_cast<int64_t>(v0 + k * kBwdThreads) * N);
-    const int t = __ldg(a.targets + row);
-    const float dl = t >= 0 && t < a.V ? __ldg(a.d_logp + row) : 0.f;
-    const float dh = a.d_entropy != nullptr ? __ldg(a.d_entropy + row) : 0.f;
-    const float H = __ldg(a.ent_in + row), lse = __ldg(a.lse_in + row);
+    const int t = a.targets[row];
+    const float dl = t >= 0 && t < a.V ? a.d_logp[row] : 0.f;
+    const float dh = a.d_entropy != nullptr ? a.d_entropy[row] : 0.f;
+    const float H = a.ent_in[row], lse = a.lse_in[row];
     if (part == 0 && threadIdx.x == 0 && t >= a.V && a.status != nullptr) atomicOr(a.status, SDM_DEV_BAD_TARGET);
     if (fabsf(lse) >= kFarLse) {
         // block-uniform and rare: z - lse from differences to the largest logit, or (lse -inf) a row of zeros

@@ -180,7 +180,7 @@ constexpr int heads_at_once() {
 
 // The token's position, or -1 for a padding token.
 __device__ __forceinline__ int position(const RopeArgs& s, int t) {
-    const int pos = __ldg(s.pos + t);
+    const int pos = s.pos[t];
     if (pos < s.max_pos) return pos < 0 ? -1 : pos;
     if (s.status != nullptr) atomicOr(s.status, SDM_DEV_BAD_POSITION);
     return -1;

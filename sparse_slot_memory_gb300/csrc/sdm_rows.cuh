@@ -44,7 +44,9 @@ __device__ __forceinline__ void get4(const __nv_bfloat16* p, float (&o)[4]) {
     o[0] = __uint_as_float(v.x << 16); o[1] = __uint_as_float(v.x & 0xFFFF0000u);
     o[2] = __uint_as_float(v.y << 16); o[3] = __uint_as_float(v.y & 0xFFFF0000u);
 }
-// A lane's 4 columns kept in the storage type until used (8 bytes bf16 / 16 bytes f32 of registers).
+// A lane's 4 columns kept in the storage type until used (8 bytes bf16 / 16 bytes f32 of registers). ld_plain is for
+// kernels that start while the kernel before may still write what they read (start_dependent): its wait makes those
+// writes visible to plain loads, while the read-only path asks for data that nothing writes while the kernel runs.
 template <typename T>
 struct Raw4;
 template <>
@@ -53,6 +55,7 @@ struct Raw4<float> {
     __device__ __forceinline__ void zero() { v = make_float4(0.f, 0.f, 0.f, 0.f); }
     __device__ __forceinline__ void ld(const float* p) { v = __ldg(reinterpret_cast<const float4*>(p)); }
     __device__ __forceinline__ void ld_cg(const float* p) { v = __ldcg(reinterpret_cast<const float4*>(p)); }
+    __device__ __forceinline__ void ld_plain(const float* p) { v = *reinterpret_cast<const float4*>(p); }
     __device__ __forceinline__ void get(float (&o)[4]) const { o[0] = v.x; o[1] = v.y; o[2] = v.z; o[3] = v.w; }
     __device__ __forceinline__ float operator[](int i) const { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
 };
@@ -62,6 +65,7 @@ struct Raw4<__nv_bfloat16> {
     __device__ __forceinline__ void zero() { v = make_uint2(0u, 0u); }
     __device__ __forceinline__ void ld(const __nv_bfloat16* p) { v = __ldg(reinterpret_cast<const uint2*>(p)); }
     __device__ __forceinline__ void ld_cg(const __nv_bfloat16* p) { v = __ldcg(reinterpret_cast<const uint2*>(p)); }
+    __device__ __forceinline__ void ld_plain(const __nv_bfloat16* p) { v = *reinterpret_cast<const uint2*>(p); }
     __device__ __forceinline__ void get(float (&o)[4]) const {
         o[0] = __uint_as_float(v.x << 16); o[1] = __uint_as_float(v.x & 0xFFFF0000u);
         o[2] = __uint_as_float(v.y << 16); o[3] = __uint_as_float(v.y & 0xFFFF0000u);
@@ -261,7 +265,7 @@ __device__ __forceinline__ Quad quad(const Raw4<T>& r) {
 }
 __device__ __forceinline__ Raw4<float> load4(const float* p) {
     Raw4<float> r;
-    r.ld(p);
+    r.ld_plain(p);
     return r;
 }
 __device__ __forceinline__ Quad quad_at(const float* p) {   // 16 bytes of shared memory

@@ -217,6 +217,27 @@ def test_rows_past_32_bits():
         check("dg", dg[r], ddg, ddge)
 
 
+def test_many_calls_in_a_row_hand_the_state_on():
+    """Kernels start while the one before still runs: 100 chunks and then 50 single tokens back to back, the state in
+    place, nothing between the calls."""
+    P, D, C, n, m = 3, 516, 40, 100, 50
+    c = case([n * C + m] * P, D, 1, xt="f32", seed=8)
+    x, g, state = c["x"].view(P, -1, D), c["g"].view(P, -1, D), c["h0"].clone()
+    xs = [x[:, i * C:(i + 1) * C].reshape(P * C, D) for i in range(n)] + [x[:, n * C + i].contiguous() for i in range(m)]
+    gs = [g[:, i * C:(i + 1) * C].reshape(P * C, D) for i in range(n)] + [g[:, n * C + i].contiguous() for i in range(m)]
+    ys = [torch.empty_like(v) for v in xs]
+    chunk, one = sdm.GlrSpec(P=P, rows=P * C, D=D, x_dtype="f32"), sdm.GlrSpec(P=P, rows=P, D=D, x_dtype="f32")
+    torch.cuda.synchronize()
+    for i in range(n):
+        sdm.glr_forward(chunk, xs[i], gs[i], ys[i], h0=state, hT=state)
+    for i in range(n, n + m):
+        sdm.glr_step(one, xs[i], gs[i], state, ys[i])
+    h, he, hT, hTe = glr_forward(f64(c["x"]), f64(c["g"]), c["cuts"], f64(c["h0"]), 1)
+    y = torch.cat([v.view(P, -1, D) for v in ys], 1)
+    check("y", y.view(-1, D), h, he)
+    check("state", state, hT, hTe)
+
+
 def test_offsets_beyond_the_rows_are_cut_and_reported():
     c = case([50, 60], 8, 1, xt="f32")
     c["offsets"] = torch.tensor([0, 50, 400], dtype=torch.int64, device="cuda")
