@@ -800,20 +800,21 @@ size_t part_bytes(const GlrArgs& a) {
 // with 8; 8 x 8192 x 2048 bfloat16, forward and backward: 456 us with 1, 397 with 2, 444 with 4). Where 8 are too few
 // and the sequences long, they are cut into segments for two blocks an SM, at the price of reading the inputs twice
 // (1 x 8192 x 1024: 97 us with clusters, 50 with segments; 1 x 4096 x 256: 48 and 47; 65537 x 512 float32: 893 and 192).
+// Unequal lengths count as long four times earlier, again for the longest.
 constexpr int64_t kBusy = 228, kSegmentRows = 256, kLong = 4096;
 
 void divide(GlrArgs* a) {
     const int64_t units = static_cast<int64_t>(a->tiles) * a->P, steps = (a->len + SDM_GLR_CHUNK - 1) / SDM_GLR_CHUNK;
-    const int64_t want = a->offsets == nullptr || a->P == 1 ? kBusy : 4 * kBusy;
+    const int64_t uneven = a->offsets == nullptr || a->P == 1 ? 1 : 4;
     a->cluster = 1;
     a->seg = 0;
-    if (units * kMaxCluster < kBusy && a->len > kLong) {
+    if (units * kMaxCluster < kBusy && a->len * uneven > kLong) {
         const int64_t cuts = 2 * 152 / units;   // of a sequence
         a->seg = std::max(kSegmentRows, (a->len + cuts - 1) / cuts);
         a->seg = (a->seg + SDM_GLR_CHUNK - 1) / SDM_GLR_CHUNK * SDM_GLR_CHUNK;
         return;
     }
-    while (a->cluster < kMaxCluster && units * a->cluster < want && a->cluster < steps) a->cluster *= 2;
+    while (a->cluster < kMaxCluster && units * a->cluster < kBusy * uneven && a->cluster < steps) a->cluster *= 2;
 }
 
 // Parts of the launch.

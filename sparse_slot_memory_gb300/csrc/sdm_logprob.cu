@@ -14,9 +14,10 @@
 // of the row and the first joins their triples and lists through its shared memory.
 //
 // Bound by HBM: a read forward, a read and a write backward. Measured on a GB300 (6.7 TB/s copy): 4096 x 65536 bfloat16,
-// forward and backward 239 us (1.61 GB: 6.7 TB/s); 1000 x 50001 float32 forward 33 us without alternatives (6.0 TB/s), 47
-// with 5, about 85 with 32: more alternatives let more logits past the bound; 500 x 32000 bfloat16 with 20, 28 us. Eight rows of
-// 131072 with 20 alternatives: 11.4 us in clusters of 8 blocks, bound by latency (loads, two list sorts, barriers).
+// forward and backward 238 us (1.61 GB: 6.8 TB/s, the second read partly from the L2); 1000 x 50001 float32 forward 33 us
+// without alternatives (6.0 TB/s), 46 with 5, 65 with 32: more alternatives let more logits past the bound; 500 x 32000
+// bfloat16 10 us without and 18 with 20. Eight rows of 131072 with 20 alternatives: 10.2 us in clusters of 8 blocks, bound
+// by latency (loads, two list sorts, barriers).
 //
 // A row whose largest logit lies under -1e30 / scale (everything masked, by -inf or by a type's lowest value)
 // leaves s = 0 and takes a second, plain look; so does the backward of a row whose lse is too large for float32
@@ -36,13 +37,15 @@ namespace {
 
 using namespace rows;
 
-constexpr int kRowThreads = 256;      // threads of a block that has a row to itself, and of one of a cluster
-constexpr int kClusterThreads = 512;
+// Threads of a block that has a row to itself, four of which share an SM (1000 rows of 50001: 74 us with two of 512 in an
+// earlier form, 59 with four of 256; eight of 128: equal there, 500 rows of 32000 2.4 times slower), and of one of a
+// cluster, where the fewer rows want more threads (8 rows of 131072: 16 us with 256, 13 with 512).
+constexpr int kRowThreads = 256, kClusterThreads = 512;
 constexpr int kMaxWarps = kClusterThreads / 32;
-static_assert(kRowThreads <= 1024 && kClusterThreads <= 1024, "a warp gives at least one of the 32 logits that bound the alternatives");
 constexpr int kRowBlocks = 4;         // blocks of kRowThreads on an SM
 constexpr int kBatch = 4;             // vectors of a thread in flight
 constexpr int kMaxK = 32;
+static_assert(kMaxK * 32 % kRowThreads == 0 && kMaxK * 32 % kClusterThreads == 0, "each warp gives its share of the 32 logits that bound the alternatives");
 constexpr int kMaxCluster = 8;
 constexpr float kLog2e = 1.44269504088896341f;
 constexpr float kLn2 = 0.69314718055994531f;
