@@ -16,7 +16,7 @@
 // Bound by HBM: a read forward, a read and a write backward. Measured on a GB300 (6.7 TB/s copy): 4096 x 65536 bfloat16,
 // forward and backward 238 us (1.61 GB: 6.8 TB/s, the second read partly from the L2); 1000 x 50001 float32 forward 33 us
 // without alternatives (6.0 TB/s), 46 with 5, 65 with 32: more alternatives let more logits past the bound; 500 x 32000
-// bfloat16 10 us without and 18 with 20. Eight rows of 131072 with 20 alternatives: 10.2 us in clusters of 8 blocks, bound
+// bfloat16 10 us without and 18 with 20. Eight rows of 131072 with 20 alternatives: 7.9 us in clusters of 8 blocks, bound
 // by latency (loads, two list sorts, barriers).
 //
 // A row whose largest logit lies under -1e30 / scale (everything masked, by -inf or by a type's lowest value)
@@ -39,7 +39,7 @@ using namespace rows;
 
 // Threads of a block that has a row to itself, four of which share an SM (1000 rows of 50001: 74 us with two of 512 in an
 // earlier form, 59 with four of 256; eight of 128: equal there, 500 rows of 32000 2.4 times slower), and of one of a
-// cluster, where the fewer rows want more threads (8 rows of 131072: 16 us with 256, 13 with 512).
+// cluster, where the fewer rows want more threads (150 rows of 131072: 21.7 us with 256, 18.2 with 512; 8 rows: 8.3 and 7.9).
 constexpr int kRowThreads = 256, kClusterThreads = 512;
 constexpr int kMaxWarps = kClusterThreads / 32;
 constexpr int kRowBlocks = 4;         // blocks of kRowThreads on an SM

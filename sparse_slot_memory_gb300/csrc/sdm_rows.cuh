@@ -45,7 +45,7 @@ __device__ __forceinline__ void get4(const __nv_bfloat16* p, float (&o)[4]) {
     o[2] = __uint_as_float(v.y << 16); o[3] = __uint_as_float(v.y & 0xFFFF0000u);
 }
 // A lane's 4 columns kept in the storage type until used (8 bytes bf16 / 16 bytes f32 of registers). ld_plain is for
-// kernels that start while the kernel before may still write what they read (start_dependent): its wait makes those
+// kernels that may start before the kernel before has written what they read (start_dependent): its wait makes those
 // writes visible to plain loads, while the read-only path asks for data that nothing writes while the kernel runs.
 template <typename T>
 struct Raw4;

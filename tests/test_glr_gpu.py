@@ -218,8 +218,8 @@ def test_rows_past_32_bits():
 
 
 def test_many_calls_in_a_row_hand_the_state_on():
-    """Kernels start while the one before still runs: 100 chunks and then 50 single tokens back to back, the state in
-    place, nothing between the calls."""
+    """Kernels are launched as dependents of the one before: 100 chunks and then 50 single tokens back to back, the state
+    in place, nothing between the calls."""
     P, D, C, n, m = 3, 516, 40, 100, 50
     c = case([n * C + m] * P, D, 1, xt="f32", seed=8)
     x, g, state = c["x"].view(P, -1, D), c["g"].view(P, -1, D), c["h0"].clone()
