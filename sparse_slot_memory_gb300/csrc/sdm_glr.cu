@@ -794,27 +794,33 @@ size_t part_bytes(const GlrArgs& a) {
     return a.tiles_per_head == 1 ? 0 : static_cast<size_t>(a.tiles_per_head) * a.rows * a.H * sizeof(float);
 }
 
-// How the rows are divided. A block alone walks a part where the tiles and sequences give 1.5 blocks an SM (152 of
-// them, kBusy blocks); else clusters of up to 8 do, and sequences of unequal lengths get four times as many blocks,
-// because the longest decides (24 sequences of 0 to 5526 rows, 30011 x 1920: 91 us with 1 block, 85 with 4, 120
-// with 8; 8 x 8192 x 2048 bfloat16, forward and backward: 456 us with 1, 397 with 2, 444 with 4). Where 8 are too few
-// and the sequences long, they are cut into segments for two blocks an SM, at the price of reading the inputs twice
-// (1 x 8192 x 1024: 97 us with clusters, 50 with segments; 1 x 4096 x 256: 48 and 47; 65537 x 512 float32: 893 and 192).
-// Unequal lengths count as long four times earlier, again for the longest.
-constexpr int64_t kBusy = 228, kSegmentRows = 256, kLong = 4096;
+// How the rows are divided: by one block a part, or by clusters of 2, 4 or 8, whichever takes the fewest steps of 64 rows
+// one after another on an SM's two blocks (152 SMs, kSlots blocks at once). Equal sequences: the waves of blocks times the
+// steps of each. Unequal ones, whose lengths the host does not know: the larger of all steps over the slots and of the
+// longest's steps, taken as four times the mean (24 sequences of 0 to 5526 rows, 30011 x 1920: 91 us with 1 block, 85
+// with 4, 120 with 8; 8 x 8192 x 2048 bfloat16, forward and backward: 456 us with 1, 397 with 2, 444 with 4). Where even 8
+// leave SMs idle and the sequences are long, they are cut into segments for two blocks an SM, at the price of reading
+// the inputs twice (1 x 8192 x 1024: 97 us with clusters, 50 with segments; 1 x 4096 x 256: 48 and 47; 65537 x 512
+// float32: 893 and 185), unequal ones four times earlier (8 sequences, 24000 x 256: 148 and 69).
+constexpr int64_t kSlots = 304, kBusy = 228, kSegmentRows = 256, kLong = 4096;
 
 void divide(GlrArgs* a) {
     const int64_t units = static_cast<int64_t>(a->tiles) * a->P, steps = (a->len + SDM_GLR_CHUNK - 1) / SDM_GLR_CHUNK;
-    const int64_t uneven = a->offsets == nullptr || a->P == 1 ? 1 : 4;
+    const bool equal = a->offsets == nullptr || a->P == 1;
     a->cluster = 1;
     a->seg = 0;
-    if (units * kMaxCluster < kBusy && a->len * uneven > kLong) {
-        const int64_t cuts = 2 * 152 / units;   // of a sequence
+    if (units * kMaxCluster < kBusy && a->len * (equal ? 1 : 4) > kLong) {
+        const int64_t cuts = kSlots / units;   // of a sequence
         a->seg = std::max(kSegmentRows, (a->len + cuts - 1) / cuts);
         a->seg = (a->seg + SDM_GLR_CHUNK - 1) / SDM_GLR_CHUNK * SDM_GLR_CHUNK;
         return;
     }
-    while (a->cluster < kMaxCluster && units * a->cluster < kBusy * uneven && a->cluster < steps) a->cluster *= 2;
+    auto cost = [&](int64_t k) {   // in steps
+        if (equal) return static_cast<double>((units * k + kSlots - 1) / kSlots * ((steps + k - 1) / k));
+        return std::max(static_cast<double>(units) * (steps + 0.5 * k) / kSlots, 4.0 * steps / k);
+    };
+    for (int k = 2; k <= kMaxCluster && k <= steps; k *= 2)
+        if (cost(k) < cost(a->cluster)) a->cluster = k;
 }
 
 // Parts of the launch.

@@ -40,12 +40,12 @@ using namespace rows;
 // Threads of a block that has a row to itself, four of which share an SM (1000 rows of 50001: 74 us with two of 512 in an
 // earlier form, 59 with four of 256; eight of 128: equal there, 500 rows of 32000 2.4 times slower), and of one of a
 // cluster, where the fewer rows want more threads (150 rows of 131072: 21.7 us with 256, 18.2 with 512; 8 rows: 8.3 and 7.9).
-constexpr int kRowThreads = 256, kClusterThreads = 512;
-constexpr int kMaxWarps = kClusterThreads / 32;
-constexpr int kRowBlocks = 4;         // blocks of kRowThreads on an SM
+// Short rows of up to kShort bytes, which are no more than two batches of two warps, are taken by blocks of those,
+// sixteen on an SM, because the fixed part of a row (bound, sort, joins) counts most.
+constexpr int kRowThreads = 256, kClusterThreads = 512, kShortThreads = 64, kShort = 8192;
+constexpr int blocks_of(int threads) { return 1024 / threads; }   // on an SM, at 64 registers
 constexpr int kBatch = 4;             // vectors of a thread in flight
 constexpr int kMaxK = 32;
-static_assert(kMaxK * 32 % kRowThreads == 0 && kMaxK * 32 % kClusterThreads == 0, "each warp gives its share of the 32 logits that bound the alternatives");
 constexpr int kMaxCluster = 8;
 constexpr float kLog2e = 1.44269504088896341f;
 constexpr float kLn2 = 0.69314718055994531f;
@@ -277,15 +277,15 @@ struct TopList {
     }
 };
 
+template <int WARPS, int CLUSTER>
 struct Shared {
-    float M[kMaxWarps], s[kMaxWarps], u[kMaxWarps];
-    uint64_t top[kMaxWarps][kMaxK];
-    float red[kMaxWarps];
-    uint64_t wait[kMaxWarps][64];
+    static_assert(kMaxK % WARPS == 0, "each warp gives its share of the 32 logits that bound the alternatives");
+    float M[WARPS], s[WARPS], u[WARPS], red[WARPS];
+    uint64_t top[WARPS][kMaxK], wait[WARPS][64];
     uint32_t least[kMaxK], bound;
     // of the cluster's blocks, in the first one
-    float cM[kMaxCluster], cs[kMaxCluster], cu[kMaxCluster];
-    uint64_t ctop[kMaxCluster][kMaxK];
+    float cM[CLUSTER], cs[CLUSTER], cu[CLUSTER];
+    uint64_t ctop[CLUSTER][kMaxK];
 };
 
 // The lists in rows 0 .. n - 1 (n a power of two, one row a warp) joined into row 0. Block-wide.
@@ -303,9 +303,9 @@ __device__ __forceinline__ void join_lists(uint64_t (*top)[kMaxK], int n, int w,
 }
 
 // The row's largest logit, then sum exp(z - z_max), sum exp(z - z_max) (z - z_max), from differences that hold for
-// any finite logits. Block-wide; every thread gets them.
+// any finite logits. Block-wide, with a float of shared memory for each warp; every thread gets them.
 template <typename T>
-__device__ void plain_stats(const T* x, int V, float scale, Shared& sh, float& m, float& s, float& u) {
+__device__ void plain_stats(const T* x, int V, float scale, float* red, float& m, float& s, float& u) {
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     auto block = [&](float v, bool sum) {
 #pragma unroll
@@ -314,10 +314,10 @@ __device__ void plain_stats(const T* x, int V, float scale, Shared& sh, float& m
             v = sum ? v + o : max_nan(v, o);
         }
         __syncthreads();
-        if (lane == 0) sh.red[w] = v;
+        if (lane == 0) red[w] = v;
         __syncthreads();
-        v = sh.red[0];
-        for (int k = 1; k < static_cast<int>(blockDim.x) / 32; ++k) v = sum ? v + sh.red[k] : max_nan(v, sh.red[k]);
+        v = red[0];
+        for (int k = 1; k < static_cast<int>(blockDim.x) / 32; ++k) v = sum ? v + red[k] : max_nan(v, red[k]);
         return v;
     };
     float most = -INFINITY;
@@ -333,10 +333,10 @@ __device__ void plain_stats(const T* x, int V, float scale, Shared& sh, float& m
     u = block(b, true);
 }
 
-template <typename T, bool TOP, bool CLUSTER>
-__global__ void __launch_bounds__(CLUSTER ? kClusterThreads : kRowThreads, CLUSTER ? 2 : kRowBlocks) lp_fwd_kernel(const LpArgs a) {
-    constexpr int kThreads = CLUSTER ? kClusterThreads : kRowThreads, kWarps = kThreads / 32;
-    __shared__ Shared sh;
+template <typename T, bool TOP, bool CLUSTER, int THREADS>
+__global__ void __launch_bounds__(THREADS, blocks_of(THREADS)) lp_fwd_kernel(const LpArgs a) {
+    constexpr int kThreads = THREADS, kWarps = THREADS / 32;
+    __shared__ Shared<kWarps, CLUSTER ? kMaxCluster : 1> sh;
     if (CLUSTER) cluster_arrive_relaxed();
     start_dependent();
     constexpr int N = Vec<T>::n;
@@ -469,7 +469,7 @@ __global__ void __launch_bounds__(CLUSTER ? kClusterThreads : kRowThreads, CLUST
     bool empty = false;
     if (acc.s == 0.f) {   // block-uniform
         float m, s, u;
-        plain_stats(x, a.V, a.scale, sh, m, s, u);
+        plain_stats(x, a.V, a.scale, sh.red, m, s, u);
         empty = m == -INFINITY;
         ref = m;
         mul = a.scale;
@@ -509,7 +509,7 @@ constexpr int kBwdVecs = 4;   // vectors of a thread
 
 template <typename T>
 __global__ void __launch_bounds__(kBwdThreads) lp_bwd_kernel(const LpArgs a, int parts) {
-    __shared__ Shared sh;
+    __shared__ float red[kBwdThreads / 32];
     start_dependent();
     constexpr int N = Vec<T>::n;
     const int64_t row = blockIdx.x / parts;
@@ -534,7 +534,7 @@ __global__ void __launch_bounds__(kBwdThreads) lp_bwd_kernel(const LpArgs a, int
         // block-uniform and rare: z - lse from differences to the largest logit, or (lse -inf) a row of zeros
         const bool empty = lse == -INFINITY;
         float m = 0.f, s = 1.f, u;
-        if (!isinf(lse)) plain_stats(x, a.V, a.scale, sh, m, s, u);
+        if (!isinf(lse)) plain_stats(x, a.V, a.scale, red, m, s, u);
         const float ls = logf(s);
         const int per = kBwdThreads * kBwdVecs * N;
         for (int i = part * per + threadIdx.x; i < (part + 1 == parts ? a.V : min(a.V, (part + 1) * per)); i += kBwdThreads) {
@@ -631,13 +631,16 @@ extern "C" sdm_status sdm_token_logprobs(const sdm_logprob_shape* shape, const v
     const bool bf = shape->dtype == SDM_BF16;
     a.cluster = cluster_of(shape);
     if (shape->rows * a.cluster > 0x7FFFFFFF) return SDM_ERR_SHAPE;
-    const dim3 grid(static_cast<unsigned>(shape->rows * a.cluster)), block(a.cluster > 1 ? kClusterThreads : kRowThreads);
+    const bool brief = static_cast<int64_t>(shape->V) * (bf ? 2 : 4) <= kShort;
+    const dim3 grid(static_cast<unsigned>(shape->rows * a.cluster));
     const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
     auto run = [&](auto t, auto with_top) {
         using T = decltype(t);
         constexpr bool TOP = decltype(with_top)::value;
-        return a.cluster > 1 ? launch_cluster(lp_fwd_kernel<T, TOP, true>, grid, block, a.cluster, cs, a)
-                             : launch_dependent(lp_fwd_kernel<T, TOP, false>, grid, block, 0, cs, a);
+        if (a.cluster > 1)
+            return launch_cluster(lp_fwd_kernel<T, TOP, true, kClusterThreads>, grid, dim3(kClusterThreads), a.cluster, cs, a);
+        if (brief) return launch_dependent(lp_fwd_kernel<T, TOP, false, kShortThreads>, grid, dim3(kShortThreads), 0, cs, a);
+        return launch_dependent(lp_fwd_kernel<T, TOP, false, kRowThreads>, grid, dim3(kRowThreads), 0, cs, a);
     };
     const std::true_type yes;
     const std::false_type no;
