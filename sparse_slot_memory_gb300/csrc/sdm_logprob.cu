@@ -6,9 +6,10 @@
 // new M when a larger logit comes; the threads' triples join the same way. log p(target) = (t_target - log2 s) ln 2,
 // H = (log2 s - u / s) ln 2. Backward: dz_v = dlogp (1[v = target] - p_v) - dH p_v (log p_v + H).
 //
-// The top alternatives are kept in the same pass: every warp holds its 32 largest (value, id) so far, one in a lane.
-// The block's first batch bounds the K-th largest from below, and what a warp's list holds raises the bound; only
-// logits at least as large are looked at, wait in the shared memory, and join the list sorted, 32 at a time.
+// The top alternatives: the same pass leaves the largest logit of every cell (64 bytes or more of a thread's share) in the
+// shared memory. The K-th largest of 32 of those bounds the K-th largest logit from below; the few cells that hold as
+// large a logit are read again, their logits wait in the shared memory and join their warp's list of the 32 largest
+// (value, id) sorted, 32 at a time, and the warps' lists join by halves.
 //
 // A row is one block's, or where there are fewer rows than the SMs hold blocks, a cluster's: each block takes a part
 // of the row and the first joins their triples and lists through its shared memory.
@@ -46,6 +47,7 @@ constexpr int kRowThreads = 256, kClusterThreads = 512, kShortThreads = 64, kSho
 constexpr int blocks_of(int threads) { return 1024 / threads; }   // on an SM, at 64 registers
 constexpr int kBatch = 4;             // vectors of a thread in flight
 constexpr int kMaxK = 32;
+constexpr int kCells = 16;            // cells of a thread's share of a row
 constexpr int kMaxCluster = 8;
 constexpr float kLog2e = 1.44269504088896341f;
 constexpr float kLn2 = 0.69314718055994531f;
@@ -226,6 +228,12 @@ struct TopList {
 #pragma unroll
         for (int d = 16; d; d >>= 1) step(key, d, true, lane);
     }
+    __device__ __forceinline__ static void sort(uint64_t& c, int lane) {
+#pragma unroll
+        for (int size = 2; size <= 32; size <<= 1)
+#pragma unroll
+            for (int d = size >> 1; d; d >>= 1) step(c, d, (lane & size) == 0, lane);
+    }
     // The first 32 that wait are sorted and join the list.
     __device__ __forceinline__ void flush() {
         __syncwarp();
@@ -234,10 +242,7 @@ struct TopList {
         __syncwarp();
         wait[lane] = rest;
         n = max(0, n - 32);
-#pragma unroll
-        for (int size = 2; size <= 32; size <<= 1)
-#pragma unroll
-            for (int d = size >> 1; d; d >>= 1) step(c, d, (lane & size) == 0, lane);
+        sort(c, lane);
         join(c);
         const uint32_t k = static_cast<uint32_t>(__shfl_sync(kFull, key, K - 1) >> 32);
         if (k != 0) {
@@ -277,12 +282,14 @@ struct TopList {
     }
 };
 
-template <int WARPS, int CLUSTER>
+template <int WARPS, int CLUSTER, bool TOP>
 struct Shared {
     static_assert(kMaxK % WARPS == 0, "each warp gives its share of the 32 logits that bound the alternatives");
     float M[WARPS], s[WARPS], u[WARPS], red[WARPS];
     uint64_t top[WARPS][kMaxK], wait[WARPS][64];
     uint32_t least[kMaxK], bound;
+    int pooled;
+    float cell[TOP ? kCells : 1][WARPS * 32];   // the largest logit of a thread's cell
     // of the cluster's blocks, in the first one
     float cM[CLUSTER], cs[CLUSTER], cu[CLUSTER];
     uint64_t ctop[CLUSTER][kMaxK];
@@ -336,7 +343,7 @@ __device__ void plain_stats(const T* x, int V, float scale, float* red, float& m
 template <typename T, bool TOP, bool CLUSTER, int THREADS>
 __global__ void __launch_bounds__(THREADS, blocks_of(THREADS)) lp_fwd_kernel(const LpArgs a) {
     constexpr int kThreads = THREADS, kWarps = THREADS / 32;
-    __shared__ Shared<kWarps, CLUSTER ? kMaxCluster : 1> sh;
+    __shared__ Shared<kWarps, CLUSTER ? kMaxCluster : 1, TOP> sh;
     if (CLUSTER) cluster_arrive_relaxed();
     start_dependent();
     constexpr int N = Vec<T>::n;
@@ -350,7 +357,10 @@ __global__ void __launch_bounds__(THREADS, blocks_of(THREADS)) lp_fwd_kernel(con
     TopList top;
     top.clear(a.K, lane, sh.wait[w], &sh.bound);
     if (TOP) {
-        if (threadIdx.x == 0) sh.bound = 0;
+        if (threadIdx.x == 0) {
+            sh.bound = 0;
+            sh.pooled = 0;
+        }
         __syncthreads();
     }
     // vectors start at the row's first 16-byte boundary; the logits before it and behind the last vector are
@@ -360,17 +370,26 @@ __global__ void __launch_bounds__(THREADS, blocks_of(THREADS)) lp_fwd_kernel(con
     const int each = CLUSTER ? (nvec + C - 1) / C : nvec;
     const int vb = rank * each, ve = CLUSTER ? min(nvec, vb + each) : nvec;   // this block's vectors
     const T* const xv = x + head;
-    auto scalars = [&](int b, int e) {   // at most 32 logits, by warp 0
-        const int i = b + lane;
-        float v[1] = {i < e ? widen(x[i]) : -INFINITY};
-        if (i < e) {
-            if (!(v[0] * c <= acc.M)) acc.raise(v[0] * c);
-            acc.add(v[0], c);
+    // at most 32 logits, by warp 0: their sums, and as alternatives
+    auto scalar = [&](int b, int e) { return b + lane < e ? widen(x[b + lane]) : -INFINITY; };
+    auto sum_scalars = [&](int b, int e) {
+        const float v = scalar(b, e);
+        if (b + lane < e) {
+            if (!(v * c <= acc.M)) acc.raise(v * c);
+            acc.add(v, c);
         }
-        if (TOP) top.offer<1>(v, v[0], i, e);
     };
-    if (w == 0 && rank == 0) scalars(0, head);
-    for (int v0 = vb; v0 < ve; v0 += kThreads * kBatch) {
+    auto offer_scalars = [&](int b, int e) {
+        const float v[1] = {scalar(b, e)};
+        top.offer<1>(v, v[0], b + lane, e);
+    };
+    const int tail = head + nvec * N;
+    if (w == 0 && rank == 0) sum_scalars(0, head);
+    // a cell of a thread: its vectors of `per` batches
+    const int batches = (max(ve - vb, 0) + kThreads * kBatch - 1) / (kThreads * kBatch), per = (batches + kCells - 1) / kCells;
+    float cell = -INFINITY, most_of_all = -INFINITY;
+    int cells = 0;
+    for (int v0 = vb, in = 0; v0 < ve; v0 += kThreads * kBatch) {
         Vec<T> r[kBatch];
         float most = -INFINITY;
 #pragma unroll
@@ -386,46 +405,68 @@ __global__ void __launch_bounds__(THREADS, blocks_of(THREADS)) lp_fwd_kernel(con
         if (!(most * c <= acc.M)) acc.raise(most * c);
         acc.add(r, c);
         if (TOP) {
-            if (v0 == vb) {
-                // block-uniform: the first batch bounds the K-th largest from below by the K-th largest of 32 of its
-                // logits, the largest of those threads of each warp that hold the warp's largest
-                constexpr int kEach = kMaxK / kWarps;
-                uint32_t o = order_of(most);
-#pragma unroll
-                for (int r = 0; r < kEach; ++r) {
-                    const uint32_t m = __reduce_max_sync(kFull, o);
-                    if (__ffs(__ballot_sync(kFull, o == m)) - 1 == lane) o = 0;
-                    if (lane == 0) sh.least[w * kEach + r] = m;
-                }
-                __syncthreads();
-                o = sh.least[lane];
-                uint32_t kth = 0;
-                if (a.K <= kMaxK / 2) {   // taken away from the top, or from the bottom
-                    for (int r = 0; r < a.K; ++r) {
-                        kth = __reduce_max_sync(kFull, o);
-                        if (__ffs(__ballot_sync(kFull, o == kth)) - 1 == lane) o = 0;
-                    }
-                } else {
-                    for (int r = kMaxK; r >= a.K; --r) {
-                        kth = __reduce_min_sync(kFull, o);
-                        if (__ffs(__ballot_sync(kFull, o == kth)) - 1 == lane) o = 0xFFFFFFFFu;
-                    }
-                }
-                top.raise(kth);
-            }
-            top.raise(*static_cast<volatile uint32_t*>(&sh.bound));
-            if (__any_sync(kFull, !(most < top.thr))) {
-#pragma unroll
-                for (int k = 0; k < kBatch; ++k) {
-                    const int v = v0 + k * kThreads + threadIdx.x;
-                    float f[N];
-                    r[k].get(f);
-                    top.offer<N>(f, r[k].most(), v < ve ? head + v * N : a.V, head + ve * N);
-                }
+            cell = max_nan(cell, most);
+            if (++in == per || v0 + kThreads * kBatch >= ve) {   // block-uniform
+                sh.cell[cells++][threadIdx.x] = cell;
+                most_of_all = max_nan(most_of_all, cell);
+                cell = -INFINITY;
+                in = 0;
             }
         }
     }
-    if (w == 0 && rank == C - 1) scalars(head + nvec * N, a.V);
+    if (w == 0 && rank == C - 1) sum_scalars(tail, a.V);
+    if (TOP) {
+        // The K-th largest logit is at least the K-th largest of any 32 of them: of the largest ones that a thread of each
+        // warp saw, the largest few. Only cells that hold as large a logit are read again.
+        constexpr int kEach = kMaxK / kWarps;
+        uint32_t o = order_of(most_of_all);
+#pragma unroll
+        for (int r = 0; r < kEach; ++r) {
+            const uint32_t m = __reduce_max_sync(kFull, o);
+            if (__ffs(__ballot_sync(kFull, o == m)) - 1 == lane) o = 0;
+            if (lane == 0) sh.least[w * kEach + r] = m;
+        }
+        __syncthreads();
+        o = sh.least[lane];
+        uint32_t kth = 0;
+        if (a.K <= kMaxK / 2) {   // taken away from the top, or from the bottom
+            for (int r = 0; r < a.K; ++r) {
+                kth = __reduce_max_sync(kFull, o);
+                if (__ffs(__ballot_sync(kFull, o == kth)) - 1 == lane) o = 0;
+            }
+        } else {
+            for (int r = kMaxK; r >= a.K; --r) {
+                kth = __reduce_min_sync(kFull, o);
+                if (__ffs(__ballot_sync(kFull, o == kth)) - 1 == lane) o = 0xFFFFFFFFu;
+            }
+        }
+        top.raise(kth);
+        if (w == 0 && rank == 0) offer_scalars(0, head);
+        for (int q = 0; q < cells; ++q) {
+            top.raise(*static_cast<volatile uint32_t*>(&sh.bound));
+            const bool want = !(sh.cell[q][threadIdx.x] < top.thr);
+            if (!__any_sync(kFull, want)) continue;
+            for (int b = q * per; b < min(batches, (q + 1) * per); ++b) {
+                Vec<T> r[kBatch];
+#pragma unroll
+                for (int k = 0; k < kBatch; ++k) {
+                    const int v = vb + (b * kBatch + k) * kThreads + threadIdx.x;
+                    if (want && v < ve)
+                        r[k].ld(xv + static_cast<int64_t>(v) * N);
+                    else
+                        r[k].none();
+                }
+#pragma unroll
+                for (int k = 0; k < kBatch; ++k) {
+                    const int v = vb + (b * kBatch + k) * kThreads + threadIdx.x;
+                    float f[N];
+                    r[k].get(f);
+                    top.offer<N>(f, r[k].most(), want && v < ve ? head + v * N : a.V, tail);
+                }
+            }
+        }
+        if (w == 0 && rank == C - 1) offer_scalars(tail, a.V);
+    }
 #pragma unroll
     for (int k = 16; k; k >>= 1) {
         const float M = __shfl_xor_sync(kFull, acc.M, k), s = __shfl_xor_sync(kFull, acc.s, k),
@@ -438,11 +479,35 @@ __global__ void __launch_bounds__(THREADS, blocks_of(THREADS)) lp_fwd_kernel(con
         sh.u[w] = acc.u;
     }
     if (TOP) {
-        while (top.n > 0) top.flush();
-        sh.top[w][lane] = top.key;
+        // what waits in all warps is at most a row of 32 for each: together, the rows sorted by a warp each and joined.
+        // Where a warp has a list already, every warp completes its own.
+        uint64_t* const pool = &sh.top[0][0];
+        const bool lists = __syncthreads_or(__any_sync(kFull, top.key != 0)) != 0;
+        if (lists) {
+            while (top.n > 0) top.flush();
+            sh.top[w][lane] = top.key;
+            __syncthreads();
+            join_lists(sh.top, kWarps, w, lane);
+        } else {
+            int at = 0;
+            if (lane == 0) at = atomicAdd(&sh.pooled, top.n);
+            at = __shfl_sync(kFull, at, 0);
+            if (lane < top.n) pool[at + lane] = top.wait[lane];
+            __syncthreads();
+            const int n = sh.pooled;
+            int rows = 1;
+            while (rows * 32 < n) rows *= 2;
+            if (w < rows) {
+                uint64_t key = w * 32 + lane < n ? pool[w * 32 + lane] : 0;
+                TopList::sort(key, lane);
+                sh.top[w][lane] = key;
+            }
+            __syncthreads();
+            join_lists(sh.top, rows, w, lane);
+        }
+    } else {
+        __syncthreads();
     }
-    __syncthreads();
-    if (TOP) join_lists(sh.top, kWarps, w, lane);
     acc.clear();
     for (int k = 0; k < kWarps; ++k) acc.join(sh.M[k], sh.s[k], sh.u[k]);
     if (CLUSTER) {
