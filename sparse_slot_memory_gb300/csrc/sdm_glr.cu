@@ -23,9 +23,9 @@
 // Bound by HBM in principle (6 bytes a bfloat16 element forward, 10 backward, 2 flops a byte); in fact by the issue of
 // instructions at the 16 warps an SM that 128 registers allow: one pass holds 8 rows, their gates and the next step's
 // rows. Measured on a GB300 (6.7 TB/s copy): 8 x 8192 x 2048 bfloat16 with a gate per channel, forward 151 us (5.3 TB/s
-// of its bytes), forward and backward 399 us (5.4 TB/s); 1 x 65537 x 512 float32 with gates per head, both, 189 us
-// (671 MB of single reads: 3.5 TB/s; 940 MB moved); 24 ragged sequences, 30011 x 1920, forward 81 us (2.9 TB/s). One
-// token of 64 requests: 7.0 us a call, the host's time for it.
+// of its bytes), forward and backward 399 us (5.4 TB/s); 1 x 65537 x 512 float32 with gates per head, both, 186 us
+// (671 MB of single reads: 3.6 TB/s; 940 MB moved); 24 ragged sequences, 30011 x 1920, forward 79 to 90 us by their lengths
+// (2.6 to 2.9 TB/s). One token of 64 requests: 7.0 us a call, the host's time for it.
 #include <cuda_bf16.h>
 
 #include <algorithm>

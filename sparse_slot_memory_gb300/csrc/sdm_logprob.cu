@@ -16,9 +16,9 @@
 //
 // Bound by HBM: a read forward, a read and a write backward. Measured on a GB300 (6.7 TB/s copy): 4096 x 65536 bfloat16,
 // forward and backward 238 us (1.61 GB: 6.8 TB/s, the second read partly from the L2); 1000 x 50001 float32 forward 33 us
-// without alternatives (6.0 TB/s), 46 with 5, 65 with 32: more alternatives let more logits past the bound; 500 x 32000
-// bfloat16 10 us without and 18 with 20. Eight rows of 131072 with 20 alternatives: 7.9 us in clusters of 8 blocks, bound
-// by latency (loads, two list sorts, barriers).
+// without alternatives (6.0 TB/s), 44 with 5; 2470 x 41414 bfloat16 40 us without, 54 with 1 and 69 with 20: a row's end
+// (bound, cells, sort) is not hidden where all blocks of an SM reach it together. Eight rows of 131072 with 20
+// alternatives: 7.5 us in clusters of 8 blocks, no more than the host's call.
 //
 // A row whose largest logit lies under -1e30 / scale (everything masked, by -inf or by a type's lowest value)
 // leaves s = 0 and takes a second, plain look; so does the backward of a row whose lse is too large for float32

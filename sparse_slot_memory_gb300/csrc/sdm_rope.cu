@@ -15,8 +15,8 @@
 //
 // Bound by HBM: 4 bytes a bfloat16 element forward, 6 backward; the table's 512 bytes a token of 128 columns count
 // little beside the heads. Measured on a GB300 (6.7 TB/s copy), 32768 tokens of 32 + 8 heads of 128 columns, bfloat16,
-// slices of a fused projection: forward 112 us (6.0 TB/s), forward and backward 284 us (5.9 TB/s); 32 tokens: 9.9 us a
-// call, the host's time for it.
+// slices of a fused projection: forward 112 us (6.0 TB/s), forward and backward 286 us (5.9 TB/s), 295 with half of the
+// head turned; 32 tokens: 9.4 to 10 us a call, the host's time for it.
 #include <cuda_bf16.h>
 
 #include <algorithm>
