@@ -2,7 +2,7 @@
 evaluation may have (u = 2^-24, half a unit in the last place of float32).
 
 Every bound is derived from the arithmetic that include/sdm.h states, for any order of the sums:
-  * expf, exp2f, log2f, rsqrtf are within 2 ulp (4 u relative) of the exact value, + - * fma within u;
+  * expf, log2f, rsqrtf and the hardware's 2^t are within 2 ulp (4 u relative) of the exact value, + - * fma within u;
   * a sum of n terms in any order is within n u of the sum of their magnitudes;
   * a result stored in bfloat16 has one more relative rounding of 2^-8 (a unit in the last place of 8 bits, twice
     what round-to-nearest needs).
@@ -46,8 +46,9 @@ def f64(t):
 
 # ---- gated linear recurrence -------------------------------------------------------------------------
 def glr_forward(x, g, cuts, h0, gw):
-    """h [rows, D], hT [P, D] and their bounds. A row adds 8 u of what it joins: 4 u of expf, one each for the
-    product of the gates, the fused multiply-add of the span, that of the join and that of the final walk."""
+    """h [rows, D], hT [P, D] and their bounds. A row adds 8 u of what it joins: 4 u + |g| u of the gate's exponential
+    (the tests' gates lie within 2.6 of 0, or give exactly 0), one of the gates' product or of the fused
+    multiply-add, and its share of the join of its span."""
     a = np.repeat(np.exp(g), gw, axis=1)
     h, e = np.zeros_like(x), np.zeros_like(x)
     hT, eT = h0.copy(), np.zeros_like(h0)
