@@ -16,8 +16,8 @@
 //
 // Bound by HBM: a read forward, a read and a write backward. Measured on a GB300 (6.7 TB/s copy): 4096 x 65536 bfloat16,
 // forward and backward 238 us (1.61 GB: 6.8 TB/s, the second read partly from the L2); 1000 x 50001 float32 forward 33 us
-// without alternatives (6.0 TB/s), 44 with 5; 2470 x 41414 bfloat16 40 us without, 54 with 1 and 69 with 20: a row's end
-// (bound, cells, sort) is not hidden where all blocks of an SM reach it together. Eight rows of 131072 with 20
+// without alternatives (6.1 TB/s), 42 with 5; 8000 x 12000 bfloat16 34 us without, 74 with 20: a row's end (bound, cells,
+// sort) is not hidden wholly where the blocks of an SM reach it together. Eight rows of 131072 with 20
 // alternatives: 7.5 us in clusters of 8 blocks, no more than the host's call.
 //
 // A row whose largest logit lies under -1e30 / scale (everything masked, by -inf or by a type's lowest value)
@@ -38,12 +38,18 @@ namespace {
 
 using namespace rows;
 
-// Threads of a block that has a row to itself, four of which share an SM (1000 rows of 50001: 74 us with two of 512 in an
-// earlier form, 59 with four of 256; eight of 128: equal there, 500 rows of 32000 2.4 times slower), and of one of a
-// cluster, where the fewer rows want more threads (150 rows of 131072: 21.7 us with 256, 18.2 with 512; 8 rows: 8.3 and 7.9).
-// Short rows of up to kShort bytes, which are no more than two batches of two warps, are taken by blocks of those,
-// sixteen on an SM, because the fixed part of a row (bound, sort, joins) counts most.
-constexpr int kRowThreads = 256, kClusterThreads = 512, kShortThreads = 64, kShort = 8192;
+// Threads of a block that has a row to itself: as few as still fill the SMs, because the fixed part of a row (bound, cells,
+// sort) costs a few warps little more than many, and more blocks on an SM hide one another's. All blocks run at 1024
+// threads an SM. Measured at bfloat16 rows with 20 alternatives (us, blocks of 256 / 128 / 64 threads):
+//   8000 x 6000: 85 / 65 / 53    8000 x 12000: 113 / 81 / 74    2000 x 12000: 32 / 24 / 24    600 x 12000: 10.4 / 9.5 / 12.4
+//   8000 x 32000: 161 / 135      1000 x 32000: 26 / 24          600 x 32000: 15.5 / 17.9 / 27
+//   1800 x 128000: 100 / 111     1000 x 128000: 63 / 64 (47 / 43 without alternatives)
+// Long rows lose with narrow blocks where a few of them are left at the end, each read by few threads, but not where all
+// run at once, when 256 threads would leave those few. Very short rows are two batches of two warps.
+// A block of a cluster has the fewest rows and the most threads (150 rows of 131072: 21.7 us with 256, 18.2 with 512; 8 rows:
+// 8.3 and 7.9).
+constexpr int kRowThreads = 256, kClusterThreads = 512, kMidThreads = 128, kShortThreads = 64;
+constexpr int64_t kMidBytes = 65536, kShortBytes = 24576, kBriefBytes = 8192, kSms = 152;
 constexpr int blocks_of(int threads) { return 1024 / threads; }   // on an SM, at 64 registers
 constexpr int kBatch = 4;             // vectors of a thread in flight
 constexpr int kMaxK = 32;
@@ -669,8 +675,16 @@ sdm_status check_logits(const sdm_logprob_shape* s, const void* p, int64_t ld, b
 int cluster_of(const sdm_logprob_shape* s) {
     const int64_t batch = kClusterThreads * 16 / (s->dtype == SDM_BF16 ? 2 : 4);
     int c = 1;
-    while (c < kMaxCluster && s->rows * c < 152 && s->V >= 2 * c * batch) c *= 2;
+    while (c < kMaxCluster && s->rows * c < kSms && s->V >= 2 * c * batch) c *= 2;
     return c;
+}
+
+// Threads of a block that has a row to itself.
+int threads_of(const sdm_logprob_shape* s) {
+    const int64_t bytes = static_cast<int64_t>(s->V) * (s->dtype == SDM_BF16 ? 2 : 4);
+    if (bytes <= kBriefBytes || (bytes <= kShortBytes && s->rows >= 8 * kSms)) return kShortThreads;
+    const bool once = s->rows >= 5 * kSms && s->rows <= 8 * kSms;   // all at once at eight blocks an SM, not at four
+    return once || (bytes <= kMidBytes && s->rows >= 4 * kSms) ? kMidThreads : kRowThreads;
 }
 
 }  // namespace
@@ -696,7 +710,6 @@ extern "C" sdm_status sdm_token_logprobs(const sdm_logprob_shape* shape, const v
     const bool bf = shape->dtype == SDM_BF16;
     a.cluster = cluster_of(shape);
     if (shape->rows * a.cluster > 0x7FFFFFFF) return SDM_ERR_SHAPE;
-    const bool brief = static_cast<int64_t>(shape->V) * (bf ? 2 : 4) <= kShort;
     const dim3 grid(static_cast<unsigned>(shape->rows * a.cluster));
     const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
     auto run = [&](auto t, auto with_top) {
@@ -704,8 +717,14 @@ extern "C" sdm_status sdm_token_logprobs(const sdm_logprob_shape* shape, const v
         constexpr bool TOP = decltype(with_top)::value;
         if (a.cluster > 1)
             return launch_cluster(lp_fwd_kernel<T, TOP, true, kClusterThreads>, grid, dim3(kClusterThreads), a.cluster, cs, a);
-        if (brief) return launch_dependent(lp_fwd_kernel<T, TOP, false, kShortThreads>, grid, dim3(kShortThreads), 0, cs, a);
-        return launch_dependent(lp_fwd_kernel<T, TOP, false, kRowThreads>, grid, dim3(kRowThreads), 0, cs, a);
+        auto go = [&](auto threads) {
+            constexpr int N = decltype(threads)::value;
+            return launch_dependent(lp_fwd_kernel<T, TOP, false, N>, grid, dim3(N), 0, cs, a);
+        };
+        const int threads = threads_of(shape);
+        if (threads == kShortThreads) return go(std::integral_constant<int, kShortThreads>{});
+        if (threads == kMidThreads) return go(std::integral_constant<int, kMidThreads>{});
+        return go(std::integral_constant<int, kRowThreads>{});
     };
     const std::true_type yes;
     const std::false_type no;

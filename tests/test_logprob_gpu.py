@@ -215,3 +215,18 @@ def test_no_rows_and_refusals():
         b = sdm.LogprobSpec(**{**dict(rows=4, V=100, K=3, dtype="f32"), **bad})
         assert _abi.load().sdm_token_logprobs(b.c(), x.data_ptr(), 100, t.data_ptr(), o.data_ptr(), None, None, None, None,
                                               None, None) == -2, bad
+
+
+@pytest.mark.parametrize("N, V, K, dtype", [
+    (1300, 5003, 20, "bf16"), (1216, 2999, 32, "f32"), (1217, 12289, 1, "bf16"), (620, 14001, 20, "bf16"),
+    (608, 3501, 32, "f32"), (760, 33000, 7, "bf16"), (607, 7001, 17, "bf16")])
+def test_many_rows_take_narrow_blocks(N, V, K, dtype):
+    """The block widths that many rows get, with ties, masked logits and rows with nothing left among them."""
+    x, t = logits(N, V, dtype, pad=1), targets(N, V)
+    x[3] = -float("inf")
+    x[4] = 1.0
+    x[5, ::2] = torch.finfo(DT[dtype]).min
+    x[6] = torch.arange(V, device="cuda") * 1e-3
+    x[7, : V - 1] = -float("inf")
+    x[N - 1] = torch.arange(V, device="cuda").flip(0) * 1e-3
+    compare(x, t, K, 1.0, run(x, t, K))
