@@ -8,7 +8,7 @@
 //
 // The top alternatives: the same pass leaves the largest logit of every cell (64 bytes or more of a thread's share) in the
 // shared memory. The K-th largest of 32 of those bounds the K-th largest logit from below; the few cells that hold as
-// large a logit are read again, their logits wait in the shared memory and join their warp's list of the 32 largest
+// large a logit are read again, a vector a lane, their logits wait in the shared memory and join their warp's list of the 32 largest
 // (value, id) sorted, 32 at a time, and the warps' lists join by halves.
 //
 // A row is one block's, or where there are fewer rows than the SMs hold blocks, a cluster's: each block takes a part
@@ -16,9 +16,9 @@
 //
 // Bound by HBM: a read forward, a read and a write backward. Measured on a GB300 (6.7 TB/s copy): 4096 x 65536 bfloat16,
 // forward and backward 238 us (1.61 GB: 6.8 TB/s, the second read partly from the L2); 1000 x 50001 float32 forward 33 us
-// without alternatives (6.1 TB/s), 42 with 5; 8000 x 12000 bfloat16 34 us without, 74 with 20: a row's end (bound, cells,
+// without alternatives (6.1 TB/s), 38 with 5; 8000 x 12000 bfloat16 32 us without, 58 with 20: a row's end (bound, cells,
 // sort) is not hidden wholly where the blocks of an SM reach it together. Eight rows of 131072 with 20
-// alternatives: 7.5 us in clusters of 8 blocks, no more than the host's call.
+// alternatives: 7.3 us in clusters of 8 blocks, no more than the host's call.
 //
 // A row whose largest logit lies under -1e30 / scale (everything masked, by -inf or by a type's lowest value)
 // leaves s = 0 and takes a second, plain look; so does the backward of a row whose lse is too large for float32
@@ -41,9 +41,9 @@ using namespace rows;
 // Threads of a block that has a row to itself: as few as still fill the SMs, because the fixed part of a row (bound, cells,
 // sort) costs a few warps little more than many, and more blocks on an SM hide one another's. All blocks run at 1024
 // threads an SM. Measured at bfloat16 rows with 20 alternatives (us, blocks of 256 / 128 / 64 threads):
-//   8000 x 6000: 85 / 65 / 53    8000 x 12000: 113 / 81 / 74    2000 x 12000: 32 / 24 / 24    600 x 12000: 10.4 / 9.5 / 12.4
-//   8000 x 32000: 161 / 135      1000 x 32000: 26 / 24          600 x 32000: 15.5 / 17.9 / 27
-//   1800 x 128000: 100 / 111     1000 x 128000: 63 / 64 (47 / 43 without alternatives)
+//   8000 x 6000: 84 / 55 / 42    8000 x 12000: 103 / 65 / 58    2000 x 12000: 30 / 20 / 18    600 x 12000: 9.3 / 8.5 / 9.7
+//   8000 x 32000: 142 / 113 / 113    1000 x 32000: 23 / 19 / 24    600 x 32000: 13 / 15 / 21    1000 x 128000: 56 / 53 / 74
+//   1800 x 128000: 92 / 95 / 94 (74 / 82 / 74 without alternatives)
 // Long rows lose with narrow blocks where a few of them are left at the end, each read by few threads, but not where all
 // run at once, when 256 threads would leave those few. Very short rows are two batches of two warps.
 // A block of a cluster has the fewest rows and the most threads (150 rows of 131072: 21.7 us with 256, 18.2 with 512; 8 rows:
@@ -205,11 +205,17 @@ struct TopList {
     int K, lane, n;   // n wait
     uint32_t pass;    // a logit enters only if its order is at least this
     float thr;        // the same as a value: logits below it do not enter (NaN: none is below)
+    uint32_t last;    // and one of that order only if its id is below this
     __device__ __forceinline__ void raise(uint32_t p) {
         if (p > pass) {
             pass = p;
             thr = value_of(p);
+            last = 0xFFFFFFFFu;
         }
+    }
+    // whether logits of at most x with ids from `id` on may enter
+    __device__ __forceinline__ bool enters(float x, int id) const {
+        return !(x < thr) && !(static_cast<uint32_t>(id) >= last && order_of(x) == pass);
     }
     __device__ __forceinline__ void clear(int k, int l, uint64_t* w, uint32_t* b) {
         key = 0;
@@ -220,6 +226,7 @@ struct TopList {
         n = 0;
         pass = 0;
         thr = value_of(0);
+        last = 0xFFFFFFFFu;
     }
     // A step of a sorting network: the lane pairs at distance d, the larger first where `down`
     __device__ __forceinline__ static void step(uint64_t& k, int d, bool down, int lane) {
@@ -250,11 +257,11 @@ struct TopList {
         n = max(0, n - 32);
         sort(c, lane);
         join(c);
-        const uint32_t k = static_cast<uint32_t>(__shfl_sync(kFull, key, K - 1) >> 32);
+        const uint64_t kth = __shfl_sync(kFull, key, K - 1);
+        const uint32_t k = static_cast<uint32_t>(kth >> 32);
         if (k != 0) {
-            // an equal logit of one of the warp's later vectors has a higher id and stays out; one of another warp
-            // may have a lower
-            raise(k == 0xFFFFFFFFu ? k : k + 1);
+            raise(k);
+            if (k == pass) last = min(last, ~static_cast<uint32_t>(kth));   // K logits of this warp go before the others
             if (lane == 0) atomicMax(bound, k);
         }
         __syncwarp();
@@ -262,13 +269,12 @@ struct TopList {
     // N logits of each lane, ids id .. id + N - 1 (a lane whose id lies at or past `end` has none)
     template <int N>
     __device__ __forceinline__ void offer(const float (&x)[N], float most, int id, int end) {
-        const float bar = thr;
-        const bool want = id < end && !(most < bar);
+        const bool want = id < end && enters(most, id);
         if (!__any_sync(kFull, want)) return;
         uint32_t mine = 0;   // the lane's logits that enter
         if (want) {
 #pragma unroll
-            for (int i = 0; i < N; ++i) mine |= !(x[i] < bar) ? 1u << i : 0u;
+            for (int i = 0; i < N; ++i) mine |= enters(x[i], id + i) ? 1u << i : 0u;
         }
         while (true) {   // one logit of each lane that has one left, room for 32 of them behind the 31 that may wait
             const uint32_t b = __ballot_sync(kFull, mine != 0);
@@ -292,7 +298,11 @@ template <int WARPS, int CLUSTER, bool TOP>
 struct Shared {
     static_assert(kMaxK % WARPS == 0, "each warp gives its share of the 32 logits that bound the alternatives");
     float M[WARPS], s[WARPS], u[WARPS], red[WARPS];
-    uint64_t top[WARPS][kMaxK], wait[WARPS][64];
+    union {
+        uint64_t top[WARPS][kMaxK];
+        uint16_t hit[WARPS][kMaxK * 4];   // before the lists: cells of a warp's threads to be read again, 32 cell + lane
+    };
+    uint64_t wait[WARPS][64];
     uint32_t least[kMaxK], bound;
     int pooled;
     float cell[TOP ? kCells : 1][WARPS * 32];   // the largest logit of a thread's cell
@@ -448,27 +458,41 @@ __global__ void __launch_bounds__(THREADS, blocks_of(THREADS)) lp_fwd_kernel(con
         }
         top.raise(kth);
         if (w == 0 && rank == 0) offer_scalars(0, head);
+        // A cell has `size` vectors; those of a warp's cells are read again one a lane, whoever's cell they are of: a
+        // few rounds of full warps instead of one for every cell and vector (8000 x 12000 bfloat16, 20 alternatives: 75 us,
+        // then 58; 1000 x 50001 float32 with 32: 58, then 47; rows whose logits all rise with the id lose: 42, then 51).
+        const int size = per * kBatch;
+        int hits = 0;
         for (int q = 0; q < cells; ++q) {
             top.raise(*static_cast<volatile uint32_t*>(&sh.bound));
-            const bool want = !(sh.cell[q][threadIdx.x] < top.thr);
-            if (!__any_sync(kFull, want)) continue;
-            for (int b = q * per; b < min(batches, (q + 1) * per); ++b) {
-                Vec<T> r[kBatch];
-#pragma unroll
-                for (int k = 0; k < kBatch; ++k) {
-                    const int v = vb + (b * kBatch + k) * kThreads + threadIdx.x;
-                    if (want && v < ve)
-                        r[k].ld(xv + static_cast<int64_t>(v) * N);
+            const float best = sh.cell[q][threadIdx.x];
+            if (__any_sync(kFull, !(best < top.thr))) {
+                const int v = min(vb + q * size * kThreads + static_cast<int>(threadIdx.x), ve);
+                const bool want = top.enters(best, head + v * N);
+                const uint32_t all = __ballot_sync(kFull, want);
+                if (want) sh.hit[w][hits + __popc(all & ((1u << lane) - 1u))] = static_cast<uint16_t>(q * 32 + lane);
+                hits += __popc(all);
+            }
+            while (hits >= 32 || (hits > 0 && q == cells - 1)) {   // the first 32
+                const int n = min(hits, 32) * size;
+                __syncwarp();
+                for (int j0 = 0; j0 < n; j0 += 32) {
+                    const int j = j0 + lane, h = min(j, n - 1) / size, code = sh.hit[w][h], col = w * 32 + (code & 31);
+                    const int v = vb + ((code >> 5) * size + j - h * size) * kThreads + col;
+                    const bool mine = j < n && v < ve && !(sh.cell[code >> 5][col] < top.thr);
+                    Vec<T> r;
+                    if (mine)
+                        r.ld(xv + static_cast<int64_t>(v) * N);
                     else
-                        r[k].none();
-                }
-#pragma unroll
-                for (int k = 0; k < kBatch; ++k) {
-                    const int v = vb + (b * kBatch + k) * kThreads + threadIdx.x;
+                        r.none();
                     float f[N];
-                    r[k].get(f);
-                    top.offer<N>(f, r[k].most(), want && v < ve ? head + v * N : a.V, tail);
+                    r.get(f);
+                    top.offer<N>(f, r.most(), mine ? head + v * N : a.V, tail);
                 }
+                const uint16_t rest = lane + 32 < hits ? sh.hit[w][lane + 32] : uint16_t(0);
+                __syncwarp();
+                if (lane + 32 < hits) sh.hit[w][lane] = rest;
+                hits = max(0, hits - 32);
             }
         }
         if (w == 0 && rank == C - 1) offer_scalars(tail, a.V);

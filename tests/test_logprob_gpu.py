@@ -230,3 +230,16 @@ def test_many_rows_take_narrow_blocks(N, V, K, dtype):
     x[7, : V - 1] = -float("inf")
     x[N - 1] = torch.arange(V, device="cuda").flip(0) * 1e-3
     compare(x, t, K, 1.0, run(x, t, K))
+
+
+@pytest.mark.parametrize("N, V, dtype", [(2, 131072, "bf16"), (3, 70001, "f32"), (40, 30000, "bf16"), (620, 4500, "bf16")])
+@pytest.mark.parametrize("K", [1, 20, 32])
+def test_ties_across_the_threads_of_a_row(N, V, dtype, K):
+    """Few different values, so that the K-th largest has equals in every part of a row; the lowest ids have to win."""
+    x, t = logits(N, V, dtype, scale=1.0).float().round(), targets(N, V)
+    x[0] = x[0].clamp(max=2.0)
+    x[1] = x[1].clamp(max=2.0)
+    x[1, V - 9:] = 3.0
+    x[1, 5] = 3.0
+    x = x.to(DT[dtype])
+    compare(x, t, K, 1.0, run(x, t, K))
