@@ -460,7 +460,8 @@ __global__ void __launch_bounds__(THREADS, blocks_of(THREADS)) lp_fwd_kernel(con
         if (w == 0 && rank == 0) offer_scalars(0, head);
         // A cell has `size` vectors; those of a warp's cells are read again one a lane, whoever's cell they are of: a
         // few rounds of full warps instead of one for every cell and vector (8000 x 12000 bfloat16, 20 alternatives: 75 us,
-        // then 58; 1000 x 50001 float32 with 32: 58, then 47; rows whose logits all rise with the id lose: 42, then 51).
+        // then 58; 1000 x 50001 float32 with 32: 58, then 47; rows whose logits all rise with the id lose:
+        // the latter with 20 42, then 51, 4000 x 12000 bfloat16 41, then 61).
         const int size = per * kBatch;
         int hits = 0;
         for (int q = 0; q < cells; ++q) {
