@@ -59,8 +59,10 @@ constexpr float kLog2e = 1.44269504088896341f;
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr float kFloor = -1e35f;      // what a masked logit counts as in the sums: its term is 0 beside any M
 constexpr float kStart = -1e30f;      // the first M
-constexpr float kGradFloor = -1e30f;  // the same in the gradient, where its products have to stay finite
 constexpr float kFarLse = 1024.f;     // |lse| from which float32 z - lse is too coarse
+// Where the gradient cuts z, and z - lse of far rows: p is 0 there beside any |lse| below kFarLse, and the products of what
+// is left with scale and d_entropy, which p multiplies, stay as small as those of the other logits (-inf times 0 is NaN).
+constexpr float kGradFloor = -2 * kFarLse;
 
 struct LpArgs {
     const void* logits;
@@ -79,6 +81,7 @@ struct LpArgs {
     int64_t rows, ld, d_ld;
     int V, K;
     float scale;
+    float floor;           // backward: the logit at kGradFloor
     int cluster;           // blocks of a row
 };
 
@@ -643,7 +646,7 @@ __global__ void __launch_bounds__(kBwdThreads) lp_bwd_kernel(const LpArgs a, int
     // dlogits = p (k1 d + k0) with d = log p, and scale dl more at the target
     const float k0 = -a.scale * (dl + dh * H), k1 = -a.scale * dh;
     auto grad = [&](float v, int id) {
-        const float d = fmaf(max_nan(v, kGradFloor), a.scale, -lse);
+        const float d = fmaf(max_nan(v, a.floor), a.scale, -lse);
         return ex2(d * kLog2e) * fmaf(d, k1, k0) + (id == t ? a.scale * dl : 0.f);
     };
     if (part == 0) {   // the logits outside the vectors
@@ -659,7 +662,7 @@ __global__ void __launch_bounds__(kBwdThreads) lp_bwd_kernel(const LpArgs a, int
         float f[N];
 #pragma unroll
         for (int i = 0; i < N / 2; ++i) {
-            const uint64_t d2 = fma2(r[k].pair(i, kGradFloor), sc2, ls2);
+            const uint64_t d2 = fma2(r[k].pair(i, a.floor), sc2, ls2);
             float p, q;
             unpack2(mul2(d2, le2), p, q);
             unpack2(mul2(pack2(ex2(p), ex2(q)), fma2(d2, k12, k02)), f[2 * i], f[2 * i + 1]);
@@ -772,7 +775,7 @@ extern "C" sdm_status sdm_token_logprobs_backward(const sdm_logprob_shape* shape
     memset(&a, 0, sizeof(a));
     a.logits = logits; a.ld = ld; a.targets = targets; a.lse_in = lse; a.ent_in = entropy; a.d_logp = d_logp;
     a.d_entropy = d_entropy; a.dlogits = dlogits; a.d_ld = d_ld; a.status = status;
-    a.rows = shape->rows; a.V = shape->V; a.scale = shape->scale;
+    a.rows = shape->rows; a.V = shape->V; a.scale = shape->scale; a.floor = kGradFloor / shape->scale;
     const bool bf = shape->dtype == SDM_BF16;
     const int per = kBwdThreads * kBwdVecs * (bf ? 8 : 4);
     const int parts = (shape->V + per - 1) / per;

@@ -1,0 +1,79 @@
+"""Corners of the token log probabilities: masked logits at other scales and under large gradients of the entropy.
+The values are those of tests/operators_testlib.py in 64 bits, with its bounds."""
+
+import numpy as np
+import pytest
+import torch
+
+import sparse_slot_memory_gb300 as sdm
+from operators_testlib import check, f64, logprobs, logprobs_backward, order_topk
+
+pytestmark = pytest.mark.gpu
+
+DT = {"f32": torch.float32, "bf16": torch.bfloat16}
+
+
+def run(x, t, scale, K=0, dh=1.0, seed=9):
+    """Forward and backward of logits x [N, V]; the entropies' gradients are `dh` times N(0, 1)."""
+    N, V = x.shape
+    s = sdm.LogprobSpec(rows=N, V=V, K=K, dtype="bf16" if x.dtype == torch.bfloat16 else "f32", scale=scale)
+    gen = torch.Generator().manual_seed(seed)
+    r = {k: torch.full((N,), float("nan"), device="cuda") for k in ("logp", "entropy", "lse")}
+    r["top_vals"] = torch.full((N, K), float("nan"), device="cuda")
+    r["top_idx"] = torch.full((N, K), -7, dtype=torch.int32, device="cuda")
+    r["d_logp"], r["d_entropy"] = torch.randn(N, generator=gen).cuda(), (dh * torch.randn(N, generator=gen)).cuda()
+    r["dlogits"] = torch.full((N, V), float("nan"), dtype=x.dtype, device="cuda")
+    sdm.token_logprobs(s, x, t, r["logp"], r["entropy"], r["lse"], r["top_vals"], r["top_idx"])
+    sdm.token_logprobs_backward(s, x, t, r["lse"], r["entropy"], r["d_logp"], r["dlogits"], r["d_entropy"])
+    return r
+
+
+def compare(x, t, scale, r, K=0):
+    """Against the definition; values past float32's range are its infinities."""
+    X, tt, sc = f64(x), t.cpu().numpy(), float(np.float32(scale))
+    with np.errstate(over="ignore"):
+        f = logprobs(X, tt, sc)
+        stored = lambda v: v.astype(np.float32).astype(np.float64)
+        check("logp", r["logp"], stored(f["logp"]), f["logp_e"])
+        check("entropy", r["entropy"], f["H"], f["H_e"])
+        check("lse", r["lse"], stored(f["lse"]), f["lse_e"])
+        if K:
+            top = order_topk(X, K)
+            assert np.array_equal(r["top_idx"].cpu().numpy(), top)
+            at = (np.arange(len(X))[:, None], top)
+            check("top_vals", r["top_vals"], stored(f["logs"][at]), f["logs_e"][at])
+    d, e = logprobs_backward(X, tt, sc, f64(r["d_logp"]), f64(r["d_entropy"]))
+    check("dlogits", r["dlogits"], d, e, x.dtype)
+
+
+def masked(N, V, dtype, scale, seed=0):
+    """Logits of N(0, 4) behind the scale, a third of them -inf, a third the type's lowest value."""
+    gen = torch.Generator().manual_seed(seed)
+    x = (torch.randn(N, V, generator=gen) * (2.0 / scale)).to(DT[dtype])
+    u = torch.rand(N, V, generator=gen)
+    x[u < 1 / 3] = -float("inf")
+    x[u > 2 / 3] = torch.finfo(DT[dtype]).min
+    t = torch.randint(0, V, (N,), generator=gen).to(torch.int32)
+    for i in range(N):   # a target that is left, but for the last row's, whose probability is 0
+        t[i] = torch.nonzero((u[i] >= 1 / 3) & (u[i] <= 2 / 3))[int(t[i]) % 10] if i + 1 < N else t[i]
+    return x.cuda(), t.cuda()
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("scale, dh", [(0.01, 1e5), (1.0, 1e9), (10.0, 4e7), (100.0, 1e5), (1000.0, 1e5)])
+def test_masked_logits_under_large_entropy_gradients(dtype, scale, dh):
+    """Masked logits have no gradient, whatever the scale and the entropy's gradient are."""
+    x, t = masked(6, 9001, dtype, scale)
+    r = run(x, t, scale, dh=dh)
+    compare(x, t, scale, r)
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("offset, scale", [(3000.0, 1.0), (-70000.0, 0.5), (50.0, 100.0)])
+def test_masked_rows_far_from_zero(dtype, offset, scale):
+    """|lse| of 1024 and more, where the backward takes differences to the largest logit, over several blocks a row."""
+    x, t = masked(5, 20001, dtype, scale)
+    x[x > -1e37] += offset
+    r = run(x, t, scale, dh=1e9)
+    assert bool((r["lse"].abs() >= 1024).all())
+    compare(x, t, scale, r)
