@@ -496,8 +496,10 @@ typedef struct {
  *   among equal logits.
  * targets int32 [rows]: below 0 is ignored (logp 0); at or above V likewise, and sets SDM_DEV_BAD_TARGET. logp
  * float32 [rows]; entropy, lse, top_vals, top_idx nullable. A row whose logits are all -inf has lse = -inf, log
- * probabilities -inf and entropy 0. A row that holds NaN or +inf (or a finite logit whose product with
- * scale log2(e) overflows) has NaN for its float outputs; NaN counts as the largest logit in top_idx.
+ * probabilities -inf and entropy 0. Finite logits of any size have the probabilities of their differences (a row of a
+ * type's lowest value is uniform); where lse lies past float32's range it is the largest or lowest finite value, and a
+ * log probability below it is -inf. A row that holds NaN or +inf has NaN for its float outputs; NaN counts as the
+ * largest logit in top_idx.
  */
 sdm_status sdm_token_logprobs(const sdm_logprob_shape* shape, const void* logits, int64_t ld, const int32_t* targets,
                               float* logp, float* entropy, float* lse, float* top_vals, int32_t* top_idx,

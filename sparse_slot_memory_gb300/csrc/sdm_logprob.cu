@@ -20,12 +20,14 @@
 // sort) is not hidden wholly where the blocks of an SM reach it together. Eight rows of 131072 with 20
 // alternatives: 7.3 us in clusters of 8 blocks, no more than the host's call.
 //
-// A row whose largest logit lies under -1e30 / scale (everything masked, by -inf or by a type's lowest value)
-// leaves s = 0 and takes a second, plain look; so does the backward of a row whose lse is too large for float32
-// differences.
+// A row whose largest logit lies under -1e30 / scale (everything masked, by -inf or by a type's lowest value) leaves
+// s = 0, one whose largest x scale log2(e) is past float32's range leaves NaN, and an M of 2^28 or more is rounded too
+// coarsely: such rows take a second, plain look, whose differences hold for any finite logits. So does the backward of a row whose lse is too large for float32 differences. lse
+// past the range is the largest or lowest finite value, so that -inf tells the backward that the row has nothing left.
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <cfloat>
 #include <cstring>
 #include <type_traits>
 
@@ -59,6 +61,7 @@ constexpr float kLog2e = 1.44269504088896341f;
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr float kFloor = -1e35f;      // what a masked logit counts as in the sums: its term is 0 beside any M
 constexpr float kStart = -1e30f;      // the first M
+constexpr float kFarM = 0x1p28f;      // |M| from which its rounding, which every term's t carries, is more than 16
 constexpr float kFarLse = 1024.f;     // |lse| from which float32 z - lse is too coarse
 // Where the gradient cuts z, and z - lse of far rows: p is 0 there beside any |lse| below kFarLse, and the products of what
 // is left with scale and d_entropy, which p multiplies, stay as small as those of the other logits (-inf times 0 is NaN).
@@ -566,14 +569,15 @@ __global__ void __launch_bounds__(THREADS, blocks_of(THREADS)) lp_fwd_kernel(con
     // z - lse = (x - ref) mul - sub for the row's logits
     float ref = 0.f, sub, lse, H, mul = 0.f;
     bool empty = false;
-    if (acc.s == 0.f) {   // block-uniform
+    if (!(acc.s > 0.f && fabsf(acc.M) < kFarM)) {   // block-uniform
         float m, s, u;
         plain_stats(x, a.V, a.scale, sh.red, m, s, u);
         empty = m == -INFINITY;
         ref = m;
         mul = a.scale;
         sub = logf(s);
-        lse = empty ? -INFINITY : m * a.scale + sub;
+        const float top = fmaf(m, a.scale, sub);
+        lse = empty ? -INFINITY : isinf(top) ? copysignf(FLT_MAX, top) : top;
         H = empty ? 0.f : sub - u / s;
     } else {
         const float l2 = log2f(acc.s);
@@ -584,7 +588,10 @@ __global__ void __launch_bounds__(THREADS, blocks_of(THREADS)) lp_fwd_kernel(con
     }
     auto logp_of = [&](float v) {
         if (empty) return -INFINITY;
-        if (mul != 0.f) return (v - ref) * mul - sub;
+        if (mul != 0.f) {
+            const float d = v - ref;   // of finite logits infinite beside a large ref alone: then the products do not cancel
+            return (isinf(d) && ref > 0.f ? v * mul - ref * mul : d * mul) - sub;
+        }
         const float t = fmaf(v, c, -acc.M) - sub;
         if (t < kStart) return v * a.scale - lse;   // a masked logit's t may have overflowed
         return t > 0.f ? 0.f : t * kLn2;            // M and the logit's product round apart: never above 0
@@ -633,7 +640,7 @@ __global__ void __launch_bounds__(kBwdThreads) lp_bwd_kernel(const LpArgs a, int
         // block-uniform and rare: z - lse from differences to the largest logit, or (lse -inf) a row of zeros
         const bool empty = lse == -INFINITY;
         float m = 0.f, s = 1.f, u;
-        if (!isinf(lse)) plain_stats(x, a.V, a.scale, red, m, s, u);
+        if (!empty) plain_stats(x, a.V, a.scale, red, m, s, u);
         const float ls = logf(s);
         const int per = kBwdThreads * kBwdVecs * N;
         for (int i = part * per + threadIdx.x; i < (part + 1 == parts ? a.V : min(a.V, (part + 1) * per)); i += kBwdThreads) {

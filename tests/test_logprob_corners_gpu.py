@@ -1,5 +1,5 @@
-"""Corners of the token log probabilities: masked logits at other scales and under large gradients of the entropy.
-The values are those of tests/operators_testlib.py in 64 bits, with its bounds."""
+"""Corners of the token log probabilities: masked logits at other scales and under large gradients of the entropy, and finite
+logits whose products leave float32's range. The values are those of tests/operators_testlib.py in 64 bits, with its bounds."""
 
 import numpy as np
 import pytest
@@ -29,14 +29,15 @@ def run(x, t, scale, K=0, dh=1.0, seed=9):
 
 
 def compare(x, t, scale, r, K=0):
-    """Against the definition; values past float32's range are its infinities."""
+    """Against the definition; past float32's range log probabilities are -inf, and a finite lse its last finite values."""
     X, tt, sc = f64(x), t.cpu().numpy(), float(np.float32(scale))
     with np.errstate(over="ignore"):
         f = logprobs(X, tt, sc)
         stored = lambda v: v.astype(np.float32).astype(np.float64)
         check("logp", r["logp"], stored(f["logp"]), f["logp_e"])
         check("entropy", r["entropy"], f["H"], f["H_e"])
-        check("lse", r["lse"], stored(f["lse"]), f["lse_e"])
+        top = float(np.finfo(np.float32).max)
+        check("lse", r["lse"], np.where(np.isinf(f["lse"]), f["lse"], f["lse"].clip(-top, top)), f["lse_e"])
         if K:
             top = order_topk(X, K)
             assert np.array_equal(r["top_idx"].cpu().numpy(), top)
@@ -77,3 +78,47 @@ def test_masked_rows_far_from_zero(dtype, offset, scale):
     r = run(x, t, scale, dh=1e9)
     assert bool((r["lse"].abs() >= 1024).all())
     compare(x, t, scale, r)
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("scale", [0.5, 1.0, 2.0, 1000.0])
+def test_finite_logits_whose_products_overflow(dtype, scale):
+    """Rows of the type's lowest and largest values, alone and beside others: the probabilities depend on differences
+    alone, in the forward and in its gradient; only what is itself past float32's range is infinite."""
+    V, low, top = 1501, torch.finfo(DT[dtype]).min, torch.finfo(DT[dtype]).max
+    x = torch.zeros(9, V)
+    x[0] = low
+    x[1], x[1, 40:] = -float("inf"), low     # equal ones, what is left of the row
+    x[2], x[2, 700] = low, -1e37
+    x[3] = top
+    x[4], x[4, 1499] = low, top
+    x[5, 3:900] = top
+    x[6] = -2e38
+    x[7] = -float("inf")
+    x[8], x[8, 0] = -float("inf"), low
+    x = x.to(DT[dtype]).cuda()
+    t = torch.tensor([5, 50, 700, 1500, 1499, 3, 0, 1, 0], dtype=torch.int32, device="cuda")
+    r = run(x, t, scale, K=7, dh=1.0)
+    compare(x, t, scale, r, K=7)
+    H = np.log([V, V - 40, 1, V, 1, 897, V, 1, 1])
+    assert np.allclose(f64(r["entropy"]), H, atol=1e-4) and r["lse"][7].item() == -float("inf")
+
+
+@pytest.mark.parametrize("scale", [0.7, 1.0, 3.0])
+def test_large_finite_logits(scale):
+    """Logits of any size between: equal ones are uniform, the next larger float is beside them or takes all."""
+    size = torch.logspace(4, 38, 400, dtype=torch.float64).float()
+    x = torch.cat([size, -size])[:, None].repeat(1, 601).cuda()
+    x[::2, 77] = torch.nextafter(x[::2, 77], torch.full_like(x[::2, 77], float("inf")))
+    t = torch.full((800,), 5, dtype=torch.int32, device="cuda")
+    compare(x, t, scale, run(x, t, scale, K=3), K=3)
+
+
+@pytest.mark.parametrize("N, V", [(2, 131072), (700, 16000)])
+def test_overflowing_products_in_other_divisions_of_a_row(N, V):
+    """The same in clusters of blocks and in narrow blocks."""
+    for value in (torch.finfo(torch.float32).min, 3e38):
+        x = torch.full((N, V), value, device="cuda")
+        x[0, V // 2:] = -float("inf")
+        t = torch.full((N,), V // 3, dtype=torch.int32, device="cuda")
+        compare(x, t, 2.0, run(x, t, 2.0, K=3), K=3)
