@@ -396,7 +396,8 @@ typedef struct {
  *   x, y [rows, D]; g [rows, D / gate_width]: log gates, at most 0 (a gate of -inf starts anew; with gates
  *   above 0 the product of a span's gates may overflow). A row of per-head gates has no alignment rule.
  *   offsets: int64 [P + 1] on the device, sequence p owns rows [offsets[p], offsets[p+1]), empty ones
- *   allowed; or NULL: P sequences of rows / P rows each (rows a multiple of P).
+ *   allowed; or NULL: P sequences of rows / P rows each (rows a multiple of P). Rows before offsets[0] and from
+ *   offsets[P] on belong to none: they are not read, and what y, dx and dg hold there stays.
  *   h0 (nullable: zeros) and hT (nullable) float32 [P, D]: the states before and after; hT may be h0; an
  *   empty sequence hands its state on.
  *   states (nullable) float32, sdm_glr_states_bytes: the state before every SDM_GLR_CHUNK-th row of each

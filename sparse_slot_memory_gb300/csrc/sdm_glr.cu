@@ -690,12 +690,18 @@ __global__ void __launch_bounds__(32 * kChain) glr_chain_kernel(const GlrArgs a)
     });
 }
 
-// dg of a head wider than a tile: the sum of its tiles' parts, in tile order.
+// dg of a head wider than a tile: the sum of its tiles' parts, in tile order, of the rows from the first sequence's first to
+// the last one's last. Rows of no sequence have no parts, and their dg stays as it is.
 template <typename GT>
 __global__ void __launch_bounds__(256) glr_dg_kernel(const GlrArgs a) {
     start_dependent();
     const int64_t n = a.rows * a.H;
-    for (int64_t i = blockIdx.x * int64_t(256) + threadIdx.x; i < n; i += gridDim.x * int64_t(256)) {
+    int64_t first = 0, end = a.rows;
+    if (a.offsets != nullptr) {
+        first = min(max(a.offsets[0], int64_t(0)), a.rows);
+        end = min(a.offsets[a.P], a.rows);
+    }
+    for (int64_t i = first * a.H + blockIdx.x * int64_t(256) + threadIdx.x; i < end * a.H; i += gridDim.x * int64_t(256)) {
         float s = a.part[i];
         for (int k = 1; k < a.tiles_per_head; ++k) s += a.part[k * n + i];
         st1(static_cast<GT*>(a.dg) + i / a.H * a.dg_ld + i % a.H, s);

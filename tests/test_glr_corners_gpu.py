@@ -1,0 +1,73 @@
+"""Corners of the gated linear recurrence: rows that belong to no sequence."""
+
+import numpy as np
+import pytest
+import torch
+
+import sparse_slot_memory_gb300 as sdm
+from operators_testlib import check, f64, glr_backward, glr_forward
+
+pytestmark = pytest.mark.gpu
+
+DT = {"f32": torch.float32, "bf16": torch.bfloat16}
+
+
+def case(rows, cuts, D, gw, xt="f32", gt="f32", seed=0, mean=3.0):
+    """Sequences between the `cuts` of `rows` rows, their states and their gradients."""
+    gen = torch.Generator().manual_seed(seed)
+    P, H = len(cuts) - 1, D // gw
+    c = {"spec": sdm.GlrSpec(P=P, rows=rows, D=D, gate_width=gw, x_dtype=xt, g_dtype=gt), "gw": gw,
+         "cuts": np.asarray(cuts, np.int64)}
+    c["x"], c["dy"] = (torch.randn(rows, D, generator=gen).to(DT[xt]).cuda() for _ in range(2))
+    c["g"] = torch.nn.functional.logsigmoid(torch.randn(rows, H, generator=gen) + mean).to(DT[gt]).cuda()
+    c["offsets"] = torch.from_numpy(c["cuts"]).cuda()
+    c["h0"], c["dhT"] = (torch.randn(P, D, generator=gen).cuda() for _ in range(2))
+    return c
+
+
+def run(c, fill=float("nan")):
+    """Every output full of `fill` beforehand, and so the states and the workspace."""
+    s = c["spec"]
+    r = {k: torch.full_like(c["x"], fill) for k in ("y", "dx")}
+    r["dg"] = torch.full_like(c["g"], fill)
+    r["hT"], r["dh0"] = (torch.full_like(c["h0"], fill) for _ in range(2))
+    states, ws = sdm.alloc_glr_states(s).fill_(fill), sdm.alloc_glr_workspace(s)
+    ws[:ws.numel() // 4 * 4].view(torch.float32).fill_(fill)
+    st = torch.zeros(1, dtype=torch.int32, device="cuda")
+    sdm.glr_forward(s, c["x"], c["g"], r["y"], offsets=c["offsets"], h0=c["h0"], hT=r["hT"], states=states, status=st)
+    sdm.glr_backward(s, c["x"], c["g"], c["dy"], states, r["dx"], r["dg"], ws, offsets=c["offsets"], dhT=c["dhT"],
+                     dh0=r["dh0"], status=st)
+    r["status"] = int(st.item())
+    return r
+
+
+def compare(c, r, rows=slice(None)):
+    s, cuts = c["spec"], c["cuts"]
+    x, g, dy, h0, dhT = (f64(c[k]) for k in ("x", "g", "dy", "h0", "dhT"))
+    with np.errstate(invalid="ignore"):
+        h, he, hT, hTe = glr_forward(x, g, cuts, h0, c["gw"])
+        dx, dxe, dg, dge, dh0, dh0e = glr_backward(x, g, cuts, h0, c["gw"], dy, dhT)
+        check("y", r["y"][rows], h[rows], he[rows], DT[s.x_dtype])
+        check("hT", r["hT"], hT, hTe)
+        check("dx", r["dx"][rows], dx[rows], dxe[rows], DT[s.x_dtype])
+        check("dg", r["dg"][rows], dg[rows], dge[rows], DT[s.g_dtype])
+        check("dh0", r["dh0"], dh0, dh0e)
+
+
+@pytest.mark.parametrize("D, gw", [(264, 1), (256, 64), (512, 256), (264, 132)])
+@pytest.mark.parametrize("rows, cuts", [(500, [70, 70, 300, 431]), (9000, [100, 8500]), (40, [0, 10, 30]), (30, [12, 12])])
+def test_rows_of_no_sequence_stay_as_they_are(rows, cuts, D, gw):
+    """Offsets may leave rows before the first and behind the last sequence (a packed batch's padding), whatever the
+    heads' width is: nothing is written there, and nothing read."""
+    c = case(rows, cuts, D, gw)
+    inside = slice(cuts[0], cuts[-1])
+    outside = torch.ones(rows, dtype=torch.bool, device="cuda")
+    outside[inside] = False
+    for k in ("x", "g", "dy"):
+        c[k][outside] = float("nan")
+    for fill in (float("nan"), 7.0):
+        r = run(c, fill)
+        assert r["status"] == 0
+        for k in ("y", "dx", "dg"):
+            assert bool((torch.isnan(r[k][outside]) if fill != fill else r[k][outside] == fill).all()), k
+        compare(c, r, inside)
