@@ -471,9 +471,9 @@ sdm_status sdm_qk_norm_rope(const sdm_rope_shape* shape, const void* q, int64_t 
 /*
  * Its backward, from the outputs' gradients and the forward's inputs: e = the gradient turned back by the angle,
  * dw += e x r over tokens and heads (r the row's rsqrt), and with u = e w: dx = r (u - x r^2 mean(u x)). Padding
- * tokens get zeros and add nothing. dwq, dwk float32 [hd] (nullable), written; ws: sdm_rope_workspace_bytes,
- * 16-byte aligned (may be NULL with norm 0 or where neither is asked for). dq may be dq_out, dk may be dk_out
- * (same ld).
+ * tokens get zeros and add nothing. dwq, dwk float32 [hd] (nullable), written (with zeros for norm 0); ws:
+ * sdm_rope_workspace_bytes, 16-byte aligned (may be NULL with norm 0 or where neither is asked for). dq may be dq_out,
+ * dk may be dk_out (same ld).
  */
 size_t sdm_rope_workspace_bytes(const sdm_rope_shape* shape);
 sdm_status sdm_qk_norm_rope_backward(const sdm_rope_shape* shape, const void* dq_out, int64_t dqo_ld,

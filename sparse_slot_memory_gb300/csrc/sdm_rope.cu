@@ -601,8 +601,8 @@ extern "C" sdm_status sdm_qk_norm_rope_backward(const sdm_rope_shape* shape, con
         return launch_dependent(rope_bwd_kernel<decltype(t), decltype(u)::value, decltype(inter)::value>, dim3(static_cast<unsigned>(blocks)),
                                 dim3(kThreads), smem, cs, a, lanes);
     });
-    if (e == cudaSuccess && sums)
+    if (e == cudaSuccess && (dwq != nullptr || dwk != nullptr))   // without the norm the sum of no blocks' rows: 0
         e = launch_dependent(rope_dw_kernel, dim3(static_cast<unsigned>((2 * shape->hd + 31) / 32)), dim3(32, 32), 0, cs,
-                             static_cast<const float*>(ws), blocks, shape->hd, dwq, dwk);
+                             static_cast<const float*>(ws), sums ? blocks : 0, shape->hd, dwq, dwk);
     return e == cudaSuccess ? SDM_OK : SDM_ERR_CUDA;
 }
