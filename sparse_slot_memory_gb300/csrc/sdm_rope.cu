@@ -178,7 +178,7 @@ constexpr int heads_at_once() {
     return U > 1 ? 1 : sizeof(T) == 2 ? 4 : 2;
 }
 
-// The token's position, or -1 for a padding token.
+// The token's position, or -1 for a padding token, which takes no row of the table.
 __device__ __forceinline__ int position(const RopeArgs& s, int t) {
     const int pos = s.pos[t];
     if (pos < s.max_pos) return pos < 0 ? -1 : pos;
@@ -240,9 +240,12 @@ __global__ void __launch_bounds__(kThreads, U == 1 ? fwd_blocks(sizeof(T) == 2) 
                 }
             Weighted wt[U];
 #pragma unroll
-            for (int i = 0; i < U; ++i)
-                wt[i] = weighted(turn_of(s, max(p, 0), pl.f[i]),
-                                 weights<INTER>(s.norm ? (isq ? s.wq : s.wk) : nullptr, pl.a[i], pl.b[i]));
+            for (int i = 0; i < U; ++i) {
+                if (FULL || p >= 0)
+                    wt[i] = weighted(turn_of(s, p, pl.f[i]), weights<INTER>(s.norm ? (isq ? s.wq : s.wk) : nullptr, pl.a[i], pl.b[i]));
+                else   // a padding token, not read: zeros whatever the table and the weights hold
+                    wt[i] = {quad(0.f), quad(0.f), quad(0.f), quad(0.f)};
+            }
             at.next(ct);
             pos = at.u < units ? position(s, at.t) : -1;
             float ss[HU];
@@ -260,7 +263,7 @@ __global__ void __launch_bounds__(kThreads, U == 1 ? fwd_blocks(sizeof(T) == 2) 
 #pragma unroll
             for (int h = 0; h < HU; ++h) {
                 float r = s.norm ? rsqrtf(fmaf(ss[h], inv, s.eps)) : 1.f;
-                if (!FULL && p < 0) r = 0.f;   // a padding token, not read: zeros
+                if (!FULL && p < 0) r = 0.f;
 #pragma unroll
                 for (int i = 0; i < U; ++i) {
                     const Pairs o = times(turned(pairs<INTER>(ra[h][i], rb[h][i]), wt[i], WHOLE, pl.f[i] >= 0), r);
@@ -334,7 +337,7 @@ __global__ void __launch_bounds__(kThreads, U == 1 ? 2 : 1) rope_bwd_kernel(cons
                     }
                 Turn turn[U];
 #pragma unroll
-                for (int i = 0; i < U; ++i) turn[i] = turn_of(s, max(p, 0), pl.f[i]);
+                for (int i = 0; i < U; ++i) turn[i] = turn_of(s, p, FULL || p >= 0 ? pl.f[i] : -1);
                 at.next(chunks);
                 pos = at.u < units ? position(s, at.t) : -1;
                 float sums[2 * HU];
@@ -355,7 +358,7 @@ __global__ void __launch_bounds__(kThreads, U == 1 ? 2 : 1) rope_bwd_kernel(cons
                 if (s.norm) lanes_sum(sums, lanes);
 #pragma unroll
                 for (int h = 0; h < HU; ++h) {
-                    // dx = r (t + k x); a padding token or a head past the last was not read, r = 0 leaves zeros
+                    // dx = r (t + k x); a padding token or a head past the last was not read and adds nothing
                     float r = 1.f, k = 0.f;
                     if (s.norm) {
                         r = rsqrtf(fmaf(sums[2 * h], inv, s.eps));
@@ -373,6 +376,7 @@ __global__ void __launch_bounds__(kThreads, U == 1 ? 2 : 1) rope_bwd_kernel(cons
                             d = times(e, wt[i]);
                             d = {fma4(v.a, kr, d.a), fma4(v.b, kr, d.b)};
                         }
+                        if (!FULL && p < 0) d = {quad(0.f), quad(0.f)};   // whatever the weights are
                         if ((FULL || h < n) && pl.on[i]) st_pairs<INTER>(y + h * s.hd + pl.a[i], y + h * s.hd + pl.b[i], d);
                     }
                 }
