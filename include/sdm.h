@@ -402,6 +402,7 @@ typedef struct {
  *   empty sequence hands its state on.
  *   states (nullable) float32, sdm_glr_states_bytes: the state before every SDM_GLR_CHUNK-th row of each
  *   sequence, for the backward (row offsets[p] / SDM_GLR_CHUNK + p + j holds sequence p's j-th).
+ *   y may be x (same ld); long sequences of few channels take longer then.
  * Spans of rows are computed apart and joined in a fixed order, so a sequence cut in two calls agrees with one
  * call to rounding, not bit for bit.
  */
@@ -415,8 +416,8 @@ sdm_status sdm_glr_forward(const sdm_glr_shape* shape, const void* x, int64_t x_
  *   dx_t = l_t,   dg_t = exp(g_t) l_t h_{t-1} (summed over the gate's channels),   dh0 = exp(g_1) l_1
  * (dhT for an empty sequence). h_{t-1} is computed again from x and the forward's states, so the rounding of
  * y enters no gradient. x, g, offsets as the forward had them; dy, dx [rows, D]; dg [rows, D / gate_width];
- * dhT, dh0 (nullable) float32 [P, D]. ws: sdm_glr_workspace_bytes, 16-byte aligned (used where gate_width >
- * 128; may be NULL otherwise).
+ * dhT, dh0 (nullable) float32 [P, D]; dh0 may be dhT; dx may be dy or x (same ld; as for y above). ws:
+ * sdm_glr_workspace_bytes, 16-byte aligned (used where gate_width > 128; may be NULL otherwise).
  */
 size_t sdm_glr_workspace_bytes(const sdm_glr_shape* shape);
 sdm_status sdm_glr_backward(const sdm_glr_shape* shape, const void* x, int64_t x_ld, const void* g, int64_t g_ld,

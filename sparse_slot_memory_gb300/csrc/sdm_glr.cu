@@ -808,14 +808,17 @@ size_t part_bytes(const GlrArgs& a) {
 // leave SMs idle and the sequences are long, they are cut into segments for two blocks an SM, at the price of reading
 // the inputs twice (1 x 8192 x 1024: 97 us with clusters, 50 with segments; 1 x 4096 x 256: 48 and 47; 65537 x 512
 // float32: 893 and 185), unequal ones four times earlier (8 sequences, 24000 x 256: 148 and 69).
+//
+// An output in place of an input (`in_place`) is not cut: the segments' pairs would lie over rows that are still to be
+// read. Uncut, every row of a step is in registers before the step writes.
 constexpr int64_t kSlots = 304, kBusy = 228, kSegmentRows = 256, kLong = 4096;
 
-void divide(GlrArgs* a) {
+void divide(GlrArgs* a, bool in_place) {
     const int64_t units = static_cast<int64_t>(a->tiles) * a->P, steps = (a->len + SDM_GLR_CHUNK - 1) / SDM_GLR_CHUNK;
     const bool equal = a->offsets == nullptr || a->P == 1;
     a->cluster = 1;
     a->seg = 0;
-    if (units * kMaxCluster < kBusy && a->len * (equal ? 1 : 4) > kLong) {
+    if (!in_place && units * kMaxCluster < kBusy && a->len * (equal ? 1 : 4) > kLong) {
         const int64_t cuts = kSlots / units;   // of a sequence
         a->seg = std::max(kSegmentRows, (a->len + cuts - 1) / cuts);
         a->seg = (a->seg + SDM_GLR_CHUNK - 1) / SDM_GLR_CHUNK * SDM_GLR_CHUNK;
@@ -880,7 +883,7 @@ extern "C" sdm_status sdm_glr_forward(const sdm_glr_shape* shape, const void* x,
     if (static_cast<int64_t>(a.tiles) * (a.P + a.rows / SDM_GLR_CHUNK) > 0x7FFFFFFF / kMaxCluster) return SDM_ERR_SHAPE;
     a.x = x; a.x_ld = x_ld; a.g = g; a.g_ld = g_ld; a.y = y; a.y_ld = y_ld;
     a.offsets = offsets; a.h0 = h0; a.hT = hT; a.states = states; a.status = status;
-    divide(&a);
+    divide(&a, y == x || y == g);
     const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
     const cudaError_t e = by_type(shape, [&](auto xt, auto gt, auto perch) {
         constexpr bool PC = decltype(perch)::value;
@@ -929,7 +932,7 @@ extern "C" sdm_status sdm_glr_backward(const sdm_glr_shape* shape, const void* x
     a.dx = dx; a.dx_ld = dx_ld; a.dg = dg; a.dg_ld = dg_ld;
     a.offsets = offsets; a.dhT = dhT; a.dh0 = dh0; a.states = const_cast<float*>(states); a.status = status;
     a.part = static_cast<float*>(ws);
-    divide(&a);
+    divide(&a, dx == x || dx == dy || dx == g);
     const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t e = by_type(shape, [&](auto xt, auto gt, auto perch) {
         constexpr bool PC = decltype(perch)::value;

@@ -137,7 +137,8 @@ def glr_forward(spec: GlrSpec, x, g, y, offsets=None, h0=None, hT=None, states=N
     ``x``, ``y`` [rows, D]; ``g`` [rows, D / gate_width] log gates, at most 0; ``offsets`` (optional) int64
     [P + 1]: sequence p owns rows offsets[p] .. offsets[p+1] - 1, else all have rows / P rows; ``h0``, ``hT``
     (optional) float32 [P, D]: the states before and after (may be one tensor); ``states`` (optional, from
-    ``alloc_glr_states``) receives what ``glr_backward`` needs."""
+    ``alloc_glr_states``) receives what ``glr_backward`` needs. ``y`` may be ``x``, which
+    costs the division of long sequences of few channels into segments."""
     xt, gt, xs, gs, PD = _glr_kinds(spec)
     D, G = xs[1], gs[1]
     st = _abi.load().sdm_glr_forward(
@@ -151,7 +152,8 @@ def glr_backward(spec: GlrSpec, x, g, dy, states, dx, dg, ws=None, offsets=None,
                  stream=None):
     """sdm_glr_backward: the gradients ``dx`` [rows, D], ``dg`` [rows, D / gate_width] and ``dh0`` (optional,
     float32 [P, D]) from ``dy`` and ``dhT`` (optional: the gradient of the states after). ``x``, ``g``, ``offsets`` and
-    ``states`` are those of the forward; ``ws`` (from ``alloc_glr_workspace``) is needed where gate_width > 128."""
+    ``states`` are those of the forward; ``ws`` (from ``alloc_glr_workspace``) is needed where gate_width > 128.
+    ``dx`` may be ``dy`` or ``x``."""
     xt, gt, xs, gs, PD = _glr_kinds(spec)
     D, G = xs[1], gs[1]
     if states is None:

@@ -1,4 +1,4 @@
-"""Corners of the gated linear recurrence: rows that belong to no sequence."""
+"""Corners of the gated linear recurrence: rows that belong to no sequence, outputs in place of inputs."""
 
 import numpy as np
 import pytest
@@ -71,3 +71,27 @@ def test_rows_of_no_sequence_stay_as_they_are(rows, cuts, D, gw):
         for k in ("y", "dx", "dg"):
             assert bool((torch.isnan(r[k][outside]) if fill != fill else r[k][outside] == fill).all()), k
         compare(c, r, inside)
+
+
+@pytest.mark.parametrize("xt, gt", [("bf16", "f32"), ("f32", "f32"), ("bf16", "bf16")])
+@pytest.mark.parametrize("rows, cuts, D, gw", [(9001, [0, 9001], 12, 4), (8400, [0, 4200, 8400], 132, 1), (300, [0, 300], 132, 1),
+                                               (12000, [0, 0, 9000, 9003, 12000], 64, 1)])
+def test_outputs_in_place_of_inputs(rows, cuts, D, gw, xt, gt):
+    """y over x, dx over dy and dx over x, also where rows of other places are divided into segments."""
+    c = case(rows, cuts, D, gw, xt, gt, seed=2)
+    s, want = c["spec"], run(c)
+    compare(c, want)
+    X, G, H0 = f64(c["x"]), f64(c["g"]), f64(c["h0"])
+    y, states, hT = c["x"].clone(), sdm.alloc_glr_states(s), torch.empty_like(c["h0"])
+    sdm.glr_forward(s, y, c["g"], y, offsets=c["offsets"], h0=c["h0"], hT=hT, states=states)
+    h, he, last, laste = glr_forward(X, G, c["cuts"], H0, gw)
+    check("y", y, h, he, DT[xt])
+    check("hT", hT, last, laste)
+    dx, dxe, dg, dge, dh0, dh0e = glr_backward(X, G, c["cuts"], H0, gw, f64(c["dy"]), f64(c["dhT"]))
+    for over in ("dy", "x"):
+        args = {k: c[k].clone() for k in ("x", "dy")}
+        out, got, first = args[over], torch.empty_like(c["g"]), torch.empty_like(c["h0"])
+        sdm.glr_backward(s, args["x"], c["g"], args["dy"], states, out, got, offsets=c["offsets"], dhT=c["dhT"], dh0=first)
+        check("dx", out, dx, dxe, DT[xt])
+        check("dg", got, dg, dge, DT[gt])
+        check("dh0", first, dh0, dh0e)
