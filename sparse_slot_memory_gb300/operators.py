@@ -18,7 +18,7 @@ import math
 import torch
 
 from . import _abi
-from .api import _DT, _TORCH_DT, _check, _need, _ptr, _stream
+from .api import _DT, _TORCH_DT, _check, _cur_device, _need, _ptr, _stream
 
 _LAYOUT = {"half": 0, "interleaved": 1}
 
@@ -37,14 +37,25 @@ class _Spec:
 
 _Tensor = torch.Tensor
 
+# the device that the library launches on: the current one, asked for without torch.cuda's wrappers where torch has it
+_here = _cur_device if _cur_device is not None else torch.cuda.current_device
+
+
+def _refuse_place(t, name: str):
+    """A CPU tensor, or one of another GPU than the current one, whose stream the call would use."""
+    if not isinstance(t, _Tensor) or not t.is_cuda:
+        raise TypeError(f"{name}: expected a CUDA tensor (the library runs on the GPU only)")
+    if t.get_device() != _here():
+        raise ValueError(f"{name}: lies on GPU {t.get_device()}, the current one is GPU {_here()}")
+
 
 def _rows(t, dtype, shape, n, name: str, out: bool = False):
     """The address of a row array [rows, ..] whose rows hold n elements, and the distance between its rows in elements.
     The library reads bare pointers, so type, shape, place and layout are checked here."""
-    if t.__class__ is _Tensor and t.dtype is dtype and t.is_cuda and t.shape == shape and t.is_contiguous():
+    if (t.__class__ is _Tensor and t.dtype is dtype and t.is_cuda and t.get_device() == _here() and t.shape == shape
+            and t.is_contiguous()):
         return t.data_ptr(), n
-    if not isinstance(t, _Tensor) or not t.is_cuda:
-        raise TypeError(f"{name}: expected a CUDA tensor (the library runs on the GPU only)")
+    _refuse_place(t, name)
     if t.dtype != dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
     if t.shape != shape:
@@ -66,9 +77,11 @@ def _small(t, dtype, numel: int, name: str):
     """The address of an optional contiguous array of at least ``numel`` elements."""
     if t is None:
         return None
-    if t.__class__ is _Tensor and t.dtype is dtype and t.is_cuda and t.numel() >= numel and t.is_contiguous():
+    if (t.__class__ is _Tensor and t.dtype is dtype and t.is_cuda and t.get_device() == _here() and t.numel() >= numel
+            and t.is_contiguous()):
         return t.data_ptr()
     _need(t, dtype, numel, name)
+    _refuse_place(t, name)
     return _ptr(t)
 
 
