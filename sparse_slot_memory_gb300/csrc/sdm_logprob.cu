@@ -76,7 +76,7 @@ struct LpArgs {
     float* top_vals;       // nullable [rows, K]
     int32_t* top_idx;      // nullable
     const float* lse_in;
-    const float* ent_in;
+    const float* ent_in;      // nullable without d_entropy
     const float* d_logp;
     const float* d_entropy;   // nullable
     void* dlogits;
@@ -634,7 +634,7 @@ __global__ void __launch_bounds__(kBwdThreads) lp_bwd_kernel(const LpArgs a, int
     const int t = a.targets[row];
     const float dl = t >= 0 && t < a.V ? a.d_logp[row] : 0.f;
     const float dh = a.d_entropy != nullptr ? a.d_entropy[row] : 0.f;
-    const float H = a.ent_in[row], lse = a.lse_in[row];
+    const float H = a.d_entropy != nullptr ? a.ent_in[row] : 0.f, lse = a.lse_in[row];
     if (part == 0 && threadIdx.x == 0 && t >= a.V && a.status != nullptr) atomicOr(a.status, SDM_DEV_BAD_TARGET);
     if (fabsf(lse) >= kFarLse) {
         // block-uniform and rare: z - lse from differences to the largest logit, or (lse -inf) a row of zeros
@@ -776,7 +776,8 @@ extern "C" sdm_status sdm_token_logprobs_backward(const sdm_logprob_shape* shape
     if (shape->rows == 0) return SDM_OK;
     if ((st = check_logits(shape, logits, ld, false)) != SDM_OK) return st;
     if ((st = check_logits(shape, dlogits, d_ld, true)) != SDM_OK) return st;
-    if (targets == nullptr || lse == nullptr || entropy == nullptr || d_logp == nullptr) return SDM_ERR_ARG;
+    if (targets == nullptr || lse == nullptr || (entropy == nullptr && d_entropy != nullptr) || d_logp == nullptr)
+        return SDM_ERR_ARG;
     if (!checks::aligned_all(4, {targets, lse, entropy, d_logp, d_entropy, status})) return SDM_ERR_ALIGN;
     LpArgs a;
     memset(&a, 0, sizeof(a));

@@ -122,3 +122,22 @@ def test_overflowing_products_in_other_divisions_of_a_row(N, V):
         x[0, V // 2:] = -float("inf")
         t = torch.full((N,), V // 3, dtype=torch.int32, device="cuda")
         compare(x, t, 2.0, run(x, t, 2.0, K=3), K=3)
+
+
+def test_no_entropy_without_its_gradient():
+    """Without a gradient of the entropy the backward takes none, and an entropy that is given does not matter."""
+    x, t = masked(5, 2003, "f32", 1.0)
+    for offset in (0.0, 4000.0):
+        x = x + offset
+        want = run(x, t, 1.0)
+        s = sdm.LogprobSpec(rows=5, V=2003, dtype="f32")
+        outs = []
+        for entropy in (None, want["entropy"], torch.full((5,), float("nan"), device="cuda")):
+            outs.append(torch.full_like(x, float("nan")))
+            sdm.token_logprobs_backward(s, x, t, want["lse"], entropy, want["d_logp"], outs[-1])
+        d, e = logprobs_backward(f64(x), t.cpu().numpy(), 1.0, f64(want["d_logp"]), None)
+        check("dlogits", outs[0], d, e)
+        assert torch.equal(outs[0], outs[1]) and torch.equal(outs[0], outs[2])
+        with pytest.raises(sdm.SdmError) as err:
+            sdm.token_logprobs_backward(s, x, t, want["lse"], None, want["d_logp"], outs[0], d_entropy=want["d_entropy"])
+        assert err.value.status == -1
