@@ -4,7 +4,6 @@
 #pragma once
 
 #include <cstdint>
-#include <initializer_list>
 
 #include "sdm_internal.cuh"
 
@@ -12,12 +11,6 @@ namespace sdm {
 namespace checks {
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-// Whether every pointer (NULL among them) lies on a multiple of n bytes.
-inline bool aligned_all(unsigned n, std::initializer_list<const void*> ps) {
-    for (const void* p : ps)
-        if (reinterpret_cast<uintptr_t>(p) % n != 0) return false;
-    return true;
-}
 
 inline sdm_status check_shape(const sdm_shape* s) {
     if (s == nullptr) return SDM_ERR_ARG;

@@ -32,9 +32,7 @@
 #include <cstring>
 #include <type_traits>
 
-#include "sdm_checks.cuh"
-#include "sdm_internal.cuh"
-#include "sdm_rows.cuh"
+#include "sdm_operators.cuh"
 
 namespace sdm {
 namespace {
@@ -232,7 +230,6 @@ struct RawGate;
 template <typename GT>
 struct RawGate<GT, true> {
     Raw4<GT> v;
-    __device__ __forceinline__ void ld_plain(const GT* p) { v.ld_plain(p); }
     __device__ __forceinline__ void zero() { v.zero(); }
     __device__ __forceinline__ Quad exps() const {
         float o[4];
@@ -245,22 +242,26 @@ struct RawGate<GT, true> {
 template <typename GT>
 struct RawGate<GT, false> {
     GT v;
-    __device__ __forceinline__ void ld_plain(const GT* p) { v = *p; }
     __device__ __forceinline__ void zero() { v = GT(0.f); }
     __device__ __forceinline__ Quad exps() const { return quad(exp2_gate(widen(v) * kLog2e)); }
 };
+
+template <typename GT>
+__device__ __forceinline__ void ld_plain(RawGate<GT, true>& r, const GT* p) { rows::ld_plain(r.v, p); }
+template <typename GT>
+__device__ __forceinline__ void ld_plain(RawGate<GT, false>& r, const GT* p) { r.v = *p; }
 
 // ROWS rows of a lane's columns; those from `live` on are zeros (the identity: gate 1, nothing added).
 template <int ROWS, typename Row, typename T>
 __device__ __forceinline__ void load_rows(Row (&r)[ROWS], const T* p, int64_t ld, int live) {
     if (live == ROWS) {   // warp-uniform
 #pragma unroll
-        for (int i = 0; i < ROWS; ++i) r[i].ld_plain(p + i * ld);
+        for (int i = 0; i < ROWS; ++i) ld_plain(r[i], p + i * ld);
     } else {
 #pragma unroll
         for (int i = 0; i < ROWS; ++i) {
             r[i].zero();
-            if (i < live) r[i].ld_plain(p + i * ld);
+            if (i < live) ld_plain(r[i], p + i * ld);
         }
     }
 }
@@ -740,9 +741,9 @@ __global__ void __launch_bounds__(256) glr_step_kernel(const StepArgs a) {
     }
     float* const st = a.state + s * a.s_ld + col;
     ld4cg(st, h);
-    x.ld_plain(static_cast<const XT*>(a.x) + r * a.x_ld + col);
+    ld_plain(x, static_cast<const XT*>(a.x) + r * a.x_ld + col);
     RawGate<GT, PERCH> gr;
-    gr.ld_plain(static_cast<const GT*>(a.g) + r * a.g_ld + (PERCH ? col : col / a.gw));
+    ld_plain(gr, static_cast<const GT*>(a.g) + r * a.g_ld + (PERCH ? col : col / a.gw));
     const Quad o = fma4(gr.exps(), quad(h), quad(x));
     st4(st, o);
     st4(y, o);

@@ -162,11 +162,6 @@ struct DWArgs {
     int64_t items;      // P * B * nsl
 };
 
-// The first instruction of a kernel that is launched as a programmatic dependent: waits for the kernel before. It does not
-// let the kernel behind start while it runs: the waiting blocks cost more than the launch they hide (8 x 131072 token
-// log probabilities 10.2 us with, 7.9 without; a short rotation 14.6 and 13.7; long kernels equal).
-__device__ __forceinline__ void start_dependent() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-
 // A launch as a programmatic dependent of the previous kernel in the stream: its CTAs may be
 // scheduled before that kernel completes (onto SMs it leaves idle) and wait in the kernel
 // (griddepcontrol.wait) until it has completed and its memory is visible. Every kernel launched so
@@ -184,26 +179,6 @@ cudaError_t launch_dependent(void (*kernel)(Params...), dim3 grid, dim3 block, s
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
-}
-
-// A launch of clusters of `cluster` blocks (a multiple of them), as a programmatic dependent.
-template <typename... Params, typename... Args>
-cudaError_t launch_cluster(void (*kernel)(Params...), dim3 grid, dim3 block, int cluster, cudaStream_t stream,
-                           Args&&... args) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = block;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[2];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = cluster;
-    attr[1].val.clusterDim.y = 1;
-    attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
 }
 

@@ -31,9 +31,7 @@
 #include <cstring>
 #include <type_traits>
 
-#include "sdm_checks.cuh"
-#include "sdm_internal.cuh"
-#include "sdm_rows.cuh"
+#include "sdm_operators.cuh"
 
 namespace sdm {
 namespace {

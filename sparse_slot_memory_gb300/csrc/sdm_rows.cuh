@@ -44,9 +44,7 @@ __device__ __forceinline__ void get4(const __nv_bfloat16* p, float (&o)[4]) {
     o[0] = __uint_as_float(v.x << 16); o[1] = __uint_as_float(v.x & 0xFFFF0000u);
     o[2] = __uint_as_float(v.y << 16); o[3] = __uint_as_float(v.y & 0xFFFF0000u);
 }
-// A lane's 4 columns kept in the storage type until used (8 bytes bf16 / 16 bytes f32 of registers). ld_plain is for
-// kernels that may start before the kernel before has written what they read (start_dependent): its wait makes those
-// writes visible to plain loads, while the read-only path asks for data that nothing writes while the kernel runs.
+// A lane's 4 columns kept in the storage type until used (8 bytes bf16 / 16 bytes f32 of registers).
 template <typename T>
 struct Raw4;
 template <>
@@ -55,7 +53,6 @@ struct Raw4<float> {
     __device__ __forceinline__ void zero() { v = make_float4(0.f, 0.f, 0.f, 0.f); }
     __device__ __forceinline__ void ld(const float* p) { v = __ldg(reinterpret_cast<const float4*>(p)); }
     __device__ __forceinline__ void ld_cg(const float* p) { v = __ldcg(reinterpret_cast<const float4*>(p)); }
-    __device__ __forceinline__ void ld_plain(const float* p) { v = *reinterpret_cast<const float4*>(p); }
     __device__ __forceinline__ void get(float (&o)[4]) const { o[0] = v.x; o[1] = v.y; o[2] = v.z; o[3] = v.w; }
     __device__ __forceinline__ float operator[](int i) const { return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w; }
 };
@@ -65,7 +62,6 @@ struct Raw4<__nv_bfloat16> {
     __device__ __forceinline__ void zero() { v = make_uint2(0u, 0u); }
     __device__ __forceinline__ void ld(const __nv_bfloat16* p) { v = __ldg(reinterpret_cast<const uint2*>(p)); }
     __device__ __forceinline__ void ld_cg(const __nv_bfloat16* p) { v = __ldcg(reinterpret_cast<const uint2*>(p)); }
-    __device__ __forceinline__ void ld_plain(const __nv_bfloat16* p) { v = *reinterpret_cast<const uint2*>(p); }
     __device__ __forceinline__ void get(float (&o)[4]) const {
         o[0] = __uint_as_float(v.x << 16); o[1] = __uint_as_float(v.x & 0xFFFF0000u);
         o[2] = __uint_as_float(v.y << 16); o[3] = __uint_as_float(v.y & 0xFFFF0000u);
@@ -113,8 +109,6 @@ struct Raw8<__nv_bfloat16> {
 };
 
 // store: f32 as is, bf16 rounded to nearest even
-__device__ __forceinline__ void st1(float* p, float v) { *p = v; }
-__device__ __forceinline__ void st1(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 __device__ __forceinline__ void st4(float* p, const float (&o)[4]) {
     *reinterpret_cast<float4*>(p) = make_float4(o[0], o[1], o[2], o[3]);
 }
@@ -218,82 +212,6 @@ __device__ __forceinline__ float tsum16(const float (&v)[16], int lane) {
     float x = keep + __shfl_xor_sync(kFull, send, 8);   // index lane & 15
     x += __shfl_xor_sync(kFull, x, 16);
     return x;
-}
-
-// Two float32 in one 64-bit register pair: one instruction multiplies, adds or multiply-adds both (each rounded as the
-// scalar instruction rounds it).
-__device__ __forceinline__ uint64_t pack2(float a, float b) {
-    uint64_t o;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(o) : "f"(a), "f"(b));
-    return o;
-}
-__device__ __forceinline__ void unpack2(uint64_t v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t o;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(o) : "l"(a), "l"(b), "l"(c));
-    return o;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-    uint64_t o;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(o) : "l"(a), "l"(b));
-    return o;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-    uint64_t o;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(o) : "l"(a), "l"(b));
-    return o;
-}
-
-// Four columns as two pairs of float32.
-struct Quad {
-    uint64_t lo, hi;
-};
-__device__ __forceinline__ Quad quad(const float (&v)[4]) { return {pack2(v[0], v[1]), pack2(v[2], v[3])}; }
-__device__ __forceinline__ Quad quad(float v) { return {pack2(v, v), pack2(v, v)}; }
-__device__ __forceinline__ void floats(const Quad& q, float (&v)[4]) {
-    unpack2(q.lo, v[0], v[1]);
-    unpack2(q.hi, v[2], v[3]);
-}
-__device__ __forceinline__ Quad fma4(const Quad& a, const Quad& b, const Quad& c) { return {fma2(a.lo, b.lo, c.lo), fma2(a.hi, b.hi, c.hi)}; }
-__device__ __forceinline__ Quad mul4(const Quad& a, const Quad& b) { return {mul2(a.lo, b.lo), mul2(a.hi, b.hi)}; }
-__device__ __forceinline__ Quad add4(const Quad& a, const Quad& b) { return {add2(a.lo, b.lo), add2(a.hi, b.hi)}; }
-template <typename T>
-__device__ __forceinline__ Quad quad(const Raw4<T>& r) {
-    float v[4];
-    r.get(v);
-    return quad(v);
-}
-__device__ __forceinline__ Raw4<float> load4(const float* p) {
-    Raw4<float> r;
-    r.ld_plain(p);
-    return r;
-}
-__device__ __forceinline__ Quad quad_at(const float* p) {   // 16 bytes of shared memory
-    float v[4];
-    get4(p, v);
-    return quad(v);
-}
-template <typename T>
-__device__ __forceinline__ void st4(T* p, const Quad& q) {
-    float v[4];
-    floats(q, v);
-    st4(p, v);
-}
-
-// The blocks of a cluster: this one's rank, the barrier in its two halves (release / acquire of every thread's accesses;
-// relaxed: the arrival alone), and the address of another block's copy of a shared variable.
-__device__ __forceinline__ uint32_t cluster_rank() {
-    uint32_t r;
-    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_arrive_relaxed() { asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory"); }
-__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
-__device__ __forceinline__ uint32_t remote_address(const void* p, uint32_t rank) {
-    uint32_t a = static_cast<uint32_t>(__cvta_generic_to_shared(p));
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(a), "r"(rank));
-    return a;
 }
 
 }  // namespace rows
