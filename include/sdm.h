@@ -395,6 +395,7 @@ typedef struct {
  * for the rows of each sequence in order, in float32.
  *   x, y [rows, D]; g [rows, D / gate_width]: log gates, at most 0 (a gate of -inf starts anew; with gates
  *   above 0 the product of a span's gates may overflow). A row of per-head gates has no alignment rule.
+ *   A product of gates below float32's range counts as 0: an infinite state may be NaN behind such a span.
  *   offsets: int64 [P + 1] on the device, sequence p owns rows [offsets[p], offsets[p+1]), empty ones
  *   allowed; or NULL: P sequences of rows / P rows each (rows a multiple of P). Rows before offsets[0] and from
  *   offsets[P] on belong to none: they are not read, and what y, dx and dg hold there stays.

@@ -1,4 +1,5 @@
-"""Corners of the gated linear recurrence: rows that belong to no sequence, outputs in place of inputs."""
+"""Corners of the gated linear recurrence: rows that belong to no sequence, outputs in place of inputs, and gates of -inf, NaN and
+infinities in sequences that several blocks walk."""
 
 import numpy as np
 import pytest
@@ -6,6 +7,7 @@ import torch
 
 import sparse_slot_memory_gb300 as sdm
 from operators_testlib import check, f64, glr_backward, glr_forward
+from operators_testlib import check as bound
 
 pytestmark = pytest.mark.gpu
 
@@ -41,8 +43,17 @@ def run(c, fill=float("nan")):
     return r
 
 
-def compare(c, r, rows=slice(None)):
+def finite(v):
+    """v with NaN in the place of infinities."""
+    if isinstance(v, torch.Tensor):
+        return torch.where(torch.isfinite(v), v, float("nan"))
+    return np.where(np.isfinite(v), v, np.nan)
+
+
+def compare(c, r, rows=slice(None), kinds=True):
+    """`kinds`: infinities and NaN are told apart."""
     s, cuts = c["spec"], c["cuts"]
+    check = lambda name, got, want, *tol: bound(name, *((got, want) if kinds else (finite(got), finite(want))), *tol)
     x, g, dy, h0, dhT = (f64(c[k]) for k in ("x", "g", "dy", "h0", "dhT"))
     with np.errstate(invalid="ignore"):
         h, he, hT, hTe = glr_forward(x, g, cuts, h0, c["gw"])
@@ -95,3 +106,24 @@ def test_outputs_in_place_of_inputs(rows, cuts, D, gw, xt, gt):
         check("dx", out, dx, dxe, DT[xt])
         check("dg", got, dg, dge, DT[gt])
         check("dh0", first, dh0, dh0e)
+
+
+@pytest.mark.parametrize("xt, gt", [("f32", "f32"), ("bf16", "bf16")])
+@pytest.mark.parametrize("rows, cuts, D, gw", [
+    (9001, [0, 9001], 12, 1), (9001, [0, 9001], 24, 12), (20000, [0, 9000, 9003, 20000], 64, 1),   # segments
+    (2100, [0, 700, 1400, 2100], 2048, 1), (700, [0, 300, 700], 2048, 128)])                        # clusters
+@pytest.mark.parametrize("mean, values", [(3.0, "nan"), (3.0, "inf"), (9.0, "inf")])
+def test_resets_nan_and_infinity_over_divided_sequences(rows, cuts, D, gw, xt, gt, mean, values):
+    """Gates of -inf and of 0, NaN or infinite inputs and gradients, in sequences that several blocks walk: they reach what
+    the definition says and nothing else. Infinities stay infinities while the gates' products stay in range (mean 9:
+    about e^-4 over all rows); past it they may be NaN."""
+    c = case(rows, cuts, D, gw, xt, gt, seed=5, mean=mean)
+    gen = torch.Generator().manual_seed(6)
+    for t in torch.randint(0, rows, (6,), generator=gen).tolist() + [cuts[1] - 1, cuts[1] % rows, 0, 64, 255, 256]:
+        c["g"][t, torch.randint(0, D // gw, (1,), generator=gen).item()] = -float("inf")
+    c["g"][rows // 2] = -float("inf")       # every channel of a row
+    c["g"][rows // 3:rows // 3 + 70] = 0.0
+    for value in (float("nan"),) if values == "nan" else (float("inf"), -float("inf")):
+        t, ch = torch.randint(0, rows, (2,), generator=gen).tolist(), torch.randint(0, D, (2,), generator=gen).tolist()
+        c["x"][t[0], ch[0]], c["dy"][t[1], ch[1]] = value, value
+    compare(c, run(c), kinds=mean > 3.0 or values == "nan")
