@@ -32,30 +32,37 @@ class _Spec:
 
     def c(self):
         cs = self.__dict__.get("_cref")
-        return self._keep("_cref", ctypes.byref(self._struct())) if cs is None else cs
+        if cs is None:
+            global _alone
+            _alone = torch.cuda.device_count() <= 1
+            cs = self._keep("_cref", ctypes.byref(self._struct()))
+        return cs
 
 
 _Tensor = torch.Tensor
+
+# Whether there is no other GPU for a tensor to lie on, so that its place needs no look (a microsecond of a call of seven).
+_alone = False
 
 # the device that the library launches on: the current one, asked for without torch.cuda's wrappers where torch has it
 _here = _cur_device if _cur_device is not None else torch.cuda.current_device
 
 
-def _refuse_place(t, name: str):
-    """A CPU tensor, or one of another GPU than the current one, whose stream the call would use."""
+def _place(t, name: str):
+    """Refuses a CPU tensor, and one of another GPU than the current one, whose stream the call would use."""
     if not isinstance(t, _Tensor) or not t.is_cuda:
         raise TypeError(f"{name}: expected a CUDA tensor (the library runs on the GPU only)")
-    if t.get_device() != _here():
+    if not _alone and t.get_device() != _here():
         raise ValueError(f"{name}: lies on GPU {t.get_device()}, the current one is GPU {_here()}")
 
 
 def _rows(t, dtype, shape, n, name: str, out: bool = False):
     """The address of a row array [rows, ..] whose rows hold n elements, and the distance between its rows in elements.
     The library reads bare pointers, so type, shape, place and layout are checked here."""
-    if (t.__class__ is _Tensor and t.dtype is dtype and t.is_cuda and t.get_device() == _here() and t.shape == shape
-            and t.is_contiguous()):
+    if (t.__class__ is _Tensor and t.dtype is dtype and t.is_cuda and (_alone or t.get_device() == _here())
+            and t.shape == shape and t.is_contiguous()):
         return t.data_ptr(), n
-    _refuse_place(t, name)
+    _place(t, name)
     if t.dtype != dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
     if t.shape != shape:
@@ -77,11 +84,11 @@ def _small(t, dtype, numel: int, name: str):
     """The address of an optional contiguous array of at least ``numel`` elements."""
     if t is None:
         return None
-    if (t.__class__ is _Tensor and t.dtype is dtype and t.is_cuda and t.get_device() == _here() and t.numel() >= numel
-            and t.is_contiguous()):
+    if (t.__class__ is _Tensor and t.dtype is dtype and t.is_cuda and (_alone or t.get_device() == _here())
+            and t.numel() >= numel and t.is_contiguous()):
         return t.data_ptr()
     _need(t, dtype, numel, name)
-    _refuse_place(t, name)
+    _place(t, name)
     return _ptr(t)
 
 

@@ -36,9 +36,21 @@ def test_tensors_of_another_gpu_are_refused(name, monkeypatch):
     call()
     torch.cuda.synchronize()
     other = torch.cuda.current_device() + 1
+    monkeypatch.setattr(operators, "_alone", False, raising=False)
     monkeypatch.setattr(operators, "_here", lambda: other, raising=False)
     with pytest.raises(ValueError, match=f"lies on GPU {other - 1}, the current one is GPU {other}"):
         call()
+
+
+def test_one_gpu_needs_no_look(monkeypatch):
+    """Where there is one GPU, no call asks where its tensors lie."""
+    call = calls()["glr_step"]
+    monkeypatch.setattr(torch.cuda, "device_count", lambda: 1)
+    call()
+    spec = sdm.GlrSpec(P=1, rows=8, D=8, x_dtype="f32")
+    spec.c()
+    monkeypatch.setattr(operators, "_here", lambda: 1 / 0, raising=False)
+    call()
 
 
 def test_optional_arrays_too(monkeypatch):
@@ -52,6 +64,8 @@ def test_optional_arrays_too(monkeypatch):
         def get_device(self):
             return here + 1
 
+    sdm.token_logprobs(lp, x, ids, row)
+    monkeypatch.setattr(operators, "_alone", False, raising=False)
     entropy = row.clone().as_subclass(Elsewhere)
     with pytest.raises(ValueError, match="entropy: lies on GPU"):
         sdm.token_logprobs(lp, x, ids, row, entropy=entropy)
