@@ -42,11 +42,8 @@ using namespace rows;
 constexpr int kTileCols = 128;   // channels of a tile
 constexpr int kMaxCluster = 8;
 
-// How a block divides its step of SDM_GLR_CHUNK rows: ROWS rows to each of kWarps warps.
-template <int ROWS>
-struct Split {
-    static constexpr int kWarps = SDM_GLR_CHUNK / ROWS, kThreads = kWarps * 32;
-};
+// How a block divides its step of SDM_GLR_CHUNK rows: kRows rows to each of kWarps warps.
+constexpr int kRows = 8, kWarps = SDM_GLR_CHUNK / kRows, kThreads = kWarps * 32;
 
 struct GlrArgs {
     const void* x;
@@ -251,15 +248,15 @@ __device__ __forceinline__ void ld_plain(RawGate<GT, true>& r, const GT* p) { ro
 template <typename GT>
 __device__ __forceinline__ void ld_plain(RawGate<GT, false>& r, const GT* p) { r.v = *p; }
 
-// ROWS rows of a lane's columns; those from `live` on are zeros (the identity: gate 1, nothing added).
-template <int ROWS, typename Row, typename T>
-__device__ __forceinline__ void load_rows(Row (&r)[ROWS], const T* p, int64_t ld, int live) {
-    if (live == ROWS) {   // warp-uniform
+// kRows rows of a lane's columns; those from `live` on are zeros (the identity: gate 1, nothing added).
+template <typename Row, typename T>
+__device__ __forceinline__ void load_rows(Row (&r)[kRows], const T* p, int64_t ld, int live) {
+    if (live == kRows) {   // warp-uniform
 #pragma unroll
-        for (int i = 0; i < ROWS; ++i) ld_plain(r[i], p + i * ld);
+        for (int i = 0; i < kRows; ++i) ld_plain(r[i], p + i * ld);
     } else {
 #pragma unroll
-        for (int i = 0; i < ROWS; ++i) {
+        for (int i = 0; i < kRows; ++i) {
             r[i].zero();
             if (i < live) ld_plain(r[i], p + i * ld);
         }
@@ -267,12 +264,12 @@ __device__ __forceinline__ void load_rows(Row (&r)[ROWS], const T* p, int64_t ld
 }
 
 // Asks for a warp's rows of its next step in the L2, from the tile's first column p on: lane l its lines l, l + 32, ..
-// of ROWS rows of up to 128 columns.
-template <int ROWS, typename T>
+// of kRows rows of up to 128 columns.
+template <typename T>
 __device__ __forceinline__ void prefetch_rows(const T* p, int64_t ld, int live, int cols, int lane) {
     constexpr int kLines = kTileCols * sizeof(T) / 128;
 #pragma unroll
-    for (int k = 0; k < (ROWS * kLines + 31) / 32; ++k) {
+    for (int k = 0; k < (kRows * kLines + 31) / 32; ++k) {
         const int l = lane + 32 * k, i = l / kLines, c = l % kLines * static_cast<int>(128 / sizeof(T));
         if (i < live && c < cols) asm volatile("prefetch.global.L2 [%0];" ::"l"(p + i * ld + c));
     }
@@ -292,15 +289,15 @@ __device__ __forceinline__ void forget(Raw4<float>& r) {
 __device__ __forceinline__ void forget(Raw4<__nv_bfloat16>& r) { asm volatile("" : "+r"(r.v.x), "+r"(r.v.y)); }
 template <typename GT, bool PERCH>
 __device__ __forceinline__ void forget(RawGate<GT, PERCH>& r) { forget(r.v); }
-template <typename Row, int ROWS>
-__device__ __forceinline__ void forget(Row (&r)[ROWS]) {
+template <typename Row>
+__device__ __forceinline__ void forget(Row (&r)[kRows]) {
 #pragma unroll
-    for (int i = 0; i < ROWS; ++i) forget(r[i]);
+    for (int i = 0; i < kRows; ++i) forget(r[i]);
 }
 
-// How many of the `rows` rows from t on lie before n.
-__device__ __forceinline__ int live_rows(int64_t t, int64_t n, int rows) {
-    return static_cast<int>(min(max(n - t, int64_t(0)), static_cast<int64_t>(rows)));
+// How many of the kRows rows from t on lie before n.
+__device__ __forceinline__ int live_rows(int64_t t, int64_t n) {
+    return static_cast<int>(min(max(n - t, int64_t(0)), static_cast<int64_t>(kRows)));
 }
 
 // A store into the shared memory of another block of the cluster.
@@ -313,13 +310,13 @@ __device__ __forceinline__ void st_remote(const float* p, uint32_t rank, const Q
 __device__ __forceinline__ void join(Quad& h, const float* A, const float* B) { h = fma4(quad_at(A), h, quad_at(B)); }
 
 // One warp joins the block's warps' pairs and writes the block's pair into every block of the cluster, at its own rank.
-template <int WARPS, bool REVERSE>
+template <bool REVERSE>
 __device__ __forceinline__ void share_pair(const float (*A)[kTileCols], const float (*B)[kTileCols], float (*cA)[kTileCols],
                                            float (*cB)[kTileCols], uint32_t rank, int K, int lane) {
     Quad pa = quad(1.f), pb = quad(0.f);
 #pragma unroll
-    for (int j = 0; j < WARPS; ++j) {
-        const int k = REVERSE ? WARPS - 1 - j : j;
+    for (int j = 0; j < kWarps; ++j) {
+        const int k = REVERSE ? kWarps - 1 - j : j;
         const Quad ak = quad_at(&A[k][lane * 4]);
         pb = fma4(ak, pb, quad_at(&B[k][lane * 4]));
         pa = mul4(ak, pa);
@@ -330,9 +327,8 @@ __device__ __forceinline__ void share_pair(const float (*A)[kTileCols], const fl
     }
 }
 
-template <typename XT, typename GT, bool PERCH, bool CLUSTER, int ROWS>
-__global__ void __launch_bounds__(Split<ROWS>::kThreads, 2) glr_fwd_kernel(const GlrArgs a) {
-    constexpr int kWarps = Split<ROWS>::kWarps;
+template <typename XT, typename GT, bool PERCH, bool CLUSTER>
+__global__ void __launch_bounds__(kThreads, 2) glr_fwd_kernel(const GlrArgs a) {
     __shared__ __align__(16) float sA[2][kWarps][kTileCols], sB[2][kWarps][kTileCols];
     __shared__ __align__(16) float cA[2][CLUSTER ? kMaxCluster : 1][kTileCols], cB[2][CLUSTER ? kMaxCluster : 1][kTileCols];
     __shared__ __align__(16) float carry[2][kTileCols];
@@ -352,16 +348,16 @@ __global__ void __launch_bounds__(Split<ROWS>::kThreads, 2) glr_fwd_kernel(const
     else if (a.h0 != nullptr)
         h = quad(load4(a.h0 + static_cast<int64_t>(p) * a.D + tl.col));
     const int64_t step = static_cast<int64_t>(K) * SDM_GLR_CHUNK;
-    int64_t t = rank * SDM_GLR_CHUNK + w * ROWS;   // the warp's first row of the step
+    int64_t t = rank * SDM_GLR_CHUNK + w * kRows;   // the warp's first row of the step
     const XT* x = static_cast<const XT*>(a.x) + (b + t) * a.x_ld;
     const GT* g = static_cast<const GT*>(a.g) + (b + t) * a.g_ld;
     XT* y = static_cast<XT*>(a.y) + (b + t) * a.y_ld + tl.col;
     float* const st = a.states == nullptr ? nullptr : a.states + part.chunk * a.D + tl.col;
     // bfloat16 rows: the next step's are loaded into registers over this one; float32 rows: asked for in the L2
     constexpr bool AHEAD = sizeof(XT) == 2;
-    Raw4<XT> xr[ROWS], xn[AHEAD ? ROWS : 1];
-    RawGate<GT, PERCH> gr[ROWS], gn[AHEAD ? ROWS : 1];
-    int live = live_rows(t, n, ROWS);
+    Raw4<XT> xr[kRows], xn[AHEAD ? kRows : 1];
+    RawGate<GT, PERCH> gr[kRows], gn[AHEAD ? kRows : 1];
+    int live = live_rows(t, n);
     if (AHEAD) {
         load_rows(gr, g + tl.gate, a.g_ld, live);
         load_rows(xr, x + tl.col, a.x_ld, live);
@@ -369,7 +365,7 @@ __global__ void __launch_bounds__(Split<ROWS>::kThreads, 2) glr_fwd_kernel(const
     if (CLUSTER) cluster_wait();   // every block of the cluster runs
     int buf = 0;
     for (int64_t t0 = 0; t0 < n; t0 += step, t += step, buf ^= 1) {
-        const int more = live_rows(t + step, n, ROWS);
+        const int more = live_rows(t + step, n);
         if (!AHEAD) {
             load_rows(gr, g + tl.gate, a.g_ld, live);
             load_rows(xr, x + tl.col, a.x_ld, live);
@@ -380,12 +376,12 @@ __global__ void __launch_bounds__(Split<ROWS>::kThreads, 2) glr_fwd_kernel(const
             load_rows(gn, g + tl.gate, a.g_ld, more);
             load_rows(xn, x + tl.col, a.x_ld, more);
         } else {
-            prefetch_rows<ROWS>(x + tl.col0, a.x_ld, more, tl.n, lane);
-            if (PERCH) prefetch_rows<ROWS>(g + tl.col0, a.g_ld, more, tl.n, lane);
+            prefetch_rows(x + tl.col0, a.x_ld, more, tl.n, lane);
+            if (PERCH) prefetch_rows(g + tl.col0, a.g_ld, more, tl.n, lane);
         }
         Quad A = quad(1.f), B = quad(0.f);
 #pragma unroll
-        for (int i = 0; i < ROWS; ++i) {
+        for (int i = 0; i < kRows; ++i) {
             const Quad e = gr[i].exps();
             A = mul4(A, e);
             B = fma4(e, B, quad(xr[i]));
@@ -396,7 +392,7 @@ __global__ void __launch_bounds__(Split<ROWS>::kThreads, 2) glr_fwd_kernel(const
         Quad hw = h;
         if (CLUSTER) {
             if (w == 0) {
-                share_pair<kWarps, false>(sA[buf], sB[buf], cA[buf], cB[buf], rank, K, lane);
+                share_pair<false>(sA[buf], sB[buf], cA[buf], cB[buf], rank, K, lane);
                 cluster_arrive();
             } else {
                 cluster_arrive_relaxed();
@@ -424,17 +420,17 @@ __global__ void __launch_bounds__(Split<ROWS>::kThreads, 2) glr_fwd_kernel(const
             forget(gr);
             forget(xr);
         }
-        if (live == ROWS) {
+        if (live == kRows) {
             if (tl.on) {
 #pragma unroll
-                for (int i = 0; i < ROWS; ++i) {
+                for (int i = 0; i < kRows; ++i) {
                     hw = fma4(gr[i].exps(), hw, quad(xr[i]));
                     st4(y + i * a.y_ld, hw);
                 }
             }
         } else {
 #pragma unroll
-            for (int i = 0; i < ROWS; ++i) {
+            for (int i = 0; i < kRows; ++i) {
                 hw = fma4(gr[i].exps(), hw, quad(xr[i]));
                 if (tl.on && i < live) st4(y + i * a.y_ld, hw);
             }
@@ -443,7 +439,7 @@ __global__ void __launch_bounds__(Split<ROWS>::kThreads, 2) glr_fwd_kernel(const
         live = more;
         if constexpr (AHEAD) {
 #pragma unroll
-            for (int i = 0; i < ROWS; ++i) {
+            for (int i = 0; i < kRows; ++i) {
                 gr[i] = gn[i];
                 xr[i] = xn[i];
             }
@@ -464,9 +460,8 @@ __device__ __forceinline__ float head_sum(float v, int seg) {
     return v;
 }
 
-template <typename XT, typename GT, bool PERCH, bool CLUSTER, int ROWS>
-__global__ void __launch_bounds__(Split<ROWS>::kThreads, 2) glr_bwd_kernel(const GlrArgs a) {
-    constexpr int kWarps = Split<ROWS>::kWarps;
+template <typename XT, typename GT, bool PERCH, bool CLUSTER>
+__global__ void __launch_bounds__(kThreads, 2) glr_bwd_kernel(const GlrArgs a) {
     __shared__ __align__(16) float sA[2][kWarps][kTileCols], sF[2][kWarps][kTileCols], sR[2][kWarps][kTileCols];
     __shared__ __align__(16) float cA[2][CLUSTER ? kMaxCluster : 1][kTileCols], cR[2][CLUSTER ? kMaxCluster : 1][kTileCols];
     __shared__ __align__(16) float carry[2][kTileCols];
@@ -491,34 +486,34 @@ __global__ void __launch_bounds__(Split<ROWS>::kThreads, 2) glr_bwd_kernel(const
     int buf = 0;
     bool first = true;
     for (int64_t t0 = (n + step - 1) / step * step - step; t0 >= 0; t0 -= step, buf ^= 1) {
-        const int64_t tc = t0 + rank * SDM_GLR_CHUNK, t = tc + w * ROWS;
-        const int live = live_rows(t, n, ROWS);
+        const int64_t tc = t0 + rank * SDM_GLR_CHUNK, t = tc + w * kRows;
+        const int live = live_rows(t, n);
         const XT* const x = static_cast<const XT*>(a.x) + (b + t) * a.x_ld;
         const GT* const g = static_cast<const GT*>(a.g) + (b + t) * a.g_ld;
         const XT* const dy = static_cast<const XT*>(a.dy) + (b + t) * a.dy_ld;
         XT* const dx = static_cast<XT*>(a.dx) + (b + t) * a.dx_ld + tl.col;
         GT* const dg = static_cast<GT*>(a.dg) + (b + t) * a.dg_ld + tl.gate;
-        Raw4<XT> xr[ROWS], dr[ROWS];
-        RawGate<GT, PERCH> gr[ROWS];
+        Raw4<XT> xr[kRows], dr[kRows];
+        RawGate<GT, PERCH> gr[kRows];
         load_rows(gr, g + tl.gate, a.g_ld, live);
         load_rows(dr, dy + tl.col, a.dy_ld, live);
         load_rows(xr, x + tl.col, a.x_ld, live);
         Quad h = quad(0.f);
         if (tc < n) h = quad(load4(st + tc / SDM_GLR_CHUNK * a.D));
         if (t0 > 0) {
-            prefetch_rows<ROWS>(x - step * a.x_ld + tl.col0, a.x_ld, ROWS, tl.n, lane);
-            prefetch_rows<ROWS>(dy - step * a.dy_ld + tl.col0, a.dy_ld, ROWS, tl.n, lane);
-            if (PERCH) prefetch_rows<ROWS>(g - step * a.g_ld + tl.col0, a.g_ld, ROWS, tl.n, lane);
+            prefetch_rows(x - step * a.x_ld + tl.col0, a.x_ld, kRows, tl.n, lane);
+            prefetch_rows(dy - step * a.dy_ld + tl.col0, a.dy_ld, kRows, tl.n, lane);
+            if (PERCH) prefetch_rows(g - step * a.g_ld + tl.col0, a.g_ld, kRows, tl.n, lane);
         }
         Quad A = quad(1.f), F = quad(0.f), R = quad(0.f);
 #pragma unroll
-        for (int i = 0; i < ROWS; ++i) {
+        for (int i = 0; i < kRows; ++i) {
             const Quad e = gr[i].exps();
             A = mul4(A, e);
             F = fma4(e, F, quad(xr[i]));
         }
 #pragma unroll
-        for (int i = ROWS - 1; i >= 0; --i) R = mul4(gr[i].exps(), add4(quad(dr[i]), R));
+        for (int i = kRows - 1; i >= 0; --i) R = mul4(gr[i].exps(), add4(quad(dr[i]), R));
         st4(&sA[buf][w][lane * 4], A);
         st4(&sF[buf][w][lane * 4], F);
         st4(&sR[buf][w][lane * 4], R);
@@ -526,7 +521,7 @@ __global__ void __launch_bounds__(Split<ROWS>::kThreads, 2) glr_bwd_kernel(const
         Quad mw = m;
         if (CLUSTER) {
             if (w == 0) {
-                share_pair<kWarps, true>(sA[buf], sR[buf], cA[buf], cR[buf], rank, K, lane);
+                share_pair<true>(sA[buf], sR[buf], cA[buf], cR[buf], rank, K, lane);
                 cluster_arrive();
             } else {
                 cluster_arrive_relaxed();
@@ -555,15 +550,15 @@ __global__ void __launch_bounds__(Split<ROWS>::kThreads, 2) glr_bwd_kernel(const
         forget(gr);
         forget(xr);
         forget(dr);
-        const bool all = live == ROWS && tl.full;   // warp-uniform
-        Quad hp[ROWS];   // the state before each row
+        const bool all = live == kRows && tl.full;   // warp-uniform
+        Quad hp[kRows];   // the state before each row
 #pragma unroll
-        for (int i = 0; i < ROWS; ++i) {
+        for (int i = 0; i < kRows; ++i) {
             hp[i] = h;
             h = fma4(gr[i].exps(), h, quad(xr[i]));
         }
 #pragma unroll
-        for (int i = ROWS - 1; i >= 0; --i) {
+        for (int i = kRows - 1; i >= 0; --i) {
             const Quad l = add4(quad(dr[i]), mw);
             mw = mul4(gr[i].exps(), l);
             const Quad q = mul4(mw, hp[i]);
@@ -605,7 +600,7 @@ __global__ void __launch_bounds__(256, 2) glr_pair_kernel(const GlrArgs a) {
     Quad A = quad(1.f), B = quad(0.f);
     for (int64_t i0 = 0; i0 < n; i0 += 8) {
         const int64_t t = REVERSE ? (n + 7) / 8 * 8 - 8 - i0 : i0;
-        const int live = live_rows(t, n, 8);
+        const int live = live_rows(t, n);
         Raw4<XT> xr[8];
         RawGate<GT, PERCH> gr[8];
         load_rows(gr, g + t * a.g_ld, a.g_ld, live);
@@ -888,7 +883,6 @@ extern "C" sdm_status sdm_glr_forward(const sdm_glr_shape* shape, const void* x,
     const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
     const cudaError_t e = by_type(shape, [&](auto xt, auto gt, auto perch) {
         constexpr bool PC = decltype(perch)::value;
-        constexpr int R = 8;
         const unsigned units = static_cast<unsigned>(a.tiles * parts_of(a));
         if (a.seg != 0) {
             using X = decltype(xt);
@@ -898,10 +892,10 @@ extern "C" sdm_status sdm_glr_forward(const sdm_glr_shape* shape, const void* x,
                                      cs, a);
             if (e != cudaSuccess) return e;
         }
-        const dim3 grid(units * a.cluster), block(Split<R>::kThreads);
+        const dim3 grid(units * a.cluster), block(kThreads);
         if (a.cluster > 1)
-            return launch_cluster(glr_fwd_kernel<decltype(xt), decltype(gt), PC, true, R>, grid, block, a.cluster, cs, a);
-        return launch_dependent(glr_fwd_kernel<decltype(xt), decltype(gt), PC, false, R>, grid, block, 0, cs, a);
+            return launch_cluster(glr_fwd_kernel<decltype(xt), decltype(gt), PC, true>, grid, block, a.cluster, cs, a);
+        return launch_dependent(glr_fwd_kernel<decltype(xt), decltype(gt), PC, false>, grid, block, 0, cs, a);
     });
     return e == cudaSuccess ? SDM_OK : SDM_ERR_CUDA;
 }
@@ -937,7 +931,6 @@ extern "C" sdm_status sdm_glr_backward(const sdm_glr_shape* shape, const void* x
     const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t e = by_type(shape, [&](auto xt, auto gt, auto perch) {
         constexpr bool PC = decltype(perch)::value;
-        constexpr int R = 8;
         const unsigned units = static_cast<unsigned>(a.tiles * parts_of(a));
         if (a.seg != 0) {
             using X = decltype(xt);
@@ -947,10 +940,10 @@ extern "C" sdm_status sdm_glr_backward(const sdm_glr_shape* shape, const void* x
                                      cs, a);
             if (e != cudaSuccess) return e;
         }
-        const dim3 grid(units * a.cluster), block(Split<R>::kThreads);
+        const dim3 grid(units * a.cluster), block(kThreads);
         if (a.cluster > 1)
-            return launch_cluster(glr_bwd_kernel<decltype(xt), decltype(gt), PC, true, R>, grid, block, a.cluster, cs, a);
-        return launch_dependent(glr_bwd_kernel<decltype(xt), decltype(gt), PC, false, R>, grid, block, 0, cs, a);
+            return launch_cluster(glr_bwd_kernel<decltype(xt), decltype(gt), PC, true>, grid, block, a.cluster, cs, a);
+        return launch_dependent(glr_bwd_kernel<decltype(xt), decltype(gt), PC, false>, grid, block, 0, cs, a);
     });
     if (e == cudaSuccess && part_bytes(a) > 0) {
         const int64_t blocks = std::min<int64_t>((a.rows * a.H + 255) / 256, 4096);
