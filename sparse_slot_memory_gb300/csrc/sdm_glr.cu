@@ -125,8 +125,13 @@ __device__ __forceinline__ void sequence(const GlrArgs& a, int p, int64_t& b, in
     if ((lo < 0 || hi > a.rows || lo > hi) && a.status != nullptr && threadIdx.x == 0) atomicOr(a.status, SDM_DEV_BAD_OFFSET);
 }
 
-// A gate's exp is 2^(g log2 e): within 4 u + |g| u (u = 2^-24), and exactly 0 and 1 at -inf and 0.
-constexpr float kLog2e = 1.44269504088896341f;
+// A gate's exp is 2^(g log2 e): within 4 u + 1.25 |g| u (u = 2^-24; the product is rounded once, log2 e by 0.22 u), and
+// exactly 0 and 1 at -inf and 0. The hardware's 2^t is low by 0.09 to 0.36 u on average for gates between 1 and 1/e, and a
+// long memory adds that row by row. For float32 rows a fifth of u goes into the product's place, which leaves a mean within
+// 0.16 u: 3000 rows with g about -0.05 (-0.0025) are within 1.3e-7 (4.6e-7) of 64 bits, without it 2.2e-7 (2.3e-6), float32
+// rows one by one with expf 1.4e-7 (1.4e-6). bfloat16 rows are 2^-9 apart, and the registers for it would cost their training
+// steps 1 to 3 %.
+constexpr float kLog2e = 1.44269504088896341f, kCenter = 0.2f * 0x1p-24f * kLog2e;
 __device__ __forceinline__ float exp2_gate(float t) {
     float o;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(o) : "f"(t));
@@ -221,32 +226,37 @@ __device__ __forceinline__ Quad kept(const T* row, int64_t ld, int i) {   // wri
     }
 }
 
-// The gates of one row as they lie in memory: the lane's four, or its head's one.
-template <typename GT, bool PERCH>
+// The gates of one row as they lie in memory: the lane's four, or its head's one. CENTER: of float32 rows.
+template <typename GT, bool PERCH, bool CENTER>
 struct RawGate;
-template <typename GT>
-struct RawGate<GT, true> {
+template <typename GT, bool CENTER>
+struct RawGate<GT, true, CENTER> {
     Raw4<GT> v;
     __device__ __forceinline__ void zero() { v.zero(); }
     __device__ __forceinline__ Quad exps() const {
         float o[4];
-        floats(mul4(quad(v), quad(kLog2e)), o);
+        if constexpr (CENTER)
+            floats(fma4(quad(v), quad(kLog2e), quad(kCenter)), o);
+        else
+            floats(mul4(quad(v), quad(kLog2e)), o);
 #pragma unroll
         for (int i = 0; i < 4; ++i) o[i] = exp2_gate(o[i]);
         return quad(o);
     }
 };
-template <typename GT>
-struct RawGate<GT, false> {
+template <typename GT, bool CENTER>
+struct RawGate<GT, false, CENTER> {
     GT v;
     __device__ __forceinline__ void zero() { v = GT(0.f); }
-    __device__ __forceinline__ Quad exps() const { return quad(exp2_gate(widen(v) * kLog2e)); }
+    __device__ __forceinline__ Quad exps() const {
+        return quad(exp2_gate(CENTER ? fmaf(widen(v), kLog2e, kCenter) : widen(v) * kLog2e));
+    }
 };
 
-template <typename GT>
-__device__ __forceinline__ void ld_plain(RawGate<GT, true>& r, const GT* p) { rows::ld_plain(r.v, p); }
-template <typename GT>
-__device__ __forceinline__ void ld_plain(RawGate<GT, false>& r, const GT* p) { r.v = *p; }
+template <typename GT, bool CENTER>
+__device__ __forceinline__ void ld_plain(RawGate<GT, true, CENTER>& r, const GT* p) { rows::ld_plain(r.v, p); }
+template <typename GT, bool CENTER>
+__device__ __forceinline__ void ld_plain(RawGate<GT, false, CENTER>& r, const GT* p) { r.v = *p; }
 
 // kRows rows of a lane's columns; those from `live` on are zeros (the identity: gate 1, nothing added).
 template <typename Row, typename T>
@@ -287,8 +297,8 @@ __device__ __forceinline__ void forget(Raw4<float>& r) {
     asm volatile("" : "+f"(r.v.x), "+f"(r.v.y), "+f"(r.v.z), "+f"(r.v.w));
 }
 __device__ __forceinline__ void forget(Raw4<__nv_bfloat16>& r) { asm volatile("" : "+r"(r.v.x), "+r"(r.v.y)); }
-template <typename GT, bool PERCH>
-__device__ __forceinline__ void forget(RawGate<GT, PERCH>& r) { forget(r.v); }
+template <typename GT, bool PERCH, bool CENTER>
+__device__ __forceinline__ void forget(RawGate<GT, PERCH, CENTER>& r) { forget(r.v); }
 template <typename Row>
 __device__ __forceinline__ void forget(Row (&r)[kRows]) {
 #pragma unroll
@@ -356,7 +366,7 @@ __global__ void __launch_bounds__(kThreads, 2) glr_fwd_kernel(const GlrArgs a) {
     // bfloat16 rows: the next step's are loaded into registers over this one; float32 rows: asked for in the L2
     constexpr bool AHEAD = sizeof(XT) == 2;
     Raw4<XT> xr[kRows], xn[AHEAD ? kRows : 1];
-    RawGate<GT, PERCH> gr[kRows], gn[AHEAD ? kRows : 1];
+    RawGate<GT, PERCH, sizeof(XT) == 4> gr[kRows], gn[AHEAD ? kRows : 1];
     int live = live_rows(t, n);
     if (AHEAD) {
         load_rows(gr, g + tl.gate, a.g_ld, live);
@@ -494,7 +504,7 @@ __global__ void __launch_bounds__(kThreads, 2) glr_bwd_kernel(const GlrArgs a) {
         XT* const dx = static_cast<XT*>(a.dx) + (b + t) * a.dx_ld + tl.col;
         GT* const dg = static_cast<GT*>(a.dg) + (b + t) * a.dg_ld + tl.gate;
         Raw4<XT> xr[kRows], dr[kRows];
-        RawGate<GT, PERCH> gr[kRows];
+        RawGate<GT, PERCH, sizeof(XT) == 4> gr[kRows];
         load_rows(gr, g + tl.gate, a.g_ld, live);
         load_rows(dr, dy + tl.col, a.dy_ld, live);
         load_rows(xr, x + tl.col, a.x_ld, live);
@@ -602,7 +612,7 @@ __global__ void __launch_bounds__(256, 2) glr_pair_kernel(const GlrArgs a) {
         const int64_t t = REVERSE ? (n + 7) / 8 * 8 - 8 - i0 : i0;
         const int live = live_rows(t, n);
         Raw4<XT> xr[8];
-        RawGate<GT, PERCH> gr[8];
+        RawGate<GT, PERCH, sizeof(XT) == 4> gr[8];
         load_rows(gr, g + t * a.g_ld, a.g_ld, live);
         load_rows(xr, v + t * v_ld, v_ld, live);
 #pragma unroll
@@ -737,7 +747,7 @@ __global__ void __launch_bounds__(256) glr_step_kernel(const StepArgs a) {
     float* const st = a.state + s * a.s_ld + col;
     ld4cg(st, h);
     ld_plain(x, static_cast<const XT*>(a.x) + r * a.x_ld + col);
-    RawGate<GT, PERCH> gr;
+    RawGate<GT, PERCH, sizeof(XT) == 4> gr;
     ld_plain(gr, static_cast<const GT*>(a.g) + r * a.g_ld + (PERCH ? col : col / a.gw));
     const Quad o = fma4(gr.exps(), quad(h), quad(x));
     st4(st, o);
