@@ -1,6 +1,6 @@
-// sdm_checks.cuh -- host-side argument checks shared by the backward entry points (sdm_pa, sdm_gwr,
+// sdm_checks.cuh -- host-side argument checks shared by the memory's backward entry points (sdm_pa, sdm_gwr,
 // sdm_gds): the shape rules of the forward's entry points (one shape describes both directions) and
-// the 16-byte alignment rule.
+// the 16-byte alignment rule, which the operators around the memory share too.
 #pragma once
 
 #include <cstdint>

@@ -20,12 +20,17 @@
 // start, so it reads x instead of y: the same bytes, and no rounding of y in the gradients. A gate per head sums its
 // channels' products over the lanes (and, for heads wider than a tile, over tiles in order in a second kernel).
 //
-// Bound by HBM in principle (6 bytes a bfloat16 element forward, 10 backward, 2 flops a byte); in fact by the issue of
-// instructions at the 16 warps an SM that 128 registers allow: one pass holds 8 rows, their gates and the next step's
-// rows. Measured on a GB300 (6.7 TB/s copy): 8 x 8192 x 2048 bfloat16 with a gate per channel, forward 151 us (5.3 TB/s
-// of its bytes), forward and backward 399 us (5.4 TB/s); 1 x 65537 x 512 float32 with gates per head, both, 186 us
-// (671 MB of single reads: 3.6 TB/s; 940 MB moved); 24 ragged sequences, 30011 x 1920, forward 79 to 90 us by their lengths
-// (2.6 to 2.9 TB/s). One token of 64 requests: 7.0 us a call, the host's time for it.
+// Bound by HBM in principle (6 bytes a bfloat16 element forward, 10 backward, 2 flops a byte); in fact by what the 16
+// warps an SM that 128 registers allow wait for: the barriers of a step's exchange in the forward, loads and barriers in the
+// backward (issue slots are used in 24 to 46 % of the cycles). One pass holds 8 rows, their gates and the next step's rows.
+// Measured on a GB300 (6.7 TB/s copy): 8 x 8192 x 2048 with a gate per channel, bfloat16 rows and gates, forward 151 us
+// (5.3 TB/s of its bytes), forward and backward 400 us (5.4 TB/s); with float32 gates 228 us (4.7 TB/s; 104 to 184 bytes of
+// registers spilled a thread) and 533 us (5.5 TB/s); half the rows in float32 with float32 gates 123 us (6.5 TB/s) and
+// 360 us (6.0 TB/s; the backward spills 152 to 204 bytes). 1 x 65537 x 512 float32 with gates per head, both, 178 us
+// (671 MB of single reads: 3.8 TB/s; 940 MB moved); 24 ragged sequences, 30011 x 1920, forward 79 to 90 us by their lengths
+// (2.6 to 2.9 TB/s). Heads that leave lanes of a tile idle, 8 x 4096 x 2040 to 2048 bfloat16, forward / both: 66 / 203 us at
+// widths 64, 128 and 256, 127 / 325 at 96, 178 / 456 to 464 at 68 and 132. One token of 64 requests: 6.8 us a call (the
+// kernel 1.6 in a graph), the host's time for it.
 #include <cuda_bf16.h>
 
 #include <algorithm>

@@ -18,7 +18,8 @@
 // forward and backward 238 us (1.61 GB: 6.8 TB/s, the second read partly from the L2); 1000 x 50001 float32 forward 33 us
 // without alternatives (6.1 TB/s), 38 with 5; 8000 x 12000 bfloat16 32 us without, 58 with 20: a row's end (bound, cells,
 // sort) is not hidden wholly where the blocks of an SM reach it together. Eight rows of 131072 with 20
-// alternatives: 7.3 us in clusters of 8 blocks, no more than the host's call.
+// alternatives: 7.3 us in clusters of 8 blocks, its latency (loads, two list sorts, cluster barriers). A backward whose rows
+// all have |lse| of 1024 or more pays for the plain look in every block of a row: 512 x 131072 float32 2.9 ms, otherwise 78 us.
 //
 // A row whose largest logit lies under -1e30 / scale (everything masked, by -inf or by a type's lowest value) leaves
 // s = 0, one whose largest x scale log2(e) is past float32's range leaves NaN, and an M of 2^28 or more is rounded too
@@ -45,7 +46,11 @@ using namespace rows;
 //   8000 x 32000: 142 / 113 / 113    1000 x 32000: 23 / 19 / 24    600 x 32000: 13 / 15 / 21    1000 x 128000: 56 / 53 / 74
 //   1800 x 128000: 92 / 95 / 94 (74 / 82 / 74 without alternatives)
 // Long rows lose with narrow blocks where a few of them are left at the end, each read by few threads, but not where all
-// run at once, when 256 threads would leave those few. Very short rows are two batches of two warps.
+// run at once, when 256 threads would leave those few. That is so from 609 rows on; the rule begins at 760, a middle of (256 /
+// 128 threads) rows with alternatives or of float32, which gain before (620 rows: 40000 bfloat16 with 20 alternatives
+// 21.3 / 18.6, 32003 float32 without 17.0 / 14.6, 64000 float32 with 20 45 / 38), and bfloat16 rows without alternatives, which
+// lose (620 rows of 128000: 30.2 / 33.9; 760: 32.3 / 35.9; 900: 44.0 / 39.8). Behind 1216 rows 256 are left some again
+// (1230 rows of 128000 with 20: 74.5 / 80.0). Very short rows are two batches of two warps.
 // A block of a cluster has the fewest rows and the most threads (150 rows of 131072: 21.7 us with 256, 18.2 with 512; 8 rows:
 // 8.3 and 7.9).
 constexpr int kRowThreads = 256, kClusterThreads = 512, kMidThreads = 128, kShortThreads = 64;
@@ -384,7 +389,8 @@ __global__ void __launch_bounds__(THREADS, blocks_of(THREADS)) lp_fwd_kernel(con
         __syncthreads();
     }
     // vectors start at the row's first 16-byte boundary; the logits before it and behind the last vector are
-    // taken one by one, by the first and the last block (ids ascend over what a warp sees)
+    // taken one by one, by the first and the last block. Ids come in no order: among equal logits the lower ids win by the keys'
+    // order, and by TopList::last, the id from which on logits equal to the K-th cannot enter
     const int head = min(a.V, static_cast<int>((16 - (reinterpret_cast<uintptr_t>(x) & 15)) % 16 / sizeof(T)));
     const int nvec = (a.V - head) / N;
     const int each = CLUSTER ? (nvec + C - 1) / C : nvec;
@@ -464,7 +470,7 @@ __global__ void __launch_bounds__(THREADS, blocks_of(THREADS)) lp_fwd_kernel(con
         if (w == 0 && rank == 0) offer_scalars(0, head);
         // A cell has `size` vectors; those of a warp's cells are read again one a lane, whoever's cell they are of: a
         // few rounds of full warps instead of one for every cell and vector (8000 x 12000 bfloat16, 20 alternatives: 75 us,
-        // then 58; 1000 x 50001 float32 with 32: 58, then 47; rows whose logits all rise with the id lose:
+        // then 58; 1000 x 50001 float32 with 32: 58, then 46; rows whose logits all rise with the id lose:
         // the latter with 20 42, then 51, 4000 x 12000 bfloat16 41, then 61).
         const int size = per * kBatch;
         int hits = 0;

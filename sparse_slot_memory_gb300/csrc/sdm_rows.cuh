@@ -1,5 +1,6 @@
-// sdm_rows.cuh -- row helpers of the DW and backward kernels: a lane's 4 or 8 columns of a row (f32 or bf16),
-// per-lane cp.async copies into shared memory, and the lane tree that sums a dot's 32 lane partials.
+// sdm_rows.cuh -- row helpers of the DW and backward kernels, and of the operators around the memory: a lane's
+// 4 or 8 columns of a row (f32 or bf16), per-lane cp.async copies into shared memory, and the lane tree that sums a
+// dot's 32 lane partials.
 #pragma once
 
 #include <cuda_bf16.h>
