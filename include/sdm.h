@@ -512,7 +512,8 @@ sdm_status sdm_token_logprobs(const sdm_logprob_shape* shape, const void* logits
  * The gradient of the logits, from the forward's lse and entropy:
  *   dlogits_v = scale (d_logp (1[v = target] - p_v) - d_entropy p_v (log p_v + entropy)),
  * d_logp float32 [rows] (taken as 0 where the target is ignored), d_entropy float32 [rows] (nullable: zeros, and
- * entropy may be NULL then). In a row whose logits are all -inf every p is 0. K is not used.
+ * entropy may be NULL then). In a row whose logits are all -inf every p is 0. dlogits may be logits (same ld). K is not
+ * used.
  */
 sdm_status sdm_token_logprobs_backward(const sdm_logprob_shape* shape, const void* logits, int64_t ld,
                                        const int32_t* targets, const float* lse, const float* entropy,

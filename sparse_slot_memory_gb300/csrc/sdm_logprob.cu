@@ -89,6 +89,7 @@ struct LpArgs {
     float scale;
     float floor;           // backward: the logit at kGradFloor
     int cluster;           // blocks of a row
+    bool in_place;         // backward: dlogits is logits
 };
 
 __device__ __forceinline__ float max_nan(float a, float b) {
@@ -641,13 +642,16 @@ __global__ void __launch_bounds__(kBwdThreads) lp_bwd_kernel(const LpArgs a, int
     const float H = a.d_entropy != nullptr ? a.ent_in[row] : 0.f, lse = a.lse_in[row];
     if (part == 0 && threadIdx.x == 0 && t >= a.V && a.status != nullptr) atomicOr(a.status, SDM_DEV_BAD_TARGET);
     if (fabsf(lse) >= kFarLse) {
-        // block-uniform and rare: z - lse from differences to the largest logit, or (lse -inf) a row of zeros
+        // block-uniform and rare: z - lse from differences to the largest logit, or (lse -inf) a row of zeros. In place
+        // the first block writes the whole row, which every block would read.
+        if (a.in_place && part != 0) return;
         const bool empty = lse == -INFINITY;
         float m = 0.f, s = 1.f, u;
         if (!empty) plain_stats(x, a.V, a.scale, red, m, s, u);
         const float ls = logf(s);
         const int per = kBwdThreads * kBwdVecs * N;
-        for (int i = part * per + threadIdx.x; i < (part + 1 == parts ? a.V : min(a.V, (part + 1) * per)); i += kBwdThreads) {
+        const int end = a.in_place || part + 1 == parts ? a.V : min(a.V, (part + 1) * per);
+        for (int i = part * per + threadIdx.x; i < end; i += kBwdThreads) {
             const float d = max_nan((widen(x[i]) - m) * a.scale - ls, kGradFloor), p = empty ? 0.f : expf(d);
             const float g = -p * (dl + dh * (empty ? 0.f : d + H)) + (i == t ? dl : 0.f);
             st1(o + i, a.scale * g);
@@ -788,6 +792,7 @@ extern "C" sdm_status sdm_token_logprobs_backward(const sdm_logprob_shape* shape
     a.logits = logits; a.ld = ld; a.targets = targets; a.lse_in = lse; a.ent_in = entropy; a.d_logp = d_logp;
     a.d_entropy = d_entropy; a.dlogits = dlogits; a.d_ld = d_ld; a.status = status;
     a.rows = shape->rows; a.V = shape->V; a.scale = shape->scale; a.floor = kGradFloor / shape->scale;
+    a.in_place = dlogits == logits;
     const bool bf = shape->dtype == SDM_BF16;
     const int per = kBwdThreads * kBwdVecs * (bf ? 8 : 4);
     const int parts = (shape->V + per - 1) / per;

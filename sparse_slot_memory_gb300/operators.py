@@ -329,7 +329,7 @@ def token_logprobs(spec: LogprobSpec, logits, targets, logp, entropy=None, lse=N
 def token_logprobs_backward(spec: LogprobSpec, logits, targets, lse, entropy, d_logp, dlogits, d_entropy=None,
                             status=None, stream=None):
     """sdm_token_logprobs_backward: ``dlogits`` [rows, V] from the gradients of logp and (optional) of the entropy,
-    with the forward's ``lse`` and ``entropy`` (None where there is no ``d_entropy``)."""
+    with the forward's ``lse`` and ``entropy`` (None where there is no ``d_entropy``). ``dlogits`` may be ``logits``."""
     N, V, dt = spec.rows, spec.V, _TORCH_DT[spec.dtype]
     st = _abi.load().sdm_token_logprobs_backward(
         spec.c(), *_rows(logits, dt, (N, V), V, "logits"), _small(targets, _I32, N, "targets"), _small(lse, _F32, N, "lse"),

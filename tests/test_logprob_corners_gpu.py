@@ -1,5 +1,6 @@
 """Corners of the token log probabilities: masked logits at other scales and under large gradients of the entropy, and finite
-logits whose products leave float32's range. The values are those of tests/operators_testlib.py in 64 bits, with its bounds."""
+logits whose products leave float32's range, and the gradient in the logits' place. The values are those of
+tests/operators_testlib.py in 64 bits, with its bounds."""
 
 import numpy as np
 import pytest
@@ -141,3 +142,23 @@ def test_no_entropy_without_its_gradient():
         with pytest.raises(sdm.SdmError) as err:
             sdm.token_logprobs_backward(s, x, t, want["lse"], None, want["d_logp"], outs[0], d_entropy=want["d_entropy"])
         assert err.value.status == -1
+
+
+@pytest.mark.parametrize("dtype", list(DT))
+@pytest.mark.parametrize("pad", [0, 3])
+def test_gradient_in_place_of_the_logits(dtype, pad):
+    """Rows near zero and far from it (which every block of a row reads once more), empty ones among them."""
+    N, V = 7, 50001
+    buf = torch.zeros(N, V + pad, dtype=DT[dtype], device="cuda")
+    x, t = masked(N, V, dtype, 1.0, seed=3)
+    for i, offset in enumerate((0.0, 3000.0, -5000.0, 0.0, 1e6)):
+        x[i][x[i] > -1e37] += offset
+    x[5] = -float("inf")
+    buf[:, :V] = x
+    want = run(x, t, 1.0)
+    compare(x, t, 1.0, want)
+    s = sdm.LogprobSpec(rows=N, V=V, dtype=dtype)
+    for _ in range(3):
+        got = buf.clone()[:, :V]
+        sdm.token_logprobs_backward(s, got, t, want["lse"], want["entropy"], want["d_logp"], got, want["d_entropy"])
+        assert torch.equal(got, want["dlogits"])
