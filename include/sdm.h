@@ -520,6 +520,68 @@ sdm_status sdm_token_logprobs_backward(const sdm_logprob_shape* shape, const voi
                                        const float* d_logp, const float* d_entropy, void* dlogits, int64_t d_ld,
                                        uint32_t* status, sdm_stream_t stream);
 
+/* Rows between two saved states of the delta rule, and rows of a block of its walk. */
+#define SDM_GDR_CHUNK 64
+
+typedef struct {
+    int32_t P;          /* sequences */
+    int32_t k_heads;    /* heads of q and k */
+    int32_t v_heads;    /* heads of v, g, beta and y, a multiple of k_heads: value head h goes with key head
+                         * h / (v_heads / k_heads) */
+    int32_t dk;         /* channels of a key head, a multiple of 8, up to 128 */
+    int32_t dv;         /* channels of a value head, a multiple of 8, up to 128 */
+    int32_t x_dtype;    /* sdm_dtype of q, k, v, y and their gradients */
+    int32_t g_dtype;    /* sdm_dtype of g, beta and their gradients */
+    float scale;        /* of the answers */
+    int64_t rows;       /* rows of all sequences together */
+} sdm_gdr_shape;
+
+/*
+ * The gated delta rule (the dense counterpart of the memory's decay, read and write): per sequence and value head, with
+ * a state S [dk, dv] of slots addressed by every key at once,
+ *   S_t = exp(g_t) S_{t-1} + k_t u_t^T,   u_t = beta_t (v_t - exp(g_t) S_{t-1}^T k_t),   y_t = scale S_t^T q_t.
+ *   q, k [rows, k_heads * dk], v, y [rows, v_heads * dv], aligned to 16 bytes like their ld; g, beta [rows, v_heads], no alignment
+ *   rule: log decays, at most 0 (-inf starts anew; a product of decays below float32's range counts as 0), and write
+ *   strengths. Keys of length 1 and beta in [0, 2] keep the state bounded.
+ *   offsets: as in sdm_glr_forward (ragged sequences, rows of no sequence).
+ *   h0 (nullable: zeros) and hT (nullable) float32 [P, v_heads, dk, dv]: the states before and after; hT may be h0; an
+ *   empty sequence hands its state on.
+ *   states (nullable), sdm_gdr_states_bytes, 16-byte aligned: the state before every SDM_GDR_CHUNK-th row of each sequence, for
+ *   the backward, in a form of its own.
+ *   ws: sdm_gdr_workspace_bytes(shape, 0), 16-byte aligned. It holds nothing from one call to the next.
+ * Blocks of 64 rows are solved together on the tensor cores; sums are float32, and float32 values enter the products as sums of
+ * two bfloat16 (within 2^-18) beside bfloat16 rows, of three (2^-25) beside float32 rows. A value that is not finite spoils its sequence and head from the start of its block on (as NaN).
+ */
+size_t sdm_gdr_states_bytes(const sdm_gdr_shape* shape);
+size_t sdm_gdr_workspace_bytes(const sdm_gdr_shape* shape, int32_t backward);
+sdm_status sdm_gdr_forward(const sdm_gdr_shape* shape, const void* q, int64_t q_ld, const void* k, int64_t k_ld,
+                           const void* v, int64_t v_ld, const void* g, int64_t g_ld, const void* beta, int64_t beta_ld,
+                           const int64_t* offsets, const float* h0, void* y, int64_t y_ld, float* hT, void* states,
+                           void* ws, size_t ws_bytes, uint32_t* status, sdm_stream_t stream);
+
+/*
+ * Its backward: the gradients dq, dk [rows, k_heads * dk] (summed over the value heads of a key head), dv [rows, v_heads * dv], dg,
+ * dbeta [rows, v_heads] and dh0 (nullable, float32 [P, v_heads, dk, dv]) from dy and dhT (nullable: zeros; the gradient of the states
+ * after). q, k, v, g, beta and offsets as the forward had them, states as it saved them; dh0 may be dhT. ws:
+ * sdm_gdr_workspace_bytes(shape, 1), 16-byte aligned. Alignments as for the forward. No output overlaps an input.
+ */
+sdm_status sdm_gdr_backward(const sdm_gdr_shape* shape, const void* q, int64_t q_ld, const void* k, int64_t k_ld,
+                            const void* v, int64_t v_ld, const void* g, int64_t g_ld, const void* beta, int64_t beta_ld,
+                            const void* dy, int64_t dy_ld, const int64_t* offsets, const void* states, const float* dhT,
+                            void* dq, int64_t dq_ld, void* dk, int64_t dk_ld, void* dv, int64_t dv_ld, void* dg,
+                            int64_t dg_ld, void* dbeta, int64_t dbeta_ld, float* dh0, void* ws, size_t ws_bytes,
+                            uint32_t* status, sdm_stream_t stream);
+
+/*
+ * One token of each of `rows` requests (P is not used), in float32: state[s] as above, with s = slots[i] (int32 [rows], distinct),
+ * or i where slots is NULL. state float32 [states, v_heads * dk * dv] with rows state_ld apart, aligned to 16 bytes. A row with
+ * a slot below 0 is padding: y_i = 0 and no state changes; so too one at or above `states`, which sets SDM_DEV_BAD_SLOT.
+ */
+sdm_status sdm_gdr_step(const sdm_gdr_shape* shape, const void* q, int64_t q_ld, const void* k, int64_t k_ld,
+                        const void* v, int64_t v_ld, const void* g, int64_t g_ld, const void* beta, int64_t beta_ld,
+                        const int32_t* slots, float* state, int64_t state_ld, int64_t states, void* y, int64_t y_ld,
+                        uint32_t* status, sdm_stream_t stream);
+
 /*
  * Synchronizes `stream`, reads the workspace's device status word into *code_out (0 = fine,
  * else SDM_DEV_* bits) and, if `clear`, zeroes it. Returns SDM_ERR_DEVICE when the word is

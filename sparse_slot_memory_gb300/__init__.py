@@ -31,12 +31,18 @@ from .api import (  # noqa: F401
     workspace_bytes,
 )
 from .operators import (  # noqa: F401
+    GdrSpec,
     GlrSpec,
     LogprobSpec,
     RopeSpec,
+    alloc_gdr_states,
+    alloc_gdr_workspace,
     alloc_glr_states,
     alloc_glr_workspace,
     alloc_rope_workspace,
+    gdr_backward,
+    gdr_forward,
+    gdr_step,
     glr_backward,
     glr_forward,
     glr_step,

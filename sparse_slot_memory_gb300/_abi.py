@@ -16,6 +16,7 @@ SDM_DEV_BAD_OFFSET = 0x2
 SDM_DEV_BAD_POSITION = 0x4
 SDM_DEV_BAD_TARGET = 0x8
 SDM_GLR_CHUNK = 64
+SDM_GDR_CHUNK = 64
 
 # every symbol include/sdm.h declares
 EXPORTS = ("sdm_workspace_bytes", "sdm_workspace_init", "sdm_phase1", "sdm_dw", "sdm_forward_chunks",
@@ -24,7 +25,9 @@ EXPORTS = ("sdm_workspace_bytes", "sdm_workspace_init", "sdm_phase1", "sdm_dw", 
            "sdm_status_string",
            "sdm_glr_states_bytes", "sdm_glr_workspace_bytes", "sdm_glr_forward", "sdm_glr_backward", "sdm_glr_step",
            "sdm_rope_workspace_bytes", "sdm_rope_table", "sdm_qk_norm_rope", "sdm_qk_norm_rope_backward",
-           "sdm_token_logprobs", "sdm_token_logprobs_backward")
+           "sdm_token_logprobs", "sdm_token_logprobs_backward",
+           "sdm_gdr_states_bytes", "sdm_gdr_workspace_bytes", "sdm_gdr_forward", "sdm_gdr_backward",
+           "sdm_gdr_step")
 NOALLOC_SCRATCH_BYTES = 16 << 20
 
 
@@ -46,6 +49,11 @@ class RopeShape(ctypes.Structure):
 
 class LogprobShape(ctypes.Structure):
     _fields_ = [("rows", c_i64), ("V", c_i32), ("K", c_i32), ("dtype", c_i32), ("scale", ctypes.c_float)]
+
+
+class GdrShape(ctypes.Structure):
+    _fields_ = [("P", c_i32), ("k_heads", c_i32), ("v_heads", c_i32), ("dk", c_i32), ("dv", c_i32), ("x_dtype", c_i32),
+                ("g_dtype", c_i32), ("scale", ctypes.c_float), ("rows", c_i64)]
 
 
 P1_FIELDS = ("log_k", "rex", "cpe", "k_eff", "is_last", "is_only", "pos_k", "log_q", "q_w", "pos_q", "q_last",
@@ -107,13 +115,18 @@ def load(path: str = LIB):
 
 def _operators(lib):
     """The argument types of the operators around the memory."""
-    glr, rope, lp = (ctypes.POINTER(s) for s in (GlrShape, RopeShape, LogprobShape))
+    glr, rope, lp, gdr = (ctypes.POINTER(s) for s in (GlrShape, RopeShape, LogprobShape, GdrShape))
     row = [c_p, c_i64]   # a row array and the distance between its rows
     for name, shape in (("sdm_glr_states_bytes", glr), ("sdm_glr_workspace_bytes", glr),
-                        ("sdm_rope_workspace_bytes", rope)):
+                        ("sdm_rope_workspace_bytes", rope), ("sdm_gdr_states_bytes", gdr)):
         fn = getattr(lib, name)
         fn.restype, fn.argtypes = c_sz, [shape]
+    lib.sdm_gdr_workspace_bytes.restype, lib.sdm_gdr_workspace_bytes.argtypes = c_sz, [gdr, c_i32]
     for name, args in (
+        ("sdm_gdr_forward", [gdr, *row, *row, *row, *row, *row, c_p, c_p, *row, c_p, c_p, c_p, c_sz, c_p, c_p]),
+        ("sdm_gdr_backward", [gdr, *row, *row, *row, *row, *row, *row, c_p, c_p, c_p, *row, *row, *row, *row, *row, c_p, c_p,
+                              c_sz, c_p, c_p]),
+        ("sdm_gdr_step", [gdr, *row, *row, *row, *row, *row, c_p, *row, c_i64, *row, c_p, c_p]),
         ("sdm_glr_forward", [glr, *row, *row, c_p, c_p, *row, c_p, c_p, c_p, c_p]),
         ("sdm_glr_backward", [glr, *row, *row, *row, c_p, c_p, c_p, *row, *row, c_p, c_p, c_sz, c_p, c_p]),
         ("sdm_glr_step", [glr, *row, *row, c_p, *row, c_i64, *row, c_p, c_p]),

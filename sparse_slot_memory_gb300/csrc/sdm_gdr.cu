@@ -1,0 +1,772 @@
+// sdm_gdr.cu -- the gated delta rule: the forward over sequences in blocks of 64 rows, and one token of every request:
+// sdm_gdr_forward / sdm_gdr_step (include/sdm.h; the backward: sdm_gdr_bwd.cu; mathematics and numbers: sdm_gdr.cuh).
+//
+// Two kernels. What a block's rows give without the state (T, A and the decays) is computed for all blocks at once; then
+// every sequence and value head is walked block by block, its state's columns divided among warps.
+//
+// The walk. A warp owns 16 of a head's value columns and keeps its part of the state transposed, S^T [16 x dk], in the
+// accumulators of its matrix instructions. An accumulator's layout is an operand's too, so the chain S -> R -> U -> S' never
+// leaves the warp's registers and warps never wait for one another: the next block's tiles arrive meanwhile. mma.sync
+// and not tcgen05: its operands would come from shared memory, so every block would move the state and R, U as pairs through it
+// four times, one after another, on a chain that has nothing else to do.
+#include "sdm_gdr.cuh"
+
+namespace sdm {
+namespace gdr {
+namespace {
+
+// ---- float32 rows as three planes of bfloat16 ------------------------------------------------------------------
+__global__ void __launch_bounds__(256) gdr_split_kernel(const float* x, int64_t ld, int64_t rows, int cols, __nv_bfloat16* out) {
+    start_dependent();
+    const int units = cols / 4;
+    const int64_t n = rows * units;
+    for (int64_t i = blockIdx.x * int64_t(256) + threadIdx.x; i < n; i += gridDim.x * int64_t(256)) {
+        const int64_t r = i / units;
+        const int c = static_cast<int>(i - r * units) * 4;
+        float v[4];
+        load4(x + r * ld + c).get(v);
+        uint32_t a[3], b[3];
+        split2<3>(v[0], v[1], a);
+        split2<3>(v[2], v[3], b);
+#pragma unroll
+        for (int t = 0; t < 3; ++t) *reinterpret_cast<uint2*>(out + (t * rows + r) * cols + c) = make_uint2(a[t], b[t]);
+    }
+}
+
+// ---- what a block's rows give without the state ---------------------------------------------------------------
+// A block of 4 warps for each block of rows and key head; warp w holds rows 16 w .. of K K^T and Q K^T, and for each value head of
+// the key head weighs them by its decays. T is built from its 16 x 16 blocks: those on the diagonal row by row in float32 (a
+// column a lane), those below by T_21 = -T_22 (N_21 T_11), first for 32 rows, then for 64, in products of terms.
+template <int XT, int DKP>
+__global__ void __launch_bounds__(128) gdr_prepare_kernel(const __grid_constant__ Args a) {
+    constexpr int kTile = kC * DKP * 2, kPlane = kC * kC * 2, NS = XT == 1 ? 2 : 3;
+    extern __shared__ __align__(1024) unsigned char smem[];
+    __shared__ float gh[kC], gl[kC], be[kC];
+    __shared__ float diag[4][16][17];
+    start_dependent();
+    const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, g = lane >> 2, qd = lane & 3;
+    const int64_t id = blockIdx.x / a.Hk;
+    const int kh = blockIdx.x - static_cast<int>(id) * a.Hk;
+    int64_t b;
+    int n;
+    block_rows(a, id, b, n);
+    if (n <= 0) return;
+    const uint32_t K = smem_of(smem), Q = K + XT * kTile, N = Q + XT * kTile, T = N + NS * kPlane;
+    load_rows<DKP, 128>(K, a.k, XT, b, n, kh * a.dk, a.dk, tid);
+    load_rows<DKP, 128>(Q, a.q, XT, b, n, kh * a.dk, a.dk, tid);
+    copies_commit();
+    copies_wait<0>();
+    __syncthreads();
+    const Lane L(lane);
+    float kk[8][4] = {}, qk[8][4] = {};
+#pragma unroll
+    for (int kt = 0; kt < DKP / 16; ++kt) {
+        uint32_t ka[XT][4], qa[XT][4];
+#pragma unroll
+        for (int x = 0; x < XT; ++x) {
+            ldsm4(ka[x], K + x * kTile + tile_at<DKP>(16 * w + L.rA, 2 * kt + L.uA));
+            ldsm4(qa[x], Q + x * kTile + tile_at<DKP>(16 * w + L.rA, 2 * kt + L.uA));
+        }
+#pragma unroll
+        for (int np = 0; np < 4; ++np) {
+            if (np > w) continue;
+#pragma unroll
+            for (int x = 0; x < XT; ++x) {
+                uint32_t f[4];
+                ldsm4(f, K + x * kTile + tile_at<DKP>(16 * np + L.rB, 2 * kt + L.uB));
+#pragma unroll
+                for (int y = 0; y < XT - x; ++y) {
+                    mma(kk[2 * np], ka[y], f[0], f[1]);
+                    mma(kk[2 * np + 1], ka[y], f[2], f[3]);
+                    mma(qk[2 * np], qa[y], f[0], f[1]);
+                    mma(qk[2 * np + 1], qa[y], f[2], f[3]);
+                }
+            }
+        }
+    }
+    const int R = a.Hv / a.Hk, a_planes = a.tri_planes - NS;
+    for (int rv = 0; rv < R; ++rv) {
+        const int h = kh * R + rv;
+        __nv_bfloat16* const tri = a.tri + (id * a.Hv + h) * a.tri_planes * int64_t(kC * kC);
+        float* const vec = a.vec + (id * a.Hv + h) * kVecs * kC;
+        if (w == 0) {
+            // gates below -150 are 0 to float32 like -150 (a product with them is), and their sums stay finite. Sums in 64
+            // bits, kept as two floats: e^(gam_i - gam_j) then has the error of one exponential.
+            double s[2];
+            float bt[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int r = 2 * lane + e;
+                const float x = r < n ? gate_at(a.g, (b + r) * a.g_ld + h, a.g_bf16) : 0.f;
+                s[e] = x < -150.f ? -150.f : x;
+                bt[e] = r < n ? gate_at(a.beta, (b + r) * a.b_ld + h, a.g_bf16) : 0.f;
+            }
+            s[1] += s[0];
+            double run = s[1];
+#pragma unroll
+            for (int d = 1; d < 32; d *= 2) {
+                const double o = __shfl_up_sync(kFull, run, d);
+                if (lane >= d) run += o;
+            }
+            const double last = __shfl_sync(kFull, run, 31);
+            const double before = run - s[1];   // exact enough: both are sums of the same terms in 53 bits
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int r = 2 * lane + e;
+                const double gam = e ? run : before + s[0];
+                const float hi = static_cast<float>(gam), lo = static_cast<float>(gam - hi);
+                gh[r] = hi;
+                gl[r] = lo;
+                be[r] = strength(bt[e]);
+                vec[3 * kC + r] = hi;
+                vec[4 * kC + r] = lo;
+                const float x = expf(hi);
+                vec[r] = fmaf(x, lo, x);
+                vec[kC + r] = bt[e];
+                vec[2 * kC + r] = expf(static_cast<float>(last - gam));
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int nt = 0; nt < 8; ++nt) {
+            if (nt > 2 * w + 1) continue;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {   // the two rows of a lane's accumulators
+                const int i = 16 * w + g + 8 * e, j = 8 * nt + 2 * qd;
+                float av[2], nv[2];
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const float d = expf((gh[i] - gh[j + c]) + (gl[i] - gl[j + c]));
+                    av[c] = j + c <= i ? d * qk[nt][2 * e + c] : 0.f;
+                    nv[c] = j + c < i ? be[i] * (d * kk[nt][2 * e + c]) : 0.f;
+                    if (nt >> 1 == w) diag[w][g + 8 * e][j + c - 16 * w] = nv[c];
+                }
+                uint32_t t[3];
+                split2<3>(av[0], av[1], t);
+                uint32_t* const A = reinterpret_cast<uint32_t*>(tri + NS * kC * kC + i * kC + j);
+                for (int pl = 0; pl < a_planes; ++pl) A[pl * (kC * kC / 2)] = pl == 0 ? t[0] : pl == 1 ? t[1] : t[2];
+                uint32_t u[NS];
+                split2<NS>(nv[0], nv[1], u);
+#pragma unroll
+                for (int pl = 0; pl < NS; ++pl) st_word(N + pl * kPlane + tile_at<kC>(i, j >> 3) + (j & 7) * 2, u[pl]);
+            }
+        }
+        __syncwarp();
+        {   // the diagonal block: column c of (I + N)^-1, from the top down
+            const int c = lane & 15;
+            float x[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                float s = i == c ? 1.f : 0.f;
+#pragma unroll
+                for (int j = 0; j < i; ++j) s = fmaf(-diag[w][i][j], x[j], s);
+                x[i] = s;
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                // lane c and c + 1 share a word: the even one writes
+                const float other = __shfl_down_sync(kFull, x[i], 1);
+                uint32_t t[NS];
+                split2<NS>(x[i], other, t);
+                if (lane < 16 && !(lane & 1)) {
+#pragma unroll
+                    for (int pl = 0; pl < NS; ++pl)
+                        st_word(T + pl * kPlane + tile_at<kC>(16 * w + i, 2 * w + (c >> 3)) + (c & 7) * 2, t[pl]);
+                }
+            }
+        }
+        __syncthreads();
+        // 8 columns of a warp: y = N_21 T_11, out = -T_22 y. M: tiles of 16 rows (and of 16 summands) of a side.
+        auto below = [&](auto mt, int r0, int c0, int c) {
+            constexpr int M = decltype(mt)::value;
+            float y[M][4] = {};
+#pragma unroll
+            for (int kt = 0; kt < M; ++kt) {
+                if (kt < (c - c0) / 16) continue;   // T_11 is zero above the diagonal
+                uint32_t t[NS][4];
+#pragma unroll
+                for (int p = 0; p < NS; ++p) ldsm4t(t[p], T + p * kPlane + tile_at<kC>(c0 + 16 * kt + L.rBt, c / 8));
+#pragma unroll
+                for (int m = 0; m < M; ++m) {
+#pragma unroll
+                    for (int p = 0; p < NS; ++p) {
+                        uint32_t f[4];
+                        ldsm4(f, N + p * kPlane + tile_at<kC>(r0 + 16 * m + L.rA, c0 / 8 + 2 * kt + L.uA));
+#pragma unroll
+                        for (int q = 0; q < NS - p; ++q) mma(y[m], f, t[q][0], t[q][1]);
+                    }
+                }
+            }
+            uint32_t yt[M][2][NS];
+#pragma unroll
+            for (int m = 0; m < M; ++m)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    split2<NS>(-y[m][2 * e], -y[m][2 * e + 1], yt[m][e]);
+#pragma unroll
+                    for (int p = 0; p < NS; ++p) yt[m][e][p] = transposed(yt[m][e][p]);
+                }
+#pragma unroll
+            for (int m = 0; m < M; ++m) {
+                float o[4] = {};
+#pragma unroll
+                for (int kt = 0; kt <= m; ++kt) {
+#pragma unroll
+                    for (int p = 0; p < NS; ++p) {
+                        uint32_t f[4];
+                        ldsm4(f, T + p * kPlane + tile_at<kC>(r0 + 16 * m + L.rA, r0 / 8 + 2 * kt + L.uA));
+#pragma unroll
+                        for (int q = 0; q < NS - p; ++q) mma(o, f, yt[kt][0][q], yt[kt][1][q]);
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    uint32_t t[NS];
+                    split2<NS>(o[2 * e], o[2 * e + 1], t);
+#pragma unroll
+                    for (int p = 0; p < NS; ++p) st_word(T + p * kPlane + tile_at<kC>(r0 + 16 * m + g + 8 * e, c / 8) + qd * 4, t[p]);
+                }
+            }
+        };
+        below(std::integral_constant<int, 1>{}, 32 * (w >> 1) + 16, 32 * (w >> 1), 32 * (w >> 1) + 8 * (w & 1));
+        __syncthreads();
+        below(std::integral_constant<int, 2>{}, 32, 0, 8 * w);
+        __syncthreads();
+        for (int i = tid; i < NS * kC * 8; i += 128) {
+            const int p = i >> 9, r = (i >> 3) & 63, u = i & 7;
+            if (u > (r >> 4) * 2 + 1) continue;
+            const uint4 v = *reinterpret_cast<const uint4*>(smem + (T - K) + p * kPlane + tile_at<kC>(r, u));
+            *reinterpret_cast<uint4*>(tri + p * kC * kC + r * kC + u * 8) = v;
+        }
+        if (rv + 1 < R) __syncthreads();
+    }
+}
+
+// ---- the walk ---------------------------------------------------------------------------------------------------
+template <int XT, int DKP, int BV>
+struct Walk {
+    static constexpr int NS = XT == 1 ? 2 : 3;   // terms of what is computed
+    static constexpr int kTile = kC * DKP * 2, kVal = kC * BV * 2, kPlane = kC * kC * 2;
+    static constexpr int K = 0, Q = K + XT * kTile, V = Q + XT * kTile, T = V + XT * kVal, A = T + NS * kPlane,
+                         vec = A + XT * kPlane, stage = vec + 3 * kC * 4, kKeep = NS * 16 * DKP * 2;
+    static constexpr int warps = BV / 16, threads = warps * 32;
+    static constexpr int stages = 2 * stage + warps * kKeep <= 227 * 1024 ? 2 : 1;
+    static constexpr int bytes(bool saving) { return stages * stage + (saving ? warps * kKeep : 0); }
+};
+
+template <int XT, int DKP, int BV, typename X>
+__global__ void __launch_bounds__(BV * 2) gdr_walk_kernel(const __grid_constant__ Args a) {
+    using W = Walk<XT, DKP, BV>;
+    constexpr int KT = DKP / 16, NS = W::NS;
+    extern __shared__ __align__(1024) unsigned char smem[];
+    start_dependent();
+    const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, g = lane >> 2, qd = lane & 3;
+    const int slices = (a.dv + BV - 1) / BV;
+    const int rank = blockIdx.x / (a.Hv * slices), rest = blockIdx.x - rank * a.Hv * slices;
+    const int h = rest / slices, c0 = (rest - h * slices) * BV;
+    const int p = by_length(a, rank), kh = h / (a.Hv / a.Hk);
+    int64_t b, len;
+    sequence(a, p, b, len);
+    const int64_t blocks = (len + kC - 1) / kC, id0 = first_block(b, p);
+    const uint32_t base = smem_of(smem);
+    const int cols = min(BV, a.dv - c0);
+
+    auto load = [&](int64_t j, int s) {
+        const uint32_t st = base + s * W::stage;
+        const int n = static_cast<int>(min(len - j * kC, int64_t(kC)));
+        const int64_t r0 = b + j * kC;
+        load_rows<DKP, W::threads>(st + W::K, a.k, XT, r0, n, kh * a.dk, a.dk, tid);
+        load_rows<DKP, W::threads>(st + W::Q, a.q, XT, r0, n, kh * a.dk, a.dk, tid);
+        load_rows<BV, W::threads>(st + W::V, a.v, XT, r0, n, h * a.dv + c0, cols, tid);
+        const int64_t at = (id0 + j) * a.Hv + h;
+        const __nv_bfloat16* const tri = a.tri + at * a.tri_planes * int64_t(kC * kC);
+#pragma unroll
+        for (int pl = 0; pl < NS + XT; ++pl) load_tri<W::threads>(st + W::T + pl * W::kPlane, tri + pl * kC * kC, tid);
+        if (tid < 48) copy16(st + W::vec + tid * 16, a.vec + at * kVecs * kC + tid * 4, true);
+        copies_commit();
+    };
+
+    const Lane L(lane);
+    float S[2 * KT][4];   // S^T: 16 value columns x dk
+    const int vc = c0 + 16 * w + g;   // this lane's value columns: vc and vc + 8
+    {
+        const float* const h0 = a.h0 == nullptr ? nullptr : a.h0 + (static_cast<int64_t>(p) * a.Hv + h) * a.dk * a.dv;
+#pragma unroll
+        for (int t = 0; t < 2 * KT; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int d = 8 * t + 2 * qd + (e & 1), c = vc + (e >> 1) * 8;
+                S[t][e] = h0 != nullptr && d < a.dk && c < a.dv ? h0[static_cast<int64_t>(d) * a.dv + c] : 0.f;
+            }
+    }
+    const uint32_t keep = base + W::stages * W::stage + w * W::kKeep;
+    if (blocks > 0 && W::stages == 2) load(0, 0);
+    for (int64_t j = 0; j < blocks; ++j) {
+        const int at = W::stages == 2 ? static_cast<int>(j & 1) : 0;
+        if (W::stages == 1) {
+            __syncthreads();
+            load(j, 0);
+        }
+        copies_wait<0>();
+        __syncthreads();
+        if (W::stages == 2 && j + 1 < blocks) load(j + 1, at ^ 1);
+        const uint32_t st = base + at * W::stage;
+        const float* const vec = reinterpret_cast<const float*>(smem + at * W::stage + W::vec);
+        if (16 * w >= cols) continue;   // a warp without columns
+        if (a.states != nullptr) {
+            if (lane == 0) bulk_wait_read();
+            __syncwarp();
+        }
+        float r[8][4] = {}, o[8][4] = {};
+#pragma unroll
+        for (int kt = 0; kt < KT; ++kt) {   // K S and Q S
+            uint32_t s[NS][4];
+            terms_of<NS>(S[2 * kt], S[2 * kt + 1], s);
+            if (a.states != nullptr) {
+#pragma unroll
+                for (int t = 0; t < NS; ++t) stsm4(keep + t * (16 * DKP * 2) + tile_at<DKP>(L.rA, 2 * kt + L.uA), s[t]);
+            }
+            products<NS, XT, NS, false, 4>(r, s, W::kTile, [&](int np) { return st + W::K + tile_at<DKP>(16 * np + L.rB, 2 * kt + L.uB); });
+            products<NS, XT, NS, false, 4>(o, s, W::kTile, [&](int np) { return st + W::Q + tile_at<DKP>(16 * np + L.rB, 2 * kt + L.uB); });
+        }
+        if (a.states != nullptr) {   // the state before the block, for the backward
+            async_fence();
+            __syncwarp();
+            if (lane == 0) {
+                const int groups = (a.dv + 15) / 16;
+                bulk_store(a.states + (((id0 + j) * a.Hv + h) * groups + c0 / 16 + w) * int64_t(NS * 16 * DKP), keep, W::kKeep);
+                bulk_commit();
+            }
+        }
+        // r = beta (v - e^gam K S); o = e^gam Q S
+#pragma unroll
+        for (int np = 0; np < 4; ++np) {
+            uint32_t f[XT][4];
+#pragma unroll
+            for (int x = 0; x < XT; ++x) ldsm4t(f[x], st + W::V + x * W::kVal + tile_at<BV>(16 * np + L.rAt, 2 * w + L.uAt));
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                const int nt = 2 * np + t;
+                const float2 eg = *reinterpret_cast<const float2*>(vec + 8 * nt + 2 * qd);
+                const float2 bt = *reinterpret_cast<const float2*>(vec + kC + 8 * nt + 2 * qd);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float v = 0.f;
+#pragma unroll
+                    for (int x = XT - 1; x >= 0; --x) {
+                        const uint32_t word = f[x][2 * t + (e >> 1)];
+                        v += __uint_as_float(e & 1 ? word & 0xFFFF0000u : word << 16);
+                    }
+                    const float x = e & 1 ? eg.y : eg.x;
+                    r[nt][e] = (e & 1 ? bt.y : bt.x) * fmaf(-x, r[nt][e], v);
+                    o[nt][e] *= x;
+                }
+            }
+        }
+        float u[8][4] = {};
+#pragma unroll
+        for (int kt = 0; kt < 4; ++kt) {   // U = T r
+            uint32_t f[NS][4];
+            terms_of<NS>(r[2 * kt], r[2 * kt + 1], f);
+            products<NS, NS, NS, false, 4>(u, f, W::kPlane, [&](int np) { return st + W::T + tile_at<kC>(16 * np + L.rB, 2 * kt + L.uB); }, kt);
+        }
+        const float last = vec[kC - 1];
+#pragma unroll
+        for (int t = 0; t < 2 * KT; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) S[t][e] *= last;
+#pragma unroll
+        for (int kt = 0; kt < 4; ++kt) {   // A U, and K^T (e^(gam_last - gam) U)
+            uint32_t f[NS][4];
+            terms_of<NS>(u[2 * kt], u[2 * kt + 1], f);
+            products<NS, XT, NS, false, 4>(o, f, W::kPlane, [&](int np) { return st + W::A + tile_at<kC>(16 * np + L.rB, 2 * kt + L.uB); }, kt);
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                const float2 c = *reinterpret_cast<const float2*>(vec + 2 * kC + 16 * kt + 8 * t + 2 * qd);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) u[2 * kt + t][e] *= e & 1 ? c.y : c.x;
+            }
+            terms_of<NS>(u[2 * kt], u[2 * kt + 1], f);
+            products<NS, XT, NS, true, KT>(S, f, W::kTile, [&](int np) { return st + W::K + tile_at<DKP>(16 * kt + L.rBt, 2 * np + L.uBt); });
+        }
+        // the rows' answers
+        const int64_t r0 = b + j * kC;
+        const int n = static_cast<int>(min(len - j * kC, int64_t(kC)));
+        if constexpr (sizeof(X) == 2) {
+            // turned in the tile of V, whose columns of this warp have been read
+#pragma unroll
+            for (int np = 0; np < 4; ++np) {
+                uint32_t f[4];
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    f[2 * t] = round2(o[2 * np + t][0] * a.scale, o[2 * np + t][1] * a.scale);
+                    f[2 * t + 1] = round2(o[2 * np + t][2] * a.scale, o[2 * np + t][3] * a.scale);
+                }
+                stsm4t(st + W::V + tile_at<BV>(16 * np + L.rAt, 2 * w + L.uAt), f);
+            }
+            __syncwarp();
+#pragma unroll
+            for (int i = lane; i < kC * 2; i += 32) {
+                const int row = i >> 1, u8 = 2 * w + (i & 1);
+                if (row < n && u8 * 8 < cols) {
+                    const uint4 v = *reinterpret_cast<const uint4*>(smem + at * W::stage + W::V + tile_at<BV>(row, u8));
+                    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.y) + (r0 + row) * a.y_ld + h * a.dv + c0 + u8 * 8) = v;
+                }
+            }
+        } else {
+#pragma unroll
+            for (int nt = 0; nt < 8; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int row = 8 * nt + 2 * qd + (e & 1), c = vc + (e >> 1) * 8;
+                    if (row < n && c < a.dv) static_cast<float*>(a.y)[(r0 + row) * a.y_ld + h * a.dv + c] = o[nt][e] * a.scale;
+                }
+        }
+    }
+    if (a.hT != nullptr && 16 * w < cols) {
+        float* const hT = a.hT + (static_cast<int64_t>(p) * a.Hv + h) * a.dk * a.dv;
+#pragma unroll
+        for (int t = 0; t < 2 * KT; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int d = 8 * t + 2 * qd + (e & 1), c = vc + (e >> 1) * 8;
+                if (d < a.dk && c < a.dv) hT[static_cast<int64_t>(d) * a.dv + c] = S[t][e];
+            }
+    }
+    if (a.states != nullptr && lane == 0) bulk_wait();
+}
+
+// ---- one token of every request -----------------------------------------------------------------------------------
+// y = scale (e^g S^T q + (k.q) u), so one look at the state gives S^T k and S^T q together; it stays in registers until
+// u is known, and is written once. Bound by HBM: 8 bytes an element of the state.
+struct StepArgs {
+    const void* q;
+    const void* k;
+    const void* v;
+    const void* g;
+    const void* beta;
+    const int32_t* slots;   // nullable
+    float* state;
+    void* y;
+    uint32_t* status;       // nullable
+    int64_t q_ld, k_ld, v_ld, g_ld, b_ld, s_ld, y_ld, states;
+    int Hk, Hv, dk, dv, g_bf16;
+    float scale;
+};
+
+template <typename X>
+__device__ __forceinline__ float value_at(const void* p, int64_t i) {
+    return widen(static_cast<const X*>(p)[i]);
+}
+
+// A block holds `cols` value columns of a head's state (a multiple of 4): thread t the columns 4 (t % (cols / 4)) .. and RPT
+// rows from RPT (t / (cols / 4)) on.
+template <typename X, int RPT>
+__global__ void __launch_bounds__(256) gdr_step_kernel(const __grid_constant__ StepArgs a, int cols) {
+    __shared__ float sk[kMaxD], sq[kMaxD];
+    __shared__ __align__(16) float part[2][32][kMaxD];
+    start_dependent();
+    const int tid = threadIdx.x, slices = (a.dv + cols - 1) / cols;
+    const int64_t unit = blockIdx.x / slices;
+    const int c0 = (blockIdx.x - static_cast<int>(unit) * slices) * cols;
+    const int64_t i = unit / a.Hv;
+    const int h = static_cast<int>(unit - i * a.Hv), kh = h / (a.Hv / a.Hk);
+    const int64_t slot = a.slots == nullptr ? i : a.slots[i];
+    const int n = min(cols, a.dv - c0), cg = cols / 4;
+    const int c = (tid % cg) * 4, part_of = tid / cg, parts = (a.dk + RPT - 1) / RPT, d0 = part_of * RPT;
+    if (slot < 0 || slot >= a.states) {
+        if (slot >= a.states && tid == 0 && a.status != nullptr) atomicOr(a.status, SDM_DEV_BAD_SLOT);
+        for (int e = tid; e < n; e += 256) st1(static_cast<X*>(a.y) + i * a.y_ld + h * a.dv + c0 + e, 0.f);
+        return;
+    }
+    const bool on = part_of < parts && c < n;
+    float* const st = a.state + slot * a.s_ld + static_cast<int64_t>(h) * a.dk * a.dv + c0 + c;
+    float4 s[RPT];
+#pragma unroll
+    for (int r = 0; r < RPT; ++r)
+        s[r] = on && d0 + r < a.dk ? *reinterpret_cast<const float4*>(st + static_cast<int64_t>(d0 + r) * a.dv) : make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int d = tid; d < a.dk; d += 256) {
+        sk[d] = value_at<X>(a.k, i * a.k_ld + kh * a.dk + d);
+        sq[d] = value_at<X>(a.q, i * a.q_ld + kh * a.dk + d);
+    }
+    const float decay = expf(gate_at(a.g, i * a.g_ld + h, a.g_bf16)), beta = gate_at(a.beta, i * a.b_ld + h, a.g_bf16);
+    float v[4] = {};
+    if (on) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = value_at<X>(a.v, i * a.v_ld + h * a.dv + c0 + c + e);
+    }
+    __syncthreads();
+    float pk[4] = {}, pq[4] = {}, kq = 0.f;
+    if (on) {
+#pragma unroll
+        for (int r = 0; r < RPT; ++r) {
+            if (d0 + r >= a.dk) break;
+            const float k = sk[d0 + r], q = sq[d0 + r];
+            pk[0] = fmaf(s[r].x, k, pk[0]); pk[1] = fmaf(s[r].y, k, pk[1]); pk[2] = fmaf(s[r].z, k, pk[2]); pk[3] = fmaf(s[r].w, k, pk[3]);
+            pq[0] = fmaf(s[r].x, q, pq[0]); pq[1] = fmaf(s[r].y, q, pq[1]); pq[2] = fmaf(s[r].z, q, pq[2]); pq[3] = fmaf(s[r].w, q, pq[3]);
+        }
+        st4(&part[0][part_of][c], pk);
+        st4(&part[1][part_of][c], pq);
+    }
+    for (int d = tid & 31; d < a.dk; d += 32) kq = fmaf(sk[d], sq[d], kq);
+#pragma unroll
+    for (int m = 16; m > 0; m /= 2) kq += __shfl_xor_sync(kFull, kq, m);
+    __syncthreads();
+    if (!on) return;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) pk[e] = pq[e] = 0.f;
+    for (int p = 0; p < parts; ++p) {
+        float x[4];
+        get4(&part[0][p][c], x);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) pk[e] += x[e];
+        if (part_of == 0) {
+            get4(&part[1][p][c], x);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) pq[e] += x[e];
+        }
+    }
+    float u[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) u[e] = beta * fmaf(-decay, pk[e], v[e]);
+#pragma unroll
+    for (int r = 0; r < RPT; ++r) {
+        if (d0 + r >= a.dk) break;
+        const float k = sk[d0 + r];
+        const float4 t = {fmaf(k, u[0], decay * s[r].x), fmaf(k, u[1], decay * s[r].y), fmaf(k, u[2], decay * s[r].z),
+                          fmaf(k, u[3], decay * s[r].w)};
+        *reinterpret_cast<float4*>(st + static_cast<int64_t>(d0 + r) * a.dv) = t;
+    }
+    if (part_of == 0) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) pq[e] = a.scale * fmaf(kq, u[e], decay * pq[e]);
+        st4(static_cast<X*>(a.y) + i * a.y_ld + h * a.dv + c0 + c, pq);
+    }
+}
+
+// ---- host side ------------------------------------------------------------------------------------------------------
+using checks::aligned16;
+using checks::aligned_all;
+
+int64_t up(int64_t n) { return (n + 255) / 256 * 256; }
+
+template <typename K>
+cudaError_t big_smem(K kernel, int bytes) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
+
+template <int XT, int DKP>
+cudaError_t prepare(const Args& a, int64_t blocks, cudaStream_t cs) {
+    constexpr int bytes = 2 * XT * kC * DKP * 2 + 2 * (XT == 1 ? 2 : 3) * kC * kC * 2;
+    auto* const k = gdr_prepare_kernel<XT, DKP>;
+    const cudaError_t e = big_smem(k, bytes);
+    if (e != cudaSuccess) return e;
+    return launch_dependent(k, dim3(static_cast<unsigned>(blocks * a.Hk)), dim3(128), bytes, cs, a);
+}
+
+template <int XT, int DKP, int BV>
+cudaError_t walk(const Args& a, cudaStream_t cs) {
+    using X = std::conditional_t<XT == 1, __nv_bfloat16, float>;
+    using W = Walk<XT, DKP, BV>;
+    auto* const k = gdr_walk_kernel<XT, DKP, BV, X>;
+    const int bytes = W::bytes(a.states != nullptr);
+    const cudaError_t e = big_smem(k, bytes);
+    if (e != cudaSuccess) return e;
+    const int64_t grid = static_cast<int64_t>(a.P) * a.Hv * ((a.dv + BV - 1) / BV);
+    return launch_dependent(k, dim3(static_cast<unsigned>(grid)), dim3(W::threads), bytes, cs, a);
+}
+
+template <int DKP>
+cudaError_t walk_bf16(const Args& a, cudaStream_t cs) {
+    switch (columns(a)) {
+        case 32: return walk<1, DKP, 32>(a, cs);
+        case 64: return walk<1, DKP, 64>(a, cs);
+        default: return walk<1, DKP, 128>(a, cs);
+    }
+}
+
+}  // namespace
+
+sdm_status check_shape(const sdm_gdr_shape* s) {
+    if (s == nullptr) return SDM_ERR_ARG;
+    if (s->x_dtype < 0 || s->x_dtype > 1 || s->g_dtype < 0 || s->g_dtype > 1) return SDM_ERR_DTYPE;
+    if (s->P < 1 || s->rows < 0 || s->rows > (int64_t(1) << 40) || s->k_heads < 1 || s->v_heads < 1 || s->v_heads > 65536 ||
+        s->v_heads % s->k_heads != 0 || s->dk < 1 || s->dk > kMaxD || s->dv < 1 || s->dv > kMaxD || !(s->scale == s->scale))
+        return SDM_ERR_SHAPE;
+    if (s->dk % 8 != 0 || s->dv % 8 != 0) return SDM_ERR_ALIGN;
+    if (blocks_of(s) > (int64_t(1) << 30) / s->v_heads || static_cast<int64_t>(s->P) * s->v_heads > (int64_t(1) << 28))
+        return SDM_ERR_SHAPE;
+    return SDM_OK;
+}
+
+Layout layout(const sdm_gdr_shape* s, bool backward) {
+    Layout l;
+    memset(&l, 0, sizeof(l));
+    const int64_t heads = blocks_of(s) * s->v_heads;
+    const bool f32 = s->x_dtype == SDM_F32;
+    int64_t at = 0;
+    auto take = [&](int64_t bytes) {
+        const int64_t here = at;
+        at += up(bytes);
+        return here;
+    };
+    l.tri = take(heads * (f32 ? 6 : backward ? 4 : 3) * kC * kC * 2);
+    l.vec = take(heads * kVecs * kC * 4);
+    if (f32) {
+        l.q = take(s->rows * s->k_heads * s->dk * 6);
+        l.k = take(s->rows * s->k_heads * s->dk * 6);
+        l.v = take(s->rows * s->v_heads * s->dv * 6);
+    }
+    if (backward) {
+        if (f32) l.dy = take(s->rows * s->v_heads * s->dv * 6);
+        const int64_t dvp = (s->dv + 15) / 16 * 16;
+        l.dstates = take(heads * dvp * padded(s->dk) * 2 * terms(s));
+        l.du = take(heads * kC * dvp * 2 * terms(s));
+        if (s->v_heads != s->k_heads) l.part = take(2 * s->rows * s->v_heads * s->dk * 4);
+    }
+    l.bytes = std::max<int64_t>(at, 256);
+    return l;
+}
+
+cudaError_t launch_split(const void* x, int64_t ld, int64_t rows, int cols, __nv_bfloat16* out, cudaStream_t cs) {
+    const int64_t blocks = std::min<int64_t>((rows * (cols / 4) + 255) / 256, 152 * 8);
+    return launch_dependent(gdr_split_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, cs, static_cast<const float*>(x), ld, rows,
+                            cols, out);
+}
+
+sdm_status check_inputs(const sdm_gdr_shape* s, const void* q, int64_t q_ld, const void* k, int64_t k_ld, const void* v, int64_t v_ld,
+                        const void* g, int64_t g_ld, const void* beta, int64_t b_ld, const int64_t* offsets, void* ws,
+                        size_t ws_bytes, bool backward, uint32_t* status, Args* a) {
+    sdm_status st = check_shape(s);
+    if (st != SDM_OK) return st;
+    if (offsets == nullptr && s->rows % s->P != 0) return SDM_ERR_SHAPE;
+    const int xe = s->x_dtype == SDM_BF16 ? 2 : 4, ge = s->g_dtype == SDM_BF16 ? 2 : 4;
+    const int64_t kn = static_cast<int64_t>(s->k_heads) * s->dk, vn = static_cast<int64_t>(s->v_heads) * s->dv;
+    if (s->rows > 0) {
+        if ((st = check_array(q, q_ld, kn, xe, 16, false)) != SDM_OK) return st;
+        if ((st = check_array(k, k_ld, kn, xe, 16, false)) != SDM_OK) return st;
+        if ((st = check_array(v, v_ld, vn, xe, 16, false)) != SDM_OK) return st;
+        if ((st = check_array(g, g_ld, s->v_heads, ge, ge, false)) != SDM_OK) return st;
+        if ((st = check_array(beta, b_ld, s->v_heads, ge, ge, false)) != SDM_OK) return st;
+    }
+    if (!aligned_all(8, {offsets}) || !aligned_all(4, {status})) return SDM_ERR_ALIGN;
+    const Layout l = layout(s, backward);
+    if (ws == nullptr || !aligned16(ws) || ws_bytes < static_cast<size_t>(l.bytes)) return SDM_ERR_WORKSPACE;
+    memset(a, 0, sizeof(*a));
+    a->P = s->P; a->Hk = s->k_heads; a->Hv = s->v_heads; a->dk = s->dk; a->dv = s->dv; a->rows = s->rows;
+    a->len = s->rows / s->P; a->scale = s->scale; a->g_bf16 = s->g_dtype == SDM_BF16;
+    a->g = g; a->g_ld = g_ld; a->beta = beta; a->b_ld = b_ld; a->offsets = offsets; a->status = status;
+    unsigned char* const w = static_cast<unsigned char*>(ws);
+    a->tri = reinterpret_cast<__nv_bfloat16*>(w + l.tri);
+    a->vec = reinterpret_cast<float*>(w + l.vec);
+    return SDM_OK;
+}
+
+cudaError_t launch_planes(const sdm_gdr_shape* s, const void* q, int64_t q_ld, const void* k, int64_t k_ld, const void* v, int64_t v_ld,
+                          void* ws, bool backward, Args* a, cudaStream_t cs) {
+    const Layout l = layout(s, backward);
+    const int64_t kn = static_cast<int64_t>(s->k_heads) * s->dk, vn = static_cast<int64_t>(s->v_heads) * s->dv;
+    cudaError_t e = cudaSuccess;
+    auto take = [&](Planes* p, const void* x, int64_t ld, int64_t n, int64_t at) {
+        if (s->x_dtype == SDM_BF16) {
+            *p = {static_cast<const __nv_bfloat16*>(x), ld, 0};
+            return;
+        }
+        __nv_bfloat16* const to = reinterpret_cast<__nv_bfloat16*>(static_cast<unsigned char*>(ws) + at);
+        *p = {to, n, s->rows * n};
+        if (e == cudaSuccess) e = launch_split(x, ld, s->rows, static_cast<int>(n), to, cs);
+    };
+    take(&a->q, q, q_ld, kn, l.q);
+    take(&a->k, k, k_ld, kn, l.k);
+    take(&a->v, v, v_ld, vn, l.v);
+    return e;
+}
+
+cudaError_t launch_prepare(const Args& a, const sdm_gdr_shape* s, cudaStream_t cs) {
+    const int64_t n = blocks_of(s);
+    if (s->x_dtype == SDM_BF16) return padded(s->dk) == 64 ? prepare<1, 64>(a, n, cs) : prepare<1, 128>(a, n, cs);
+    return padded(s->dk) == 64 ? prepare<3, 64>(a, n, cs) : prepare<3, 128>(a, n, cs);
+}
+
+}  // namespace gdr
+}  // namespace sdm
+
+using namespace sdm;
+using namespace sdm::gdr;
+
+extern "C" size_t sdm_gdr_states_bytes(const sdm_gdr_shape* shape) {
+    if (check_shape(shape) != SDM_OK) return 0;
+    return static_cast<size_t>(blocks_of(shape)) * shape->v_heads * ((shape->dv + 15) / 16 * 16) * padded(shape->dk) * 2 * terms(shape);
+}
+
+extern "C" size_t sdm_gdr_workspace_bytes(const sdm_gdr_shape* shape, int32_t backward) {
+    if (check_shape(shape) != SDM_OK) return 0;
+    return static_cast<size_t>(layout(shape, backward != 0).bytes);
+}
+
+extern "C" sdm_status sdm_gdr_forward(const sdm_gdr_shape* shape, const void* q, int64_t q_ld, const void* k, int64_t k_ld,
+                                      const void* v, int64_t v_ld, const void* g, int64_t g_ld, const void* beta,
+                                      int64_t beta_ld, const int64_t* offsets, const float* h0, void* y, int64_t y_ld,
+                                      float* hT, void* states, void* ws, size_t ws_bytes, uint32_t* status,
+                                      sdm_stream_t stream) {
+    Args a;
+    sdm_status st = check_inputs(shape, q, q_ld, k, k_ld, v, v_ld, g, g_ld, beta, beta_ld, offsets, ws, ws_bytes, false, status, &a);
+    if (st != SDM_OK) return st;
+    const int64_t vn = static_cast<int64_t>(shape->v_heads) * shape->dv;
+    if (shape->rows > 0 && (st = check_array(y, y_ld, vn, shape->x_dtype == SDM_BF16 ? 2 : 4, 16, true)) != SDM_OK) return st;
+    if (!aligned_all(16, {h0, hT, states})) return SDM_ERR_ALIGN;
+    a.h0 = h0; a.y = y; a.y_ld = y_ld; a.hT = hT;
+    a.states = static_cast<__nv_bfloat16*>(states);
+    a.tri_planes = shape->x_dtype == SDM_F32 ? 6 : 3;
+    const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+    cudaError_t e = cudaSuccess;
+    if (shape->rows > 0) {
+        e = launch_planes(shape, q, q_ld, k, k_ld, v, v_ld, ws, false, &a, cs);
+        if (e == cudaSuccess) e = launch_prepare(a, shape, cs);
+    }
+    const bool narrow = padded(shape->dk) == 64;
+    if (e == cudaSuccess) {
+        if (shape->x_dtype == SDM_BF16) e = narrow ? walk_bf16<64>(a, cs) : walk_bf16<128>(a, cs);
+        else e = narrow ? walk<3, 64, 32>(a, cs) : walk<3, 128, 32>(a, cs);
+    }
+    return e == cudaSuccess ? SDM_OK : SDM_ERR_CUDA;
+}
+
+extern "C" sdm_status sdm_gdr_step(const sdm_gdr_shape* shape, const void* q, int64_t q_ld, const void* k, int64_t k_ld,
+                                   const void* v, int64_t v_ld, const void* g, int64_t g_ld, const void* beta,
+                                   int64_t beta_ld, const int32_t* slots, float* state, int64_t state_ld, int64_t states,
+                                   void* y, int64_t y_ld, uint32_t* status, sdm_stream_t stream) {
+    sdm_status st = check_shape(shape);
+    if (st != SDM_OK) return st;
+    if (states < 0 || (slots == nullptr && states < shape->rows)) return SDM_ERR_SHAPE;
+    if (shape->rows == 0) return SDM_OK;
+    if (!aligned_all(4, {slots, status})) return SDM_ERR_ALIGN;
+    const int xe = shape->x_dtype == SDM_BF16 ? 2 : 4, ge = shape->g_dtype == SDM_BF16 ? 2 : 4;
+    const int64_t kn = static_cast<int64_t>(shape->k_heads) * shape->dk, vn = static_cast<int64_t>(shape->v_heads) * shape->dv;
+    if ((st = check_array(q, q_ld, kn, xe, 16, false)) != SDM_OK) return st;
+    if ((st = check_array(k, k_ld, kn, xe, 16, false)) != SDM_OK) return st;
+    if ((st = check_array(v, v_ld, vn, xe, 16, false)) != SDM_OK) return st;
+    if ((st = check_array(g, g_ld, shape->v_heads, ge, ge, false)) != SDM_OK) return st;
+    if ((st = check_array(beta, beta_ld, shape->v_heads, ge, ge, false)) != SDM_OK) return st;
+    if ((st = check_array(y, y_ld, vn, xe, 16, true)) != SDM_OK) return st;
+    if (states > 0 && (st = check_array(state, state_ld, vn * shape->dk, 4, 16, true)) != SDM_OK) return st;
+    StepArgs a;
+    memset(&a, 0, sizeof(a));
+    a.q = q; a.q_ld = q_ld; a.k = k; a.k_ld = k_ld; a.v = v; a.v_ld = v_ld; a.g = g; a.g_ld = g_ld; a.beta = beta; a.b_ld = beta_ld;
+    a.slots = slots; a.state = state; a.s_ld = state_ld; a.states = states; a.y = y; a.y_ld = y_ld; a.status = status;
+    a.Hk = shape->k_heads; a.Hv = shape->v_heads; a.dk = shape->dk; a.dv = shape->dv; a.g_bf16 = shape->g_dtype == SDM_BF16;
+    a.scale = shape->scale;
+    // 64 columns of a head to a block: 16 threads across, so 8 rows of up to 128 to each; narrower heads leave threads idle
+    const int cols = std::min(64, shape->dv), parts = 256 / (cols / 4);
+    const int64_t blocks = shape->rows * shape->v_heads * ((shape->dv + cols - 1) / cols);
+    if (blocks > 0x7FFFFFFF) return SDM_ERR_SHAPE;
+    const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+    auto launch = [&](auto x, auto rpt) {
+        return launch_dependent(gdr_step_kernel<decltype(x), decltype(rpt)::value>, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, cs, a, cols);
+    };
+    auto by_rows = [&](auto x) {
+        return (shape->dk + 3) / 4 <= std::min(parts, 32) ? launch(x, std::integral_constant<int, 4>{}) : launch(x, std::integral_constant<int, 8>{});
+    };
+    const cudaError_t e = shape->x_dtype == SDM_BF16 ? by_rows(__nv_bfloat16{}) : by_rows(0.f);
+    return e == cudaSuccess ? SDM_OK : SDM_ERR_CUDA;
+}

@@ -1,0 +1,331 @@
+// sdm_gdr.cuh -- what the kernels of the gated delta rule share (sdm_gdr.cu, sdm_gdr_bwd.cu): their arguments, how rows are cut
+// into blocks of 64, tiles of bfloat16 in shared memory, and the tensor cores' fragments.
+//
+// Mathematics. With gam the running sum of g over a block's rows, D_ij = e^(gam_i - gam_j), G = D o K K^T strictly below the
+// diagonal, A = D o Q K^T up to it, and T = (I + diag(beta) G)^-1, a block that starts from the state S gives
+//   R = V - e^gam o K S,   U = T (beta o R),   y = scale (e^gam o Q S + A U),   S' = e^gam_last S + K^T (e^(gam_last - gam) o U),
+// which is the rule row by row with the rows' writes u_t = beta_t (v_t - e^g_t S_{t-1}^T k_t) solved for together.
+//
+// Numbers. The tensor cores multiply bfloat16 and add in float32. A float32 operand is a sum of bfloat16 terms, its value
+// rounded, the rest rounded, and so on: two terms hold 16 bits of mantissa and a bit (2^-18 off at most), three hold all 24.
+// Of two such operands' product the terms (i, j) with i + j below the number of terms are taken. bfloat16 rows are exact
+// operands of one term, and what is computed from them has two: states, writes and the solution of the triangular system
+// keep 17 bits through a product and 24 where they are added (measured: states 4e-6 off 64 bits after 4096 rows, where the rows'
+// answers are rounded to 2e-3; a third term would bring 3e-7 for 1.4 times the products). float32 rows are cut into three
+// terms once, ahead of everything, and so are what is computed from them.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include <algorithm>
+#include <cstdint>
+#include <cstring>
+#include <type_traits>
+
+#include "sdm_operators.cuh"
+
+namespace sdm {
+namespace gdr {
+
+using namespace rows;
+
+constexpr int kC = SDM_GDR_CHUNK;   // rows of a block
+constexpr int kMaxD = 128;          // channels of a head at most
+constexpr int kVecs = 5;
+
+// A write strength below 2^-80 counts as 2^-80 in T and in the backward, so that the error v - e^g S^T k behind a write can
+// be had from the write: what a row of strength 0 writes is then 2^-80 of that error, which no other value feels.
+__device__ __forceinline__ float strength(float beta) { return fabsf(beta) < 0x1p-80f ? copysignf(0x1p-80f, beta) : beta; }
+
+// Rows as the tensor cores take them: planes of bfloat16 (one, or the three terms of float32 rows).
+struct Planes {
+    const __nv_bfloat16* p;
+    int64_t ld;      // elements between rows
+    int64_t plane;   // elements between planes
+};
+
+struct Args {
+    Planes q, k, v, dy;
+    const void* g;
+    const void* beta;
+    const int64_t* offsets;   // nullable: equal lengths
+    const float* h0;          // nullable
+    const float* dhT;         // nullable
+    float* hT;                // nullable
+    float* dh0;               // nullable
+    __nv_bfloat16* states;    // nullable in the forward: [blocks][Hv][dv / 16][terms], tiles [16 value columns][dk padded]
+    void* y;
+    void* dq;
+    void* dk_out;
+    void* dv_out;
+    void* dg;
+    void* dbeta;
+    __nv_bfloat16* tri;       // workspace: [blocks][Hv][planes][64][64], first T's terms, then A's
+    float* vec;               // workspace: [blocks][Hv][kVecs][64]: e^gam, beta, e^(gam_last - gam), gam as a sum of two floats
+    __nv_bfloat16* dstates;   // workspace of the backward: the gradients of the states behind the blocks, as `states`
+    __nv_bfloat16* du;        // workspace of the backward: [blocks][Hv][dv / 16][terms], tiles [64][16], the gradients of the writes, dv before beta
+    float* part;              // workspace of the backward: gradients of shared queries and keys
+    uint32_t* status;         // nullable
+    int64_t rows, len;        // len: rows of every sequence where offsets is null
+    int64_t g_ld, b_ld, y_ld, dq_ld, dk_ld, dv_ld, dg_ld, db_ld;
+    int P, Hk, Hv, dk, dv, g_bf16, tri_planes;
+    float scale;
+};
+
+// The rows [b, b + n) of sequence p. Offsets that are not ascending within [0, rows] are cut to it and reported.
+__device__ __forceinline__ void sequence(const Args& a, int p, int64_t& b, int64_t& n) {
+    if (a.offsets == nullptr) {
+        b = p * a.len;
+        n = a.len;
+        return;
+    }
+    const int64_t lo = a.offsets[p], hi = a.offsets[p + 1];
+    b = min(max(lo, int64_t(0)), a.rows);
+    n = max(min(hi, a.rows) - b, int64_t(0));
+    if ((lo < 0 || hi > a.rows || lo > hi) && a.status != nullptr && threadIdx.x == 0) atomicOr(a.status, SDM_DEV_BAD_OFFSET);
+}
+
+// Sequence p's blocks have the numbers from b / 64 + p on; numbers between two sequences' name nothing.
+__device__ __forceinline__ int64_t first_block(int64_t b, int p) { return b / kC + p; }
+
+// The rows [b, b + n) of block number `id`, n <= 0 where it names nothing. Warp-wide.
+__device__ __forceinline__ void block_rows(const Args& a, int64_t id, int64_t& b, int& n) {
+    const int lane = threadIdx.x & 31;
+    int lo = 0, hi = a.P;   // the last sequence whose first number is at most id is in [lo, hi): 32 probes a round
+    if (a.offsets == nullptr) {
+        // len / 64 + 1 numbers a sequence or one less: b / 64 + p with b = p len
+        while (hi - lo > 1) {
+            const int w = (hi - lo + 31) / 32, q = lo + (lane + 1) * w;
+            const bool le = q < hi && first_block(q * a.len, q) <= id;
+            const int c = __popc(__ballot_sync(kFull, le));
+            lo += c * w;
+            hi = min(hi, lo + w);
+        }
+    } else {
+        while (hi - lo > 1) {
+            const int w = (hi - lo + 31) / 32, q = lo + (lane + 1) * w;
+            const bool le = q < hi && first_block(min(max(a.offsets[q], int64_t(0)), a.rows), q) <= id;
+            const int c = __popc(__ballot_sync(kFull, le));
+            lo += c * w;
+            hi = min(hi, lo + w);
+        }
+    }
+    int64_t b0, len;
+    sequence(a, lo, b0, len);
+    const int64_t j = id - first_block(b0, lo);
+    b = b0 + j * kC;
+    n = j < 0 ? 0 : static_cast<int>(min(len - j * kC, int64_t(kC)));
+}
+
+// The sequence that a launch's rank-th one walks: the longest first where their number allows a look by one warp. Warp-wide.
+__device__ __forceinline__ int by_length(const Args& a, int rank) {
+    if (a.offsets == nullptr || a.P > 32 || a.P == 1) return rank;
+    const int lane = threadIdx.x & 31;
+    const int64_t mine = lane < a.P ? a.offsets[lane + 1] - a.offsets[lane] : -1;
+    int before = 0;
+    for (int q = 0; q < a.P; ++q) {
+        const int64_t other = __shfl_sync(kFull, mine, q);
+        before += other > mine || (other == mine && q < lane);
+    }
+    return __ffs(__ballot_sync(kFull, before == rank && lane < a.P)) - 1;
+}
+
+__device__ __forceinline__ float gate_at(const void* p, int64_t i, int bf16) {
+    return bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]) : static_cast<const float*>(p)[i];
+}
+
+// ---- tiles in shared memory: rows of W bfloat16 in units of 16 bytes, which the row's number permutes so that eight rows'
+// units of one column lie in different banks ------------------------------------------------------------
+template <int W>
+__device__ __forceinline__ uint32_t tile_at(int r, int u) {
+    constexpr int U = W / 8;
+    static_assert(U == 2 || U == 4 || U % 8 == 0, "tile width");
+    const int s = U >= 8 ? (r & 7) : U == 4 ? ((r >> 1) & 3) : ((r >> 2) & 1);
+    return static_cast<uint32_t>(r * (W * 2) + ((u ^ s) << 4));
+}
+__device__ __forceinline__ uint32_t smem_of(const void* p) { return static_cast<uint32_t>(__cvta_generic_to_shared(p)); }
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool there) {   // zeros where it is not
+    const int n = there ? 16 : 0;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// A tile of 64 rows x W columns of `planes` planes from rows [b, b + n) and columns [c0, c0 + cols) of x; the rest zeros.
+template <int W, int THREADS>
+__device__ __forceinline__ void load_rows(uint32_t dst, const Planes& x, int planes, int64_t b, int n, int c0, int cols, int tid) {
+    constexpr int U = W / 8;
+    for (int pl = 0; pl < planes; ++pl) {
+        const __nv_bfloat16* const src = x.p + pl * x.plane + b * x.ld + c0;
+#pragma unroll
+        for (int i = tid; i < kC * U; i += THREADS) {
+            const int r = i / U, u = i % U;
+            const bool there = r < n && u * 8 < cols;
+            copy16(dst + pl * (kC * W * 2) + tile_at<W>(r, u), there ? src + r * x.ld + u * 8 : x.p, there);
+        }
+    }
+}
+// A 64 x 64 plane's blocks of 16 up to the diagonal, as the workspace holds them
+template <int THREADS>
+__device__ __forceinline__ void load_tri(uint32_t dst, const __nv_bfloat16* src, int tid) {
+#pragma unroll
+    for (int i = tid; i < kC * 8; i += THREADS) {
+        const int r = i >> 3, u = i & 7;
+        if (u <= (r >> 4) * 2 + 1) copy16(dst + tile_at<kC>(r, u), src + r * kC + u * 8, true);
+    }
+}
+
+// ---- fragments ------------------------------------------------------------------------------------------
+// (loads of fragments keep their place among barriers and stores by being volatile; the products are free to move)
+__device__ __forceinline__ void ldsm4(uint32_t (&f)[4], uint32_t a) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(f[0]), "=r"(f[1]), "=r"(f[2]), "=r"(f[3]) : "r"(a));
+}
+__device__ __forceinline__ void ldsm4t(uint32_t (&f)[4], uint32_t a) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(f[0]), "=r"(f[1]), "=r"(f[2]), "=r"(f[3]) : "r"(a));
+}
+__device__ __forceinline__ void stsm4(uint32_t a, const uint32_t (&f)[4]) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(f[0]), "r"(f[1]), "r"(f[2]),
+                 "r"(f[3]) : "memory");
+}
+__device__ __forceinline__ void stsm4t(uint32_t a, const uint32_t (&f)[4]) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1,%2,%3,%4};" ::"r"(a), "r"(f[0]), "r"(f[1]),
+                 "r"(f[2]), "r"(f[3]) : "memory");
+}
+__device__ __forceinline__ void st_word(uint32_t a, uint32_t v) { asm volatile("st.shared.b32 [%0], %1;" ::"r"(a), "r"(v) : "memory"); }
+__device__ __forceinline__ uint32_t transposed(uint32_t f) {
+    uint32_t o;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(o) : "r"(f));
+    return o;
+}
+__device__ __forceinline__ void mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+// Two float32 as bfloat16 (the first in the low half), and as a sum of N such (an infinity's rests are NaN)
+__device__ __forceinline__ uint32_t round2(float x, float y) {
+    uint32_t o;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(o) : "f"(y), "f"(x));
+    return o;
+}
+template <int N>
+__device__ __forceinline__ void split2(float x, float y, uint32_t (&t)[N]) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        t[i] = round2(x, y);
+        if (i + 1 < N) {
+            x -= __uint_as_float(t[i] << 16);
+            y -= __uint_as_float(t[i] & 0xFFFF0000u);
+        }
+    }
+}
+// The places that a lane's address of ldsm4 / ldsm4t names in a tile, for fragments
+//   B of n x k from a tile [n][k] (not transposed): n 0..15, k 0..15 -> {b0, b1} of n 0..7, {b0, b1} of n 8..15
+//   B from a tile [k][n] (transposed): the same order
+//   A of m x k from a tile [m][k] (not transposed), and from a tile [k][m] (transposed)
+struct Lane {
+    int rB, uB;     // B, not transposed: row, unit
+    int rBt, uBt;   // B, transposed
+    int rA, uA;     // A, not transposed
+    int rAt, uAt;   // A, transposed (also an accumulator's own transpose)
+    __device__ __forceinline__ explicit Lane(int lane) {
+        const int m = lane >> 3, r = lane & 7;
+        rB = (m >> 1) * 8 + r; uB = m & 1;
+        rBt = (m & 1) * 8 + r; uBt = m >> 1;
+        rA = (m & 1) * 8 + r; uA = m >> 1;
+        rAt = (m >> 1) * 8 + r; uAt = m & 1;
+    }
+};
+// An operand A of 16 columns k from the accumulators of two neighbouring tiles of 8, in N terms
+template <int N>
+__device__ __forceinline__ void terms_of(const float (&c0)[4], const float (&c1)[4], uint32_t (&f)[N][4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float(&c)[4] = i < 2 ? c0 : c1;
+        uint32_t t[N];
+        split2<N>(c[2 * (i & 1)], c[2 * (i & 1) + 1], t);
+#pragma unroll
+        for (int n = 0; n < N; ++n) f[n][i] = t[n];
+    }
+}
+// acc += A B for an operand A of NA terms and tiles of 16 columns of B, np0 .. np1 - 1, of NB planes (`plane` bytes apart), whose
+// fragments `at(np)` names; terms (i, j) with i + j < N. The same accumulator comes round after the others.
+template <int NA, int NB, int N, bool TRANS, int NP, typename At, int M>
+__device__ __forceinline__ void products(float (&acc)[M][4], const uint32_t (&a)[NA][4], int plane, At at, int np0 = 0, int np1 = NP) {
+    constexpr int G = NP < 4 ? NP : 4;   // tiles whose fragments are held together
+#pragma unroll
+    for (int g0 = 0; g0 < NP; g0 += G) {
+#pragma unroll
+        for (int j = 0; j < (NB < N ? NB : N); ++j) {
+            uint32_t f[G][4];
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+                if (g0 + g < np0 || g0 + g >= np1) continue;
+                if (TRANS) ldsm4t(f[g], at(g0 + g) + j * plane);
+                else ldsm4(f[g], at(g0 + g) + j * plane);
+            }
+#pragma unroll
+            for (int i = 0; i < NA; ++i) {
+                if (i + j >= N) continue;
+#pragma unroll
+                for (int g = 0; g < G; ++g) {
+                    if (g0 + g < np0 || g0 + g >= np1) continue;
+                    mma(acc[2 * (g0 + g)], a[i], f[g][0], f[g][1]);
+                    mma(acc[2 * (g0 + g) + 1], a[i], f[g][2], f[g][3]);
+                }
+            }
+        }
+    }
+}
+
+// A whole tile in shared memory leaves for contiguous global memory by itself; the writes before were the block's own.
+__device__ __forceinline__ void bulk_store(void* dst, uint32_t src, int bytes) {
+    asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+__device__ __forceinline__ void async_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// ---- host side, in sdm_gdr.cu ---------------------------------------------------------------------------
+inline int padded(int d) { return d <= 64 ? 64 : 128; }
+inline int64_t blocks_of(const sdm_gdr_shape* s) { return s->rows / kC + s->P; }
+
+// Columns of a block of a walk: fewer while the grid leaves SMs idle.
+inline int columns(const Args& a) {
+    int bv = a.dv <= 32 ? 32 : a.dv <= 64 ? 64 : 128;
+    while (bv > 32 && static_cast<int64_t>(a.P) * a.Hv * ((a.dv + bv - 1) / bv) * 2 <= 152) bv /= 2;
+    return bv;
+}
+inline sdm_status check_array(const void* p, int64_t ld, int64_t n, int elem, int align, bool out) {
+    if (p == nullptr) return SDM_ERR_ARG;
+    if (reinterpret_cast<uintptr_t>(p) % align != 0 || (ld * elem) % align != 0) return SDM_ERR_ALIGN;
+    if (ld < (out ? n : 0) || ld > (int64_t(1) << 40)) return SDM_ERR_ARG;
+    return SDM_OK;
+}
+
+// The workspace's parts in bytes from its start
+struct Layout {
+    int64_t tri, vec, q, k, v, dy, dstates, du, part, bytes;
+};
+inline int terms(const sdm_gdr_shape* s) { return s->x_dtype == SDM_F32 ? 3 : 2; }   // of what is computed
+sdm_status check_shape(const sdm_gdr_shape* s);
+Layout layout(const sdm_gdr_shape* s, bool backward);
+// The checks of what both directions take, and the arguments that follow from it
+sdm_status check_inputs(const sdm_gdr_shape* s, const void* q, int64_t q_ld, const void* k, int64_t k_ld, const void* v, int64_t v_ld,
+                        const void* g, int64_t g_ld, const void* beta, int64_t b_ld, const int64_t* offsets, void* ws,
+                        size_t ws_bytes, bool backward, uint32_t* status, Args* a);
+cudaError_t launch_split(const void* x, int64_t ld, int64_t rows, int cols, __nv_bfloat16* out, cudaStream_t cs);
+// q, k and v as planes (float32 rows are cut first)
+cudaError_t launch_planes(const sdm_gdr_shape* s, const void* q, int64_t q_ld, const void* k, int64_t k_ld, const void* v, int64_t v_ld,
+                          void* ws, bool backward, Args* a, cudaStream_t cs);
+cudaError_t launch_prepare(const Args& a, const sdm_gdr_shape* s, cudaStream_t cs);
+
+}  // namespace gdr
+}  // namespace sdm

@@ -1,0 +1,764 @@
+// sdm_gdr_bwd.cu -- the gated delta rule's backward: sdm_gdr_backward (include/sdm.h; mathematics and numbers: sdm_gdr.cuh).
+//
+// With S and S' the states before and behind a block, dS' the gradient of the latter, W the gradients of the writes u (so that
+// dV = beta o W), and the forward's R, U, A, G, T:
+//   W  = T^T (scale A^T dY + e^(gam_last - gam) o K dS')
+//   dS = e^gam_last dS' + scale Q^T (e^gam o dY) - K^T (e^gam o dV)
+//   M  = dV U^T, N = scale dY U^T
+//   dQ = scale e^gam o dY S^T + (N o D) K
+//   dK = (N o D)^T Q - (M o D) K - (M o D)^T K - e^gam o dV S^T + e^(gam_last - gam) o U dS'^T     (M o D strictly below the diagonal)
+//   dbeta_i = W_i . U_i / beta_i
+// and dg_t sums what every decay over row t brings, never a difference of such sums, so that strong decays keep their digits:
+//   dg_t = sum_{j < t <= i} (N o A - M o G)_ij + sum_{i >= t} a_i + sum_{j < t} e_j + e^gam_last <dS', S>,
+//   a_i = e^gam_i (scale q_i . (S dY_i) - dV_i . (S^T k_i)),   e_j = e^(gam_last - gam_j) u_j . (dS'^T k_j).
+//
+// Three kernels: sdm_gdr.cu's of what needs no state, a walk from each sequence's end that carries dS as the forward's
+// carries S (a warp 16 value columns, transposed, nothing leaves its registers) and writes dV, W and every block's dS'; and one
+// for all blocks at once that has the rest, from the states that the forward saved.
+#include "sdm_gdr.cuh"
+
+namespace sdm {
+namespace gdr {
+namespace {
+
+// ---- the walk from the end -----------------------------------------------------------------------------------------
+template <int XT, int DKP, int BV>
+struct Back {
+    static constexpr int NS = XT == 1 ? 2 : 3;
+    static constexpr int kTile = kC * DKP * 2, kVal = kC * BV * 2, kPlane = kC * kC * 2;
+    static constexpr int K = 0, Q = K + XT * kTile, Y = Q + XT * kTile, T = Y + XT * kVal, A = T + NS * kPlane,
+                         vec = A + NS * kPlane, stage = vec + 3 * kC * 4, kKeep = NS * 16 * DKP * 2;
+    static constexpr int warps = BV / 16, threads = warps * 32;
+    static constexpr int stages = 2 * stage + warps * kKeep <= 227 * 1024 ? 2 : 1;
+    static constexpr int bytes = stages * stage + warps * kKeep;
+};
+
+template <int XT, int DKP, int BV, typename X>
+__global__ void __launch_bounds__(BV * 2) gdr_back_kernel(const __grid_constant__ Args a) {
+    using W = Back<XT, DKP, BV>;
+    constexpr int KT = DKP / 16, NS = W::NS;
+    extern __shared__ __align__(1024) unsigned char smem[];
+    start_dependent();
+    const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, g = lane >> 2, qd = lane & 3;
+    const int slices = (a.dv + BV - 1) / BV;
+    const int rank = blockIdx.x / (a.Hv * slices), rest = blockIdx.x - rank * a.Hv * slices;
+    const int h = rest / slices, c0 = (rest - h * slices) * BV;
+    const int p = by_length(a, rank), kh = h / (a.Hv / a.Hk);
+    int64_t b, len;
+    sequence(a, p, b, len);
+    const int64_t blocks = (len + kC - 1) / kC, id0 = first_block(b, p);
+    const uint32_t base = smem_of(smem);
+    const int cols = min(BV, a.dv - c0), groups = (a.dv + 15) / 16;
+
+    auto load = [&](int64_t j, int s) {
+        const uint32_t st = base + s * W::stage;
+        const int n = static_cast<int>(min(len - j * kC, int64_t(kC)));
+        const int64_t r0 = b + j * kC;
+        load_rows<DKP, W::threads>(st + W::K, a.k, XT, r0, n, kh * a.dk, a.dk, tid);
+        load_rows<DKP, W::threads>(st + W::Q, a.q, XT, r0, n, kh * a.dk, a.dk, tid);
+        load_rows<BV, W::threads>(st + W::Y, a.dy, XT, r0, n, h * a.dv + c0, cols, tid);
+        const int64_t at = (id0 + j) * a.Hv + h;
+        const __nv_bfloat16* const tri = a.tri + at * a.tri_planes * int64_t(kC * kC);
+#pragma unroll
+        for (int pl = 0; pl < 2 * NS; ++pl) load_tri<W::threads>(st + W::T + pl * W::kPlane, tri + pl * kC * kC, tid);
+        if (tid < 48) copy16(st + W::vec + tid * 16, a.vec + at * kVecs * kC + tid * 4, true);
+        copies_commit();
+    };
+
+    const Lane L(lane);
+    float S[2 * KT][4];   // dS^T: 16 value columns x dk
+    const int vc = c0 + 16 * w + g;
+    {
+        const float* const d = a.dhT == nullptr ? nullptr : a.dhT + (static_cast<int64_t>(p) * a.Hv + h) * a.dk * a.dv;
+#pragma unroll
+        for (int t = 0; t < 2 * KT; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int i = 8 * t + 2 * qd + (e & 1), c = vc + (e >> 1) * 8;
+                S[t][e] = d != nullptr && i < a.dk && c < a.dv ? d[static_cast<int64_t>(i) * a.dv + c] : 0.f;
+            }
+    }
+    const uint32_t keep = base + W::stages * W::stage + w * W::kKeep;
+    if (blocks > 0 && W::stages == 2) load(blocks - 1, 0);
+    for (int64_t it = 0; it < blocks; ++it) {
+        const int64_t j = blocks - 1 - it;
+        const int at = W::stages == 2 ? static_cast<int>(it & 1) : 0;
+        if (W::stages == 1) {
+            __syncthreads();
+            load(j, 0);
+        }
+        copies_wait<0>();
+        __syncthreads();
+        if (W::stages == 2 && j > 0) load(j - 1, at ^ 1);
+        const uint32_t st = base + at * W::stage;
+        const float* const vec = reinterpret_cast<const float*>(smem + at * W::stage + W::vec);
+        if (16 * w >= cols) continue;
+        if (lane == 0) bulk_wait_read();
+        __syncwarp();
+        const int64_t tile = ((id0 + j) * a.Hv + h) * groups + c0 / 16 + w;
+        float x[8][4] = {};
+#pragma unroll
+        for (int kt = 0; kt < KT; ++kt) {   // K dS'
+            uint32_t s[NS][4];
+            terms_of<NS>(S[2 * kt], S[2 * kt + 1], s);
+#pragma unroll
+            for (int t = 0; t < NS; ++t) stsm4(keep + t * (16 * DKP * 2) + tile_at<DKP>(L.rA, 2 * kt + L.uA), s[t]);
+            products<NS, XT, NS, false, 4>(x, s, W::kTile, [&](int np) { return st + W::K + tile_at<DKP>(16 * np + L.rB, 2 * kt + L.uB); });
+        }
+        async_fence();
+        __syncwarp();
+        if (lane == 0) {
+            bulk_store(a.dstates + tile * int64_t(NS * 16 * DKP), keep, W::kKeep);
+            bulk_commit();
+        }
+        const float last = vec[kC - 1];
+#pragma unroll
+        for (int t = 0; t < 2 * KT; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) S[t][e] *= last;
+        float u[8][4] = {};
+#pragma unroll
+        for (int kt = 0; kt < 4; ++kt) {   // A^T dY, and Q^T (scale e^gam dY)
+            uint32_t y[XT][4];
+#pragma unroll
+            for (int t = 0; t < XT; ++t) ldsm4t(y[t], st + W::Y + t * W::kVal + tile_at<BV>(16 * kt + L.rAt, 2 * w + L.uAt));
+            products<XT, NS, NS, true, 4>(u, y, W::kPlane, [&](int np) { return st + W::A + tile_at<kC>(16 * kt + L.rBt, 2 * np + L.uBt); }, 0, kt + 1);
+            // the operand's columns are rows: 16 kt + 2 qd + {0, 1}, and 8 on
+            uint32_t f[NS][4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 eg = *reinterpret_cast<const float2*>(vec + 16 * kt + 8 * (i >> 1) + 2 * qd);
+                float v0 = 0.f, v1 = 0.f;
+#pragma unroll
+                for (int t = XT - 1; t >= 0; --t) {
+                    v0 += __uint_as_float(y[t][i] << 16);
+                    v1 += __uint_as_float(y[t][i] & 0xFFFF0000u);
+                }
+                uint32_t o[NS];
+                split2<NS>(a.scale * eg.x * v0, a.scale * eg.y * v1, o);
+#pragma unroll
+                for (int t = 0; t < NS; ++t) f[t][i] = o[t];
+            }
+            products<NS, XT, NS, true, KT>(S, f, W::kTile, [&](int np) { return st + W::Q + tile_at<DKP>(16 * kt + L.rBt, 2 * np + L.uBt); });
+        }
+#pragma unroll
+        for (int nt = 0; nt < 8; ++nt) {
+            const float2 c = *reinterpret_cast<const float2*>(vec + 2 * kC + 8 * nt + 2 * qd);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) u[nt][e] = fmaf(e & 1 ? c.y : c.x, x[nt][e], a.scale * u[nt][e]);
+        }
+#pragma unroll
+        for (int nt = 0; nt < 8; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[nt][e] = 0.f;
+#pragma unroll
+        for (int kt = 0; kt < 4; ++kt) {   // W = T^T dU
+            uint32_t f[NS][4];
+            terms_of<NS>(u[2 * kt], u[2 * kt + 1], f);
+            products<NS, NS, NS, true, 4>(x, f, W::kPlane, [&](int np) { return st + W::T + tile_at<kC>(16 * kt + L.rBt, 2 * np + L.uBt); }, 0, kt + 1);
+        }
+        if (lane == 0) bulk_wait_read();   // the state's tile has left long ago
+        __syncwarp();
+#pragma unroll
+        for (int kt = 0; kt < 4; ++kt) {   // W leaves; dV = beta W; - K^T (e^gam dV)
+            uint32_t f[NS][4], o[NS][4];
+            terms_of<NS>(x[2 * kt], x[2 * kt + 1], f);
+#pragma unroll
+            for (int t = 0; t < NS; ++t) stsm4t(keep + t * (kC * 32) + tile_at<16>(16 * kt + L.rAt, L.uAt), f[t]);
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                const float2 bt = *reinterpret_cast<const float2*>(vec + kC + 16 * kt + 8 * t + 2 * qd);
+                const float2 eg = *reinterpret_cast<const float2*>(vec + 16 * kt + 8 * t + 2 * qd);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    x[2 * kt + t][e] *= e & 1 ? bt.y : bt.x;
+                    u[2 * kt + t][e] = -(e & 1 ? eg.y : eg.x) * x[2 * kt + t][e];
+                }
+            }
+            terms_of<NS>(u[2 * kt], u[2 * kt + 1], o);
+            products<NS, XT, NS, true, KT>(S, o, W::kTile, [&](int np) { return st + W::K + tile_at<DKP>(16 * kt + L.rBt, 2 * np + L.uBt); });
+        }
+        async_fence();
+        __syncwarp();
+        if (lane == 0) {
+            bulk_store(a.du + tile * int64_t(NS * kC * 16), keep, NS * kC * 32);
+            bulk_commit();
+        }
+        const int64_t r0 = b + j * kC;
+        const int n = static_cast<int>(min(len - j * kC, int64_t(kC)));
+        if constexpr (sizeof(X) == 2) {   // dV, turned in the tile of dY
+#pragma unroll
+            for (int np = 0; np < 4; ++np) {
+                uint32_t f[4];
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    f[2 * t] = round2(x[2 * np + t][0], x[2 * np + t][1]);
+                    f[2 * t + 1] = round2(x[2 * np + t][2], x[2 * np + t][3]);
+                }
+                stsm4t(st + W::Y + tile_at<BV>(16 * np + L.rAt, 2 * w + L.uAt), f);
+            }
+            __syncwarp();
+#pragma unroll
+            for (int i = lane; i < kC * 2; i += 32) {
+                const int row = i >> 1, u8 = 2 * w + (i & 1);
+                if (row < n && u8 * 8 < cols) {
+                    const uint4 v = *reinterpret_cast<const uint4*>(smem + at * W::stage + W::Y + tile_at<BV>(row, u8));
+                    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.dv_out) + (r0 + row) * a.dv_ld + h * a.dv + c0 + u8 * 8) = v;
+                }
+            }
+        } else {
+#pragma unroll
+            for (int nt = 0; nt < 8; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int row = 8 * nt + 2 * qd + (e & 1), c = vc + (e >> 1) * 8;
+                    if (row < n && c < a.dv) static_cast<float*>(a.dv_out)[(r0 + row) * a.dv_ld + h * a.dv + c] = x[nt][e];
+                }
+        }
+    }
+    if (a.dh0 != nullptr && 16 * w < cols) {
+        float* const d = a.dh0 + (static_cast<int64_t>(p) * a.Hv + h) * a.dk * a.dv;
+#pragma unroll
+        for (int t = 0; t < 2 * KT; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int i = 8 * t + 2 * qd + (e & 1), c = vc + (e >> 1) * 8;
+                if (i < a.dk && c < a.dv) d[static_cast<int64_t>(i) * a.dv + c] = S[t][e];
+            }
+    }
+    if (lane == 0) bulk_wait();
+}
+
+// ---- all blocks at once ---------------------------------------------------------------------------------------------
+// 16 warps: warp w has rows 16 (w % 4) .. of everything, and of each product's columns the (w / 4)-th part: 8 of a slice's value
+// columns, 16 of the 64 columns of M and N, a quarter of dk. A block walks the value columns in slices of SL, the next one's
+// states and rows on their way.
+template <int XT, int DKP>
+struct Grad {
+    static constexpr int NS = XT == 1 ? 2 : 3, NG = XT == 1 ? 1 : 3;   // NG: terms of what only rows' gradients take
+    static constexpr int SL = XT == 1 ? 32 : 16, stages = XT == 1 ? 2 : 1;
+    static constexpr int kTile = kC * DKP * 2, kPlane = kC * kC * 2, kVal = kC * SL * 2;
+    static constexpr int kState = SL / 16 * NS * 16 * DKP * 2, kDu = SL / 16 * NS * kC * 32;
+    // within a stage
+    static constexpr int S = 0, dS = kState, dU = 2 * kState, V = dU + kDu, Y = V + XT * kVal, stage = Y + XT * kVal;
+    // the whole
+    static constexpr int K = 0, Q = XT * kTile, T = 2 * XT * kTile, R = T + NS * kPlane, U = R + NS * kVal, slices = U + NS * kVal,
+                         end = slices + stages * stage;
+    // over T, R, U and the slices when they are done: N o D and - M o D, the sums of dg, and the rows' gradients
+    static constexpr int ND = T, XD = ND + NG * kPlane, Z = XD + NG * kPlane, last = Z + kC * 65 * 4;
+    static constexpr int bytes = end > last ? end : last;
+    static_assert(ND + 2 * kTile <= bytes, "the rows' gradients leave through the place of the products");
+    static constexpr int threads = 512;
+};
+
+template <int XT, int DKP, typename X>
+__global__ void __launch_bounds__(512) gdr_grad_kernel(const __grid_constant__ Args a) {
+    using W = Grad<XT, DKP>;
+    constexpr int NS = W::NS, NG = W::NG, SL = W::SL, KT = DKP / 16, DN = DKP / 64;   // DN: tiles of 16 columns of dk of a warp
+    extern __shared__ __align__(1024) unsigned char smem[];
+    __shared__ __align__(16) float vec[kVecs * kC];
+    __shared__ float sums[3][4][kC];   // a, e, W.U by quarters
+    __shared__ float inner[16];
+    start_dependent();
+    const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, g = lane >> 2, qd = lane & 3, mi = w & 3, qf = w >> 2;
+    const int64_t id = blockIdx.x / a.Hv;
+    const int h = blockIdx.x - static_cast<int>(id) * a.Hv, kh = h / (a.Hv / a.Hk);
+    int64_t b;
+    int n;
+    block_rows(a, id, b, n);
+    if (n <= 0) return;
+    const uint32_t base = smem_of(smem);
+    const int groups = (a.dv + 15) / 16, nslices = (a.dv + SL - 1) / SL;
+    const int64_t unit = id * a.Hv + h;
+
+    auto load = [&](int s) {
+        const uint32_t st = base + W::slices + (W::stages == 2 ? (s & 1) * W::stage : 0);
+        const int c0 = s * SL, cols = min(SL, a.dv - c0);
+        const int have = min(SL / 16, groups - c0 / 16);   // groups of 16 value columns that there are; the others are zeros
+        const __nv_bfloat16* const sp = a.states + (unit * groups + c0 / 16) * (NS * 16 * DKP);
+        const __nv_bfloat16* const dp = a.dstates + (unit * groups + c0 / 16) * (NS * 16 * DKP);
+        const __nv_bfloat16* const up = a.du + (unit * groups + c0 / 16) * (NS * kC * 16);
+        for (int i = tid; i < W::kState / 16; i += W::threads) {
+            const bool there = i < have * NS * 16 * DKP / 8;
+            copy16(st + W::S + i * 16, there ? sp + i * 8 : sp, there);
+            copy16(st + W::dS + i * 16, there ? dp + i * 8 : dp, there);
+        }
+        for (int i = tid; i < W::kDu / 16; i += W::threads) {
+            const bool there = i < have * NS * kC * 2;
+            copy16(st + W::dU + i * 16, there ? up + i * 8 : up, there);
+        }
+        load_rows<SL, W::threads>(st + W::V, a.v, XT, b, n, h * a.dv + c0, cols, tid);
+        load_rows<SL, W::threads>(st + W::Y, a.dy, XT, b, n, h * a.dv + c0, cols, tid);
+        copies_commit();
+    };
+    load_rows<DKP, W::threads>(base + W::K, a.k, XT, b, n, kh * a.dk, a.dk, tid);
+    load_rows<DKP, W::threads>(base + W::Q, a.q, XT, b, n, kh * a.dk, a.dk, tid);
+#pragma unroll
+    for (int pl = 0; pl < NS; ++pl)
+        load_tri<W::threads>(base + W::T + pl * W::kPlane, a.tri + (unit * a.tri_planes + pl) * int64_t(kC * kC), tid);
+    load(0);
+    for (int i = tid; i < kVecs * kC; i += W::threads) vec[i] = a.vec[unit * kVecs * kC + i];
+
+    const Lane L(lane);
+    const int row[2] = {16 * mi + g, 16 * mi + g + 8};   // of a lane's accumulators
+    float dq[2 * DN][4] = {}, k2[2 * DN][4] = {}, k3[2 * DN][4] = {}, m[2][4] = {}, nn[2][4] = {};
+    float a2[2] = {}, wu[2] = {}, ss = 0.f;
+    for (int s = 0; s < nslices; ++s) {
+        if (W::stages == 1 && s > 0) {
+            __syncthreads();
+            load(s);
+        }
+        copies_wait<0>();
+        __syncthreads();
+        if (W::stages == 2 && s + 1 < nslices) load(s + 1);
+        const int so = W::slices + (W::stages == 2 ? (s & 1) * W::stage : 0);
+        const uint32_t st = base + so;
+        float du[4] = {};   // W at this lane's places of the slice
+        if (qf < SL / 8) {   // K S, then beta R = beta (V - e^gam K S)
+            const uint32_t Sg = st + W::S + (qf >> 1) * (NS * 16 * DKP * 2);
+            float ks[4] = {};
+#pragma unroll
+            for (int kq = 0; kq < KT / 2; ++kq) {
+                uint32_t ka[XT][2][4];
+#pragma unroll
+                for (int t = 0; t < XT; ++t)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        ldsm4(ka[t][e], base + W::K + t * W::kTile + tile_at<DKP>(16 * mi + L.rA, 4 * kq + 2 * e + L.uA));
+#pragma unroll
+                for (int t = 0; t < NS; ++t) {
+                    uint32_t f[4];
+                    ldsm4(f, Sg + t * (16 * DKP * 2) + tile_at<DKP>(8 * (qf & 1) + (lane & 7), 4 * kq + (lane >> 3)));
+#pragma unroll
+                    for (int i = 0; i < XT; ++i) {
+                        if (i + t >= NS) continue;
+                        mma(ks, ka[i][0], f[0], f[1]);
+                        mma(ks, ka[i][1], f[2], f[3]);
+                    }
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int r = row[e];
+                float v[2] = {};
+#pragma unroll
+                for (int t = XT - 1; t >= 0; --t) {
+                    const uint32_t x = *reinterpret_cast<const uint32_t*>(smem + so + W::V + t * W::kVal + tile_at<SL>(r, qf) + qd * 4);
+                    v[0] += __uint_as_float(x << 16);
+                    v[1] += __uint_as_float(x & 0xFFFF0000u);
+                }
+#pragma unroll
+                for (int t = NS - 1; t >= 0; --t) {
+                    const uint32_t x = *reinterpret_cast<const uint32_t*>(smem + so + W::dU + (qf >> 1) * (NS * kC * 32) + t * (kC * 32) +
+                                                                           tile_at<16>(r, qf & 1) + qd * 4);
+                    du[2 * e] += __uint_as_float(x << 16);
+                    du[2 * e + 1] += __uint_as_float(x & 0xFFFF0000u);
+                }
+                a2[e] = fmaf(du[2 * e], ks[2 * e], a2[e]);
+                a2[e] = fmaf(du[2 * e + 1], ks[2 * e + 1], a2[e]);
+                const float bt = strength(vec[kC + r]);
+                uint32_t o[NS];
+                split2<NS>(bt * fmaf(-vec[r], ks[2 * e], v[0]), bt * fmaf(-vec[r], ks[2 * e + 1], v[1]), o);
+#pragma unroll
+                for (int t = 0; t < NS; ++t) st_word(base + W::R + t * W::kVal + tile_at<SL>(r, qf) + qd * 4, o[t]);
+            }
+        }
+        __syncthreads();
+        if (qf < SL / 8) {   // U = T (beta R)
+            float u[4] = {};
+#pragma unroll
+            for (int kq = 0; kq < 2; ++kq) {
+                if (kq > (mi >> 1)) continue;
+                uint32_t f[NS][4];
+#pragma unroll
+                for (int t = 0; t < NS; ++t) ldsm4t(f[t], base + W::R + t * W::kVal + tile_at<SL>(32 * kq + lane, qf));
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    if (2 * kq + e > mi) continue;
+#pragma unroll
+                    for (int t = 0; t < NS; ++t) {
+                        uint32_t ta[4];
+                        ldsm4(ta, base + W::T + t * W::kPlane + tile_at<kC>(16 * mi + L.rA, 4 * kq + 2 * e + L.uA));
+#pragma unroll
+                        for (int i = 0; i < NS - t; ++i) mma(u, ta, f[i][2 * e], f[i][2 * e + 1]);
+                    }
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                wu[e] = fmaf(u[2 * e], du[2 * e], wu[e]);
+                wu[e] = fmaf(u[2 * e + 1], du[2 * e + 1], wu[e]);
+                uint32_t o[NS];
+                split2<NS>(u[2 * e], u[2 * e + 1], o);
+#pragma unroll
+                for (int t = 0; t < NS; ++t) st_word(base + W::U + t * W::kVal + tile_at<SL>(row[e], qf) + qd * 4, o[t]);
+            }
+        }
+        // <dS', S>, both in the same tiles
+        for (int i = tid; i < SL / 16 * 16 * DKP / 8; i += W::threads) {
+            const int gr = i / (16 * DKP / 8), o = gr * (NS * 16 * DKP * 2) + (i - gr * (16 * DKP / 8)) * 16;
+            float x[8] = {}, y[8] = {};
+#pragma unroll
+            for (int t = NS - 1; t >= 0; --t) {
+                const uint4 p = *reinterpret_cast<const uint4*>(smem + so + W::S + o + t * (16 * DKP * 2));
+                const uint4 q = *reinterpret_cast<const uint4*>(smem + so + W::dS + o + t * (16 * DKP * 2));
+                const uint32_t pw[4] = {p.x, p.y, p.z, p.w}, qw[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    x[2 * e] += __uint_as_float(pw[e] << 16);
+                    x[2 * e + 1] += __uint_as_float(pw[e] & 0xFFFF0000u);
+                    y[2 * e] += __uint_as_float(qw[e] << 16);
+                    y[2 * e + 1] += __uint_as_float(qw[e] & 0xFFFF0000u);
+                }
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) ss = fmaf(x[e], y[e], ss);
+        }
+        __syncthreads();
+#pragma unroll
+        for (int kt = 0; kt < SL / 16; ++kt) {
+            const uint32_t Sg = st + W::S + kt * (NS * 16 * DKP * 2), Dg = st + W::dS + kt * (NS * 16 * DKP * 2);
+            uint32_t wa[NS][4], ya[XT][4], ua[NS][4];
+#pragma unroll
+            for (int t = 0; t < NS; ++t) {
+                ldsm4(wa[t], st + W::dU + kt * (NS * kC * 32) + t * (kC * 32) + tile_at<16>(16 * mi + L.rA, L.uA));
+                ldsm4(ua[t], base + W::U + t * W::kVal + tile_at<SL>(16 * mi + L.rA, 2 * kt + L.uA));
+            }
+#pragma unroll
+            for (int t = 0; t < XT; ++t) ldsm4(ya[t], st + W::Y + t * W::kVal + tile_at<SL>(16 * mi + L.rA, 2 * kt + L.uA));
+            if (qf <= mi) {   // W U^T and dY U^T
+                auto at = [&](int) { return base + W::U + tile_at<SL>(16 * qf + L.rB, 2 * kt + L.uB); };
+                products<NS, NS, NS, false, 1>(m, wa, W::kVal, at);
+                products<XT, NS, NS, false, 1>(nn, ya, W::kVal, at);
+            }
+            // dY S^T, W S^T, U dS'^T
+            auto sa = [&](int np) { return Sg + tile_at<DKP>(L.rBt, 2 * (DN * qf + np) + L.uBt); };
+            auto da = [&](int np) { return Dg + tile_at<DKP>(L.rBt, 2 * (DN * qf + np) + L.uBt); };
+            products<XT, NS, NS, true, DN>(dq, ya, 16 * DKP * 2, sa);
+            products<NS, NS, NG, true, DN>(k2, wa, 16 * DKP * 2, sa);
+            products<NS, NS, NS, true, DN>(k3, ua, 16 * DKP * 2, da);
+        }
+    }
+    // A and G once more, in float32
+    float kk[2][4] = {}, qk[2][4] = {};
+    if (qf <= mi) {
+#pragma unroll
+        for (int kt = 0; kt < KT; ++kt) {
+            uint32_t ka[XT][4], qa[XT][4];
+#pragma unroll
+            for (int t = 0; t < XT; ++t) {
+                ldsm4(ka[t], base + W::K + t * W::kTile + tile_at<DKP>(16 * mi + L.rA, 2 * kt + L.uA));
+                ldsm4(qa[t], base + W::Q + t * W::kTile + tile_at<DKP>(16 * mi + L.rA, 2 * kt + L.uA));
+            }
+            auto at = [&](int) { return base + W::K + tile_at<DKP>(16 * qf + L.rB, 2 * kt + L.uB); };
+            products<XT, XT, XT, false, 1>(kk, ka, W::kTile, at);
+            products<XT, XT, XT, false, 1>(qk, qa, W::kTile, at);
+        }
+    }
+    __syncthreads();   // every slice is done: their place is free
+    float* const Z = reinterpret_cast<float*>(smem + W::Z);
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int i = row[e], j = 16 * qf + 8 * t + 2 * qd;
+            float x[2], y[2];
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                float d = 0.f;
+                if (j + c <= i) d = expf((vec[3 * kC + i] - vec[3 * kC + j + c]) + (vec[4 * kC + i] - vec[4 * kC + j + c]));
+                const float N = a.scale * nn[t][2 * e + c], M = vec[kC + i] * m[t][2 * e + c];
+                x[c] = j + c <= i ? d * N : 0.f;
+                y[c] = j + c < i ? -d * M : 0.f;
+                Z[i * 65 + j + c] = j + c < i ? fmaf(x[c], qk[t][2 * e + c], y[c] * kk[t][2 * e + c]) : 0.f;
+            }
+            uint32_t o[NG];
+            split2<NG>(x[0], x[1], o);
+#pragma unroll
+            for (int p = 0; p < NG; ++p) st_word(base + W::ND + p * W::kPlane + tile_at<kC>(i, j >> 3) + qd * 4, o[p]);
+            split2<NG>(y[0], y[1], o);
+#pragma unroll
+            for (int p = 0; p < NG; ++p) st_word(base + W::XD + p * W::kPlane + tile_at<kC>(i, j >> 3) + qd * 4, o[p]);
+        }
+    // the rows' scalars: a = e^gam (scale q . (S dY) - beta W . (S^T k)), e = e^(gam_last - gam) k . (dS' u), W . U
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+        const int r = row[e];
+        float qd1 = 0.f, kd3 = 0.f;
+#pragma unroll
+        for (int t = 0; t < 2 * DN; ++t) {
+            const uint32_t at = tile_at<DKP>(r, 2 * DN * qf + t) + qd * 4;
+            float q[2] = {}, k[2] = {};
+#pragma unroll
+            for (int p = XT - 1; p >= 0; --p) {
+                const uint32_t x = *reinterpret_cast<const uint32_t*>(smem + W::Q + p * W::kTile + at);
+                const uint32_t y = *reinterpret_cast<const uint32_t*>(smem + W::K + p * W::kTile + at);
+                q[0] += __uint_as_float(x << 16);
+                q[1] += __uint_as_float(x & 0xFFFF0000u);
+                k[0] += __uint_as_float(y << 16);
+                k[1] += __uint_as_float(y & 0xFFFF0000u);
+            }
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                qd1 = fmaf(q[c], dq[t][2 * e + c], qd1);
+                kd3 = fmaf(k[c], k3[t][2 * e + c], kd3);
+            }
+        }
+        const float eg = vec[r], be = vec[kC + r], c = vec[2 * kC + r];
+        float x[3] = {eg * (a.scale * qd1 - be * a2[e]), c * kd3, wu[e]};
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+            x[i] += __shfl_xor_sync(kFull, x[i], 1);
+            x[i] += __shfl_xor_sync(kFull, x[i], 2);
+            if (qd == 0) sums[i][qf][r] = x[i];
+        }
+        // the rows' gradients so far
+#pragma unroll
+        for (int t = 0; t < 2 * DN; ++t)
+#pragma unroll
+            for (int p = 0; p < 2; ++p) {
+                dq[t][2 * e + p] *= a.scale * eg;
+                k3[t][2 * e + p] = fmaf(-eg * be, k2[t][2 * e + p], c * k3[t][2 * e + p]);
+            }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o /= 2) ss += __shfl_xor_sync(kFull, ss, o);
+    if (lane == 0) inner[w] = ss;
+    __syncthreads();
+    // dQ += (N o D) K; dK += (N o D)^T Q - (M o D) K - (M o D)^T K
+#pragma unroll
+    for (int kt = 0; kt < 4; ++kt) {
+        auto ka = [&](int np) { return base + W::K + tile_at<DKP>(16 * kt + L.rBt, 2 * (DN * qf + np) + L.uBt); };
+        auto qa = [&](int np) { return base + W::Q + tile_at<DKP>(16 * kt + L.rBt, 2 * (DN * qf + np) + L.uBt); };
+        uint32_t f[NG][4];
+        if (kt <= mi) {
+#pragma unroll
+            for (int p = 0; p < NG; ++p) ldsm4(f[p], base + W::ND + p * W::kPlane + tile_at<kC>(16 * mi + L.rA, 2 * kt + L.uA));
+            products<NG, XT, NG, true, DN>(dq, f, W::kTile, ka);
+#pragma unroll
+            for (int p = 0; p < NG; ++p) ldsm4(f[p], base + W::XD + p * W::kPlane + tile_at<kC>(16 * mi + L.rA, 2 * kt + L.uA));
+            products<NG, XT, NG, true, DN>(k3, f, W::kTile, ka);
+        }
+        if (kt >= mi) {
+#pragma unroll
+            for (int p = 0; p < NG; ++p) ldsm4t(f[p], base + W::XD + p * W::kPlane + tile_at<kC>(16 * kt + L.rAt, 2 * mi + L.uAt));
+            products<NG, XT, NG, true, DN>(k3, f, W::kTile, ka);
+#pragma unroll
+            for (int p = 0; p < NG; ++p) ldsm4t(f[p], base + W::ND + p * W::kPlane + tile_at<kC>(16 * kt + L.rAt, 2 * mi + L.uAt));
+            products<NG, XT, NG, true, DN>(k3, f, W::kTile, qa);
+        }
+    }
+    // dg. Column by column sums from the bottom (8 rows a thread, then what lies below them), then row by row up to the diagonal.
+    {
+        const int j = tid & 63, s8 = tid >> 6;
+        float run = 0.f;
+#pragma unroll
+        for (int i = 7; i >= 0; --i) {
+            run += Z[(8 * s8 + i) * 65 + j];
+            Z[(8 * s8 + i) * 65 + j] = run;
+        }
+        __syncthreads();
+        float below = 0.f;
+        for (int q = 7; q > s8; --q) below += Z[8 * q * 65 + j];
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) Z[(8 * s8 + i) * 65 + j] += below;
+        __syncthreads();
+        const int t = tid >> 3, part = tid & 7;
+        float x = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int c = 8 * part + i;   // a column before row t, its end's share, and a row from t on
+            if (c < t) {
+                x += Z[t * 65 + c];
+                x += sums[1][0][c] + sums[1][1][c] + sums[1][2][c] + sums[1][3][c];
+            } else {
+                x += sums[0][0][c] + sums[0][1][c] + sums[0][2][c] + sums[0][3][c];
+            }
+        }
+#pragma unroll
+        for (int o = 4; o > 0; o /= 2) x += __shfl_xor_sync(kFull, x, o);
+        if (part == 0 && t < n) {
+            float s = 0.f;
+#pragma unroll
+            for (int i = 0; i < 16; ++i) s += inner[i];
+            x = fmaf(vec[kC - 1], s, x);
+            const float db = (sums[2][0][t] + sums[2][1][t] + sums[2][2][t] + sums[2][3][t]) / strength(vec[kC + t]);
+            const int64_t gi = (b + t) * a.dg_ld + h, bi = (b + t) * a.db_ld + h;
+            if (a.g_bf16) {
+                static_cast<__nv_bfloat16*>(a.dg)[gi] = __float2bfloat16_rn(x);
+                static_cast<__nv_bfloat16*>(a.dbeta)[bi] = __float2bfloat16_rn(db);
+            } else {
+                static_cast<float*>(a.dg)[gi] = x;
+                static_cast<float*>(a.dbeta)[bi] = db;
+            }
+        }
+    }
+    // the rows' gradients: of a head's own queries and keys, or a value head's share of them in float32
+    if (a.part == nullptr && sizeof(X) == 2) {
+        __syncthreads();   // the sums of dg have been read
+#pragma unroll
+        for (int np = 0; np < DN; ++np) {
+            uint32_t f[4], k[4];
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                f[2 * t] = round2(dq[2 * np + t][0], dq[2 * np + t][1]);
+                f[2 * t + 1] = round2(dq[2 * np + t][2], dq[2 * np + t][3]);
+                k[2 * t] = round2(k3[2 * np + t][0], k3[2 * np + t][1]);
+                k[2 * t + 1] = round2(k3[2 * np + t][2], k3[2 * np + t][3]);
+            }
+            const uint32_t at = tile_at<DKP>(16 * mi + L.rA, 2 * (DN * qf + np) + L.uA);
+            stsm4(base + W::ND + at, f);
+            stsm4(base + W::ND + W::kTile + at, k);
+        }
+        __syncthreads();
+        for (int i = tid; i < kC * (DKP / 8); i += W::threads) {
+            const int r = i / (DKP / 8), u = i % (DKP / 8);
+            if (r >= n || u * 8 >= a.dk) continue;
+            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.dq) + (b + r) * a.dq_ld + kh * a.dk + u * 8) =
+                *reinterpret_cast<const uint4*>(smem + W::ND + tile_at<DKP>(r, u));
+            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.dk_out) + (b + r) * a.dk_ld + kh * a.dk + u * 8) =
+                *reinterpret_cast<const uint4*>(smem + W::ND + W::kTile + tile_at<DKP>(r, u));
+        }
+        return;
+    }
+    const int64_t HD = static_cast<int64_t>(a.Hv) * a.dk;
+#pragma unroll
+    for (int t = 0; t < 2 * DN; ++t)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int r = row[e], c = 16 * DN * qf + 8 * t + 2 * qd;
+            if (r >= n || c >= a.dk) continue;
+            float* const q = a.part != nullptr ? a.part + (b + r) * HD + h * a.dk + c : static_cast<float*>(a.dq) + (b + r) * a.dq_ld + kh * a.dk + c;
+            float* const k = a.part != nullptr ? a.part + (a.rows + b + r) * HD + h * a.dk + c
+                                               : static_cast<float*>(a.dk_out) + (b + r) * a.dk_ld + kh * a.dk + c;
+            *reinterpret_cast<float2*>(q) = make_float2(dq[t][2 * e], dq[t][2 * e + 1]);
+            *reinterpret_cast<float2*>(k) = make_float2(k3[t][2 * e], k3[t][2 * e + 1]);
+        }
+}
+
+// The gradients of queries and keys that several value heads share: their heads' shares in order, 4 columns a thread. Rows
+// of no sequence stay as they are.
+template <typename X>
+__global__ void __launch_bounds__(256) gdr_join_kernel(const __grid_constant__ Args a) {
+    start_dependent();
+    const int R = a.Hv / a.Hk, units = a.Hk * a.dk / 4;
+    const int64_t first = a.offsets == nullptr ? 0 : min(max(a.offsets[0], int64_t(0)), a.rows);
+    const int64_t last = a.offsets == nullptr ? a.rows : max(min(a.offsets[a.P], a.rows), first);
+    const int64_t count = (last - first) * units * 2;
+    for (int64_t i = blockIdx.x * int64_t(256) + threadIdx.x; i < count; i += gridDim.x * int64_t(256)) {
+        const bool k = i >= (last - first) * units;
+        const int64_t at = k ? i - (last - first) * units : i, r = first + at / units;
+        const int c = static_cast<int>(at % units) * 4, kh = c / a.dk, d = c - kh * a.dk;
+        const float* src = a.part + ((k ? a.rows : 0) + r) * a.Hv * a.dk + static_cast<int64_t>(kh) * R * a.dk + d;
+        float s[4] = {};
+        for (int q = 0; q < R; ++q) {
+            float x[4];
+            load4(src + static_cast<int64_t>(q) * a.dk).get(x);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[e] += x[e];
+        }
+        st4(static_cast<X*>(k ? a.dk_out : a.dq) + r * (k ? a.dk_ld : a.dq_ld) + c, s);
+    }
+}
+
+// ---- host side ------------------------------------------------------------------------------------------------------
+template <typename K>
+cudaError_t big_smem(K kernel, int bytes) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+}
+
+template <int XT, int DKP, int BV>
+cudaError_t back(const Args& a, cudaStream_t cs) {
+    using X = std::conditional_t<XT == 1, __nv_bfloat16, float>;
+    using W = Back<XT, DKP, BV>;
+    auto* const k = gdr_back_kernel<XT, DKP, BV, X>;
+    const cudaError_t e = big_smem(k, W::bytes);
+    if (e != cudaSuccess) return e;
+    const int64_t grid = static_cast<int64_t>(a.P) * a.Hv * ((a.dv + BV - 1) / BV);
+    return launch_dependent(k, dim3(static_cast<unsigned>(grid)), dim3(W::threads), W::bytes, cs, a);
+}
+
+template <int XT, int DKP>
+cudaError_t grad(const Args& a, int64_t blocks, cudaStream_t cs) {
+    using X = std::conditional_t<XT == 1, __nv_bfloat16, float>;
+    using W = Grad<XT, DKP>;
+    auto* const k = gdr_grad_kernel<XT, DKP, X>;
+    const cudaError_t e = big_smem(k, W::bytes);
+    if (e != cudaSuccess) return e;
+    return launch_dependent(k, dim3(static_cast<unsigned>(blocks * a.Hv)), dim3(W::threads), W::bytes, cs, a);
+}
+
+template <int DKP>
+cudaError_t back_bf16(const Args& a, cudaStream_t cs) {
+    switch (columns(a)) {
+        case 32: return back<1, DKP, 32>(a, cs);
+        case 64: return back<1, DKP, 64>(a, cs);
+        default: return back<1, DKP, 128>(a, cs);
+    }
+}
+
+}  // namespace
+}  // namespace gdr
+}  // namespace sdm
+
+using namespace sdm;
+using namespace sdm::gdr;
+
+extern "C" sdm_status sdm_gdr_backward(const sdm_gdr_shape* shape, const void* q, int64_t q_ld, const void* k, int64_t k_ld,
+                                       const void* v, int64_t v_ld, const void* g, int64_t g_ld, const void* beta,
+                                       int64_t beta_ld, const void* dy, int64_t dy_ld, const int64_t* offsets,
+                                       const void* states, const float* dhT, void* dq, int64_t dq_ld, void* dk, int64_t dk_ld,
+                                       void* dv, int64_t dv_ld, void* dg, int64_t dg_ld, void* dbeta, int64_t dbeta_ld,
+                                       float* dh0, void* ws, size_t ws_bytes, uint32_t* status, sdm_stream_t stream) {
+    Args a;
+    sdm_status st = check_inputs(shape, q, q_ld, k, k_ld, v, v_ld, g, g_ld, beta, beta_ld, offsets, ws, ws_bytes, true, status, &a);
+    if (st != SDM_OK) return st;
+    const int xe = shape->x_dtype == SDM_BF16 ? 2 : 4, ge = shape->g_dtype == SDM_BF16 ? 2 : 4;
+    const int64_t kn = static_cast<int64_t>(shape->k_heads) * shape->dk, vn = static_cast<int64_t>(shape->v_heads) * shape->dv;
+    if (shape->rows > 0) {
+        if ((st = check_array(dy, dy_ld, vn, xe, 16, false)) != SDM_OK) return st;
+        if ((st = check_array(dq, dq_ld, kn, xe, 16, true)) != SDM_OK) return st;
+        if ((st = check_array(dk, dk_ld, kn, xe, 16, true)) != SDM_OK) return st;
+        if ((st = check_array(dv, dv_ld, vn, xe, 16, true)) != SDM_OK) return st;
+        if ((st = check_array(dg, dg_ld, shape->v_heads, ge, ge, true)) != SDM_OK) return st;
+        if ((st = check_array(dbeta, dbeta_ld, shape->v_heads, ge, ge, true)) != SDM_OK) return st;
+        if (states == nullptr) return SDM_ERR_ARG;
+    }
+    if (!checks::aligned_all(16, {states, dhT, dh0})) return SDM_ERR_ALIGN;
+    a.dq = dq; a.dq_ld = dq_ld; a.dk_out = dk; a.dk_ld = dk_ld; a.dv_out = dv; a.dv_ld = dv_ld;
+    a.dg = dg; a.dg_ld = dg_ld; a.dbeta = dbeta; a.db_ld = dbeta_ld; a.dhT = dhT; a.dh0 = dh0;
+    a.states = static_cast<__nv_bfloat16*>(const_cast<void*>(states));
+    const Layout l = layout(shape, true);
+    unsigned char* const w = static_cast<unsigned char*>(ws);
+    a.dstates = reinterpret_cast<__nv_bfloat16*>(w + l.dstates);
+    a.du = reinterpret_cast<__nv_bfloat16*>(w + l.du);
+    a.part = shape->v_heads == shape->k_heads ? nullptr : reinterpret_cast<float*>(w + l.part);
+    a.tri_planes = 2 * terms(shape);
+    const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+    cudaError_t e = cudaSuccess;
+    if (shape->rows > 0) {
+        e = launch_planes(shape, q, q_ld, k, k_ld, v, v_ld, ws, true, &a, cs);
+        if (shape->x_dtype == SDM_BF16) {
+            a.dy = {static_cast<const __nv_bfloat16*>(dy), dy_ld, 0};
+        } else {
+            __nv_bfloat16* const to = reinterpret_cast<__nv_bfloat16*>(w + l.dy);
+            a.dy = {to, vn, shape->rows * vn};
+            if (e == cudaSuccess) e = launch_split(dy, dy_ld, shape->rows, static_cast<int>(vn), to, cs);
+        }
+        if (e == cudaSuccess) e = launch_prepare(a, shape, cs);
+    }
+    const bool narrow = padded(shape->dk) == 64, bf16 = shape->x_dtype == SDM_BF16;
+    if (e == cudaSuccess)
+        e = bf16 ? (narrow ? back_bf16<64>(a, cs) : back_bf16<128>(a, cs)) : (narrow ? back<3, 64, 32>(a, cs) : back<3, 128, 32>(a, cs));
+    const int64_t blocks = blocks_of(shape);
+    if (e == cudaSuccess && shape->rows > 0)
+        e = bf16 ? (narrow ? grad<1, 64>(a, blocks, cs) : grad<1, 128>(a, blocks, cs))
+                 : (narrow ? grad<3, 64>(a, blocks, cs) : grad<3, 128>(a, blocks, cs));
+    if (e == cudaSuccess && shape->rows > 0 && a.part != nullptr) {
+        const int64_t grid = std::min<int64_t>((shape->rows * (kn / 4) * 2 + 255) / 256, 152 * 16);
+        e = launch_dependent(bf16 ? gdr_join_kernel<__nv_bfloat16> : gdr_join_kernel<float>, dim3(static_cast<unsigned>(grid)), dim3(256), 0,
+                             cs, a);
+    }
+    return e == cudaSuccess ? SDM_OK : SDM_ERR_CUDA;
+}

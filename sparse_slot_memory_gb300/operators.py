@@ -1,6 +1,8 @@
 """Python face of the operators around the memory layer (include/sdm.h): argument marshalling only.
 
 * ``glr_*``: the gated linear recurrence h_t = exp(g_t) h_{t-1} + x_t, its backward, and one token per request;
+* ``gdr_*``: the gated delta rule, a state of dk slots a head that every token decays, corrects and reads, its backward, and one
+  token per request;
 * ``qk_norm_rope*``: the norm of every query and key head with the position rotation in the same pass;
 * ``token_logprobs*``: log probabilities of given tokens, entropy, top alternatives, and the logits' gradient.
 
@@ -198,6 +200,119 @@ def glr_step(spec: GlrSpec, x, g, state, y, slots=None, status=None, stream=None
         spec.c(), *_rows(x, xt, xs, D, "x"), *_rows(g, gt, gs, gs[1], "g"), _small(slots, _I32, xs[0], "slots"),
         *_rows(state, _F32, (n, D), D, "state", True), n, *_rows(y, xt, xs, D, "y", True), _status(status), _stream(stream))
     _check(st, "sdm_glr_step")
+
+
+# ---- the gated delta rule ------------------------------------------------------------------------------
+@dataclasses.dataclass(frozen=True)
+class GdrSpec(_Spec):
+    """P sequences of together ``rows`` rows; ``k_heads`` heads of queries and keys of ``dk`` channels, ``v_heads`` (a multiple) heads
+    of values of ``dv`` channels, each with its decay, write strength and state [dk, dv]. dk and dv: multiples of 8, up to 128."""
+
+    P: int
+    rows: int
+    k_heads: int
+    v_heads: int
+    dk: int
+    dv: int
+    x_dtype: str = "bf16"
+    g_dtype: str = "f32"
+    scale: float = 1.0
+
+    def _struct(self):
+        return _abi.GdrShape(self.P, self.k_heads, self.v_heads, self.dk, self.dv, _DT[self.x_dtype], _DT[self.g_dtype],
+                             self.scale, self.rows)
+
+
+def alloc_gdr_states(spec: GdrSpec, device="cuda") -> torch.Tensor:
+    """What the forward saves for the backward: the state before every 64th row, in the kernels' own form (bytes)."""
+    return torch.empty(_bytes(spec, "sdm_gdr_states_bytes"), dtype=torch.uint8, device=device)
+
+
+def _gdr_bytes(spec: GdrSpec, backward: bool) -> int:
+    name = "_ws_backward" if backward else "_ws_forward"
+    n = spec.__dict__.get(name)
+    if n is None:
+        n = spec._keep(name, int(_abi.load().sdm_gdr_workspace_bytes(spec.c(), int(backward))))
+        if n == 0:
+            raise ValueError(f"invalid shape {spec}")
+    return n
+
+
+def alloc_gdr_workspace(spec: GdrSpec, backward: bool = True, device="cuda") -> torch.Tensor:
+    """The workspace of ``gdr_forward`` and, with ``backward``, of ``gdr_backward`` (one for both; it holds nothing between calls)."""
+    return torch.empty(_gdr_bytes(spec, backward), dtype=torch.uint8, device=device)
+
+
+def _gdr_kinds(spec: GdrSpec):
+    """The tensors' types and shapes: x's, g's, queries and keys, values, gates, numbers in a row of each, of a state, and of
+    all states."""
+    k = spec.__dict__.get("_kinds")
+    if k is None:
+        n, Hk, Hv, dk, dv = spec.rows, spec.k_heads, spec.v_heads, spec.dk, spec.dv
+        k = spec._keep("_kinds", (_TORCH_DT[spec.x_dtype], _TORCH_DT[spec.g_dtype], (n, Hk, dk), (n, Hv, dv), (n, Hv), Hk * dk,
+                                  Hv * dv, Hv, Hv * dk * dv, spec.P * Hv * dk * dv))
+    return k
+
+
+def _gdr_inputs(kinds, q, k, v, g, beta):
+    xt, gt, ks, vs, gs, kn, vn, H = kinds[:8]
+    return (*_rows(q, xt, ks, kn, "q"), *_rows(k, xt, ks, kn, "k"), *_rows(v, xt, vs, vn, "v"), *_rows(g, gt, gs, H, "g"),
+            *_rows(beta, gt, gs, H, "beta"))
+
+
+def _gdr_states(spec: GdrSpec, states):
+    return _small(states, torch.uint8, _bytes(spec, "sdm_gdr_states_bytes") if states is not None else 0, "states")
+
+
+def _workspace(ws):
+    return _small(ws, torch.uint8, 0, "ws"), 0 if ws is None else ws.numel()
+
+
+def gdr_forward(spec: GdrSpec, q, k, v, g, beta, y, ws, offsets=None, h0=None, hT=None, states=None, status=None, stream=None):
+    """sdm_gdr_forward: per sequence and value head S_t = exp(g_t) S_{t-1} + k_t u_t^T with u_t = beta_t (v_t - exp(g_t) S_{t-1}^T k_t),
+    and y_t = scale S_t^T q_t. ``q``, ``k`` [rows, k_heads, dk]; ``v``, ``y`` [rows, v_heads, dv]; ``g`` (log decays, at most 0) and
+    ``beta`` [rows, v_heads]; ``ws`` from ``alloc_gdr_workspace``; ``offsets`` (optional) int64 [P + 1] as in ``glr_forward``; ``h0``,
+    ``hT`` (optional) float32 [P, v_heads, dk, dv]: the states before and after (may be one tensor); ``states`` (optional, from
+    ``alloc_gdr_states``) receives what ``gdr_backward`` needs."""
+    kinds = _gdr_kinds(spec)
+    st = _abi.load().sdm_gdr_forward(
+        spec.c(), *_gdr_inputs(kinds, q, k, v, g, beta), _small(offsets, torch.int64, spec.P + 1, "offsets"),
+        _small(h0, _F32, kinds[9], "h0"), *_rows(y, kinds[0], kinds[3], kinds[6], "y", True), _small(hT, _F32, kinds[9], "hT"),
+        _gdr_states(spec, states), *_workspace(ws), _status(status), _stream(stream))
+    _check(st, "sdm_gdr_forward")
+
+
+def gdr_backward(spec: GdrSpec, q, k, v, g, beta, dy, states, dq, dk, dv, dg, dbeta, ws, offsets=None, dhT=None, dh0=None,
+                 status=None, stream=None):
+    """sdm_gdr_backward: the gradients ``dq``, ``dk`` [rows, k_heads, dk], ``dv`` [rows, v_heads, dv], ``dg``, ``dbeta`` [rows, v_heads] and
+    ``dh0`` (optional, float32 [P, v_heads, dk, dv]) from ``dy`` and ``dhT`` (optional: the gradient of the states after). The other
+    arrays are the forward's, with the ``states`` that it saved; ``ws`` from ``alloc_gdr_workspace``."""
+    kinds = _gdr_kinds(spec)
+    xt, gt, ks, vs, gs, kn, vn, H = kinds[:8]
+    if states is None:
+        raise ValueError("states: the backward needs the states that the forward saved")
+    st = _abi.load().sdm_gdr_backward(
+        spec.c(), *_gdr_inputs(kinds, q, k, v, g, beta), *_rows(dy, xt, vs, vn, "dy"),
+        _small(offsets, torch.int64, spec.P + 1, "offsets"), _gdr_states(spec, states), _small(dhT, _F32, kinds[9], "dhT"),
+        *_rows(dq, xt, ks, kn, "dq", True), *_rows(dk, xt, ks, kn, "dk", True), *_rows(dv, xt, vs, vn, "dv", True),
+        *_rows(dg, gt, gs, H, "dg", True), *_rows(dbeta, gt, gs, H, "dbeta", True), _small(dh0, _F32, kinds[9], "dh0"),
+        *_workspace(ws), _status(status), _stream(stream))
+    _check(st, "sdm_gdr_backward")
+
+
+def gdr_step(spec: GdrSpec, q, k, v, g, beta, state, y, slots=None, status=None, stream=None):
+    """sdm_gdr_step: one token of each of ``spec.rows`` requests. ``state`` float32 [states, v_heads, dk, dv] is updated in place:
+    ``state[slots[i]]`` (int32, distinct; below 0: a padding row) for token i, or ``state[i]`` without ``slots``."""
+    kinds = _gdr_kinds(spec)
+    xt, H = kinds[0], spec.v_heads
+    if not isinstance(state, _Tensor) or state.dim() != 4:
+        raise ValueError("state: expected a float32 tensor [states, v_heads, dk, dv]")
+    n = state.shape[0]
+    st = _abi.load().sdm_gdr_step(
+        spec.c(), *_gdr_inputs(kinds, q, k, v, g, beta), _small(slots, _I32, spec.rows, "slots"),
+        *_rows(state, _F32, (n, H, spec.dk, spec.dv), kinds[8], "state", True), n, *_rows(y, xt, kinds[3], kinds[6], "y", True),
+        _status(status), _stream(stream))
+    _check(st, "sdm_gdr_step")
 
 
 # ---- norms of queries and keys with the position rotation ---------------------------------------------
