@@ -550,7 +550,7 @@ typedef struct {
  *   the backward, in a form of its own.
  *   ws: sdm_gdr_workspace_bytes(shape, 0), 16-byte aligned. It holds nothing from one call to the next.
  * Blocks of 64 rows are solved together on the tensor cores; sums are float32, and float32 values enter the products as sums of
- * two bfloat16 (within 2^-18) beside bfloat16 rows, of three (2^-25) beside float32 rows. A value that is not finite spoils its sequence and head from the start of its block on (as NaN).
+ * two bfloat16 (within 2^-17) beside bfloat16 rows, of three (2^-25) beside float32 rows. A value that is not finite spoils its sequence and head from the start of its block on (as NaN).
  */
 size_t sdm_gdr_states_bytes(const sdm_gdr_shape* shape);
 size_t sdm_gdr_workspace_bytes(const sdm_gdr_shape* shape, int32_t backward);

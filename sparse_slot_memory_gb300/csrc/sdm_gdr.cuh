@@ -7,7 +7,7 @@
 // which is the rule row by row with the rows' writes u_t = beta_t (v_t - e^g_t S_{t-1}^T k_t) solved for together.
 //
 // Numbers. The tensor cores multiply bfloat16 and add in float32. A float32 operand is a sum of bfloat16 terms, its value
-// rounded, the rest rounded, and so on: two terms hold 16 bits of mantissa and a bit (2^-18 off at most), three hold all 24.
+// rounded, the rest rounded, and so on: two terms hold 16 bits of mantissa and a bit (2^-17 off at most), three hold all 24.
 // Of two such operands' product the terms (i, j) with i + j below the number of terms are taken. bfloat16 rows are exact
 // operands of one term, and what is computed from them has two: states, writes and the solution of the triangular system
 // keep 17 bits through a product and 24 where they are added (measured: states 4e-6 off 64 bits after 4096 rows, where the rows'
@@ -33,8 +33,8 @@ constexpr int kC = SDM_GDR_CHUNK;   // rows of a block
 constexpr int kMaxD = 128;          // channels of a head at most
 constexpr int kVecs = 5;
 
-// A write strength below 2^-80 counts as 2^-80 in T and in the backward, so that the error v - e^g S^T k behind a write can
-// be had from the write: what a row of strength 0 writes is then 2^-80 of that error, which no other value feels.
+// A write strength below 2^-80 counts as 2^-80 in T, so that the error v - e^g S^T k behind a write, which the strength's gradient
+// takes, can be had from the write. A row of strength 0 then holds 2^-80 of the others' writes, which no other value feels.
 __device__ __forceinline__ float strength(float beta) { return fabsf(beta) < 0x1p-80f ? copysignf(0x1p-80f, beta) : beta; }
 
 // Rows as the tensor cores take them: planes of bfloat16 (one, or the three terms of float32 rows).

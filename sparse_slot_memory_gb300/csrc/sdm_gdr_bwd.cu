@@ -388,8 +388,9 @@ __global__ void __launch_bounds__(512) gdr_grad_kernel(const __grid_constant__ A
             for (int e = 0; e < 2; ++e) {
                 wu[e] = fmaf(u[2 * e], du[2 * e], wu[e]);
                 wu[e] = fmaf(u[2 * e + 1], du[2 * e + 1], wu[e]);
+                const float bt = vec[kC + row[e]], own = bt / strength(bt);   // 1, or nothing where nothing is written
                 uint32_t o[NS];
-                split2<NS>(u[2 * e], u[2 * e + 1], o);
+                split2<NS>(own * u[2 * e], own * u[2 * e + 1], o);
 #pragma unroll
                 for (int t = 0; t < NS; ++t) st_word(base + W::U + t * W::kVal + tile_at<SL>(row[e], qf) + qd * 4, o[t]);
             }
