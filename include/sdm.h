@@ -3,7 +3,7 @@
  * recurrence: the forward's Phase 1 and Phase-2 decay-and-write (DW), the saving forward's dense
  * snapshot, and the deterministic backward's step kernels (Phase A, GWR, GDS); and of the operators a model
  * needs around that layer (gated linear recurrence, norm and rotation of queries and keys, token log
- * probabilities; from their own section on).
+ * probabilities, gated delta rule, norms around a block, embedding; from their own section on).
  *
  * Definitions followed (sparse-delta-memory 2.0.0):
  *   phase1_cuda.py, module docstring ........ the Phase-1 outputs and the determinism contract
@@ -74,6 +74,7 @@ typedef enum { SDM_F32 = 0, SDM_BF16 = 1 } sdm_dtype;
 #define SDM_DEV_BAD_OFFSET 0x2u   /* sequence offsets not ascending within [0, rows]: cut to it */
 #define SDM_DEV_BAD_POSITION 0x4u /* a position at or above max_pos: treated as padding */
 #define SDM_DEV_BAD_TARGET 0x8u   /* a target at or above V: treated as ignored */
+#define SDM_DEV_BAD_TOKEN 0x10u   /* a token id at or above V: treated as padding */
 
 typedef struct {
     int32_t P;              /* streams */
@@ -362,7 +363,7 @@ sdm_status sdm_gds(const sdm_shape* shape, int32_t grad_dtype, const int32_t* so
 
 /* ================================================================================================
  * The operators around the memory: the gated linear recurrence, the norm and rotation of query and
- * key heads, and log probabilities of tokens. They share the conventions above (caller-owned device
+ * key heads, log probabilities of tokens, the gated delta rule, the norms around a block, and the embedding. They share the conventions above (caller-owned device
  * pointers, no allocation, no synchronization, checks before any launch, every output bitwise
  * reproducible) and differ in these:
  *   - Row arrays take the distance between rows in elements (`*_ld`), so that a slice of a wider row
@@ -581,6 +582,71 @@ sdm_status sdm_gdr_step(const sdm_gdr_shape* shape, const void* q, int64_t q_ld,
                         const void* v, int64_t v_ld, const void* g, int64_t g_ld, const void* beta, int64_t beta_ld,
                         const int32_t* slots, float* state, int64_t state_ld, int64_t states, void* y, int64_t y_ld,
                         uint32_t* status, sdm_stream_t stream);
+
+typedef struct {
+    int64_t rows;
+    int32_t D;          /* columns of a row, a multiple of 4, up to 16384 */
+    int32_t group;      /* columns that the norm behind the block takes together: a multiple of 4 that divides D (D: whole
+                         * rows); with very many narrow groups a row does not fit (SDM_ERR_SHAPE): always up to D = 2048 */
+    int32_t post;       /* 1: the block's output is normed; 0: taken as it is (w_post unused) */
+    int32_t gate;       /* of the block's output: 0 none, 1 sigmoid(z), 2 z sigmoid(z) */
+    int32_t residual;   /* 1: x is added */
+    int32_t pre;        /* 1: the sum is normed for the next block; 0: not (y, w_pre unused) */
+    int32_t dtype;      /* sdm_dtype of all rows */
+    float eps;
+    float scale;        /* of the gated output */
+} sdm_norm_shape;
+
+/*
+ * The norms behind and before a block, with its gate and the residual. Per row, in float32:
+ *   m = o rsqrt(mean o^2 + eps) w_post over each group (post 0: m = o),   n = m act(z),
+ *   r = x + scale channel_scale n, rounded,   y = r rsqrt(mean r^2 + eps) w_pre over the row, of r as it is stored.
+ * o, z, x, r, y [rows, D]; w_post float32 [group], the same for every group; w_pre, channel_scale float32 [D] (each nullable: ones). r may
+ * be x or o, and y may be o, z or x (same ld).
+ */
+sdm_status sdm_block_norm(const sdm_norm_shape* shape, const void* o, int64_t o_ld, const void* z, int64_t z_ld, const void* x,
+                          int64_t x_ld, const float* w_post, const float* w_pre, const float* channel_scale, void* r,
+                          int64_t r_ld, void* y, int64_t y_ld, sdm_stream_t stream);
+
+/*
+ * Its backward, from the forward's inputs and its r (which the norm before the next block needs; unused where pre is 0): dr is the
+ * gradient of r (nullable where pre is 1: zeros), dy that of y. d_o, dz (gate), dx (nullable: the gradient of the sum, x's and
+ * all that came before) [rows, D]; dw_post [group], dw_pre, d_channel_scale [D] float32 (nullable), written, with zeros for what the
+ * shape does not have. dx may be dr, dz may be z and d_o may be o (same ld). ws: sdm_block_norm_workspace_bytes, 16-byte aligned
+ * (may be NULL where no weight's gradient is asked for).
+ */
+size_t sdm_block_norm_workspace_bytes(const sdm_norm_shape* shape);
+sdm_status sdm_block_norm_backward(const sdm_norm_shape* shape, const void* o, int64_t o_ld, const void* z, int64_t z_ld,
+                                   const void* r, int64_t r_ld, const void* dr, int64_t dr_ld, const void* dy, int64_t dy_ld,
+                                   const float* w_post, const float* w_pre, const float* channel_scale, void* d_o, int64_t do_ld,
+                                   void* dz, int64_t dz_ld, void* dx, int64_t dx_ld, float* dw_post, float* dw_pre,
+                                   float* d_channel_scale, void* ws, size_t ws_bytes, sdm_stream_t stream);
+
+typedef struct {
+    int64_t tokens;      /* below 2^31 - 2^20 */
+    int32_t V;           /* rows of the table, up to 2^28 */
+    int32_t D;           /* columns of a row, a multiple of 4, up to 2^20 */
+    int32_t table_dtype; /* sdm_dtype of table and dtable */
+    int32_t dtype;       /* sdm_dtype of y and dy */
+    float scale;
+} sdm_embed_shape;
+
+/*
+ * y_i = scale table[ids_i], in float32, rounded. ids int32 [tokens]: below 0 is padding (y_i = 0); at or above V likewise, and sets
+ * SDM_DEV_BAD_TOKEN. table [V, D], y [tokens, D].
+ */
+sdm_status sdm_embed(const sdm_embed_shape* shape, const int32_t* ids, const void* table, int64_t table_ld, void* y, int64_t y_ld,
+                     uint32_t* status, sdm_stream_t stream);
+
+/*
+ * The table's gradient: row v of dtable [V, D] is scale times the sum of dy_i over the tokens with ids_i = v, added in float32 in an order
+ * that the ids alone fix, and rounded once. accumulate 0: every row is written (zeros where there is no token); 1: the sum
+ * is added to rows that have tokens, the others are not touched. ws: sdm_embed_workspace_bytes, 16-byte aligned.
+ */
+size_t sdm_embed_workspace_bytes(const sdm_embed_shape* shape);
+sdm_status sdm_embed_backward(const sdm_embed_shape* shape, const int32_t* ids, const void* dy, int64_t dy_ld, void* dtable,
+                              int64_t dtable_ld, int32_t accumulate, void* ws, size_t ws_bytes, uint32_t* status,
+                              sdm_stream_t stream);
 
 /*
  * Synchronizes `stream`, reads the workspace's device status word into *code_out (0 = fine,

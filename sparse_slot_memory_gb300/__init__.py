@@ -31,15 +31,23 @@ from .api import (  # noqa: F401
     workspace_bytes,
 )
 from .operators import (  # noqa: F401
+    BlockNormSpec,
+    EmbedSpec,
     GdrSpec,
     GlrSpec,
     LogprobSpec,
     RopeSpec,
+    alloc_block_norm_workspace,
+    alloc_embed_workspace,
     alloc_gdr_states,
     alloc_gdr_workspace,
     alloc_glr_states,
     alloc_glr_workspace,
     alloc_rope_workspace,
+    block_norm,
+    block_norm_backward,
+    embed,
+    embed_backward,
     gdr_backward,
     gdr_forward,
     gdr_step,

@@ -15,6 +15,7 @@ SDM_DEV_BAD_SLOT = 0x1
 SDM_DEV_BAD_OFFSET = 0x2
 SDM_DEV_BAD_POSITION = 0x4
 SDM_DEV_BAD_TARGET = 0x8
+SDM_DEV_BAD_TOKEN = 0x10
 SDM_GLR_CHUNK = 64
 SDM_GDR_CHUNK = 64
 
@@ -27,7 +28,8 @@ EXPORTS = ("sdm_workspace_bytes", "sdm_workspace_init", "sdm_phase1", "sdm_dw", 
            "sdm_rope_workspace_bytes", "sdm_rope_table", "sdm_qk_norm_rope", "sdm_qk_norm_rope_backward",
            "sdm_token_logprobs", "sdm_token_logprobs_backward",
            "sdm_gdr_states_bytes", "sdm_gdr_workspace_bytes", "sdm_gdr_forward", "sdm_gdr_backward",
-           "sdm_gdr_step")
+           "sdm_gdr_step", "sdm_block_norm_workspace_bytes", "sdm_block_norm", "sdm_block_norm_backward",
+           "sdm_embed_workspace_bytes", "sdm_embed", "sdm_embed_backward")
 NOALLOC_SCRATCH_BYTES = 16 << 20
 
 
@@ -54,6 +56,15 @@ class LogprobShape(ctypes.Structure):
 class GdrShape(ctypes.Structure):
     _fields_ = [("P", c_i32), ("k_heads", c_i32), ("v_heads", c_i32), ("dk", c_i32), ("dv", c_i32), ("x_dtype", c_i32),
                 ("g_dtype", c_i32), ("scale", ctypes.c_float), ("rows", c_i64)]
+
+
+class NormShape(ctypes.Structure):
+    _fields_ = [("rows", c_i64), ("D", c_i32), ("group", c_i32), ("post", c_i32), ("gate", c_i32), ("residual", c_i32),
+                ("pre", c_i32), ("dtype", c_i32), ("eps", ctypes.c_float), ("scale", ctypes.c_float)]
+
+
+class EmbedShape(ctypes.Structure):
+    _fields_ = [("tokens", c_i64), ("V", c_i32), ("D", c_i32), ("table_dtype", c_i32), ("dtype", c_i32), ("scale", ctypes.c_float)]
 
 
 P1_FIELDS = ("log_k", "rex", "cpe", "k_eff", "is_last", "is_only", "pos_k", "log_q", "q_w", "pos_q", "q_last",
@@ -115,10 +126,11 @@ def load(path: str = LIB):
 
 def _operators(lib):
     """The argument types of the operators around the memory."""
-    glr, rope, lp, gdr = (ctypes.POINTER(s) for s in (GlrShape, RopeShape, LogprobShape, GdrShape))
+    glr, rope, lp, gdr, norm, embed = (ctypes.POINTER(s) for s in (GlrShape, RopeShape, LogprobShape, GdrShape, NormShape, EmbedShape))
     row = [c_p, c_i64]   # a row array and the distance between its rows
     for name, shape in (("sdm_glr_states_bytes", glr), ("sdm_glr_workspace_bytes", glr),
-                        ("sdm_rope_workspace_bytes", rope), ("sdm_gdr_states_bytes", gdr)):
+                        ("sdm_rope_workspace_bytes", rope), ("sdm_gdr_states_bytes", gdr),
+                        ("sdm_block_norm_workspace_bytes", norm), ("sdm_embed_workspace_bytes", embed)):
         fn = getattr(lib, name)
         fn.restype, fn.argtypes = c_sz, [shape]
     lib.sdm_gdr_workspace_bytes.restype, lib.sdm_gdr_workspace_bytes.argtypes = c_sz, [gdr, c_i32]
@@ -127,6 +139,11 @@ def _operators(lib):
         ("sdm_gdr_backward", [gdr, *row, *row, *row, *row, *row, *row, c_p, c_p, c_p, *row, *row, *row, *row, *row, c_p, c_p,
                               c_sz, c_p, c_p]),
         ("sdm_gdr_step", [gdr, *row, *row, *row, *row, *row, c_p, *row, c_i64, *row, c_p, c_p]),
+        ("sdm_block_norm", [norm, *row, *row, *row, c_p, c_p, c_p, *row, *row, c_p]),
+        ("sdm_block_norm_backward", [norm, *row, *row, *row, *row, *row, c_p, c_p, c_p, *row, *row, *row, c_p, c_p, c_p, c_p, c_sz,
+                                     c_p]),
+        ("sdm_embed", [embed, c_p, *row, *row, c_p, c_p]),
+        ("sdm_embed_backward", [embed, c_p, *row, *row, c_i32, c_p, c_sz, c_p, c_p]),
         ("sdm_glr_forward", [glr, *row, *row, c_p, c_p, *row, c_p, c_p, c_p, c_p]),
         ("sdm_glr_backward", [glr, *row, *row, *row, c_p, c_p, c_p, *row, *row, c_p, c_p, c_sz, c_p, c_p]),
         ("sdm_glr_step", [glr, *row, *row, c_p, *row, c_i64, *row, c_p, c_p]),

@@ -1,0 +1,558 @@
+// sdm_norm.cu -- the norms behind and before a block, fused with its gate, the residual's scale and its sum, and their backward:
+// sdm_block_norm / sdm_block_norm_backward (include/sdm.h).
+//
+// Mathematics. Of a row: m = o rsqrt(mean o^2 + eps) w_post by groups of columns, n = m act(z), r = x + scale cs n rounded to
+// the rows' type, y = r rsqrt(mean r^2 + eps) w_pre of r as it is stored. Backward, with p and q the two rsqrt, u = dy w_pre:
+//   dR = dr + q (u - r q^2 mean(u r)) = dx,   dn = scale cs dR,   dz = dn m act'(z),   v = dn act(z) w_post,
+//   do = p (v - o p^2 mean(v o)),   dw_pre += dy r q,   dw_post += dn act(z) o p,   dcs += scale dR n.
+// Everything between the loads and the stores is float32; each output is rounded once.
+//
+// Layout. A group's columns lie on `lanes` threads (a power of two), U units of 4 columns each, a row's groups on neighbouring
+// threads, so a row is read once and stays in registers through both norms; sums go through shuffles and, beyond a warp, one
+// barrier. Resident blocks walk the rows; the weights' gradients grow in shared memory, where every place has one thread, to
+// a row of partial sums for each block, which a second kernel adds in order. Bound by HBM.
+#include <cuda_bf16.h>
+
+#include <algorithm>
+#include <cstring>
+#include <type_traits>
+
+#include "sdm_operators.cuh"
+
+namespace sdm {
+namespace {
+
+using namespace rows;
+
+constexpr int kMaxThreads = 512;
+constexpr int kMaxCols = 16384;
+constexpr int kPartBlocks = 608;   // blocks of the backward at most (four for each of 152 SMs): a row of partial sums each
+
+struct NormArgs {
+    const void* o;
+    const void* z;          // gate: nullable
+    const void* x;          // forward, residual: nullable
+    const void* rin;        // backward: r
+    const void* dr;         // nullable: zeros
+    const void* dy;
+    const float* w_post;    // nullable: ones
+    const float* w_pre;     // nullable: ones
+    const float* cs;        // nullable: ones
+    void* r;
+    void* y;
+    void* d_o;
+    void* dz;
+    void* dx;               // nullable
+    float* part;            // backward: [3][blocks][D]: dw_post, dw_pre, dcs
+    int64_t o_ld, z_ld, x_ld, r_ld, dr_ld, dy_ld, y_ld, do_ld, dz_ld, dx_ld;
+    int64_t rows;
+    int D, G, groups, post, gate, pre;
+    int lanes;              // threads of a group
+    int row_threads;        // threads of a row: a power of two up to a warp, else whole warps
+    int rows_block;         // rows of a block
+    int want;               // backward: 1 dw_post, 2 dw_pre, 4 dcs
+    float eps, scale;
+};
+
+// Sums over a row's and over a group's threads. Beyond a warp they meet in shared memory; two buffers take turns, so that one
+// barrier a call suffices.
+struct Sums {
+    float (*red)[3][kMaxThreads / 32];
+    int turn, lane, warp, row_warp, row_warps, group_warp, group_warps, row_width, group_width;
+    __device__ __forceinline__ Sums(const NormArgs& a, float (*shared)[3][kMaxThreads / 32]) : red(shared), turn(0) {
+        lane = threadIdx.x & 31;
+        warp = threadIdx.x >> 5;
+        row_width = min(a.row_threads, 32);
+        group_width = min(a.lanes, 32);
+        row_warps = (a.row_threads + 31) / 32;
+        group_warps = (a.lanes + 31) / 32;
+        row_warp = warp / row_warps * row_warps;
+        // a group of several warps starts at a multiple of its threads within its row
+        group_warp = row_warp + (warp - row_warp) / group_warps * group_warps;
+    }
+    template <int N>
+    __device__ __forceinline__ void row_and_group(float (&row)[N], float& group) {
+        for (int m = row_width / 2; m > 0; m /= 2)
+#pragma unroll
+            for (int i = 0; i < N; ++i) row[i] += __shfl_xor_sync(kFull, row[i], m);
+        for (int m = group_width / 2; m > 0; m /= 2) group += __shfl_xor_sync(kFull, group, m);
+        if (row_warps == 1) return;
+        if (lane == 0) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) red[turn][i][warp] = row[i];
+            red[turn][2][warp] = group;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            row[i] = 0.f;
+            for (int w = 0; w < row_warps; ++w) row[i] += red[turn][i][row_warp + w];
+        }
+        if (group_warps > 1) {
+            group = 0.f;
+            for (int w = 0; w < group_warps; ++w) group += red[turn][2][group_warp + w];
+        }
+        turn ^= 1;
+    }
+};
+
+// act and its slope: 1 sigmoid, 2 z sigmoid(z)
+__device__ __forceinline__ void gate_of(int kind, float z, float& act, float& slope) {
+    const float t = expf(-fabsf(z)), s = 1.f / (1.f + t);
+    const float sg = z >= 0.f ? s : t * s, rest = z >= 0.f ? t * s : s;   // sigmoid and 1 - sigmoid (NaN stays: t is)
+    if (kind == 1) {
+        act = sg;
+        slope = sg * rest;
+    } else {
+        act = sg == 0.f ? 0.f : z * sg;
+        slope = sg + (sg == 0.f || rest == 0.f ? 0.f : z * sg * rest);
+    }
+}
+
+// A thread's units: U places of 4 columns, `lanes` units apart within its group.
+template <int U>
+struct Columns {
+    int c[U];
+    bool on[U];
+    int row;    // its row within the block's
+    __device__ __forceinline__ explicit Columns(const NormArgs& a) {
+        row = threadIdx.x / a.row_threads;
+        const int t = threadIdx.x - row * a.row_threads, group = t / a.lanes, sub = t - group * a.lanes;
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const int u = sub + i * a.lanes;
+            on[i] = group < a.groups && u * 4 < a.G && row < a.rows_block;
+            c[i] = on[i] ? group * a.G + u * 4 : 0;
+        }
+    }
+};
+
+__device__ __forceinline__ void weights(const float* w, int c, float (&o)[4]) {
+    if (w == nullptr) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[e] = 1.f;
+    } else {
+        load4(w + c).get(o);
+    }
+}
+template <typename T>
+__device__ __forceinline__ void take(Raw4<T>& r, const void* p, int64_t row, int64_t ld, int c, bool on) {
+    r.zero();
+    if (on) ld_plain(r, static_cast<const T*>(p) + row * ld + c);
+}
+
+template <typename T, int U>
+__global__ void __launch_bounds__(kMaxThreads) norm_fwd_kernel(const __grid_constant__ NormArgs a) {
+    __shared__ float red[2][3][kMaxThreads / 32];
+    start_dependent();
+    const Columns<U> col(a);
+    Sums sums(a, red);
+    for (int64_t base = blockIdx.x * int64_t(a.rows_block); base < a.rows; base += gridDim.x * int64_t(a.rows_block)) {
+        const int64_t row = base + col.row;
+        const bool here = row < a.rows;
+        Raw4<T> o[U], z[U], x[U];
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const bool on = here && col.on[i];
+            take(o[i], a.o, row, a.o_ld, col.c[i], on);
+            take(z[i], a.z, row, a.z_ld, col.c[i], on && a.gate != 0);
+            take(x[i], a.x, row, a.x_ld, col.c[i], on && a.x != nullptr);
+        }
+        float p = 1.f;
+        if (a.post) {
+            float none[1] = {}, s = 0.f;
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                float v[4];
+                o[i].get(v);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s = fmaf(v[e], v[e], s);
+            }
+            sums.row_and_group(none, s);
+            p = rsqrtf(s / a.G + a.eps);
+        }
+        float r[U][4], s[1] = {};
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            float ov[4], zv[4], wv[4], cv[4];
+            o[i].get(ov);
+            z[i].get(zv);
+            x[i].get(r[i]);
+            if (a.post) weights(a.w_post, col.c[i] % a.G, wv);
+            weights(a.cs, col.c[i], cv);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                float n = a.post ? ov[e] * p * wv[e] : ov[e];
+                if (a.gate != 0) {
+                    float act, slope;
+                    gate_of(a.gate, zv[e], act, slope);
+                    n *= act;
+                }
+                r[i][e] = fmaf(a.scale * cv[e], n, r[i][e]);
+            }
+            if (sizeof(T) == 2) {   // as it is stored
+#pragma unroll
+                for (int e = 0; e < 4; ++e) r[i][e] = __bfloat162float(__float2bfloat16_rn(r[i][e]));
+            }
+            if (here && col.on[i]) st4(static_cast<T*>(a.r) + row * a.r_ld + col.c[i], r[i]);
+            else r[i][0] = r[i][1] = r[i][2] = r[i][3] = 0.f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) s[0] = fmaf(r[i][e], r[i][e], s[0]);
+        }
+        if (!a.pre) continue;
+        float none = 0.f;
+        sums.row_and_group(s, none);
+        const float q = rsqrtf(s[0] / a.D + a.eps);
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            if (!here || !col.on[i]) continue;
+            float w[4];
+            weights(a.w_pre, col.c[i], w);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) w[e] *= r[i][e] * q;
+            st4(static_cast<T*>(a.y) + row * a.y_ld + col.c[i], w);
+        }
+    }
+}
+
+// With U of 8 a thread cannot hold five rows' places: they are read again (from the L2) where they are used.
+template <typename T, int U>
+__global__ void __launch_bounds__(kMaxThreads) norm_bwd_kernel(const __grid_constant__ NormArgs a) {
+    constexpr bool kAgain = U == 8;
+    __shared__ float red[2][3][kMaxThreads / 32];
+    extern __shared__ __align__(16) float grown[];   // [rows of the block][kinds wanted][D]
+    start_dependent();
+    const Columns<U> col(a);
+    Sums sums(a, red);
+    const int kinds = __popc(a.want);
+    float* const mine = grown + static_cast<int64_t>(min(col.row, a.rows_block - 1)) * kinds * a.D;
+    float* const dpost = mine;
+    float* const dpre = mine + __popc(a.want & 1) * a.D;
+    float* const dcs = mine + __popc(a.want & 3) * a.D;
+    auto grow = [&](float* p, const float (&v)[4]) {
+        float t[4];
+        get4(p, t);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) t[e] += v[e];
+        st4(p, t);
+    };
+    for (int i = threadIdx.x; i < a.rows_block * kinds * a.D; i += blockDim.x) grown[i] = 0.f;
+    __syncthreads();
+    for (int64_t base = blockIdx.x * int64_t(a.rows_block); base < a.rows; base += gridDim.x * int64_t(a.rows_block)) {
+        const int64_t row = base + col.row;
+        const bool here = row < a.rows;
+        Raw4<T> o[U], z[U], r[U], g[U], dy[U];
+        auto take_r = [&](int i) {
+            const bool on = here && col.on[i] && a.pre;
+            take(r[i], a.rin, row, a.r_ld, col.c[i], on);
+            take(dy[i], a.dy, row, a.dy_ld, col.c[i], on);
+        };
+        auto take_g = [&](int i) {
+            const bool on = here && col.on[i];
+            take(z[i], a.z, row, a.z_ld, col.c[i], on && a.gate != 0);
+            take(g[i], a.dr, row, a.dr_ld, col.c[i], on && a.dr != nullptr);
+        };
+        auto take_o = [&](int i) { take(o[i], a.o, row, a.o_ld, col.c[i], here && col.on[i]); };
+        if (!kAgain) {
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                take_r(i);
+                take_o(i);
+                take_g(i);
+            }
+        }
+        float s[2] = {}, so = 0.f;   // of r^2, of u r; of o^2
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            if (kAgain) {
+                take_r(i);
+                take_o(i);
+            }
+            if (a.pre) {
+                float rv[4], dv[4], w[4];
+                r[i].get(rv);
+                dy[i].get(dv);
+                weights(a.w_pre, col.c[i], w);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    s[0] = fmaf(rv[e], rv[e], s[0]);
+                    s[1] = fmaf(dv[e] * w[e], rv[e], s[1]);
+                }
+            }
+            if (a.post) {
+                float v[4];
+                o[i].get(v);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) so = fmaf(v[e], v[e], so);
+            }
+        }
+        if (a.pre || a.post) sums.row_and_group(s, so);
+        const float q = rsqrtf(s[0] / a.D + a.eps), p = a.post ? rsqrtf(so / a.G + a.eps) : 1.f;
+        const float back = q * q * (s[1] / a.D);
+        float v[U][4];   // dn act(z) w_post
+        float sv = 0.f;
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            if (kAgain) {
+                take_r(i);
+                take_o(i);
+                take_g(i);
+            }
+            const bool on = here && col.on[i];
+            float ov[4], zv[4], d[4], w[4], cv[4], dzv[4], t[4];
+            o[i].get(ov);
+            z[i].get(zv);
+            g[i].get(d);
+            if (a.pre) {
+                float rv[4], dv[4];
+                r[i].get(rv);
+                dy[i].get(dv);
+                weights(a.w_pre, col.c[i], w);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    t[e] = dv[e] * (rv[e] * q);
+                    d[e] = fmaf(q, fmaf(-rv[e], back, dv[e] * w[e]), d[e]);
+                }
+                if (on && (a.want & 2)) grow(dpre + col.c[i], t);
+            }
+            if (a.dx != nullptr && on) st4(static_cast<T*>(a.dx) + row * a.dx_ld + col.c[i], d);
+            if (a.post) weights(a.w_post, col.c[i] % a.G, w);
+            weights(a.cs, col.c[i], cv);
+            float u[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float h = ov[e] * p, m = a.post ? h * w[e] : ov[e];
+                float act = 1.f, slope = 0.f;
+                if (a.gate != 0) gate_of(a.gate, zv[e], act, slope);
+                t[e] = a.scale * d[e] * (m * act);
+                const float dn = a.scale * cv[e] * d[e], dm = dn * act;
+                dzv[e] = dn * m * slope;
+                v[i][e] = dm;
+                u[e] = dm * h;
+                if (a.post) {
+                    v[i][e] = dm * w[e];
+                    sv = fmaf(v[i][e], ov[e], sv);
+                }
+            }
+            if (!on) continue;
+            if (a.want & 4) grow(dcs + col.c[i], t);
+            if (a.want & 1) grow(dpost + col.c[i], u);
+            if (a.gate != 0) st4(static_cast<T*>(a.dz) + row * a.dz_ld + col.c[i], dzv);
+        }
+        float k = 0.f;
+        if (a.post) {
+            float none[1] = {};
+            sums.row_and_group(none, sv);
+            k = p * p * (sv / a.G);
+        }
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            if (kAgain) take_o(i);
+            if (!here || !col.on[i]) continue;
+            float ov[4];
+            o[i].get(ov);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) ov[e] = a.post ? p * fmaf(-ov[e], k, v[i][e]) : v[i][e];
+            st4(static_cast<T*>(a.d_o) + row * a.do_ld + col.c[i], ov);
+        }
+    }
+    if (kinds == 0) return;
+    __syncthreads();
+    for (int i = threadIdx.x; i < kinds * a.D; i += blockDim.x) {   // the block's rows in order
+        float s = grown[i];
+        for (int w = 1; w < a.rows_block; ++w) s += grown[w * kinds * a.D + i];
+        const int nth = i / a.D;
+        int kind = 0;
+        for (int left = nth; left > 0 || !(a.want >> kind & 1); ++kind) left -= a.want >> kind & 1;
+        a.part[(static_cast<int64_t>(kind) * gridDim.x + blockIdx.x) * a.D + (i - nth * a.D)] = s;
+    }
+}
+
+// A kind's gradients: the blocks' rows in 32 shares, each in order, and those in order; of dw_post also its groups. Block y: the kind.
+__global__ void __launch_bounds__(1024) norm_dw_kernel(const float* part, int blocks, int D, int G, int want, float* dw_post,
+                                                       float* dw_pre, float* dcs) {
+    __shared__ float s[32][33];
+    start_dependent();
+    const int kind = blockIdx.y, n = kind == 0 ? G : D;
+    const int c = blockIdx.x * 32 + threadIdx.x;
+    if (!(want >> kind & 1) || blockIdx.x * 32 >= n) return;
+    float sum = 0.f;
+    if (c < n) {
+        const float* const p = part + static_cast<int64_t>(kind) * blocks * D + c;
+        for (int b = threadIdx.y; b < blocks; b += 32)
+            for (int g = 0; g < (kind == 0 ? D / G : 1); ++g) sum += p[static_cast<int64_t>(b) * D + g * G];
+    }
+    s[threadIdx.y][threadIdx.x] = sum;
+    __syncthreads();
+    if (threadIdx.y != 0 || c >= n) return;
+    sum = 0.f;
+    for (int i = 0; i < 32; ++i) sum += s[i][threadIdx.x];
+    (kind == 0 ? dw_post : kind == 1 ? dw_pre : dcs)[c] = sum;
+}
+
+// ---- host side ------------------------------------------------------------------------------------
+using checks::aligned16;
+using checks::aligned_all;
+
+sdm_status check(const sdm_norm_shape* s) {
+    if (s == nullptr) return SDM_ERR_ARG;
+    if (s->dtype < 0 || s->dtype > 1) return SDM_ERR_DTYPE;
+    if (s->rows < 0 || s->rows > (int64_t(1) << 40) || s->D < 1 || s->D > kMaxCols || s->group < 1 || s->group > s->D ||
+        s->D % s->group != 0 || s->post < 0 || s->post > 1 || s->gate < 0 || s->gate > 2 || s->residual < 0 || s->residual > 1 ||
+        s->pre < 0 || s->pre > 1 || !(s->eps >= 0.f) || !(s->scale == s->scale))
+        return SDM_ERR_SHAPE;
+    if (s->group % 4 != 0) return SDM_ERR_ALIGN;
+    return SDM_OK;
+}
+
+sdm_status check_rows(const sdm_norm_shape* s, const void* p, int64_t ld, bool out) {
+    if (p == nullptr) return SDM_ERR_ARG;
+    const int e = s->dtype == SDM_BF16 ? 2 : 4;
+    if (reinterpret_cast<uintptr_t>(p) % (4 * e) != 0 || ld % 4 != 0) return SDM_ERR_ALIGN;
+    if (ld < (out ? s->D : 0) || ld > (int64_t(1) << 40)) return SDM_ERR_ARG;
+    return SDM_OK;
+}
+
+int pow2(int n) {
+    int p = 1;
+    while (p < n) p *= 2;
+    return p;
+}
+
+// The threads of a group, U and the rows of a block: the U that leaves the fewest places idle, 4 where it makes no difference.
+// 0: a row's threads do not fit a block.
+int geometry(const sdm_norm_shape* s, NormArgs* a) {
+    memset(a, 0, sizeof(*a));
+    a->rows = s->rows;
+    a->D = s->D;
+    a->G = s->post ? s->group : s->D;   // without the norm behind the block its groups do not matter
+    a->groups = a->D / a->G;
+    a->post = s->post;
+    a->gate = s->gate;
+    a->pre = s->pre;
+    a->eps = s->eps;
+    a->scale = s->scale;
+    int best = 0, U = 0;
+    for (int u : {4, 3, 2, 1, 8}) {
+        const int lanes = pow2((a->G / 4 + u - 1) / u), threads = a->groups * lanes;
+        if (threads > kMaxThreads) continue;
+        if (U != 0 && lanes * u >= best) continue;
+        best = lanes * u;
+        U = u;
+        a->lanes = lanes;
+    }
+    if (U == 0) return 0;
+    const int threads = a->groups * a->lanes;
+    a->row_threads = threads <= 32 ? pow2(threads) : (threads + 31) / 32 * 32;
+    a->rows_block = std::max(1, 256 / a->row_threads);
+    return U;
+}
+
+int bwd_blocks(const NormArgs& a) {
+    const int64_t n = (a.rows + a.rows_block - 1) / a.rows_block;
+    return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(kPartBlocks, n)));
+}
+
+template <typename F>
+cudaError_t by_type(const sdm_norm_shape* s, int U, F f) {
+    auto units = [&](auto t) {
+        switch (U) {
+            case 1: return f(t, std::integral_constant<int, 1>{});
+            case 2: return f(t, std::integral_constant<int, 2>{});
+            case 3: return f(t, std::integral_constant<int, 3>{});
+            case 4: return f(t, std::integral_constant<int, 4>{});
+            default: return f(t, std::integral_constant<int, 8>{});
+        }
+    };
+    return s->dtype == SDM_BF16 ? units(__nv_bfloat16{}) : units(0.f);
+}
+
+}  // namespace
+}  // namespace sdm
+
+using namespace sdm;
+
+extern "C" size_t sdm_block_norm_workspace_bytes(const sdm_norm_shape* shape) {
+    NormArgs a;
+    if (check(shape) != SDM_OK || geometry(shape, &a) == 0) return 0;
+    return static_cast<size_t>(3) * bwd_blocks(a) * a.D * sizeof(float);
+}
+
+extern "C" sdm_status sdm_block_norm(const sdm_norm_shape* shape, const void* o, int64_t o_ld, const void* z, int64_t z_ld,
+                                     const void* x, int64_t x_ld, const float* w_post, const float* w_pre,
+                                     const float* channel_scale, void* r, int64_t r_ld, void* y, int64_t y_ld,
+                                     sdm_stream_t stream) {
+    sdm_status st = check(shape);
+    if (st != SDM_OK) return st;
+    NormArgs a;
+    const int U = geometry(shape, &a);
+    if (U == 0) return SDM_ERR_SHAPE;
+    if (shape->rows == 0) return SDM_OK;
+    if ((st = check_rows(shape, o, o_ld, false)) != SDM_OK) return st;
+    if (shape->gate && (st = check_rows(shape, z, z_ld, false)) != SDM_OK) return st;
+    if (shape->residual && (st = check_rows(shape, x, x_ld, false)) != SDM_OK) return st;
+    if ((st = check_rows(shape, r, r_ld, true)) != SDM_OK) return st;
+    if (shape->pre && (st = check_rows(shape, y, y_ld, true)) != SDM_OK) return st;
+    if (!aligned_all(16, {w_post, w_pre, channel_scale})) return SDM_ERR_ALIGN;
+    a.o = o; a.o_ld = o_ld; a.z = z; a.z_ld = z_ld; a.x = shape->residual ? x : nullptr; a.x_ld = x_ld;
+    a.w_post = w_post; a.w_pre = w_pre; a.cs = channel_scale; a.r = r; a.r_ld = r_ld; a.y = y; a.y_ld = y_ld;
+    const int threads = (a.rows_block * a.row_threads + 31) / 32 * 32;
+    const int64_t blocks = std::min<int64_t>((a.rows + a.rows_block - 1) / a.rows_block, 152 * (2048 / threads));
+    const cudaError_t e = by_type(shape, U, [&](auto t, auto u) {
+        return launch_dependent(norm_fwd_kernel<decltype(t), decltype(u)::value>, dim3(static_cast<unsigned>(blocks)), dim3(threads), 0,
+                                reinterpret_cast<cudaStream_t>(stream), a);
+    });
+    return e == cudaSuccess ? SDM_OK : SDM_ERR_CUDA;
+}
+
+extern "C" sdm_status sdm_block_norm_backward(const sdm_norm_shape* shape, const void* o, int64_t o_ld, const void* z, int64_t z_ld,
+                                              const void* r, int64_t r_ld, const void* dr, int64_t dr_ld, const void* dy,
+                                              int64_t dy_ld, const float* w_post, const float* w_pre,
+                                              const float* channel_scale, void* d_o, int64_t do_ld, void* dz, int64_t dz_ld,
+                                              void* dx, int64_t dx_ld, float* dw_post, float* dw_pre, float* d_channel_scale,
+                                              void* ws, size_t ws_bytes, sdm_stream_t stream) {
+    sdm_status st = check(shape);
+    if (st != SDM_OK) return st;
+    NormArgs a;
+    const int U = geometry(shape, &a);
+    if (U == 0) return SDM_ERR_SHAPE;
+    if (shape->rows > 0) {
+        if ((st = check_rows(shape, o, o_ld, false)) != SDM_OK) return st;
+        if (shape->gate && (st = check_rows(shape, z, z_ld, false)) != SDM_OK) return st;
+        if (shape->pre && (st = check_rows(shape, r, r_ld, false)) != SDM_OK) return st;
+        if (shape->pre && (st = check_rows(shape, dy, dy_ld, false)) != SDM_OK) return st;
+        if (dr == nullptr && !shape->pre) return SDM_ERR_ARG;
+        if (dr != nullptr && (st = check_rows(shape, dr, dr_ld, false)) != SDM_OK) return st;
+        if ((st = check_rows(shape, d_o, do_ld, true)) != SDM_OK) return st;
+        if (shape->gate && (st = check_rows(shape, dz, dz_ld, true)) != SDM_OK) return st;
+        if (dx != nullptr && (st = check_rows(shape, dx, dx_ld, true)) != SDM_OK) return st;
+    }
+    if (!aligned_all(16, {w_post, w_pre, channel_scale}) || !aligned_all(4, {dw_post, dw_pre, d_channel_scale})) return SDM_ERR_ALIGN;
+    const int asked = (dw_post != nullptr ? 1 : 0) | (dw_pre != nullptr ? 2 : 0) | (d_channel_scale != nullptr ? 4 : 0);
+    a.want = asked & ((shape->post ? 1 : 0) | (shape->pre ? 2 : 0) | 4);
+    const int blocks = bwd_blocks(a);
+    if (a.want && (ws == nullptr || !aligned16(ws) || ws_bytes < static_cast<size_t>(3) * blocks * a.D * sizeof(float)))
+        return SDM_ERR_WORKSPACE;
+    a.o = o; a.o_ld = o_ld; a.z = z; a.z_ld = z_ld; a.rin = r; a.r_ld = r_ld; a.dr = dr; a.dr_ld = dr_ld; a.dy = dy; a.dy_ld = dy_ld;
+    a.w_post = w_post; a.w_pre = w_pre; a.cs = channel_scale;
+    a.d_o = d_o; a.do_ld = do_ld; a.dz = dz; a.dz_ld = dz_ld; a.dx = dx; a.dx_ld = dx_ld;
+    a.part = static_cast<float*>(ws);
+    const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+    const int threads = (a.rows_block * a.row_threads + 31) / 32 * 32;
+    const int kinds = (a.want & 1) + (a.want >> 1 & 1) + (a.want >> 2 & 1);
+    const int smem = a.rows_block * kinds * a.D * static_cast<int>(sizeof(float));
+    cudaError_t e = cudaSuccess;
+    if (shape->rows > 0)
+        e = by_type(shape, U, [&](auto t, auto u) {
+            auto* const k = norm_bwd_kernel<decltype(t), decltype(u)::value>;
+            if (smem > 47 * 1024) {
+                const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+                if (e != cudaSuccess) return e;
+            }
+            return launch_dependent(k, dim3(static_cast<unsigned>(blocks)), dim3(threads), smem, cs, a);
+        });
+    if (e == cudaSuccess && asked)   // what the shape does not have is the sum of no blocks' rows: 0
+        e = launch_dependent(norm_dw_kernel, dim3(static_cast<unsigned>((a.D + 31) / 32), 3), dim3(32, 32), 0, cs, static_cast<const float*>(ws),
+                             shape->rows > 0 ? blocks : 0, a.D, shape->group, asked, dw_post, dw_pre, d_channel_scale);
+    return e == cudaSuccess ? SDM_OK : SDM_ERR_CUDA;
+}

@@ -4,6 +4,8 @@
 * ``gdr_*``: the gated delta rule, a state of dk slots a head that every token decays, corrects and reads, its backward, and one
   token per request;
 * ``qk_norm_rope*``: the norm of every query and key head with the position rotation in the same pass;
+* ``block_norm*``: the norms behind and before a block with its gate, the residual's scale and sum;
+* ``embed*``: the rows of an embedding table for tokens, and the table's gradient by sorted tokens;
 * ``token_logprobs*``: log probabilities of given tokens, entropy, top alternatives, and the logits' gradient.
 
 Tensors are CUDA tensors owned by the caller. Row arrays are two-dimensional (heads: three-dimensional) views
@@ -411,6 +413,112 @@ def qk_norm_rope_backward(spec: RopeSpec, dq_out, dk_out, q, k, positions, table
         _small(dwq, _F32, spec.hd, "dwq"), _small(dwk, _F32, spec.hd, "dwk"), _small(ws, torch.uint8, 0, "ws"),
         0 if ws is None else ws.numel(), _status(status), _stream(stream))
     _check(st, "sdm_qk_norm_rope_backward")
+
+
+# ---- the norms around a block -------------------------------------------------------------------------
+_GATE = {"none": 0, "sigmoid": 1, "silu": 2}
+
+
+@dataclasses.dataclass(frozen=True)
+class BlockNormSpec(_Spec):
+    """``rows`` rows of D columns. ``post``: the block's output is normed, by groups of ``group`` columns (0: whole rows); ``gate``:
+    "none", "sigmoid" or "silu"; ``residual``: a stream is added; ``pre``: the sum is normed for the next block."""
+
+    rows: int
+    D: int
+    group: int = 0
+    post: bool = True
+    gate: str = "none"
+    residual: bool = True
+    pre: bool = True
+    scale: float = 1.0
+    dtype: str = "bf16"
+    eps: float = 1e-6
+
+    def _struct(self):
+        return _abi.NormShape(self.rows, self.D, self.group or self.D, int(self.post), _GATE[self.gate], int(self.residual),
+                              int(self.pre), _DT[self.dtype], self.eps, self.scale)
+
+
+def alloc_block_norm_workspace(spec: BlockNormSpec, device="cuda") -> torch.Tensor:
+    return torch.empty(_bytes(spec, "sdm_block_norm_workspace_bytes"), dtype=torch.uint8, device=device)
+
+
+def _norm_rows(spec: BlockNormSpec, t, name: str, out: bool = False, optional: bool = False):
+    if t is None and optional:
+        return None, 0
+    return _rows(t, _TORCH_DT[spec.dtype], (spec.rows, spec.D), spec.D, name, out)
+
+
+def block_norm(spec: BlockNormSpec, o, r, x=None, z=None, y=None, w_post=None, w_pre=None, channel_scale=None, stream=None):
+    """sdm_block_norm: ``r`` = x + scale * channel_scale * act(z) * norm(o) * w_post and ``y`` = norm(r) * w_pre, rows [rows, D].
+    ``o``: the block's output; ``z`` (with a gate), ``x`` (with residual) and ``y`` (with pre) where the spec has them; ``w_post`` float32
+    [group], ``w_pre``, ``channel_scale`` float32 [D] (None: ones). ``r`` may be ``x``, ``y`` may be ``o``."""
+    D = spec.D
+    st = _abi.load().sdm_block_norm(
+        spec.c(), *_norm_rows(spec, o, "o"), *_norm_rows(spec, z, "z", optional=spec.gate == "none"),
+        *_norm_rows(spec, x, "x", optional=not spec.residual), _small(w_post, _F32, spec.group or D, "w_post"),
+        _small(w_pre, _F32, D, "w_pre"), _small(channel_scale, _F32, D, "channel_scale"), *_norm_rows(spec, r, "r", True),
+        *_norm_rows(spec, y, "y", True, not spec.pre), _stream(stream))
+    _check(st, "sdm_block_norm")
+
+
+def block_norm_backward(spec: BlockNormSpec, o, r, dr, d_o, ws=None, z=None, dy=None, w_post=None, w_pre=None, channel_scale=None,
+                        dx=None, dz=None, dw_post=None, dw_pre=None, d_channel_scale=None, stream=None):
+    """sdm_block_norm_backward: from ``dr`` (the gradient of r; None for zeros where there is ``dy``) and ``dy`` the gradients ``d_o``, ``dz``
+    (with a gate), ``dx`` (optional: of the sum, the stream's) [rows, D] and of the weights, ``dw_post`` [group], ``dw_pre``,
+    ``d_channel_scale`` [D] (optional, float32; they need ``ws`` from ``alloc_block_norm_workspace``). ``r`` is the forward's."""
+    D = spec.D
+    st = _abi.load().sdm_block_norm_backward(
+        spec.c(), *_norm_rows(spec, o, "o"), *_norm_rows(spec, z, "z", optional=spec.gate == "none"),
+        *_norm_rows(spec, r, "r", optional=not spec.pre), *_norm_rows(spec, dr, "dr", optional=spec.pre),
+        *_norm_rows(spec, dy, "dy", optional=not spec.pre), _small(w_post, _F32, spec.group or D, "w_post"),
+        _small(w_pre, _F32, D, "w_pre"), _small(channel_scale, _F32, D, "channel_scale"), *_norm_rows(spec, d_o, "d_o", True),
+        *_norm_rows(spec, dz, "dz", True, spec.gate == "none"), *_norm_rows(spec, dx, "dx", True, True),
+        _small(dw_post, _F32, spec.group or D, "dw_post"), _small(dw_pre, _F32, D, "dw_pre"),
+        _small(d_channel_scale, _F32, D, "d_channel_scale"), *_workspace(ws), _stream(stream))
+    _check(st, "sdm_block_norm_backward")
+
+
+# ---- the embedding ------------------------------------------------------------------------------------
+@dataclasses.dataclass(frozen=True)
+class EmbedSpec(_Spec):
+    """``tokens`` tokens and a table of V rows of D columns; ``table_dtype`` of the table and its gradient, ``dtype`` of the tokens'
+    rows and theirs."""
+
+    tokens: int
+    V: int
+    D: int
+    table_dtype: str = "f32"
+    dtype: str = "bf16"
+    scale: float = 1.0
+
+    def _struct(self):
+        return _abi.EmbedShape(self.tokens, self.V, self.D, _DT[self.table_dtype], _DT[self.dtype], self.scale)
+
+
+def alloc_embed_workspace(spec: EmbedSpec, device="cuda") -> torch.Tensor:
+    return torch.empty(_bytes(spec, "sdm_embed_workspace_bytes"), dtype=torch.uint8, device=device)
+
+
+def embed(spec: EmbedSpec, ids, table, y, status=None, stream=None):
+    """sdm_embed: ``y[i]`` = scale * ``table[ids[i]]`` (``ids`` int32 [tokens]; below 0: padding, zeros; ``table`` [V, D], ``y`` [tokens, D])."""
+    D = spec.D
+    st = _abi.load().sdm_embed(
+        spec.c(), _small(ids, _I32, spec.tokens, "ids"), *_rows(table, _TORCH_DT[spec.table_dtype], (spec.V, D), D, "table"),
+        *_rows(y, _TORCH_DT[spec.dtype], (spec.tokens, D), D, "y", True), _status(status), _stream(stream))
+    _check(st, "sdm_embed")
+
+
+def embed_backward(spec: EmbedSpec, ids, dy, dtable, ws, accumulate=False, status=None, stream=None):
+    """sdm_embed_backward: ``dtable`` [V, D], row v scale times the sum of ``dy`` over the tokens with id v, in a fixed order. Without
+    ``accumulate`` every row is written; with it the sums are added to the rows that have tokens. ``ws`` from ``alloc_embed_workspace``."""
+    D = spec.D
+    st = _abi.load().sdm_embed_backward(
+        spec.c(), _small(ids, _I32, spec.tokens, "ids"), *_rows(dy, _TORCH_DT[spec.dtype], (spec.tokens, D), D, "dy"),
+        *_rows(dtable, _TORCH_DT[spec.table_dtype], (spec.V, D), D, "dtable", True), int(accumulate), *_workspace(ws), _status(status),
+        _stream(stream))
+    _check(st, "sdm_embed_backward")
 
 
 # ---- log probabilities of tokens ---------------------------------------------------------------------
