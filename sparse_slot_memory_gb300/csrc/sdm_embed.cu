@@ -20,6 +20,7 @@ namespace {
 
 using namespace rows;
 
+constexpr int kHeld = 4;        // rounds of a warp's tokens that stay in registers
 constexpr int kSortBlocks = 8, kSortThreads = 1024, kSortWarps = kSortThreads / 32;
 constexpr int kSlice = 512;     // columns of a warp's unit: 16 a lane
 constexpr int kMany = 64;       // tokens from which a row is a block's
@@ -107,21 +108,43 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const __grid_c
             if (id >= a.V && a.status != nullptr) atomicOr(a.status, SDM_DEV_BAD_TOKEN);
             return id < 0 || id >= a.V ? a.V : id;   // padding sorts last
         };
+        // a warp's tokens, 32 at a time; the first kHeld rounds' stay in registers for the second look
+        auto round_of = [&](int64_t i, int (&k)[kHeld], int (&t)[kHeld]) {
+#pragma unroll
+            for (int r = 0; r < kHeld; ++r) {
+                const int64_t j = i + 32 * r;
+                k[r] = j < hi ? key_at(j) : -1;
+                t[r] = j < hi ? (pass > 0 ? __ldcg(tin + j) : static_cast<int>(j)) : 0;
+            }
+        };
+        int k0[kHeld], t0[kHeld];
+        round_of(lo + lane, k0, t0);
         for (int i = lane; i < 256; i += 32) hist[w][i] = 0;
         __syncwarp();
-        for (int64_t i = lo + lane; i - lane < hi; i += 32) {
-            const int d = i < hi ? (key_at(i) >> shift) & 255 : 256;
-            const uint32_t same = __match_any_sync(kFull, d);
-            if (d < 256 && (same & ((1u << lane) - 1)) == 0) hist[w][d] += __popc(same);
-            __syncwarp();
+        auto count = [&](const int (&k)[kHeld]) {
+#pragma unroll
+            for (int r = 0; r < kHeld; ++r) {
+                const int d = k[r] >= 0 ? (k[r] >> shift) & 255 : 256;
+                const uint32_t same = __match_any_sync(kFull, d);
+                if (d < 256 && (same & ((1u << lane) - 1)) == 0) hist[w][d] += __popc(same);
+                __syncwarp();
+            }
+        };
+        count(k0);
+        for (int64_t i = lo + 32 * kHeld; i < hi; i += 32 * kHeld) {
+            int k[kHeld], t[kHeld];
+            round_of(i + lane, k, t);
+            count(k);
         }
         __syncthreads();
         if (tid < 256) {
-            int sum = 0;
+            int c[kSortWarps], sum = 0;
+#pragma unroll
+            for (int i = 0; i < kSortWarps; ++i) c[i] = hist[i][tid];
+#pragma unroll
             for (int i = 0; i < kSortWarps; ++i) {
-                const int c = hist[i][tid];
                 hist[i][tid] = sum;
-                sum += c;
+                sum += c[i];
             }
             total[tid] = sum;
         }
@@ -129,11 +152,14 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const __grid_c
         cluster_wait();
         int all = 0, before = 0;
         if (tid < 256) {
+            int c[kSortBlocks];
+#pragma unroll
+            for (int r = 0; r < kSortBlocks; ++r)
+                asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(c[r]) : "r"(remote_address(&total[tid], r)) : "memory");
+#pragma unroll
             for (int r = 0; r < kSortBlocks; ++r) {
-                int c;
-                asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(c) : "r"(remote_address(&total[tid], r)) : "memory");
-                all += c;
-                before += r < rank ? c : 0;
+                all += c[r];
+                before += r < rank ? c[r] : 0;
             }
             int run = all;   // the digits' places: a scan over 256
             for (int m = 1; m < 32; m *= 2) {
@@ -150,21 +176,28 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const __grid_c
             first[tid] += c;
         }
         __syncthreads();
-        for (int64_t i = lo + lane; i - lane < hi; i += 32) {
-            const int k = i < hi ? key_at(i) : 0;
-            const int d = i < hi ? (k >> shift) & 255 : 256;
-            const int t = i < hi ? (pass > 0 ? __ldcg(tin + i) : static_cast<int>(i)) : 0;
-            const uint32_t same = __match_any_sync(kFull, d);
-            const int ahead = __popc(same & ((1u << lane) - 1));
-            int at = 0;
-            if (d < 256) at = first[d] + hist[w][d] + ahead;
-            __syncwarp();
-            if (d < 256 && ahead == 0) hist[w][d] += __popc(same);
-            __syncwarp();
-            if (d < 256) {
-                kout[at] = k;
-                tout[at] = t;
+        auto place = [&](const int (&k)[kHeld], const int (&t)[kHeld]) {
+#pragma unroll
+            for (int r = 0; r < kHeld; ++r) {
+                const int d = k[r] >= 0 ? (k[r] >> shift) & 255 : 256;
+                const uint32_t same = __match_any_sync(kFull, d);
+                const int ahead = __popc(same & ((1u << lane) - 1));
+                int at = 0;
+                if (d < 256) at = first[d] + hist[w][d] + ahead;
+                __syncwarp();
+                if (d < 256 && ahead == 0) hist[w][d] += __popc(same);
+                __syncwarp();
+                if (d < 256) {
+                    kout[at] = k[r];
+                    tout[at] = t[r];
+                }
             }
+        };
+        place(k0, t0);
+        for (int64_t i = lo + 32 * kHeld; i < hi; i += 32 * kHeld) {
+            int k[kHeld], t[kHeld];
+            round_of(i + lane, k, t);
+            place(k, t);
         }
         // the next pass reads what the cluster wrote, and writes the totals that it read
         cluster_arrive();

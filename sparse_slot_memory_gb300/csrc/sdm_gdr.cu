@@ -38,7 +38,7 @@ __global__ void __launch_bounds__(256) gdr_split_kernel(const float* x, int64_t 
 // the key head weighs them by its decays. T is built from its 16 x 16 blocks: those on the diagonal row by row in float32 (a
 // column a lane), those below by T_21 = -T_22 (N_21 T_11), first for 32 rows, then for 64, in products of terms.
 template <int XT, int DKP>
-__global__ void __launch_bounds__(128) gdr_prepare_kernel(const __grid_constant__ Args a) {
+__global__ void __launch_bounds__(128, XT == 1 ? 4 : 2) gdr_prepare_kernel(const __grid_constant__ Args a) {
     constexpr int kTile = kC * DKP * 2, kPlane = kC * kC * 2, NS = XT == 1 ? 2 : 3;
     extern __shared__ __align__(1024) unsigned char smem[];
     __shared__ float gh[kC], gl[kC], be[kC];
@@ -51,7 +51,8 @@ __global__ void __launch_bounds__(128) gdr_prepare_kernel(const __grid_constant_
     int n;
     block_rows(a, id, b, n);
     if (n <= 0) return;
-    const uint32_t K = smem_of(smem), Q = K + XT * kTile, N = Q + XT * kTile, T = N + NS * kPlane;
+    // N and T take the place of K and Q, which the accumulators have taken in
+    const uint32_t K = smem_of(smem), Q = K + XT * kTile, N = K, T = N + NS * kPlane;
     load_rows<DKP, 128>(K, a.k, XT, b, n, kh * a.dk, a.dk, tid);
     load_rows<DKP, 128>(Q, a.q, XT, b, n, kh * a.dk, a.dk, tid);
     copies_commit();
@@ -84,6 +85,7 @@ __global__ void __launch_bounds__(128) gdr_prepare_kernel(const __grid_constant_
             }
         }
     }
+    __syncthreads();
     const int R = a.Hv / a.Hk, a_planes = a.tri_planes - NS;
     for (int rv = 0; rv < R; ++rv) {
         const int h = kh * R + rv;
@@ -136,7 +138,7 @@ __global__ void __launch_bounds__(128) gdr_prepare_kernel(const __grid_constant_
                 float av[2], nv[2];
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    const float d = expf((gh[i] - gh[j + c]) + (gl[i] - gl[j + c]));
+                    const float d = decay<XT>((gh[i] - gh[j + c]) + (gl[i] - gl[j + c]));
                     av[c] = j + c <= i ? d * qk[nt][2 * e + c] : 0.f;
                     nv[c] = j + c < i ? be[i] * (d * kk[nt][2 * e + c]) : 0.f;
                     if (nt >> 1 == w) diag[w][g + 8 * e][j + c - 16 * w] = nv[c];
@@ -557,7 +559,7 @@ cudaError_t big_smem(K kernel, int bytes) {
 
 template <int XT, int DKP>
 cudaError_t prepare(const Args& a, int64_t blocks, cudaStream_t cs) {
-    constexpr int bytes = 2 * XT * kC * DKP * 2 + 2 * (XT == 1 ? 2 : 3) * kC * kC * 2;
+    constexpr int tiles = 2 * XT * kC * DKP * 2, planes = 2 * (XT == 1 ? 2 : 3) * kC * kC * 2, bytes = tiles > planes ? tiles : planes;
     auto* const k = gdr_prepare_kernel<XT, DKP>;
     const cudaError_t e = big_smem(k, bytes);
     if (e != cudaSuccess) return e;

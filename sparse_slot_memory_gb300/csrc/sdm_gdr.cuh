@@ -134,6 +134,13 @@ __device__ __forceinline__ float gate_at(const void* p, int64_t i, int bf16) {
     return bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(p)[i]) : static_cast<const float*>(p)[i];
 }
 
+// e^x of a difference of decays' sums. Beside bfloat16 rows by the hardware's exponential: 2 + 1.2 |x| units of 2^-23, and what e^x
+// loses in digits it has lost in size.
+template <int XT>
+__device__ __forceinline__ float decay(float x) {
+    return XT == 1 ? __expf(x) : expf(x);
+}
+
 // ---- tiles in shared memory: rows of W bfloat16 in units of 16 bytes, which the row's number permutes so that eight rows'
 // units of one column lie in different banks ------------------------------------------------------------
 template <int W>

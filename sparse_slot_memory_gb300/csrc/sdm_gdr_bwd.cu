@@ -467,7 +467,7 @@ __global__ void __launch_bounds__(512) gdr_grad_kernel(const __grid_constant__ A
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
                 float d = 0.f;
-                if (j + c <= i) d = expf((vec[3 * kC + i] - vec[3 * kC + j + c]) + (vec[4 * kC + i] - vec[4 * kC + j + c]));
+                if (j + c <= i) d = decay<XT>((vec[3 * kC + i] - vec[3 * kC + j + c]) + (vec[4 * kC + i] - vec[4 * kC + j + c]));
                 const float N = a.scale * nn[t][2 * e + c], M = vec[kC + i] * m[t][2 * e + c];
                 x[c] = j + c <= i ? d * N : 0.f;
                 y[c] = j + c < i ? -d * M : 0.f;

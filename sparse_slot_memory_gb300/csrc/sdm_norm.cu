@@ -26,7 +26,7 @@ using namespace rows;
 
 constexpr int kMaxThreads = 512;
 constexpr int kMaxCols = 16384;
-constexpr int kPartBlocks = 608;   // blocks of the backward at most (four for each of 152 SMs): a row of partial sums each
+constexpr int kPartBlocks = 304;   // blocks of the backward at most (two for each of 152 SMs): a row of partial sums each
 
 struct NormArgs {
     const void* o;
@@ -43,10 +43,10 @@ struct NormArgs {
     void* d_o;
     void* dz;
     void* dx;               // nullable
-    float* part;            // backward: [3][blocks][D]: dw_post, dw_pre, dcs
+    float* part;            // backward: [3][blocks][D]: dw_post (of its rows the first G columns), dw_pre, dcs
     int64_t o_ld, z_ld, x_ld, r_ld, dr_ld, dy_ld, y_ld, do_ld, dz_ld, dx_ld;
     int64_t rows;
-    int D, G, groups, post, gate, pre;
+    int D, G, groups, post, pre;
     int lanes;              // threads of a group
     int row_threads;        // threads of a row: a power of two up to a warp, else whole warps
     int rows_block;         // rows of a block
@@ -96,16 +96,19 @@ struct Sums {
     }
 };
 
-// act and its slope: 1 sigmoid, 2 z sigmoid(z)
-__device__ __forceinline__ void gate_of(int kind, float z, float& act, float& slope) {
-    const float t = expf(-fabsf(z)), s = 1.f / (1.f + t);
-    const float sg = z >= 0.f ? s : t * s, rest = z >= 0.f ? t * s : s;   // sigmoid and 1 - sigmoid (NaN stays: t is)
-    if (kind == 1) {
+// act and its slope: GATE 1 sigmoid, 2 z sigmoid(z). bfloat16 rows take the hardware's exponential and division, which are off by
+// 2^-21 (|z| + 1) at most where the rows are 2^-8 apart; float32 rows expf and a rounded division.
+template <typename T, int GATE>
+__device__ __forceinline__ void gate_of(float z, float& act, float& slope) {
+    const float t = sizeof(T) == 2 ? __expf(-fabsf(z)) : expf(-fabsf(z));
+    const float s = sizeof(T) == 2 ? __fdividef(1.f, 1.f + t) : 1.f / (1.f + t);
+    const float ts = t * s, sg = z >= 0.f ? s : ts, rest = z >= 0.f ? ts : s;   // sigmoid and 1 - sigmoid (NaN stays: t is)
+    if (GATE == 1) {
         act = sg;
         slope = sg * rest;
-    } else {
+    } else {   // at infinite z their limits
         act = sg == 0.f ? 0.f : z * sg;
-        slope = sg + (sg == 0.f || rest == 0.f ? 0.f : z * sg * rest);
+        slope = ts == 0.f ? sg : fmaf(act, rest, sg);
     }
 }
 
@@ -113,6 +116,7 @@ __device__ __forceinline__ void gate_of(int kind, float z, float& act, float& sl
 template <int U>
 struct Columns {
     int c[U];
+    int w[U];   // its place in the group
     bool on[U];
     int row;    // its row within the block's
     __device__ __forceinline__ explicit Columns(const NormArgs& a) {
@@ -122,6 +126,7 @@ struct Columns {
         for (int i = 0; i < U; ++i) {
             const int u = sub + i * a.lanes;
             on[i] = group < a.groups && u * 4 < a.G && row < a.rows_block;
+            w[i] = on[i] ? u * 4 : 0;
             c[i] = on[i] ? group * a.G + u * 4 : 0;
         }
     }
@@ -141,7 +146,7 @@ __device__ __forceinline__ void take(Raw4<T>& r, const void* p, int64_t row, int
     if (on) ld_plain(r, static_cast<const T*>(p) + row * ld + c);
 }
 
-template <typename T, int U>
+template <typename T, int U, int GATE>
 __global__ void __launch_bounds__(kMaxThreads) norm_fwd_kernel(const __grid_constant__ NormArgs a) {
     __shared__ float red[2][3][kMaxThreads / 32];
     start_dependent();
@@ -155,7 +160,7 @@ __global__ void __launch_bounds__(kMaxThreads) norm_fwd_kernel(const __grid_cons
         for (int i = 0; i < U; ++i) {
             const bool on = here && col.on[i];
             take(o[i], a.o, row, a.o_ld, col.c[i], on);
-            take(z[i], a.z, row, a.z_ld, col.c[i], on && a.gate != 0);
+            take(z[i], a.z, row, a.z_ld, col.c[i], on && GATE != 0);
             take(x[i], a.x, row, a.x_ld, col.c[i], on && a.x != nullptr);
         }
         float p = 1.f;
@@ -178,14 +183,14 @@ __global__ void __launch_bounds__(kMaxThreads) norm_fwd_kernel(const __grid_cons
             o[i].get(ov);
             z[i].get(zv);
             x[i].get(r[i]);
-            if (a.post) weights(a.w_post, col.c[i] % a.G, wv);
+            if (a.post) weights(a.w_post, col.w[i], wv);
             weights(a.cs, col.c[i], cv);
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 float n = a.post ? ov[e] * p * wv[e] : ov[e];
-                if (a.gate != 0) {
+                if constexpr (GATE != 0) {
                     float act, slope;
-                    gate_of(a.gate, zv[e], act, slope);
+                    gate_of<T, GATE>(zv[e], act, slope);
                     n *= act;
                 }
                 r[i][e] = fmaf(a.scale * cv[e], n, r[i][e]);
@@ -216,7 +221,7 @@ __global__ void __launch_bounds__(kMaxThreads) norm_fwd_kernel(const __grid_cons
 }
 
 // With U of 8 a thread cannot hold five rows' places: they are read again (from the L2) where they are used.
-template <typename T, int U>
+template <typename T, int U, int GATE>
 __global__ void __launch_bounds__(kMaxThreads) norm_bwd_kernel(const __grid_constant__ NormArgs a) {
     constexpr bool kAgain = U == 8;
     __shared__ float red[2][3][kMaxThreads / 32];
@@ -249,7 +254,7 @@ __global__ void __launch_bounds__(kMaxThreads) norm_bwd_kernel(const __grid_cons
         };
         auto take_g = [&](int i) {
             const bool on = here && col.on[i];
-            take(z[i], a.z, row, a.z_ld, col.c[i], on && a.gate != 0);
+            take(z[i], a.z, row, a.z_ld, col.c[i], on && GATE != 0);
             take(g[i], a.dr, row, a.dr_ld, col.c[i], on && a.dr != nullptr);
         };
         auto take_o = [&](int i) { take(o[i], a.o, row, a.o_ld, col.c[i], here && col.on[i]); };
@@ -316,14 +321,14 @@ __global__ void __launch_bounds__(kMaxThreads) norm_bwd_kernel(const __grid_cons
                 if (on && (a.want & 2)) grow(dpre + col.c[i], t);
             }
             if (a.dx != nullptr && on) st4(static_cast<T*>(a.dx) + row * a.dx_ld + col.c[i], d);
-            if (a.post) weights(a.w_post, col.c[i] % a.G, w);
+            if (a.post) weights(a.w_post, col.w[i], w);
             weights(a.cs, col.c[i], cv);
             float u[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const float h = ov[e] * p, m = a.post ? h * w[e] : ov[e];
                 float act = 1.f, slope = 0.f;
-                if (a.gate != 0) gate_of(a.gate, zv[e], act, slope);
+                if constexpr (GATE != 0) gate_of<T, GATE>(zv[e], act, slope);
                 t[e] = a.scale * d[e] * (m * act);
                 const float dn = a.scale * cv[e] * d[e], dm = dn * act;
                 dzv[e] = dn * m * slope;
@@ -337,7 +342,7 @@ __global__ void __launch_bounds__(kMaxThreads) norm_bwd_kernel(const __grid_cons
             if (!on) continue;
             if (a.want & 4) grow(dcs + col.c[i], t);
             if (a.want & 1) grow(dpost + col.c[i], u);
-            if (a.gate != 0) st4(static_cast<T*>(a.dz) + row * a.dz_ld + col.c[i], dzv);
+            if (GATE != 0) st4(static_cast<T*>(a.dz) + row * a.dz_ld + col.c[i], dzv);
         }
         float k = 0.f;
         if (a.post) {
@@ -358,17 +363,21 @@ __global__ void __launch_bounds__(kMaxThreads) norm_bwd_kernel(const __grid_cons
     }
     if (kinds == 0) return;
     __syncthreads();
-    for (int i = threadIdx.x; i < kinds * a.D; i += blockDim.x) {   // the block's rows in order
-        float s = grown[i];
-        for (int w = 1; w < a.rows_block; ++w) s += grown[w * kinds * a.D + i];
-        const int nth = i / a.D;
-        int kind = 0;
-        for (int left = nth; left > 0 || !(a.want >> kind & 1); ++kind) left -= a.want >> kind & 1;
-        a.part[(static_cast<int64_t>(kind) * gridDim.x + blockIdx.x) * a.D + (i - nth * a.D)] = s;
+    // the block's rows in order, of dw_post for each group in order
+    for (int kind = 0; kind < 3; ++kind) {
+        if (!(a.want >> kind & 1)) continue;
+        const float* const from = kind == 0 ? grown + (dpost - mine) : kind == 1 ? grown + (dpre - mine) : grown + (dcs - mine);
+        const int n = kind == 0 ? a.G : a.D;
+        for (int i = threadIdx.x; i < n; i += blockDim.x) {
+            float s = 0.f;
+            for (int w = 0; w < a.rows_block; ++w)
+                for (int c = i; c < a.D; c += n) s += from[w * kinds * a.D + c];
+            a.part[(static_cast<int64_t>(kind) * gridDim.x + blockIdx.x) * a.D + i] = s;
+        }
     }
 }
 
-// A kind's gradients: the blocks' rows in 32 shares, each in order, and those in order; of dw_post also its groups. Block y: the kind.
+// A kind's gradients: the blocks' rows in 32 shares, each in order, and those in order. Block y: the kind.
 __global__ void __launch_bounds__(1024) norm_dw_kernel(const float* part, int blocks, int D, int G, int want, float* dw_post,
                                                        float* dw_pre, float* dcs) {
     __shared__ float s[32][33];
@@ -379,8 +388,8 @@ __global__ void __launch_bounds__(1024) norm_dw_kernel(const float* part, int bl
     float sum = 0.f;
     if (c < n) {
         const float* const p = part + static_cast<int64_t>(kind) * blocks * D + c;
-        for (int b = threadIdx.y; b < blocks; b += 32)
-            for (int g = 0; g < (kind == 0 ? D / G : 1); ++g) sum += p[static_cast<int64_t>(b) * D + g * G];
+#pragma unroll 5
+        for (int b = threadIdx.y; b < blocks; b += 32) sum += p[static_cast<int64_t>(b) * D];
     }
     s[threadIdx.y][threadIdx.x] = sum;
     __syncthreads();
@@ -428,7 +437,6 @@ int geometry(const sdm_norm_shape* s, NormArgs* a) {
     a->G = s->post ? s->group : s->D;   // without the norm behind the block its groups do not matter
     a->groups = a->D / a->G;
     a->post = s->post;
-    a->gate = s->gate;
     a->pre = s->pre;
     a->eps = s->eps;
     a->scale = s->scale;
@@ -455,13 +463,17 @@ int bwd_blocks(const NormArgs& a) {
 
 template <typename F>
 cudaError_t by_type(const sdm_norm_shape* s, int U, F f) {
+    auto gates = [&](auto t, auto u) {
+        return s->gate == 0 ? f(t, u, std::integral_constant<int, 0>{})
+               : s->gate == 1 ? f(t, u, std::integral_constant<int, 1>{}) : f(t, u, std::integral_constant<int, 2>{});
+    };
     auto units = [&](auto t) {
         switch (U) {
-            case 1: return f(t, std::integral_constant<int, 1>{});
-            case 2: return f(t, std::integral_constant<int, 2>{});
-            case 3: return f(t, std::integral_constant<int, 3>{});
-            case 4: return f(t, std::integral_constant<int, 4>{});
-            default: return f(t, std::integral_constant<int, 8>{});
+            case 1: return gates(t, std::integral_constant<int, 1>{});
+            case 2: return gates(t, std::integral_constant<int, 2>{});
+            case 3: return gates(t, std::integral_constant<int, 3>{});
+            case 4: return gates(t, std::integral_constant<int, 4>{});
+            default: return gates(t, std::integral_constant<int, 8>{});
         }
     };
     return s->dtype == SDM_BF16 ? units(__nv_bfloat16{}) : units(0.f);
@@ -498,8 +510,8 @@ extern "C" sdm_status sdm_block_norm(const sdm_norm_shape* shape, const void* o,
     a.w_post = w_post; a.w_pre = w_pre; a.cs = channel_scale; a.r = r; a.r_ld = r_ld; a.y = y; a.y_ld = y_ld;
     const int threads = (a.rows_block * a.row_threads + 31) / 32 * 32;
     const int64_t blocks = std::min<int64_t>((a.rows + a.rows_block - 1) / a.rows_block, 152 * (2048 / threads));
-    const cudaError_t e = by_type(shape, U, [&](auto t, auto u) {
-        return launch_dependent(norm_fwd_kernel<decltype(t), decltype(u)::value>, dim3(static_cast<unsigned>(blocks)), dim3(threads), 0,
+    const cudaError_t e = by_type(shape, U, [&](auto t, auto u, auto gate) {
+        return launch_dependent(norm_fwd_kernel<decltype(t), decltype(u)::value, decltype(gate)::value>, dim3(static_cast<unsigned>(blocks)), dim3(threads), 0,
                                 reinterpret_cast<cudaStream_t>(stream), a);
     });
     return e == cudaSuccess ? SDM_OK : SDM_ERR_CUDA;
@@ -543,8 +555,8 @@ extern "C" sdm_status sdm_block_norm_backward(const sdm_norm_shape* shape, const
     const int smem = a.rows_block * kinds * a.D * static_cast<int>(sizeof(float));
     cudaError_t e = cudaSuccess;
     if (shape->rows > 0)
-        e = by_type(shape, U, [&](auto t, auto u) {
-            auto* const k = norm_bwd_kernel<decltype(t), decltype(u)::value>;
+        e = by_type(shape, U, [&](auto t, auto u, auto gate) {
+            auto* const k = norm_bwd_kernel<decltype(t), decltype(u)::value, decltype(gate)::value>;
             if (smem > 47 * 1024) {
                 const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
                 if (e != cudaSuccess) return e;
