@@ -1,12 +1,13 @@
 // sdm_embed.cu -- the rows of an embedding table for tokens, scaled, and the table's gradient by sorted tokens:
 // sdm_embed / sdm_embed_backward (include/sdm.h).
 //
-// The gradient's row v is scale times the sum of dy over the tokens with id v. The tokens are sorted by id first, stably, by one
-// cluster of 8 blocks (a radix sort of 8 bits a pass: histograms of contiguous parts, exchanged through the cluster's shared
-// memory), which also notes where every id's tokens begin and end. Then every row has one writer that adds its tokens in order:
-// no sum depends on timing. Rows with many tokens, the frequent words, are a block's: its warps take contiguous shares of the
-// tokens, joined in order, and come first, so that the many rows of zeros hide them. Bound by HBM: the table's gradient is
-// written once (float32, 131072 x 2048: 1.07 GB), the tokens' rows are read once.
+// The gradient's row v is scale times the sum of dy over the tokens with id v. The tokens are sorted by id, stably, by one
+// cluster of 8 blocks (a radix sort of 10 bits a pass: histograms of contiguous parts, exchanged through the cluster's shared
+// memory), which also lists the ids that there are and where their tokens begin and end; the other SMs write the table's zeros
+// meanwhile, a kernel that starts with the sort and ends behind it. Then every id has one writer that adds its tokens in order: no
+// sum depends on timing. Ids with many tokens, the frequent words, are a block's and come first: its warps take contiguous
+// shares of the tokens, joined in order. Bound by HBM: the table's gradient is written once (float32, 131072 x 2048: 1.07 GB),
+// the tokens' rows are read once.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -20,6 +21,7 @@ namespace {
 
 using namespace rows;
 
+constexpr int kBits = 10, kDigits = 1 << kBits;   // of a pass
 constexpr int kHeld = 4;        // rounds of a warp's tokens that stay in registers
 constexpr int kSortBlocks = 8, kSortThreads = 1024, kSortWarps = kSortThreads / 32;
 constexpr int kSlice = 512;     // columns of a warp's unit: 16 a lane
@@ -39,65 +41,74 @@ struct EmbedArgs {
     // workspace of the backward
     int32_t* key[2];
     int32_t* tok[2];
-    int2* range;        // [V]: where an id's tokens begin and end
-    int32_t* many;      // [0] their number, then the ids with more than kMany tokens
+    int32_t* end;       // [V]: where an id's tokens end, of ids that there are
+    int32_t* count;     // [2]: of the lists
+    int4* many;         // the ids with more than kMany tokens: id, where they begin and end, the first token
+    int4* few;          // the others that there are
     int passes;
 };
 
 // ---- forward ----------------------------------------------------------------------------------------------------------
-// A thread takes 4 columns of up to 4 rows' places: independent loads in flight.
+// A warp takes a token's slice of kSlice columns, 16 a lane, and the next one's id ahead.
 template <typename TT, typename T>
-__global__ void __launch_bounds__(256) embed_kernel(const __grid_constant__ EmbedArgs a, int64_t units, int per) {
+__global__ void __launch_bounds__(256) embed_kernel(const __grid_constant__ EmbedArgs a) {
     start_dependent();
-    const int64_t stride = gridDim.x * int64_t(256);
-    for (int64_t base = blockIdx.x * int64_t(256) + threadIdx.x; base < units; base += 4 * stride) {
+    const int lane = threadIdx.x & 31, slices = (a.D + kSlice - 1) / kSlice;
+    const int64_t units = a.tokens * slices, stride = gridDim.x * int64_t(8);
+    int64_t u = blockIdx.x * int64_t(8) + (threadIdx.x >> 5), t = u / slices;
+    int next = u < units ? a.ids[t] : 0;
+    for (; u < units; u += stride) {
+        const int id = next, c = static_cast<int>(u - t * slices) * kSlice + 4 * lane;
+        const int64_t row = t;
+        const bool real = id >= 0 && id < a.V;
+        if (id >= a.V && lane == 0 && a.status != nullptr) atomicOr(a.status, SDM_DEV_BAD_TOKEN);
         Raw4<TT> v[4];
-        int id[4];
-        int64_t row[4];
-        int c[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int64_t u = base + i * stride;
-            row[i] = u < units ? u / per : -1;
-            c[i] = static_cast<int>(u - row[i] * per) * 4;
-            id[i] = row[i] >= 0 ? a.ids[row[i]] : -1;
+        for (int q = 0; q < 4; ++q) {
+            v[q].zero();
+            if (real && c + 128 * q < a.D) ld_plain(v[q], static_cast<const TT*>(a.table) + id * a.t_ld + c + 128 * q);
+        }
+        if (u + stride < units) {
+            t = (u + stride) / slices;
+            next = a.ids[t];
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[i].zero();
-            if (id[i] >= 0 && id[i] < a.V) ld_plain(v[i], static_cast<const TT*>(a.table) + id[i] * a.t_ld + c[i]);
-            else if (id[i] >= a.V && a.status != nullptr) atomicOr(a.status, SDM_DEV_BAD_TOKEN);
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if (row[i] < 0) continue;
-            float x[4];
-            v[i].get(x);
-            const bool real = id[i] >= 0 && id[i] < a.V;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) x[e] = real ? x[e] * a.scale : 0.f;
-            st4(static_cast<T*>(a.y) + row[i] * a.y_ld + c[i], x);
-        }
+        for (int q = 0; q < 4; ++q)
+            if (c + 128 * q < a.D)
+                st4(static_cast<T*>(a.y) + row * a.y_ld + c + 128 * q, real ? mul4(quad(v[q]), quad(a.scale)) : quad(0.f));
     }
+}
+
+// The lanes whose digit (-1: none) is this lane's: a ballot for each bit.
+__device__ __forceinline__ uint32_t same_digit(int d) {
+    uint32_t m = __ballot_sync(kFull, d >= 0);
+#pragma unroll
+    for (int b = 0; b < kBits; ++b) {
+        const uint32_t v = __ballot_sync(kFull, d >> b & 1);
+        m &= d >> b & 1 ? v : ~v;
+    }
+    return d >= 0 ? m : 0u;
 }
 
 // ---- the sort -----------------------------------------------------------------------------------------------------------
 __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const __grid_constant__ EmbedArgs a) {
-    __shared__ int hist[kSortWarps][256];   // a warp's counts, then the places of the warps before it
-    __shared__ int total[256];              // of this block's part, which the cluster's other blocks read
-    __shared__ int first[256];
-    __shared__ int carry[8];
+    extern __shared__ int hist_of[];
+    int (*const hist)[kDigits] = reinterpret_cast<int (*)[kDigits]>(hist_of);   // a warp's counts, then the places of the warps before it
+    __shared__ int total[kDigits];          // of this block's part, which the cluster's other blocks read
+    __shared__ int first[kDigits];
+    __shared__ int carry[kSortWarps];
+    static_assert(kDigits == kSortThreads, "a thread for each digit");
     start_dependent();
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");   // the zeros may start: what came before this sort is done
     const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
     const int rank = static_cast<int>(cluster_rank());
     const int n = static_cast<int>(a.tokens);
     // contiguous parts, so that their order is the tokens'
     const int64_t share = (static_cast<int64_t>(n) + kSortBlocks * kSortWarps - 1) / (kSortBlocks * kSortWarps);
     const int64_t lo = min((static_cast<int64_t>(rank) * kSortWarps + w) * share, int64_t(n)), hi = min(lo + share, int64_t(n));
-    for (int64_t i = rank * int64_t(kSortThreads) + tid; i < a.V; i += kSortBlocks * kSortThreads) a.range[i] = make_int2(0, 0);
-    if (rank == 0 && tid == 0) a.many[0] = 0;
+    if (rank == 0 && tid == 0) a.count[0] = a.count[1] = 0;
     for (int pass = 0; pass < a.passes; ++pass) {
-        const int shift = 8 * pass;
+        const int shift = kBits * pass;
         const int32_t* const kin = a.key[(pass + 1) & 1];
         const int32_t* const tin = a.tok[(pass + 1) & 1];
         int32_t* const kout = a.key[pass & 1];
@@ -119,14 +130,14 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const __grid_c
         };
         int k0[kHeld], t0[kHeld];
         round_of(lo + lane, k0, t0);
-        for (int i = lane; i < 256; i += 32) hist[w][i] = 0;
+        for (int i = lane; i < kDigits; i += 32) hist[w][i] = 0;
         __syncwarp();
         auto count = [&](const int (&k)[kHeld]) {
 #pragma unroll
             for (int r = 0; r < kHeld; ++r) {
-                const int d = k[r] >= 0 ? (k[r] >> shift) & 255 : 256;
-                const uint32_t same = __match_any_sync(kFull, d);
-                if (d < 256 && (same & ((1u << lane) - 1)) == 0) hist[w][d] += __popc(same);
+                const int d = k[r] >= 0 ? (k[r] >> shift) & (kDigits - 1) : -1;
+                const uint32_t same = same_digit(d);
+                if (d >= 0 && (same & ((1u << lane) - 1)) == 0) hist[w][d] += __popc(same);
                 __syncwarp();
             }
         };
@@ -137,7 +148,7 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const __grid_c
             count(k);
         }
         __syncthreads();
-        if (tid < 256) {
+        {
             int c[kSortWarps], sum = 0;
 #pragma unroll
             for (int i = 0; i < kSortWarps; ++i) c[i] = hist[i][tid];
@@ -151,7 +162,7 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const __grid_c
         cluster_arrive();
         cluster_wait();
         int all = 0, before = 0;
-        if (tid < 256) {
+        {
             int c[kSortBlocks];
 #pragma unroll
             for (int r = 0; r < kSortBlocks; ++r)
@@ -161,7 +172,7 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const __grid_c
                 all += c[r];
                 before += r < rank ? c[r] : 0;
             }
-            int run = all;   // the digits' places: a scan over 256
+            int run = all;   // the digits' places: a scan over them
             for (int m = 1; m < 32; m *= 2) {
                 const int o = __shfl_up_sync(kFull, run, m);
                 if (lane >= m) run += o;
@@ -170,24 +181,25 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const __grid_c
             first[tid] = run - all + before;
         }
         __syncthreads();
-        if (tid < 256) {
-            int c = 0;
-            for (int i = 0; i < w; ++i) c += carry[i];
+        {
+            int c = lane < w ? carry[lane] : 0;
+#pragma unroll
+            for (int m = 16; m > 0; m /= 2) c += __shfl_xor_sync(kFull, c, m);
             first[tid] += c;
         }
         __syncthreads();
         auto place = [&](const int (&k)[kHeld], const int (&t)[kHeld]) {
 #pragma unroll
             for (int r = 0; r < kHeld; ++r) {
-                const int d = k[r] >= 0 ? (k[r] >> shift) & 255 : 256;
-                const uint32_t same = __match_any_sync(kFull, d);
+                const int d = k[r] >= 0 ? (k[r] >> shift) & (kDigits - 1) : -1;
+                const uint32_t same = same_digit(d);
                 const int ahead = __popc(same & ((1u << lane) - 1));
                 int at = 0;
-                if (d < 256) at = first[d] + hist[w][d] + ahead;
+                if (d >= 0) at = first[d] + hist[w][d] + ahead;
                 __syncwarp();
-                if (d < 256 && ahead == 0) hist[w][d] += __popc(same);
+                if (d >= 0 && ahead == 0) hist[w][d] += __popc(same);
                 __syncwarp();
-                if (d < 256) {
+                if (d >= 0) {
                     kout[at] = k[r];
                     tout[at] = t[r];
                 }
@@ -204,51 +216,84 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const __grid_c
         cluster_wait();
     }
     const int32_t* const key = a.key[(a.passes + 1) & 1];
+    const int32_t* const tok = a.tok[(a.passes + 1) & 1];
     for (int64_t i = rank * int64_t(kSortThreads) + tid; i < n; i += kSortBlocks * kSortThreads) {
         const int k = __ldcg(key + i);
         if (k >= a.V) continue;
-        if (i == 0 || __ldcg(key + i - 1) != k) a.range[k].x = static_cast<int>(i);
-        if (i + 1 == n || __ldcg(key + i + 1) != k) a.range[k].y = static_cast<int>(i) + 1;
+        if (i + 1 == n || __ldcg(key + i + 1) != k) a.end[k] = static_cast<int>(i) + 1;
     }
     cluster_arrive();
     cluster_wait();
-    for (int64_t i = rank * int64_t(kSortThreads) + tid; i < n; i += kSortBlocks * kSortThreads) {
-        const int k = __ldcg(key + i);
-        if (k >= a.V || !(i == 0 || __ldcg(key + i - 1) != k)) continue;
-        if (__ldcg(&a.range[k].y) - static_cast<int>(i) > kMany) a.many[1 + atomicAdd(a.many, 1)] = k;   // in whatever order
+    for (int64_t i = rank * int64_t(kSortThreads) + tid; i - lane < n; i += kSortBlocks * kSortThreads) {
+        const int k = i < n ? __ldcg(key + i) : a.V;
+        const bool head = k < a.V && (i == 0 || __ldcg(key + i - 1) != k);
+        const int end = head ? __ldcg(a.end + k) : 0;
+        const bool many = head && end - static_cast<int>(i) > kMany;
+        // the lists' order is whatever it is; a warp takes its places together
+#pragma unroll
+        for (int list = 0; list < 2; ++list) {
+            const bool mine = head && many == (list == 0);
+            const uint32_t m = __ballot_sync(kFull, mine);
+            int at = 0;
+            if (lane == 0 && m != 0) at = atomicAdd(a.count + list, __popc(m));
+            at = __shfl_sync(kFull, at, 0) + __popc(m & ((1u << lane) - 1));
+            if (mine) (list == 0 ? a.many : a.few)[at] = make_int4(k, static_cast<int>(i), end, __ldcg(tok + i));
+        }
     }
 }
 
+// ---- the zeros --------------------------------------------------------------------------------------------------------------
+// Rows of zeros, 16 bytes a store where rows lie without gaps. It starts with the sort and waits for its end before its own, so that
+// what follows has both behind it.
+template <typename TT>
+__global__ void __launch_bounds__(256) embed_zero_kernel(const __grid_constant__ EmbedArgs a) {
+    const int64_t stride = gridDim.x * int64_t(256), i0 = blockIdx.x * int64_t(256) + threadIdx.x;
+    const Quad none = quad(0.f);
+    if (a.t_ld == a.D && sizeof(TT) == 2 && reinterpret_cast<uintptr_t>(a.dtable) % 16 == 0) {
+        const int64_t n = static_cast<int64_t>(a.V) * a.D / 8;
+        for (int64_t i = i0; i < n; i += stride) static_cast<uint4*>(a.dtable)[i] = make_uint4(0, 0, 0, 0);
+        if (i0 == 0)
+            for (int64_t i = n * 8; i < static_cast<int64_t>(a.V) * a.D; i += 4) st4(static_cast<TT*>(a.dtable) + i, none);
+    } else if (a.t_ld == a.D) {
+        const int64_t n = static_cast<int64_t>(a.V) * a.D / 4;
+        for (int64_t i = i0; i < n; i += stride) st4(static_cast<TT*>(a.dtable) + 4 * i, none);
+    } else {
+        const int64_t per = a.D / 4, n = a.V * per;
+        for (int64_t i = i0; i < n; i += stride) st4(static_cast<TT*>(a.dtable) + i / per * a.t_ld + i % per * 4, none);
+    }
+    start_dependent();
+}
+
 // ---- the sums ------------------------------------------------------------------------------------------------------------
-// acc += dy of the tokens tok[b .. e), in order, at a lane's columns c0 + 4 lane + 128 i
-template <typename T>
-__device__ __forceinline__ void add_tokens(const EmbedArgs& a, const int32_t* tok, int b, int e, int c, int n, Quad (&acc)[4]) {
-    constexpr int kFlight = 4;
-    for (int i = b; i < e; i += kFlight) {
-        Raw4<T> v[kFlight][4];
+// acc += dy of the tokens tok[b .. e), in order, at a lane's columns c + 128 q for q below n; F tokens on their way at once. The first
+// token is known.
+template <typename T, int Q, int F>
+__device__ __forceinline__ void add_tokens(const EmbedArgs& a, const int32_t* tok, int first, int b, int e, int c, int n, Quad (&acc)[Q]) {
+    for (int i = b; i < e; i += F) {
+        Raw4<T> v[F][Q];
 #pragma unroll
-        for (int f = 0; f < kFlight; ++f) {
-            const int64_t t = i + f < e ? tok[i + f] : -1;
+        for (int f = 0; f < F; ++f) {
+            const int64_t t = i + f >= e ? -1 : i + f == b ? first : tok[i + f];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
+            for (int q = 0; q < Q; ++q) {
                 v[f][q].zero();
                 if (t >= 0 && q < n) ld_plain(v[f][q], static_cast<const T*>(a.dy) + t * a.y_ld + c + 128 * q);
             }
         }
 #pragma unroll
-        for (int f = 0; f < kFlight; ++f)
+        for (int f = 0; f < F; ++f)
 #pragma unroll
-            for (int q = 0; q < 4; ++q) acc[q] = add4(acc[q], quad(v[f][q]));
+            for (int q = 0; q < Q; ++q) acc[q] = add4(acc[q], quad(v[f][q]));
     }
 }
 
 // The sums, scaled, to row v: n of a lane's four places of 4 columns lie in it.
-template <typename TT>
-__device__ __forceinline__ void put_row(const EmbedArgs& a, int v, int c, int n, const Quad (&acc)[4]) {
+template <typename TT, int Q>
+__device__ __forceinline__ void put_row(const EmbedArgs& a, int v, int c, int n, const Quad (&acc)[Q]) {
     TT* const out = static_cast<TT*>(a.dtable) + v * a.t_ld + c;
     const Quad s = quad(a.scale);
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
+    for (int q = 0; q < Q; ++q) {
         if (q >= n) continue;
         Quad x = mul4(acc[q], s);
         if (a.accumulate) {
@@ -260,41 +305,52 @@ __device__ __forceinline__ void put_row(const EmbedArgs& a, int v, int c, int n,
     }
 }
 
+// A frequent word's slice of Q * 128 columns: the block's warps take shares of the tokens.
+template <typename TT, typename T, int Q, int F>
+__device__ __forceinline__ void block_row(const EmbedArgs& a, const int32_t* tok, float (*part)[kSlice], int64_t u, int slices) {
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    const int4 r = a.many[u / slices];
+    const int c = static_cast<int>(u % slices) * Q * 128 + 4 * lane, n = max(0, min(Q, (a.D - c + 127) / 128));
+    const int share = (r.z - r.y + kWarps - 1) / kWarps, b = min(r.y + w * share, r.z);
+    Quad acc[Q] = {};
+    add_tokens<T, Q, F>(a, tok, b < r.z ? tok[b] : 0, b, min(b + share, r.z), c, n, acc);
+#pragma unroll
+    for (int q = 0; q < Q; ++q) st4(&part[w][4 * lane + 128 * q], acc[q]);
+    __syncthreads();
+    if (w == 0) {
+        for (int i = 1; i < kWarps; ++i)
+#pragma unroll
+            for (int q = 0; q < Q; ++q) acc[q] = add4(acc[q], quad_at(&part[i][4 * lane + 128 * q]));
+        put_row<TT>(a, r.x, c, n, acc);
+    }
+    __syncthreads();
+}
+
 template <typename TT, typename T>
 __global__ void __launch_bounds__(kThreads, 2) embed_bwd_kernel(const __grid_constant__ EmbedArgs a) {
     __shared__ __align__(16) float part[kWarps][kSlice];
     start_dependent();
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-    const int slices = (a.D + kSlice - 1) / kSlice;
+    const int slices = (a.D + kSlice - 1) / kSlice, thin = (a.D + 127) / 128;
     const int32_t* const tok = a.tok[(a.passes + 1) & 1];
-    auto places = [&](int c0) { return max(0, min(4, (a.D - c0 - 4 * lane + 127) / 128)); };
-    const int64_t many = static_cast<int64_t>(a.many[0]) * slices;
-    for (int64_t u = blockIdx.x; u < many; u += gridDim.x) {
-        const int v = a.many[1 + u / slices], c0 = static_cast<int>(u % slices) * kSlice, c = c0 + 4 * lane, n = places(c0);
-        const int2 r = a.range[v];
-        const int share = (r.y - r.x + kWarps - 1) / kWarps, b = min(r.x + w * share, r.y);
+    constexpr int F = sizeof(T) == 2 ? 3 : 2;   // tokens of 512 columns on their way: what 64 registers hold
+    // frequent words in slices of 128 columns with 4 F tokens on their way, while those do not outnumber the blocks four times
+    const int64_t many = a.count[0];
+    if (many * thin <= 4 * gridDim.x)
+        for (int64_t u = blockIdx.x; u < many * thin; u += gridDim.x) block_row<TT, T, 1, 4 * F>(a, tok, part, u, thin);
+    else
+        for (int64_t u = blockIdx.x; u < many * slices; u += gridDim.x) block_row<TT, T, 4, F>(a, tok, part, u, slices);
+    // from the last block on: the first ones may still be at the frequent words. The next word is known ahead.
+    const int64_t few = static_cast<int64_t>(a.count[1]) * slices, stride = static_cast<int64_t>(gridDim.x) * kWarps;
+    int64_t u = static_cast<int64_t>(gridDim.x - 1 - blockIdx.x) * kWarps + w;
+    int4 next = u < few ? a.few[u / slices] : make_int4(0, 0, 0, 0);
+    for (; u < few; u += stride) {
+        const int4 r = next;
+        const int c = static_cast<int>(u % slices) * kSlice + 4 * lane, n = max(0, min(4, (a.D - c + 127) / 128));
+        if (u + stride < few) next = a.few[(u + stride) / slices];
         Quad acc[4] = {};
-        add_tokens<T>(a, tok, b, min(b + share, r.y), c, n, acc);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) st4(&part[w][4 * lane + 128 * q], acc[q]);
-        __syncthreads();
-        if (w == 0) {
-            for (int i = 1; i < kWarps; ++i)
-#pragma unroll
-                for (int q = 0; q < 4; ++q) acc[q] = add4(acc[q], quad_at(&part[i][4 * lane + 128 * q]));
-            put_row<TT>(a, v, c, n, acc);
-        }
-        __syncthreads();
-    }
-    const int64_t units = static_cast<int64_t>(a.V) * slices, stride = static_cast<int64_t>(gridDim.x) * kWarps;
-    for (int64_t u = static_cast<int64_t>(blockIdx.x) * kWarps + w; u < units; u += stride) {
-        const int v = static_cast<int>(u / slices), c0 = static_cast<int>(u - static_cast<int64_t>(v) * slices) * kSlice;
-        const int2 r = a.range[v];
-        if (r.y - r.x > kMany || (a.accumulate && r.y == r.x)) continue;
-        const int c = c0 + 4 * lane, n = places(c0);
-        Quad acc[4] = {};
-        if (r.y > r.x) add_tokens<T>(a, tok, r.x, r.y, c, n, acc);
-        put_row<TT>(a, v, c, n, acc);
+        add_tokens<T, 4, F>(a, tok, r.w, r.y, r.z, c, n, acc);
+        put_row<TT>(a, r.x, c, n, acc);
     }
 }
 
@@ -327,7 +383,7 @@ void fill(const sdm_embed_shape* s, EmbedArgs* a) {
     a->D = s->D;
     a->scale = s->scale;
     a->passes = 1;
-    while (a->passes < 4 && s->V >> (8 * a->passes) != 0) ++a->passes;   // keys 0 .. V
+    while (s->V >> (kBits * a->passes) != 0) ++a->passes;   // keys 0 .. V
 }
 
 int64_t up(int64_t n) { return (n + 255) / 256 * 256; }
@@ -346,7 +402,8 @@ using namespace sdm;
 extern "C" size_t sdm_embed_workspace_bytes(const sdm_embed_shape* shape) {
     if (check(shape) != SDM_OK) return 0;
     const int64_t T = shape->tokens;
-    return static_cast<size_t>(4 * up(4 * T) + up(8 * static_cast<int64_t>(shape->V)) + up(4 * (T / kMany + 2)));
+    return static_cast<size_t>(4 * up(4 * T) + up(4 * static_cast<int64_t>(shape->V)) + 256 + up(16 * (T / kMany + 1)) +
+                               up(16 * std::min<int64_t>(T, shape->V)));
 }
 
 extern "C" sdm_status sdm_embed(const sdm_embed_shape* shape, const int32_t* ids, const void* table, int64_t table_ld, void* y,
@@ -361,11 +418,11 @@ extern "C" sdm_status sdm_embed(const sdm_embed_shape* shape, const int32_t* ids
     EmbedArgs a;
     fill(shape, &a);
     a.ids = ids; a.table = table; a.t_ld = table_ld; a.y = y; a.y_ld = y_ld; a.status = status;
-    const int64_t units = shape->tokens * (shape->D / 4);
-    const int64_t blocks = std::min<int64_t>((units + 255) / 256, 152 * 8);
+    const int64_t units = shape->tokens * ((shape->D + kSlice - 1) / kSlice);
+    const int64_t blocks = std::min<int64_t>((units + 7) / 8, 152 * 8);
     const cudaError_t e = by_type(shape, [&](auto tt, auto t) {
         return launch_dependent(embed_kernel<decltype(tt), decltype(t)>, dim3(static_cast<unsigned>(blocks)), dim3(256), 0,
-                                reinterpret_cast<cudaStream_t>(stream), a, units, shape->D / 4);
+                                reinterpret_cast<cudaStream_t>(stream), a);
     });
     return e == cudaSuccess ? SDM_OK : SDM_ERR_CUDA;
 }
@@ -393,14 +450,25 @@ extern "C" sdm_status sdm_embed_backward(const sdm_embed_shape* shape, const int
         a.tok[i] = reinterpret_cast<int32_t*>(w);
         w += up(4 * shape->tokens);
     }
-    a.range = reinterpret_cast<int2*>(w);
-    w += up(8 * static_cast<int64_t>(shape->V));
-    a.many = reinterpret_cast<int32_t*>(w);
+    a.end = reinterpret_cast<int32_t*>(w);
+    w += up(4 * static_cast<int64_t>(shape->V));
+    a.count = reinterpret_cast<int32_t*>(w);
+    w += 256;
+    a.many = reinterpret_cast<int4*>(w);
+    w += up(16 * (shape->tokens / kMany + 1));
+    a.few = reinterpret_cast<int4*>(w);
     const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-    cudaError_t e = launch_cluster(embed_sort_kernel, dim3(kSortBlocks), dim3(kSortThreads), kSortBlocks, cs, a);
-    const int64_t units = static_cast<int64_t>(shape->V) * ((shape->D + kSlice - 1) / kSlice);
-    const int64_t blocks = std::min<int64_t>((units + kWarps - 1) / kWarps, 152 * 2);
-    if (e == cudaSuccess)
+    constexpr int smem = kSortWarps * kDigits * static_cast<int>(sizeof(int));
+    cudaError_t e = cudaFuncSetAttribute(embed_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess) e = launch_cluster_smem(embed_sort_kernel, dim3(kSortBlocks), dim3(kSortThreads), kSortBlocks, smem, cs, a);
+    if (e == cudaSuccess && !accumulate) {
+        const int64_t blocks = std::min<int64_t>((static_cast<int64_t>(shape->V) * (shape->D / 4) + 1023) / 1024, 144 * 8);
+        e = launch_dependent(shape->table_dtype == SDM_BF16 ? embed_zero_kernel<__nv_bfloat16> : embed_zero_kernel<float>,
+                             dim3(static_cast<unsigned>(blocks)), dim3(256), 0, cs, a);
+    }
+    const int64_t units = shape->tokens * ((shape->D + kSlice - 1) / kSlice);
+    const int64_t blocks = std::max<int64_t>(1, std::min<int64_t>((units + kWarps - 1) / kWarps, 152 * 2));
+    if (e == cudaSuccess && shape->tokens > 0)
         e = by_type(shape, [&](auto tt, auto t) {
             return launch_dependent(embed_bwd_kernel<decltype(tt), decltype(t)>, dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0, cs, a);
         });

@@ -24,7 +24,7 @@ namespace {
 
 using namespace rows;
 
-constexpr int kMaxThreads = 512;
+constexpr int kNormThreads = 512;
 constexpr int kMaxCols = 16384;
 constexpr int kPartBlocks = 304;   // blocks of the backward at most (two for each of 152 SMs): a row of partial sums each
 
@@ -54,12 +54,12 @@ struct NormArgs {
     float eps, scale;
 };
 
-// Sums over a row's and over a group's threads. Beyond a warp they meet in shared memory; two buffers take turns, so that one
-// barrier a call suffices.
+// Sums of NR values over a row's threads and of NG over a group's. Beyond a warp they meet in shared memory, a warp's sum a lane;
+// two buffers take turns, so that one barrier a call suffices.
 struct Sums {
-    float (*red)[3][kMaxThreads / 32];
+    float (*red)[3][kNormThreads / 32];
     int turn, lane, warp, row_warp, row_warps, group_warp, group_warps, row_width, group_width;
-    __device__ __forceinline__ Sums(const NormArgs& a, float (*shared)[3][kMaxThreads / 32]) : red(shared), turn(0) {
+    __device__ __forceinline__ Sums(const NormArgs& a, float (*shared)[3][kNormThreads / 32]) : red(shared), turn(0) {
         lane = threadIdx.x & 31;
         warp = threadIdx.x >> 5;
         row_width = min(a.row_threads, 32);
@@ -71,45 +71,144 @@ struct Sums {
         group_warp = row_warp + (warp - row_warp) / group_warps * group_warps;
     }
     template <int N>
-    __device__ __forceinline__ void row_and_group(float (&row)[N], float& group) {
-        for (int m = row_width / 2; m > 0; m /= 2)
+    __device__ __forceinline__ static void across(float (&v)[N], int width) {
+        if (width == 32) {
 #pragma unroll
-            for (int i = 0; i < N; ++i) row[i] += __shfl_xor_sync(kFull, row[i], m);
-        for (int m = group_width / 2; m > 0; m /= 2) group += __shfl_xor_sync(kFull, group, m);
+            for (int m = 16; m > 0; m /= 2)
+#pragma unroll
+                for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(kFull, v[i], m);
+        } else {
+            for (int m = width / 2; m > 0; m /= 2)
+#pragma unroll
+                for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(kFull, v[i], m);
+        }
+    }
+    template <int N>
+    __device__ __forceinline__ void meet(float (&v)[N], int first, int warps, int at) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = lane < warps ? red[turn][at + i][first + lane] : 0.f;
+#pragma unroll
+        for (int m = kNormThreads / 64; m > 0; m /= 2)
+#pragma unroll
+            for (int i = 0; i < N; ++i) v[i] += __shfl_xor_sync(kFull, v[i], m);
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = __shfl_sync(kFull, v[i], 0);
+    }
+    template <int N>
+    __device__ __forceinline__ void row(float (&v)[N]) {
+        across(v, row_width);
         if (row_warps == 1) return;
         if (lane == 0) {
 #pragma unroll
-            for (int i = 0; i < N; ++i) red[turn][i][warp] = row[i];
-            red[turn][2][warp] = group;
+            for (int i = 0; i < N; ++i) red[turn][i][warp] = v[i];
         }
         __syncthreads();
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            row[i] = 0.f;
-            for (int w = 0; w < row_warps; ++w) row[i] += red[turn][i][row_warp + w];
-        }
-        if (group_warps > 1) {
-            group = 0.f;
-            for (int w = 0; w < group_warps; ++w) group += red[turn][2][group_warp + w];
-        }
+        meet(v, row_warp, row_warps, 0);
         turn ^= 1;
+    }
+    __device__ __forceinline__ void group(float& x) {
+        float v[1] = {x};
+        across(v, group_width);
+        if (group_warps > 1) {
+            if (lane == 0) red[turn][2][warp] = v[0];
+            __syncthreads();
+            meet(v, group_warp, group_warps, 2);
+            turn ^= 1;
+        }
+        x = v[0];
+    }
+    __device__ __forceinline__ void row_and_group(float (&r)[2], float& x) {
+        float v[1] = {x};
+        across(r, row_width);
+        across(v, group_width);
+        if (row_warps > 1) {
+            if (lane == 0) {
+                red[turn][0][warp] = r[0];
+                red[turn][1][warp] = r[1];
+                red[turn][2][warp] = v[0];
+            }
+            __syncthreads();
+            meet(r, row_warp, row_warps, 0);
+            if (group_warps > 1) meet(v, group_warp, group_warps, 2);
+            turn ^= 1;
+        }
+        x = v[0];
     }
 };
 
-// act and its slope: GATE 1 sigmoid, 2 z sigmoid(z). bfloat16 rows take the hardware's exponential and division, which are off by
-// 2^-21 (|z| + 1) at most where the rows are 2^-8 apart; float32 rows expf and a rounded division.
+// act and its slope: GATE 1 sigmoid, 2 z sigmoid(z); at infinite z their limits, NaN stays. bfloat16 rows take the hardware's
+// exponential and reciprocal, off by 2^-21 (|z| + 1) at most where the rows are 2^-8 apart, and cut z off at -80 and, in the
+// slope, at 80, where what is left is below 2^-115; float32 rows take expf and a rounded division.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float o;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(o) : "f"(a), "f"(b));
+    return o;
+}
+__device__ __forceinline__ float min_nan(float a, float b) {
+    float o;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(o) : "f"(a), "f"(b));
+    return o;
+}
 template <typename T, int GATE>
 __device__ __forceinline__ void gate_of(float z, float& act, float& slope) {
-    const float t = sizeof(T) == 2 ? __expf(-fabsf(z)) : expf(-fabsf(z));
-    const float s = sizeof(T) == 2 ? __fdividef(1.f, 1.f + t) : 1.f / (1.f + t);
-    const float ts = t * s, sg = z >= 0.f ? s : ts, rest = z >= 0.f ? ts : s;   // sigmoid and 1 - sigmoid (NaN stays: t is)
+    float sg, rest, zc = z;   // sigmoid, 1 - sigmoid
+    if (sizeof(T) == 2) {
+        z = max_nan(z, -80.f);
+        zc = min_nan(z, 80.f);
+        float e;
+        asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(zc * -1.44269504088896341f));
+        asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(sg) : "f"(1.f + e));
+        rest = e * sg;
+    } else {
+        const float t = expf(-fabsf(z)), s = 1.f / (1.f + t);
+        sg = z >= 0.f ? s : t * s;
+        rest = z >= 0.f ? t * s : s;
+        if (t == 0.f) {
+            z = sg == 0.f ? 0.f : z;
+            zc = 0.f;
+        }
+    }
     if (GATE == 1) {
         act = sg;
         slope = sg * rest;
-    } else {   // at infinite z their limits
-        act = sg == 0.f ? 0.f : z * sg;
-        slope = ts == 0.f ? sg : fmaf(act, rest, sg);
+    } else {
+        act = z * sg;
+        slope = fmaf(zc * sg, rest, sg);
     }
+}
+template <typename T, int GATE>
+__device__ __forceinline__ void gates_of(const Raw4<T>& z, Quad& act, Quad& slope) {
+    float v[4], a[4], s[4];
+    z.get(v);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) gate_of<T, GATE>(v[e], a[e], s[e]);
+    act = quad(a);
+    slope = quad(s);
+}
+
+// Four values in the rows' type, as they are stored
+__device__ __forceinline__ Raw4<float> rounded(const Quad& q, float) {
+    float v[4];
+    floats(q, v);
+    Raw4<float> r;
+    r.v = make_float4(v[0], v[1], v[2], v[3]);
+    return r;
+}
+__device__ __forceinline__ Raw4<__nv_bfloat16> rounded(const Quad& q, __nv_bfloat16) {
+    float v[4];
+    floats(q, v);
+    Raw4<__nv_bfloat16> r;
+    const __nv_bfloat162 lo = __floats2bfloat162_rn(v[0], v[1]), hi = __floats2bfloat162_rn(v[2], v[3]);
+    r.v.x = *reinterpret_cast<const uint32_t*>(&lo);
+    r.v.y = *reinterpret_cast<const uint32_t*>(&hi);
+    return r;
+}
+__device__ __forceinline__ void put(float* p, const Raw4<float>& r) { *reinterpret_cast<float4*>(p) = r.v; }
+__device__ __forceinline__ void put(__nv_bfloat16* p, const Raw4<__nv_bfloat16>& r) { *reinterpret_cast<uint2*>(p) = r.v; }
+__device__ __forceinline__ float sum_of(const Quad& q) {
+    float v[4];
+    floats(q, v);
+    return (v[0] + v[1]) + (v[2] + v[3]);
 }
 
 // A thread's units: U places of 4 columns, `lanes` units apart within its group.
@@ -132,99 +231,81 @@ struct Columns {
     }
 };
 
-__device__ __forceinline__ void weights(const float* w, int c, float (&o)[4]) {
-    if (w == nullptr) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) o[e] = 1.f;
-    } else {
-        load4(w + c).get(o);
-    }
-}
+__device__ __forceinline__ Quad weights(const float* w, int c) { return w == nullptr ? quad(1.f) : quad(load4(w + c)); }
 template <typename T>
 __device__ __forceinline__ void take(Raw4<T>& r, const void* p, int64_t row, int64_t ld, int c, bool on) {
     r.zero();
     if (on) ld_plain(r, static_cast<const T*>(p) + row * ld + c);
 }
 
-template <typename T, int U, int GATE>
-__global__ void __launch_bounds__(kMaxThreads) norm_fwd_kernel(const __grid_constant__ NormArgs a) {
-    __shared__ float red[2][3][kMaxThreads / 32];
+// MAXT: threads of a block at most
+template <typename T, int U, int GATE, int MAXT>
+__global__ void __launch_bounds__(MAXT, MAXT == 256 ? (sizeof(T) == 2 ? 3 : 2) : 1) norm_fwd_kernel(const __grid_constant__ NormArgs a) {
+    __shared__ float red[2][3][kNormThreads / 32];
     start_dependent();
     const Columns<U> col(a);
     Sums sums(a, red);
-    for (int64_t base = blockIdx.x * int64_t(a.rows_block); base < a.rows; base += gridDim.x * int64_t(a.rows_block)) {
+    const int64_t stride = gridDim.x * int64_t(a.rows_block);
+    Raw4<T> o[U], z[U], x[U];
+    auto take_row = [&](int64_t row, int i) {
+        const bool on = row < a.rows && col.on[i];
+        take(o[i], a.o, row, a.o_ld, col.c[i], on);
+        take(z[i], a.z, row, a.z_ld, col.c[i], on && GATE != 0);
+        take(x[i], a.x, row, a.x_ld, col.c[i], on && a.x != nullptr);
+    };
+#pragma unroll
+    for (int i = 0; i < U; ++i) take_row(blockIdx.x * int64_t(a.rows_block) + col.row, i);
+    for (int64_t base = blockIdx.x * int64_t(a.rows_block); base < a.rows; base += stride) {
         const int64_t row = base + col.row;
         const bool here = row < a.rows;
-        Raw4<T> o[U], z[U], x[U];
-#pragma unroll
-        for (int i = 0; i < U; ++i) {
-            const bool on = here && col.on[i];
-            take(o[i], a.o, row, a.o_ld, col.c[i], on);
-            take(z[i], a.z, row, a.z_ld, col.c[i], on && GATE != 0);
-            take(x[i], a.x, row, a.x_ld, col.c[i], on && a.x != nullptr);
-        }
         float p = 1.f;
         if (a.post) {
-            float none[1] = {}, s = 0.f;
+            Quad sq = quad(0.f);
 #pragma unroll
-            for (int i = 0; i < U; ++i) {
-                float v[4];
-                o[i].get(v);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) s = fmaf(v[e], v[e], s);
-            }
-            sums.row_and_group(none, s);
+            for (int i = 0; i < U; ++i) sq = fma4(quad(o[i]), quad(o[i]), sq);
+            float s = sum_of(sq);
+            sums.group(s);
             p = rsqrtf(s / a.G + a.eps);
         }
-        float r[U][4], s[1] = {};
+        Raw4<T> r[U];
+        Quad sq = quad(0.f);
 #pragma unroll
         for (int i = 0; i < U; ++i) {
-            float ov[4], zv[4], wv[4], cv[4];
-            o[i].get(ov);
-            z[i].get(zv);
-            x[i].get(r[i]);
-            if (a.post) weights(a.w_post, col.w[i], wv);
-            weights(a.cs, col.c[i], cv);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                float n = a.post ? ov[e] * p * wv[e] : ov[e];
-                if constexpr (GATE != 0) {
-                    float act, slope;
-                    gate_of<T, GATE>(zv[e], act, slope);
-                    n *= act;
-                }
-                r[i][e] = fmaf(a.scale * cv[e], n, r[i][e]);
+            Quad n = quad(o[i]);
+            if (a.post) n = mul4(mul4(n, quad(p)), weights(a.w_post, col.w[i]));
+            if constexpr (GATE != 0) {
+                Quad act, slope;
+                gates_of<T, GATE>(z[i], act, slope);
+                n = mul4(n, act);
             }
-            if (sizeof(T) == 2) {   // as it is stored
-#pragma unroll
-                for (int e = 0; e < 4; ++e) r[i][e] = __bfloat162float(__float2bfloat16_rn(r[i][e]));
-            }
-            if (here && col.on[i]) st4(static_cast<T*>(a.r) + row * a.r_ld + col.c[i], r[i]);
-            else r[i][0] = r[i][1] = r[i][2] = r[i][3] = 0.f;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) s[0] = fmaf(r[i][e], r[i][e], s[0]);
+            Quad k = quad(a.scale);
+            if (a.cs != nullptr) k = mul4(k, weights(a.cs, col.c[i]));
+            r[i] = rounded(fma4(k, n, quad(x[i])), T{});   // as it is stored
+            if (here && col.on[i]) put(static_cast<T*>(a.r) + row * a.r_ld + col.c[i], r[i]);
+            else r[i].zero();
+            sq = fma4(quad(r[i]), quad(r[i]), sq);
         }
+        // the next row comes while this one's second norm goes on
+#pragma unroll
+        for (int i = 0; i < U; ++i) take_row(row + stride, i);
         if (!a.pre) continue;
-        float none = 0.f;
-        sums.row_and_group(s, none);
+        float s[1] = {sum_of(sq)};
+        sums.row(s);
         const float q = rsqrtf(s[0] / a.D + a.eps);
 #pragma unroll
         for (int i = 0; i < U; ++i) {
             if (!here || !col.on[i]) continue;
-            float w[4];
-            weights(a.w_pre, col.c[i], w);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) w[e] *= r[i][e] * q;
-            st4(static_cast<T*>(a.y) + row * a.y_ld + col.c[i], w);
+            put(static_cast<T*>(a.y) + row * a.y_ld + col.c[i],
+                rounded(mul4(mul4(quad(r[i]), quad(q)), weights(a.w_pre, col.c[i])), T{}));
         }
     }
 }
 
 // With U of 8 a thread cannot hold five rows' places: they are read again (from the L2) where they are used.
-template <typename T, int U, int GATE>
-__global__ void __launch_bounds__(kMaxThreads) norm_bwd_kernel(const __grid_constant__ NormArgs a) {
+template <typename T, int U, int GATE, int MAXT>
+__global__ void __launch_bounds__(MAXT, MAXT == 256 ? 2 : 1) norm_bwd_kernel(const __grid_constant__ NormArgs a) {
     constexpr bool kAgain = U == 8;
-    __shared__ float red[2][3][kMaxThreads / 32];
+    __shared__ float red[2][3][kNormThreads / 32];
     extern __shared__ __align__(16) float grown[];   // [rows of the block][kinds wanted][D]
     start_dependent();
     const Columns<U> col(a);
@@ -234,131 +315,112 @@ __global__ void __launch_bounds__(kMaxThreads) norm_bwd_kernel(const __grid_cons
     float* const dpost = mine;
     float* const dpre = mine + __popc(a.want & 1) * a.D;
     float* const dcs = mine + __popc(a.want & 3) * a.D;
-    auto grow = [&](float* p, const float (&v)[4]) {
-        float t[4];
-        get4(p, t);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) t[e] += v[e];
-        st4(p, t);
-    };
+    auto grow = [&](float* p, const Quad& v) { st4(p, add4(quad_at(p), v)); };
     for (int i = threadIdx.x; i < a.rows_block * kinds * a.D; i += blockDim.x) grown[i] = 0.f;
     __syncthreads();
-    for (int64_t base = blockIdx.x * int64_t(a.rows_block); base < a.rows; base += gridDim.x * int64_t(a.rows_block)) {
+    const int64_t stride = gridDim.x * int64_t(a.rows_block);
+    Raw4<T> o[U], z[U], r[U], g[U], dy[U], next[U];
+    auto take_r = [&](int64_t row, int i) {
+        const bool on = row < a.rows && col.on[i] && a.pre;
+        take(r[i], a.rin, row, a.r_ld, col.c[i], on);
+        take(dy[i], a.dy, row, a.dy_ld, col.c[i], on);
+    };
+    auto take_g = [&](int64_t row, int i) {
+        const bool on = row < a.rows && col.on[i];
+        take(z[i], a.z, row, a.z_ld, col.c[i], on && GATE != 0);
+        take(g[i], a.dr, row, a.dr_ld, col.c[i], on && a.dr != nullptr);
+    };
+    auto take_o = [&](Raw4<T>& to, int64_t row, int i) { take(to, a.o, row, a.o_ld, col.c[i], row < a.rows && col.on[i]); };
+    if (!kAgain) {
+#pragma unroll
+        for (int i = 0; i < U; ++i) {
+            const int64_t row = blockIdx.x * int64_t(a.rows_block) + col.row;
+            take_r(row, i);
+            take_o(next[i], row, i);
+            take_g(row, i);
+        }
+    }
+    for (int64_t base = blockIdx.x * int64_t(a.rows_block); base < a.rows; base += stride) {
         const int64_t row = base + col.row;
         const bool here = row < a.rows;
-        Raw4<T> o[U], z[U], r[U], g[U], dy[U];
-        auto take_r = [&](int i) {
-            const bool on = here && col.on[i] && a.pre;
-            take(r[i], a.rin, row, a.r_ld, col.c[i], on);
-            take(dy[i], a.dy, row, a.dy_ld, col.c[i], on);
-        };
-        auto take_g = [&](int i) {
-            const bool on = here && col.on[i];
-            take(z[i], a.z, row, a.z_ld, col.c[i], on && GATE != 0);
-            take(g[i], a.dr, row, a.dr_ld, col.c[i], on && a.dr != nullptr);
-        };
-        auto take_o = [&](int i) { take(o[i], a.o, row, a.o_ld, col.c[i], here && col.on[i]); };
         if (!kAgain) {
 #pragma unroll
-            for (int i = 0; i < U; ++i) {
-                take_r(i);
-                take_o(i);
-                take_g(i);
-            }
+            for (int i = 0; i < U; ++i) o[i] = next[i];
         }
-        float s[2] = {}, so = 0.f;   // of r^2, of u r; of o^2
+        Quad rr = quad(0.f), ur = quad(0.f), oo = quad(0.f);
 #pragma unroll
         for (int i = 0; i < U; ++i) {
             if (kAgain) {
-                take_r(i);
-                take_o(i);
+                take_r(row, i);
+                take_o(o[i], row, i);
             }
             if (a.pre) {
-                float rv[4], dv[4], w[4];
-                r[i].get(rv);
-                dy[i].get(dv);
-                weights(a.w_pre, col.c[i], w);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    s[0] = fmaf(rv[e], rv[e], s[0]);
-                    s[1] = fmaf(dv[e] * w[e], rv[e], s[1]);
-                }
+                const Quad rv = quad(r[i]);
+                rr = fma4(rv, rv, rr);
+                ur = fma4(mul4(quad(dy[i]), weights(a.w_pre, col.c[i])), rv, ur);
             }
-            if (a.post) {
-                float v[4];
-                o[i].get(v);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) so = fmaf(v[e], v[e], so);
-            }
+            if (a.post) oo = fma4(quad(o[i]), quad(o[i]), oo);
         }
-        if (a.pre || a.post) sums.row_and_group(s, so);
+        float s[2] = {sum_of(rr), sum_of(ur)}, so = sum_of(oo);
+        if (a.pre && a.post) sums.row_and_group(s, so);
+        else if (a.pre) sums.row(s);
+        else if (a.post) sums.group(so);
         const float q = rsqrtf(s[0] / a.D + a.eps), p = a.post ? rsqrtf(so / a.G + a.eps) : 1.f;
-        const float back = q * q * (s[1] / a.D);
-        float v[U][4];   // dn act(z) w_post
-        float sv = 0.f;
+        const Quad back = quad(-q * q * (s[1] / a.D)), q4 = quad(q), p4 = quad(p), scale = quad(a.scale);
+        Quad v[U], vo = quad(0.f);   // dn act(z) w_post, and its product with o
 #pragma unroll
         for (int i = 0; i < U; ++i) {
             if (kAgain) {
-                take_r(i);
-                take_o(i);
-                take_g(i);
+                take_r(row, i);
+                take_o(o[i], row, i);
+                take_g(row, i);
             }
             const bool on = here && col.on[i];
-            float ov[4], zv[4], d[4], w[4], cv[4], dzv[4], t[4];
-            o[i].get(ov);
-            z[i].get(zv);
-            g[i].get(d);
+            Quad d = quad(g[i]);
             if (a.pre) {
-                float rv[4], dv[4];
-                r[i].get(rv);
-                dy[i].get(dv);
-                weights(a.w_pre, col.c[i], w);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    t[e] = dv[e] * (rv[e] * q);
-                    d[e] = fmaf(q, fmaf(-rv[e], back, dv[e] * w[e]), d[e]);
-                }
-                if (on && (a.want & 2)) grow(dpre + col.c[i], t);
+                const Quad rv = quad(r[i]), dv = quad(dy[i]);
+                d = fma4(q4, fma4(rv, back, mul4(dv, weights(a.w_pre, col.c[i]))), d);
+                if (on && (a.want & 2)) grow(dpre + col.c[i], mul4(dv, mul4(rv, q4)));
             }
-            if (a.dx != nullptr && on) st4(static_cast<T*>(a.dx) + row * a.dx_ld + col.c[i], d);
-            if (a.post) weights(a.w_post, col.w[i], w);
-            weights(a.cs, col.c[i], cv);
-            float u[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float h = ov[e] * p, m = a.post ? h * w[e] : ov[e];
-                float act = 1.f, slope = 0.f;
-                if constexpr (GATE != 0) gate_of<T, GATE>(zv[e], act, slope);
-                t[e] = a.scale * d[e] * (m * act);
-                const float dn = a.scale * cv[e] * d[e], dm = dn * act;
-                dzv[e] = dn * m * slope;
-                v[i][e] = dm;
-                u[e] = dm * h;
-                if (a.post) {
-                    v[i][e] = dm * w[e];
-                    sv = fmaf(v[i][e], ov[e], sv);
-                }
+            if (a.dx != nullptr && on) put(static_cast<T*>(a.dx) + row * a.dx_ld + col.c[i], rounded(d, T{}));
+            const Quad ov = quad(o[i]), h = mul4(ov, p4);
+            const Quad w = a.post ? weights(a.w_post, col.w[i]) : quad(1.f);
+            const Quad m = a.post ? mul4(h, w) : ov;
+            d = mul4(scale, d);
+            Quad act = quad(1.f), slope;
+            if constexpr (GATE != 0) gates_of<T, GATE>(z[i], act, slope);
+            if (on && (a.want & 4)) grow(dcs + col.c[i], mul4(d, GATE != 0 ? mul4(m, act) : m));
+            if (a.cs != nullptr) d = mul4(d, weights(a.cs, col.c[i]));
+            if constexpr (GATE != 0) {
+                if (on) put(static_cast<T*>(a.dz) + row * a.dz_ld + col.c[i], rounded(mul4(mul4(d, m), slope), T{}));
+                d = mul4(d, act);
             }
-            if (!on) continue;
-            if (a.want & 4) grow(dcs + col.c[i], t);
-            if (a.want & 1) grow(dpost + col.c[i], u);
-            if (GATE != 0) st4(static_cast<T*>(a.dz) + row * a.dz_ld + col.c[i], dzv);
+            v[i] = d;
+            if (a.post) {
+                if (on && (a.want & 1)) grow(dpost + col.c[i], mul4(d, h));
+                v[i] = mul4(d, w);
+                vo = fma4(v[i], ov, vo);
+            }
         }
-        float k = 0.f;
+        if (!kAgain) {   // the next row comes while this one's second sum goes on
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                take_r(row + stride, i);
+                take_o(next[i], row + stride, i);
+                take_g(row + stride, i);
+            }
+        }
+        Quad k = quad(0.f);
         if (a.post) {
-            float none[1] = {};
-            sums.row_and_group(none, sv);
-            k = p * p * (sv / a.G);
+            float sv = sum_of(vo);
+            sums.group(sv);
+            k = quad(-p * p * (sv / a.G));
         }
 #pragma unroll
         for (int i = 0; i < U; ++i) {
-            if (kAgain) take_o(i);
+            if (kAgain) take_o(o[i], row, i);
             if (!here || !col.on[i]) continue;
-            float ov[4];
-            o[i].get(ov);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) ov[e] = a.post ? p * fmaf(-ov[e], k, v[i][e]) : v[i][e];
-            st4(static_cast<T*>(a.d_o) + row * a.do_ld + col.c[i], ov);
+            put(static_cast<T*>(a.d_o) + row * a.do_ld + col.c[i], rounded(a.post ? mul4(p4, fma4(quad(o[i]), k, v[i])) : v[i], T{}));
         }
     }
     if (kinds == 0) return;
@@ -443,7 +505,7 @@ int geometry(const sdm_norm_shape* s, NormArgs* a) {
     int best = 0, U = 0;
     for (int u : {4, 3, 2, 1, 8}) {
         const int lanes = pow2((a->G / 4 + u - 1) / u), threads = a->groups * lanes;
-        if (threads > kMaxThreads) continue;
+        if (threads > kNormThreads) continue;
         if (U != 0 && lanes * u >= best) continue;
         best = lanes * u;
         U = u;
@@ -511,7 +573,8 @@ extern "C" sdm_status sdm_block_norm(const sdm_norm_shape* shape, const void* o,
     const int threads = (a.rows_block * a.row_threads + 31) / 32 * 32;
     const int64_t blocks = std::min<int64_t>((a.rows + a.rows_block - 1) / a.rows_block, 152 * (2048 / threads));
     const cudaError_t e = by_type(shape, U, [&](auto t, auto u, auto gate) {
-        return launch_dependent(norm_fwd_kernel<decltype(t), decltype(u)::value, decltype(gate)::value>, dim3(static_cast<unsigned>(blocks)), dim3(threads), 0,
+        constexpr int N = decltype(u)::value, G = decltype(gate)::value;
+        return launch_dependent(threads <= 256 ? norm_fwd_kernel<decltype(t), N, G, 256> : norm_fwd_kernel<decltype(t), N, G, kNormThreads>, dim3(static_cast<unsigned>(blocks)), dim3(threads), 0,
                                 reinterpret_cast<cudaStream_t>(stream), a);
     });
     return e == cudaSuccess ? SDM_OK : SDM_ERR_CUDA;
@@ -556,7 +619,8 @@ extern "C" sdm_status sdm_block_norm_backward(const sdm_norm_shape* shape, const
     cudaError_t e = cudaSuccess;
     if (shape->rows > 0)
         e = by_type(shape, U, [&](auto t, auto u, auto gate) {
-            auto* const k = norm_bwd_kernel<decltype(t), decltype(u)::value, decltype(gate)::value>;
+            constexpr int N = decltype(u)::value, G = decltype(gate)::value;
+            auto* const k = threads <= 256 ? norm_bwd_kernel<decltype(t), N, G, 256> : norm_bwd_kernel<decltype(t), N, G, kNormThreads>;
             if (smem > 47 * 1024) {
                 const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
                 if (e != cudaSuccess) return e;

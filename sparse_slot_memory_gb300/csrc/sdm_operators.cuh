@@ -20,13 +20,15 @@ namespace sdm {
 // log probabilities 10.2 us with, 7.9 without; a short rotation 14.6 and 13.7; long kernels equal).
 __device__ __forceinline__ void start_dependent() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
-// A launch of clusters of `cluster` blocks (a multiple of them), as a programmatic dependent.
+// A launch of clusters of `cluster` blocks (a multiple of them) with `smem` bytes of dynamic shared memory, as a programmatic
+// dependent.
 template <typename... Params, typename... Args>
-cudaError_t launch_cluster(void (*kernel)(Params...), dim3 grid, dim3 block, int cluster, cudaStream_t stream,
-                           Args&&... args) {
+cudaError_t launch_cluster_smem(void (*kernel)(Params...), dim3 grid, dim3 block, int cluster, size_t smem, cudaStream_t stream,
+                                Args&&... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -38,6 +40,12 @@ cudaError_t launch_cluster(void (*kernel)(Params...), dim3 grid, dim3 block, int
     cfg.attrs = attr;
     cfg.numAttrs = 2;
     return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
+
+template <typename... Params, typename... Args>
+cudaError_t launch_cluster(void (*kernel)(Params...), dim3 grid, dim3 block, int cluster, cudaStream_t stream,
+                           Args&&... args) {
+    return launch_cluster_smem(kernel, grid, block, cluster, 0, stream, std::forward<Args>(args)...);
 }
 
 namespace checks {
