@@ -4,9 +4,9 @@
 // The gradient's row v is scale times the sum of dy over the tokens with id v. The tokens are sorted by id, stably, by one
 // cluster of 8 blocks (a radix sort of 10 bits a pass: histograms of contiguous parts, exchanged through the cluster's shared
 // memory), which also lists the ids that there are and where their tokens begin and end; the other SMs write the table's zeros
-// meanwhile, a kernel that starts with the sort and ends behind it. Then every id has one writer that adds its tokens in order: no
-// sum depends on timing. Ids with many tokens, the frequent words, are a block's and come first: its warps take contiguous
-// shares of the tokens, joined in order. Bound by HBM: the table's gradient is written once (float32, 131072 x 2048: 1.07 GB),
+// meanwhile, a kernel that starts with the sort and ends behind it. Then a warp adds the tokens of an id in their order, or of
+// a part of 16 where an id has more, the frequent words; their parts' sums wait in the workspace and are joined in order by a
+// last kernel. No sum depends on timing. Bound by HBM: the table's gradient is written once (float32, 131072 x 2048: 1.07 GB),
 // the tokens' rows are read once.
 #include <cuda_bf16.h>
 
@@ -25,8 +25,8 @@ constexpr int kBits = 10, kDigits = 1 << kBits;   // of a pass
 constexpr int kHeld = 4;        // rounds of a warp's tokens that stay in registers
 constexpr int kSortBlocks = 8, kSortThreads = 1024, kSortWarps = kSortThreads / 32;
 constexpr int kSlice = 512;     // columns of a warp's unit: 16 a lane
-constexpr int kMany = 64;       // tokens from which a row is a block's
-constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kPart = 16;       // tokens of an id that a warp adds
+constexpr int kThreads = 256, kWarps = kThreads / 32;
 
 struct EmbedArgs {
     const int32_t* ids;
@@ -41,10 +41,12 @@ struct EmbedArgs {
     // workspace of the backward
     int32_t* key[2];
     int32_t* tok[2];
-    int32_t* end;       // [V]: where an id's tokens end, of ids that there are
-    int32_t* count;     // [2]: of the lists
-    int4* many;         // the ids with more than kMany tokens: id, where they begin and end, the first token
-    int4* few;          // the others that there are
+    int2* range;        // [V]: where an id's tokens begin and end, of ids that there are
+    int32_t* count;     // [2]: of work and joins
+    int4* work;         // an id, or -1 - a part's number; where its tokens begin and end; the first token
+    int4* joins;        // an id of several parts: id, first part, parts
+    float* part;        // [tokens / 8][D]: their sums. Part p of an id whose tokens begin at b has the row b / 8 + p: an id of several parts
+                        // has at least 17 tokens, so the rows of two ids never meet
     int passes;
 };
 
@@ -106,7 +108,7 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const __grid_c
     // contiguous parts, so that their order is the tokens'
     const int64_t share = (static_cast<int64_t>(n) + kSortBlocks * kSortWarps - 1) / (kSortBlocks * kSortWarps);
     const int64_t lo = min((static_cast<int64_t>(rank) * kSortWarps + w) * share, int64_t(n)), hi = min(lo + share, int64_t(n));
-    if (rank == 0 && tid == 0) a.count[0] = a.count[1] = 0;
+    if (rank == 0 && tid < 2) a.count[tid] = 0;
     for (int pass = 0; pass < a.passes; ++pass) {
         const int shift = kBits * pass;
         const int32_t* const kin = a.key[(pass + 1) & 1];
@@ -132,20 +134,21 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const __grid_c
         round_of(lo + lane, k0, t0);
         for (int i = lane; i < kDigits; i += 32) hist[w][i] = 0;
         __syncwarp();
-        auto count = [&](const int (&k)[kHeld]) {
+        auto count = [&](int64_t i, const int (&k)[kHeld]) {
 #pragma unroll
             for (int r = 0; r < kHeld; ++r) {
+                if (i + 32 * r >= hi) break;
                 const int d = k[r] >= 0 ? (k[r] >> shift) & (kDigits - 1) : -1;
                 const uint32_t same = same_digit(d);
                 if (d >= 0 && (same & ((1u << lane) - 1)) == 0) hist[w][d] += __popc(same);
                 __syncwarp();
             }
         };
-        count(k0);
+        count(lo, k0);
         for (int64_t i = lo + 32 * kHeld; i < hi; i += 32 * kHeld) {
             int k[kHeld], t[kHeld];
             round_of(i + lane, k, t);
-            count(k);
+            count(i, k);
         }
         __syncthreads();
         {
@@ -188,9 +191,10 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const __grid_c
             first[tid] += c;
         }
         __syncthreads();
-        auto place = [&](const int (&k)[kHeld], const int (&t)[kHeld]) {
+        auto place = [&](int64_t i, const int (&k)[kHeld], const int (&t)[kHeld]) {
 #pragma unroll
             for (int r = 0; r < kHeld; ++r) {
+                if (i + 32 * r >= hi) break;
                 const int d = k[r] >= 0 ? (k[r] >> shift) & (kDigits - 1) : -1;
                 const uint32_t same = same_digit(d);
                 const int ahead = __popc(same & ((1u << lane) - 1));
@@ -205,11 +209,11 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const __grid_c
                 }
             }
         };
-        place(k0, t0);
+        place(lo, k0, t0);
         for (int64_t i = lo + 32 * kHeld; i < hi; i += 32 * kHeld) {
             int k[kHeld], t[kHeld];
             round_of(i + lane, k, t);
-            place(k, t);
+            place(i, k, t);
         }
         // the next pass reads what the cluster wrote, and writes the totals that it read
         cluster_arrive();
@@ -220,25 +224,25 @@ __global__ void __launch_bounds__(kSortThreads) embed_sort_kernel(const __grid_c
     for (int64_t i = rank * int64_t(kSortThreads) + tid; i < n; i += kSortBlocks * kSortThreads) {
         const int k = __ldcg(key + i);
         if (k >= a.V) continue;
-        if (i + 1 == n || __ldcg(key + i + 1) != k) a.end[k] = static_cast<int>(i) + 1;
+        if (i == 0 || __ldcg(key + i - 1) != k) a.range[k].x = static_cast<int>(i);
+        if (i + 1 == n || __ldcg(key + i + 1) != k) a.range[k].y = static_cast<int>(i) + 1;
     }
     cluster_arrive();
     cluster_wait();
     for (int64_t i = rank * int64_t(kSortThreads) + tid; i - lane < n; i += kSortBlocks * kSortThreads) {
-        const int k = i < n ? __ldcg(key + i) : a.V;
-        const bool head = k < a.V && (i == 0 || __ldcg(key + i - 1) != k);
-        const int end = head ? __ldcg(a.end + k) : 0;
-        const bool many = head && end - static_cast<int>(i) > kMany;
+        const int k = i < n ? __ldcg(key + i) : a.V, at = static_cast<int>(i);
+        const int2 r = k < a.V ? __ldcg(a.range + k) : make_int2(0, 0);
+        const bool several = r.y - r.x > kPart;
         // the lists' order is whatever it is; a warp takes its places together
-#pragma unroll
-        for (int list = 0; list < 2; ++list) {
-            const bool mine = head && many == (list == 0);
-            const uint32_t m = __ballot_sync(kFull, mine);
-            int at = 0;
-            if (lane == 0 && m != 0) at = atomicAdd(a.count + list, __popc(m));
-            at = __shfl_sync(kFull, at, 0) + __popc(m & ((1u << lane) - 1));
-            if (mine) (list == 0 ? a.many : a.few)[at] = make_int4(k, static_cast<int>(i), end, __ldcg(tok + i));
-        }
+        const bool starts = k < a.V && (several ? (at - r.x) % kPart == 0 : at == r.x), joins = starts && several && at == r.x;
+        const uint32_t ms = __ballot_sync(kFull, starts), mj = __ballot_sync(kFull, joins), before = (1u << lane) - 1;
+        int ws = 0, wj = 0;
+        if (lane == 0 && ms != 0) ws = atomicAdd(a.count, __popc(ms));
+        if (lane == 0 && mj != 0) wj = atomicAdd(a.count + 1, __popc(mj));
+        ws = __shfl_sync(kFull, ws, 0) + __popc(ms & before);
+        wj = __shfl_sync(kFull, wj, 0) + __popc(mj & before);
+        if (starts) a.work[ws] = make_int4(several ? -1 - (r.x / 8 + (at - r.x) / kPart) : k, at, several ? min(at + kPart, r.y) : r.y, __ldcg(tok + i));
+        if (joins) a.joins[wj] = make_int4(k, r.x / 8, (r.y - r.x + kPart - 1) / kPart, 0);
     }
 }
 
@@ -305,52 +309,59 @@ __device__ __forceinline__ void put_row(const EmbedArgs& a, int v, int c, int n,
     }
 }
 
-// A frequent word's slice of Q * 128 columns: the block's warps take shares of the tokens.
-template <typename TT, typename T, int Q, int F>
-__device__ __forceinline__ void block_row(const EmbedArgs& a, const int32_t* tok, float (*part)[kSlice], int64_t u, int slices) {
-    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-    const int4 r = a.many[u / slices];
-    const int c = static_cast<int>(u % slices) * Q * 128 + 4 * lane, n = max(0, min(Q, (a.D - c + 127) / 128));
-    const int share = (r.z - r.y + kWarps - 1) / kWarps, b = min(r.y + w * share, r.z);
-    Quad acc[Q] = {};
-    add_tokens<T, Q, F>(a, tok, b < r.z ? tok[b] : 0, b, min(b + share, r.z), c, n, acc);
-#pragma unroll
-    for (int q = 0; q < Q; ++q) st4(&part[w][4 * lane + 128 * q], acc[q]);
-    __syncthreads();
-    if (w == 0) {
-        for (int i = 1; i < kWarps; ++i)
-#pragma unroll
-            for (int q = 0; q < Q; ++q) acc[q] = add4(acc[q], quad_at(&part[i][4 * lane + 128 * q]));
-        put_row<TT>(a, r.x, c, n, acc);
-    }
-    __syncthreads();
-}
-
 template <typename TT, typename T>
-__global__ void __launch_bounds__(kThreads, 2) embed_bwd_kernel(const __grid_constant__ EmbedArgs a) {
-    __shared__ __align__(16) float part[kWarps][kSlice];
+__global__ void __launch_bounds__(kThreads, 4) embed_bwd_kernel(const __grid_constant__ EmbedArgs a) {
     start_dependent();
-    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-    const int slices = (a.D + kSlice - 1) / kSlice, thin = (a.D + 127) / 128;
+    constexpr int F = sizeof(T) == 2 ? 4 : 2;   // tokens of 512 columns on their way: what 64 registers hold
+    const int lane = threadIdx.x & 31, slices = (a.D + kSlice - 1) / kSlice;
     const int32_t* const tok = a.tok[(a.passes + 1) & 1];
-    constexpr int F = sizeof(T) == 2 ? 3 : 2;   // tokens of 512 columns on their way: what 64 registers hold
-    // frequent words in slices of 128 columns with 4 F tokens on their way, while those do not outnumber the blocks four times
-    const int64_t many = a.count[0];
-    if (many * thin <= 4 * gridDim.x)
-        for (int64_t u = blockIdx.x; u < many * thin; u += gridDim.x) block_row<TT, T, 1, 4 * F>(a, tok, part, u, thin);
-    else
-        for (int64_t u = blockIdx.x; u < many * slices; u += gridDim.x) block_row<TT, T, 4, F>(a, tok, part, u, slices);
-    // from the last block on: the first ones may still be at the frequent words. The next word is known ahead.
-    const int64_t few = static_cast<int64_t>(a.count[1]) * slices, stride = static_cast<int64_t>(gridDim.x) * kWarps;
-    int64_t u = static_cast<int64_t>(gridDim.x - 1 - blockIdx.x) * kWarps + w;
-    int4 next = u < few ? a.few[u / slices] : make_int4(0, 0, 0, 0);
-    for (; u < few; u += stride) {
+    const int64_t units = static_cast<int64_t>(a.count[0]) * slices, stride = static_cast<int64_t>(gridDim.x) * kWarps;
+    int64_t u = blockIdx.x * int64_t(kWarps) + (threadIdx.x >> 5);
+    int4 next = u < units ? a.work[u / slices] : make_int4(0, 0, 0, 0);   // known ahead
+    for (; u < units; u += stride) {
         const int4 r = next;
         const int c = static_cast<int>(u % slices) * kSlice + 4 * lane, n = max(0, min(4, (a.D - c + 127) / 128));
-        if (u + stride < few) next = a.few[(u + stride) / slices];
+        if (u + stride < units) next = a.work[(u + stride) / slices];
         Quad acc[4] = {};
         add_tokens<T, 4, F>(a, tok, r.w, r.y, r.z, c, n, acc);
-        put_row<TT>(a, r.x, c, n, acc);
+        if (r.x >= 0) {
+            put_row<TT>(a, r.x, c, n, acc);
+        } else {
+            float* const out = a.part + static_cast<int64_t>(-1 - r.x) * a.D + c;
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                if (q < n) st4(out + 128 * q, acc[q]);
+        }
+    }
+}
+
+// An id's parts: a block's warps add contiguous shares of them, those are joined in order.
+template <typename TT>
+__global__ void __launch_bounds__(kThreads) embed_join_kernel(const __grid_constant__ EmbedArgs a) {
+    __shared__ __align__(16) float sum[kWarps][kSlice];
+    start_dependent();
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, slices = (a.D + kSlice - 1) / kSlice;
+    const int64_t units = static_cast<int64_t>(a.count[1]) * slices;
+    for (int64_t u = blockIdx.x; u < units; u += gridDim.x) {
+        const int4 r = a.joins[u / slices];
+        const int c = static_cast<int>(u % slices) * kSlice + 4 * lane, n = max(0, min(4, (a.D - c + 127) / 128));
+        const int share = (r.z + kWarps - 1) / kWarps, b = min(w * share, r.z), e = min(b + share, r.z);
+        Quad acc[4] = {};
+#pragma unroll 4
+        for (int i = b; i < e; ++i)
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                if (q < n) acc[q] = add4(acc[q], quad(load4(a.part + (static_cast<int64_t>(r.y) + i) * a.D + c + 128 * q)));
+#pragma unroll
+        for (int q = 0; q < 4; ++q) st4(&sum[w][4 * lane + 128 * q], acc[q]);
+        __syncthreads();
+        if (w == 0) {
+            for (int i = 1; i < kWarps; ++i)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) acc[q] = add4(acc[q], quad_at(&sum[i][4 * lane + 128 * q]));
+            put_row<TT>(a, r.x, c, n, acc);
+        }
+        __syncthreads();
     }
 }
 
@@ -387,6 +398,9 @@ void fill(const sdm_embed_shape* s, EmbedArgs* a) {
 }
 
 int64_t up(int64_t n) { return (n + 255) / 256 * 256; }
+// ids of several parts at most, and the rows of their parts
+int64_t joins_of(int64_t tokens) { return tokens / (kPart + 1); }
+int64_t parts_of(int64_t tokens) { return joins_of(tokens) > 0 ? tokens / 8 + 1 : 0; }
 
 template <typename F>
 cudaError_t by_type(const sdm_embed_shape* s, F f) {
@@ -401,9 +415,9 @@ using namespace sdm;
 
 extern "C" size_t sdm_embed_workspace_bytes(const sdm_embed_shape* shape) {
     if (check(shape) != SDM_OK) return 0;
-    const int64_t T = shape->tokens;
-    return static_cast<size_t>(4 * up(4 * T) + up(4 * static_cast<int64_t>(shape->V)) + 256 + up(16 * (T / kMany + 1)) +
-                               up(16 * std::min<int64_t>(T, shape->V)));
+    const int64_t T = shape->tokens, V = shape->V;
+    return static_cast<size_t>(4 * up(4 * T) + up(8 * V) + 256 + up(16 * (std::min(T, V) + parts_of(T))) + up(16 * joins_of(T)) +
+                               up(4 * parts_of(T) * shape->D));
 }
 
 extern "C" sdm_status sdm_embed(const sdm_embed_shape* shape, const int32_t* ids, const void* table, int64_t table_ld, void* y,
@@ -450,13 +464,15 @@ extern "C" sdm_status sdm_embed_backward(const sdm_embed_shape* shape, const int
         a.tok[i] = reinterpret_cast<int32_t*>(w);
         w += up(4 * shape->tokens);
     }
-    a.end = reinterpret_cast<int32_t*>(w);
-    w += up(4 * static_cast<int64_t>(shape->V));
+    a.range = reinterpret_cast<int2*>(w);
+    w += up(8 * static_cast<int64_t>(shape->V));
     a.count = reinterpret_cast<int32_t*>(w);
     w += 256;
-    a.many = reinterpret_cast<int4*>(w);
-    w += up(16 * (shape->tokens / kMany + 1));
-    a.few = reinterpret_cast<int4*>(w);
+    a.work = reinterpret_cast<int4*>(w);
+    w += up(16 * (std::min<int64_t>(shape->tokens, shape->V) + parts_of(shape->tokens)));
+    a.joins = reinterpret_cast<int4*>(w);
+    w += up(16 * joins_of(shape->tokens));
+    a.part = reinterpret_cast<float*>(w);
     const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
     constexpr int smem = kSortWarps * kDigits * static_cast<int>(sizeof(int));
     cudaError_t e = cudaFuncSetAttribute(embed_sort_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
@@ -466,11 +482,14 @@ extern "C" sdm_status sdm_embed_backward(const sdm_embed_shape* shape, const int
         e = launch_dependent(shape->table_dtype == SDM_BF16 ? embed_zero_kernel<__nv_bfloat16> : embed_zero_kernel<float>,
                              dim3(static_cast<unsigned>(blocks)), dim3(256), 0, cs, a);
     }
-    const int64_t units = shape->tokens * ((shape->D + kSlice - 1) / kSlice);
-    const int64_t blocks = std::max<int64_t>(1, std::min<int64_t>((units + kWarps - 1) / kWarps, 152 * 2));
+    const int64_t slices = (shape->D + kSlice - 1) / kSlice;
+    const int64_t blocks = std::min<int64_t>((shape->tokens * slices + kWarps - 1) / kWarps, 152 * 4);
     if (e == cudaSuccess && shape->tokens > 0)
         e = by_type(shape, [&](auto tt, auto t) {
             return launch_dependent(embed_bwd_kernel<decltype(tt), decltype(t)>, dim3(static_cast<unsigned>(blocks)), dim3(kThreads), 0, cs, a);
         });
+    if (e == cudaSuccess && joins_of(shape->tokens) > 0)
+        e = launch_dependent(shape->table_dtype == SDM_BF16 ? embed_join_kernel<__nv_bfloat16> : embed_join_kernel<float>,
+                             dim3(static_cast<unsigned>(std::min<int64_t>(joins_of(shape->tokens) * slices, 152 * 4))), dim3(kThreads), 0, cs, a);
     return e == cudaSuccess ? SDM_OK : SDM_ERR_CUDA;
 }

@@ -78,8 +78,8 @@ def test_rows_and_gradient(name, accumulate):
 
 
 def test_counts_around_the_block_s_rows():
-    """Rows of 0, 1, 3, 4, 5, 63, 64, 65, 66 and 5000 tokens, in a mixed order."""
-    counts = [0, 1, 3, 4, 5, 63, 64, 65, 66, 5000, 1025]
+    """Rows of no, one and several tokens around a part of 16 and a block of parts, and of 5000, in a mixed order."""
+    counts = [0, 1, 3, 4, 5, 15, 16, 17, 32, 33, 128, 129, 5000, 1025]
     ids = torch.cat([torch.full((n,), i) for i, n in enumerate(counts)])
     ids = ids[torch.randperm(len(ids), generator=torch.Generator().manual_seed(1))]
     for xt in ("bf16", "f32"):
@@ -130,9 +130,9 @@ def test_runs_are_bitwise_equal_and_follow_the_tokens_order():
         sdm.embed_backward(s, c["ids"], c["dy"], d, sdm.alloc_embed_workspace(s))
         out.append(d)
     assert torch.equal(out[0], out[1]) and torch.equal(out[0], out[2])
-    # rows of up to 64 tokens are added in the tokens' order
+    # rows of up to 16 tokens are added in the tokens' order
     ids = c["ids"].long()
-    for v in [int(i) for i in range(300) if 1 < int((ids == i).sum()) <= 64][:20]:
+    for v in [int(i) for i in range(300) if 1 < int((ids == i).sum()) <= 16][:20]:
         t = torch.zeros(132, device="cuda")
         for i in torch.nonzero(ids == v).reshape(-1).tolist():
             t = t + c["dy"][i]
