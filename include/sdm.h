@@ -543,12 +543,12 @@ typedef struct {
  *   S_t = exp(g_t) S_{t-1} + k_t u_t^T,   u_t = beta_t (v_t - exp(g_t) S_{t-1}^T k_t),   y_t = scale S_t^T q_t.
  *   q, k [rows, k_heads * dk], v, y [rows, v_heads * dv], aligned to 16 bytes like their ld; g, beta [rows, v_heads], no alignment
  *   rule: log decays, at most 0 (-inf starts anew; a product of decays below float32's range counts as 0), and write
- *   strengths. Keys of length 1 and beta in [0, 2] keep the state bounded.
+ *   strengths (below 2^-80 they count as 2^-80). Keys of length 1 and beta in [0, 2] keep the state bounded.
  *   offsets: as in sdm_glr_forward (ragged sequences, rows of no sequence).
  *   h0 (nullable: zeros) and hT (nullable) float32 [P, v_heads, dk, dv]: the states before and after; hT may be h0; an
  *   empty sequence hands its state on.
- *   states (nullable), sdm_gdr_states_bytes, 16-byte aligned: the state before every SDM_GDR_CHUNK-th row of each sequence, for
- *   the backward, in a form of its own.
+ *   states (nullable), sdm_gdr_states_bytes, 16-byte aligned: the state before every SDM_GDR_CHUNK-th row of each sequence and
+ *   what every row writes, for the backward, in a form of its own.
  *   ws: sdm_gdr_workspace_bytes(shape, 0), 16-byte aligned. It holds nothing from one call to the next.
  * Blocks of 64 rows are solved together on the tensor cores; sums are float32, and float32 values enter the products as sums of
  * two bfloat16 (within 2^-17) beside bfloat16 rows, of three (2^-25) beside float32 rows. A value that is not finite spoils its sequence and head from the start of its block on (as NaN).

@@ -101,7 +101,7 @@ __global__ void __launch_bounds__(128, XT == 1 ? 4 : 2) gdr_prepare_kernel(const
                 const int r = 2 * lane + e;
                 const float x = r < n ? gate_at(a.g, (b + r) * a.g_ld + h, a.g_bf16) : 0.f;
                 s[e] = x < -150.f ? -150.f : x;
-                bt[e] = r < n ? gate_at(a.beta, (b + r) * a.b_ld + h, a.g_bf16) : 0.f;
+                bt[e] = strength(r < n ? gate_at(a.beta, (b + r) * a.b_ld + h, a.g_bf16) : 0.f);
             }
             s[1] += s[0];
             double run = s[1];
@@ -119,7 +119,7 @@ __global__ void __launch_bounds__(128, XT == 1 ? 4 : 2) gdr_prepare_kernel(const
                 const float hi = static_cast<float>(gam), lo = static_cast<float>(gam - hi);
                 gh[r] = hi;
                 gl[r] = lo;
-                be[r] = strength(bt[e]);
+                be[r] = bt[e];
                 vec[3 * kC + r] = hi;
                 vec[4 * kC + r] = lo;
                 const float x = expf(hi);
@@ -271,7 +271,7 @@ __global__ void __launch_bounds__(BV * 2) gdr_walk_kernel(const __grid_constant_
     sequence(a, p, b, len);
     const int64_t blocks = (len + kC - 1) / kC, id0 = first_block(b, p);
     const uint32_t base = smem_of(smem);
-    const int cols = min(BV, a.dv - c0);
+    const int cols = min(BV, a.dv - c0), groups = (a.dv + 15) / 16;
 
     auto load = [&](int64_t j, int s) {
         const uint32_t st = base + s * W::stage;
@@ -335,7 +335,6 @@ __global__ void __launch_bounds__(BV * 2) gdr_walk_kernel(const __grid_constant_
             async_fence();
             __syncwarp();
             if (lane == 0) {
-                const int groups = (a.dv + 15) / 16;
                 bulk_store(a.states + (((id0 + j) * a.Hv + h) * groups + c0 / 16 + w) * int64_t(NS * 16 * DKP), keep, W::kKeep);
                 bulk_commit();
             }
@@ -377,10 +376,18 @@ __global__ void __launch_bounds__(BV * 2) gdr_walk_kernel(const __grid_constant_
         for (int t = 0; t < 2 * KT; ++t)
 #pragma unroll
             for (int e = 0; e < 4; ++e) S[t][e] *= last;
+        if (a.states != nullptr) {   // the state's tile has left long ago
+            if (lane == 0) bulk_wait_read();
+            __syncwarp();
+        }
 #pragma unroll
         for (int kt = 0; kt < 4; ++kt) {   // A U, and K^T (e^(gam_last - gam) U)
             uint32_t f[NS][4];
             terms_of<NS>(u[2 * kt], u[2 * kt + 1], f);
+            if (a.states != nullptr) {
+#pragma unroll
+                for (int t = 0; t < NS; ++t) stsm4t(keep + t * (kC * 32) + tile_at<16>(16 * kt + L.rAt, L.uAt), f[t]);
+            }
             products<NS, XT, NS, false, 4>(o, f, W::kPlane, [&](int np) { return st + W::A + tile_at<kC>(16 * np + L.rB, 2 * kt + L.uB); }, kt);
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
@@ -390,6 +397,14 @@ __global__ void __launch_bounds__(BV * 2) gdr_walk_kernel(const __grid_constant_
             }
             terms_of<NS>(u[2 * kt], u[2 * kt + 1], f);
             products<NS, XT, NS, true, KT>(S, f, W::kTile, [&](int np) { return st + W::K + tile_at<DKP>(16 * kt + L.rBt, 2 * np + L.uBt); });
+        }
+        if (a.states != nullptr) {   // the writes, for the backward
+            async_fence();
+            __syncwarp();
+            if (lane == 0) {
+                bulk_store(a.writes + (((id0 + j) * a.Hv + h) * groups + c0 / 16 + w) * int64_t(NS * kC * 16), keep, NS * kC * 32);
+                bulk_commit();
+            }
         }
         // the rows' answers
         const int64_t r0 = b + j * kC;
@@ -630,6 +645,11 @@ Layout layout(const sdm_gdr_shape* s, bool backward) {
     return l;
 }
 
+void set_states(const sdm_gdr_shape* s, void* states, Args* a) {
+    a->states = static_cast<__nv_bfloat16*>(states);
+    if (states != nullptr) a->writes = a->states + blocks_of(s) * s->v_heads * ((s->dv + 15) / 16 * 16) * padded(s->dk) * terms(s);
+}
+
 cudaError_t launch_split(const void* x, int64_t ld, int64_t rows, int cols, __nv_bfloat16* out, cudaStream_t cs) {
     const int64_t blocks = std::min<int64_t>((rows * (cols / 4) + 255) / 256, 152 * 8);
     return launch_dependent(gdr_split_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, cs, static_cast<const float*>(x), ld, rows,
@@ -698,7 +718,7 @@ using namespace sdm::gdr;
 
 extern "C" size_t sdm_gdr_states_bytes(const sdm_gdr_shape* shape) {
     if (check_shape(shape) != SDM_OK) return 0;
-    return static_cast<size_t>(blocks_of(shape)) * shape->v_heads * ((shape->dv + 15) / 16 * 16) * padded(shape->dk) * 2 * terms(shape);
+    return static_cast<size_t>(blocks_of(shape)) * shape->v_heads * ((shape->dv + 15) / 16 * 16) * (padded(shape->dk) + kC) * 2 * terms(shape);
 }
 
 extern "C" size_t sdm_gdr_workspace_bytes(const sdm_gdr_shape* shape, int32_t backward) {
@@ -718,7 +738,7 @@ extern "C" sdm_status sdm_gdr_forward(const sdm_gdr_shape* shape, const void* q,
     if (shape->rows > 0 && (st = check_array(y, y_ld, vn, shape->x_dtype == SDM_BF16 ? 2 : 4, 16, true)) != SDM_OK) return st;
     if (!aligned_all(16, {h0, hT, states})) return SDM_ERR_ALIGN;
     a.h0 = h0; a.y = y; a.y_ld = y_ld; a.hT = hT;
-    a.states = static_cast<__nv_bfloat16*>(states);
+    set_states(shape, states, &a);
     a.tri_planes = shape->x_dtype == SDM_F32 ? 6 : 3;
     const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t e = cudaSuccess;

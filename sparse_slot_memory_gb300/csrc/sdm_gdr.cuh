@@ -33,8 +33,8 @@ constexpr int kC = SDM_GDR_CHUNK;   // rows of a block
 constexpr int kMaxD = 128;          // channels of a head at most
 constexpr int kVecs = 5;
 
-// A write strength below 2^-80 counts as 2^-80 in T, so that the error v - e^g S^T k behind a write, which the strength's gradient
-// takes, can be had from the write. A row of strength 0 then holds 2^-80 of the others' writes, which no other value feels.
+// A write strength below 2^-80 counts as 2^-80, so that the error v - e^g S^T k behind a write, which the strength's gradient
+// takes, can be had from the write. What a row of strength 0 writes is then 2^-80 of that error, which no other value feels.
 __device__ __forceinline__ float strength(float beta) { return fabsf(beta) < 0x1p-80f ? copysignf(0x1p-80f, beta) : beta; }
 
 // Rows as the tensor cores take them: planes of bfloat16 (one, or the three terms of float32 rows).
@@ -54,6 +54,7 @@ struct Args {
     float* hT;                // nullable
     float* dh0;               // nullable
     __nv_bfloat16* states;    // nullable in the forward: [blocks][Hv][dv / 16][terms], tiles [16 value columns][dk padded]
+    __nv_bfloat16* writes;    // behind the states: U, [blocks][Hv][dv / 16][terms], tiles [64][16]
     void* y;
     void* dq;
     void* dk_out;
@@ -324,6 +325,8 @@ struct Layout {
 inline int terms(const sdm_gdr_shape* s) { return s->x_dtype == SDM_F32 ? 3 : 2; }   // of what is computed
 sdm_status check_shape(const sdm_gdr_shape* s);
 Layout layout(const sdm_gdr_shape* s, bool backward);
+// The saved states and writes: the parts of one array
+void set_states(const sdm_gdr_shape* s, void* states, Args* a);
 // The checks of what both directions take, and the arguments that follow from it
 sdm_status check_inputs(const sdm_gdr_shape* s, const void* q, int64_t q_ld, const void* k, int64_t k_ld, const void* v, int64_t v_ld,
                         const void* g, int64_t g_ld, const void* beta, int64_t b_ld, const int64_t* offsets, void* ws,

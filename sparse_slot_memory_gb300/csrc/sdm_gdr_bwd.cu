@@ -7,14 +7,14 @@
 //   M  = dV U^T, N = scale dY U^T
 //   dQ = scale e^gam o dY S^T + (N o D) K
 //   dK = (N o D)^T Q - (M o D) K - (M o D)^T K - e^gam o dV S^T + e^(gam_last - gam) o U dS'^T     (M o D strictly below the diagonal)
-//   dbeta_i = W_i . U_i / beta_i
+//   dbeta_i = W_i . U_i / beta_i      (a strength is never 0: sdm_gdr.cuh)
 // and dg_t sums what every decay over row t brings, never a difference of such sums, so that strong decays keep their digits:
 //   dg_t = sum_{j < t <= i} (N o A - M o G)_ij + sum_{i >= t} a_i + sum_{j < t} e_j + e^gam_last <dS', S>,
 //   a_i = e^gam_i (scale q_i . (S dY_i) - dV_i . (S^T k_i)),   e_j = e^(gam_last - gam_j) u_j . (dS'^T k_j).
 //
 // Three kernels: sdm_gdr.cu's of what needs no state, a walk from each sequence's end that carries dS as the forward's
 // carries S (a warp 16 value columns, transposed, nothing leaves its registers) and writes dV, W and every block's dS'; and one
-// for all blocks at once that has the rest, from the states that the forward saved.
+// for all blocks at once that has the rest, from the states and the writes that the forward saved.
 #include "sdm_gdr.cuh"
 
 namespace sdm {
@@ -230,22 +230,21 @@ __global__ void __launch_bounds__(BV * 2) gdr_back_kernel(const __grid_constant_
 }
 
 // ---- all blocks at once ---------------------------------------------------------------------------------------------
-// 16 warps: warp w has rows 16 (w % 4) .. of everything, and of each product's columns the (w / 4)-th part: 8 of a slice's value
-// columns, 16 of the 64 columns of M and N, a quarter of dk. A block walks the value columns in slices of SL, the next one's
-// states and rows on their way.
+// 16 warps: warp w has rows 16 (w % 4) .. of everything, and of each product's columns the (w / 4)-th part: 16 of the 64 columns
+// of M and N, a quarter of dk. A block walks the value columns in slices of SL, the next ones' states, writes and gradients on
+// their way; all operands come from shared memory as they were stored, so a slice needs one barrier.
 template <int XT, int DKP>
 struct Grad {
     static constexpr int NS = XT == 1 ? 2 : 3, NG = XT == 1 ? 1 : 3;   // NG: terms of what only rows' gradients take
-    static constexpr int SL = XT == 1 ? 32 : 16, stages = XT == 1 ? 2 : 1;
+    static constexpr int SL = XT == 1 ? 32 : 16, stages = XT == 1 ? 3 : 2;
     static constexpr int kTile = kC * DKP * 2, kPlane = kC * kC * 2, kVal = kC * SL * 2;
-    static constexpr int kState = SL / 16 * NS * 16 * DKP * 2, kDu = SL / 16 * NS * kC * 32;
+    static constexpr int kState = SL / 16 * NS * 16 * DKP * 2, kRows = SL / 16 * NS * kC * 32;
     // within a stage
-    static constexpr int S = 0, dS = kState, dU = 2 * kState, V = dU + kDu, Y = V + XT * kVal, stage = Y + XT * kVal;
+    static constexpr int S = 0, dS = kState, W = 2 * kState, U = W + kRows, Y = U + kRows, stage = Y + XT * kVal;
     // the whole
-    static constexpr int K = 0, Q = XT * kTile, T = 2 * XT * kTile, R = T + NS * kPlane, U = R + NS * kVal, slices = U + NS * kVal,
-                         end = slices + stages * stage;
-    // over T, R, U and the slices when they are done: N o D and - M o D, the sums of dg, and the rows' gradients
-    static constexpr int ND = T, XD = ND + NG * kPlane, Z = XD + NG * kPlane, last = Z + kC * 65 * 4;
+    static constexpr int K = 0, Q = XT * kTile, slices = 2 * XT * kTile, end = slices + stages * stage;
+    // over the slices when they are done: N o D and - M o D, the sums of dg, and the rows' gradients
+    static constexpr int ND = slices, XD = ND + NG * kPlane, Z = XD + NG * kPlane, last = Z + kC * 65 * 4;
     static constexpr int bytes = end > last ? end : last;
     static_assert(ND + 2 * kTile <= bytes, "the rows' gradients leave through the place of the products");
     static constexpr int threads = 512;
@@ -257,7 +256,8 @@ __global__ void __launch_bounds__(512) gdr_grad_kernel(const __grid_constant__ A
     constexpr int NS = W::NS, NG = W::NG, SL = W::SL, KT = DKP / 16, DN = DKP / 64;   // DN: tiles of 16 columns of dk of a warp
     extern __shared__ __align__(1024) unsigned char smem[];
     __shared__ __align__(16) float vec[kVecs * kC];
-    __shared__ float sums[3][4][kC];   // a, e, W.U by quarters
+    __shared__ float sums[2][4][kC];   // a, e by quarters
+    __shared__ float diag[kC];         // W . U
     __shared__ float inner[16];
     start_dependent();
     const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, g = lane >> 2, qd = lane & 3, mi = w & 3, qf = w >> 2;
@@ -272,172 +272,90 @@ __global__ void __launch_bounds__(512) gdr_grad_kernel(const __grid_constant__ A
     const int64_t unit = id * a.Hv + h;
 
     auto load = [&](int s) {
-        const uint32_t st = base + W::slices + (W::stages == 2 ? (s & 1) * W::stage : 0);
-        const int c0 = s * SL, cols = min(SL, a.dv - c0);
-        const int have = min(SL / 16, groups - c0 / 16);   // groups of 16 value columns that there are; the others are zeros
-        const __nv_bfloat16* const sp = a.states + (unit * groups + c0 / 16) * (NS * 16 * DKP);
-        const __nv_bfloat16* const dp = a.dstates + (unit * groups + c0 / 16) * (NS * 16 * DKP);
-        const __nv_bfloat16* const up = a.du + (unit * groups + c0 / 16) * (NS * kC * 16);
-        for (int i = tid; i < W::kState / 16; i += W::threads) {
-            const bool there = i < have * NS * 16 * DKP / 8;
-            copy16(st + W::S + i * 16, there ? sp + i * 8 : sp, there);
-            copy16(st + W::dS + i * 16, there ? dp + i * 8 : dp, there);
+        if (s < nslices) {
+            const uint32_t st = base + W::slices + s % W::stages * W::stage;
+            const int c0 = s * SL, cols = min(SL, a.dv - c0);
+            const int have = min(SL / 16, groups - c0 / 16);   // groups of 16 value columns that there are; the others are zeros
+            const __nv_bfloat16* const sp = a.states + (unit * groups + c0 / 16) * (NS * 16 * DKP);
+            const __nv_bfloat16* const dp = a.dstates + (unit * groups + c0 / 16) * (NS * 16 * DKP);
+            const __nv_bfloat16* const wp = a.du + (unit * groups + c0 / 16) * (NS * kC * 16);
+            const __nv_bfloat16* const up = a.writes + (unit * groups + c0 / 16) * (NS * kC * 16);
+#pragma unroll
+            for (int i = tid; i < W::kState / 16; i += W::threads) {
+                const bool there = i < have * NS * 16 * DKP / 8;
+                copy16(st + W::S + i * 16, there ? sp + i * 8 : sp, there);
+                copy16(st + W::dS + i * 16, there ? dp + i * 8 : dp, there);
+            }
+#pragma unroll
+            for (int i = tid; i < W::kRows / 16; i += W::threads) {
+                const bool there = i < have * NS * kC * 2;
+                copy16(st + W::W + i * 16, there ? wp + i * 8 : wp, there);
+                copy16(st + W::U + i * 16, there ? up + i * 8 : up, there);
+            }
+            load_rows<SL, W::threads>(st + W::Y, a.dy, XT, b, n, h * a.dv + c0, cols, tid);
         }
-        for (int i = tid; i < W::kDu / 16; i += W::threads) {
-            const bool there = i < have * NS * kC * 2;
-            copy16(st + W::dU + i * 16, there ? up + i * 8 : up, there);
-        }
-        load_rows<SL, W::threads>(st + W::V, a.v, XT, b, n, h * a.dv + c0, cols, tid);
-        load_rows<SL, W::threads>(st + W::Y, a.dy, XT, b, n, h * a.dv + c0, cols, tid);
         copies_commit();
     };
     load_rows<DKP, W::threads>(base + W::K, a.k, XT, b, n, kh * a.dk, a.dk, tid);
     load_rows<DKP, W::threads>(base + W::Q, a.q, XT, b, n, kh * a.dk, a.dk, tid);
 #pragma unroll
-    for (int pl = 0; pl < NS; ++pl)
-        load_tri<W::threads>(base + W::T + pl * W::kPlane, a.tri + (unit * a.tri_planes + pl) * int64_t(kC * kC), tid);
-    load(0);
+    for (int s = 0; s + 1 < W::stages; ++s) load(s);
     for (int i = tid; i < kVecs * kC; i += W::threads) vec[i] = a.vec[unit * kVecs * kC + i];
 
     const Lane L(lane);
     const int row[2] = {16 * mi + g, 16 * mi + g + 8};   // of a lane's accumulators
     float dq[2 * DN][4] = {}, k2[2 * DN][4] = {}, k3[2 * DN][4] = {}, m[2][4] = {}, nn[2][4] = {};
-    float a2[2] = {}, wu[2] = {}, ss = 0.f;
+    float ss = 0.f;
     for (int s = 0; s < nslices; ++s) {
-        if (W::stages == 1 && s > 0) {
-            __syncthreads();
-            load(s);
-        }
-        copies_wait<0>();
+        copies_wait<W::stages - 2>();
         __syncthreads();
-        if (W::stages == 2 && s + 1 < nslices) load(s + 1);
-        const int so = W::slices + (W::stages == 2 ? (s & 1) * W::stage : 0);
+        load(s + W::stages - 1);
+        const int so = W::slices + s % W::stages * W::stage;
         const uint32_t st = base + so;
-        float du[4] = {};   // W at this lane's places of the slice
-        if (qf < SL / 8) {   // K S, then beta R = beta (V - e^gam K S)
-            const uint32_t Sg = st + W::S + (qf >> 1) * (NS * 16 * DKP * 2);
-            float ks[4] = {};
-#pragma unroll
-            for (int kq = 0; kq < KT / 2; ++kq) {
-                uint32_t ka[XT][2][4];
-#pragma unroll
-                for (int t = 0; t < XT; ++t)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e)
-                        ldsm4(ka[t][e], base + W::K + t * W::kTile + tile_at<DKP>(16 * mi + L.rA, 4 * kq + 2 * e + L.uA));
-#pragma unroll
-                for (int t = 0; t < NS; ++t) {
-                    uint32_t f[4];
-                    ldsm4(f, Sg + t * (16 * DKP * 2) + tile_at<DKP>(8 * (qf & 1) + (lane & 7), 4 * kq + (lane >> 3)));
-#pragma unroll
-                    for (int i = 0; i < XT; ++i) {
-                        if (i + t >= NS) continue;
-                        mma(ks, ka[i][0], f[0], f[1]);
-                        mma(ks, ka[i][1], f[2], f[3]);
-                    }
-                }
-            }
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int r = row[e];
-                float v[2] = {};
-#pragma unroll
-                for (int t = XT - 1; t >= 0; --t) {
-                    const uint32_t x = *reinterpret_cast<const uint32_t*>(smem + so + W::V + t * W::kVal + tile_at<SL>(r, qf) + qd * 4);
-                    v[0] += __uint_as_float(x << 16);
-                    v[1] += __uint_as_float(x & 0xFFFF0000u);
-                }
-#pragma unroll
-                for (int t = NS - 1; t >= 0; --t) {
-                    const uint32_t x = *reinterpret_cast<const uint32_t*>(smem + so + W::dU + (qf >> 1) * (NS * kC * 32) + t * (kC * 32) +
-                                                                           tile_at<16>(r, qf & 1) + qd * 4);
-                    du[2 * e] += __uint_as_float(x << 16);
-                    du[2 * e + 1] += __uint_as_float(x & 0xFFFF0000u);
-                }
-                a2[e] = fmaf(du[2 * e], ks[2 * e], a2[e]);
-                a2[e] = fmaf(du[2 * e + 1], ks[2 * e + 1], a2[e]);
-                const float bt = strength(vec[kC + r]);
-                uint32_t o[NS];
-                split2<NS>(bt * fmaf(-vec[r], ks[2 * e], v[0]), bt * fmaf(-vec[r], ks[2 * e + 1], v[1]), o);
-#pragma unroll
-                for (int t = 0; t < NS; ++t) st_word(base + W::R + t * W::kVal + tile_at<SL>(r, qf) + qd * 4, o[t]);
-            }
-        }
-        __syncthreads();
-        if (qf < SL / 8) {   // U = T (beta R)
-            float u[4] = {};
-#pragma unroll
-            for (int kq = 0; kq < 2; ++kq) {
-                if (kq > (mi >> 1)) continue;
-                uint32_t f[NS][4];
-#pragma unroll
-                for (int t = 0; t < NS; ++t) ldsm4t(f[t], base + W::R + t * W::kVal + tile_at<SL>(32 * kq + lane, qf));
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    if (2 * kq + e > mi) continue;
-#pragma unroll
-                    for (int t = 0; t < NS; ++t) {
-                        uint32_t ta[4];
-                        ldsm4(ta, base + W::T + t * W::kPlane + tile_at<kC>(16 * mi + L.rA, 4 * kq + 2 * e + L.uA));
-#pragma unroll
-                        for (int i = 0; i < NS - t; ++i) mma(u, ta, f[i][2 * e], f[i][2 * e + 1]);
-                    }
-                }
-            }
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                wu[e] = fmaf(u[2 * e], du[2 * e], wu[e]);
-                wu[e] = fmaf(u[2 * e + 1], du[2 * e + 1], wu[e]);
-                const float bt = vec[kC + row[e]], own = bt / strength(bt);   // 1, or nothing where nothing is written
-                uint32_t o[NS];
-                split2<NS>(own * u[2 * e], own * u[2 * e + 1], o);
-#pragma unroll
-                for (int t = 0; t < NS; ++t) st_word(base + W::U + t * W::kVal + tile_at<SL>(row[e], qf) + qd * 4, o[t]);
-            }
-        }
-        // <dS', S>, both in the same tiles
-        for (int i = tid; i < SL / 16 * 16 * DKP / 8; i += W::threads) {
-            const int gr = i / (16 * DKP / 8), o = gr * (NS * 16 * DKP * 2) + (i - gr * (16 * DKP / 8)) * 16;
-            float x[8] = {}, y[8] = {};
-#pragma unroll
-            for (int t = NS - 1; t >= 0; --t) {
-                const uint4 p = *reinterpret_cast<const uint4*>(smem + so + W::S + o + t * (16 * DKP * 2));
-                const uint4 q = *reinterpret_cast<const uint4*>(smem + so + W::dS + o + t * (16 * DKP * 2));
-                const uint32_t pw[4] = {p.x, p.y, p.z, p.w}, qw[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    x[2 * e] += __uint_as_float(pw[e] << 16);
-                    x[2 * e + 1] += __uint_as_float(pw[e] & 0xFFFF0000u);
-                    y[2 * e] += __uint_as_float(qw[e] << 16);
-                    y[2 * e + 1] += __uint_as_float(qw[e] & 0xFFFF0000u);
-                }
-            }
-#pragma unroll
-            for (int e = 0; e < 8; ++e) ss = fmaf(x[e], y[e], ss);
-        }
-        __syncthreads();
 #pragma unroll
         for (int kt = 0; kt < SL / 16; ++kt) {
             const uint32_t Sg = st + W::S + kt * (NS * 16 * DKP * 2), Dg = st + W::dS + kt * (NS * 16 * DKP * 2);
+            const uint32_t Ug = st + W::U + kt * (NS * kC * 32);
             uint32_t wa[NS][4], ya[XT][4], ua[NS][4];
 #pragma unroll
             for (int t = 0; t < NS; ++t) {
-                ldsm4(wa[t], st + W::dU + kt * (NS * kC * 32) + t * (kC * 32) + tile_at<16>(16 * mi + L.rA, L.uA));
-                ldsm4(ua[t], base + W::U + t * W::kVal + tile_at<SL>(16 * mi + L.rA, 2 * kt + L.uA));
+                ldsm4(wa[t], st + W::W + kt * (NS * kC * 32) + t * (kC * 32) + tile_at<16>(16 * mi + L.rA, L.uA));
+                ldsm4(ua[t], Ug + t * (kC * 32) + tile_at<16>(16 * mi + L.rA, L.uA));
             }
 #pragma unroll
             for (int t = 0; t < XT; ++t) ldsm4(ya[t], st + W::Y + t * W::kVal + tile_at<SL>(16 * mi + L.rA, 2 * kt + L.uA));
             if (qf <= mi) {   // W U^T and dY U^T
-                auto at = [&](int) { return base + W::U + tile_at<SL>(16 * qf + L.rB, 2 * kt + L.uB); };
-                products<NS, NS, NS, false, 1>(m, wa, W::kVal, at);
-                products<XT, NS, NS, false, 1>(nn, ya, W::kVal, at);
+                auto at = [&](int) { return Ug + tile_at<16>(16 * qf + L.rB, L.uB); };
+                products<NS, NS, NS, false, 1>(m, wa, kC * 32, at);
+                products<XT, NS, NS, false, 1>(nn, ya, kC * 32, at);
             }
             // dY S^T, W S^T, U dS'^T
             auto sa = [&](int np) { return Sg + tile_at<DKP>(L.rBt, 2 * (DN * qf + np) + L.uBt); };
             auto da = [&](int np) { return Dg + tile_at<DKP>(L.rBt, 2 * (DN * qf + np) + L.uBt); };
             products<XT, NS, NS, true, DN>(dq, ya, 16 * DKP * 2, sa);
-            products<NS, NS, NG, true, DN>(k2, wa, 16 * DKP * 2, sa);
+            products<NS, NS, NS, true, DN>(k2, wa, 16 * DKP * 2, sa);
             products<NS, NS, NS, true, DN>(k3, ua, 16 * DKP * 2, da);
+        }
+        if (vec[kC - 1] != 0.f) {   // <dS', S>, both in the same tiles
+            for (int i = tid; i < SL / 16 * 16 * DKP / 8; i += W::threads) {
+                const int gr = i / (16 * DKP / 8), o = gr * (NS * 16 * DKP * 2) + (i - gr * (16 * DKP / 8)) * 16;
+                float x[8] = {}, y[8] = {};
+#pragma unroll
+                for (int t = NS - 1; t >= 0; --t) {
+                    const uint4 p = *reinterpret_cast<const uint4*>(smem + so + W::S + o + t * (16 * DKP * 2));
+                    const uint4 q = *reinterpret_cast<const uint4*>(smem + so + W::dS + o + t * (16 * DKP * 2));
+                    const uint32_t pw[4] = {p.x, p.y, p.z, p.w}, qw[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        x[2 * e] += __uint_as_float(pw[e] << 16);
+                        x[2 * e + 1] += __uint_as_float(pw[e] & 0xFFFF0000u);
+                        y[2 * e] += __uint_as_float(qw[e] << 16);
+                        y[2 * e + 1] += __uint_as_float(qw[e] & 0xFFFF0000u);
+                    }
+                }
+#pragma unroll
+                for (int e = 0; e < 8; ++e) ss = fmaf(x[e], y[e], ss);
+            }
         }
     }
     // A and G once more, in float32
@@ -469,6 +387,7 @@ __global__ void __launch_bounds__(512) gdr_grad_kernel(const __grid_constant__ A
                 float d = 0.f;
                 if (j + c <= i) d = decay<XT>((vec[3 * kC + i] - vec[3 * kC + j + c]) + (vec[4 * kC + i] - vec[4 * kC + j + c]));
                 const float N = a.scale * nn[t][2 * e + c], M = vec[kC + i] * m[t][2 * e + c];
+                if (j + c == i) diag[i] = m[t][2 * e + c];
                 x[c] = j + c <= i ? d * N : 0.f;
                 y[c] = j + c < i ? -d * M : 0.f;
                 Z[i * 65 + j + c] = j + c < i ? fmaf(x[c], qk[t][2 * e + c], y[c] * kk[t][2 * e + c]) : 0.f;
@@ -481,11 +400,11 @@ __global__ void __launch_bounds__(512) gdr_grad_kernel(const __grid_constant__ A
 #pragma unroll
             for (int p = 0; p < NG; ++p) st_word(base + W::XD + p * W::kPlane + tile_at<kC>(i, j >> 3) + qd * 4, o[p]);
         }
-    // the rows' scalars: a = e^gam (scale q . (S dY) - beta W . (S^T k)), e = e^(gam_last - gam) k . (dS' u), W . U
+    // the rows' scalars: a = e^gam (scale q . (S dY) - beta k . (S W)), e = e^(gam_last - gam) k . (dS' u)
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
         const int r = row[e];
-        float qd1 = 0.f, kd3 = 0.f;
+        float qd1 = 0.f, kd2 = 0.f, kd3 = 0.f;
 #pragma unroll
         for (int t = 0; t < 2 * DN; ++t) {
             const uint32_t at = tile_at<DKP>(r, 2 * DN * qf + t) + qd * 4;
@@ -502,13 +421,14 @@ __global__ void __launch_bounds__(512) gdr_grad_kernel(const __grid_constant__ A
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
                 qd1 = fmaf(q[c], dq[t][2 * e + c], qd1);
+                kd2 = fmaf(k[c], k2[t][2 * e + c], kd2);
                 kd3 = fmaf(k[c], k3[t][2 * e + c], kd3);
             }
         }
         const float eg = vec[r], be = vec[kC + r], c = vec[2 * kC + r];
-        float x[3] = {eg * (a.scale * qd1 - be * a2[e]), c * kd3, wu[e]};
+        float x[2] = {eg * (a.scale * qd1 - be * kd2), c * kd3};
 #pragma unroll
-        for (int i = 0; i < 3; ++i) {
+        for (int i = 0; i < 2; ++i) {
             x[i] += __shfl_xor_sync(kFull, x[i], 1);
             x[i] += __shfl_xor_sync(kFull, x[i], 2);
             if (qd == 0) sums[i][qf][r] = x[i];
@@ -584,7 +504,7 @@ __global__ void __launch_bounds__(512) gdr_grad_kernel(const __grid_constant__ A
 #pragma unroll
             for (int i = 0; i < 16; ++i) s += inner[i];
             x = fmaf(vec[kC - 1], s, x);
-            const float db = (sums[2][0][t] + sums[2][1][t] + sums[2][2][t] + sums[2][3][t]) / strength(vec[kC + t]);
+            const float db = diag[t] / vec[kC + t];
             const int64_t gi = (b + t) * a.dg_ld + h, bi = (b + t) * a.db_ld + h;
             if (a.g_bf16) {
                 static_cast<__nv_bfloat16*>(a.dg)[gi] = __float2bfloat16_rn(x);
@@ -729,7 +649,7 @@ extern "C" sdm_status sdm_gdr_backward(const sdm_gdr_shape* shape, const void* q
     if (!checks::aligned_all(16, {states, dhT, dh0})) return SDM_ERR_ALIGN;
     a.dq = dq; a.dq_ld = dq_ld; a.dk_out = dk; a.dk_ld = dk_ld; a.dv_out = dv; a.dv_ld = dv_ld;
     a.dg = dg; a.dg_ld = dg_ld; a.dbeta = dbeta; a.db_ld = dbeta_ld; a.dhT = dhT; a.dh0 = dh0;
-    a.states = static_cast<__nv_bfloat16*>(const_cast<void*>(states));
+    set_states(shape, const_cast<void*>(states), &a);
     const Layout l = layout(shape, true);
     unsigned char* const w = static_cast<unsigned char*>(ws);
     a.dstates = reinterpret_cast<__nv_bfloat16*>(w + l.dstates);

@@ -140,6 +140,8 @@ def oracle(x, cuts, scale, x_dtype, train=True):
     R = Hv // Hk
     dev = deviations(x_dtype)
     names = {"y": "v", "hT": "h0"} | ({"dq": "q", "dk": "k", "dv": "v", "dg": "g", "dbeta": "g", "dh0": "h0"} if train else {})
+    # a strength below 2^-80 counts as 2^-80
+    x = x | {"beta": np.where(np.abs(x["beta"]) < 2.0 ** -80, np.copysign(2.0 ** -80, x["beta"]), x["beta"])}
     val = {n: np.full_like(x[m], np.nan) for n, m in names.items()}
     tol = {n: np.zeros_like(x[m]) for n, m in names.items()}
     for n in ("dq", "dk"):
