@@ -75,6 +75,7 @@ typedef enum { SDM_F32 = 0, SDM_BF16 = 1 } sdm_dtype;
 #define SDM_DEV_BAD_POSITION 0x4u /* a position at or above max_pos: treated as padding */
 #define SDM_DEV_BAD_TARGET 0x8u   /* a target at or above V: treated as ignored */
 #define SDM_DEV_BAD_TOKEN 0x10u   /* a token id at or above V: treated as padding */
+#define SDM_DEV_STALLED 0x20u     /* a wait inside a kernel ran out: the call's outputs are not valid */
 
 typedef struct {
     int32_t P;              /* streams */

@@ -16,6 +16,7 @@ SDM_DEV_BAD_OFFSET = 0x2
 SDM_DEV_BAD_POSITION = 0x4
 SDM_DEV_BAD_TARGET = 0x8
 SDM_DEV_BAD_TOKEN = 0x10
+SDM_DEV_STALLED = 0x20
 SDM_GLR_CHUNK = 64
 SDM_GDR_CHUNK = 64
 

@@ -326,7 +326,7 @@ __global__ void __launch_bounds__(BV * 2) gdr_walk_kernel(const __grid_constant_
             terms_of<NS>(S[2 * kt], S[2 * kt + 1], s);
             if (a.states != nullptr) {
 #pragma unroll
-                for (int t = 0; t < NS; ++t) stsm4(keep + t * (16 * DKP * 2) + tile_at<DKP>(L.rA, 2 * kt + L.uA), s[t]);
+                for (int t = 0; t < NS; ++t) stsm4(keep + t * (16 * DKP * 2) + state_at(L.rA, 2 * kt + L.uA), s[t]);
             }
             products<NS, XT, NS, false, 4>(r, s, W::kTile, [&](int np) { return st + W::K + tile_at<DKP>(16 * np + L.rB, 2 * kt + L.uB); });
             products<NS, XT, NS, false, 4>(o, s, W::kTile, [&](int np) { return st + W::Q + tile_at<DKP>(16 * np + L.rB, 2 * kt + L.uB); });
@@ -386,7 +386,7 @@ __global__ void __launch_bounds__(BV * 2) gdr_walk_kernel(const __grid_constant_
             terms_of<NS>(u[2 * kt], u[2 * kt + 1], f);
             if (a.states != nullptr) {
 #pragma unroll
-                for (int t = 0; t < NS; ++t) stsm4t(keep + t * (kC * 32) + tile_at<16>(16 * kt + L.rAt, L.uAt), f[t]);
+                for (int t = 0; t < NS; ++t) stsm4t(keep + t * (kC * 32) + rows_at(16 * kt + L.rAt, L.uAt), f[t]);
             }
             products<NS, XT, NS, false, 4>(o, f, W::kPlane, [&](int np) { return st + W::A + tile_at<kC>(16 * np + L.rB, 2 * kt + L.uB); }, kt);
 #pragma unroll

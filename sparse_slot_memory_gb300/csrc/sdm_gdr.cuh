@@ -292,6 +292,11 @@ __device__ __forceinline__ void products(float (&acc)[M][4], const uint32_t (&a)
     }
 }
 
+// The saved tiles lie in cores of 8 rows of 16 bytes (sdm_tensor.cuh): states [16 value columns][dk], writes and their gradients
+// [64 rows][16 value columns]; row r, unit u of 8 columns.
+__device__ __forceinline__ uint32_t state_at(int r, int u) { return static_cast<uint32_t>(u * 256 + (r >> 3) * 128 + (r & 7) * 16); }
+__device__ __forceinline__ uint32_t rows_at(int r, int u) { return static_cast<uint32_t>(u * 1024 + (r >> 3) * 128 + (r & 7) * 16); }
+
 // A whole tile in shared memory leaves for contiguous global memory by itself; the writes before were the block's own.
 __device__ __forceinline__ void bulk_store(void* dst, uint32_t src, int bytes) {
     asm volatile("cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;" ::"l"(dst), "r"(src), "r"(bytes) : "memory");

@@ -16,6 +16,7 @@
 // carries S (a warp 16 value columns, transposed, nothing leaves its registers) and writes dV, W and every block's dS'; and one
 // for all blocks at once that has the rest, from the states and the writes that the forward saved.
 #include "sdm_gdr.cuh"
+#include "sdm_tensor.cuh"
 
 namespace sdm {
 namespace gdr {
@@ -102,7 +103,7 @@ __global__ void __launch_bounds__(BV * 2) gdr_back_kernel(const __grid_constant_
             uint32_t s[NS][4];
             terms_of<NS>(S[2 * kt], S[2 * kt + 1], s);
 #pragma unroll
-            for (int t = 0; t < NS; ++t) stsm4(keep + t * (16 * DKP * 2) + tile_at<DKP>(L.rA, 2 * kt + L.uA), s[t]);
+            for (int t = 0; t < NS; ++t) stsm4(keep + t * (16 * DKP * 2) + state_at(L.rA, 2 * kt + L.uA), s[t]);
             products<NS, XT, NS, false, 4>(x, s, W::kTile, [&](int np) { return st + W::K + tile_at<DKP>(16 * np + L.rB, 2 * kt + L.uB); });
         }
         async_fence();
@@ -164,7 +165,7 @@ __global__ void __launch_bounds__(BV * 2) gdr_back_kernel(const __grid_constant_
             uint32_t f[NS][4], o[NS][4];
             terms_of<NS>(x[2 * kt], x[2 * kt + 1], f);
 #pragma unroll
-            for (int t = 0; t < NS; ++t) stsm4t(keep + t * (kC * 32) + tile_at<16>(16 * kt + L.rAt, L.uAt), f[t]);
+            for (int t = 0; t < NS; ++t) stsm4t(keep + t * (kC * 32) + rows_at(16 * kt + L.rAt, L.uAt), f[t]);
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
                 const float2 bt = *reinterpret_cast<const float2*>(vec + kC + 16 * kt + 8 * t + 2 * qd);
@@ -229,7 +230,7 @@ __global__ void __launch_bounds__(BV * 2) gdr_back_kernel(const __grid_constant_
     if (lane == 0) bulk_wait();
 }
 
-// ---- all blocks at once ---------------------------------------------------------------------------------------------
+// ---- all blocks at once, float32 rows ---------------------------------------------------------------------------------
 // 16 warps: warp w has rows 16 (w % 4) .. of everything, and of each product's columns the (w / 4)-th part: 16 of the 64 columns
 // of M and N, a quarter of dk. A block walks the value columns in slices of SL, the next ones' states, writes and gradients on
 // their way; all operands come from shared memory as they were stored, so a slice needs one barrier.
@@ -319,19 +320,19 @@ __global__ void __launch_bounds__(512) gdr_grad_kernel(const __grid_constant__ A
             uint32_t wa[NS][4], ya[XT][4], ua[NS][4];
 #pragma unroll
             for (int t = 0; t < NS; ++t) {
-                ldsm4(wa[t], st + W::W + kt * (NS * kC * 32) + t * (kC * 32) + tile_at<16>(16 * mi + L.rA, L.uA));
-                ldsm4(ua[t], Ug + t * (kC * 32) + tile_at<16>(16 * mi + L.rA, L.uA));
+                ldsm4(wa[t], st + W::W + kt * (NS * kC * 32) + t * (kC * 32) + rows_at(16 * mi + L.rA, L.uA));
+                ldsm4(ua[t], Ug + t * (kC * 32) + rows_at(16 * mi + L.rA, L.uA));
             }
 #pragma unroll
             for (int t = 0; t < XT; ++t) ldsm4(ya[t], st + W::Y + t * W::kVal + tile_at<SL>(16 * mi + L.rA, 2 * kt + L.uA));
             if (qf <= mi) {   // W U^T and dY U^T
-                auto at = [&](int) { return Ug + tile_at<16>(16 * qf + L.rB, L.uB); };
+                auto at = [&](int) { return Ug + rows_at(16 * qf + L.rB, L.uB); };
                 products<NS, NS, NS, false, 1>(m, wa, kC * 32, at);
                 products<XT, NS, NS, false, 1>(nn, ya, kC * 32, at);
             }
             // dY S^T, W S^T, U dS'^T
-            auto sa = [&](int np) { return Sg + tile_at<DKP>(L.rBt, 2 * (DN * qf + np) + L.uBt); };
-            auto da = [&](int np) { return Dg + tile_at<DKP>(L.rBt, 2 * (DN * qf + np) + L.uBt); };
+            auto sa = [&](int np) { return Sg + state_at(L.rBt, 2 * (DN * qf + np) + L.uBt); };
+            auto da = [&](int np) { return Dg + state_at(L.rBt, 2 * (DN * qf + np) + L.uBt); };
             products<XT, NS, NS, true, DN>(dq, ya, 16 * DKP * 2, sa);
             products<NS, NS, NS, true, DN>(k2, wa, 16 * DKP * 2, sa);
             products<NS, NS, NS, true, DN>(k3, ua, 16 * DKP * 2, da);
@@ -558,6 +559,390 @@ __global__ void __launch_bounds__(512) gdr_grad_kernel(const __grid_constant__ A
         }
 }
 
+// ---- all blocks at once, bfloat16 rows --------------------------------------------------------------------------------
+// All of the slices' products read what is stored as it is, so they are the fifth-generation tensor core's: one thread issues them,
+// the sums stay in tensor memory, and the threads turn to them when a block's slices are through. Rows are stacked to the
+// instruction's 128, [W; dY] against S and U, [U; W] against dS' (its lower half is not used), [K; Q] against K:
+//   D1 = [W; dY] S^T, D2 = [U; .] dS'^T, D3 = [W; dY] U^T, D4 = [K; Q] K^T, then with the decays in
+//   D5 = [-(M o D); N o D] K, D6 = (N o D)^T Q - (M o D)^T K,
+// so a thread that has row r of tensor memory has row r of the key's side (r < 64) or row r - 64 of the query's. Resident
+// blocks take (block of rows, head) after (block, head); the next ones' rows and states arrive while these are finished.
+template <int DKP>
+struct GradTc {
+    static constexpr int kGroup = 2 * 6144;                  // rows of 16 value columns: per core along K [U | W | dY], then the rests [U | W | 0]
+    static constexpr int kImage = 16 * DKP * 2, kStates = 4 * kImage;
+    static constexpr int rows = 0, S = 2 * kGroup, dS = S + kStates, stage = dS + kStates;
+    static constexpr int kKQ = DKP / 8 * 2048;               // [K; Q], two of them
+    static constexpr int slices = 2 * kKQ, XN = slices + 2 * stage, Z = XN + 16384, bytes = Z + kC * 65 * 4;
+    static constexpr int threads = 256;
+};
+
+__device__ __forceinline__ uint32_t stacked_at(int r, int u) { return static_cast<uint32_t>(u * 2048 + (r >> 3) * 128 + (r & 7) * 16); }
+
+template <int DKP>
+__global__ void __launch_bounds__(256) gdr_grad_tc_kernel(const __grid_constant__ Args a) {
+    using W = GradTc<DKP>;
+    constexpr int HC = DKP / 2;   // columns of dk of a thread
+    extern __shared__ __align__(1024) unsigned char smem[];
+    __shared__ __align__(16) float vecs[2][kVecs * kC];
+    __shared__ float sums[3][2][kC];   // scale-free q . (S dY), k . (S W), k . (dS' u) by halves of dk
+    __shared__ float diag[kC];         // W . U
+    __shared__ float share[2][kC];     // a and e
+    __shared__ float inner[8];
+    __shared__ __align__(8) uint64_t bars[3];   // a stage's products each, and the last ones
+    __shared__ uint32_t tmem;
+    start_dependent();
+    const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
+    const uint32_t base = smem_of(smem), bar = smem_of(bars);
+    const int groups = (a.dv + 15) / 16, nslices = (groups + 1) / 2;
+    const int64_t units = (a.rows / kC + a.P) * a.Hv;
+
+    struct Unit {
+        int64_t id, b;   // id: block x head
+        int h, n;
+    };
+    auto find = [&](int64_t id) {   // the first one from id on, in steps of the grid, that has rows
+        Unit u;
+        u.n = 0;
+        for (u.id = id; u.id < units; u.id += gridDim.x) {
+            const int64_t blk = u.id / a.Hv;
+            u.h = static_cast<int>(u.id - blk * a.Hv);
+            block_rows(a, blk, u.b, u.n);
+            if (u.n > 0) break;
+        }
+        return u;
+    };
+    Unit lu = find(blockIdx.x);   // what is loaded next
+    int ls = 0, lkq = 0;
+    int64_t issued = 0;           // slices on their way or there
+    auto load = [&]() {
+        if (lu.id < units) {
+            const uint32_t st = base + W::slices + static_cast<int>(issued & 1) * W::stage;
+            const int g0 = 2 * ls, have = min(2, groups - g0), c0 = 32 * ls, cols = min(32, a.dv - c0);
+            const __nv_bfloat16* const sp = a.states + (lu.id * groups + g0) * (2 * 16 * DKP);
+            const __nv_bfloat16* const dp = a.dstates + (lu.id * groups + g0) * (2 * 16 * DKP);
+            const __nv_bfloat16* const wp = a.du + (lu.id * groups + g0) * (2 * kC * 16);
+            const __nv_bfloat16* const up = a.writes + (lu.id * groups + g0) * (2 * kC * 16);
+#pragma unroll
+            for (int i = tid; i < W::kStates / 16; i += W::threads) {
+                const bool there = i < have * 2 * W::kImage / 16;
+                copy16(st + W::S + i * 16, there ? sp + i * 8 : sp, there);
+                copy16(st + W::dS + i * 16, there ? dp + i * 8 : dp, there);
+            }
+#pragma unroll
+            for (int i = tid; i < 512; i += W::threads) {   // group, term, core along K, row
+                const bool there = i < have * 256;
+                const uint32_t to = st + W::rows + (i >> 8) * W::kGroup + (i >> 7 & 1) * 6144 + (i >> 6 & 1) * 3072 + (i & 63) * 16;
+                copy16(to, there ? up + i * 8 : up, there);
+                copy16(to + 1024, there ? wp + i * 8 : wp, there);
+            }
+            {
+                const int r = tid >> 2, u = tid & 3;
+                const bool there = r < lu.n && u * 8 < cols;
+                copy16(st + W::rows + (u >> 1) * W::kGroup + (u & 1) * 3072 + 2048 + r * 16,
+                       there ? a.dy.p + (lu.b + r) * a.dy.ld + lu.h * a.dv + c0 + u * 8 : a.dy.p, there);
+            }
+            if (ls == 0) {
+                const int kh = lu.h / (a.Hv / a.Hk);
+#pragma unroll
+                for (int i = tid; i < 2 * kC * (DKP / 8); i += W::threads) {
+                    const int r = i / (DKP / 8), u = i % (DKP / 8), t = r & 63;
+                    const Planes& x = r < kC ? a.k : a.q;
+                    const bool there = t < lu.n && u * 8 < a.dk;
+                    copy16(base + lkq * W::kKQ + stacked_at(r, u), there ? x.p + (lu.b + t) * x.ld + kh * a.dk + u * 8 : x.p, there);
+                }
+                if (tid < kVecs * kC / 4) copy16(smem_of(vecs[lkq]) + tid * 16, a.vec + lu.id * kVecs * kC + tid * 4, true);
+            }
+            if (++ls == nslices) {
+                ls = 0;
+                lkq ^= 1;
+                lu = find(lu.id + gridDim.x);
+            }
+        }
+        copies_commit();
+        ++issued;
+    };
+    // zeros under dY's rests stay
+    for (int i = tid; i < 2 * 2 * 2 * 64; i += W::threads) {
+        const int at = W::slices + (i >> 8) * W::stage + W::rows + (i >> 7 & 1) * W::kGroup + 6144 + (i >> 6 & 1) * 3072 + 2048 + (i & 63) * 16;
+        *reinterpret_cast<uint4*>(smem + at) = make_uint4(0, 0, 0, 0);
+    }
+    if (w == 0) tensor::allocate<512>(smem_of(&tmem));
+    if (tid == 0) {
+        for (int i = 0; i < 3; ++i) tensor::barrier_init(bar + 8 * i, 1);
+        tensor::barrier_fence();
+    }
+    Unit u = lu;
+    load();
+    tensor::fence_before();
+    __syncthreads();
+    tensor::fence_after();
+    const uint32_t D1 = tmem, D2 = D1 + 128, D3 = D1 + 256, D4 = D1 + 320, D5 = D1 + 384, D6 = D1 + 256;
+    const uint32_t mine = static_cast<uint32_t>(w & 3) << 21;   // this warp's 32 rows
+    const int r = 32 * (w & 3) + lane, half = w >> 2, i = r & 63;
+    const bool key = r < kC;                                    // the key's side
+    uint32_t phase[3] = {};
+    int64_t waited[2] = {}, step = 0;   // steps whose products were waited for, by stage
+    bool bad = false;
+    int kq = 0;
+    auto wait_stage = [&](int s, int64_t before) {   // the products of the stage's steps before step `before`
+        while (waited[s] < (before - s + 1) / 2) {
+            bad |= !tensor::barrier_wait(bar + 8 * s, phase[s]);
+            phase[s] ^= 1;
+            ++waited[s];
+        }
+    };
+    while (u.id < units) {
+        const uint32_t KQ = base + kq * W::kKQ;
+        const float* const vec = vecs[kq];
+        float ss = 0.f;
+        bool out = false;
+        for (int s = 0; s < nslices; ++s, ++step) {
+            if (issued == step + 2) copies_wait<1>();
+            else copies_wait<0>();
+            async_fence();
+            out = __syncthreads_or(bad);
+            if (out) break;
+            const int sg = static_cast<int>(step & 1), so = W::slices + sg * W::stage;
+            if (tid == 0) {
+                tensor::fence_after();
+                const uint32_t st = base + so;
+                if (s == 0)
+                    for (int ks = 0; ks < DKP / 16; ++ks) {
+                        const uint64_t x = tensor::operand(KQ + ks * 4096, 2048, 128);
+                        tensor::mma(D4, x, x, tensor::shape(128, 64, false, false), ks > 0);
+                    }
+                for (int gr = 0; gr < min(2, groups - 2 * s); ++gr) {
+                    const uint32_t hi = st + W::rows + gr * W::kGroup, lo = hi + 6144;
+                    const uint64_t wy = tensor::operand(hi + 1024, 3072, 128), w0 = tensor::operand(lo + 1024, 3072, 128);
+                    const uint64_t uh = tensor::operand(hi, 3072, 128), ul = tensor::operand(lo, 3072, 128);
+                    const uint32_t sa = st + W::S + gr * 2 * W::kImage, da = st + W::dS + gr * 2 * W::kImage;
+                    const uint64_t sh = tensor::operand(sa, 128, 256), sl = tensor::operand(sa + W::kImage, 128, 256);
+                    const uint64_t dh = tensor::operand(da, 128, 256), dl = tensor::operand(da + W::kImage, 128, 256);
+                    constexpr uint32_t wide = tensor::shape(128, DKP, false, true), square = tensor::shape(128, 64, false, false);
+                    const bool add = s + gr > 0;
+                    tensor::mma(D3, wy, uh, square, add);
+                    tensor::mma(D3, wy, ul, square, true);
+                    tensor::mma(D3, w0, uh, square, true);
+                    tensor::mma(D3, w0, ul, square, true);   // W . U, which dbeta takes, to 2^-17
+                    tensor::mma(D1, wy, sh, wide, add);
+                    tensor::mma(D1, wy, sl, wide, true);
+                    tensor::mma(D1, w0, sh, wide, true);
+                    tensor::mma(D2, uh, dh, wide, add);
+                    tensor::mma(D2, uh, dl, wide, true);
+                    tensor::mma(D2, ul, dh, wide, true);
+                }
+                tensor::commit(bar + 8 * sg);
+            }
+            if (issued == step + 1) {   // the other stage is free once its products are done
+                wait_stage(sg ^ 1, step);
+                load();
+            }
+            if (vec[kC - 1] != 0.f) {   // <dS', S>, both in the same tiles
+                for (int x = tid; x < 2 * 16 * DKP / 8; x += W::threads) {
+                    const int o = x / (W::kImage / 16) * (2 * W::kImage) + x % (W::kImage / 16) * 16;
+                    float p[8] = {}, q[8] = {};
+#pragma unroll
+                    for (int t = 1; t >= 0; --t) {
+                        const uint4 y = *reinterpret_cast<const uint4*>(smem + so + W::S + o + t * W::kImage);
+                        const uint4 z = *reinterpret_cast<const uint4*>(smem + so + W::dS + o + t * W::kImage);
+                        const uint32_t yw[4] = {y.x, y.y, y.z, y.w}, zw[4] = {z.x, z.y, z.z, z.w};
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            p[2 * e] += __uint_as_float(yw[e] << 16);
+                            p[2 * e + 1] += __uint_as_float(yw[e] & 0xFFFF0000u);
+                            q[2 * e] += __uint_as_float(zw[e] << 16);
+                            q[2 * e + 1] += __uint_as_float(zw[e] & 0xFFFF0000u);
+                        }
+                    }
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) ss = fmaf(p[e], q[e], ss);
+                }
+            }
+        }
+        if (out) break;
+        wait_stage(0, step);
+        wait_stage(1, step);
+        __syncthreads();   // the last stage's states have been read
+        if (ls != 0 || lkq != kq) load();   // not yet queries and keys in these ones' place
+        tensor::fence_after();
+        // N o D and - M o D, and the terms of dg that both give
+        float* const Z = reinterpret_cast<float*>(smem + W::Z);
+        {
+            float x[32], y[32];
+            tensor::load32(D3 + mine + 32 * half, x);
+            tensor::load32(D4 + mine + 32 * half, y);
+            tensor::loaded();
+            const float gh = vec[3 * kC + i], gl = vec[4 * kC + i], mul = key ? -vec[kC + i] : a.scale;
+            float z[32];
+#pragma unroll
+            for (int c = 0; c < 32; ++c) {
+                const int j = 32 * half + c;
+                if (key && j == i) diag[i] = x[c];
+                const float d = decay<1>((gh - vec[3 * kC + j]) + (gl - vec[4 * kC + j]));
+                x[c] = j < i || (!key && j == i) ? d * (mul * x[c]) : 0.f;
+                z[c] = j < i ? x[c] * y[c] : 0.f;
+            }
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                *reinterpret_cast<uint4*>(smem + W::XN + stacked_at(r, 4 * half + q)) =
+                    make_uint4(round2(x[8 * q], x[8 * q + 1]), round2(x[8 * q + 2], x[8 * q + 3]), round2(x[8 * q + 4], x[8 * q + 5]),
+                               round2(x[8 * q + 6], x[8 * q + 7]));
+            async_fence();
+            tensor::fence_before();
+            if (key) {
+#pragma unroll
+                for (int c = 0; c < 32; ++c) Z[i * 65 + 32 * half + c] = z[c];
+            }
+            __syncthreads();
+            if (tid == 0) {
+                tensor::fence_after();
+                constexpr uint32_t out5 = tensor::shape(128, DKP, false, true), out6 = tensor::shape(128, DKP, true, true);
+                const uint32_t XN = base + W::XN;
+                for (int ks = 0; ks < 4; ++ks) {
+                    const uint64_t k = tensor::operand(KQ + ks * 256, 128, 2048), q = tensor::operand(KQ + 1024 + ks * 256, 128, 2048);
+                    tensor::mma(D5, tensor::operand(XN + ks * 4096, 2048, 128), k, out5, ks > 0);
+                    tensor::mma(D6, tensor::operand(XN + 1024 + ks * 256, 128, 2048), q, out6, ks > 0);
+                    tensor::mma(D6, tensor::operand(XN + ks * 256, 128, 2048), k, out6, true);
+                }
+                tensor::commit(bar + 16);
+            }
+            if (!key) {
+#pragma unroll
+                for (int c = 0; c < 32; ++c) Z[i * 65 + 32 * half + c] += z[c];
+            }
+        }
+        // the rows' products with their own queries and keys
+        {
+            float s1 = 0.f, s3 = 0.f;
+#pragma unroll
+            for (int p = 0; p < HC / 32; ++p) {
+                const int c0 = HC * half + 32 * p;
+                float v[32], t[32];
+                tensor::load32(D1 + mine + c0, v);
+                tensor::load32(D2 + mine + c0, t);
+                tensor::loaded();
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const uint4 x = *reinterpret_cast<const uint4*>(smem + kq * W::kKQ + stacked_at(r, c0 / 8 + q));
+                    const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const float k = __uint_as_float(e & 1 ? xw[e >> 1] & 0xFFFF0000u : xw[e >> 1] << 16);
+                        s1 = fmaf(k, v[8 * q + e], s1);
+                        s3 = fmaf(k, t[8 * q + e], s3);
+                    }
+                }
+            }
+            sums[key ? 1 : 0][half][i] = s1;
+            if (key) sums[2][half][i] = s3;
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o /= 2) ss += __shfl_xor_sync(kFull, ss, o);
+        if (lane == 0) inner[w] = ss;
+        __syncthreads();
+        if (tid < kC) {
+            const float eg = vec[tid];
+            share[0][tid] = eg * (a.scale * (sums[0][0][tid] + sums[0][1][tid]) - vec[kC + tid] * (sums[1][0][tid] + sums[1][1][tid]));
+            share[1][tid] = vec[2 * kC + tid] * (sums[2][0][tid] + sums[2][1][tid]);
+        }
+        // dg. Column by column sums from the bottom (16 rows a thread, then what lies below them), then row by row up to the diagonal.
+        {
+            const int j = tid & 63, part = tid >> 6;
+            float run = 0.f;
+#pragma unroll
+            for (int x = 15; x >= 0; --x) {
+                run += Z[(16 * part + x) * 65 + j];
+                Z[(16 * part + x) * 65 + j] = run;
+            }
+            __syncthreads();
+            float below = 0.f;
+            for (int q = 3; q > part; --q) below += Z[16 * q * 65 + j];
+            __syncthreads();
+            if (part < 3) {
+#pragma unroll
+                for (int x = 0; x < 16; ++x) Z[(16 * part + x) * 65 + j] += below;
+            }
+            __syncthreads();
+            const int t = tid >> 2, fourth = tid & 3;
+            float x = 0.f;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                const int c = 16 * fourth + e;   // a column before row t, its end's share, and a row from t on
+                x += c < t ? Z[t * 65 + c] + share[1][c] : share[0][c];
+            }
+            x += __shfl_xor_sync(kFull, x, 1);
+            x += __shfl_xor_sync(kFull, x, 2);
+            if (fourth == 0 && t < u.n) {
+                float s = 0.f;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) s += inner[e];
+                x = fmaf(vec[kC - 1], s, x);
+                const float db = diag[t] / vec[kC + t];
+                const int64_t gi = (u.b + t) * a.dg_ld + u.h, bi = (u.b + t) * a.db_ld + u.h;
+                if (a.g_bf16) {
+                    static_cast<__nv_bfloat16*>(a.dg)[gi] = __float2bfloat16_rn(x);
+                    static_cast<__nv_bfloat16*>(a.dbeta)[bi] = __float2bfloat16_rn(db);
+                } else {
+                    static_cast<float*>(a.dg)[gi] = x;
+                    static_cast<float*>(a.dbeta)[bi] = db;
+                }
+            }
+        }
+        // the rows' gradients: of a head's own queries and keys, or a value head's share of them in float32
+        bad |= !tensor::barrier_wait(bar + 16, phase[2]);
+        phase[2] ^= 1;
+        tensor::fence_after();
+        const float f1 = key ? -vec[i] * vec[kC + i] : a.scale * vec[i], f2 = vec[2 * kC + i];
+#pragma unroll
+        for (int p = 0; p < HC / 32; ++p) {
+            const int c0 = HC * half + 32 * p;
+            float v[32], t[32];
+            tensor::load32(D1 + mine + c0, v);
+            tensor::load32(D5 + mine + c0, t);
+            tensor::loaded();
+#pragma unroll
+            for (int c = 0; c < 32; ++c) v[c] = fmaf(f1, v[c], t[c]);
+            if (key) {   // whole warps
+                tensor::load32(D2 + mine + c0, t);
+                tensor::loaded();
+#pragma unroll
+                for (int c = 0; c < 32; ++c) v[c] = fmaf(f2, t[c], v[c]);
+                tensor::load32(D6 + mine + c0, t);
+                tensor::loaded();
+#pragma unroll
+                for (int c = 0; c < 32; ++c) v[c] += t[c];
+            }
+            if (i < u.n && a.part != nullptr) {
+                float* const to = a.part + ((key ? a.rows : 0) + u.b + i) * a.Hv * a.dk + u.h * a.dk + c0;
+#pragma unroll
+                for (int q = 0; q < 8; ++q)
+                    if (c0 + 4 * q < a.dk) *reinterpret_cast<float4*>(to + 4 * q) = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+            } else if (i < u.n) {
+                const int64_t at = key ? (u.b + i) * a.dk_ld : (u.b + i) * a.dq_ld;
+                __nv_bfloat16* const to = static_cast<__nv_bfloat16*>(key ? a.dk_out : a.dq) + at + u.h * a.dk + c0;
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    if (c0 + 8 * q < a.dk)
+                        *reinterpret_cast<uint4*>(to + 8 * q) = make_uint4(round2(v[8 * q], v[8 * q + 1]), round2(v[8 * q + 2], v[8 * q + 3]),
+                                                                           round2(v[8 * q + 4], v[8 * q + 5]), round2(v[8 * q + 6], v[8 * q + 7]));
+            }
+            __syncwarp();
+        }
+        tensor::fence_before();
+        u = find(u.id + gridDim.x);
+        kq ^= 1;
+    }
+    copies_wait<0>();
+    if (__syncthreads_or(bad)) {   // a wait ran out: what has been written so far is not to be trusted
+        if (tid == 0 && a.status != nullptr) atomicOr(a.status, SDM_DEV_STALLED);
+        for (int s = 0; s < 3; ++s) tensor::barrier_wait(bar + 8 * s, phase[s]);
+        __syncthreads();
+    }
+    tensor::fence_after();
+    if (w == 0) tensor::release<512>(tmem);
+}
+
 // The gradients of queries and keys that several value heads share: their heads' shares in order, 4 columns a thread. Rows
 // of no sequence stay as they are.
 template <typename X>
@@ -598,6 +983,15 @@ cudaError_t back(const Args& a, cudaStream_t cs) {
     if (e != cudaSuccess) return e;
     const int64_t grid = static_cast<int64_t>(a.P) * a.Hv * ((a.dv + BV - 1) / BV);
     return launch_dependent(k, dim3(static_cast<unsigned>(grid)), dim3(W::threads), W::bytes, cs, a);
+}
+
+template <int DKP>
+cudaError_t grad_tc(const Args& a, int64_t blocks, cudaStream_t cs) {
+    using W = GradTc<DKP>;
+    auto* const k = gdr_grad_tc_kernel<DKP>;
+    const cudaError_t e = big_smem(k, W::bytes);
+    if (e != cudaSuccess) return e;
+    return launch_dependent(k, dim3(static_cast<unsigned>(std::min<int64_t>(blocks * a.Hv, 152))), dim3(W::threads), W::bytes, cs, a);
 }
 
 template <int XT, int DKP>
@@ -674,7 +1068,7 @@ extern "C" sdm_status sdm_gdr_backward(const sdm_gdr_shape* shape, const void* q
         e = bf16 ? (narrow ? back_bf16<64>(a, cs) : back_bf16<128>(a, cs)) : (narrow ? back<3, 64, 32>(a, cs) : back<3, 128, 32>(a, cs));
     const int64_t blocks = blocks_of(shape);
     if (e == cudaSuccess && shape->rows > 0)
-        e = bf16 ? (narrow ? grad<1, 64>(a, blocks, cs) : grad<1, 128>(a, blocks, cs))
+        e = bf16 ? (narrow ? grad_tc<64>(a, blocks, cs) : grad_tc<128>(a, blocks, cs))
                  : (narrow ? grad<3, 64>(a, blocks, cs) : grad<3, 128>(a, blocks, cs));
     if (e == cudaSuccess && shape->rows > 0 && a.part != nullptr) {
         const int64_t grid = std::min<int64_t>((shape->rows * (kn / 4) * 2 + 255) / 256, 152 * 16);
