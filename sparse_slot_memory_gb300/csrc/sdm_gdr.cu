@@ -1,15 +1,10 @@
 // sdm_gdr.cu -- the gated delta rule: the forward over sequences in blocks of 64 rows, and one token of every request:
 // sdm_gdr_forward / sdm_gdr_step (include/sdm.h; the backward: sdm_gdr_bwd.cu; mathematics and numbers: sdm_gdr.cuh).
 //
-// Two kernels. What a block's rows give without the state (T, A and the decays) is computed for all blocks at once; then
-// every sequence and value head is walked block by block, its state's columns divided among warps.
-//
-// The walk. A warp owns 16 of a head's value columns and keeps its part of the state transposed, S^T [16 x dk], in the
-// accumulators of its matrix instructions. An accumulator's layout is an operand's too, so the chain S -> R -> U -> S' never
-// leaves the warp's registers and warps never wait for one another: the next block's tiles arrive meanwhile. mma.sync
-// and not tcgen05: its operands would come from shared memory, so every block would move the state and R, U as pairs through it
-// four times, one after another, on a chain that has nothing else to do.
+// Two kernels. What a block's rows give without the state (T, A T and the decays) is computed for all blocks at once; then
+// every sequence and value head is walked block by block, its state's columns divided among blocks of threads where there are few.
 #include "sdm_gdr.cuh"
+#include "sdm_tensor.cuh"
 
 namespace sdm {
 namespace gdr {
@@ -52,7 +47,7 @@ __global__ void __launch_bounds__(128, XT == 1 ? 4 : 2) gdr_prepare_kernel(const
     block_rows(a, id, b, n);
     if (n <= 0) return;
     // N and T take the place of K and Q, which the accumulators have taken in
-    const uint32_t K = smem_of(smem), Q = K + XT * kTile, N = K, T = N + NS * kPlane;
+    const uint32_t K = smem_of(smem), Q = K + XT * kTile, N = K, T = N + NS * kPlane, A = T + NS * kPlane;
     load_rows<DKP, 128>(K, a.k, XT, b, n, kh * a.dk, a.dk, tid);
     load_rows<DKP, 128>(Q, a.q, XT, b, n, kh * a.dk, a.dk, tid);
     copies_commit();
@@ -86,10 +81,10 @@ __global__ void __launch_bounds__(128, XT == 1 ? 4 : 2) gdr_prepare_kernel(const
         }
     }
     __syncthreads();
-    const int R = a.Hv / a.Hk, a_planes = a.tri_planes - NS;
+    const int R = a.Hv / a.Hk;
     for (int rv = 0; rv < R; ++rv) {
         const int h = kh * R + rv;
-        __nv_bfloat16* const tri = a.tri + (id * a.Hv + h) * a.tri_planes * int64_t(kC * kC);
+        __nv_bfloat16* const tri = a.tri + (id * a.Hv + h) * (2 * NS) * int64_t(kC * kC);
         float* const vec = a.vec + (id * a.Hv + h) * kVecs * kC;
         if (w == 0) {
             // gates below -150 are 0 to float32 like -150 (a product with them is), and their sums stay finite. Sums in 64
@@ -143,10 +138,13 @@ __global__ void __launch_bounds__(128, XT == 1 ? 4 : 2) gdr_prepare_kernel(const
                     nv[c] = j + c < i ? be[i] * (d * kk[nt][2 * e + c]) : 0.f;
                     if (nt >> 1 == w) diag[w][g + 8 * e][j + c - 16 * w] = nv[c];
                 }
-                uint32_t t[3];
-                split2<3>(av[0], av[1], t);
-                uint32_t* const A = reinterpret_cast<uint32_t*>(tri + NS * kC * kC + i * kC + j);
-                for (int pl = 0; pl < a_planes; ++pl) A[pl * (kC * kC / 2)] = pl == 0 ? t[0] : pl == 1 ? t[1] : t[2];
+                uint32_t t[NS];
+                split2<NS>(av[0], av[1], t);
+#pragma unroll
+                for (int pl = 0; pl < NS; ++pl) {
+                    if (XT == 1) st_word(A + pl * kPlane + tile_at<kC>(i, j >> 3) + (j & 7) * 2, t[pl]);
+                    else *reinterpret_cast<uint32_t*>(tri + (NS + pl) * kC * kC + i * kC + j) = t[pl];
+                }
                 uint32_t u[NS];
                 split2<NS>(nv[0], nv[1], u);
 #pragma unroll
@@ -234,17 +232,52 @@ __global__ void __launch_bounds__(128, XT == 1 ? 4 : 2) gdr_prepare_kernel(const
         __syncthreads();
         below(std::integral_constant<int, 2>{}, 32, 0, 8 * w);
         __syncthreads();
-        for (int i = tid; i < NS * kC * 8; i += 128) {
-            const int p = i >> 9, r = (i >> 3) & 63, u = i & 7;
-            if (u > (r >> 4) * 2 + 1) continue;
-            const uint4 v = *reinterpret_cast<const uint4*>(smem + (T - K) + p * kPlane + tile_at<kC>(r, u));
-            *reinterpret_cast<uint4*>(tri + p * kC * kC + r * kC + u * 8) = v;
+        if constexpr (XT == 1) {   // scale A T, over A, whose rows are this warp's own
+            float at[8][4] = {};
+#pragma unroll
+            for (int kt = 0; kt < 4; ++kt) {
+                if (kt > w) continue;
+                uint32_t f[NS][4];
+#pragma unroll
+                for (int p = 0; p < NS; ++p) ldsm4(f[p], A + p * kPlane + tile_at<kC>(16 * w + L.rA, 2 * kt + L.uA));
+                products<NS, NS, NS, true, 4>(at, f, kPlane, [&](int np) { return T + tile_at<kC>(16 * kt + L.rBt, 2 * np + L.uBt); }, 0, kt + 1);
+            }
+            __syncwarp();
+#pragma unroll
+            for (int nt = 0; nt < 8; ++nt) {
+                if (nt > 2 * w + 1) continue;
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    uint32_t t[NS];
+                    split2<NS>(a.scale * at[nt][2 * e], a.scale * at[nt][2 * e + 1], t);
+#pragma unroll
+                    for (int p = 0; p < NS; ++p) st_word(A + p * kPlane + tile_at<kC>(16 * w + g + 8 * e, nt) + qd * 4, t[p]);
+                }
+            }
+            __syncthreads();
+            // [T; scale A T] in cores of 8 rows: a term's 128 rows x 64
+            for (int i = tid; i < 2 * NS * kC * 8; i += 128) {
+                const int r = i & 63, u = i >> 6 & 7, lower = i >> 9 & 1, p = i >> 10;
+                if (u > (r >> 4) * 2 + 1) continue;
+                const uint4 v = *reinterpret_cast<const uint4*>(smem + ((lower ? A : T) - K) + p * kPlane + tile_at<kC>(r, u));
+                *reinterpret_cast<uint4*>(reinterpret_cast<unsigned char*>(tri) + p * 16384 + stacked_at(64 * lower + r, u)) = v;
+            }
+        } else {
+            for (int i = tid; i < NS * kC * 8; i += 128) {
+                const int p = i >> 9, r = (i >> 3) & 63, u = i & 7;
+                if (u > (r >> 4) * 2 + 1) continue;
+                const uint4 v = *reinterpret_cast<const uint4*>(smem + (T - K) + p * kPlane + tile_at<kC>(r, u));
+                *reinterpret_cast<uint4*>(tri + p * kC * kC + r * kC + u * 8) = v;
+            }
         }
         if (rv + 1 < R) __syncthreads();
     }
 }
 
-// ---- the walk ---------------------------------------------------------------------------------------------------
+// ---- the walk, float32 rows ---------------------------------------------------------------------------------------
+// A warp owns 16 of a head's value columns and keeps its part of the state transposed, S^T [16 x dk], in the accumulators of its
+// matrix instructions (mma.sync): an accumulator's layout is an operand's too, so the chain S -> R -> U -> S' never leaves the
+// warp's registers. Three terms would not fit beside one another as operands in shared memory, as the tensor core above them wants.
 template <int XT, int DKP, int BV>
 struct Walk {
     static constexpr int NS = XT == 1 ? 2 : 3;   // terms of what is computed
@@ -281,7 +314,7 @@ __global__ void __launch_bounds__(BV * 2) gdr_walk_kernel(const __grid_constant_
         load_rows<DKP, W::threads>(st + W::Q, a.q, XT, r0, n, kh * a.dk, a.dk, tid);
         load_rows<BV, W::threads>(st + W::V, a.v, XT, r0, n, h * a.dv + c0, cols, tid);
         const int64_t at = (id0 + j) * a.Hv + h;
-        const __nv_bfloat16* const tri = a.tri + at * a.tri_planes * int64_t(kC * kC);
+        const __nv_bfloat16* const tri = a.tri + at * (2 * NS) * int64_t(kC * kC);
 #pragma unroll
         for (int pl = 0; pl < NS + XT; ++pl) load_tri<W::threads>(st + W::T + pl * W::kPlane, tri + pl * kC * kC, tid);
         if (tid < 48) copy16(st + W::vec + tid * 16, a.vec + at * kVecs * kC + tid * 4, true);
@@ -453,6 +486,235 @@ __global__ void __launch_bounds__(BV * 2) gdr_walk_kernel(const __grid_constant_
     if (a.states != nullptr && lane == 0) bulk_wait();
 }
 
+// ---- the walk, bfloat16 rows ---------------------------------------------------------------------------------------
+// A block walks a sequence of a value head, BV of its value columns, with the state in its threads' registers in float32: thread
+// (row r of 128, 32 columns) holds S[r]. Per block of rows three products follow one another on the fifth-generation tensor core,
+//   [K; Q] S   ->  beta R = beta (V - e^gam K S)  ->  [T; scale A T] (beta R) = [U; scale A U]  ->  K^T (e^(gam_last - gam) U),
+// their sums in tensor memory, their computed operands (S, R, U) as two terms in shared memory, in cores that their own threads
+// write without conflicts. What bounds it is this chain: with 128 columns 2300 cycles of products, then 4 turns of a barrier,
+// loads from tensor memory and the cut into terms. Tiles of K and Q arrive a block ahead, V and T while the state is brought up
+// to date.
+template <int DKP, int BV>
+__global__ void __launch_bounds__(BV * 4) gdr_walk_tc_kernel(const __grid_constant__ Args a) {
+    using W = WalkTc<DKP, BV>;
+    extern __shared__ __align__(1024) unsigned char smem[];
+    __shared__ __align__(16) float vecs[2][kVecs * kC];
+    __shared__ __align__(8) uint64_t bars[3];
+    __shared__ uint32_t tmem;
+    start_dependent();
+    const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
+    const int slices = (a.dv + BV - 1) / BV;
+    const int rank = blockIdx.x / (a.Hv * slices), rest = blockIdx.x - rank * a.Hv * slices;
+    const int h = rest / slices, c0 = (rest - h * slices) * BV;
+    const int p = by_length(a, rank), kh = h / (a.Hv / a.Hk);
+    int64_t b, len;
+    sequence(a, p, b, len);
+    const int64_t blocks = (len + kC - 1) / kC, id0 = first_block(b, p);
+    const uint32_t base = smem_of(smem), bar = smem_of(bars);
+    const int cols = min(BV, a.dv - c0), nb = (a.dv + 15) / 16 * 2;   // units of 8 value columns that are saved
+
+    auto load_kq = [&](int64_t j) {
+        if (j < blocks) {
+            const int n = static_cast<int>(min(len - j * kC, int64_t(kC)));
+            const int64_t r0 = b + j * kC;
+            const uint32_t to = base + W::KQ + static_cast<int>(j & 1) * W::kKQ;
+#pragma unroll
+            for (int i = tid; i < 2 * kC * (DKP / 8); i += W::threads) {
+                const int r = i / (DKP / 8), u = i % (DKP / 8), t = r & 63;
+                const Planes& x = r < kC ? a.k : a.q;
+                const bool there = t < n && u * 8 < a.dk;
+                copy16(to + stacked_at(r, u), there ? x.p + (r0 + t) * x.ld + kh * a.dk + u * 8 : x.p, there);
+            }
+            for (int i = tid; i < kVecs * kC / 4; i += W::threads)
+                copy16(smem_of(vecs[j & 1]) + i * 16, a.vec + ((id0 + j) * a.Hv + h) * kVecs * kC + i * 4, true);
+        }
+        copies_commit();
+    };
+    auto load_vt = [&](int64_t j) {
+        if (j < blocks) {
+            const int n = static_cast<int>(min(len - j * kC, int64_t(kC)));
+            const int64_t r0 = b + j * kC;
+#pragma unroll
+            for (int i = tid; i < kC * (BV / 8); i += W::threads) {
+                const int r = i / (BV / 8), u = i % (BV / 8);
+                const bool there = r < n && u * 8 < cols;
+                copy16(base + W::V + rows_at(r, u), there ? a.v.p + (r0 + r) * a.v.ld + h * a.dv + c0 + u * 8 : a.v.p, there);
+            }
+            load_tri_stacked<W::threads>(base + W::T, a.tri + ((id0 + j) * a.Hv + h) * 4 * int64_t(kC * kC), tid);
+        }
+        copies_commit();
+    };
+    // what of T lies above the diagonal stays zero
+    for (int i = tid; i < W::kT / 16; i += W::threads) *reinterpret_cast<uint4*>(smem + W::T + i * 16) = make_uint4(0, 0, 0, 0);
+    __syncthreads();
+    load_kq(0);
+    load_vt(0);
+
+    const int r = 32 * (w & 3) + lane, part = w >> 2, i = r & 63;   // a row of tensor memory, 32 columns, a token
+    const bool key = r < kC;
+    const int vc = c0 + 32 * part;                                  // this thread's first value column
+    float S[32];
+    {
+        const float* const h0 = a.h0 == nullptr ? nullptr : a.h0 + ((static_cast<int64_t>(p) * a.Hv + h) * a.dk + r) * a.dv + vc;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            float v[4] = {};
+            if (h0 != nullptr && r < a.dk && vc + 4 * q < a.dv) load4(h0 + 4 * q).get(v);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) S[4 * q + e] = v[e];
+        }
+    }
+    unsigned char* const Sp = smem + W::S + part * 4 * (DKP * 16) + r * 16;   // a unit of 8 columns: DKP rows of 16 bytes
+    unsigned char* const Rp = smem + W::R + part * 4 * 1024 + i * 16;
+    auto put_state = [&](int64_t j) {   // S as operand, and for the backward before block j
+        if (r >= DKP) return;
+        put_terms(Sp, Sp + W::kS, DKP * 16, S);
+        if (a.states != nullptr && j < blocks) {
+            unsigned char* const to = reinterpret_cast<unsigned char*>(a.states) + (((id0 + j) * a.Hv + h) * 2 * nb + vc / 8) * int64_t(DKP * 16) + r * 16;
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    if (vc / 8 + q < nb)
+                        *reinterpret_cast<uint4*>(to + (t * static_cast<int64_t>(nb) + q) * (DKP * 16)) = *reinterpret_cast<const uint4*>(Sp + t * W::kS + q * (DKP * 16));
+        }
+    };
+    put_state(0);
+    if (w == 0) tensor::allocate<W::cols>(smem_of(&tmem));
+    if (tid == 0) {
+        for (int x = 0; x < 3; ++x) tensor::barrier_init(bar + 8 * x, 1);
+        tensor::barrier_fence();
+    }
+    tensor::fence_before();
+    __syncthreads();
+    tensor::fence_after();
+    const uint32_t Da = tmem, Db = tmem + BV, Dc = tmem + 2 * BV;
+    const uint32_t mine = (static_cast<uint32_t>(w & 3) << 21) + 32 * part;
+    uint32_t phase = 0;
+    bool bad = false;
+    for (int64_t j = 0; j < blocks; ++j) {
+        const uint32_t KQ = base + W::KQ + static_cast<int>(j & 1) * W::kKQ;
+        const float* const vec = vecs[j & 1];
+        copies_wait<1>();
+        async_fence();
+        if (__syncthreads_or(bad)) break;
+        if (tid == 0) {
+            tensor::fence_after();
+            for (int ks = 0; ks < DKP / 16; ++ks)
+                for (int t = 0; t < 2; ++t)
+                    tensor::mma(Da, tensor::operand(KQ + ks * 4096, 2048, 128), tensor::operand(base + W::S + t * W::kS + ks * 256, 128, DKP * 16),
+                                tensor::shape(128, BV, false, true), ks + t > 0);
+            tensor::commit(bar);
+        }
+        load_kq(j + 1);
+        bad |= !tensor::barrier_wait(bar, phase);
+        copies_wait<1>();
+        async_fence();
+        __syncthreads();
+        tensor::fence_after();
+        float x[32];
+        tensor::load32(Da + mine, x);
+        tensor::loaded();
+        const float eg = vec[i];
+        if (key) {   // beta R
+            const float bt = vec[kC + i];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const uint4 v = *reinterpret_cast<const uint4*>(smem + W::V + rows_at(i, 4 * part + q));
+                const uint32_t vw[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    x[8 * q + e] = bt * fmaf(-eg, x[8 * q + e], __uint_as_float(e & 1 ? vw[e >> 1] & 0xFFFF0000u : vw[e >> 1] << 16));
+            }
+            put_terms(Rp, Rp + W::kR, 1024, x);
+        }
+        async_fence();
+        tensor::fence_before();
+        __syncthreads();
+        if (tid == 0) {
+            tensor::fence_after();
+            for (int t = 0; t < 3; ++t)   // T's first term with both of R's, its second with the first
+                for (int ks = 0; ks < 4; ++ks)
+                    tensor::mma(Db, tensor::operand(base + W::T + (t >> 1) * 16384 + ks * 4096, 2048, 128),
+                                tensor::operand(base + W::R + (t & 1) * W::kR + ks * 256, 128, 1024), tensor::shape(128, BV, false, true), t + ks > 0);
+            tensor::commit(bar + 8);
+        }
+        if (!key) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) x[e] *= a.scale * eg;
+        }
+        bad |= !tensor::barrier_wait(bar + 8, phase);
+        tensor::fence_after();
+        float u[32];
+        tensor::load32(Db + mine, u);
+        tensor::loaded();
+        if (key) {
+            const float c = vec[2 * kC + i];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) x[e] = c * u[e];
+            put_terms(Rp, Rp + W::kR, 1024, x);
+        }
+        async_fence();
+        tensor::fence_before();
+        __syncthreads();
+        if (tid == 0) {
+            tensor::fence_after();
+            for (int ks = 0; ks < 4; ++ks)
+                for (int t = 0; t < 2; ++t)
+                    tensor::mma(Dc, tensor::operand(KQ + ks * 256, 128, 2048), tensor::operand(base + W::R + t * W::kR + ks * 256, 128, 1024),
+                                tensor::shape(128, BV, true, true), ks + t > 0);
+            tensor::commit(bar + 16);
+        }
+        load_vt(j + 1);
+        const int64_t r0 = b + j * kC;
+        const int n = static_cast<int>(min(len - j * kC, int64_t(kC)));
+        if (key) {
+            if (a.states != nullptr) {   // the writes, for the backward
+                unsigned char* const to = reinterpret_cast<unsigned char*>(a.writes) + (((id0 + j) * a.Hv + h) * 2 * nb + vc / 8) * int64_t(1024) + i * 16;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    if (vc / 8 + q >= nb) continue;
+                    uint32_t t[4][2];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) split2<2>(u[8 * q + 2 * e], u[8 * q + 2 * e + 1], t[e]);
+                    *reinterpret_cast<uint4*>(to + q * 1024) = make_uint4(t[0][0], t[1][0], t[2][0], t[3][0]);
+                    *reinterpret_cast<uint4*>(to + (nb + q) * 1024) = make_uint4(t[0][1], t[1][1], t[2][1], t[3][1]);
+                }
+            }
+        } else if (i < n) {   // the row's answer
+            __nv_bfloat16* const y = static_cast<__nv_bfloat16*>(a.y) + (r0 + i) * a.y_ld + h * a.dv + vc;
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                if (vc + 8 * q < a.dv)
+                    *reinterpret_cast<uint4*>(y + 8 * q) = make_uint4(round2(x[8 * q] + u[8 * q], x[8 * q + 1] + u[8 * q + 1]),
+                                                                      round2(x[8 * q + 2] + u[8 * q + 2], x[8 * q + 3] + u[8 * q + 3]),
+                                                                      round2(x[8 * q + 4] + u[8 * q + 4], x[8 * q + 5] + u[8 * q + 5]),
+                                                                      round2(x[8 * q + 6] + u[8 * q + 6], x[8 * q + 7] + u[8 * q + 7]));
+        }
+        __syncwarp();
+        const float last = vec[kC - 1];
+        bad |= !tensor::barrier_wait(bar + 16, phase);
+        phase ^= 1;
+        tensor::fence_after();
+        tensor::load32(Dc + mine, u);
+        tensor::loaded();
+#pragma unroll
+        for (int e = 0; e < 32; ++e) S[e] = fmaf(last, S[e], u[e]);
+        put_state(j + 1);
+        tensor::fence_before();
+    }
+    if (a.hT != nullptr && r < a.dk) {
+        float* const hT = a.hT + ((static_cast<int64_t>(p) * a.Hv + h) * a.dk + r) * a.dv + vc;
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+            if (vc + 4 * q < a.dv) *reinterpret_cast<float4*>(hT + 4 * q) = make_float4(S[4 * q], S[4 * q + 1], S[4 * q + 2], S[4 * q + 3]);
+    }
+    copies_wait<0>();
+    if (__syncthreads_or(bad) && tid == 0 && a.status != nullptr) atomicOr(a.status, SDM_DEV_STALLED);
+    tensor::fence_after();
+    if (w == 0) tensor::release<W::cols>(tmem);
+}
+
 // ---- one token of every request -----------------------------------------------------------------------------------
 // y = scale (e^g S^T q + (k.q) u), so one look at the state gives S^T k and S^T q together; it stays in registers until
 // u is known, and is written once. Bound by HBM: 8 bytes an element of the state.
@@ -574,7 +836,7 @@ cudaError_t big_smem(K kernel, int bytes) {
 
 template <int XT, int DKP>
 cudaError_t prepare(const Args& a, int64_t blocks, cudaStream_t cs) {
-    constexpr int tiles = 2 * XT * kC * DKP * 2, planes = 2 * (XT == 1 ? 2 : 3) * kC * kC * 2, bytes = tiles > planes ? tiles : planes;
+    constexpr int tiles = 2 * XT * kC * DKP * 2, planes = (XT == 1 ? 3 * 2 : 2 * 3) * kC * kC * 2, bytes = tiles > planes ? tiles : planes;
     auto* const k = gdr_prepare_kernel<XT, DKP>;
     const cudaError_t e = big_smem(k, bytes);
     if (e != cudaSuccess) return e;
@@ -593,12 +855,22 @@ cudaError_t walk(const Args& a, cudaStream_t cs) {
     return launch_dependent(k, dim3(static_cast<unsigned>(grid)), dim3(W::threads), bytes, cs, a);
 }
 
+template <int DKP, int BV>
+cudaError_t walk_tc(const Args& a, cudaStream_t cs) {
+    using W = WalkTc<DKP, BV>;
+    auto* const k = gdr_walk_tc_kernel<DKP, BV>;
+    const cudaError_t e = big_smem(k, W::bytes);
+    if (e != cudaSuccess) return e;
+    const int64_t grid = static_cast<int64_t>(a.P) * a.Hv * ((a.dv + BV - 1) / BV);
+    return launch_dependent(k, dim3(static_cast<unsigned>(grid)), dim3(W::threads), W::bytes, cs, a);
+}
+
 template <int DKP>
 cudaError_t walk_bf16(const Args& a, cudaStream_t cs) {
     switch (columns(a)) {
-        case 32: return walk<1, DKP, 32>(a, cs);
-        case 64: return walk<1, DKP, 64>(a, cs);
-        default: return walk<1, DKP, 128>(a, cs);
+        case 32: return walk_tc<DKP, 32>(a, cs);
+        case 64: return walk_tc<DKP, 64>(a, cs);
+        default: return walk_tc<DKP, 128>(a, cs);
     }
 }
 
@@ -627,7 +899,7 @@ Layout layout(const sdm_gdr_shape* s, bool backward) {
         at += up(bytes);
         return here;
     };
-    l.tri = take(heads * (f32 ? 6 : backward ? 4 : 3) * kC * kC * 2);
+    l.tri = take(heads * 2 * terms(s) * kC * kC * 2);
     l.vec = take(heads * kVecs * kC * 4);
     if (f32) {
         l.q = take(s->rows * s->k_heads * s->dk * 6);
@@ -739,7 +1011,6 @@ extern "C" sdm_status sdm_gdr_forward(const sdm_gdr_shape* shape, const void* q,
     if (!aligned_all(16, {h0, hT, states})) return SDM_ERR_ALIGN;
     a.h0 = h0; a.y = y; a.y_ld = y_ld; a.hT = hT;
     set_states(shape, states, &a);
-    a.tri_planes = shape->x_dtype == SDM_F32 ? 6 : 3;
     const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t e = cudaSuccess;
     if (shape->rows > 0) {

@@ -53,23 +53,24 @@ struct Args {
     const float* dhT;         // nullable
     float* hT;                // nullable
     float* dh0;               // nullable
-    __nv_bfloat16* states;    // nullable in the forward: [blocks][Hv][dv / 16][terms], tiles [16 value columns][dk padded]
-    __nv_bfloat16* writes;    // behind the states: U, [blocks][Hv][dv / 16][terms], tiles [64][16]
+    __nv_bfloat16* states;    // nullable in the forward: [blocks][Hv] (float32 rows: [dv / 16] tiles)
+    __nv_bfloat16* writes;    // behind the states: U, [blocks][Hv]
     void* y;
     void* dq;
     void* dk_out;
     void* dv_out;
     void* dg;
     void* dbeta;
-    __nv_bfloat16* tri;       // workspace: [blocks][Hv][planes][64][64], first T's terms, then A's
+    __nv_bfloat16* tri;       // workspace: [blocks][Hv]: of bfloat16 rows two terms of [T; scale A T], [128][64] in cores of 8 rows; of
+                              // float32 rows six planes [64][64], T's terms and A's
     float* vec;               // workspace: [blocks][Hv][kVecs][64]: e^gam, beta, e^(gam_last - gam), gam as a sum of two floats
     __nv_bfloat16* dstates;   // workspace of the backward: the gradients of the states behind the blocks, as `states`
-    __nv_bfloat16* du;        // workspace of the backward: [blocks][Hv][dv / 16][terms], tiles [64][16], the gradients of the writes, dv before beta
+    __nv_bfloat16* du;        // workspace of the backward: the gradients of the writes (dv before beta), as `writes`
     float* part;              // workspace of the backward: gradients of shared queries and keys
     uint32_t* status;         // nullable
     int64_t rows, len;        // len: rows of every sequence where offsets is null
     int64_t g_ld, b_ld, y_ld, dq_ld, dk_ld, dv_ld, dg_ld, db_ld;
-    int P, Hk, Hv, dk, dv, g_bf16, tri_planes;
+    int P, Hk, Hv, dk, dv, g_bf16;
     float scale;
 };
 
@@ -187,6 +188,16 @@ __device__ __forceinline__ void load_tri(uint32_t dst, const __nv_bfloat16* src,
     }
 }
 
+// A tile's stacked halves, [128 rows], in cores of 8 rows (sdm_tensor.cuh)
+__device__ __forceinline__ uint32_t stacked_at(int r, int u) { return static_cast<uint32_t>(u * 2048 + (r >> 3) * 128 + (r & 7) * 16); }
+// Both terms of [T; scale A T]: the blocks of 16 up to the diagonal
+template <int THREADS>
+__device__ __forceinline__ void load_tri_stacked(uint32_t dst, const __nv_bfloat16* src, int tid) {
+#pragma unroll
+    for (int i = tid; i < 2 * 1024; i += THREADS)
+        if ((i >> 7 & 7) <= (i >> 4 & 3) * 2 + 1) copy16(dst + i * 16, src + i * 8, true);   // i: term, unit, row
+}
+
 // ---- fragments ------------------------------------------------------------------------------------------
 // (loads of fragments keep their place among barriers and stores by being volatile; the products are free to move)
 __device__ __forceinline__ void ldsm4(uint32_t (&f)[4], uint32_t a) {
@@ -292,8 +303,9 @@ __device__ __forceinline__ void products(float (&acc)[M][4], const uint32_t (&a)
     }
 }
 
-// The saved tiles lie in cores of 8 rows of 16 bytes (sdm_tensor.cuh): states [16 value columns][dk], writes and their gradients
-// [64 rows][16 value columns]; row r, unit u of 8 columns.
+// Float32 rows' saved tiles lie in cores of 8 rows of 16 bytes: states [16 value columns][dk], writes and their gradients [64
+// rows][16 value columns]; row r, unit u of 8 columns. bfloat16 rows' are whole: per term units of 8 value columns, of dk or 64
+// rows of 16 bytes.
 __device__ __forceinline__ uint32_t state_at(int r, int u) { return static_cast<uint32_t>(u * 256 + (r >> 3) * 128 + (r & 7) * 16); }
 __device__ __forceinline__ uint32_t rows_at(int r, int u) { return static_cast<uint32_t>(u * 1024 + (r >> 3) * 128 + (r & 7) * 16); }
 
@@ -305,6 +317,29 @@ __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.comm
 __device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 __device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 __device__ __forceinline__ void async_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// ---- the walks of bfloat16 rows, forwards and from the end: what they keep in shared memory ----------------------------------
+template <int DKP, int BV>
+struct WalkTc {
+    static constexpr int kKQ = DKP / 8 * 2048, kV = kC * BV * 2, kT = 2 * 16384, kS = BV * DKP * 2, kR = kC * BV * 2;
+    // [K; Q] twice, V (or dY), [T; scale A T], the state's terms, R's and U's (or their gradients')
+    static constexpr int KQ = 0, V = 2 * kKQ, T = V + kV, S = T + kT, R = S + 2 * kS, end = R + 2 * kR;
+    // a core column of K^T and T^T beyond their own 64 is read (and not used): up to 16 columns from the tile's start
+    static constexpr int bytes = end > 16 * 2048 + kKQ ? end : 16 * 2048 + kKQ;
+    static constexpr int threads = BV * 4, cols = BV <= 32 ? 128 : BV == 64 ? 256 : 512;
+};
+
+// 32 values as two terms: units of 8 columns, 16 bytes each, `pitch` bytes apart
+__device__ __forceinline__ void put_terms(unsigned char* hi, unsigned char* lo, int pitch, const float (&v)[32]) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+        uint32_t t[4][2];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) split2<2>(v[8 * q + 2 * e], v[8 * q + 2 * e + 1], t[e]);
+        *reinterpret_cast<uint4*>(hi + q * pitch) = make_uint4(t[0][0], t[1][0], t[2][0], t[3][0]);
+        *reinterpret_cast<uint4*>(lo + q * pitch) = make_uint4(t[0][1], t[1][1], t[2][1], t[3][1]);
+    }
+}
 
 // ---- host side, in sdm_gdr.cu ---------------------------------------------------------------------------
 inline int padded(int d) { return d <= 64 ? 64 : 128; }

@@ -22,7 +22,7 @@ namespace sdm {
 namespace gdr {
 namespace {
 
-// ---- the walk from the end -----------------------------------------------------------------------------------------
+// ---- the walk from the end, float32 rows ------------------------------------------------------------------------------
 template <int XT, int DKP, int BV>
 struct Back {
     static constexpr int NS = XT == 1 ? 2 : 3;
@@ -59,7 +59,7 @@ __global__ void __launch_bounds__(BV * 2) gdr_back_kernel(const __grid_constant_
         load_rows<DKP, W::threads>(st + W::Q, a.q, XT, r0, n, kh * a.dk, a.dk, tid);
         load_rows<BV, W::threads>(st + W::Y, a.dy, XT, r0, n, h * a.dv + c0, cols, tid);
         const int64_t at = (id0 + j) * a.Hv + h;
-        const __nv_bfloat16* const tri = a.tri + at * a.tri_planes * int64_t(kC * kC);
+        const __nv_bfloat16* const tri = a.tri + at * (2 * NS) * int64_t(kC * kC);
 #pragma unroll
         for (int pl = 0; pl < 2 * NS; ++pl) load_tri<W::threads>(st + W::T + pl * W::kPlane, tri + pl * kC * kC, tid);
         if (tid < 48) copy16(st + W::vec + tid * 16, a.vec + at * kVecs * kC + tid * 4, true);
@@ -228,6 +228,235 @@ __global__ void __launch_bounds__(BV * 2) gdr_back_kernel(const __grid_constant_
             }
     }
     if (lane == 0) bulk_wait();
+}
+
+// ---- the walk from the end, bfloat16 rows ------------------------------------------------------------------------------
+// As the forward's walk (sdm_gdr.cu), with dS in the threads' registers: per block of rows
+//   K dS'  ->  x = e^(gam_last - gam) o K dS'  ->  W = T^T x + (scale A T)^T dY  ->  dS = e^gam_last dS' + Q^T (scale e^gam o dY) - K^T (e^gam o beta o W).
+// What dY gives by itself is multiplied beside the chain; its scaled rows take the place of the state's terms while those are not needed.
+template <int DKP, int BV>
+__global__ void __launch_bounds__(BV * 4) gdr_back_tc_kernel(const __grid_constant__ Args a) {
+    using W = WalkTc<DKP, BV>;
+    static_assert(W::kR <= W::kS, "dY's terms lie over the state's");
+    extern __shared__ __align__(1024) unsigned char smem[];
+    __shared__ __align__(16) float vecs[2][kVecs * kC];
+    __shared__ __align__(8) uint64_t bars[3];
+    __shared__ uint32_t tmem;
+    start_dependent();
+    const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
+    const int slices = (a.dv + BV - 1) / BV;
+    const int rank = blockIdx.x / (a.Hv * slices), rest = blockIdx.x - rank * a.Hv * slices;
+    const int h = rest / slices, c0 = (rest - h * slices) * BV;
+    const int p = by_length(a, rank), kh = h / (a.Hv / a.Hk);
+    int64_t b, len;
+    sequence(a, p, b, len);
+    const int64_t blocks = (len + kC - 1) / kC, id0 = first_block(b, p);
+    const uint32_t base = smem_of(smem), bar = smem_of(bars);
+    const int cols = min(BV, a.dv - c0), nb = (a.dv + 15) / 16 * 2;
+
+    auto load_kq = [&](int64_t j) {
+        if (j >= 0) {
+            const int n = static_cast<int>(min(len - j * kC, int64_t(kC)));
+            const int64_t r0 = b + j * kC;
+            const uint32_t to = base + W::KQ + static_cast<int>(j & 1) * W::kKQ;
+#pragma unroll
+            for (int i = tid; i < 2 * kC * (DKP / 8); i += W::threads) {
+                const int r = i / (DKP / 8), u = i % (DKP / 8), t = r & 63;
+                const Planes& x = r < kC ? a.k : a.q;
+                const bool there = t < n && u * 8 < a.dk;
+                copy16(to + stacked_at(r, u), there ? x.p + (r0 + t) * x.ld + kh * a.dk + u * 8 : x.p, there);
+            }
+            for (int i = tid; i < kVecs * kC / 4; i += W::threads)
+                copy16(smem_of(vecs[j & 1]) + i * 16, a.vec + ((id0 + j) * a.Hv + h) * kVecs * kC + i * 4, true);
+        }
+        copies_commit();
+    };
+    auto load_yt = [&](int64_t j) {
+        if (j >= 0) {
+            const int n = static_cast<int>(min(len - j * kC, int64_t(kC)));
+            const int64_t r0 = b + j * kC;
+#pragma unroll
+            for (int i = tid; i < kC * (BV / 8); i += W::threads) {
+                const int r = i / (BV / 8), u = i % (BV / 8);
+                const bool there = r < n && u * 8 < cols;
+                copy16(base + W::V + rows_at(r, u), there ? a.dy.p + (r0 + r) * a.dy.ld + h * a.dv + c0 + u * 8 : a.dy.p, there);
+            }
+            load_tri_stacked<W::threads>(base + W::T, a.tri + ((id0 + j) * a.Hv + h) * 4 * int64_t(kC * kC), tid);
+        }
+        copies_commit();
+    };
+    for (int i = tid; i < W::kT / 16; i += W::threads) *reinterpret_cast<uint4*>(smem + W::T + i * 16) = make_uint4(0, 0, 0, 0);
+    __syncthreads();
+    load_kq(blocks - 1);
+    load_yt(blocks - 1);
+
+    const int r = 32 * (w & 3) + lane, part = w >> 2, i = r & 63;
+    const bool key = r < kC;
+    const int vc = c0 + 32 * part;
+    float S[32];
+    {
+        const float* const d = a.dhT == nullptr ? nullptr : a.dhT + ((static_cast<int64_t>(p) * a.Hv + h) * a.dk + r) * a.dv + vc;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            float v[4] = {};
+            if (d != nullptr && r < a.dk && vc + 4 * q < a.dv) load4(d + 4 * q).get(v);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) S[4 * q + e] = v[e];
+        }
+    }
+    unsigned char* const Sp = smem + W::S + part * 4 * (DKP * 16) + r * 16;
+    unsigned char* const Yp = smem + W::S + part * 4 * 1024 + i * 16;
+    unsigned char* const Xp = smem + W::R + part * 4 * 1024 + i * 16;
+    auto put_state = [&](int64_t j) {   // dS as operand, and for the other gradients behind block j
+        if (r >= DKP) return;
+        put_terms(Sp, Sp + W::kS, DKP * 16, S);
+        if (j >= 0) {
+            unsigned char* const to = reinterpret_cast<unsigned char*>(a.dstates) + (((id0 + j) * a.Hv + h) * 2 * nb + vc / 8) * int64_t(DKP * 16) + r * 16;
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    if (vc / 8 + q < nb)
+                        *reinterpret_cast<uint4*>(to + (t * static_cast<int64_t>(nb) + q) * (DKP * 16)) = *reinterpret_cast<const uint4*>(Sp + t * W::kS + q * (DKP * 16));
+        }
+    };
+    put_state(blocks - 1);
+    if (w == 0) tensor::allocate<W::cols>(smem_of(&tmem));
+    if (tid == 0) {
+        for (int x = 0; x < 3; ++x) tensor::barrier_init(bar + 8 * x, 1);
+        tensor::barrier_fence();
+    }
+    tensor::fence_before();
+    __syncthreads();
+    tensor::fence_after();
+    const uint32_t Da = tmem, Db = tmem + BV, Dc = tmem + 2 * BV;
+    const uint32_t mine = (static_cast<uint32_t>(w & 3) << 21) + 32 * part;
+    uint32_t phase = 0;
+    bool bad = false;
+    for (int64_t j = blocks - 1; j >= 0; --j) {
+        const uint32_t KQ = base + W::KQ + static_cast<int>(j & 1) * W::kKQ;
+        const float* const vec = vecs[j & 1];
+        copies_wait<1>();
+        async_fence();
+        if (__syncthreads_or(bad)) break;
+        if (tid == 0) {
+            tensor::fence_after();
+            for (int ks = 0; ks < DKP / 16; ++ks)
+                for (int t = 0; t < 2; ++t)
+                    tensor::mma(Da, tensor::operand(KQ + ks * 4096, 2048, 128), tensor::operand(base + W::S + t * W::kS + ks * 256, 128, DKP * 16),
+                                tensor::shape(128, BV, false, true), ks + t > 0);
+            tensor::commit(bar);
+        }
+        load_kq(j - 1);
+        bad |= !tensor::barrier_wait(bar, phase);
+        copies_wait<1>();
+        async_fence();
+        __syncthreads();
+        tensor::fence_after();
+        if (tid == 0) {   // what dY gives by A T
+            for (int t = 0; t < 2; ++t)
+                for (int ks = 0; ks < 4; ++ks)
+                    tensor::mma(Db, tensor::operand(base + W::T + t * 16384 + 1024 + ks * 256, 128, 2048),
+                                tensor::operand(base + W::V + ks * 256, 128, 1024), tensor::shape(128, BV, true, true), t + ks > 0);
+        }
+        float x[32];
+        const float eg = vec[i], bt = vec[kC + i];
+        if (key) {
+            tensor::load32(Da + mine, x);
+            tensor::loaded();
+            const float c = vec[2 * kC + i];
+#pragma unroll
+            for (int e = 0; e < 32; ++e) x[e] *= c;
+            put_terms(Xp, Xp + W::kR, 1024, x);
+        } else {
+            const float f = a.scale * eg;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const uint4 v = *reinterpret_cast<const uint4*>(smem + W::V + rows_at(i, 4 * part + q));
+                const uint32_t vw[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[8 * q + e] = f * __uint_as_float(e & 1 ? vw[e >> 1] & 0xFFFF0000u : vw[e >> 1] << 16);
+            }
+            put_terms(Yp, Yp + W::kS, 1024, x);
+        }
+        async_fence();
+        tensor::fence_before();
+        __syncthreads();
+        if (tid == 0) {
+            tensor::fence_after();
+            for (int t = 0; t < 3; ++t)   // T's first term with both of x's, its second with the first
+                for (int ks = 0; ks < 4; ++ks)
+                    tensor::mma(Db, tensor::operand(base + W::T + (t >> 1) * 16384 + ks * 256, 128, 2048),
+                                tensor::operand(base + W::R + (t & 1) * W::kR + ks * 256, 128, 1024), tensor::shape(128, BV, true, true), true);
+            tensor::commit(bar + 8);
+            for (int ks = 0; ks < 4; ++ks)
+                for (int t = 0; t < 2; ++t)
+                    tensor::mma(Dc, tensor::operand(KQ + 1024 + ks * 256, 128, 2048), tensor::operand(base + W::S + t * W::kS + ks * 256, 128, 1024),
+                                tensor::shape(128, BV, true, true), ks + t > 0);
+        }
+        bad |= !tensor::barrier_wait(bar + 8, phase);
+        tensor::fence_after();
+        float u[32];
+        if (key) {
+            tensor::load32(Db + mine, u);
+            tensor::loaded();
+            const float f = -eg * bt;
+#pragma unroll
+            for (int e = 0; e < 32; ++e) x[e] = f * u[e];
+            put_terms(Xp, Xp + W::kR, 1024, x);
+        }
+        async_fence();
+        tensor::fence_before();
+        __syncthreads();
+        if (tid == 0) {
+            tensor::fence_after();
+            for (int ks = 0; ks < 4; ++ks)
+                for (int t = 0; t < 2; ++t)
+                    tensor::mma(Dc, tensor::operand(KQ + ks * 256, 128, 2048), tensor::operand(base + W::R + t * W::kR + ks * 256, 128, 1024),
+                                tensor::shape(128, BV, true, true), true);
+            tensor::commit(bar + 16);
+        }
+        load_yt(j - 1);
+        if (key) {
+            unsigned char* const to = reinterpret_cast<unsigned char*>(a.du) + (((id0 + j) * a.Hv + h) * 2 * nb + vc / 8) * int64_t(1024) + i * 16;
+            const bool there = i < min(len - j * kC, int64_t(kC));
+            __nv_bfloat16* const dv = static_cast<__nv_bfloat16*>(a.dv_out) + (b + j * kC + i) * a.dv_ld + h * a.dv + vc;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                if (vc / 8 + q >= nb) continue;
+                uint32_t t[4][2], o[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    split2<2>(u[8 * q + 2 * e], u[8 * q + 2 * e + 1], t[e]);
+                    o[e] = round2(bt * u[8 * q + 2 * e], bt * u[8 * q + 2 * e + 1]);
+                }
+                *reinterpret_cast<uint4*>(to + q * 1024) = make_uint4(t[0][0], t[1][0], t[2][0], t[3][0]);
+                *reinterpret_cast<uint4*>(to + (nb + q) * 1024) = make_uint4(t[0][1], t[1][1], t[2][1], t[3][1]);
+                if (there && vc + 8 * q < a.dv) *reinterpret_cast<uint4*>(dv + 8 * q) = make_uint4(o[0], o[1], o[2], o[3]);
+            }
+        }
+        __syncwarp();
+        const float last = vec[kC - 1];
+        bad |= !tensor::barrier_wait(bar + 16, phase);
+        phase ^= 1;
+        tensor::fence_after();
+        tensor::load32(Dc + mine, u);
+        tensor::loaded();
+#pragma unroll
+        for (int e = 0; e < 32; ++e) S[e] = fmaf(last, S[e], u[e]);
+        put_state(j - 1);
+        tensor::fence_before();
+    }
+    if (a.dh0 != nullptr && r < a.dk) {
+        float* const d = a.dh0 + ((static_cast<int64_t>(p) * a.Hv + h) * a.dk + r) * a.dv + vc;
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+            if (vc + 4 * q < a.dv) *reinterpret_cast<float4*>(d + 4 * q) = make_float4(S[4 * q], S[4 * q + 1], S[4 * q + 2], S[4 * q + 3]);
+    }
+    copies_wait<0>();
+    if (__syncthreads_or(bad) && tid == 0 && a.status != nullptr) atomicOr(a.status, SDM_DEV_STALLED);
+    tensor::fence_after();
+    if (w == 0) tensor::release<W::cols>(tmem);
 }
 
 // ---- all blocks at once, float32 rows ---------------------------------------------------------------------------------
@@ -570,14 +799,12 @@ __global__ void __launch_bounds__(512) gdr_grad_kernel(const __grid_constant__ A
 template <int DKP>
 struct GradTc {
     static constexpr int kGroup = 2 * 6144;                  // rows of 16 value columns: per core along K [U | W | dY], then the rests [U | W | 0]
-    static constexpr int kImage = 16 * DKP * 2, kStates = 4 * kImage;
+    static constexpr int kUnit = DKP * 16, kTerm = 4 * kUnit, kStates = 2 * kTerm;   // of states: 8 value columns, 32
     static constexpr int rows = 0, S = 2 * kGroup, dS = S + kStates, stage = dS + kStates;
     static constexpr int kKQ = DKP / 8 * 2048;               // [K; Q], two of them
     static constexpr int slices = 2 * kKQ, XN = slices + 2 * stage, Z = XN + 16384, bytes = Z + kC * 65 * 4;
     static constexpr int threads = 256;
 };
-
-__device__ __forceinline__ uint32_t stacked_at(int r, int u) { return static_cast<uint32_t>(u * 2048 + (r >> 3) * 128 + (r & 7) * 16); }
 
 template <int DKP>
 __global__ void __launch_bounds__(256) gdr_grad_tc_kernel(const __grid_constant__ Args a) {
@@ -619,22 +846,27 @@ __global__ void __launch_bounds__(256) gdr_grad_tc_kernel(const __grid_constant_
         if (lu.id < units) {
             const uint32_t st = base + W::slices + static_cast<int>(issued & 1) * W::stage;
             const int g0 = 2 * ls, have = min(2, groups - g0), c0 = 32 * ls, cols = min(32, a.dv - c0);
-            const __nv_bfloat16* const sp = a.states + (lu.id * groups + g0) * (2 * 16 * DKP);
-            const __nv_bfloat16* const dp = a.dstates + (lu.id * groups + g0) * (2 * 16 * DKP);
-            const __nv_bfloat16* const wp = a.du + (lu.id * groups + g0) * (2 * kC * 16);
-            const __nv_bfloat16* const up = a.writes + (lu.id * groups + g0) * (2 * kC * 16);
+            const int64_t first = lu.id * 2 * (2 * groups) + 2 * g0;   // the slice's first unit of 8 value columns of the first term
+            const __nv_bfloat16* const sp = a.states + first * (DKP * 8);
+            const __nv_bfloat16* const dp = a.dstates + first * (DKP * 8);
+            const __nv_bfloat16* const wp = a.du + first * (kC * 8);
+            const __nv_bfloat16* const up = a.writes + first * (kC * 8);
 #pragma unroll
             for (int i = tid; i < W::kStates / 16; i += W::threads) {
-                const bool there = i < have * 2 * W::kImage / 16;
-                copy16(st + W::S + i * 16, there ? sp + i * 8 : sp, there);
-                copy16(st + W::dS + i * 16, there ? dp + i * 8 : dp, there);
+                const int t = i / (4 * DKP), x = i % (4 * DKP);
+                const bool there = x < have * 2 * DKP;
+                const int64_t at = there ? (static_cast<int64_t>(t) * 2 * groups * DKP + x) * 8 : 0;
+                copy16(st + W::S + i * 16, sp + at, there);
+                copy16(st + W::dS + i * 16, dp + at, there);
             }
 #pragma unroll
-            for (int i = tid; i < 512; i += W::threads) {   // group, term, core along K, row
-                const bool there = i < have * 256;
-                const uint32_t to = st + W::rows + (i >> 8) * W::kGroup + (i >> 7 & 1) * 6144 + (i >> 6 & 1) * 3072 + (i & 63) * 16;
-                copy16(to, there ? up + i * 8 : up, there);
-                copy16(to + 1024, there ? wp + i * 8 : wp, there);
+            for (int i = tid; i < 512; i += W::threads) {   // term, group, core along K, row
+                const int t = i >> 8, x = i & 255;
+                const bool there = x < have * 128;
+                const int64_t at = there ? (static_cast<int64_t>(t) * 2 * groups * kC + x) * 8 : 0;
+                const uint32_t to = st + W::rows + (x >> 7) * W::kGroup + t * 6144 + (x >> 6 & 1) * 3072 + (x & 63) * 16;
+                copy16(to, up + at, there);
+                copy16(to + 1024, wp + at, there);
             }
             {
                 const int r = tid >> 2, u = tid & 3;
@@ -716,10 +948,10 @@ __global__ void __launch_bounds__(256) gdr_grad_tc_kernel(const __grid_constant_
                     const uint32_t hi = st + W::rows + gr * W::kGroup, lo = hi + 6144;
                     const uint64_t wy = tensor::operand(hi + 1024, 3072, 128), w0 = tensor::operand(lo + 1024, 3072, 128);
                     const uint64_t uh = tensor::operand(hi, 3072, 128), ul = tensor::operand(lo, 3072, 128);
-                    const uint32_t sa = st + W::S + gr * 2 * W::kImage, da = st + W::dS + gr * 2 * W::kImage;
-                    const uint64_t sh = tensor::operand(sa, 128, 256), sl = tensor::operand(sa + W::kImage, 128, 256);
-                    const uint64_t dh = tensor::operand(da, 128, 256), dl = tensor::operand(da + W::kImage, 128, 256);
-                    constexpr uint32_t wide = tensor::shape(128, DKP, false, true), square = tensor::shape(128, 64, false, false);
+                    const uint32_t sa = st + W::S + gr * 2 * W::kUnit, da = st + W::dS + gr * 2 * W::kUnit;
+                    const uint64_t sh = tensor::operand(sa, W::kUnit, 128), sl = tensor::operand(sa + W::kTerm, W::kUnit, 128);
+                    const uint64_t dh = tensor::operand(da, W::kUnit, 128), dl = tensor::operand(da + W::kTerm, W::kUnit, 128);
+                    constexpr uint32_t wide = tensor::shape(128, DKP, false, false), square = tensor::shape(128, 64, false, false);
                     const bool add = s + gr > 0;
                     tensor::mma(D3, wy, uh, square, add);
                     tensor::mma(D3, wy, ul, square, true);
@@ -739,13 +971,13 @@ __global__ void __launch_bounds__(256) gdr_grad_tc_kernel(const __grid_constant_
                 load();
             }
             if (vec[kC - 1] != 0.f) {   // <dS', S>, both in the same tiles
-                for (int x = tid; x < 2 * 16 * DKP / 8; x += W::threads) {
-                    const int o = x / (W::kImage / 16) * (2 * W::kImage) + x % (W::kImage / 16) * 16;
+                for (int x = tid; x < W::kTerm / 16; x += W::threads) {
+                    const int o = x * 16;
                     float p[8] = {}, q[8] = {};
 #pragma unroll
                     for (int t = 1; t >= 0; --t) {
-                        const uint4 y = *reinterpret_cast<const uint4*>(smem + so + W::S + o + t * W::kImage);
-                        const uint4 z = *reinterpret_cast<const uint4*>(smem + so + W::dS + o + t * W::kImage);
+                        const uint4 y = *reinterpret_cast<const uint4*>(smem + so + W::S + o + t * W::kTerm);
+                        const uint4 z = *reinterpret_cast<const uint4*>(smem + so + W::dS + o + t * W::kTerm);
                         const uint32_t yw[4] = {y.x, y.y, y.z, y.w}, zw[4] = {z.x, z.y, z.z, z.w};
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
@@ -1004,12 +1236,22 @@ cudaError_t grad(const Args& a, int64_t blocks, cudaStream_t cs) {
     return launch_dependent(k, dim3(static_cast<unsigned>(blocks * a.Hv)), dim3(W::threads), W::bytes, cs, a);
 }
 
+template <int DKP, int BV>
+cudaError_t back_tc(const Args& a, cudaStream_t cs) {
+    using W = WalkTc<DKP, BV>;
+    auto* const k = gdr_back_tc_kernel<DKP, BV>;
+    const cudaError_t e = big_smem(k, W::bytes);
+    if (e != cudaSuccess) return e;
+    const int64_t grid = static_cast<int64_t>(a.P) * a.Hv * ((a.dv + BV - 1) / BV);
+    return launch_dependent(k, dim3(static_cast<unsigned>(grid)), dim3(W::threads), W::bytes, cs, a);
+}
+
 template <int DKP>
 cudaError_t back_bf16(const Args& a, cudaStream_t cs) {
     switch (columns(a)) {
-        case 32: return back<1, DKP, 32>(a, cs);
-        case 64: return back<1, DKP, 64>(a, cs);
-        default: return back<1, DKP, 128>(a, cs);
+        case 32: return back_tc<DKP, 32>(a, cs);
+        case 64: return back_tc<DKP, 64>(a, cs);
+        default: return back_tc<DKP, 128>(a, cs);
     }
 }
 
@@ -1049,7 +1291,6 @@ extern "C" sdm_status sdm_gdr_backward(const sdm_gdr_shape* shape, const void* q
     a.dstates = reinterpret_cast<__nv_bfloat16*>(w + l.dstates);
     a.du = reinterpret_cast<__nv_bfloat16*>(w + l.du);
     a.part = shape->v_heads == shape->k_heads ? nullptr : reinterpret_cast<float*>(w + l.part);
-    a.tri_planes = 2 * terms(shape);
     const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
     cudaError_t e = cudaSuccess;
     if (shape->rows > 0) {
