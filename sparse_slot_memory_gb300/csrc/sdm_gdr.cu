@@ -513,34 +513,18 @@ __global__ void __launch_bounds__(BV * 4) gdr_walk_tc_kernel(const __grid_consta
     const uint32_t base = smem_of(smem), bar = smem_of(bars);
     const int cols = min(BV, a.dv - c0), nb = (a.dv + 15) / 16 * 2;   // units of 8 value columns that are saved
 
+    WalkCopies<DKP, BV> copies(a, a.v, base, smem_of(vecs), b, id0, 0, kh, h, c0, cols, tid);
     auto load_kq = [&](int64_t j) {
         if (j < blocks) {
-            const int n = static_cast<int>(min(len - j * kC, int64_t(kC)));
-            const int64_t r0 = b + j * kC;
-            const uint32_t to = base + W::KQ + static_cast<int>(j & 1) * W::kKQ;
-#pragma unroll
-            for (int i = tid; i < 2 * kC * (DKP / 8); i += W::threads) {
-                const int r = i / (DKP / 8), u = i % (DKP / 8), t = r & 63;
-                const Planes& x = r < kC ? a.k : a.q;
-                const bool there = t < n && u * 8 < a.dk;
-                copy16(to + stacked_at(r, u), there ? x.p + (r0 + t) * x.ld + kh * a.dk + u * 8 : x.p, there);
-            }
-            for (int i = tid; i < kVecs * kC / 4; i += W::threads)
-                copy16(smem_of(vecs[j & 1]) + i * 16, a.vec + ((id0 + j) * a.Hv + h) * kVecs * kC + i * 4, true);
+            copies.kq(static_cast<int>(j & 1), static_cast<int>(min(len - j * kC, int64_t(kC))), tid);
+            copies.go_kq(1);
         }
         copies_commit();
     };
     auto load_vt = [&](int64_t j) {
         if (j < blocks) {
-            const int n = static_cast<int>(min(len - j * kC, int64_t(kC)));
-            const int64_t r0 = b + j * kC;
-#pragma unroll
-            for (int i = tid; i < kC * (BV / 8); i += W::threads) {
-                const int r = i / (BV / 8), u = i % (BV / 8);
-                const bool there = r < n && u * 8 < cols;
-                copy16(base + W::V + rows_at(r, u), there ? a.v.p + (r0 + r) * a.v.ld + h * a.dv + c0 + u * 8 : a.v.p, there);
-            }
-            load_tri_stacked<W::threads>(base + W::T, a.tri + ((id0 + j) * a.Hv + h) * 4 * int64_t(kC * kC), tid);
+            copies.vt(static_cast<int>(min(len - j * kC, int64_t(kC))), tid);
+            copies.go_vt(1);
         }
         copies_commit();
     };
@@ -553,15 +537,15 @@ __global__ void __launch_bounds__(BV * 4) gdr_walk_tc_kernel(const __grid_consta
     const int r = 32 * (w & 3) + lane, part = w >> 2, i = r & 63;   // a row of tensor memory, 32 columns, a token
     const bool key = r < kC;
     const int vc = c0 + 32 * part;                                  // this thread's first value column
-    float S[32];
+    uint64_t S[16];   // 32 columns of a row of the state, in pairs
     {
         const float* const h0 = a.h0 == nullptr ? nullptr : a.h0 + ((static_cast<int64_t>(p) * a.Hv + h) * a.dk + r) * a.dv + vc;
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
             float v[4] = {};
             if (h0 != nullptr && r < a.dk && vc + 4 * q < a.dv) load4(h0 + 4 * q).get(v);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) S[4 * q + e] = v[e];
+            S[2 * q] = pack2(v[0], v[1]);
+            S[2 * q + 1] = pack2(v[2], v[3]);
         }
     }
     unsigned char* const Sp = smem + W::S + part * 4 * (DKP * 16) + r * 16;   // a unit of 8 columns: DKP rows of 16 bytes
@@ -590,20 +574,25 @@ __global__ void __launch_bounds__(BV * 4) gdr_walk_tc_kernel(const __grid_consta
     tensor::fence_after();
     const uint32_t Da = tmem, Db = tmem + BV, Dc = tmem + 2 * BV;
     const uint32_t mine = (static_cast<uint32_t>(w & 3) << 21) + 32 * part;
+    // the products' operands: per 16 summands 4096 bytes of [K; Q] and T along their rows, 256 of the others and along tokens
+    const uint64_t KQd = tensor::operand(base + W::KQ, 2048, 128), KTd = tensor::operand(base + W::KQ, 128, 2048);
+    const uint64_t Sd = tensor::operand(base + W::S, 128, DKP * 16), Td = tensor::operand(base + W::T, 2048, 128);
+    const uint64_t Rd = tensor::operand(base + W::R, 128, 1024);
     uint32_t phase = 0;
     bool bad = false;
     for (int64_t j = 0; j < blocks; ++j) {
-        const uint32_t KQ = base + W::KQ + static_cast<int>(j & 1) * W::kKQ;
+        const uint64_t kq = static_cast<uint64_t>((j & 1) * W::kKQ) >> 4;   // the stage's distance, in a descriptor's units
         const float* const vec = vecs[j & 1];
         copies_wait<1>();
         async_fence();
         if (__syncthreads_or(bad)) break;
         if (tid == 0) {
             tensor::fence_after();
+#pragma unroll
             for (int ks = 0; ks < DKP / 16; ++ks)
+#pragma unroll
                 for (int t = 0; t < 2; ++t)
-                    tensor::mma(Da, tensor::operand(KQ + ks * 4096, 2048, 128), tensor::operand(base + W::S + t * W::kS + ks * 256, 128, DKP * 16),
-                                tensor::shape(128, BV, false, true), ks + t > 0);
+                    tensor::mma(Da, KQd + kq + ks * 256, Sd + (t * W::kS + ks * 256) / 16, tensor::shape(128, BV, false, true), ks + t > 0);
             tensor::commit(bar);
         }
         load_kq(j + 1);
@@ -612,19 +601,18 @@ __global__ void __launch_bounds__(BV * 4) gdr_walk_tc_kernel(const __grid_consta
         async_fence();
         __syncthreads();
         tensor::fence_after();
-        float x[32];
+        uint64_t x[16];
         tensor::load32(Da + mine, x);
-        tensor::loaded();
         const float eg = vec[i];
         if (key) {   // beta R
             const float bt = vec[kC + i];
+            const uint64_t f = pack2(-bt * eg, -bt * eg), bt2 = pack2(bt, bt);
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 const uint4 v = *reinterpret_cast<const uint4*>(smem + W::V + rows_at(i, 4 * part + q));
                 const uint32_t vw[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    x[8 * q + e] = bt * fmaf(-eg, x[8 * q + e], __uint_as_float(e & 1 ? vw[e >> 1] & 0xFFFF0000u : vw[e >> 1] << 16));
+                for (int e = 0; e < 4; ++e) x[4 * q + e] = fma2(f, x[4 * q + e], mul2(bt2, widen2(vw[e])));
             }
             put_terms(Rp, Rp + W::kR, 1024, x);
         }
@@ -633,25 +621,21 @@ __global__ void __launch_bounds__(BV * 4) gdr_walk_tc_kernel(const __grid_consta
         __syncthreads();
         if (tid == 0) {
             tensor::fence_after();
-            for (int t = 0; t < 3; ++t)   // T's first term with both of R's, its second with the first
-                for (int ks = 0; ks < 4; ++ks)
-                    tensor::mma(Db, tensor::operand(base + W::T + (t >> 1) * 16384 + ks * 4096, 2048, 128),
-                                tensor::operand(base + W::R + (t & 1) * W::kR + ks * 256, 128, 1024), tensor::shape(128, BV, false, true), t + ks > 0);
-            tensor::commit(bar + 8);
-        }
-        if (!key) {
 #pragma unroll
-            for (int e = 0; e < 32; ++e) x[e] *= a.scale * eg;
+            for (int t = 0; t < 3; ++t)   // T's first term with both of R's, its second with the first
+#pragma unroll
+                for (int ks = 0; ks < 4; ++ks)
+                    tensor::mma(Db, Td + (t >> 1) * 1024 + ks * 256, Rd + ((t & 1) * W::kR + ks * 256) / 16, tensor::shape(128, BV, false, true), t + ks > 0);
+            tensor::commit(bar + 8);
         }
         bad |= !tensor::barrier_wait(bar + 8, phase);
         tensor::fence_after();
-        float u[32];
+        uint64_t u[16];
         tensor::load32(Db + mine, u);
-        tensor::loaded();
         if (key) {
             const float c = vec[2 * kC + i];
 #pragma unroll
-            for (int e = 0; e < 32; ++e) x[e] = c * u[e];
+            for (int e = 0; e < 16; ++e) x[e] = mul2(pack2(c, c), u[e]);
             put_terms(Rp, Rp + W::kR, 1024, x);
         }
         async_fence();
@@ -659,10 +643,11 @@ __global__ void __launch_bounds__(BV * 4) gdr_walk_tc_kernel(const __grid_consta
         __syncthreads();
         if (tid == 0) {
             tensor::fence_after();
+#pragma unroll
             for (int ks = 0; ks < 4; ++ks)
+#pragma unroll
                 for (int t = 0; t < 2; ++t)
-                    tensor::mma(Dc, tensor::operand(KQ + ks * 256, 128, 2048), tensor::operand(base + W::R + t * W::kR + ks * 256, 128, 1024),
-                                tensor::shape(128, BV, true, true), ks + t > 0);
+                    tensor::mma(Dc, KTd + kq + ks * 16, Rd + (t * W::kR + ks * 256) / 16, tensor::shape(128, BV, true, true), ks + t > 0);
             tensor::commit(bar + 16);
         }
         load_vt(j + 1);
@@ -674,22 +659,28 @@ __global__ void __launch_bounds__(BV * 4) gdr_walk_tc_kernel(const __grid_consta
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     if (vc / 8 + q >= nb) continue;
-                    uint32_t t[4][2];
+                    uint32_t hi[4], lo[4];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) split2<2>(u[8 * q + 2 * e], u[8 * q + 2 * e + 1], t[e]);
-                    *reinterpret_cast<uint4*>(to + q * 1024) = make_uint4(t[0][0], t[1][0], t[2][0], t[3][0]);
-                    *reinterpret_cast<uint4*>(to + (nb + q) * 1024) = make_uint4(t[0][1], t[1][1], t[2][1], t[3][1]);
+                    for (int e = 0; e < 4; ++e) terms2(u[4 * q + e], hi[e], lo[e]);
+                    *reinterpret_cast<uint4*>(to + q * 1024) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    *reinterpret_cast<uint4*>(to + (nb + q) * 1024) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                 }
             }
         } else if (i < n) {   // the row's answer
             __nv_bfloat16* const y = static_cast<__nv_bfloat16*>(a.y) + (r0 + i) * a.y_ld + h * a.dv + vc;
+            const uint64_t f = pack2(a.scale * eg, a.scale * eg);
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-                if (vc + 8 * q < a.dv)
-                    *reinterpret_cast<uint4*>(y + 8 * q) = make_uint4(round2(x[8 * q] + u[8 * q], x[8 * q + 1] + u[8 * q + 1]),
-                                                                      round2(x[8 * q + 2] + u[8 * q + 2], x[8 * q + 3] + u[8 * q + 3]),
-                                                                      round2(x[8 * q + 4] + u[8 * q + 4], x[8 * q + 5] + u[8 * q + 5]),
-                                                                      round2(x[8 * q + 6] + u[8 * q + 6], x[8 * q + 7] + u[8 * q + 7]));
+            for (int q = 0; q < 4; ++q) {
+                if (vc + 8 * q >= a.dv) continue;
+                uint32_t o[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float s, t;
+                    unpack2(fma2(f, x[4 * q + e], u[4 * q + e]), s, t);
+                    o[e] = round2(s, t);
+                }
+                *reinterpret_cast<uint4*>(y + 8 * q) = make_uint4(o[0], o[1], o[2], o[3]);
+            }
         }
         __syncwarp();
         const float last = vec[kC - 1];
@@ -697,9 +688,8 @@ __global__ void __launch_bounds__(BV * 4) gdr_walk_tc_kernel(const __grid_consta
         phase ^= 1;
         tensor::fence_after();
         tensor::load32(Dc + mine, u);
-        tensor::loaded();
 #pragma unroll
-        for (int e = 0; e < 32; ++e) S[e] = fmaf(last, S[e], u[e]);
+        for (int e = 0; e < 16; ++e) S[e] = fma2(pack2(last, last), S[e], u[e]);
         put_state(j + 1);
         tensor::fence_before();
     }
@@ -707,7 +697,7 @@ __global__ void __launch_bounds__(BV * 4) gdr_walk_tc_kernel(const __grid_consta
         float* const hT = a.hT + ((static_cast<int64_t>(p) * a.Hv + h) * a.dk + r) * a.dv + vc;
 #pragma unroll
         for (int q = 0; q < 8; ++q)
-            if (vc + 4 * q < a.dv) *reinterpret_cast<float4*>(hT + 4 * q) = make_float4(S[4 * q], S[4 * q + 1], S[4 * q + 2], S[4 * q + 3]);
+            if (vc + 4 * q < a.dv) st4(hT + 4 * q, Quad{S[2 * q], S[2 * q + 1]});
     }
     copies_wait<0>();
     if (__syncthreads_or(bad) && tid == 0 && a.status != nullptr) atomicOr(a.status, SDM_DEV_STALLED);

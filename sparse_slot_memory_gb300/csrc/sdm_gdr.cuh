@@ -190,14 +190,14 @@ __device__ __forceinline__ void load_tri(uint32_t dst, const __nv_bfloat16* src,
 
 // A tile's stacked halves, [128 rows], in cores of 8 rows (sdm_tensor.cuh)
 __device__ __forceinline__ uint32_t stacked_at(int r, int u) { return static_cast<uint32_t>(u * 2048 + (r >> 3) * 128 + (r & 7) * 16); }
-// Both terms of [T; scale A T]: the blocks of 16 up to the diagonal
-template <int THREADS>
-__device__ __forceinline__ void load_tri_stacked(uint32_t dst, const __nv_bfloat16* src, int tid) {
-#pragma unroll
-    for (int i = tid; i < 2 * 1024; i += THREADS)
-        if ((i >> 7 & 7) <= (i >> 4 & 3) * 2 + 1) copy16(dst + i * 16, src + i * 8, true);   // i: term, unit, row
+// Copy number i of a tile of rows of U units into such cores: eight rows of a unit lie in 128 contiguous bytes, so a warp takes eight
+// rows of four units (64 bytes of a row) and meets no bank twice.
+template <int U>
+__device__ __forceinline__ void core_place(int i, int& r, int& u) {
+    const int x = i >> 5;
+    r = (i & 7) + x / (U / 4) * 8;
+    u = (i >> 3 & 3) + x % (U / 4) * 4;
 }
-
 // ---- fragments ------------------------------------------------------------------------------------------
 // (loads of fragments keep their place among barriers and stores by being volatile; the products are free to move)
 __device__ __forceinline__ void ldsm4(uint32_t (&f)[4], uint32_t a) {
@@ -329,17 +329,95 @@ struct WalkTc {
     static constexpr int threads = BV * 4, cols = BV <= 32 ? 128 : BV == 64 ? 256 : 512;
 };
 
-// 32 values as two terms: units of 8 columns, 16 bytes each, `pitch` bytes apart
-__device__ __forceinline__ void put_terms(unsigned char* hi, unsigned char* lo, int pitch, const float (&v)[32]) {
+// Two float32 as two terms of bfloat16, the rests subtracted together
+__device__ __forceinline__ void terms2(uint64_t v, uint32_t& hi, uint32_t& lo) {
+    float x, y;
+    unpack2(v, x, y);
+    hi = round2(x, y);
+    float s, t;
+    unpack2(add2(v, pack2(__uint_as_float((hi << 16) ^ 0x80000000u), __uint_as_float((hi & 0xFFFF0000u) ^ 0x80000000u))), s, t);
+    lo = round2(s, t);
+}
+// 32 values (16 pairs) as two terms: units of 8 columns, 16 bytes each, `pitch` bytes apart
+__device__ __forceinline__ void put_terms(unsigned char* hi, unsigned char* lo, int pitch, const uint64_t (&v)[16]) {
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
-        uint32_t t[4][2];
+        uint32_t h[4], l[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) split2<2>(v[8 * q + 2 * e], v[8 * q + 2 * e + 1], t[e]);
-        *reinterpret_cast<uint4*>(hi + q * pitch) = make_uint4(t[0][0], t[1][0], t[2][0], t[3][0]);
-        *reinterpret_cast<uint4*>(lo + q * pitch) = make_uint4(t[0][1], t[1][1], t[2][1], t[3][1]);
+        for (int e = 0; e < 4; ++e) terms2(v[4 * q + e], h[e], l[e]);
+        *reinterpret_cast<uint4*>(hi + q * pitch) = make_uint4(h[0], h[1], h[2], h[3]);
+        *reinterpret_cast<uint4*>(lo + q * pitch) = make_uint4(l[0], l[1], l[2], l[3]);
     }
 }
+// Two bfloat16 as a pair of float32
+__device__ __forceinline__ uint64_t widen2(uint32_t w) { return pack2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u)); }
+
+// What a thread copies of each block's queries, keys and rows of values: its places stay the same, its addresses go on by 64 rows
+template <int DKP, int BV>
+struct WalkCopies {
+    using W = WalkTc<DKP, BV>;
+    static constexpr int kRows = W::threads / (DKP / 8), kSlots = kC / kRows;   // rows of a sweep over K (or Q), sweeps
+    static_assert(kC % kRows == 0 && W::threads / (BV / 8) == 32, "whole sweeps");
+    const __nv_bfloat16 *k, *q, *v, *tri, *none;
+    const float* vec;
+    int64_t k_ld, q_ld, v_ld, heads;
+    uint32_t kq_at, v_at, t_at, vec_at;
+    int r, vr;
+    bool on, v_on;
+    // rows: V or dY; block j's first row is b + 64 j
+    __device__ __forceinline__ WalkCopies(const Args& a, const Planes& rows, uint32_t base, uint32_t vecs, int64_t b, int64_t id0, int64_t j, int kh,
+                                          int h, int c0, int cols, int tid) {
+        int u, vu;
+        core_place<DKP / 8>(tid, r, u);
+        core_place<BV / 8>(tid, vr, vu);
+        on = u * 8 < a.dk;
+        v_on = vu * 8 < cols;
+        k_ld = a.k.ld;
+        q_ld = a.q.ld;
+        v_ld = rows.ld;
+        none = a.k.p;
+        k = a.k.p + (b + j * kC + r) * k_ld + kh * a.dk + u * 8;
+        q = a.q.p + (b + j * kC + r) * q_ld + kh * a.dk + u * 8;
+        v = rows.p + (b + j * kC + vr) * v_ld + h * a.dv + c0 + vu * 8;
+        kq_at = base + W::KQ + stacked_at(r, u);
+        v_at = base + W::V + rows_at(vr, vu);
+        heads = a.Hv;
+        tri = a.tri + ((id0 + j) * heads + h) * 4 * int64_t(kC * kC) + tid * 8;
+        t_at = base + W::T + tid * 16;
+        vec = a.vec + ((id0 + j) * heads + h) * kVecs * kC + tid * 4;
+        vec_at = vecs + tid * 16;
+    }
+    // [K; Q] and the decays of a block of n rows, to stage `s`
+    __device__ __forceinline__ void kq(int s, int n, int tid) {
+        const uint32_t to = kq_at + s * W::kKQ;
+#pragma unroll
+        for (int x = 0; x < kSlots; ++x) {
+            const bool there = on && r + x * kRows < n;
+            copy16(to + x * kRows * 16, there ? k + x * kRows * k_ld : none, there);
+            copy16(to + 1024 + x * kRows * 16, there ? q + x * kRows * q_ld : none, there);
+        }
+        if (tid < kVecs * kC / 4) copy16(vec_at + s * (kVecs * kC * 4), vec, true);
+    }
+    __device__ __forceinline__ void vt(int n, int tid) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const bool there = v_on && vr + 32 * x < n;
+            copy16(v_at + x * 32 * 16, there ? v + x * 32 * v_ld : none, there);
+        }
+#pragma unroll
+        for (int x = 0; x < 2048 / W::threads; ++x)
+            if ((x * (W::threads / 128) + (tid >> 7) & 7) <= (tid >> 4 & 3) * 2 + 1) copy16(t_at + x * W::threads * 16, tri + x * W::threads * 8, true);
+    }
+    __device__ __forceinline__ void go_kq(int blocks) {
+        k += blocks * kC * k_ld;
+        q += blocks * kC * q_ld;
+        vec += blocks * heads * (kVecs * kC);
+    }
+    __device__ __forceinline__ void go_vt(int blocks) {
+        v += blocks * kC * v_ld;
+        tri += blocks * heads * (4 * kC * kC);
+    }
+};
 
 // ---- host side, in sdm_gdr.cu ---------------------------------------------------------------------------
 inline int padded(int d) { return d <= 64 ? 64 : 128; }

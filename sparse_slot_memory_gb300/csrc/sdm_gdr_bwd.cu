@@ -254,34 +254,18 @@ __global__ void __launch_bounds__(BV * 4) gdr_back_tc_kernel(const __grid_consta
     const uint32_t base = smem_of(smem), bar = smem_of(bars);
     const int cols = min(BV, a.dv - c0), nb = (a.dv + 15) / 16 * 2;
 
+    WalkCopies<DKP, BV> copies(a, a.dy, base, smem_of(vecs), b, id0, blocks - 1, kh, h, c0, cols, tid);
     auto load_kq = [&](int64_t j) {
         if (j >= 0) {
-            const int n = static_cast<int>(min(len - j * kC, int64_t(kC)));
-            const int64_t r0 = b + j * kC;
-            const uint32_t to = base + W::KQ + static_cast<int>(j & 1) * W::kKQ;
-#pragma unroll
-            for (int i = tid; i < 2 * kC * (DKP / 8); i += W::threads) {
-                const int r = i / (DKP / 8), u = i % (DKP / 8), t = r & 63;
-                const Planes& x = r < kC ? a.k : a.q;
-                const bool there = t < n && u * 8 < a.dk;
-                copy16(to + stacked_at(r, u), there ? x.p + (r0 + t) * x.ld + kh * a.dk + u * 8 : x.p, there);
-            }
-            for (int i = tid; i < kVecs * kC / 4; i += W::threads)
-                copy16(smem_of(vecs[j & 1]) + i * 16, a.vec + ((id0 + j) * a.Hv + h) * kVecs * kC + i * 4, true);
+            copies.kq(static_cast<int>(j & 1), static_cast<int>(min(len - j * kC, int64_t(kC))), tid);
+            copies.go_kq(-1);
         }
         copies_commit();
     };
     auto load_yt = [&](int64_t j) {
         if (j >= 0) {
-            const int n = static_cast<int>(min(len - j * kC, int64_t(kC)));
-            const int64_t r0 = b + j * kC;
-#pragma unroll
-            for (int i = tid; i < kC * (BV / 8); i += W::threads) {
-                const int r = i / (BV / 8), u = i % (BV / 8);
-                const bool there = r < n && u * 8 < cols;
-                copy16(base + W::V + rows_at(r, u), there ? a.dy.p + (r0 + r) * a.dy.ld + h * a.dv + c0 + u * 8 : a.dy.p, there);
-            }
-            load_tri_stacked<W::threads>(base + W::T, a.tri + ((id0 + j) * a.Hv + h) * 4 * int64_t(kC * kC), tid);
+            copies.vt(static_cast<int>(min(len - j * kC, int64_t(kC))), tid);
+            copies.go_vt(-1);
         }
         copies_commit();
     };
@@ -293,15 +277,15 @@ __global__ void __launch_bounds__(BV * 4) gdr_back_tc_kernel(const __grid_consta
     const int r = 32 * (w & 3) + lane, part = w >> 2, i = r & 63;
     const bool key = r < kC;
     const int vc = c0 + 32 * part;
-    float S[32];
+    uint64_t S[16];
     {
         const float* const d = a.dhT == nullptr ? nullptr : a.dhT + ((static_cast<int64_t>(p) * a.Hv + h) * a.dk + r) * a.dv + vc;
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
             float v[4] = {};
             if (d != nullptr && r < a.dk && vc + 4 * q < a.dv) load4(d + 4 * q).get(v);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) S[4 * q + e] = v[e];
+            S[2 * q] = pack2(v[0], v[1]);
+            S[2 * q + 1] = pack2(v[2], v[3]);
         }
     }
     unsigned char* const Sp = smem + W::S + part * 4 * (DKP * 16) + r * 16;
@@ -331,20 +315,25 @@ __global__ void __launch_bounds__(BV * 4) gdr_back_tc_kernel(const __grid_consta
     tensor::fence_after();
     const uint32_t Da = tmem, Db = tmem + BV, Dc = tmem + 2 * BV;
     const uint32_t mine = (static_cast<uint32_t>(w & 3) << 21) + 32 * part;
+    const uint64_t KQd = tensor::operand(base + W::KQ, 2048, 128), KTd = tensor::operand(base + W::KQ, 128, 2048);
+    const uint64_t Sd = tensor::operand(base + W::S, 128, DKP * 16), Yd = tensor::operand(base + W::S, 128, 1024);
+    const uint64_t Td = tensor::operand(base + W::T, 128, 2048), dYd = tensor::operand(base + W::V, 128, 1024);
+    const uint64_t Rd = tensor::operand(base + W::R, 128, 1024);
     uint32_t phase = 0;
     bool bad = false;
     for (int64_t j = blocks - 1; j >= 0; --j) {
-        const uint32_t KQ = base + W::KQ + static_cast<int>(j & 1) * W::kKQ;
+        const uint64_t kq = static_cast<uint64_t>((j & 1) * W::kKQ) >> 4;
         const float* const vec = vecs[j & 1];
         copies_wait<1>();
         async_fence();
         if (__syncthreads_or(bad)) break;
         if (tid == 0) {
             tensor::fence_after();
+#pragma unroll
             for (int ks = 0; ks < DKP / 16; ++ks)
+#pragma unroll
                 for (int t = 0; t < 2; ++t)
-                    tensor::mma(Da, tensor::operand(KQ + ks * 4096, 2048, 128), tensor::operand(base + W::S + t * W::kS + ks * 256, 128, DKP * 16),
-                                tensor::shape(128, BV, false, true), ks + t > 0);
+                    tensor::mma(Da, KQd + kq + ks * 256, Sd + (t * W::kS + ks * 256) / 16, tensor::shape(128, BV, false, true), ks + t > 0);
             tensor::commit(bar);
         }
         load_kq(j - 1);
@@ -354,19 +343,19 @@ __global__ void __launch_bounds__(BV * 4) gdr_back_tc_kernel(const __grid_consta
         __syncthreads();
         tensor::fence_after();
         if (tid == 0) {   // what dY gives by A T
+#pragma unroll
             for (int t = 0; t < 2; ++t)
+#pragma unroll
                 for (int ks = 0; ks < 4; ++ks)
-                    tensor::mma(Db, tensor::operand(base + W::T + t * 16384 + 1024 + ks * 256, 128, 2048),
-                                tensor::operand(base + W::V + ks * 256, 128, 1024), tensor::shape(128, BV, true, true), t + ks > 0);
+                    tensor::mma(Db, Td + (t * 16384 + 1024 + ks * 256) / 16, dYd + ks * 16, tensor::shape(128, BV, true, true), t + ks > 0);
         }
-        float x[32];
+        uint64_t x[16];
         const float eg = vec[i], bt = vec[kC + i];
         if (key) {
             tensor::load32(Da + mine, x);
-            tensor::loaded();
             const float c = vec[2 * kC + i];
 #pragma unroll
-            for (int e = 0; e < 32; ++e) x[e] *= c;
+            for (int e = 0; e < 16; ++e) x[e] = mul2(pack2(c, c), x[e]);
             put_terms(Xp, Xp + W::kR, 1024, x);
         } else {
             const float f = a.scale * eg;
@@ -375,7 +364,7 @@ __global__ void __launch_bounds__(BV * 4) gdr_back_tc_kernel(const __grid_consta
                 const uint4 v = *reinterpret_cast<const uint4*>(smem + W::V + rows_at(i, 4 * part + q));
                 const uint32_t vw[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-                for (int e = 0; e < 8; ++e) x[8 * q + e] = f * __uint_as_float(e & 1 ? vw[e >> 1] & 0xFFFF0000u : vw[e >> 1] << 16);
+                for (int e = 0; e < 4; ++e) x[4 * q + e] = mul2(pack2(f, f), widen2(vw[e]));
             }
             put_terms(Yp, Yp + W::kS, 1024, x);
         }
@@ -384,25 +373,26 @@ __global__ void __launch_bounds__(BV * 4) gdr_back_tc_kernel(const __grid_consta
         __syncthreads();
         if (tid == 0) {
             tensor::fence_after();
+#pragma unroll
             for (int t = 0; t < 3; ++t)   // T's first term with both of x's, its second with the first
+#pragma unroll
                 for (int ks = 0; ks < 4; ++ks)
-                    tensor::mma(Db, tensor::operand(base + W::T + (t >> 1) * 16384 + ks * 256, 128, 2048),
-                                tensor::operand(base + W::R + (t & 1) * W::kR + ks * 256, 128, 1024), tensor::shape(128, BV, true, true), true);
+                    tensor::mma(Db, Td + (t >> 1) * 1024 + ks * 16, Rd + ((t & 1) * W::kR + ks * 256) / 16, tensor::shape(128, BV, true, true), true);
             tensor::commit(bar + 8);
+#pragma unroll
             for (int ks = 0; ks < 4; ++ks)
+#pragma unroll
                 for (int t = 0; t < 2; ++t)
-                    tensor::mma(Dc, tensor::operand(KQ + 1024 + ks * 256, 128, 2048), tensor::operand(base + W::S + t * W::kS + ks * 256, 128, 1024),
-                                tensor::shape(128, BV, true, true), ks + t > 0);
+                    tensor::mma(Dc, KTd + kq + 64 + ks * 16, Yd + (t * W::kS + ks * 256) / 16, tensor::shape(128, BV, true, true), ks + t > 0);
         }
         bad |= !tensor::barrier_wait(bar + 8, phase);
         tensor::fence_after();
-        float u[32];
+        uint64_t u[16];
         if (key) {
             tensor::load32(Db + mine, u);
-            tensor::loaded();
             const float f = -eg * bt;
 #pragma unroll
-            for (int e = 0; e < 32; ++e) x[e] = f * u[e];
+            for (int e = 0; e < 16; ++e) x[e] = mul2(pack2(f, f), u[e]);
             put_terms(Xp, Xp + W::kR, 1024, x);
         }
         async_fence();
@@ -410,10 +400,11 @@ __global__ void __launch_bounds__(BV * 4) gdr_back_tc_kernel(const __grid_consta
         __syncthreads();
         if (tid == 0) {
             tensor::fence_after();
+#pragma unroll
             for (int ks = 0; ks < 4; ++ks)
+#pragma unroll
                 for (int t = 0; t < 2; ++t)
-                    tensor::mma(Dc, tensor::operand(KQ + ks * 256, 128, 2048), tensor::operand(base + W::R + t * W::kR + ks * 256, 128, 1024),
-                                tensor::shape(128, BV, true, true), true);
+                    tensor::mma(Dc, KTd + kq + ks * 16, Rd + (t * W::kR + ks * 256) / 16, tensor::shape(128, BV, true, true), true);
             tensor::commit(bar + 16);
         }
         load_yt(j - 1);
@@ -424,14 +415,16 @@ __global__ void __launch_bounds__(BV * 4) gdr_back_tc_kernel(const __grid_consta
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 if (vc / 8 + q >= nb) continue;
-                uint32_t t[4][2], o[4];
+                uint32_t hi[4], lo[4], o[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    split2<2>(u[8 * q + 2 * e], u[8 * q + 2 * e + 1], t[e]);
-                    o[e] = round2(bt * u[8 * q + 2 * e], bt * u[8 * q + 2 * e + 1]);
+                    terms2(u[4 * q + e], hi[e], lo[e]);
+                    float s, t;
+                    unpack2(mul2(pack2(bt, bt), u[4 * q + e]), s, t);
+                    o[e] = round2(s, t);
                 }
-                *reinterpret_cast<uint4*>(to + q * 1024) = make_uint4(t[0][0], t[1][0], t[2][0], t[3][0]);
-                *reinterpret_cast<uint4*>(to + (nb + q) * 1024) = make_uint4(t[0][1], t[1][1], t[2][1], t[3][1]);
+                *reinterpret_cast<uint4*>(to + q * 1024) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                *reinterpret_cast<uint4*>(to + (nb + q) * 1024) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                 if (there && vc + 8 * q < a.dv) *reinterpret_cast<uint4*>(dv + 8 * q) = make_uint4(o[0], o[1], o[2], o[3]);
             }
         }
@@ -441,9 +434,8 @@ __global__ void __launch_bounds__(BV * 4) gdr_back_tc_kernel(const __grid_consta
         phase ^= 1;
         tensor::fence_after();
         tensor::load32(Dc + mine, u);
-        tensor::loaded();
 #pragma unroll
-        for (int e = 0; e < 32; ++e) S[e] = fmaf(last, S[e], u[e]);
+        for (int e = 0; e < 16; ++e) S[e] = fma2(pack2(last, last), S[e], u[e]);
         put_state(j - 1);
         tensor::fence_before();
     }
@@ -451,7 +443,7 @@ __global__ void __launch_bounds__(BV * 4) gdr_back_tc_kernel(const __grid_consta
         float* const d = a.dh0 + ((static_cast<int64_t>(p) * a.Hv + h) * a.dk + r) * a.dv + vc;
 #pragma unroll
         for (int q = 0; q < 8; ++q)
-            if (vc + 4 * q < a.dv) *reinterpret_cast<float4*>(d + 4 * q) = make_float4(S[4 * q], S[4 * q + 1], S[4 * q + 2], S[4 * q + 3]);
+            if (vc + 4 * q < a.dv) st4(d + 4 * q, Quad{S[2 * q], S[2 * q + 1]});
     }
     copies_wait<0>();
     if (__syncthreads_or(bad) && tid == 0 && a.status != nullptr) atomicOr(a.status, SDM_DEV_STALLED);
@@ -869,7 +861,8 @@ __global__ void __launch_bounds__(256) gdr_grad_tc_kernel(const __grid_constant_
                 copy16(to + 1024, wp + at, there);
             }
             {
-                const int r = tid >> 2, u = tid & 3;
+                int r, u;
+                core_place<4>(tid, r, u);
                 const bool there = r < lu.n && u * 8 < cols;
                 copy16(st + W::rows + (u >> 1) * W::kGroup + (u & 1) * 3072 + 2048 + r * 16,
                        there ? a.dy.p + (lu.b + r) * a.dy.ld + lu.h * a.dv + c0 + u * 8 : a.dy.p, there);
@@ -878,7 +871,9 @@ __global__ void __launch_bounds__(256) gdr_grad_tc_kernel(const __grid_constant_
                 const int kh = lu.h / (a.Hv / a.Hk);
 #pragma unroll
                 for (int i = tid; i < 2 * kC * (DKP / 8); i += W::threads) {
-                    const int r = i / (DKP / 8), u = i % (DKP / 8), t = r & 63;
+                    int r, u;
+                    core_place<DKP / 8>(i, r, u);
+                    const int t = r & 63;
                     const Planes& x = r < kC ? a.k : a.q;
                     const bool there = t < lu.n && u * 8 < a.dk;
                     copy16(base + lkq * W::kKQ + stacked_at(r, u), there ? x.p + (lu.b + t) * x.ld + kh * a.dk + u * 8 : x.p, there);
@@ -1002,9 +997,10 @@ __global__ void __launch_bounds__(256) gdr_grad_tc_kernel(const __grid_constant_
         float* const Z = reinterpret_cast<float*>(smem + W::Z);
         {
             float x[32], y[32];
-            tensor::load32(D3 + mine + 32 * half, x);
-            tensor::load32(D4 + mine + 32 * half, y);
-            tensor::loaded();
+            tensor::fetch32(D3 + mine + 32 * half, x);
+            tensor::fetch32(D4 + mine + 32 * half, y);
+            tensor::arrived(x);
+            tensor::arrived(y);
             const float gh = vec[3 * kC + i], gl = vec[4 * kC + i], mul = key ? -vec[kC + i] : a.scale;
             float z[32];
 #pragma unroll
@@ -1051,9 +1047,10 @@ __global__ void __launch_bounds__(256) gdr_grad_tc_kernel(const __grid_constant_
             for (int p = 0; p < HC / 32; ++p) {
                 const int c0 = HC * half + 32 * p;
                 float v[32], t[32];
-                tensor::load32(D1 + mine + c0, v);
-                tensor::load32(D2 + mine + c0, t);
-                tensor::loaded();
+                tensor::fetch32(D1 + mine + c0, v);
+                tensor::fetch32(D2 + mine + c0, t);
+                tensor::arrived(v);
+                tensor::arrived(t);
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     const uint4 x = *reinterpret_cast<const uint4*>(smem + kq * W::kKQ + stacked_at(r, c0 / 8 + q));
@@ -1130,18 +1127,17 @@ __global__ void __launch_bounds__(256) gdr_grad_tc_kernel(const __grid_constant_
         for (int p = 0; p < HC / 32; ++p) {
             const int c0 = HC * half + 32 * p;
             float v[32], t[32];
-            tensor::load32(D1 + mine + c0, v);
-            tensor::load32(D5 + mine + c0, t);
-            tensor::loaded();
+            tensor::fetch32(D1 + mine + c0, v);
+            tensor::fetch32(D5 + mine + c0, t);
+            tensor::arrived(v);
+            tensor::arrived(t);
 #pragma unroll
             for (int c = 0; c < 32; ++c) v[c] = fmaf(f1, v[c], t[c]);
             if (key) {   // whole warps
                 tensor::load32(D2 + mine + c0, t);
-                tensor::loaded();
 #pragma unroll
                 for (int c = 0; c < 32; ++c) v[c] = fmaf(f2, t[c], v[c]);
                 tensor::load32(D6 + mine + c0, t);
-                tensor::loaded();
 #pragma unroll
                 for (int c = 0; c < 32; ++c) v[c] += t[c];
             }

@@ -45,8 +45,9 @@ template <int COLS>
 __device__ __forceinline__ void release(uint32_t d) {
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(d), "n"(COLS) : "memory");
 }
-// 32 columns of this warp's 32 rows (rows 32 (warp % 4) ..): lane l holds row l.
-__device__ __forceinline__ void load32(uint32_t d, float (&v)[32]) {
+// 32 columns of this warp's 32 rows (rows 32 (warp % 4) ..): lane l holds row l. What fetch32 names is there once arrived has
+// named it too.
+__device__ __forceinline__ void fetch32(uint32_t d, float (&v)[32]) {
     uint32_t* r = reinterpret_cast<uint32_t*>(v);
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, "
@@ -57,7 +58,27 @@ __device__ __forceinline__ void load32(uint32_t d, float (&v)[32]) {
           "=r"(r[31])
         : "r"(d));
 }
-__device__ __forceinline__ void loaded() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void arrived(float (&v)[32]) {
+    uint32_t* r = reinterpret_cast<uint32_t*>(v);
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]),
+                   "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+                 :: "memory");
+    asm volatile("" : "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]),
+                      "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+                 :: "memory");
+}
+__device__ __forceinline__ void load32(uint32_t d, float (&v)[32]) {
+    fetch32(d, v);
+    arrived(v);
+}
+// The same as 16 pairs of neighbouring columns.
+__device__ __forceinline__ void load32(uint32_t d, uint64_t (&v)[16]) {
+    float x[32];
+    load32(d, x);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) asm("mov.b64 %0, {%1, %2};" : "=l"(v[i]) : "f"(x[2 * i]), "f"(x[2 * i + 1]));
+}
 
 __device__ __forceinline__ void barrier_init(uint32_t bar, int arrivals) {
     asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(arrivals) : "memory");
