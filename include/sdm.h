@@ -548,8 +548,8 @@ typedef struct {
  *   offsets: as in sdm_glr_forward (ragged sequences, rows of no sequence).
  *   h0 (nullable: zeros) and hT (nullable) float32 [P, v_heads, dk, dv]: the states before and after; hT may be h0; an
  *   empty sequence hands its state on.
- *   states (nullable), sdm_gdr_states_bytes, 16-byte aligned: the state before every SDM_GDR_CHUNK-th row of each sequence and
- *   what every row writes, for the backward, in a form of its own.
+ *   states (nullable), sdm_gdr_states_bytes, 16-byte aligned: the state before every SDM_GDR_CHUNK-th row of each sequence,
+ *   what every row writes and what its block gives without the state, for the backward, in a form of its own.
  *   ws: sdm_gdr_workspace_bytes(shape, 0), 16-byte aligned. It holds nothing from one call to the next.
  * Blocks of 64 rows are solved together on the tensor cores; sums are float32, and float32 values enter the products as sums of
  * two bfloat16 (within 2^-17) beside bfloat16 rows, of three (2^-25) beside float32 rows. A value that is not finite spoils its sequence and head from the start of its block on (as NaN).
@@ -565,7 +565,7 @@ sdm_status sdm_gdr_forward(const sdm_gdr_shape* shape, const void* q, int64_t q_
  * Its backward: the gradients dq, dk [rows, k_heads * dk] (summed over the value heads of a key head), dv [rows, v_heads * dv], dg,
  * dbeta [rows, v_heads] and dh0 (nullable, float32 [P, v_heads, dk, dv]) from dy and dhT (nullable: zeros; the gradient of the states
  * after). q, k, v, g, beta and offsets as the forward had them, states as it saved them; dh0 may be dhT. ws:
- * sdm_gdr_workspace_bytes(shape, 1), 16-byte aligned. Alignments as for the forward. No output overlaps an input.
+ * sdm_gdr_workspace_bytes(shape, 1), 16-byte aligned; it serves the forward too. Alignments as for the forward. No output overlaps an input.
  */
 sdm_status sdm_gdr_backward(const sdm_gdr_shape* shape, const void* q, int64_t q_ld, const void* k, int64_t k_ld,
                             const void* v, int64_t v_ld, const void* g, int64_t g_ld, const void* beta, int64_t beta_ld,

@@ -4,7 +4,6 @@
 // Two kernels. What a block's rows give without the state (T, A T and the decays) is computed for all blocks at once; then
 // every sequence and value head is walked block by block, its state's columns divided among blocks of threads where there are few.
 #include "sdm_gdr.cuh"
-#include "sdm_tensor.cuh"
 
 namespace sdm {
 namespace gdr {
@@ -258,8 +257,8 @@ __global__ void __launch_bounds__(128, XT == 1 ? 4 : 2) gdr_prepare_kernel(const
             // [T; scale A T] in cores of 8 rows: a term's 128 rows x 64
             for (int i = tid; i < 2 * NS * kC * 8; i += 128) {
                 const int r = i & 63, u = i >> 6 & 7, lower = i >> 9 & 1, p = i >> 10;
-                if (u > (r >> 4) * 2 + 1) continue;
-                const uint4 v = *reinterpret_cast<const uint4*>(smem + ((lower ? A : T) - K) + p * kPlane + tile_at<kC>(r, u));
+                uint4 v = make_uint4(0, 0, 0, 0);
+                if (u <= (r >> 4) * 2 + 1) v = *reinterpret_cast<const uint4*>(smem + ((lower ? A : T) - K) + p * kPlane + tile_at<kC>(r, u));
                 *reinterpret_cast<uint4*>(reinterpret_cast<unsigned char*>(tri) + p * 16384 + stacked_at(64 * lower + r, u)) = v;
             }
         } else {
@@ -493,16 +492,16 @@ __global__ void __launch_bounds__(BV * 2) gdr_walk_kernel(const __grid_constant_
 // their sums in tensor memory, their computed operands (S, R, U) as two terms in shared memory, in cores that their own threads
 // write without conflicts. What bounds it is this chain: with 128 columns 2300 cycles of products, then 4 turns of a barrier,
 // loads from tensor memory and the cut into terms. Tiles of K and Q arrive a block ahead, V and T while the state is brought up
-// to date.
+// to date, in boxes of a tensor map and bulk copies.
 template <int DKP, int BV>
-__global__ void __launch_bounds__(BV * 4) gdr_walk_tc_kernel(const __grid_constant__ Args a) {
+__global__ void __launch_bounds__(BV * 4) gdr_walk_tc_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps) {
     using W = WalkTc<DKP, BV>;
     extern __shared__ __align__(1024) unsigned char smem[];
-    __shared__ __align__(16) float vecs[2][kVecs * kC];
-    __shared__ __align__(8) uint64_t bars[3];
+    __shared__ __align__(128) float vecs[2][kVecs * kC];
+    __shared__ __align__(8) uint64_t bars[6];   // the three products', then the copies' (WalkLoads)
     __shared__ uint32_t tmem;
     start_dependent();
-    const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, w = __shfl_sync(kFull, tid >> 5, 0), lane = tid & 31;
     const int slices = (a.dv + BV - 1) / BV;
     const int rank = blockIdx.x / (a.Hv * slices), rest = blockIdx.x - rank * a.Hv * slices;
     const int h = rest / slices, c0 = (rest - h * slices) * BV;
@@ -513,23 +512,20 @@ __global__ void __launch_bounds__(BV * 4) gdr_walk_tc_kernel(const __grid_consta
     const uint32_t base = smem_of(smem), bar = smem_of(bars);
     const int cols = min(BV, a.dv - c0), nb = (a.dv + 15) / 16 * 2;   // units of 8 value columns that are saved
 
-    WalkCopies<DKP, BV> copies(a, a.v, base, smem_of(vecs), b, id0, 0, kh, h, c0, cols, tid);
+    const WalkLoads<DKP, BV> loads{a, maps, a.v, b, len, id0, base, smem_of(vecs), smem_of(bars) + 24, h, kh, c0, cols, tid, w};
     auto load_kq = [&](int64_t j) {
-        if (j < blocks) {
-            copies.kq(static_cast<int>(j & 1), static_cast<int>(min(len - j * kC, int64_t(kC))), tid);
-            copies.go_kq(1);
-        }
-        copies_commit();
+        if (j < blocks) loads.kq(j);
     };
     auto load_vt = [&](int64_t j) {
-        if (j < blocks) {
-            copies.vt(static_cast<int>(min(len - j * kC, int64_t(kC))), tid);
-            copies.go_vt(1);
-        }
-        copies_commit();
+        if (j < blocks) loads.vt(j);
     };
-    // what of T lies above the diagonal stays zero
-    for (int i = tid; i < W::kT / 16; i += W::threads) *reinterpret_cast<uint4*>(smem + W::T + i * 16) = make_uint4(0, 0, 0, 0);
+    // what no copy reaches is a number
+    for (int i = tid; i < W::bytes / 16; i += W::threads) *reinterpret_cast<uint4*>(smem + i * 16) = make_uint4(0, 0, 0, 0);
+    if (tid == 32) {
+        for (int x = 0; x < 6; ++x) tensor::barrier_init(bar + 8 * x, 1);
+        tensor::barrier_fence();
+    }
+    async_fence();
     __syncthreads();
     load_kq(0);
     load_vt(0);
@@ -565,51 +561,53 @@ __global__ void __launch_bounds__(BV * 4) gdr_walk_tc_kernel(const __grid_consta
     };
     put_state(0);
     if (w == 0) tensor::allocate<W::cols>(smem_of(&tmem));
-    if (tid == 0) {
-        for (int x = 0; x < 3; ++x) tensor::barrier_init(bar + 8 * x, 1);
-        tensor::barrier_fence();
-    }
     tensor::fence_before();
     __syncthreads();
     tensor::fence_after();
-    const uint32_t Da = tmem, Db = tmem + BV, Dc = tmem + 2 * BV;
+    const uint32_t Da = tmem, Db = tmem + W::N, Dc = Da;
     const uint32_t mine = (static_cast<uint32_t>(w & 3) << 21) + 32 * part;
-    // the products' operands: per 16 summands 4096 bytes of [K; Q] and T along their rows, 256 of the others and along tokens
-    const uint64_t KQd = tensor::operand(base + W::KQ, 2048, 128), KTd = tensor::operand(base + W::KQ, 128, 2048);
+    // the products' operands. Per 16 summands: 32 bytes of [K; Q]'s rows (a tile for 64), 4096 of T's; 2048 along swizzled tokens, 256 of
+    // the others
+    const uint64_t KQd = tensor::swizzled(base + W::KQ, 0), KTd = tensor::swizzled(base + W::KQ, 16384);
     const uint64_t Sd = tensor::operand(base + W::S, 128, DKP * 16), Td = tensor::operand(base + W::T, 2048, 128);
     const uint64_t Rd = tensor::operand(base + W::R, 128, 1024);
-    uint32_t phase = 0;
+    uint32_t phase = 0, full = 0;
     bool bad = false;
     for (int64_t j = 0; j < blocks; ++j) {
         const uint64_t kq = static_cast<uint64_t>((j & 1) * W::kKQ) >> 4;   // the stage's distance, in a descriptor's units
         const float* const vec = vecs[j & 1];
-        copies_wait<1>();
+        bad |= !tensor::barrier_wait(bar + 24 + 8 * (j & 1), full >> (j & 1) & 1);
+        full ^= 1u << (j & 1);
+        copies_wait<0>();
         async_fence();
         if (__syncthreads_or(bad)) break;
-        if (tid == 0) {
+        if (w == 0 && tensor::elect()) {
             tensor::fence_after();
 #pragma unroll
             for (int ks = 0; ks < DKP / 16; ++ks)
 #pragma unroll
-                for (int t = 0; t < 2; ++t)
-                    tensor::mma(Da, KQd + kq + ks * 256, Sd + (t * W::kS + ks * 256) / 16, tensor::shape(128, BV, false, true), ks + t > 0);
+                for (int t = 0; t < W::terms; ++t)
+                    tensor::mma(Da, KQd + kq + (ks >> 2) * 1024 + (ks & 3) * 2, Sd + (t * W::kS + ks * 256) / 16, tensor::shape(128, W::N, false, true), ks + t > 0);
             tensor::commit(bar);
         }
         load_kq(j + 1);
         bad |= !tensor::barrier_wait(bar, phase);
-        copies_wait<1>();
-        async_fence();
-        __syncthreads();
+        bad |= !tensor::barrier_wait(bar + 40, phase);
+        if (!loads.boxed(j)) {   // V came by the threads' own copies
+            copies_wait<0>();
+            async_fence();
+            __syncthreads();
+        }
         tensor::fence_after();
         uint64_t x[16];
-        tensor::load32(Da + mine, x);
+        W::sums(Da + mine, x);
         const float eg = vec[i];
         if (key) {   // beta R
             const float bt = vec[kC + i];
             const uint64_t f = pack2(-bt * eg, -bt * eg), bt2 = pack2(bt, bt);
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                const uint4 v = *reinterpret_cast<const uint4*>(smem + W::V + rows_at(i, 4 * part + q));
+                const uint4 v = *reinterpret_cast<const uint4*>(smem + W::V + (part >> 1) * 8192 + swizzled_at(i, loads.first() + (part & 1) * 4 + q));
                 const uint32_t vw[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
                 for (int e = 0; e < 4; ++e) x[4 * q + e] = fma2(f, x[4 * q + e], mul2(bt2, widen2(vw[e])));
@@ -619,19 +617,21 @@ __global__ void __launch_bounds__(BV * 4) gdr_walk_tc_kernel(const __grid_consta
         async_fence();
         tensor::fence_before();
         __syncthreads();
-        if (tid == 0) {
+        if (w == 0 && tensor::elect()) {
             tensor::fence_after();
 #pragma unroll
-            for (int t = 0; t < 3; ++t)   // T's first term with both of R's, its second with the first
+            for (int t = 0; t < W::terms; ++t)   // T's first term with both of R's, its second with the first
 #pragma unroll
                 for (int ks = 0; ks < 4; ++ks)
-                    tensor::mma(Db, Td + (t >> 1) * 1024 + ks * 256, Rd + ((t & 1) * W::kR + ks * 256) / 16, tensor::shape(128, BV, false, true), t + ks > 0);
+                    tensor::mma(Db, Td + ks * 256, Rd + (t * W::kR + ks * 256) / 16, tensor::shape(128, W::N, false, true), t + ks > 0);
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks) tensor::mma(Db, Td + 1024 + ks * 256, Rd + ks * 16, tensor::shape(128, BV, false, true), true);
             tensor::commit(bar + 8);
         }
         bad |= !tensor::barrier_wait(bar + 8, phase);
         tensor::fence_after();
         uint64_t u[16];
-        tensor::load32(Db + mine, u);
+        W::sums(Db + mine, u);
         if (key) {
             const float c = vec[2 * kC + i];
 #pragma unroll
@@ -641,13 +641,13 @@ __global__ void __launch_bounds__(BV * 4) gdr_walk_tc_kernel(const __grid_consta
         async_fence();
         tensor::fence_before();
         __syncthreads();
-        if (tid == 0) {
+        if (w == 0 && tensor::elect()) {
             tensor::fence_after();
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks)
 #pragma unroll
-                for (int t = 0; t < 2; ++t)
-                    tensor::mma(Dc, KTd + kq + ks * 16, Rd + (t * W::kR + ks * 256) / 16, tensor::shape(128, BV, true, true), ks + t > 0);
+                for (int t = 0; t < W::terms; ++t)
+                    tensor::mma(Dc, KTd + kq + ks * 128, Rd + (t * W::kR + ks * 256) / 16, tensor::shape(128, W::N, true, true), ks + t > 0);
             tensor::commit(bar + 16);
         }
         load_vt(j + 1);
@@ -687,7 +687,7 @@ __global__ void __launch_bounds__(BV * 4) gdr_walk_tc_kernel(const __grid_consta
         bad |= !tensor::barrier_wait(bar + 16, phase);
         phase ^= 1;
         tensor::fence_after();
-        tensor::load32(Dc + mine, u);
+        W::sums(Dc + mine, u);
 #pragma unroll
         for (int e = 0; e < 16; ++e) S[e] = fma2(pack2(last, last), S[e], u[e]);
         put_state(j + 1);
@@ -852,7 +852,10 @@ cudaError_t walk_tc(const Args& a, cudaStream_t cs) {
     const cudaError_t e = big_smem(k, W::bytes);
     if (e != cudaSuccess) return e;
     const int64_t grid = static_cast<int64_t>(a.P) * a.Hv * ((a.dv + BV - 1) / BV);
-    return launch_dependent(k, dim3(static_cast<unsigned>(grid)), dim3(W::threads), W::bytes, cs, a);
+    Maps m;
+    const cudaError_t f = make_maps(&m, a, a.v, BV);
+    if (f != cudaSuccess) return f;
+    return launch_dependent(k, dim3(static_cast<unsigned>(grid)), dim3(W::threads), W::bytes, cs, a, m);
 }
 
 template <int DKP>
@@ -878,6 +881,12 @@ sdm_status check_shape(const sdm_gdr_shape* s) {
     return SDM_OK;
 }
 
+// Bytes of a head's block of rows
+int64_t tri_bytes(const sdm_gdr_shape* s) { return 2 * terms(s) * int64_t(kC * kC) * 2; }
+constexpr int64_t kVecBytes = kVecs * kC * 4;
+int64_t state_bytes(const sdm_gdr_shape* s) { return (s->dv + 15) / 16 * 16 * int64_t(padded(s->dk)) * 2 * terms(s); }
+int64_t write_bytes(const sdm_gdr_shape* s) { return (s->dv + 15) / 16 * 16 * int64_t(kC) * 2 * terms(s); }
+
 Layout layout(const sdm_gdr_shape* s, bool backward) {
     Layout l;
     memset(&l, 0, sizeof(l));
@@ -889,8 +898,10 @@ Layout layout(const sdm_gdr_shape* s, bool backward) {
         at += up(bytes);
         return here;
     };
-    l.tri = take(heads * 2 * terms(s) * kC * kC * 2);
-    l.vec = take(heads * kVecs * kC * 4);
+    if (!backward) {   // from the end on they are read where the forward saved them
+        l.tri = take(heads * tri_bytes(s));
+        l.vec = take(heads * kVecBytes);
+    }
     if (f32) {
         l.q = take(s->rows * s->k_heads * s->dk * 6);
         l.k = take(s->rows * s->k_heads * s->dk * 6);
@@ -898,18 +909,23 @@ Layout layout(const sdm_gdr_shape* s, bool backward) {
     }
     if (backward) {
         if (f32) l.dy = take(s->rows * s->v_heads * s->dv * 6);
-        const int64_t dvp = (s->dv + 15) / 16 * 16;
-        l.dstates = take(heads * dvp * padded(s->dk) * 2 * terms(s));
-        l.du = take(heads * kC * dvp * 2 * terms(s));
+        l.dstates = take(heads * state_bytes(s));
+        l.du = take(heads * write_bytes(s));
         if (s->v_heads != s->k_heads) l.part = take(2 * s->rows * s->v_heads * s->dk * 4);
     }
-    l.bytes = std::max<int64_t>(at, 256);
+    l.bytes = std::max<int64_t>(at, backward ? layout(s, false).bytes : 256);   // a forward can use it too
     return l;
 }
 
 void set_states(const sdm_gdr_shape* s, void* states, Args* a) {
     a->states = static_cast<__nv_bfloat16*>(states);
-    if (states != nullptr) a->writes = a->states + blocks_of(s) * s->v_heads * ((s->dv + 15) / 16 * 16) * padded(s->dk) * terms(s);
+    if (states == nullptr) return;
+    const int64_t heads = blocks_of(s) * s->v_heads;
+    unsigned char* at = static_cast<unsigned char*>(states) + heads * state_bytes(s);
+    a->writes = reinterpret_cast<__nv_bfloat16*>(at);
+    at += heads * write_bytes(s);
+    a->tri = reinterpret_cast<__nv_bfloat16*>(at);
+    a->vec = reinterpret_cast<float*>(at + heads * tri_bytes(s));
 }
 
 cudaError_t launch_split(const void* x, int64_t ld, int64_t rows, int cols, __nv_bfloat16* out, cudaStream_t cs) {
@@ -946,6 +962,30 @@ sdm_status check_inputs(const sdm_gdr_shape* s, const void* q, int64_t q_ld, con
     return SDM_OK;
 }
 
+cudaError_t make_maps(Maps* m, const Args& a, const Planes& v, int bv) {
+    static const auto encode = [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &found) != cudaSuccess || found != cudaDriverEntryPointSuccess)
+            f = nullptr;
+        return reinterpret_cast<decltype(&cuTensorMapEncodeTiled)>(f);
+    }();
+    if (encode == nullptr) return cudaErrorNotSupported;
+    memset(m, 0, sizeof(*m));
+    constexpr int64_t far = int64_t(1) << 38;   // elements between rows
+    m->boxes = a.dk == padded(a.dk) && a.dv % (bv < 64 ? 64 : bv) == 0 && a.rows >= kC && a.rows < (int64_t(1) << 31) && a.k.ld >= a.Hk * a.dk &&
+               a.q.ld >= a.Hk * a.dk && v.ld >= a.Hv * a.dv && a.k.ld < far && a.q.ld < far && v.ld < far;
+    if (!m->boxes) return cudaSuccess;
+    auto map = [&](CUtensorMap* to, const Planes& x, int cols) {
+        const cuuint64_t size[2] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(a.rows)}, stride[1] = {static_cast<cuuint64_t>(x.ld) * 2};
+        const cuuint32_t box[2] = {64, 64}, step[2] = {1, 1};
+        return encode(to, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<__nv_bfloat16*>(x.p), size, stride, box, step,
+                      CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                      CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    };
+    return map(&m->k, a.k, a.Hk * a.dk) && map(&m->q, a.q, a.Hk * a.dk) && map(&m->v, v, a.Hv * a.dv) ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 cudaError_t launch_planes(const sdm_gdr_shape* s, const void* q, int64_t q_ld, const void* k, int64_t k_ld, const void* v, int64_t v_ld,
                           void* ws, bool backward, Args* a, cudaStream_t cs) {
     const Layout l = layout(s, backward);
@@ -980,7 +1020,7 @@ using namespace sdm::gdr;
 
 extern "C" size_t sdm_gdr_states_bytes(const sdm_gdr_shape* shape) {
     if (check_shape(shape) != SDM_OK) return 0;
-    return static_cast<size_t>(blocks_of(shape)) * shape->v_heads * ((shape->dv + 15) / 16 * 16) * (padded(shape->dk) + kC) * 2 * terms(shape);
+    return static_cast<size_t>(blocks_of(shape) * shape->v_heads * (state_bytes(shape) + write_bytes(shape) + tri_bytes(shape) + kVecBytes));
 }
 
 extern "C" size_t sdm_gdr_workspace_bytes(const sdm_gdr_shape* shape, int32_t backward) {

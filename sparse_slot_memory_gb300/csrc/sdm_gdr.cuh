@@ -15,6 +15,7 @@
 // terms once, ahead of everything, and so are what is computed from them.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -23,6 +24,7 @@
 #include <type_traits>
 
 #include "sdm_operators.cuh"
+#include "sdm_tensor.cuh"
 
 namespace sdm {
 namespace gdr {
@@ -61,9 +63,9 @@ struct Args {
     void* dv_out;
     void* dg;
     void* dbeta;
-    __nv_bfloat16* tri;       // workspace: [blocks][Hv]: of bfloat16 rows two terms of [T; scale A T], [128][64] in cores of 8 rows; of
+    __nv_bfloat16* tri;       // behind the writes, or workspace: [blocks][Hv]: of bfloat16 rows two terms of [T; scale A T], [128][64] in cores of 8 rows; of
                               // float32 rows six planes [64][64], T's terms and A's
-    float* vec;               // workspace: [blocks][Hv][kVecs][64]: e^gam, beta, e^(gam_last - gam), gam as a sum of two floats
+    float* vec;               // as `tri`: [blocks][Hv][kVecs][64]: e^gam, beta, e^(gam_last - gam), gam as a sum of two floats
     __nv_bfloat16* dstates;   // workspace of the backward: the gradients of the states behind the blocks, as `states`
     __nv_bfloat16* du;        // workspace of the backward: the gradients of the writes (dv before beta), as `writes`
     float* part;              // workspace of the backward: gradients of shared queries and keys
@@ -72,6 +74,12 @@ struct Args {
     int64_t g_ld, b_ld, y_ld, dq_ld, dk_ld, dv_ld, dg_ld, db_ld;
     int P, Hk, Hv, dk, dv, g_bf16;
     float scale;
+};
+
+// Tensor maps of bfloat16 rows [rows][heads x d] for boxes of 64 rows x 64 columns.
+struct Maps {
+    CUtensorMap k, q, v;   // v: V of the walk, dY from the end
+    int boxes;             // whether they serve: heads of 64 or 128 columns, rows apart from one another
 };
 
 // The rows [b, b + n) of sequence p. Offsets that are not ascending within [0, rows] are cut to it and reported.
@@ -188,16 +196,11 @@ __device__ __forceinline__ void load_tri(uint32_t dst, const __nv_bfloat16* src,
     }
 }
 
-// A tile's stacked halves, [128 rows], in cores of 8 rows (sdm_tensor.cuh)
+// Rows as boxes bring them: 128 bytes, a unit of 16 swizzled by the row
+__device__ __forceinline__ uint32_t swizzled_at(int r, int u) { return static_cast<uint32_t>(r * 128 + ((u ^ (r & 7)) << 4)); }
+// [T; scale A T]: units of 8 columns, of each 128 rows of 16 bytes
 __device__ __forceinline__ uint32_t stacked_at(int r, int u) { return static_cast<uint32_t>(u * 2048 + (r >> 3) * 128 + (r & 7) * 16); }
-// Copy number i of a tile of rows of U units into such cores: eight rows of a unit lie in 128 contiguous bytes, so a warp takes eight
-// rows of four units (64 bytes of a row) and meets no bank twice.
-template <int U>
-__device__ __forceinline__ void core_place(int i, int& r, int& u) {
-    const int x = i >> 5;
-    r = (i & 7) + x / (U / 4) * 8;
-    u = (i >> 3 & 3) + x % (U / 4) * 4;
-}
+
 // ---- fragments ------------------------------------------------------------------------------------------
 // (loads of fragments keep their place among barriers and stores by being volatile; the products are free to move)
 __device__ __forceinline__ void ldsm4(uint32_t (&f)[4], uint32_t a) {
@@ -318,15 +321,34 @@ __device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.w
 __device__ __forceinline__ void bulk_wait() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 __device__ __forceinline__ void async_fence() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
-// ---- the walks of bfloat16 rows, forwards and from the end: what they keep in shared memory ----------------------------------
+// ---- the walks of bfloat16 rows, forwards and from the end ---------------------------------------------------------------------
 template <int DKP, int BV>
 struct WalkTc {
-    static constexpr int kKQ = DKP / 8 * 2048, kV = kC * BV * 2, kT = 2 * 16384, kS = BV * DKP * 2, kR = kC * BV * 2;
-    // [K; Q] twice, V (or dY), [T; scale A T], the state's terms, R's and U's (or their gradients')
+    static constexpr int kKQ = 2 * kC * DKP * 2, kV = kC * (BV < 64 ? 64 : BV) * 2, kT = 2 * 16384, kS = BV * DKP * 2, kR = kC * BV * 2;
+    // [K; Q] twice (a tile of 128 rows for 64 columns), V or dY (64 rows for 64 columns), [T; scale A T], the state's terms, R's and
+    // U's (or their gradients')
     static constexpr int KQ = 0, V = 2 * kKQ, T = V + kV, S = T + kT, R = S + 2 * kS, end = R + 2 * kR;
-    // a core column of K^T and T^T beyond their own 64 is read (and not used): up to 16 columns from the tile's start
-    static constexpr int bytes = end > 16 * 2048 + kKQ ? end : 16 * 2048 + kKQ;
-    static constexpr int threads = BV * 4, cols = BV <= 32 ? 128 : BV == 64 ? 256 : 512;
+    // K^T and T^T are read as operands of 128 columns from their tiles' starts (what lies beyond their own is not used)
+    static constexpr int bytes = end > kKQ + 32768 ? end : kKQ + 32768;
+    static constexpr int threads = BV * 4;
+    // Two terms of a computed operand lie side by side, so one product takes both, with sums side by side, where that is faster:
+    // 42 cycles for 2 x 32 columns and 65 for 2 x 64, not 2 x 34 and 2 x 42; 130 for 2 x 128 columns as for 2 products.
+    static constexpr int terms = BV <= 64 ? 1 : 2, N = BV <= 64 ? 2 * BV : BV;   // products for two terms, and the columns of each
+    static constexpr int cols = 2 * N;
+    // 32 columns of a row of the sums
+    __device__ static __forceinline__ void sums(uint32_t d, uint64_t (&v)[16]) {
+        if constexpr (terms == 1) {
+            float x[32], y[32];
+            tensor::fetch32(d, x);
+            tensor::fetch32(d + BV, y);
+            tensor::arrived(x);
+            tensor::arrived(y);
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[i] = add2(pack2(x[2 * i], x[2 * i + 1]), pack2(y[2 * i], y[2 * i + 1]));
+        } else {
+            tensor::load32(d, v);
+        }
+    }
 };
 
 // Two float32 as two terms of bfloat16, the rests subtracted together
@@ -335,7 +357,7 @@ __device__ __forceinline__ void terms2(uint64_t v, uint32_t& hi, uint32_t& lo) {
     unpack2(v, x, y);
     hi = round2(x, y);
     float s, t;
-    unpack2(add2(v, pack2(__uint_as_float((hi << 16) ^ 0x80000000u), __uint_as_float((hi & 0xFFFF0000u) ^ 0x80000000u))), s, t);
+    unpack2(fma2(pack2(__uint_as_float(hi << 16), __uint_as_float(hi & 0xFFFF0000u)), pack2(-1.f, -1.f), v), s, t);
     lo = round2(s, t);
 }
 // 32 values (16 pairs) as two terms: units of 8 columns, 16 bytes each, `pitch` bytes apart
@@ -352,70 +374,68 @@ __device__ __forceinline__ void put_terms(unsigned char* hi, unsigned char* lo, 
 // Two bfloat16 as a pair of float32
 __device__ __forceinline__ uint64_t widen2(uint32_t w) { return pack2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u)); }
 
-// What a thread copies of each block's queries, keys and rows of values: its places stay the same, its addresses go on by 64 rows
+// The copies of a walk's blocks. Whole blocks arrive by themselves (one thread names them);
+// a sequence's last rows, and heads of other sizes, are copied by all threads, with zeros where there is nothing.
 template <int DKP, int BV>
-struct WalkCopies {
+struct WalkLoads {
     using W = WalkTc<DKP, BV>;
-    static constexpr int kRows = W::threads / (DKP / 8), kSlots = kC / kRows;   // rows of a sweep over K (or Q), sweeps
-    static_assert(kC % kRows == 0 && W::threads / (BV / 8) == 32, "whole sweeps");
-    const __nv_bfloat16 *k, *q, *v, *tri, *none;
-    const float* vec;
-    int64_t k_ld, q_ld, v_ld, heads;
-    uint32_t kq_at, v_at, t_at, vec_at;
-    int r, vr;
-    bool on, v_on;
-    // rows: V or dY; block j's first row is b + 64 j
-    __device__ __forceinline__ WalkCopies(const Args& a, const Planes& rows, uint32_t base, uint32_t vecs, int64_t b, int64_t id0, int64_t j, int kh,
-                                          int h, int c0, int cols, int tid) {
-        int u, vu;
-        core_place<DKP / 8>(tid, r, u);
-        core_place<BV / 8>(tid, vr, vu);
-        on = u * 8 < a.dk;
-        v_on = vu * 8 < cols;
-        k_ld = a.k.ld;
-        q_ld = a.q.ld;
-        v_ld = rows.ld;
-        none = a.k.p;
-        k = a.k.p + (b + j * kC + r) * k_ld + kh * a.dk + u * 8;
-        q = a.q.p + (b + j * kC + r) * q_ld + kh * a.dk + u * 8;
-        v = rows.p + (b + j * kC + vr) * v_ld + h * a.dv + c0 + vu * 8;
-        kq_at = base + W::KQ + stacked_at(r, u);
-        v_at = base + W::V + rows_at(vr, vu);
-        heads = a.Hv;
-        tri = a.tri + ((id0 + j) * heads + h) * 4 * int64_t(kC * kC) + tid * 8;
-        t_at = base + W::T + tid * 16;
-        vec = a.vec + ((id0 + j) * heads + h) * kVecs * kC + tid * 4;
-        vec_at = vecs + tid * 16;
-    }
-    // [K; Q] and the decays of a block of n rows, to stage `s`
-    __device__ __forceinline__ void kq(int s, int n, int tid) {
-        const uint32_t to = kq_at + s * W::kKQ;
+    const Args& a;
+    const Maps& m;
+    const Planes& v;
+    int64_t b, len, id0;
+    uint32_t base, vecs, bar;   // bar: of [K; Q]'s two stages, and of V and T
+    int h, kh, c0, cols, tid, warp;
+    __device__ __forceinline__ int rows_of(int64_t j) const { return static_cast<int>(min(len - j * kC, int64_t(kC))); }
+    __device__ __forceinline__ bool boxed(int64_t j) const { return m.boxes && rows_of(j) == kC; }
+    __device__ __forceinline__ int first() const { return BV < 64 ? c0 >> 3 & 4 : 0; }   // the block's first unit of its box
+    __device__ __forceinline__ void kq(int64_t j) const {
+        const int s = static_cast<int>(j & 1);
+        const uint32_t to = base + W::KQ + s * W::kKQ, full = bar + 8 * s;
+        const bool box = boxed(j);
+        if (warp == 1 && tensor::elect()) {
+            tensor::barrier_expect(full, kVecs * kC * 4 + (box ? W::kKQ : 0));
+            if (box) {
+                const int row = static_cast<int>(b + j * kC);
 #pragma unroll
-        for (int x = 0; x < kSlots; ++x) {
-            const bool there = on && r + x * kRows < n;
-            copy16(to + x * kRows * 16, there ? k + x * kRows * k_ld : none, there);
-            copy16(to + 1024 + x * kRows * 16, there ? q + x * kRows * q_ld : none, there);
+                for (int x = 0; x < DKP / 64; ++x) {
+                    tensor::copy_box(to + x * 16384, &m.k, kh * DKP + x * 64, row, full);
+                    tensor::copy_box(to + x * 16384 + 8192, &m.q, kh * DKP + x * 64, row, full);
+                }
+            }
+            tensor::copy_bulk(vecs + s * (kVecs * kC * 4), a.vec + ((id0 + j) * a.Hv + h) * kVecs * kC, kVecs * kC * 4, full);
         }
-        if (tid < kVecs * kC / 4) copy16(vec_at + s * (kVecs * kC * 4), vec, true);
-    }
-    __device__ __forceinline__ void vt(int n, int tid) {
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-            const bool there = v_on && vr + 32 * x < n;
-            copy16(v_at + x * 32 * 16, there ? v + x * 32 * v_ld : none, there);
+        if (!box) {
+            const int n = rows_of(j);
+            for (int i = tid; i < 2 * kC * (DKP / 8); i += W::threads) {
+                const int r = i / (DKP / 8), u = i % (DKP / 8), t = r & 63;
+                const Planes x = r < kC ? a.k : a.q;
+                const bool there = t < n && u * 8 < a.dk;
+                copy16(to + (u >> 3) * 16384 + swizzled_at(r, u & 7), there ? x.p + (b + j * kC + t) * x.ld + kh * a.dk + u * 8 : x.p, there);
+            }
+            copies_commit();
         }
+    }
+    __device__ __forceinline__ void vt(int64_t j) const {
+        const uint32_t full = bar + 16;
+        const bool box = boxed(j);
+        if (warp == 1 && tensor::elect()) {
+            tensor::barrier_expect(full, W::kT + (box ? W::kV : 0));
+            tensor::copy_bulk(base + W::T, a.tri + ((id0 + j) * a.Hv + h) * (W::kT / 2), W::kT, full);
+            if (box) {
 #pragma unroll
-        for (int x = 0; x < 2048 / W::threads; ++x)
-            if ((x * (W::threads / 128) + (tid >> 7) & 7) <= (tid >> 4 & 3) * 2 + 1) copy16(t_at + x * W::threads * 16, tri + x * W::threads * 8, true);
-    }
-    __device__ __forceinline__ void go_kq(int blocks) {
-        k += blocks * kC * k_ld;
-        q += blocks * kC * q_ld;
-        vec += blocks * heads * (kVecs * kC);
-    }
-    __device__ __forceinline__ void go_vt(int blocks) {
-        v += blocks * kC * v_ld;
-        tri += blocks * heads * (4 * kC * kC);
+                for (int x = 0; x < W::kV / 8192; ++x)
+                    tensor::copy_box(base + W::V + x * 8192, &m.v, h * a.dv + (c0 & ~63) + x * 64, static_cast<int>(b + j * kC), full);
+            }
+        }
+        if (!box) {
+            const int n = rows_of(j);
+            for (int i = tid; i < kC * (BV / 8); i += W::threads) {
+                const int r = i / (BV / 8), u = i % (BV / 8);
+                const bool there = r < n && u * 8 < cols;
+                copy16(base + W::V + (u >> 3) * 8192 + swizzled_at(r, first() + (u & 7)), there ? v.p + (b + j * kC + r) * v.ld + h * a.dv + c0 + u * 8 : v.p, there);
+            }
+            copies_commit();
+        }
     }
 };
 
@@ -423,7 +443,7 @@ struct WalkCopies {
 inline int padded(int d) { return d <= 64 ? 64 : 128; }
 inline int64_t blocks_of(const sdm_gdr_shape* s) { return s->rows / kC + s->P; }
 
-// Columns of a block of a walk: fewer while the grid leaves SMs idle.
+// Value columns of a block of a walk of bfloat16 rows: fewer while the grid leaves SMs idle.
 inline int columns(const Args& a) {
     int bv = a.dv <= 32 ? 32 : a.dv <= 64 ? 64 : 128;
     while (bv > 32 && static_cast<int64_t>(a.P) * a.Hv * ((a.dv + bv - 1) / bv) * 2 <= 152) bv /= 2;
@@ -443,7 +463,7 @@ struct Layout {
 inline int terms(const sdm_gdr_shape* s) { return s->x_dtype == SDM_F32 ? 3 : 2; }   // of what is computed
 sdm_status check_shape(const sdm_gdr_shape* s);
 Layout layout(const sdm_gdr_shape* s, bool backward);
-// The saved states and writes: the parts of one array
+// The saved states, writes, triangles and gates: the parts of one array
 void set_states(const sdm_gdr_shape* s, void* states, Args* a);
 // The checks of what both directions take, and the arguments that follow from it
 sdm_status check_inputs(const sdm_gdr_shape* s, const void* q, int64_t q_ld, const void* k, int64_t k_ld, const void* v, int64_t v_ld,
@@ -454,6 +474,8 @@ cudaError_t launch_split(const void* x, int64_t ld, int64_t rows, int cols, __nv
 cudaError_t launch_planes(const sdm_gdr_shape* s, const void* q, int64_t q_ld, const void* k, int64_t k_ld, const void* v, int64_t v_ld,
                           void* ws, bool backward, Args* a, cudaStream_t cs);
 cudaError_t launch_prepare(const Args& a, const sdm_gdr_shape* s, cudaStream_t cs);
+// The maps of a walk over BV value columns a block
+cudaError_t make_maps(Maps* m, const Args& a, const Planes& v, int bv);
 
 }  // namespace gdr
 }  // namespace sdm

@@ -12,11 +12,9 @@
 //   dg_t = sum_{j < t <= i} (N o A - M o G)_ij + sum_{i >= t} a_i + sum_{j < t} e_j + e^gam_last <dS', S>,
 //   a_i = e^gam_i (scale q_i . (S dY_i) - dV_i . (S^T k_i)),   e_j = e^(gam_last - gam_j) u_j . (dS'^T k_j).
 //
-// Three kernels: sdm_gdr.cu's of what needs no state, a walk from each sequence's end that carries dS as the forward's
-// carries S (a warp 16 value columns, transposed, nothing leaves its registers) and writes dV, W and every block's dS'; and one
-// for all blocks at once that has the rest, from the states and the writes that the forward saved.
+// Two kernels: a walk from each sequence's end that carries dS as the forward's carries S and writes dV, W and every block's dS';
+// and one for all blocks at once that has the rest, from what the forward saved: the states, the writes, T, A T and the decays.
 #include "sdm_gdr.cuh"
-#include "sdm_tensor.cuh"
 
 namespace sdm {
 namespace gdr {
@@ -235,15 +233,15 @@ __global__ void __launch_bounds__(BV * 2) gdr_back_kernel(const __grid_constant_
 //   K dS'  ->  x = e^(gam_last - gam) o K dS'  ->  W = T^T x + (scale A T)^T dY  ->  dS = e^gam_last dS' + Q^T (scale e^gam o dY) - K^T (e^gam o beta o W).
 // What dY gives by itself is multiplied beside the chain; its scaled rows take the place of the state's terms while those are not needed.
 template <int DKP, int BV>
-__global__ void __launch_bounds__(BV * 4) gdr_back_tc_kernel(const __grid_constant__ Args a) {
+__global__ void __launch_bounds__(BV * 4) gdr_back_tc_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps) {
     using W = WalkTc<DKP, BV>;
     static_assert(W::kR <= W::kS, "dY's terms lie over the state's");
     extern __shared__ __align__(1024) unsigned char smem[];
-    __shared__ __align__(16) float vecs[2][kVecs * kC];
-    __shared__ __align__(8) uint64_t bars[3];
+    __shared__ __align__(128) float vecs[2][kVecs * kC];
+    __shared__ __align__(8) uint64_t bars[6];   // the three products', then the copies' (WalkLoads)
     __shared__ uint32_t tmem;
     start_dependent();
-    const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, w = __shfl_sync(kFull, tid >> 5, 0), lane = tid & 31;
     const int slices = (a.dv + BV - 1) / BV;
     const int rank = blockIdx.x / (a.Hv * slices), rest = blockIdx.x - rank * a.Hv * slices;
     const int h = rest / slices, c0 = (rest - h * slices) * BV;
@@ -254,22 +252,20 @@ __global__ void __launch_bounds__(BV * 4) gdr_back_tc_kernel(const __grid_consta
     const uint32_t base = smem_of(smem), bar = smem_of(bars);
     const int cols = min(BV, a.dv - c0), nb = (a.dv + 15) / 16 * 2;
 
-    WalkCopies<DKP, BV> copies(a, a.dy, base, smem_of(vecs), b, id0, blocks - 1, kh, h, c0, cols, tid);
+    const WalkLoads<DKP, BV> loads{a, maps, a.dy, b, len, id0, base, smem_of(vecs), smem_of(bars) + 24, h, kh, c0, cols, tid, w};
     auto load_kq = [&](int64_t j) {
-        if (j >= 0) {
-            copies.kq(static_cast<int>(j & 1), static_cast<int>(min(len - j * kC, int64_t(kC))), tid);
-            copies.go_kq(-1);
-        }
-        copies_commit();
+        if (j >= 0) loads.kq(j);
     };
     auto load_yt = [&](int64_t j) {
-        if (j >= 0) {
-            copies.vt(static_cast<int>(min(len - j * kC, int64_t(kC))), tid);
-            copies.go_vt(-1);
-        }
-        copies_commit();
+        if (j >= 0) loads.vt(j);
     };
-    for (int i = tid; i < W::kT / 16; i += W::threads) *reinterpret_cast<uint4*>(smem + W::T + i * 16) = make_uint4(0, 0, 0, 0);
+    // what no copy reaches is a number
+    for (int i = tid; i < W::bytes / 16; i += W::threads) *reinterpret_cast<uint4*>(smem + i * 16) = make_uint4(0, 0, 0, 0);
+    if (tid == 32) {
+        for (int x = 0; x < 6; ++x) tensor::barrier_init(bar + 8 * x, 1);
+        tensor::barrier_fence();
+    }
+    async_fence();
     __syncthreads();
     load_kq(blocks - 1);
     load_yt(blocks - 1);
@@ -306,53 +302,54 @@ __global__ void __launch_bounds__(BV * 4) gdr_back_tc_kernel(const __grid_consta
     };
     put_state(blocks - 1);
     if (w == 0) tensor::allocate<W::cols>(smem_of(&tmem));
-    if (tid == 0) {
-        for (int x = 0; x < 3; ++x) tensor::barrier_init(bar + 8 * x, 1);
-        tensor::barrier_fence();
-    }
     tensor::fence_before();
     __syncthreads();
     tensor::fence_after();
-    const uint32_t Da = tmem, Db = tmem + BV, Dc = tmem + 2 * BV;
+    const uint32_t Da = tmem, Db = tmem + W::N, Dc = Da;
     const uint32_t mine = (static_cast<uint32_t>(w & 3) << 21) + 32 * part;
-    const uint64_t KQd = tensor::operand(base + W::KQ, 2048, 128), KTd = tensor::operand(base + W::KQ, 128, 2048);
+    const uint64_t KQd = tensor::swizzled(base + W::KQ, 0), KTd = tensor::swizzled(base + W::KQ, 16384);
     const uint64_t Sd = tensor::operand(base + W::S, 128, DKP * 16), Yd = tensor::operand(base + W::S, 128, 1024);
-    const uint64_t Td = tensor::operand(base + W::T, 128, 2048), dYd = tensor::operand(base + W::V, 128, 1024);
+    const uint64_t Td = tensor::operand(base + W::T, 128, 2048), dYd = tensor::swizzled(base + W::V + loads.first() * 16, 8192);
     const uint64_t Rd = tensor::operand(base + W::R, 128, 1024);
-    uint32_t phase = 0;
+    uint32_t phase = 0, full = 0;
     bool bad = false;
     for (int64_t j = blocks - 1; j >= 0; --j) {
         const uint64_t kq = static_cast<uint64_t>((j & 1) * W::kKQ) >> 4;
         const float* const vec = vecs[j & 1];
-        copies_wait<1>();
+        bad |= !tensor::barrier_wait(bar + 24 + 8 * (j & 1), full >> (j & 1) & 1);
+        full ^= 1u << (j & 1);
+        copies_wait<0>();
         async_fence();
         if (__syncthreads_or(bad)) break;
-        if (tid == 0) {
+        if (w == 0 && tensor::elect()) {
             tensor::fence_after();
 #pragma unroll
             for (int ks = 0; ks < DKP / 16; ++ks)
 #pragma unroll
-                for (int t = 0; t < 2; ++t)
-                    tensor::mma(Da, KQd + kq + ks * 256, Sd + (t * W::kS + ks * 256) / 16, tensor::shape(128, BV, false, true), ks + t > 0);
+                for (int t = 0; t < W::terms; ++t)
+                    tensor::mma(Da, KQd + kq + (ks >> 2) * 1024 + (ks & 3) * 2, Sd + (t * W::kS + ks * 256) / 16, tensor::shape(128, W::N, false, true), ks + t > 0);
             tensor::commit(bar);
         }
         load_kq(j - 1);
         bad |= !tensor::barrier_wait(bar, phase);
-        copies_wait<1>();
-        async_fence();
-        __syncthreads();
+        bad |= !tensor::barrier_wait(bar + 40, phase);
+        if (!loads.boxed(j)) {   // dY came by the threads' own copies
+            copies_wait<0>();
+            async_fence();
+            __syncthreads();
+        }
         tensor::fence_after();
         if (tid == 0) {   // what dY gives by A T
 #pragma unroll
             for (int t = 0; t < 2; ++t)
 #pragma unroll
                 for (int ks = 0; ks < 4; ++ks)
-                    tensor::mma(Db, Td + (t * 16384 + 1024 + ks * 256) / 16, dYd + ks * 16, tensor::shape(128, BV, true, true), t + ks > 0);
+                    tensor::mma(W::terms == 1 ? Db + t * BV : Db, Td + (t * 16384 + 1024 + ks * 256) / 16, dYd + ks * 128, tensor::shape(128, BV, true, true), W::terms == 1 ? ks > 0 : t + ks > 0);
         }
         uint64_t x[16];
         const float eg = vec[i], bt = vec[kC + i];
         if (key) {
-            tensor::load32(Da + mine, x);
+            W::sums(Da + mine, x);
             const float c = vec[2 * kC + i];
 #pragma unroll
             for (int e = 0; e < 16; ++e) x[e] = mul2(pack2(c, c), x[e]);
@@ -361,35 +358,37 @@ __global__ void __launch_bounds__(BV * 4) gdr_back_tc_kernel(const __grid_consta
             const float f = a.scale * eg;
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                const uint4 v = *reinterpret_cast<const uint4*>(smem + W::V + rows_at(i, 4 * part + q));
+                const uint4 v = *reinterpret_cast<const uint4*>(smem + W::V + (part >> 1) * 8192 + swizzled_at(i, loads.first() + (part & 1) * 4 + q));
                 const uint32_t vw[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
                 for (int e = 0; e < 4; ++e) x[4 * q + e] = mul2(pack2(f, f), widen2(vw[e]));
             }
-            put_terms(Yp, Yp + W::kS, 1024, x);
+            put_terms(Yp, Yp + W::kR, 1024, x);
         }
         async_fence();
         tensor::fence_before();
         __syncthreads();
-        if (tid == 0) {
+        if (w == 0 && tensor::elect()) {
             tensor::fence_after();
 #pragma unroll
-            for (int t = 0; t < 3; ++t)   // T's first term with both of x's, its second with the first
+            for (int t = 0; t < W::terms; ++t)   // T's first term with both of x's, its second with the first
 #pragma unroll
                 for (int ks = 0; ks < 4; ++ks)
-                    tensor::mma(Db, Td + (t >> 1) * 1024 + ks * 16, Rd + ((t & 1) * W::kR + ks * 256) / 16, tensor::shape(128, BV, true, true), true);
+                    tensor::mma(Db, Td + ks * 16, Rd + (t * W::kR + ks * 256) / 16, tensor::shape(128, W::N, true, true), true);
+#pragma unroll
+            for (int ks = 0; ks < 4; ++ks) tensor::mma(Db, Td + 1024 + ks * 16, Rd + ks * 16, tensor::shape(128, BV, true, true), true);
             tensor::commit(bar + 8);
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks)
 #pragma unroll
-                for (int t = 0; t < 2; ++t)
-                    tensor::mma(Dc, KTd + kq + 64 + ks * 16, Yd + (t * W::kS + ks * 256) / 16, tensor::shape(128, BV, true, true), ks + t > 0);
+                for (int t = 0; t < W::terms; ++t)
+                    tensor::mma(Dc, KTd + kq + 512 + ks * 128, Yd + (t * W::kR + ks * 256) / 16, tensor::shape(128, W::N, true, true), ks + t > 0);
         }
         bad |= !tensor::barrier_wait(bar + 8, phase);
         tensor::fence_after();
         uint64_t u[16];
         if (key) {
-            tensor::load32(Db + mine, u);
+            W::sums(Db + mine, u);
             const float f = -eg * bt;
 #pragma unroll
             for (int e = 0; e < 16; ++e) x[e] = mul2(pack2(f, f), u[e]);
@@ -398,13 +397,13 @@ __global__ void __launch_bounds__(BV * 4) gdr_back_tc_kernel(const __grid_consta
         async_fence();
         tensor::fence_before();
         __syncthreads();
-        if (tid == 0) {
+        if (w == 0 && tensor::elect()) {
             tensor::fence_after();
 #pragma unroll
             for (int ks = 0; ks < 4; ++ks)
 #pragma unroll
-                for (int t = 0; t < 2; ++t)
-                    tensor::mma(Dc, KTd + kq + ks * 16, Rd + (t * W::kR + ks * 256) / 16, tensor::shape(128, BV, true, true), true);
+                for (int t = 0; t < W::terms; ++t)
+                    tensor::mma(Dc, KTd + kq + ks * 128, Rd + (t * W::kR + ks * 256) / 16, tensor::shape(128, W::N, true, true), true);
             tensor::commit(bar + 16);
         }
         load_yt(j - 1);
@@ -433,7 +432,7 @@ __global__ void __launch_bounds__(BV * 4) gdr_back_tc_kernel(const __grid_consta
         bad |= !tensor::barrier_wait(bar + 16, phase);
         phase ^= 1;
         tensor::fence_after();
-        tensor::load32(Dc + mine, u);
+        W::sums(Dc + mine, u);
 #pragma unroll
         for (int e = 0; e < 16; ++e) S[e] = fma2(pack2(last, last), S[e], u[e]);
         put_state(j - 1);
@@ -788,6 +787,14 @@ __global__ void __launch_bounds__(512) gdr_grad_kernel(const __grid_constant__ A
 //   D5 = [-(M o D); N o D] K, D6 = (N o D)^T Q - (M o D)^T K,
 // so a thread that has row r of tensor memory has row r of the key's side (r < 64) or row r - 64 of the query's. Resident
 // blocks take (block of rows, head) after (block, head); the next ones' rows and states arrive while these are finished.
+// Copy number i of a tile of rows of U units into cores: a warp takes eight rows of four units.
+template <int U>
+__device__ __forceinline__ void core_place(int i, int& r, int& u) {
+    const int x = i >> 5;
+    r = (i & 7) + x / (U / 4) * 8;
+    u = (i >> 3 & 3) + x % (U / 4) * 4;
+}
+
 template <int DKP>
 struct GradTc {
     static constexpr int kGroup = 2 * 6144;                  // rows of 16 value columns: per core along K [U | W | dY], then the rests [U | W | 0]
@@ -811,7 +818,7 @@ __global__ void __launch_bounds__(256) gdr_grad_tc_kernel(const __grid_constant_
     __shared__ __align__(8) uint64_t bars[3];   // a stage's products each, and the last ones
     __shared__ uint32_t tmem;
     start_dependent();
-    const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, w = __shfl_sync(kFull, tid >> 5, 0), lane = tid & 31;
     const uint32_t base = smem_of(smem), bar = smem_of(bars);
     const int groups = (a.dv + 15) / 16, nslices = (groups + 1) / 2;
     const int64_t units = (a.rows / kC + a.P) * a.Hv;
@@ -931,7 +938,7 @@ __global__ void __launch_bounds__(256) gdr_grad_tc_kernel(const __grid_constant_
             out = __syncthreads_or(bad);
             if (out) break;
             const int sg = static_cast<int>(step & 1), so = W::slices + sg * W::stage;
-            if (tid == 0) {
+            if (w == 0 && tensor::elect()) {
                 tensor::fence_after();
                 const uint32_t st = base + so;
                 if (s == 0)
@@ -1023,7 +1030,7 @@ __global__ void __launch_bounds__(256) gdr_grad_tc_kernel(const __grid_constant_
                 for (int c = 0; c < 32; ++c) Z[i * 65 + 32 * half + c] = z[c];
             }
             __syncthreads();
-            if (tid == 0) {
+            if (w == 0 && tensor::elect()) {
                 tensor::fence_after();
                 constexpr uint32_t out5 = tensor::shape(128, DKP, false, true), out6 = tensor::shape(128, DKP, true, true);
                 const uint32_t XN = base + W::XN;
@@ -1239,7 +1246,10 @@ cudaError_t back_tc(const Args& a, cudaStream_t cs) {
     const cudaError_t e = big_smem(k, W::bytes);
     if (e != cudaSuccess) return e;
     const int64_t grid = static_cast<int64_t>(a.P) * a.Hv * ((a.dv + BV - 1) / BV);
-    return launch_dependent(k, dim3(static_cast<unsigned>(grid)), dim3(W::threads), W::bytes, cs, a);
+    Maps m;
+    const cudaError_t f = make_maps(&m, a, a.dy, BV);
+    if (f != cudaSuccess) return f;
+    return launch_dependent(k, dim3(static_cast<unsigned>(grid)), dim3(W::threads), W::bytes, cs, a, m);
 }
 
 template <int DKP>
@@ -1298,7 +1308,6 @@ extern "C" sdm_status sdm_gdr_backward(const sdm_gdr_shape* shape, const void* q
             a.dy = {to, vn, shape->rows * vn};
             if (e == cudaSuccess) e = launch_split(dy, dy_ld, shape->rows, static_cast<int>(vn), to, cs);
         }
-        if (e == cudaSuccess) e = launch_prepare(a, shape, cs);
     }
     const bool narrow = padded(shape->dk) == 64, bf16 = shape->x_dtype == SDM_BF16;
     if (e == cudaSuccess)

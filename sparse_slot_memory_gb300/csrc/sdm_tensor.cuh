@@ -1,10 +1,12 @@
 // sdm_tensor.cuh -- the fifth-generation tensor core's instructions (tcgen05) as the operators use them: bfloat16 operands in
 // shared memory, float32 accumulators in tensor memory, one thread that issues.
 //
-// Operands lie in cores of 8 x 8 elements, 128 contiguous bytes: 8 rows of 16 bytes. A matrix whose rows run along the summed
+// Computed operands lie in cores of 8 x 8 elements, 128 contiguous bytes: 8 rows of 16 bytes. A matrix whose rows run along the summed
 // dimension (K) has cores of 8 rows x 8 summands; one whose rows run along M or N has cores of 8 summands x 8 columns. A
 // descriptor names the first core and the distances between cores along K and along M or N; no swizzle. The same bytes serve
-// ldmatrix and stmatrix without bank conflicts, and either reading of a matrix (itself or its transpose) needs no copy.
+// ldmatrix and stmatrix without bank conflicts, and either reading of a matrix (itself or its transpose) needs no copy. Rows that a
+// tensor map brings are swizzled. Measured on a GB300: 128 x N x 16 takes 34 cycles for N of 32, 42 for 64, 65 for 128, 130 for
+// 256, whatever the layout and the direction.
 #pragma once
 
 #include <cstdint>
@@ -12,12 +14,22 @@
 namespace sdm {
 namespace tensor {
 
+// One thread of a whole warp, always the same. Products and copies that it names in a branch that whole warps take are issued back to
+// back (four products: 76 cycles, 265 from a thread chosen by its number).
+__device__ __forceinline__ bool elect() {
+    uint32_t p;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.b32 %0, 1, 0, p;\n}" : "=r"(p));
+    return p != 0;
+}
 // A matrix operand at shared address `a`: bytes between cores along K and along M or N (the descriptor's leading and stride
 // distances; 0b001 in bits 46..48 is its version).
 __device__ __forceinline__ uint64_t operand(uint32_t a, uint32_t along_k, uint32_t along_mn) {
     return static_cast<uint64_t>((a & 0x3FFFF) >> 4) | static_cast<uint64_t>((along_k & 0x3FFFF) >> 4) << 16 |
            static_cast<uint64_t>((along_mn & 0x3FFFF) >> 4) << 32 | uint64_t(1) << 46;
 }
+// The same of rows of 128 bytes whose units of 16 lie swizzled by the row's number in its eight (as a tensor map's boxes of 64
+// columns arrive): along M or N in tiles `next` bytes apart where rows run along M or N, eight rows 1024 bytes.
+__device__ __forceinline__ uint64_t swizzled(uint32_t a, uint32_t next) { return operand(a, next, 1024) | uint64_t(2) << 61; }
 // The instruction's shape: M x N, bfloat16 operands, float32 sums; ta / tb: the operand's rows run along M / N.
 __host__ __device__ constexpr uint32_t shape(int M, int N, bool ta, bool tb) {
     return 1u << 4 | 1u << 7 | 1u << 10 | static_cast<uint32_t>(ta) << 15 | static_cast<uint32_t>(tb) << 16 |
@@ -84,6 +96,20 @@ __device__ __forceinline__ void barrier_init(uint32_t bar, int arrivals) {
     asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(arrivals) : "memory");
 }
 __device__ __forceinline__ void barrier_fence() { asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory"); }
+// An arrival that also announces bytes of copies to come.
+__device__ __forceinline__ void barrier_expect(uint32_t bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+// Contiguous bytes (a multiple of 16) from global to shared memory; and a box of a tensor map, from a column that is a multiple of 8 on.
+__device__ __forceinline__ void copy_bulk(uint32_t to, const void* from, uint32_t bytes, uint32_t bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(to), "l"(from), "r"(bytes), "r"(bar)
+                 : "memory");
+}
+__device__ __forceinline__ void copy_box(uint32_t to, const void* map, int col, int row, uint32_t bar) {
+    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(to),
+                 "l"(map), "r"(col), "r"(row), "r"(bar)
+                 : "memory");
+}
 // Waits for the phase to end, for a second or so at most; false where it has not.
 __device__ __forceinline__ bool barrier_wait(uint32_t bar, uint32_t phase) {
     for (int i = 0; i < 1 << 20; ++i) {

@@ -226,7 +226,8 @@ class GdrSpec(_Spec):
 
 
 def alloc_gdr_states(spec: GdrSpec, device="cuda") -> torch.Tensor:
-    """What the forward saves for the backward: the state before every 64th row and the rows' writes, in the kernels' own form (bytes)."""
+    """What the forward saves for the backward: the state before every 64th row, the rows' writes and what their blocks give
+    without the state, in the kernels' own form (bytes)."""
     return torch.empty(_bytes(spec, "sdm_gdr_states_bytes"), dtype=torch.uint8, device=device)
 
 
