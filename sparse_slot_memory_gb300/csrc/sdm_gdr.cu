@@ -700,7 +700,11 @@ __global__ void __launch_bounds__(BV * 4) gdr_walk_tc_kernel(const __grid_consta
             if (vc + 4 * q < a.dv) st4(hT + 4 * q, Quad{S[2 * q], S[2 * q + 1]});
     }
     copies_wait<0>();
-    if (__syncthreads_or(bad) && tid == 0 && a.status != nullptr) atomicOr(a.status, SDM_DEV_STALLED);
+    if (__syncthreads_or(bad)) {
+        if (tid == 0 && a.status != nullptr) atomicOr(a.status, SDM_DEV_STALLED);
+        tensor::drain(bar, 6);
+        __syncthreads();
+    }
     tensor::fence_after();
     if (w == 0) tensor::release<W::cols>(tmem);
 }

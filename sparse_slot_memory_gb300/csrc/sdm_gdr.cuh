@@ -443,11 +443,18 @@ struct WalkLoads {
 inline int padded(int d) { return d <= 64 ? 64 : 128; }
 inline int64_t blocks_of(const sdm_gdr_shape* s) { return s->rows / kC + s->P; }
 
-// Value columns of a block of a walk of bfloat16 rows: fewer while the grid leaves SMs idle.
+// Value columns of a block of a walk of bfloat16 rows. A block of rows took 1.8 us with 32, 2.1 with 64 and 3.6 with 128 columns
+// (keys of 64), and the SMs hold one block each: the fewest rounds of the grid times that. 12 prompts of 16 heads of 128 took 294 us
+// with 64 and 402 with 128, 8 of 4096 rows 380 with 64 and 349 with 128, one of 8 heads 952 with 32 and 1143 with 64.
 inline int columns(const Args& a) {
-    int bv = a.dv <= 32 ? 32 : a.dv <= 64 ? 64 : 128;
-    while (bv > 32 && static_cast<int64_t>(a.P) * a.Hv * ((a.dv + bv - 1) / bv) * 2 <= 152) bv /= 2;
-    return bv;
+    int best = 32;
+    int64_t least = INT64_MAX;
+    for (const auto& [bv, cost] : {std::pair{128, 10}, {64, 6}, {32, 5}}) {
+        if (bv > 32 && a.dv <= bv / 2) continue;
+        const int64_t grid = static_cast<int64_t>(a.P) * a.Hv * ((a.dv + bv - 1) / bv), t = (grid + 151) / 152 * cost;
+        if (t < least) best = bv, least = t;
+    }
+    return best;
 }
 inline sdm_status check_array(const void* p, int64_t ld, int64_t n, int elem, int align, bool out) {
     if (p == nullptr) return SDM_ERR_ARG;
@@ -474,7 +481,7 @@ cudaError_t launch_split(const void* x, int64_t ld, int64_t rows, int cols, __nv
 cudaError_t launch_planes(const sdm_gdr_shape* s, const void* q, int64_t q_ld, const void* k, int64_t k_ld, const void* v, int64_t v_ld,
                           void* ws, bool backward, Args* a, cudaStream_t cs);
 cudaError_t launch_prepare(const Args& a, const sdm_gdr_shape* s, cudaStream_t cs);
-// The maps of a walk over BV value columns a block
+// The maps of a walk over bv value columns a block
 cudaError_t make_maps(Maps* m, const Args& a, const Planes& v, int bv);
 
 }  // namespace gdr

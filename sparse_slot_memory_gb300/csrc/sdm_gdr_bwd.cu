@@ -445,7 +445,11 @@ __global__ void __launch_bounds__(BV * 4) gdr_back_tc_kernel(const __grid_consta
             if (vc + 4 * q < a.dv) st4(d + 4 * q, Quad{S[2 * q], S[2 * q + 1]});
     }
     copies_wait<0>();
-    if (__syncthreads_or(bad) && tid == 0 && a.status != nullptr) atomicOr(a.status, SDM_DEV_STALLED);
+    if (__syncthreads_or(bad)) {
+        if (tid == 0 && a.status != nullptr) atomicOr(a.status, SDM_DEV_STALLED);
+        tensor::drain(bar, 6);
+        __syncthreads();
+    }
     tensor::fence_after();
     if (w == 0) tensor::release<W::cols>(tmem);
 }
@@ -782,40 +786,42 @@ __global__ void __launch_bounds__(512) gdr_grad_kernel(const __grid_constant__ A
 // ---- all blocks at once, bfloat16 rows --------------------------------------------------------------------------------
 // All of the slices' products read what is stored as it is, so they are the fifth-generation tensor core's: one thread issues them,
 // the sums stay in tensor memory, and the threads turn to them when a block's slices are through. Rows are stacked to the
-// instruction's 128, [W; dY] against S and U, [U; W] against dS' (its lower half is not used), [K; Q] against K:
+// instruction's 128, [W; dY] against S and U, [U; .] against dS' (its lower half is not used), [K; Q] against K:
 //   D1 = [W; dY] S^T, D2 = [U; .] dS'^T, D3 = [W; dY] U^T, D4 = [K; Q] K^T, then with the decays in
 //   D5 = [-(M o D); N o D] K, D6 = (N o D)^T Q - (M o D)^T K,
-// so a thread that has row r of tensor memory has row r of the key's side (r < 64) or row r - 64 of the query's. Resident
-// blocks take (block of rows, head) after (block, head); the next ones' rows and states arrive while these are finished.
-// Copy number i of a tile of rows of U units into cores: a warp takes eight rows of four units.
-template <int U>
-__device__ __forceinline__ void core_place(int i, int& r, int& u) {
-    const int x = i >> 5;
-    r = (i & 7) + x / (U / 4) * 8;
-    u = (i >> 3 & 3) + x % (U / 4) * 4;
-}
-
+// so a thread that has row r of tensor memory has row r of the key's side (r < 64) or row r - 64 of the query's, and a quarter of its
+// columns. Resident blocks take (block of rows, head) after (block, head); the next ones' rows and states arrive, two slices of 32
+// value columns ahead, while these are finished. Its floor is HBM: 272 KB a block of a head of 128, of which the states are 128 (6.7
+// us on each of 152 SMs; measured 13.2). What bounds it is one chain of a block: shared memory is read by the products for half of
+// a slice (a product of 128 x 128 x 16 takes as long as its operands take to be read), and a block's sums fill tensor memory, so
+// the next block's products wait for these to be taken in.
 template <int DKP>
 struct GradTc {
-    static constexpr int kGroup = 2 * 6144;                  // rows of 16 value columns: per core along K [U | W | dY], then the rests [U | W | 0]
-    static constexpr int kUnit = DKP * 16, kTerm = 4 * kUnit, kStates = 2 * kTerm;   // of states: 8 value columns, 32
-    static constexpr int rows = 0, S = 2 * kGroup, dS = S + kStates, stage = dS + kStates;
-    static constexpr int kKQ = DKP / 8 * 2048;               // [K; Q], two of them
+    // a slice: U's two terms, [W; dY], [W's rests; 0], S's and dS's two terms, all in units of 8 value columns
+    static constexpr int kUnit = DKP * 16, kTerm = 4 * kUnit, kStates = 2 * kTerm;
+    static constexpr int U = 0, WY = 8192, S = WY + 16384, dS = S + kStates, stage = dS + kStates;
+    static constexpr int kKQ = 2 * kC * DKP * 2;             // [K; Q], two of them: tiles of 128 rows for 64 columns
     static constexpr int slices = 2 * kKQ, XN = slices + 2 * stage, Z = XN + 16384, bytes = Z + kC * 65 * 4;
-    static constexpr int threads = 256;
+    static constexpr int threads = 512;
 };
 
 template <int DKP>
-__global__ void __launch_bounds__(256) gdr_grad_tc_kernel(const __grid_constant__ Args a) {
+__global__ void __launch_bounds__(512, 1) gdr_grad_tc_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps) {
     using W = GradTc<DKP>;
-    constexpr int HC = DKP / 2;   // columns of dk of a thread
+    constexpr int QC = DKP / 4;   // columns of dk of a thread
+    struct Unit {
+        int64_t id, b;   // id: block x head; its rows are [b, b + n)
+        int h, kh, n;
+    };
     extern __shared__ __align__(1024) unsigned char smem[];
-    __shared__ __align__(16) float vecs[2][kVecs * kC];
-    __shared__ float sums[3][2][kC];   // scale-free q . (S dY), k . (S W), k . (dS' u) by halves of dk
+    __shared__ __align__(128) float vecs[2][kVecs * kC];
+    __shared__ float sums[3][4][kC];   // scale-free q . (S dY), k . (S W), k . (dS' u) by quarters of dk
     __shared__ float diag[kC];         // W . U
     __shared__ float share[2][kC];     // a and e
-    __shared__ float inner[8];
-    __shared__ __align__(8) uint64_t bars[3];   // a stage's products each, and the last ones
+    __shared__ float inner[W::threads / 32];
+    __shared__ __align__(16) float far[4][68], near[kC];   // decays: e^(gam_16b - gam_j) before block b of 16 rows, e^(gam_i - gam_16b) within
+    __shared__ Unit ring[4];           // the units that are loaded, by their number
+    __shared__ __align__(8) uint64_t bars[7];   // a stage's products each, and the last ones; a stage's copies each, and [K; Q]'s
     __shared__ uint32_t tmem;
     start_dependent();
     const int tid = threadIdx.x, w = __shfl_sync(kFull, tid >> 5, 0), lane = tid & 31;
@@ -823,100 +829,109 @@ __global__ void __launch_bounds__(256) gdr_grad_tc_kernel(const __grid_constant_
     const int groups = (a.dv + 15) / 16, nslices = (groups + 1) / 2;
     const int64_t units = (a.rows / kC + a.P) * a.Hv;
 
-    struct Unit {
-        int64_t id, b;   // id: block x head
-        int h, n;
-    };
-    auto find = [&](int64_t id) {   // the first one from id on, in steps of the grid, that has rows
+    auto find = [&](int64_t id) {   // the first one from id on, in steps of the grid, that has rows: by one warp
         Unit u;
-        u.n = 0;
+        u.n = u.h = u.kh = 0;
+        u.b = 0;
         for (u.id = id; u.id < units; u.id += gridDim.x) {
-            const int64_t blk = u.id / a.Hv;
-            u.h = static_cast<int>(u.id - blk * a.Hv);
+            const int blk = static_cast<int>(u.id) / a.Hv;
+            u.h = static_cast<int>(u.id) - blk * a.Hv;
+            u.kh = u.h / (a.Hv / a.Hk);
             block_rows(a, blk, u.b, u.n);
             if (u.n > 0) break;
         }
         return u;
     };
-    Unit lu = find(blockIdx.x);   // what is loaded next
+    Unit lu;   // what is loaded next
     int ls = 0, lkq = 0;
-    int64_t issued = 0;           // slices on their way or there
-    auto load = [&]() {
+    int64_t issued = 0, found = 0;   // slices on their way or there; units that follow the first
+    auto load = [&]() {              // behind a barrier that stands behind the last one
+        if (ls == 0) lu = ring[found & 3];
         if (lu.id < units) {
-            const uint32_t st = base + W::slices + static_cast<int>(issued & 1) * W::stage;
-            const int g0 = 2 * ls, have = min(2, groups - g0), c0 = 32 * ls, cols = min(32, a.dv - c0);
-            const int64_t first = lu.id * 2 * (2 * groups) + 2 * g0;   // the slice's first unit of 8 value columns of the first term
-            const __nv_bfloat16* const sp = a.states + first * (DKP * 8);
-            const __nv_bfloat16* const dp = a.dstates + first * (DKP * 8);
-            const __nv_bfloat16* const wp = a.du + first * (kC * 8);
-            const __nv_bfloat16* const up = a.writes + first * (kC * 8);
+            const int sg = static_cast<int>(issued & 1);
+            const uint32_t st = base + W::slices + sg * W::stage;
+            const int g0 = 2 * ls, have = min(2, groups - g0), c0 = 32 * ls, cols = min(32, a.dv - c0), kh = lu.kh;
+            const bool box = maps.boxes && lu.n == kC;
+            // a copy takes its thread 80 cycles, so five warps share them
+            if (w >= 1 && w < 5 + (ls == 0) && tensor::elect()) {
+                const int64_t first = lu.id * 2 * (2 * groups) + 2 * g0, rest = first + 2 * groups;   // the slice's first unit of 8 value columns, by terms
+                const uint32_t full = bar + 24 + 8 * sg, sb = have * 2 * W::kUnit, rb = have * 2048;
+                if (w == 1) {
+                    tensor::barrier_expect(full, 4 * (sb + rb));
+                    tensor::copy_bulk(st + W::S, a.states + first * (DKP * 8), sb, full);
+                    tensor::copy_bulk(st + W::S + W::kTerm, a.states + rest * (DKP * 8), sb, full);
+                } else if (w == 2) {
+                    tensor::copy_bulk(st + W::dS, a.dstates + first * (DKP * 8), sb, full);
+                    tensor::copy_bulk(st + W::dS + W::kTerm, a.dstates + rest * (DKP * 8), sb, full);
+                    tensor::copy_bulk(st + W::U, a.writes + first * (kC * 8), rb, full);
+                    tensor::copy_bulk(st + W::U + 4096, a.writes + rest * (kC * 8), rb, full);
+                } else if (w == 3) {
+                    for (int x = 0; x < 2 * have; ++x) tensor::copy_bulk(st + W::WY + x * 2048, a.du + (first + x) * (kC * 8), 1024, full);
+                } else if (w == 4) {
+                    for (int x = 0; x < 2 * have; ++x) tensor::copy_bulk(st + W::WY + 8192 + x * 2048, a.du + (rest + x) * (kC * 8), 1024, full);
+                } else {
+                    const uint32_t to = base + lkq * W::kKQ, kqfull = bar + 40 + 8 * lkq;
+                    tensor::barrier_expect(kqfull, kVecs * kC * 4 + (box ? W::kKQ : 0));
+                    tensor::copy_bulk(smem_of(vecs[lkq]), a.vec + lu.id * kVecs * kC, kVecs * kC * 4, kqfull);
+                    if (box) {
 #pragma unroll
-            for (int i = tid; i < W::kStates / 16; i += W::threads) {
-                const int t = i / (4 * DKP), x = i % (4 * DKP);
-                const bool there = x < have * 2 * DKP;
-                const int64_t at = there ? (static_cast<int64_t>(t) * 2 * groups * DKP + x) * 8 : 0;
-                copy16(st + W::S + i * 16, sp + at, there);
-                copy16(st + W::dS + i * 16, dp + at, there);
-            }
-#pragma unroll
-            for (int i = tid; i < 512; i += W::threads) {   // term, group, core along K, row
-                const int t = i >> 8, x = i & 255;
-                const bool there = x < have * 128;
-                const int64_t at = there ? (static_cast<int64_t>(t) * 2 * groups * kC + x) * 8 : 0;
-                const uint32_t to = st + W::rows + (x >> 7) * W::kGroup + t * 6144 + (x >> 6 & 1) * 3072 + (x & 63) * 16;
-                copy16(to, up + at, there);
-                copy16(to + 1024, wp + at, there);
-            }
-            {
-                int r, u;
-                core_place<4>(tid, r, u);
-                const bool there = r < lu.n && u * 8 < cols;
-                copy16(st + W::rows + (u >> 1) * W::kGroup + (u & 1) * 3072 + 2048 + r * 16,
-                       there ? a.dy.p + (lu.b + r) * a.dy.ld + lu.h * a.dv + c0 + u * 8 : a.dy.p, there);
-            }
-            if (ls == 0) {
-                const int kh = lu.h / (a.Hv / a.Hk);
-#pragma unroll
-                for (int i = tid; i < 2 * kC * (DKP / 8); i += W::threads) {
-                    int r, u;
-                    core_place<DKP / 8>(i, r, u);
-                    const int t = r & 63;
-                    const Planes& x = r < kC ? a.k : a.q;
-                    const bool there = t < lu.n && u * 8 < a.dk;
-                    copy16(base + lkq * W::kKQ + stacked_at(r, u), there ? x.p + (lu.b + t) * x.ld + kh * a.dk + u * 8 : x.p, there);
+                        for (int x = 0; x < DKP / 64; ++x) {
+                            tensor::copy_box(to + x * 16384, &maps.k, kh * DKP + x * 64, static_cast<int>(lu.b), kqfull);
+                            tensor::copy_box(to + x * 16384 + 8192, &maps.q, kh * DKP + x * 64, static_cast<int>(lu.b), kqfull);
+                        }
+                    }
                 }
-                if (tid < kVecs * kC / 4) copy16(smem_of(vecs[lkq]) + tid * 16, a.vec + lu.id * kVecs * kC + tid * 4, true);
+            }
+            if (tid >= 256) {   // dY: a warp takes eight rows of four units
+                const int r = (tid & 7) + (tid >> 5 & 7) * 8, u = tid >> 3 & 3;
+                const bool there = r < lu.n && u * 8 < cols;
+                copy16(st + W::WY + u * 2048 + 1024 + r * 16, there ? a.dy.p + (lu.b + r) * a.dy.ld + lu.h * a.dv + c0 + u * 8 : a.dy.p, there);
+            }
+            if (ls == 0 && !box) {
+                for (int x = tid; x < 2 * kC * (DKP / 8); x += W::threads) {
+                    const int r = x / (DKP / 8), u = x % (DKP / 8), t = r & 63;
+                    const Planes& p = r < kC ? a.k : a.q;
+                    const bool there = t < lu.n && u * 8 < a.dk;
+                    copy16(base + lkq * W::kKQ + (u >> 3) * 16384 + swizzled_at(r, u & 7),
+                           there ? p.p + (lu.b + t) * p.ld + kh * a.dk + u * 8 : p.p, there);
+                }
             }
             if (++ls == nslices) {
                 ls = 0;
                 lkq ^= 1;
-                lu = find(lu.id + gridDim.x);
+                ++found;
+                if (w == 6) {
+                    const Unit next = find(lu.id + gridDim.x);
+                    if (lane == 0) ring[found & 3] = next;
+                }
             }
         }
         copies_commit();
         ++issued;
     };
-    // zeros under dY's rests stay
-    for (int i = tid; i < 2 * 2 * 2 * 64; i += W::threads) {
-        const int at = W::slices + (i >> 8) * W::stage + W::rows + (i >> 7 & 1) * W::kGroup + 6144 + (i >> 6 & 1) * 3072 + 2048 + (i & 63) * 16;
-        *reinterpret_cast<uint4*>(smem + at) = make_uint4(0, 0, 0, 0);
-    }
+    // zeros under dY's rests stay; what no copy reaches is a number
+    for (int i = tid; i < W::bytes / 16; i += W::threads) *reinterpret_cast<uint4*>(smem + i * 16) = make_uint4(0, 0, 0, 0);
     if (w == 0) tensor::allocate<512>(smem_of(&tmem));
     if (tid == 0) {
-        for (int i = 0; i < 3; ++i) tensor::barrier_init(bar + 8 * i, 1);
+        for (int i = 0; i < 7; ++i) tensor::barrier_init(bar + 8 * i, 1);
         tensor::barrier_fence();
     }
-    Unit u = lu;
-    load();
+    if (w == 1) {
+        const Unit first = find(blockIdx.x);
+        if (lane == 0) ring[0] = first;
+    }
+    async_fence();
     tensor::fence_before();
     __syncthreads();
     tensor::fence_after();
+    load();
+    Unit u = lu;
     const uint32_t D1 = tmem, D2 = D1 + 128, D3 = D1 + 256, D4 = D1 + 320, D5 = D1 + 384, D6 = D1 + 256;
     const uint32_t mine = static_cast<uint32_t>(w & 3) << 21;   // this warp's 32 rows
-    const int r = 32 * (w & 3) + lane, half = w >> 2, i = r & 63;
+    const int r = 32 * (w & 3) + lane, quarter = w >> 2, i = r & 63;
     const bool key = r < kC;                                    // the key's side
     uint32_t phase[3] = {};
-    int64_t waited[2] = {}, step = 0;   // steps whose products were waited for, by stage
+    int64_t waited[2] = {}, step = 0, number = 0;   // steps whose products were waited for, by stage; slices and units that are through
     bool bad = false;
     int kq = 0;
     auto wait_stage = [&](int s, int64_t before) {   // the products of the stage's steps before step `before`
@@ -929,30 +944,35 @@ __global__ void __launch_bounds__(256) gdr_grad_tc_kernel(const __grid_constant_
     while (u.id < units) {
         const uint32_t KQ = base + kq * W::kKQ;
         const float* const vec = vecs[kq];
-        float ss = 0.f;
+        uint64_t ss = 0;
         bool out = false;
         for (int s = 0; s < nslices; ++s, ++step) {
-            if (issued == step + 2) copies_wait<1>();
-            else copies_wait<0>();
+            // the last slice's products are done and its states read, so the next one's copies follow this one's products
+            const int sg = static_cast<int>(step & 1), so = W::slices + sg * W::stage;
+            wait_stage(sg ^ 1, step);
+            if (s == 0) bad |= !tensor::barrier_wait(bar + 40 + 8 * kq, static_cast<uint32_t>(number >> 1) & 1);
+            copies_wait<0>();
             async_fence();
             out = __syncthreads_or(bad);
             if (out) break;
-            const int sg = static_cast<int>(step & 1), so = W::slices + sg * W::stage;
+            bad |= !tensor::barrier_wait(bar + 24 + 8 * sg, static_cast<uint32_t>(step >> 1) & 1);
+            __syncwarp();
+            const int have = min(2, groups - 2 * s);
             if (w == 0 && tensor::elect()) {
                 tensor::fence_after();
                 const uint32_t st = base + so;
-                if (s == 0)
+                if (s == 0) {
+#pragma unroll
                     for (int ks = 0; ks < DKP / 16; ++ks) {
-                        const uint64_t x = tensor::operand(KQ + ks * 4096, 2048, 128);
+                        const uint64_t x = tensor::swizzled(KQ + (ks >> 2) * 16384 + (ks & 3) * 32, 0);
                         tensor::mma(D4, x, x, tensor::shape(128, 64, false, false), ks > 0);
                     }
-                for (int gr = 0; gr < min(2, groups - 2 * s); ++gr) {
-                    const uint32_t hi = st + W::rows + gr * W::kGroup, lo = hi + 6144;
-                    const uint64_t wy = tensor::operand(hi + 1024, 3072, 128), w0 = tensor::operand(lo + 1024, 3072, 128);
-                    const uint64_t uh = tensor::operand(hi, 3072, 128), ul = tensor::operand(lo, 3072, 128);
-                    const uint32_t sa = st + W::S + gr * 2 * W::kUnit, da = st + W::dS + gr * 2 * W::kUnit;
-                    const uint64_t sh = tensor::operand(sa, W::kUnit, 128), sl = tensor::operand(sa + W::kTerm, W::kUnit, 128);
-                    const uint64_t dh = tensor::operand(da, W::kUnit, 128), dl = tensor::operand(da + W::kTerm, W::kUnit, 128);
+                }
+                for (int gr = 0; gr < have; ++gr) {
+                    const uint64_t wy = tensor::operand(st + W::WY + gr * 4096, 2048, 128), w0 = wy + 8192 / 16;
+                    const uint64_t uh = tensor::operand(st + W::U + gr * 2048, 1024, 128), ul = uh + 4096 / 16;
+                    const uint64_t sh = tensor::operand(st + W::S + gr * 2 * W::kUnit, W::kUnit, 128), sl = sh + W::kTerm / 16;
+                    const uint64_t dh = tensor::operand(st + W::dS + gr * 2 * W::kUnit, W::kUnit, 128), dl = dh + W::kTerm / 16;
                     constexpr uint32_t wide = tensor::shape(128, DKP, false, false), square = tensor::shape(128, 64, false, false);
                     const bool add = s + gr > 0;
                     tensor::mma(D3, wy, uh, square, add);
@@ -968,14 +988,20 @@ __global__ void __launch_bounds__(256) gdr_grad_tc_kernel(const __grid_constant_
                 }
                 tensor::commit(bar + 8 * sg);
             }
-            if (issued == step + 1) {   // the other stage is free once its products are done
-                wait_stage(sg ^ 1, step);
-                load();
+            if (issued == step + 1) load();
+            if (s == 0) {
+                auto gap = [&](int i, int j) { return decay<1>((vec[3 * kC + i] - vec[3 * kC + j]) + (vec[4 * kC + i] - vec[4 * kC + j])); };
+                const int x = tid & 63, y = tid >> 6;
+                if (y < 4) {
+                    if (x < 16 * y) far[y][x] = gap(16 * y, x);
+                } else if (y == 4) {
+                    near[x] = gap(x, x & ~15);
+                }
             }
             if (vec[kC - 1] != 0.f) {   // <dS', S>, both in the same tiles
-                for (int x = tid; x < W::kTerm / 16; x += W::threads) {
+                for (int x = tid; x < have * 2 * DKP; x += W::threads) {
                     const int o = x * 16;
-                    float p[8] = {}, q[8] = {};
+                    uint64_t p[4], q[4];
 #pragma unroll
                     for (int t = 1; t >= 0; --t) {
                         const uint4 y = *reinterpret_cast<const uint4*>(smem + so + W::S + o + t * W::kTerm);
@@ -983,16 +1009,15 @@ __global__ void __launch_bounds__(256) gdr_grad_tc_kernel(const __grid_constant_
                         const uint32_t yw[4] = {y.x, y.y, y.z, y.w}, zw[4] = {z.x, z.y, z.z, z.w};
 #pragma unroll
                         for (int e = 0; e < 4; ++e) {
-                            p[2 * e] += __uint_as_float(yw[e] << 16);
-                            p[2 * e + 1] += __uint_as_float(yw[e] & 0xFFFF0000u);
-                            q[2 * e] += __uint_as_float(zw[e] << 16);
-                            q[2 * e + 1] += __uint_as_float(zw[e] & 0xFFFF0000u);
+                            p[e] = t ? widen2(yw[e]) : add2(p[e], widen2(yw[e]));
+                            q[e] = t ? widen2(zw[e]) : add2(q[e], widen2(zw[e]));
                         }
                     }
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) ss = fmaf(p[e], q[e], ss);
+                    for (int e = 0; e < 4; ++e) ss = fma2(p[e], q[e], ss);
                 }
             }
+            __syncwarp();
         }
         if (out) break;
         wait_stage(0, step);
@@ -1003,64 +1028,80 @@ __global__ void __launch_bounds__(256) gdr_grad_tc_kernel(const __grid_constant_
         // N o D and - M o D, and the terms of dg that both give
         float* const Z = reinterpret_cast<float*>(smem + W::Z);
         {
-            float x[32], y[32];
-            tensor::fetch32(D3 + mine + 32 * half, x);
-            tensor::fetch32(D4 + mine + 32 * half, y);
+            float x[16], y[16];
+            const int own = i >> 4;   // the row's block of 16
+            tensor::fetch16(D3 + mine + 16 * quarter, x);
+            tensor::fetch16(D4 + mine + 16 * quarter, y);
             tensor::arrived(x);
             tensor::arrived(y);
-            const float gh = vec[3 * kC + i], gl = vec[4 * kC + i], mul = key ? -vec[kC + i] : a.scale;
-            float z[32];
+            const float mul = key ? -vec[kC + i] : a.scale;
+            if (quarter < own) {
+                const float f = mul * near[i];
 #pragma unroll
-            for (int c = 0; c < 32; ++c) {
-                const int j = 32 * half + c;
-                if (key && j == i) diag[i] = x[c];
-                const float d = decay<1>((gh - vec[3 * kC + j]) + (gl - vec[4 * kC + j]));
-                x[c] = j < i || (!key && j == i) ? d * (mul * x[c]) : 0.f;
-                z[c] = j < i ? x[c] * y[c] : 0.f;
+                for (int c = 0; c < 16; ++c) {
+                    x[c] *= f * far[own][16 * quarter + c];
+                    y[c] *= x[c];
+                }
+            } else if (quarter == own) {
+                const float gh = vec[3 * kC + i], gl = vec[4 * kC + i];
+#pragma unroll
+                for (int c = 0; c < 16; ++c) {
+                    const int j = 16 * quarter + c;
+                    if (key && j == i) diag[i] = x[c];
+                    const float d = decay<1>((gh - vec[3 * kC + j]) + (gl - vec[4 * kC + j]));
+                    x[c] = j < i || (!key && j == i) ? d * (mul * x[c]) : 0.f;
+                    y[c] = j < i ? x[c] * y[c] : 0.f;
+                }
+            } else {
+#pragma unroll
+                for (int c = 0; c < 16; ++c) x[c] = y[c] = 0.f;
             }
+            __syncwarp();
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-                *reinterpret_cast<uint4*>(smem + W::XN + stacked_at(r, 4 * half + q)) =
+            for (int q = 0; q < 2; ++q)
+                *reinterpret_cast<uint4*>(smem + W::XN + stacked_at(r, 2 * quarter + q)) =
                     make_uint4(round2(x[8 * q], x[8 * q + 1]), round2(x[8 * q + 2], x[8 * q + 3]), round2(x[8 * q + 4], x[8 * q + 5]),
                                round2(x[8 * q + 6], x[8 * q + 7]));
             async_fence();
             tensor::fence_before();
             if (key) {
 #pragma unroll
-                for (int c = 0; c < 32; ++c) Z[i * 65 + 32 * half + c] = z[c];
+                for (int c = 0; c < 16; ++c) Z[i * 65 + 16 * quarter + c] = y[c];
             }
             __syncthreads();
             if (w == 0 && tensor::elect()) {
                 tensor::fence_after();
                 constexpr uint32_t out5 = tensor::shape(128, DKP, false, true), out6 = tensor::shape(128, DKP, true, true);
-                const uint32_t XN = base + W::XN;
+                const uint64_t k = tensor::swizzled(KQ, 16384), q = k + 8192 / 16, X = tensor::operand(base + W::XN, 2048, 128);
+                const uint64_t Xt = tensor::operand(base + W::XN, 128, 2048);
+#pragma unroll
                 for (int ks = 0; ks < 4; ++ks) {
-                    const uint64_t k = tensor::operand(KQ + ks * 256, 128, 2048), q = tensor::operand(KQ + 1024 + ks * 256, 128, 2048);
-                    tensor::mma(D5, tensor::operand(XN + ks * 4096, 2048, 128), k, out5, ks > 0);
-                    tensor::mma(D6, tensor::operand(XN + 1024 + ks * 256, 128, 2048), q, out6, ks > 0);
-                    tensor::mma(D6, tensor::operand(XN + ks * 256, 128, 2048), k, out6, true);
+                    tensor::mma(D5, X + ks * 256, k + ks * 128, out5, ks > 0);
+                    tensor::mma(D6, Xt + 64 + ks * 16, q + ks * 128, out6, ks > 0);
+                    tensor::mma(D6, Xt + ks * 16, k + ks * 128, out6, true);
                 }
                 tensor::commit(bar + 16);
             }
             if (!key) {
 #pragma unroll
-                for (int c = 0; c < 32; ++c) Z[i * 65 + 32 * half + c] += z[c];
+                for (int c = 0; c < 16; ++c) Z[i * 65 + 16 * quarter + c] += y[c];
             }
         }
         // the rows' products with their own queries and keys
         {
             float s1 = 0.f, s3 = 0.f;
 #pragma unroll
-            for (int p = 0; p < HC / 32; ++p) {
-                const int c0 = HC * half + 32 * p;
-                float v[32], t[32];
-                tensor::fetch32(D1 + mine + c0, v);
-                tensor::fetch32(D2 + mine + c0, t);
+            for (int p = 0; p < QC / 16; ++p) {
+                const int c0 = QC * quarter + 16 * p;
+                float v[16], t[16];
+                tensor::fetch16(D1 + mine + c0, v);
+                tensor::fetch16(D2 + mine + c0, t);
                 tensor::arrived(v);
                 tensor::arrived(t);
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const uint4 x = *reinterpret_cast<const uint4*>(smem + kq * W::kKQ + stacked_at(r, c0 / 8 + q));
+                for (int q = 0; q < 2; ++q) {
+                    const int un = c0 / 8 + q;
+                    const uint4 x = *reinterpret_cast<const uint4*>(smem + kq * W::kKQ + (un >> 3) * 16384 + swizzled_at(r, un & 7));
                     const uint32_t xw[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
@@ -1070,49 +1111,54 @@ __global__ void __launch_bounds__(256) gdr_grad_tc_kernel(const __grid_constant_
                     }
                 }
             }
-            sums[key ? 1 : 0][half][i] = s1;
-            if (key) sums[2][half][i] = s3;
+            sums[key ? 1 : 0][quarter][i] = s1;
+            if (key) sums[2][quarter][i] = s3;
         }
+        {
+            float s, t;
+            unpack2(ss, s, t);
+            s += t;
 #pragma unroll
-        for (int o = 16; o > 0; o /= 2) ss += __shfl_xor_sync(kFull, ss, o);
-        if (lane == 0) inner[w] = ss;
+            for (int o = 16; o > 0; o /= 2) s += __shfl_xor_sync(kFull, s, o);
+            if (lane == 0) inner[w] = s;
+        }
         __syncthreads();
         if (tid < kC) {
             const float eg = vec[tid];
-            share[0][tid] = eg * (a.scale * (sums[0][0][tid] + sums[0][1][tid]) - vec[kC + tid] * (sums[1][0][tid] + sums[1][1][tid]));
-            share[1][tid] = vec[2 * kC + tid] * (sums[2][0][tid] + sums[2][1][tid]);
+            auto four = [&](int x) { return (sums[x][0][tid] + sums[x][1][tid]) + (sums[x][2][tid] + sums[x][3][tid]); };
+            share[0][tid] = eg * (a.scale * four(0) - vec[kC + tid] * four(1));
+            share[1][tid] = vec[2 * kC + tid] * four(2);
         }
-        // dg. Column by column sums from the bottom (16 rows a thread, then what lies below them), then row by row up to the diagonal.
+        // dg. Column by column sums from the bottom (8 rows a thread, then what lies below them), then row by row up to the diagonal.
         {
             const int j = tid & 63, part = tid >> 6;
-            float run = 0.f;
+            float run = 0.f, z[8];
 #pragma unroll
-            for (int x = 15; x >= 0; --x) {
-                run += Z[(16 * part + x) * 65 + j];
-                Z[(16 * part + x) * 65 + j] = run;
+            for (int x = 7; x >= 0; --x) {
+                run += Z[(8 * part + x) * 65 + j];
+                z[x] = run;
             }
+            Z[8 * part * 65 + j] = run;   // a part's sum where its first row was
             __syncthreads();
             float below = 0.f;
-            for (int q = 3; q > part; --q) below += Z[16 * q * 65 + j];
+            for (int q = 7; q > part; --q) below += Z[8 * q * 65 + j];
             __syncthreads();
-            if (part < 3) {
 #pragma unroll
-                for (int x = 0; x < 16; ++x) Z[(16 * part + x) * 65 + j] += below;
-            }
+            for (int x = 0; x < 8; ++x) Z[(8 * part + x) * 65 + j] = z[x] + below;
             __syncthreads();
-            const int t = tid >> 2, fourth = tid & 3;
+            const int t = tid >> 3, eighth = tid & 7;
             float x = 0.f;
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                const int c = 16 * fourth + e;   // a column before row t, its end's share, and a row from t on
+            for (int e = 0; e < 8; ++e) {
+                const int c = 8 * e + eighth;   // a column before row t, its end's share, and a row from t on
                 x += c < t ? Z[t * 65 + c] + share[1][c] : share[0][c];
             }
-            x += __shfl_xor_sync(kFull, x, 1);
-            x += __shfl_xor_sync(kFull, x, 2);
-            if (fourth == 0 && t < u.n) {
+#pragma unroll
+            for (int o = 1; o < 8; o *= 2) x += __shfl_xor_sync(kFull, x, o);
+            if (eighth == 0 && t < u.n) {
                 float s = 0.f;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) s += inner[e];
+                for (int e = 0; e < W::threads / 32; ++e) s += inner[e];
                 x = fmaf(vec[kC - 1], s, x);
                 const float db = diag[t] / vec[kC + t];
                 const int64_t gi = (u.b + t) * a.dg_ld + u.h, bi = (u.b + t) * a.db_ld + u.h;
@@ -1124,6 +1170,7 @@ __global__ void __launch_bounds__(256) gdr_grad_tc_kernel(const __grid_constant_
                     static_cast<float*>(a.dbeta)[bi] = db;
                 }
             }
+            __syncwarp();
         }
         // the rows' gradients: of a head's own queries and keys, or a value head's share of them in float32
         bad |= !tensor::barrier_wait(bar + 16, phase[2]);
@@ -1131,33 +1178,34 @@ __global__ void __launch_bounds__(256) gdr_grad_tc_kernel(const __grid_constant_
         tensor::fence_after();
         const float f1 = key ? -vec[i] * vec[kC + i] : a.scale * vec[i], f2 = vec[2 * kC + i];
 #pragma unroll
-        for (int p = 0; p < HC / 32; ++p) {
-            const int c0 = HC * half + 32 * p;
-            float v[32], t[32];
-            tensor::fetch32(D1 + mine + c0, v);
-            tensor::fetch32(D5 + mine + c0, t);
+        for (int p = 0; p < QC / 16; ++p) {
+            const int c0 = QC * quarter + 16 * p;
+            float v[16], t[16];
+            tensor::fetch16(D1 + mine + c0, v);
+            tensor::fetch16(D5 + mine + c0, t);
             tensor::arrived(v);
             tensor::arrived(t);
 #pragma unroll
-            for (int c = 0; c < 32; ++c) v[c] = fmaf(f1, v[c], t[c]);
+            for (int c = 0; c < 16; ++c) v[c] = fmaf(f1, v[c], t[c]);
             if (key) {   // whole warps
-                tensor::load32(D2 + mine + c0, t);
+                float x[16];
+                tensor::fetch16(D2 + mine + c0, t);
+                tensor::fetch16(D6 + mine + c0, x);
+                tensor::arrived(t);
+                tensor::arrived(x);
 #pragma unroll
-                for (int c = 0; c < 32; ++c) v[c] = fmaf(f2, t[c], v[c]);
-                tensor::load32(D6 + mine + c0, t);
-#pragma unroll
-                for (int c = 0; c < 32; ++c) v[c] += t[c];
+                for (int c = 0; c < 16; ++c) v[c] = fmaf(f2, t[c], v[c]) + x[c];
             }
             if (i < u.n && a.part != nullptr) {
                 float* const to = a.part + ((key ? a.rows : 0) + u.b + i) * a.Hv * a.dk + u.h * a.dk + c0;
 #pragma unroll
-                for (int q = 0; q < 8; ++q)
+                for (int q = 0; q < 4; ++q)
                     if (c0 + 4 * q < a.dk) *reinterpret_cast<float4*>(to + 4 * q) = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
             } else if (i < u.n) {
                 const int64_t at = key ? (u.b + i) * a.dk_ld : (u.b + i) * a.dq_ld;
                 __nv_bfloat16* const to = static_cast<__nv_bfloat16*>(key ? a.dk_out : a.dq) + at + u.h * a.dk + c0;
 #pragma unroll
-                for (int q = 0; q < 4; ++q)
+                for (int q = 0; q < 2; ++q)
                     if (c0 + 8 * q < a.dk)
                         *reinterpret_cast<uint4*>(to + 8 * q) = make_uint4(round2(v[8 * q], v[8 * q + 1]), round2(v[8 * q + 2], v[8 * q + 3]),
                                                                            round2(v[8 * q + 4], v[8 * q + 5]), round2(v[8 * q + 6], v[8 * q + 7]));
@@ -1165,13 +1213,14 @@ __global__ void __launch_bounds__(256) gdr_grad_tc_kernel(const __grid_constant_
             __syncwarp();
         }
         tensor::fence_before();
-        u = find(u.id + gridDim.x);
+        ++number;
+        u = ring[number & 3];
         kq ^= 1;
     }
     copies_wait<0>();
     if (__syncthreads_or(bad)) {   // a wait ran out: what has been written so far is not to be trusted
         if (tid == 0 && a.status != nullptr) atomicOr(a.status, SDM_DEV_STALLED);
-        for (int s = 0; s < 3; ++s) tensor::barrier_wait(bar + 8 * s, phase[s]);
+        tensor::drain(bar, 7);
         __syncthreads();
     }
     tensor::fence_after();
@@ -1226,7 +1275,10 @@ cudaError_t grad_tc(const Args& a, int64_t blocks, cudaStream_t cs) {
     auto* const k = gdr_grad_tc_kernel<DKP>;
     const cudaError_t e = big_smem(k, W::bytes);
     if (e != cudaSuccess) return e;
-    return launch_dependent(k, dim3(static_cast<unsigned>(std::min<int64_t>(blocks * a.Hv, 152))), dim3(W::threads), W::bytes, cs, a);
+    Maps m;
+    const cudaError_t f = make_maps(&m, a, a.dy, 64);
+    if (f != cudaSuccess) return f;
+    return launch_dependent(k, dim3(static_cast<unsigned>(std::min<int64_t>(blocks * a.Hv, 152))), dim3(W::threads), W::bytes, cs, a, m);
 }
 
 template <int XT, int DKP>

@@ -84,7 +84,23 @@ __device__ __forceinline__ void load32(uint32_t d, float (&v)[32]) {
     fetch32(d, v);
     arrived(v);
 }
-// The same as 16 pairs of neighbouring columns.
+// 16 columns
+__device__ __forceinline__ void fetch16(uint32_t d, float (&v)[16]) {
+    uint32_t* r = reinterpret_cast<uint32_t*>(v);
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]),
+          "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(d));
+}
+__device__ __forceinline__ void arrived(float (&v)[16]) {
+    uint32_t* r = reinterpret_cast<uint32_t*>(v);
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]),
+                   "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+                 :: "memory");
+}
+// 32 columns as 16 pairs of neighbours.
 __device__ __forceinline__ void load32(uint32_t d, uint64_t (&v)[16]) {
     float x[32];
     load32(d, x);
@@ -112,7 +128,7 @@ __device__ __forceinline__ void copy_box(uint32_t to, const void* map, int col, 
 }
 // Waits for the phase to end, for a second or so at most; false where it has not.
 __device__ __forceinline__ bool barrier_wait(uint32_t bar, uint32_t phase) {
-    for (int i = 0; i < 1 << 20; ++i) {
+    for (int i = 0; i < 1 << 18; ++i) {   // a try takes 7800 cycles
         uint32_t done;
         asm volatile(
             "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.b32 %0, 1, 0, p;\n}"
@@ -120,6 +136,14 @@ __device__ __forceinline__ bool barrier_wait(uint32_t bar, uint32_t phase) {
         if (done) return true;
     }
     return false;
+}
+
+// After a wait that ran out: waits, as long again at most, for what the barriers still expect, before memory is given back.
+__device__ __forceinline__ void drain(uint32_t bars, int n) {
+    for (int x = 0; x < n; ++x) {
+        barrier_wait(bars + 8 * x, 0);
+        barrier_wait(bars + 8 * x, 1);
+    }
 }
 
 }  // namespace tensor
