@@ -493,8 +493,14 @@ __global__ void __launch_bounds__(BV * 2) gdr_walk_kernel(const __grid_constant_
 // write without conflicts. What bounds it is this chain: with 128 columns 2300 cycles of products, then 4 turns of a barrier,
 // loads from tensor memory and the cut into terms. Tiles of K and Q arrive a block ahead, V and T while the state is brought up
 // to date, in boxes of a tensor map and bulk copies.
-template <int DKP, int BV>
-__global__ void __launch_bounds__(BV * 4) gdr_walk_tc_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps) {
+//
+// Where the walks are few and long, every sequence is cut into segments that are walked side by side, twice. A segment makes
+// M S + B of the state S before it: the first time (FIRST) blocks start from zeros for B, and others, without V, from the identity
+// for M; gdr_chain_kernel joins them to the states before the segments, from which the second walk starts. One sequence of 32769
+// rows, 8 heads of 64 x 128: 952 us whole, 420 in 16 segments.
+template <int DKP, int BV, bool FIRST>
+__global__ void __launch_bounds__(BV * 4) gdr_walk_tc_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps,
+                                                             const __grid_constant__ Segments sg) {
     using W = WalkTc<DKP, BV>;
     extern __shared__ __align__(1024) unsigned char smem[];
     __shared__ __align__(128) float vecs[2][kVecs * kC];
@@ -502,22 +508,26 @@ __global__ void __launch_bounds__(BV * 4) gdr_walk_tc_kernel(const __grid_consta
     __shared__ uint32_t tmem;
     start_dependent();
     const int tid = threadIdx.x, w = __shfl_sync(kFull, tid >> 5, 0), lane = tid & 31;
-    const int slices = (a.dv + BV - 1) / BV;
-    const int rank = blockIdx.x / (a.Hv * slices), rest = blockIdx.x - rank * a.Hv * slices;
-    const int h = rest / slices, c0 = (rest - h * slices) * BV;
+    const int own = (a.dv + BV - 1) / BV, slices = own + (FIRST ? (a.dk + BV - 1) / BV : 0), walks = sg.n - (FIRST ? 1 : 0);
+    const int rank = blockIdx.x / (a.Hv * slices * walks), rest = blockIdx.x - rank * a.Hv * slices * walks;
+    const int seg = rest / (a.Hv * slices), rest2 = rest - seg * a.Hv * slices;
+    const int h = rest2 / slices, slice = rest2 - h * slices;
+    const bool moving = FIRST && slice >= own;                       // the identity's columns
+    const int width = moving ? a.dk : a.dv, c0 = (moving ? slice - own : slice) * BV;
     const int p = by_length(a, rank), kh = h / (a.Hv / a.Hk);
     int64_t b, len;
     sequence(a, p, b, len);
     const int64_t blocks = (len + kC - 1) / kC, id0 = first_block(b, p);
     const uint32_t base = smem_of(smem), bar = smem_of(bars);
-    const int cols = min(BV, a.dv - c0), nb = (a.dv + 15) / 16 * 2;   // units of 8 value columns that are saved
+    const int64_t per = (blocks + sg.n - 1) / sg.n, j0 = min(seg * per, blocks), j1 = min(j0 + per, blocks);
+    const int cols = min(BV, width - c0), nb = (a.dv + 15) / 16 * 2;   // units of 8 value columns that are saved
 
-    const WalkLoads<DKP, BV> loads{a, maps, a.v, b, len, id0, base, smem_of(vecs), smem_of(bars) + 24, h, kh, c0, cols, tid, w};
+    const WalkLoads<DKP, BV> loads{a, maps, a.v, b, len, id0, base, smem_of(vecs), smem_of(bars) + 24, h, kh, c0, cols, tid, w, moving};
     auto load_kq = [&](int64_t j) {
-        if (j < blocks) loads.kq(j);
+        if (j < j1) loads.kq(j);
     };
     auto load_vt = [&](int64_t j) {
-        if (j < blocks) loads.vt(j);
+        if (j < j1) loads.vt(j);
     };
     // what no copy reaches is a number
     for (int i = tid; i < W::bytes / 16; i += W::threads) *reinterpret_cast<uint4*>(smem + i * 16) = make_uint4(0, 0, 0, 0);
@@ -527,19 +537,24 @@ __global__ void __launch_bounds__(BV * 4) gdr_walk_tc_kernel(const __grid_consta
     }
     async_fence();
     __syncthreads();
-    load_kq(0);
-    load_vt(0);
+    load_kq(j0);
+    load_vt(j0);
 
     const int r = 32 * (w & 3) + lane, part = w >> 2, i = r & 63;   // a row of tensor memory, 32 columns, a token
     const bool key = r < kC;
     const int vc = c0 + 32 * part;                                  // this thread's first value column
     uint64_t S[16];   // 32 columns of a row of the state, in pairs
     {
-        const float* const h0 = a.h0 == nullptr ? nullptr : a.h0 + ((static_cast<int64_t>(p) * a.Hv + h) * a.dk + r) * a.dv + vc;
+        const float* const h0 =
+            FIRST || sg.start == nullptr ? nullptr : sg.start + (((static_cast<int64_t>(p) * a.Hv + h) * sg.n + seg) * a.dk + r) * a.dv + vc;
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
             float v[4] = {};
             if (h0 != nullptr && r < a.dk && vc + 4 * q < a.dv) load4(h0 + 4 * q).get(v);
+            if (moving && r < a.dk) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] = vc + 4 * q + e == r ? 1.f : 0.f;
+            }
             S[2 * q] = pack2(v[0], v[1]);
             S[2 * q + 1] = pack2(v[2], v[3]);
         }
@@ -549,7 +564,7 @@ __global__ void __launch_bounds__(BV * 4) gdr_walk_tc_kernel(const __grid_consta
     auto put_state = [&](int64_t j) {   // S as operand, and for the backward before block j
         if (r >= DKP) return;
         put_terms(Sp, Sp + W::kS, DKP * 16, S);
-        if (a.states != nullptr && j < blocks) {
+        if (!FIRST && a.states != nullptr && j < j1) {
             unsigned char* const to = reinterpret_cast<unsigned char*>(a.states) + (((id0 + j) * a.Hv + h) * 2 * nb + vc / 8) * int64_t(DKP * 16) + r * 16;
 #pragma unroll
             for (int t = 0; t < 2; ++t)
@@ -559,7 +574,7 @@ __global__ void __launch_bounds__(BV * 4) gdr_walk_tc_kernel(const __grid_consta
                         *reinterpret_cast<uint4*>(to + (t * static_cast<int64_t>(nb) + q) * (DKP * 16)) = *reinterpret_cast<const uint4*>(Sp + t * W::kS + q * (DKP * 16));
         }
     };
-    put_state(0);
+    put_state(j0);
     if (w == 0) tensor::allocate<W::cols>(smem_of(&tmem));
     tensor::fence_before();
     __syncthreads();
@@ -573,7 +588,7 @@ __global__ void __launch_bounds__(BV * 4) gdr_walk_tc_kernel(const __grid_consta
     const uint64_t Rd = tensor::operand(base + W::R, 128, 1024);
     uint32_t phase = 0, full = 0;
     bool bad = false;
-    for (int64_t j = 0; j < blocks; ++j) {
+    for (int64_t j = j0; j < j1; ++j) {
         const uint64_t kq = static_cast<uint64_t>((j & 1) * W::kKQ) >> 4;   // the stage's distance, in a descriptor's units
         const float* const vec = vecs[j & 1];
         bad |= !tensor::barrier_wait(bar + 24 + 8 * (j & 1), full >> (j & 1) & 1);
@@ -654,7 +669,7 @@ __global__ void __launch_bounds__(BV * 4) gdr_walk_tc_kernel(const __grid_consta
         const int64_t r0 = b + j * kC;
         const int n = static_cast<int>(min(len - j * kC, int64_t(kC)));
         if (key) {
-            if (a.states != nullptr) {   // the writes, for the backward
+            if (!FIRST && a.states != nullptr) {   // the writes, for the backward
                 unsigned char* const to = reinterpret_cast<unsigned char*>(a.writes) + (((id0 + j) * a.Hv + h) * 2 * nb + vc / 8) * int64_t(1024) + i * 16;
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
@@ -666,7 +681,7 @@ __global__ void __launch_bounds__(BV * 4) gdr_walk_tc_kernel(const __grid_consta
                     *reinterpret_cast<uint4*>(to + (nb + q) * 1024) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                 }
             }
-        } else if (i < n) {   // the row's answer
+        } else if (!FIRST && i < n) {   // the row's answer
             __nv_bfloat16* const y = static_cast<__nv_bfloat16*>(a.y) + (r0 + i) * a.y_ld + h * a.dv + vc;
             const uint64_t f = pack2(a.scale * eg, a.scale * eg);
 #pragma unroll
@@ -693,11 +708,14 @@ __global__ void __launch_bounds__(BV * 4) gdr_walk_tc_kernel(const __grid_consta
         put_state(j + 1);
         tensor::fence_before();
     }
-    if (a.hT != nullptr && r < a.dk) {
-        float* const hT = a.hT + ((static_cast<int64_t>(p) * a.Hv + h) * a.dk + r) * a.dv + vc;
+    const int64_t head = static_cast<int64_t>(p) * a.Hv + h;
+    float* to = nullptr;
+    if (FIRST) to = moving ? sg.move + (head * walks + seg) * a.dk * a.dk : sg.start + (head * sg.n + seg + 1) * a.dk * a.dv;
+    else if (a.hT != nullptr && seg == sg.n - 1) to = a.hT + head * a.dk * a.dv;
+    if (to != nullptr && r < a.dk) {
 #pragma unroll
         for (int q = 0; q < 8; ++q)
-            if (vc + 4 * q < a.dv) st4(hT + 4 * q, Quad{S[2 * q], S[2 * q + 1]});
+            if (vc + 4 * q < width) st4(to + static_cast<int64_t>(r) * width + vc + 4 * q, Quad{S[2 * q], S[2 * q + 1]});
     }
     copies_wait<0>();
     if (__syncthreads_or(bad)) {
@@ -707,6 +725,74 @@ __global__ void __launch_bounds__(BV * 4) gdr_walk_tc_kernel(const __grid_consta
     }
     tensor::fence_after();
     if (w == 0) tensor::release<W::cols>(tmem);
+}
+
+// The states before a sequence's segments, one after another: S' = M S + B in float32, 32 value columns a block. Rows of M are read
+// by whole warps at once; the next M is on its way meanwhile.
+__global__ void __launch_bounds__(256) gdr_chain_kernel(const __grid_constant__ Args a, const __grid_constant__ Segments sg) {
+    extern __shared__ __align__(1024) unsigned char smem[];
+    start_dependent();
+    const int slices = (a.dv + 31) / 32, tid = threadIdx.x, c = tid & 31, w = tid >> 5;
+    const int64_t head = blockIdx.x / slices;
+    const int col = (static_cast<int>(blockIdx.x - head * slices)) * 32 + c;
+    const bool there = col < a.dv;
+    float* const M = reinterpret_cast<float*>(smem);                 // two of [dk][dk]
+    float* const S = M + 2 * a.dk * a.dk;                            // [dk][32]
+    const int64_t size = static_cast<int64_t>(a.dk) * a.dv;
+    float* const start = sg.start + head * sg.n * size;
+    const float* const move = sg.move + head * (sg.n - 1) * a.dk * a.dk;
+    auto load = [&](int s) {
+        if (s < sg.n - 1)
+            for (int i = tid * 4; i < a.dk * a.dk; i += 1024)
+                copy16(smem_of(M + (s & 1) * a.dk * a.dk + i), move + static_cast<int64_t>(s) * a.dk * a.dk + i, true);
+        copies_commit();
+    };
+    load(0);
+    for (int r = w; r < a.dk; r += 8) {
+        const float x = a.h0 != nullptr && there ? a.h0[head * size + static_cast<int64_t>(r) * a.dv + col] : 0.f;
+        S[r * 32 + c] = x;
+        if (there) start[static_cast<int64_t>(r) * a.dv + col] = x;
+    }
+    float x[16], ahead[16];   // rows w, w + 8 ..: dk is a multiple of 8
+    auto fetch = [&](int s) {
+        const float* const from = start + s * size;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) ahead[i] = s < sg.n && 8 * i < a.dk && there ? from[static_cast<int64_t>(w + 8 * i) * a.dv + col] : 0.f;
+    };
+    fetch(1);
+    for (int s = 0; s + 1 < sg.n; ++s) {
+        load(s + 1);
+        float* const next = start + (s + 1) * size;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x[i] = ahead[i];
+        fetch(s + 2);
+        copies_wait<1>();
+        __syncthreads();
+        const float* const m = M + (s & 1) * a.dk * a.dk + w * a.dk;
+#pragma unroll 2
+        for (int k = 0; k < a.dk; k += 4) {
+            float y[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) y[e] = S[(k + e) * 32 + c];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                if (8 * i >= a.dk) continue;
+                const float4 f = *reinterpret_cast<const float4*>(m + 8 * i * a.dk + k);
+                x[i] = fmaf(f.x, y[0], x[i]);
+                x[i] = fmaf(f.y, y[1], x[i]);
+                x[i] = fmaf(f.z, y[2], x[i]);
+                x[i] = fmaf(f.w, y[3], x[i]);
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            if (8 * i >= a.dk) continue;
+            S[(w + 8 * i) * 32 + c] = x[i];
+            if (there) next[static_cast<int64_t>(w + 8 * i) * a.dv + col] = x[i];
+        }
+    }
+    copies_wait<0>();
 }
 
 // ---- one token of every request -----------------------------------------------------------------------------------
@@ -849,26 +935,62 @@ cudaError_t walk(const Args& a, cudaStream_t cs) {
     return launch_dependent(k, dim3(static_cast<unsigned>(grid)), dim3(W::threads), bytes, cs, a);
 }
 
-template <int DKP, int BV>
-cudaError_t walk_tc(const Args& a, cudaStream_t cs) {
+template <int DKP, int BV, bool FIRST>
+cudaError_t walk_tc(const Args& a, const Segments& sg, cudaStream_t cs) {
     using W = WalkTc<DKP, BV>;
-    auto* const k = gdr_walk_tc_kernel<DKP, BV>;
-    const cudaError_t e = big_smem(k, W::bytes);
+    auto* const k = gdr_walk_tc_kernel<DKP, BV, FIRST>;
+    cudaError_t e = big_smem(k, W::bytes);
     if (e != cudaSuccess) return e;
-    const int64_t grid = static_cast<int64_t>(a.P) * a.Hv * ((a.dv + BV - 1) / BV);
+    const int64_t grid = static_cast<int64_t>(a.P) * a.Hv * (FIRST ? (sg.n - 1) * ((a.dv + BV - 1) / BV + (a.dk + BV - 1) / BV) : sg.n * ((a.dv + BV - 1) / BV));
     Maps m;
-    const cudaError_t f = make_maps(&m, a, a.v, BV);
-    if (f != cudaSuccess) return f;
-    return launch_dependent(k, dim3(static_cast<unsigned>(grid)), dim3(W::threads), W::bytes, cs, a, m);
+    e = make_maps(&m, a, a.v, BV);
+    if (e != cudaSuccess) return e;
+    return launch_dependent(k, dim3(static_cast<unsigned>(grid)), dim3(W::threads), W::bytes, cs, a, m, sg);
+}
+
+template <int DKP, bool FIRST>
+cudaError_t walk_tc(const Args& a, const Segments& sg, cudaStream_t cs) {
+    const int64_t walks = static_cast<int64_t>(a.P) * a.Hv * (FIRST ? sg.n - 1 : sg.n);
+    switch (columns(walks, a.dv, FIRST ? a.dk : 0)) {
+        case 32: return walk_tc<DKP, 32, FIRST>(a, sg, cs);
+        case 64: return walk_tc<DKP, 64, FIRST>(a, sg, cs);
+        default: return walk_tc<DKP, 128, FIRST>(a, sg, cs);
+    }
 }
 
 template <int DKP>
-cudaError_t walk_bf16(const Args& a, cudaStream_t cs) {
-    switch (columns(a)) {
-        case 32: return walk_tc<DKP, 32>(a, cs);
-        case 64: return walk_tc<DKP, 64>(a, cs);
-        default: return walk_tc<DKP, 128>(a, cs);
+cudaError_t walk_bf16(const Args& a, const Segments& sg, cudaStream_t cs) {
+    if (sg.n > 1) {
+        cudaError_t e = walk_tc<DKP, true>(a, sg, cs);
+        if (e != cudaSuccess) return e;
+        const int smem = (2 * a.dk * a.dk + a.dk * 32) * 4;
+        e = big_smem(gdr_chain_kernel, smem);
+        if (e == cudaSuccess)
+            e = launch_dependent(gdr_chain_kernel, dim3(static_cast<unsigned>(a.P * a.Hv * ((a.dv + 31) / 32))), dim3(256), smem, cs, a, sg);
+        if (e != cudaSuccess) return e;
     }
+    return walk_tc<DKP, false>(a, sg, cs);
+}
+
+// Segments of a sequence's walk, of 16 blocks of rows each at least: two walks of a segment and the chain's 4.5 us a segment and 10
+// against one walk of all rows (columns(), a fifth on top for what that leaves out). Measured, heads of 128 but for the first: one
+// sequence of 4096 rows, 2 heads of 64, 80 us in 4 segments and 110 whole; 32768 rows, 4 heads, 374 in 16 and 931 whole; 4096 rows, 16
+// heads, 163 in 4 and 140 whole; 2 of 8192, 16 heads, 494 in 4 and 330 whole.
+int segments(const sdm_gdr_shape* s) {
+    const int64_t walks = static_cast<int64_t>(s->P) * s->v_heads, blocks = s->rows / s->P / kC;
+    if (s->x_dtype != SDM_BF16 || walks > 152) return 1;
+    int best = 1;
+    int64_t whole, first, second;   // in 0.01 us
+    columns(walks, s->dv, 0, &whole);
+    int64_t least = whole * blocks * 36;
+    for (int n : {4, 8, 16}) {
+        if (blocks < 16 * n) break;
+        columns(walks * (n - 1), s->dv, s->dk, &first);
+        columns(walks * n, s->dv, 0, &second);
+        const int64_t t = ((first + second) * ((blocks + n - 1) / n) * 36 + n * 450 + 1000) * 6 / 5;
+        if (t < least) best = n, least = t;
+    }
+    return best;
 }
 
 }  // namespace
@@ -905,6 +1027,10 @@ Layout layout(const sdm_gdr_shape* s, bool backward) {
     if (!backward) {   // from the end on they are read where the forward saved them
         l.tri = take(heads * tri_bytes(s));
         l.vec = take(heads * kVecBytes);
+    }
+    if (const int n = segments(s); n > 1) {
+        l.start = take(static_cast<int64_t>(s->P) * s->v_heads * n * s->dk * s->dv * 4);
+        l.move = take(static_cast<int64_t>(s->P) * s->v_heads * (n - 1) * s->dk * s->dk * 4);
     }
     if (f32) {
         l.q = take(s->rows * s->k_heads * s->dk * 6);
@@ -1053,7 +1179,13 @@ extern "C" sdm_status sdm_gdr_forward(const sdm_gdr_shape* shape, const void* q,
     }
     const bool narrow = padded(shape->dk) == 64;
     if (e == cudaSuccess) {
-        if (shape->x_dtype == SDM_BF16) e = narrow ? walk_bf16<64>(a, cs) : walk_bf16<128>(a, cs);
+        Segments sg = {segments(shape), const_cast<float*>(h0), nullptr};
+        if (sg.n > 1) {
+            const Layout l = layout(shape, false);
+            sg.start = reinterpret_cast<float*>(static_cast<unsigned char*>(ws) + l.start);
+            sg.move = reinterpret_cast<float*>(static_cast<unsigned char*>(ws) + l.move);
+        }
+        if (shape->x_dtype == SDM_BF16) e = narrow ? walk_bf16<64>(a, sg, cs) : walk_bf16<128>(a, sg, cs);
         else e = narrow ? walk<3, 64, 32>(a, cs) : walk<3, 128, 32>(a, cs);
     }
     return e == cudaSuccess ? SDM_OK : SDM_ERR_CUDA;

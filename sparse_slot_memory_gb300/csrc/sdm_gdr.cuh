@@ -82,6 +82,13 @@ struct Maps {
     int boxes;             // whether they serve: heads of 64 or 128 columns, rows apart from one another
 };
 
+// Segments of every sequence that are walked side by side (columns of bfloat16 rows' states): n of them, and what they need.
+struct Segments {
+    int n;
+    float* start;   // [P][Hv][n][dk][dv]: the states before them (n = 1: h0, nullable)
+    float* move;    // [P][Hv][n - 1][dk][dk]: what they make of a state that they start from, beside what they write
+};
+
 // The rows [b, b + n) of sequence p. Offsets that are not ascending within [0, rows] are cut to it and reported.
 __device__ __forceinline__ void sequence(const Args& a, int p, int64_t& b, int64_t& n) {
     if (a.offsets == nullptr) {
@@ -385,6 +392,7 @@ struct WalkLoads {
     int64_t b, len, id0;
     uint32_t base, vecs, bar;   // bar: of [K; Q]'s two stages, and of V and T
     int h, kh, c0, cols, tid, warp;
+    bool empty;                 // V is zero
     __device__ __forceinline__ int rows_of(int64_t j) const { return static_cast<int>(min(len - j * kC, int64_t(kC))); }
     __device__ __forceinline__ bool boxed(int64_t j) const { return m.boxes && rows_of(j) == kC; }
     __device__ __forceinline__ int first() const { return BV < 64 ? c0 >> 3 & 4 : 0; }   // the block's first unit of its box
@@ -417,7 +425,7 @@ struct WalkLoads {
     }
     __device__ __forceinline__ void vt(int64_t j) const {
         const uint32_t full = bar + 16;
-        const bool box = boxed(j);
+        const bool box = boxed(j) && !empty;
         if (warp == 1 && tensor::elect()) {
             tensor::barrier_expect(full, W::kT + (box ? W::kV : 0));
             tensor::copy_bulk(base + W::T, a.tri + ((id0 + j) * a.Hv + h) * (W::kT / 2), W::kT, full);
@@ -427,7 +435,7 @@ struct WalkLoads {
                     tensor::copy_box(base + W::V + x * 8192, &m.v, h * a.dv + (c0 & ~63) + x * 64, static_cast<int>(b + j * kC), full);
             }
         }
-        if (!box) {
+        if (!box && !empty) {
             const int n = rows_of(j);
             for (int i = tid; i < kC * (BV / 8); i += W::threads) {
                 const int r = i / (BV / 8), u = i % (BV / 8);
@@ -443,17 +451,19 @@ struct WalkLoads {
 inline int padded(int d) { return d <= 64 ? 64 : 128; }
 inline int64_t blocks_of(const sdm_gdr_shape* s) { return s->rows / kC + s->P; }
 
-// Value columns of a block of a walk of bfloat16 rows. A block of rows took 1.8 us with 32, 2.1 with 64 and 3.6 with 128 columns
-// (keys of 64), and the SMs hold one block each: the fewest rounds of the grid times that. 12 prompts of 16 heads of 128 took 294 us
-// with 64 and 402 with 128, 8 of 4096 rows 380 with 64 and 349 with 128, one of 8 heads 952 with 32 and 1143 with 64.
-inline int columns(const Args& a) {
+// Value columns of a block of a walk of bfloat16 rows, of `heads` walks of dv (and dk, for a segment's move) columns. A block of rows
+// took 1.8 us with 32, 2.1 with 64 and 3.6 with 128 columns (keys of 64), and the SMs hold one block each: the fewest rounds of the
+// grid times that (`time`, in 0.36 us a block of rows). 12 prompts of 16 heads of 128 took 294 us with 64 and 402 with 128, 8 of 4096 rows 380 with 64 and 349 with 128,
+// one of 8 heads 952 with 32 and 1143 with 64.
+inline int columns(int64_t heads, int dv, int dk = 0, int64_t* time = nullptr) {
     int best = 32;
     int64_t least = INT64_MAX;
     for (const auto& [bv, cost] : {std::pair{128, 10}, {64, 6}, {32, 5}}) {
-        if (bv > 32 && a.dv <= bv / 2) continue;
-        const int64_t grid = static_cast<int64_t>(a.P) * a.Hv * ((a.dv + bv - 1) / bv), t = (grid + 151) / 152 * cost;
+        if (bv > 32 && dv <= bv / 2) continue;
+        const int64_t grid = heads * ((dv + bv - 1) / bv + (dk + bv - 1) / bv), t = (grid + 151) / 152 * cost;
         if (t < least) best = bv, least = t;
     }
+    if (time != nullptr) *time = least;
     return best;
 }
 inline sdm_status check_array(const void* p, int64_t ld, int64_t n, int elem, int align, bool out) {
@@ -465,7 +475,7 @@ inline sdm_status check_array(const void* p, int64_t ld, int64_t n, int elem, in
 
 // The workspace's parts in bytes from its start
 struct Layout {
-    int64_t tri, vec, q, k, v, dy, dstates, du, part, bytes;
+    int64_t tri, vec, q, k, v, start, move, dy, dstates, du, part, bytes;
 };
 inline int terms(const sdm_gdr_shape* s) { return s->x_dtype == SDM_F32 ? 3 : 2; }   // of what is computed
 sdm_status check_shape(const sdm_gdr_shape* s);

@@ -252,7 +252,7 @@ __global__ void __launch_bounds__(BV * 4) gdr_back_tc_kernel(const __grid_consta
     const uint32_t base = smem_of(smem), bar = smem_of(bars);
     const int cols = min(BV, a.dv - c0), nb = (a.dv + 15) / 16 * 2;
 
-    const WalkLoads<DKP, BV> loads{a, maps, a.dy, b, len, id0, base, smem_of(vecs), smem_of(bars) + 24, h, kh, c0, cols, tid, w};
+    const WalkLoads<DKP, BV> loads{a, maps, a.dy, b, len, id0, base, smem_of(vecs), smem_of(bars) + 24, h, kh, c0, cols, tid, w, false};
     auto load_kq = [&](int64_t j) {
         if (j >= 0) loads.kq(j);
     };
@@ -1306,7 +1306,7 @@ cudaError_t back_tc(const Args& a, cudaStream_t cs) {
 
 template <int DKP>
 cudaError_t back_bf16(const Args& a, cudaStream_t cs) {
-    switch (columns(a)) {
+    switch (columns(static_cast<int64_t>(a.P) * a.Hv, a.dv)) {
         case 32: return back_tc<DKP, 32>(a, cs);
         case 64: return back_tc<DKP, 64>(a, cs);
         default: return back_tc<DKP, 128>(a, cs);

@@ -12,6 +12,9 @@ include/sdm.h states gives them, relative to the square root of sum a^2 b^2 for 
 Within a block of 64 rows the variances are followed through the block's formulas. Across blocks an error of the state is not
 amplified: with keys no longer than 1 and strengths in [0, 1] every step S -> e^g (I - beta k k^T) S shortens each of its columns,
 so the variances of a column's errors add up, and a row takes at most its own length times their root.
+A sequence walked in segments (not `whole`) has each segment's matrix from walking the identity. Every block rounds its columns, no
+longer than 1, as it rounds a state's: what the matrix then makes of the state before the segment is off by a variance of eta times
+that state's squared lengths for every block (its writes' operands once, its state's once).
 """
 
 from __future__ import annotations
@@ -61,7 +64,7 @@ def backward(q, k, v, g, beta, states, E, scale, dy, dS):
     return d, behind
 
 
-def bounds(q, k, v, g, beta, states, E, scale, dy, behind, dev):
+def bounds(q, k, v, g, beta, states, E, scale, dy, behind, dev, whole=True):
     """The bounds of a head's outputs, block by block: forwards for the states, backwards for their gradients. v..: variances,
     ..2: squares."""
     n = len(q)
@@ -70,6 +73,7 @@ def bounds(q, k, v, g, beta, states, E, scale, dy, behind, dev):
     t = {name: np.zeros_like(x) for name, x in (("y", v), ("dq", q), ("dk", k), ("dv", v), ("dg", g), ("dbeta", g))}
     blocks = []
     vS = np.zeros(v.shape[1])   # of the columns of the state
+    peak = np.zeros(v.shape[1])   # their largest squared lengths so far
     for r in range(0, n, C):
         s = slice(r, min(r + C, n))
         K, Q, V, S = k[s], q[s], v[s], states[r]
@@ -91,6 +95,9 @@ def bounds(q, k, v, g, beta, states, E, scale, dy, behind, dev):
         blocks.append(dict(s=s, S=S, S2=S2, K=K, Q=Q, K2=K2, Q2=Q2, nk=nk, nq=nq, b=b, D=D, eg=eg, ec=ec, G=G, A=A, vG=vG, vA=vA, T=T, vT=vT,
                            u=u, vU=vU, vS=vS))
         vS = vS + (K2.T @ (ec ** 2 * (vU + eta * u ** 2)) + eta * states[s.stop] ** 2).sum(0)
+        peak = np.maximum(peak, S2.sum(0))
+        if not whole:
+            vS = vS + 2 * eta * peak
     t["hT"] = vS[None, :] + np.zeros_like(states[0])
     if dy is not None:
         vD = np.zeros(v.shape[1])
@@ -133,7 +140,7 @@ def bounds(q, k, v, g, beta, states, E, scale, dy, behind, dev):
     return {name: 6 * x ** 0.5 for name, x in t.items()}
 
 
-def oracle(x, cuts, scale, x_dtype, train=True):
+def oracle(x, cuts, scale, x_dtype, train=True, whole=True):
     """x: float64 arrays q, k [rows, Hk, dk], v [rows, Hv, dv], g, beta [rows, Hv], h0 [P, Hv, dk, dv] (dy, dhT): the outputs'
     values and bounds, as the calls lay them out; rows of no sequence NaN."""
     Hk, Hv = x["k"].shape[1], x["v"].shape[1]
@@ -159,7 +166,7 @@ def oracle(x, cuts, scale, x_dtype, train=True):
                 dy = x["dy"][s, h]
                 d, behind = backward(*a, states, E, scale, dy, x["dhT"][p, h])
                 val["dh0"][p, h] = behind[0]
-            b = bounds(*a, states, E, scale, dy, behind, dev)
+            b = bounds(*a, states, E, scale, dy, behind, dev, whole)
             tol["y"][s, h], tol["hT"][p, h] = b["y"], b["hT"]
             if train:
                 tol["dh0"][p, h] = b["dh0"]

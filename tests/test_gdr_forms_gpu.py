@@ -31,6 +31,46 @@ def test_forms(name):
     compare(c, run(c))
 
 
+SEGMENTS = {
+    # few heads of long sequences, whose rows are walked in segments: boxes and copies by hand, tails, a sequence of fewer blocks than
+    # segments and none, blocks of other sequences' lengths
+    "boxes": dict(lens=[4160], Hk=1, Hv=2, dk=64, dv=128), "wide": dict(lens=[4096], dk=128, dv=64), "narrow": dict(lens=[4131], Hk=1, Hv=2, dk=24, dv=40),
+    "ragged": dict(lens=[3, 9000, 0, 7500, 130], dk=64, dv=64), "no_state": dict(lens=[8300], dk=32, dv=32, state=False, gt="bf16"),
+    "slow": dict(lens=[4200], dk=64, dv=64, rate=0.003), "outside": dict(lens=[5000], dk=16, dv=8, before=70, behind=9),
+}
+
+
+@pytest.mark.parametrize("name", list(SEGMENTS))
+def test_segments(name):
+    c = case(**SEGMENTS[name])
+    compare(c, run(c), whole=False)
+
+
+def test_segments_with_states_in_place_and_gates_that_start_anew():
+    c = case([4400], Hv=2, dk=64, dv=64)
+    c["g"][700:710, 0] = -float("inf")
+    c["g"][2111, :] = -float("inf")
+    want = run(c, False)
+    compare(c, want, False, whole=False)
+    h, y, s = c["h0"].clone(), torch.empty_like(c["v"]), c["spec"]
+    sdm.gdr_forward(s, *[c[n] for n in ("q", "k", "v", "g", "beta")], y, sdm.alloc_gdr_workspace(s, backward=False), h0=h, hT=h)
+    assert torch.equal(h, want["hT"]) and torch.equal(y, want["y"])
+
+
+def test_segments_keep_what_is_before_a_nan():
+    """A value that is not finite spoils what follows it, across segments, and nothing before its block nor another head's."""
+    c = case([4400], Hk=2, Hv=2, dk=64, dv=64)
+    want = run(c, False)
+    for name, at in (("v", 2500), ("k", 2500)):
+        d = dict(c) | {name: c[name].clone()}
+        d[name][at, 0, 3] = float("nan")
+        got = run(d, False)
+        block = at // 64 * 64
+        assert torch.equal(got["y"][:block], want["y"][:block]) and torch.equal(got["y"][:, 1], want["y"][:, 1])
+        assert torch.equal(got["hT"][:, 1], want["hT"][:, 1])
+        assert bool(got["y"][at + 64:, 0].isnan().any(1).all()) and bool(got["hT"][0, 0].isnan().any())
+
+
 @pytest.mark.parametrize("xt", ["bf16", "f32"])
 def test_rows_that_repeat(xt):
     """Inputs with a distance of 0 between rows are one row for all."""
@@ -84,10 +124,10 @@ def test_past_2_31_elements(xt):
     x = [view[n] for n in ("q", "k", "v", "g", "beta")]
     sdm.gdr_forward(s, *x, view["y"], ws, offsets=offsets, states=states)
     sdm.gdr_backward(s, *x, view["dy"], states, *[view[n] for n in ("dq", "dk", "dv", "dg", "dbeta")], ws, offsets=offsets)
-    want = run(c)
-    for n in ("y", "dq", "dk", "dv", "dg", "dbeta"):
-        assert torch.equal(view[n][rows - tail:], want[n]), n
-        assert not view[n][:rows - tail].any(), n
+    got = {n: view[n] for n in ("y", "dq", "dk", "dv", "dg", "dbeta")}
+    compare(c, {n: t[rows - tail:] for n, t in got.items()}, whole=False)   # in segments, as the rows of all sequences suggest them
+    for n, t in got.items():
+        assert not t[:rows - tail].any(), n
 
 
 def test_step_of_a_table_past_2_31_elements():

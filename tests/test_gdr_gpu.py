@@ -77,12 +77,12 @@ def run(c, train=True):
     return r
 
 
-def compare(c, r, train=True):
+def compare(c, r, train=True, whole=True):
     s = c["spec"]
     x = {n: f64(c[n]) for n in ("q", "k", "v", "g", "beta", "dy")}
     for n in ("h0", "dhT"):
         x[n] = f64(c[n]) if c[n] is not None else np.zeros((s.P, s.v_heads, s.dk, s.dv))
-    val, tol = oracle(x, c["cuts"], s.scale, s.x_dtype, train)
+    val, tol = oracle(x, c["cuts"], s.scale, s.x_dtype, train, whole)
     types = {"y": s.x_dtype, "dq": s.x_dtype, "dk": s.x_dtype, "dv": s.x_dtype, "dg": s.g_dtype, "dbeta": s.g_dtype}
     for n in r:
         check(n, r[n], val[n], tol[n], DT[types.get(n, "f32")])
