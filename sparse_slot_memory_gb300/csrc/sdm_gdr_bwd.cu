@@ -792,9 +792,11 @@ __global__ void __launch_bounds__(512) gdr_grad_kernel(const __grid_constant__ A
 // so a thread that has row r of tensor memory has row r of the key's side (r < 64) or row r - 64 of the query's, and a quarter of its
 // columns. Resident blocks take (block of rows, head) after (block, head); the next ones' rows and states arrive, two slices of 32
 // value columns ahead, while these are finished. Its floor is HBM: 272 KB a block of a head of 128, of which the states are 128 (6.7
-// us on each of 152 SMs; measured 13.2). What bounds it is one chain of a block: shared memory is read by the products for half of
-// a slice (a product of 128 x 128 x 16 takes as long as its operands take to be read), and a block's sums fill tensor memory, so
-// the next block's products wait for these to be taken in.
+// us on each of 152 SMs; measured 11.5). What bounds it is the chain of a block's phases: four slices of copies, products (1400
+// cycles, in which shared memory is read all the time) and <dS', S>; the decays; then the gates' gradients beside the rows'. A
+// block's sums fill tensor memory, so the next block's products wait until these are taken in. Left out one at a time, <dS', S> was
+// worth 36 us of 725, the sums with queries and keys 19, the slices' products 50; the gates' gradients 118 and the rows' 147 before
+// half of the warps took each and the rows left through shared memory (630).
 template <int DKP>
 struct GradTc {
     // a slice: U's two terms, [W; dY], [W's rests; 0], S's and dS's two terms, all in units of 8 value columns
@@ -930,7 +932,7 @@ __global__ void __launch_bounds__(512, 1) gdr_grad_tc_kernel(const __grid_consta
     const uint32_t mine = static_cast<uint32_t>(w & 3) << 21;   // this warp's 32 rows
     const int r = 32 * (w & 3) + lane, quarter = w >> 2, i = r & 63;
     const bool key = r < kC;                                    // the key's side
-    uint32_t phase[3] = {};
+    uint32_t phase[2] = {};
     int64_t waited[2] = {}, step = 0, number = 0;   // steps whose products were waited for, by stage; slices and units that are through
     bool bad = false;
     int kq = 0;
@@ -1123,39 +1125,42 @@ __global__ void __launch_bounds__(512, 1) gdr_grad_tc_kernel(const __grid_consta
             if (lane == 0) inner[w] = s;
         }
         __syncthreads();
-        if (tid < kC) {
-            const float eg = vec[tid];
-            auto four = [&](int x) { return (sums[x][0][tid] + sums[x][1][tid]) + (sums[x][2][tid] + sums[x][3][tid]); };
-            share[0][tid] = eg * (a.scale * four(0) - vec[kC + tid] * four(1));
-            share[1][tid] = vec[2 * kC + tid] * four(2);
-        }
-        // dg. Column by column sums from the bottom (8 rows a thread, then what lies below them), then row by row up to the diagonal.
-        {
-            const int j = tid & 63, part = tid >> 6;
-            float run = 0.f, z[8];
+        // Half of the warps write dg and dbeta, the others meanwhile the rows' gradients.
+        if (quarter >= 2) {
+            const int g = tid - 256;
+            auto sync = [&]() { asm volatile("bar.sync 1, 256;" ::: "memory"); };
+            if (g < kC) {
+                const float eg = vec[g];
+                auto four = [&](int x) { return (sums[x][0][g] + sums[x][1][g]) + (sums[x][2][g] + sums[x][3][g]); };
+                share[0][g] = eg * (a.scale * four(0) - vec[kC + g] * four(1));
+                share[1][g] = vec[2 * kC + g] * four(2);
+            }
+            // Column by column sums from the bottom (16 rows a thread, then what lies below them), then row by row up to the diagonal.
+            const int j = g & 63, part = g >> 6;
+            float run = 0.f, z[16];
 #pragma unroll
-            for (int x = 7; x >= 0; --x) {
-                run += Z[(8 * part + x) * 65 + j];
+            for (int x = 15; x >= 0; --x) {
+                run += Z[(16 * part + x) * 65 + j];
                 z[x] = run;
             }
-            Z[8 * part * 65 + j] = run;   // a part's sum where its first row was
-            __syncthreads();
+            Z[16 * part * 65 + j] = run;   // a part's sum where its first row was
+            sync();
             float below = 0.f;
-            for (int q = 7; q > part; --q) below += Z[8 * q * 65 + j];
-            __syncthreads();
+            for (int q = 3; q > part; --q) below += Z[16 * q * 65 + j];
+            sync();
 #pragma unroll
-            for (int x = 0; x < 8; ++x) Z[(8 * part + x) * 65 + j] = z[x] + below;
-            __syncthreads();
-            const int t = tid >> 3, eighth = tid & 7;
+            for (int x = 0; x < 16; ++x) Z[(16 * part + x) * 65 + j] = z[x] + below;
+            sync();
+            const int t = g >> 2, fourth = g & 3;
             float x = 0.f;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int c = 8 * e + eighth;   // a column before row t, its end's share, and a row from t on
+            for (int e = 0; e < 16; ++e) {
+                const int c = 4 * e + fourth;   // a column before row t, its end's share, and a row from t on
                 x += c < t ? Z[t * 65 + c] + share[1][c] : share[0][c];
             }
-#pragma unroll
-            for (int o = 1; o < 8; o *= 2) x += __shfl_xor_sync(kFull, x, o);
-            if (eighth == 0 && t < u.n) {
+            x += __shfl_xor_sync(kFull, x, 1);
+            x += __shfl_xor_sync(kFull, x, 2);
+            if (fourth == 0 && t < u.n) {
                 float s = 0.f;
 #pragma unroll
                 for (int e = 0; e < W::threads / 32; ++e) s += inner[e];
@@ -1171,44 +1176,60 @@ __global__ void __launch_bounds__(512, 1) gdr_grad_tc_kernel(const __grid_consta
                 }
             }
             __syncwarp();
-        }
-        // the rows' gradients: of a head's own queries and keys, or a value head's share of them in float32
-        bad |= !tensor::barrier_wait(bar + 16, phase[2]);
-        phase[2] ^= 1;
-        tensor::fence_after();
-        const float f1 = key ? -vec[i] * vec[kC + i] : a.scale * vec[i], f2 = vec[2 * kC + i];
+        } else {
+            // of a head's own queries and keys, or a value head's share of them in float32
+            bad |= !tensor::barrier_wait(bar + 16, static_cast<uint32_t>(number) & 1);
+            tensor::fence_after();
+            const float f1 = key ? -vec[i] * vec[kC + i] : a.scale * vec[i], f2 = vec[2 * kC + i];
 #pragma unroll
-        for (int p = 0; p < QC / 16; ++p) {
-            const int c0 = QC * quarter + 16 * p;
-            float v[16], t[16];
-            tensor::fetch16(D1 + mine + c0, v);
-            tensor::fetch16(D5 + mine + c0, t);
-            tensor::arrived(v);
-            tensor::arrived(t);
+            for (int p = 0; p < DKP / 32; ++p) {
+                const int c0 = DKP / 2 * quarter + 16 * p;
+                float v[16], t[16];
+                tensor::fetch16(D1 + mine + c0, v);
+                tensor::fetch16(D5 + mine + c0, t);
+                if (key) {   // whole warps
+                    float x[16], y[16];
+                    tensor::fetch16(D2 + mine + c0, x);
+                    tensor::fetch16(D6 + mine + c0, y);
+                    tensor::arrived(x);
+                    tensor::arrived(y);
+                    tensor::arrived(v);
+                    tensor::arrived(t);
 #pragma unroll
-            for (int c = 0; c < 16; ++c) v[c] = fmaf(f1, v[c], t[c]);
-            if (key) {   // whole warps
-                float x[16];
-                tensor::fetch16(D2 + mine + c0, t);
-                tensor::fetch16(D6 + mine + c0, x);
-                tensor::arrived(t);
-                tensor::arrived(x);
+                    for (int c = 0; c < 16; ++c) v[c] = fmaf(f2, x[c], fmaf(f1, v[c], t[c])) + y[c];
+                } else {
+                    tensor::arrived(v);
+                    tensor::arrived(t);
 #pragma unroll
-                for (int c = 0; c < 16; ++c) v[c] = fmaf(f2, t[c], v[c]) + x[c];
+                    for (int c = 0; c < 16; ++c) v[c] = fmaf(f1, v[c], t[c]);
+                }
+                if (a.part != nullptr) {
+                    float* const to = a.part + ((key ? a.rows : 0) + u.b + i) * a.Hv * a.dk + u.h * a.dk + c0;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        if (i < u.n && c0 + 4 * q < a.dk)
+                            *reinterpret_cast<float4*>(to + 4 * q) = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+                } else {   // over K and Q, which nobody needs any more, to leave in whole rows
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        const int un = c0 / 8 + q;
+                        *reinterpret_cast<uint4*>(smem + kq * W::kKQ + (un >> 3) * 16384 + swizzled_at(r, un & 7)) =
+                            make_uint4(round2(v[8 * q], v[8 * q + 1]), round2(v[8 * q + 2], v[8 * q + 3]), round2(v[8 * q + 4], v[8 * q + 5]),
+                                       round2(v[8 * q + 6], v[8 * q + 7]));
+                    }
+                }
             }
-            if (i < u.n && a.part != nullptr) {
-                float* const to = a.part + ((key ? a.rows : 0) + u.b + i) * a.Hv * a.dk + u.h * a.dk + c0;
+            if (a.part == nullptr) {
+                asm volatile("bar.sync 2, 256;" ::: "memory");
 #pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    if (c0 + 4 * q < a.dk) *reinterpret_cast<float4*>(to + 4 * q) = make_float4(v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
-            } else if (i < u.n) {
-                const int64_t at = key ? (u.b + i) * a.dk_ld : (u.b + i) * a.dq_ld;
-                __nv_bfloat16* const to = static_cast<__nv_bfloat16*>(key ? a.dk_out : a.dq) + at + u.h * a.dk + c0;
-#pragma unroll
-                for (int q = 0; q < 2; ++q)
-                    if (c0 + 8 * q < a.dk)
-                        *reinterpret_cast<uint4*>(to + 8 * q) = make_uint4(round2(v[8 * q], v[8 * q + 1]), round2(v[8 * q + 2], v[8 * q + 3]),
-                                                                           round2(v[8 * q + 4], v[8 * q + 5]), round2(v[8 * q + 6], v[8 * q + 7]));
+                for (int x = tid; x < 2 * kC * (DKP / 8); x += 256) {
+                    const int row = x / (DKP / 8), un = x % (DKP / 8), t = row & 63;
+                    if (t < u.n && un * 8 < a.dk) {
+                        const uint4 v = *reinterpret_cast<const uint4*>(smem + kq * W::kKQ + (un >> 3) * 16384 + swizzled_at(row, un & 7));
+                        const int64_t at = row < kC ? (u.b + t) * a.dk_ld : (u.b + t) * a.dq_ld;
+                        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(row < kC ? a.dk_out : a.dq) + at + u.h * a.dk + un * 8) = v;
+                    }
+                }
             }
             __syncwarp();
         }

@@ -127,8 +127,8 @@ __device__ __forceinline__ void copy_box(uint32_t to, const void* map, int col, 
                  : "memory");
 }
 // Waits for the phase to end, for a second or so at most; false where it has not.
-__device__ __forceinline__ bool barrier_wait(uint32_t bar, uint32_t phase) {
-    for (int i = 0; i < 1 << 18; ++i) {   // a try takes 7800 cycles
+__device__ __forceinline__ bool barrier_wait(uint32_t bar, uint32_t phase, int tries = 1 << 18) {
+    for (int i = 0; i < tries; ++i) {   // a try takes 7800 cycles
         uint32_t done;
         asm volatile(
             "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.b32 %0, 1, 0, p;\n}"
@@ -138,11 +138,11 @@ __device__ __forceinline__ bool barrier_wait(uint32_t bar, uint32_t phase) {
     return false;
 }
 
-// After a wait that ran out: waits, as long again at most, for what the barriers still expect, before memory is given back.
+// After a wait that ran out: waits, a tenth of a second each at most, for what the barriers still expect, before memory is given back.
 __device__ __forceinline__ void drain(uint32_t bars, int n) {
     for (int x = 0; x < n; ++x) {
-        barrier_wait(bars + 8 * x, 0);
-        barrier_wait(bars + 8 * x, 1);
+        barrier_wait(bars + 8 * x, 0, 1 << 15);
+        barrier_wait(bars + 8 * x, 1, 1 << 15);
     }
 }
 
