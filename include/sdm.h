@@ -547,12 +547,13 @@ typedef struct {
  *   strengths (below 2^-80 they count as 2^-80). Keys of length 1 and beta in [0, 2] keep the state bounded.
  *   offsets: as in sdm_glr_forward (ragged sequences, rows of no sequence).
  *   h0 (nullable: zeros) and hT (nullable) float32 [P, v_heads, dk, dv]: the states before and after; hT may be h0; an
- *   empty sequence hands its state on.
+ *   empty sequence hands its state on. No other output overlaps an input.
  *   states (nullable), sdm_gdr_states_bytes, 16-byte aligned: the state before every SDM_GDR_CHUNK-th row of each sequence,
  *   what every row writes and what its block gives without the state, for the backward, in a form of its own.
  *   ws: sdm_gdr_workspace_bytes(shape, 0), 16-byte aligned. It holds nothing from one call to the next.
  * Few and long sequences (of bfloat16 rows) are walked in segments, as the shape alone decides, so the same sequence in calls of
- * different shapes agrees to rounding.
+ * different shapes agrees to rounding. A segment's matrix stays as small as a state does for keys no longer than 1; with longer keys it
+ * may leave float32's range (NaN from there on) where the states alone would not.
  * Blocks of 64 rows are solved together on the tensor cores; sums are float32, and float32 values enter the products as sums of
  * two bfloat16 (within 2^-17) beside bfloat16 rows, of three (2^-25) beside float32 rows. A value that is not finite spoils its sequence and head from the start of its block on (as NaN).
  */

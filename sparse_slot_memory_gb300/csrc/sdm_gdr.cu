@@ -561,20 +561,11 @@ __global__ void __launch_bounds__(BV * 4) gdr_walk_tc_kernel(const __grid_consta
     }
     unsigned char* const Sp = smem + W::S + part * 4 * (DKP * 16) + r * 16;   // a unit of 8 columns: DKP rows of 16 bytes
     unsigned char* const Rp = smem + W::R + part * 4 * 1024 + i * 16;
-    auto put_state = [&](int64_t j) {   // S as operand, and for the backward before block j
-        if (r >= DKP) return;
-        put_terms(Sp, Sp + W::kS, DKP * 16, S);
-        if (!FIRST && a.states != nullptr && j < j1) {
-            unsigned char* const to = reinterpret_cast<unsigned char*>(a.states) + (((id0 + j) * a.Hv + h) * 2 * nb + vc / 8) * int64_t(DKP * 16) + r * 16;
-#pragma unroll
-            for (int t = 0; t < 2; ++t)
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    if (vc / 8 + q < nb)
-                        *reinterpret_cast<uint4*>(to + (t * static_cast<int64_t>(nb) + q) * (DKP * 16)) = *reinterpret_cast<const uint4*>(Sp + t * W::kS + q * (DKP * 16));
-        }
+    auto put_state = [&]() {   // S as operand
+        if (r < DKP) put_terms(Sp, Sp + W::kS, DKP * 16, S);
     };
-    put_state(j0);
+    const bool saving = !FIRST && a.states != nullptr && w == 2;   // this warp's elected thread sends it off, for the backward
+    put_state();
     if (w == 0) tensor::allocate<W::cols>(smem_of(&tmem));
     tensor::fence_before();
     __syncthreads();
@@ -596,6 +587,14 @@ __global__ void __launch_bounds__(BV * 4) gdr_walk_tc_kernel(const __grid_consta
         copies_wait<0>();
         async_fence();
         if (__syncthreads_or(bad)) break;
+        if (saving && tensor::elect()) {
+            unsigned char* const to = reinterpret_cast<unsigned char*>(a.states) + (((id0 + j) * a.Hv + h) * 2 * nb + c0 / 8) * int64_t(DKP * 16);
+            const int bytes = min(BV / 8, nb - c0 / 8) * (DKP * 16);
+            bulk_store(to, base + W::S, bytes);
+            bulk_store(to + static_cast<int64_t>(nb) * (DKP * 16), base + W::S + W::kS, bytes);
+            bulk_commit();
+        }
+        __syncwarp();
         if (w == 0 && tensor::elect()) {
             tensor::fence_after();
 #pragma unroll
@@ -653,6 +652,8 @@ __global__ void __launch_bounds__(BV * 4) gdr_walk_tc_kernel(const __grid_consta
             for (int e = 0; e < 16; ++e) x[e] = mul2(pack2(c, c), u[e]);
             put_terms(Rp, Rp + W::kR, 1024, x);
         }
+        if (saving && tensor::elect()) bulk_wait_read();   // before the state is written anew
+        __syncwarp();
         async_fence();
         tensor::fence_before();
         __syncthreads();
@@ -705,7 +706,7 @@ __global__ void __launch_bounds__(BV * 4) gdr_walk_tc_kernel(const __grid_consta
         W::sums(Dc + mine, u);
 #pragma unroll
         for (int e = 0; e < 16; ++e) S[e] = fma2(pack2(last, last), S[e], u[e]);
-        put_state(j + 1);
+        put_state();
         tensor::fence_before();
     }
     const int64_t head = static_cast<int64_t>(p) * a.Hv + h;
@@ -717,6 +718,8 @@ __global__ void __launch_bounds__(BV * 4) gdr_walk_tc_kernel(const __grid_consta
         for (int q = 0; q < 8; ++q)
             if (vc + 4 * q < width) st4(to + static_cast<int64_t>(r) * width + vc + 4 * q, Quad{S[2 * q], S[2 * q + 1]});
     }
+    if (saving && tensor::elect()) bulk_wait();
+    __syncwarp();
     copies_wait<0>();
     if (__syncthreads_or(bad)) {
         if (tid == 0 && a.status != nullptr) atomicOr(a.status, SDM_DEV_STALLED);
