@@ -682,12 +682,15 @@ __global__ void __launch_bounds__(BV * 4) gdr_walk_tc_kernel(const __grid_consta
                     *reinterpret_cast<uint4*>(to + (nb + q) * 1024) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                 }
             }
-        } else if (!FIRST && i < n) {   // the row's answer
-            __nv_bfloat16* const y = static_cast<__nv_bfloat16*>(a.y) + (r0 + i) * a.y_ld + h * a.dv + vc;
+        } else if (!FIRST) {   // the row's answer
             const uint64_t f = pack2(a.scale * eg, a.scale * eg);
+            __nv_bfloat16* const y = static_cast<__nv_bfloat16*>(a.y) + r0 * a.y_ld + h * a.dv;
+            // Of 128 columns through the place of Q, which the first product has read, to leave in whole rows (8 x 4096 rows of 16 heads:
+            // 288 us, 308 in 16 bytes a thread); fewer are not worth the barrier (12 prompts in 64 columns: 314 and 294).
+            constexpr bool whole = BV == 128 && DKP == 128;
+            unsigned char* const Q = smem + W::KQ + (j & 1) * W::kKQ + 8192;
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                if (vc + 8 * q >= a.dv) continue;
                 uint32_t o[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
@@ -695,7 +698,18 @@ __global__ void __launch_bounds__(BV * 4) gdr_walk_tc_kernel(const __grid_consta
                     unpack2(fma2(f, x[4 * q + e], u[4 * q + e]), s, t);
                     o[e] = round2(s, t);
                 }
-                *reinterpret_cast<uint4*>(y + 8 * q) = make_uint4(o[0], o[1], o[2], o[3]);
+                const uint4 v = make_uint4(o[0], o[1], o[2], o[3]);
+                if (whole) *reinterpret_cast<uint4*>(Q + (part >> 1) * 16384 + swizzled_at(i, (part & 1) * 4 + q)) = v;
+                else if (i < n && vc + 8 * q < a.dv) *reinterpret_cast<uint4*>(y + i * a.y_ld + vc + 8 * q) = v;
+            }
+            if (whole) {
+                asm volatile("bar.sync 1, %0;" ::"n"(W::threads / 2) : "memory");
+#pragma unroll
+                for (int t = 64 * part + i; t < kC * (BV / 8); t += W::threads / 2) {
+                    const int row = t / (BV / 8), un = t % (BV / 8);
+                    if (row < n && c0 + 8 * un < a.dv)
+                        *reinterpret_cast<uint4*>(y + row * a.y_ld + c0 + 8 * un) = *reinterpret_cast<const uint4*>(Q + (un >> 3) * 16384 + swizzled_at(row, un & 7));
+                }
             }
         }
         __syncwarp();
