@@ -497,7 +497,7 @@ __global__ void __launch_bounds__(BV * 2) gdr_walk_kernel(const __grid_constant_
 // Where the walks are few and long, every sequence is cut into segments that are walked side by side, twice. A segment makes
 // M S + B of the state S before it: the first time (FIRST) blocks start from zeros for B, and others, without V, from the identity
 // for M; gdr_chain_kernel joins them to the states before the segments, from which the second walk starts. One sequence of 32769
-// rows, 8 heads of 64 x 128: 952 us whole, 420 in 16 segments.
+// rows, 8 heads of 64 x 128: 952 us whole, 402 in 16 segments.
 template <int DKP, int BV, bool FIRST>
 __global__ void __launch_bounds__(BV * 4) gdr_walk_tc_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps,
                                                              const __grid_constant__ Segments sg) {
@@ -745,7 +745,8 @@ __global__ void __launch_bounds__(BV * 4) gdr_walk_tc_kernel(const __grid_consta
 }
 
 // The states before a sequence's segments, one after another: S' = M S + B in float32, 32 value columns a block. Rows of M are read
-// by whole warps at once; the next M is on its way meanwhile.
+// by whole warps at once; the next M is on its way meanwhile. R: rows of a thread, dk / 8 or more (the last ones are computed again).
+template <int R>
 __global__ void __launch_bounds__(256) gdr_chain_kernel(const __grid_constant__ Args a, const __grid_constant__ Segments sg) {
     extern __shared__ __align__(1024) unsigned char smem[];
     start_dependent();
@@ -770,18 +771,18 @@ __global__ void __launch_bounds__(256) gdr_chain_kernel(const __grid_constant__ 
         S[r * 32 + c] = x;
         if (there) start[static_cast<int64_t>(r) * a.dv + col] = x;
     }
-    float x[16], ahead[16];   // rows w, w + 8 ..: dk is a multiple of 8
+    float x[R], ahead[R];   // rows w, w + 8 ..: dk is a multiple of 8
     auto fetch = [&](int s) {
         const float* const from = start + s * size;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) ahead[i] = s < sg.n && 8 * i < a.dk && there ? from[static_cast<int64_t>(w + 8 * i) * a.dv + col] : 0.f;
+        for (int i = 0; i < R; ++i) ahead[i] = s < sg.n && 8 * i < a.dk && there ? from[static_cast<int64_t>(w + 8 * i) * a.dv + col] : 0.f;
     };
     fetch(1);
     for (int s = 0; s + 1 < sg.n; ++s) {
         load(s + 1);
         float* const next = start + (s + 1) * size;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) x[i] = ahead[i];
+        for (int i = 0; i < R; ++i) x[i] = ahead[i];
         fetch(s + 2);
         copies_wait<1>();
         __syncthreads();
@@ -792,9 +793,8 @@ __global__ void __launch_bounds__(256) gdr_chain_kernel(const __grid_constant__ 
 #pragma unroll
             for (int e = 0; e < 4; ++e) y[e] = S[(k + e) * 32 + c];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-                if (8 * i >= a.dk) continue;
-                const float4 f = *reinterpret_cast<const float4*>(m + 8 * i * a.dk + k);
+            for (int i = 0; i < R; ++i) {
+                const float4 f = *reinterpret_cast<const float4*>(m + min(8 * i, a.dk - 8) * a.dk + k);
                 x[i] = fmaf(f.x, y[0], x[i]);
                 x[i] = fmaf(f.y, y[1], x[i]);
                 x[i] = fmaf(f.z, y[2], x[i]);
@@ -803,7 +803,7 @@ __global__ void __launch_bounds__(256) gdr_chain_kernel(const __grid_constant__ 
         }
         __syncthreads();
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
+        for (int i = 0; i < R; ++i) {
             if (8 * i >= a.dk) continue;
             S[(w + 8 * i) * 32 + c] = x[i];
             if (there) next[static_cast<int64_t>(w + 8 * i) * a.dv + col] = x[i];
@@ -981,15 +981,15 @@ cudaError_t walk_bf16(const Args& a, const Segments& sg, cudaStream_t cs) {
         cudaError_t e = walk_tc<DKP, true>(a, sg, cs);
         if (e != cudaSuccess) return e;
         const int smem = (2 * a.dk * a.dk + a.dk * 32) * 4;
-        e = big_smem(gdr_chain_kernel, smem);
-        if (e == cudaSuccess)
-            e = launch_dependent(gdr_chain_kernel, dim3(static_cast<unsigned>(a.P * a.Hv * ((a.dv + 31) / 32))), dim3(256), smem, cs, a, sg);
+        auto* const chain = gdr_chain_kernel<DKP / 8>;
+        e = big_smem(chain, smem);
+        if (e == cudaSuccess) e = launch_dependent(chain, dim3(static_cast<unsigned>(a.P * a.Hv * ((a.dv + 31) / 32))), dim3(256), smem, cs, a, sg);
         if (e != cudaSuccess) return e;
     }
     return walk_tc<DKP, false>(a, sg, cs);
 }
 
-// Segments of a sequence's walk, of 16 blocks of rows each at least: two walks of a segment and the chain's 4.5 us a segment and 10
+// Segments of a sequence's walk, of 16 blocks of rows each at least: two walks of a segment and the chain's 3 us a segment and 10
 // against one walk of all rows (columns(), a fifth on top for what that leaves out). Measured, heads of 128 but for the first: one
 // sequence of 4096 rows, 2 heads of 64, 80 us in 4 segments and 110 whole; 32768 rows, 4 heads, 374 in 16 and 931 whole; 4096 rows, 16
 // heads, 163 in 4 and 140 whole; 2 of 8192, 16 heads, 494 in 4 and 330 whole.
@@ -1004,7 +1004,7 @@ int segments(const sdm_gdr_shape* s) {
         if (blocks < 16 * n) break;
         columns(walks * (n - 1), s->dv, s->dk, &first);
         columns(walks * n, s->dv, 0, &second);
-        const int64_t t = ((first + second) * ((blocks + n - 1) / n) * 36 + n * 450 + 1000) * 6 / 5;
+        const int64_t t = ((first + second) * ((blocks + n - 1) / n) * 36 + n * 300 + 1000) * 6 / 5;
         if (t < least) best = n, least = t;
     }
     return best;
