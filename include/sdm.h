@@ -617,7 +617,7 @@ sdm_status sdm_block_norm(const sdm_norm_shape* shape, const void* o, int64_t o_
  * gradient of r (nullable where pre is 1: zeros), dy that of y. d_o, dz (gate), dx (nullable: the gradient of the sum, x's and
  * all that came before) [rows, D]; dw_post [group], dw_pre, d_channel_scale [D] float32 (nullable), written, with zeros for what the
  * shape does not have. dx may be dr, dz may be z and d_o may be o (same ld). ws: sdm_block_norm_workspace_bytes, 16-byte aligned
- * (may be NULL where no weight's gradient is asked for).
+ * (may be NULL where no gradient of a weight that the shape has is asked for).
  */
 size_t sdm_block_norm_workspace_bytes(const sdm_norm_shape* shape);
 sdm_status sdm_block_norm_backward(const sdm_norm_shape* shape, const void* o, int64_t o_ld, const void* z, int64_t z_ld,

@@ -441,14 +441,16 @@ __global__ void __launch_bounds__(MAXT, MAXT == 256 ? 2 : 1) norm_bwd_kernel(con
     }
 }
 
-// A kind's gradients: the blocks' rows in 32 shares, each in order, and those in order. Block y: the kind.
-__global__ void __launch_bounds__(1024) norm_dw_kernel(const float* part, int blocks, int D, int G, int want, float* dw_post,
+// A kind's gradients: the blocks' rows in 32 shares, each in order, and those in order. Block y: the kind. What the shape does not have
+// (asked for and not in `want`, so that no block wrote a row of it) is the sum of no rows: 0.
+__global__ void __launch_bounds__(1024) norm_dw_kernel(const float* part, int blocks, int D, int G, int asked, int want, float* dw_post,
                                                        float* dw_pre, float* dcs) {
     __shared__ float s[32][33];
     start_dependent();
     const int kind = blockIdx.y, n = kind == 0 ? G : D;
     const int c = blockIdx.x * 32 + threadIdx.x;
-    if (!(want >> kind & 1) || blockIdx.x * 32 >= n) return;
+    if (!(asked >> kind & 1) || blockIdx.x * 32 >= n) return;
+    if (!(want >> kind & 1)) blocks = 0;
     float sum = 0.f;
     if (c < n) {
         const float* const p = part + static_cast<int64_t>(kind) * blocks * D + c;
@@ -629,8 +631,8 @@ extern "C" sdm_status sdm_block_norm_backward(const sdm_norm_shape* shape, const
             }
             return launch_dependent(k, dim3(static_cast<unsigned>(blocks)), dim3(threads), smem, cs, a);
         });
-    if (e == cudaSuccess && asked)   // what the shape does not have is the sum of no blocks' rows: 0
+    if (e == cudaSuccess && asked)
         e = launch_dependent(norm_dw_kernel, dim3(static_cast<unsigned>((a.D + 31) / 32), 3), dim3(32, 32), 0, cs, static_cast<const float*>(ws),
-                             shape->rows > 0 ? blocks : 0, a.D, shape->group, asked, dw_post, dw_pre, d_channel_scale);
+                             shape->rows > 0 ? blocks : 0, a.D, shape->group, asked, a.want, dw_post, dw_pre, d_channel_scale);
     return e == cudaSuccess ? SDM_OK : SDM_ERR_CUDA;
 }
