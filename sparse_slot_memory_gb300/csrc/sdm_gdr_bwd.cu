@@ -340,13 +340,14 @@ __global__ void __launch_bounds__(BV * 4) gdr_back_tc_kernel(const __grid_consta
             __syncthreads();
         }
         tensor::fence_after();
-        if (tid == 0) {   // what dY gives by A T
+        if (w == 0 && tensor::elect()) {   // what dY gives by A T: by the thread that commits it with T's products
 #pragma unroll
             for (int t = 0; t < 2; ++t)
 #pragma unroll
                 for (int ks = 0; ks < 4; ++ks)
                     tensor::mma(W::terms == 1 ? Db + t * BV : Db, Td + (t * 16384 + 1024 + ks * 256) / 16, dYd + ks * 128, tensor::shape(128, BV, true, true), W::terms == 1 ? ks > 0 : t + ks > 0);
         }
+        __syncwarp();
         uint64_t x[16];
         const float eg = vec[i], bt = vec[kC + i];
         if (key) {
