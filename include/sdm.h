@@ -552,8 +552,8 @@ typedef struct {
  *   what every row writes and what its block gives without the state, for the backward, in a form of its own.
  *   ws: sdm_gdr_workspace_bytes(shape, 0), 16-byte aligned. It holds nothing from one call to the next.
  * Few and long sequences (of bfloat16 rows) are walked in segments, as the shape alone decides, so the same sequence in calls of
- * different shapes agrees to rounding. A segment's matrix stays as small as a state does for keys no longer than 1; with longer keys it
- * may leave float32's range (NaN from there on) where the states alone would not.
+ * different shapes agrees to rounding. A segment's matrix stays as small as a state does for keys no longer than 1; where longer keys take
+ * it or a state out of float32's range, the segment walks on to the sequence's end for that head.
  * Blocks of 64 rows are solved together on the tensor cores; sums are float32, and float32 values enter the products as sums of
  * two bfloat16 (within 2^-17) beside bfloat16 rows, of three (2^-25) beside float32 rows. A value that is not finite spoils its sequence and head from the start of its block on (as NaN).
  */

@@ -499,7 +499,9 @@ __global__ void __launch_bounds__(BV * 2) gdr_walk_kernel(const __grid_constant_
 // Where the walks are few and long, every sequence is cut into segments that are walked side by side, twice. A segment makes
 // M S + B of the state S before it: the first time (FIRST) blocks start from zeros for B, and others, without V, from the identity
 // for M; gdr_chain_kernel joins them to the states before the segments, from which the second walk starts. One sequence of 32769
-// rows, 8 heads of 64 x 128: 952 us whole, 402 in 16 segments.
+// rows, 8 heads of 64 x 128: 952 us whole, 406 in 16 segments. Keys longer than 1 may grow M out of float32's range where the states
+// stay in it, so the second walk of a head does not start from a state that came out as not finite: the segment before walks on to the
+// sequence's end (4 us of the 406, and 1 to 4 of walks of whole sequences).
 template <int DKP, int BV, bool FIRST>
 __global__ void __launch_bounds__(BV * 4) gdr_walk_tc_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps,
                                                              const __grid_constant__ Segments sg) {
@@ -520,8 +522,12 @@ __global__ void __launch_bounds__(BV * 4) gdr_walk_tc_kernel(const __grid_consta
     int64_t b, len;
     sequence(a, p, b, len);
     const int64_t blocks = (len + kC - 1) / kC, id0 = first_block(b, p);
+    if (FIRST && seg + slice + tid == 0) sg.ends[p * a.Hv + h] = sg.n;
+    const int ends = FIRST || sg.n == 1 ? sg.n : sg.ends[p * a.Hv + h];
+    if (seg >= ends) return;
+    const bool last_one = seg == ends - 1;
     const uint32_t base = smem_of(smem), bar = smem_of(bars);
-    const int64_t per = (blocks + sg.n - 1) / sg.n, j0 = min(seg * per, blocks), j1 = min(j0 + per, blocks);
+    const int64_t per = (blocks + sg.n - 1) / sg.n, j0 = min(seg * per, blocks), j1 = !FIRST && last_one ? blocks : min(j0 + per, blocks);
     const int cols = min(BV, width - c0), nb = (a.dv + 15) / 16 * 2;   // units of 8 value columns that are saved
 
     const WalkLoads<DKP, BV> loads{a, maps, a.v, b, len, id0, base, smem_of(vecs), smem_of(bars) + 24, h, kh, c0, cols, tid, w, moving};
@@ -728,7 +734,7 @@ __global__ void __launch_bounds__(BV * 4) gdr_walk_tc_kernel(const __grid_consta
     const int64_t head = static_cast<int64_t>(p) * a.Hv + h;
     float* to = nullptr;
     if (FIRST) to = moving ? sg.move + (head * walks + seg) * a.dk * a.dk : sg.start + (head * sg.n + seg + 1) * a.dk * a.dv;
-    else if (a.hT != nullptr && seg == sg.n - 1) to = a.hT + head * a.dk * a.dv;
+    else if (a.hT != nullptr && last_one) to = a.hT + head * a.dk * a.dv;
     if (to != nullptr && r < a.dk) {
 #pragma unroll
         for (int q = 0; q < 8; ++q)
@@ -780,6 +786,7 @@ __global__ void __launch_bounds__(256) gdr_chain_kernel(const __grid_constant__ 
         for (int i = 0; i < R; ++i) ahead[i] = s < sg.n && 8 * i < a.dk && there ? from[static_cast<int64_t>(w + 8 * i) * a.dv + col] : 0.f;
     };
     fetch(1);
+    int ends = sg.n;
     for (int s = 0; s + 1 < sg.n; ++s) {
         load(s + 1);
         float* const next = start + (s + 1) * size;
@@ -807,10 +814,12 @@ __global__ void __launch_bounds__(256) gdr_chain_kernel(const __grid_constant__ 
 #pragma unroll
         for (int i = 0; i < R; ++i) {
             if (8 * i >= a.dk) continue;
+            if (!isfinite(x[i])) ends = min(ends, s + 1);
             S[(w + 8 * i) * 32 + c] = x[i];
             if (there) next[static_cast<int64_t>(w + 8 * i) * a.dv + col] = x[i];
         }
     }
+    if (there && ends < sg.n) atomicMin(sg.ends + head, ends);
     copies_wait<0>();
 }
 
@@ -1051,6 +1060,7 @@ Layout layout(const sdm_gdr_shape* s, bool backward) {
     if (const int n = segments(s); n > 1) {
         l.start = take(static_cast<int64_t>(s->P) * s->v_heads * n * s->dk * s->dv * 4);
         l.move = take(static_cast<int64_t>(s->P) * s->v_heads * (n - 1) * s->dk * s->dk * 4);
+        l.ends = take(static_cast<int64_t>(s->P) * s->v_heads * 4);
     }
     if (f32) {
         l.q = take(s->rows * s->k_heads * s->dk * 6);
@@ -1199,11 +1209,12 @@ extern "C" sdm_status sdm_gdr_forward(const sdm_gdr_shape* shape, const void* q,
     }
     const bool narrow = padded(shape->dk) == 64;
     if (e == cudaSuccess) {
-        Segments sg = {segments(shape), const_cast<float*>(h0), nullptr};
+        Segments sg = {segments(shape), const_cast<float*>(h0), nullptr, nullptr};
         if (sg.n > 1) {
             const Layout l = layout(shape, false);
             sg.start = reinterpret_cast<float*>(static_cast<unsigned char*>(ws) + l.start);
             sg.move = reinterpret_cast<float*>(static_cast<unsigned char*>(ws) + l.move);
+            sg.ends = reinterpret_cast<int32_t*>(static_cast<unsigned char*>(ws) + l.ends);
         }
         if (shape->x_dtype == SDM_BF16) e = narrow ? walk_bf16<64>(a, sg, cs) : walk_bf16<128>(a, sg, cs);
         else e = narrow ? walk<3, 64, 32>(a, cs) : walk<3, 128, 32>(a, cs);

@@ -87,6 +87,7 @@ struct Segments {
     int n;
     float* start;   // [P][Hv][n][dk][dv]: the states before them (n = 1: h0, nullable)
     float* move;    // [P][Hv][n - 1][dk][dk]: what they make of a state that they start from, beside what they write
+    int32_t* ends;  // [P][Hv]: segments that start from a state of finite values; the last of them walks on to the sequence's end
 };
 
 // The rows [b, b + n) of sequence p. Offsets that are not ascending within [0, rows] are cut to it and reported.
@@ -475,7 +476,7 @@ inline sdm_status check_array(const void* p, int64_t ld, int64_t n, int elem, in
 
 // The workspace's parts in bytes from its start
 struct Layout {
-    int64_t tri, vec, q, k, v, start, move, dy, dstates, du, part, bytes;
+    int64_t tri, vec, q, k, v, start, move, ends, dy, dstates, du, part, bytes;
 };
 inline int terms(const sdm_gdr_shape* s) { return s->x_dtype == SDM_F32 ? 3 : 2; }   // of what is computed
 sdm_status check_shape(const sdm_gdr_shape* s);
