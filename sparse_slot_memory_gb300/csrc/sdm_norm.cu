@@ -139,8 +139,9 @@ struct Sums {
 };
 
 // act and its slope: GATE 1 sigmoid, 2 z sigmoid(z); at infinite z their limits, NaN stays. bfloat16 rows take the hardware's
-// exponential and reciprocal, off by 2^-21 (|z| + 1) at most where the rows are 2^-8 apart, and cut z off at -80 and, in the
-// slope, at 80, where what is left is below 2^-115; float32 rows take expf and a rounded division.
+// exponential and reciprocal, off by 2^-21 (|z| + 1) at most where the rows are 2^-8 apart, and cut z off at -88 and, in the
+// slope, at 88. Both instructions give 0 for what is below 2^-126, so that gates and slopes are at their limits there, and what they
+// lose on the way is below 2^-126 of a sigmoid and 2^-119 of z sigmoid(z). float32 rows take expf and a rounded division.
 __device__ __forceinline__ float max_nan(float a, float b) {
     float o;
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(o) : "f"(a), "f"(b));
@@ -155,8 +156,8 @@ template <typename T, int GATE>
 __device__ __forceinline__ void gate_of(float z, float& act, float& slope) {
     float sg, rest, zc = z;   // sigmoid, 1 - sigmoid
     if (sizeof(T) == 2) {
-        z = max_nan(z, -80.f);
-        zc = min_nan(z, 80.f);
+        z = max_nan(z, -88.f);
+        zc = min_nan(z, 88.f);
         float e;
         asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(zc * -1.44269504088896341f));
         asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(sg) : "f"(1.f + e));
