@@ -278,21 +278,20 @@ __global__ void __launch_bounds__(128, XT == 1 ? 4 : 2) gdr_prepare_kernel(const
 // A warp owns 16 of a head's value columns and keeps its part of the state transposed, S^T [16 x dk], in the accumulators of its
 // matrix instructions (mma.sync): an accumulator's layout is an operand's too, so the chain S -> R -> U -> S' never leaves the
 // warp's registers. Three terms would not fit beside one another as operands in shared memory, as the tensor core above them wants.
-template <int XT, int DKP, int BV>
+template <int DKP>
 struct Walk {
-    static constexpr int NS = XT == 1 ? 2 : 3;   // terms of what is computed
+    static constexpr int BV = 32;   // value columns of a block
     static constexpr int kTile = kC * DKP * 2, kVal = kC * BV * 2, kPlane = kC * kC * 2;
-    static constexpr int K = 0, Q = K + XT * kTile, V = Q + XT * kTile, T = V + XT * kVal, A = T + NS * kPlane,
-                         vec = A + XT * kPlane, stage = vec + 3 * kC * 4, kKeep = NS * 16 * DKP * 2;
+    static constexpr int K = 0, Q = K + kTerms * kTile, V = Q + kTerms * kTile, T = V + kTerms * kVal, A = T + kTerms * kPlane,
+                         vec = A + kTerms * kPlane, keep = vec + 3 * kC * 4, kKeep = kTerms * 16 * DKP * 2;
     static constexpr int warps = BV / 16, threads = warps * 32;
-    static constexpr int stages = 2 * stage + warps * kKeep <= 227 * 1024 ? 2 : 1;
-    static constexpr int bytes(bool saving) { return stages * stage + (saving ? warps * kKeep : 0); }
+    static constexpr int bytes(bool saving) { return keep + (saving ? warps * kKeep : 0); }
 };
 
-template <int XT, int DKP, int BV, typename X>
-__global__ void __launch_bounds__(BV * 2) gdr_walk_kernel(const __grid_constant__ Args a) {
-    using W = Walk<XT, DKP, BV>;
-    constexpr int KT = DKP / 16, NS = W::NS;
+template <int DKP>
+__global__ void __launch_bounds__(Walk<DKP>::threads) gdr_walk_kernel(const __grid_constant__ Args a) {
+    using W = Walk<DKP>;
+    constexpr int KT = DKP / 16, NS = kTerms, BV = W::BV;
     extern __shared__ __align__(1024) unsigned char smem[];
     start_dependent();
     const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, g = lane >> 2, qd = lane & 3;
@@ -306,18 +305,17 @@ __global__ void __launch_bounds__(BV * 2) gdr_walk_kernel(const __grid_constant_
     const uint32_t base = smem_of(smem);
     const int cols = min(BV, a.dv - c0), groups = (a.dv + 15) / 16;
 
-    auto load = [&](int64_t j, int s) {
-        const uint32_t st = base + s * W::stage;
+    auto load = [&](int64_t j) {
         const int n = static_cast<int>(min(len - j * kC, int64_t(kC)));
         const int64_t r0 = b + j * kC;
-        load_rows<DKP, W::threads>(st + W::K, a.k, XT, r0, n, kh * a.dk, a.dk, tid);
-        load_rows<DKP, W::threads>(st + W::Q, a.q, XT, r0, n, kh * a.dk, a.dk, tid);
-        load_rows<BV, W::threads>(st + W::V, a.v, XT, r0, n, h * a.dv + c0, cols, tid);
+        load_rows<DKP, W::threads>(base + W::K, a.k, NS, r0, n, kh * a.dk, a.dk, tid);
+        load_rows<DKP, W::threads>(base + W::Q, a.q, NS, r0, n, kh * a.dk, a.dk, tid);
+        load_rows<BV, W::threads>(base + W::V, a.v, NS, r0, n, h * a.dv + c0, cols, tid);
         const int64_t at = (id0 + j) * a.Hv + h;
         const __nv_bfloat16* const tri = a.tri + at * (2 * NS) * int64_t(kC * kC);
 #pragma unroll
-        for (int pl = 0; pl < NS + XT; ++pl) load_tri<W::threads>(st + W::T + pl * W::kPlane, tri + pl * kC * kC, tid);
-        if (tid < 48) copy16(st + W::vec + tid * 16, a.vec + at * kVecs * kC + tid * 4, true);
+        for (int pl = 0; pl < 2 * NS; ++pl) load_tri<W::threads>(base + W::T + pl * W::kPlane, tri + pl * kC * kC, tid);
+        if (tid < 48) copy16(base + W::vec + tid * 16, a.vec + at * kVecs * kC + tid * 4, true);
         copies_commit();
     };
 
@@ -334,19 +332,13 @@ __global__ void __launch_bounds__(BV * 2) gdr_walk_kernel(const __grid_constant_
                 S[t][e] = h0 != nullptr && d < a.dk && c < a.dv ? h0[static_cast<int64_t>(d) * a.dv + c] : 0.f;
             }
     }
-    const uint32_t keep = base + W::stages * W::stage + w * W::kKeep;
-    if (blocks > 0 && W::stages == 2) load(0, 0);
+    const uint32_t keep = base + W::keep + w * W::kKeep;
+    const float* const vec = reinterpret_cast<const float*>(smem + W::vec);
     for (int64_t j = 0; j < blocks; ++j) {
-        const int at = W::stages == 2 ? static_cast<int>(j & 1) : 0;
-        if (W::stages == 1) {
-            __syncthreads();
-            load(j, 0);
-        }
+        __syncthreads();
+        load(j);
         copies_wait<0>();
         __syncthreads();
-        if (W::stages == 2 && j + 1 < blocks) load(j + 1, at ^ 1);
-        const uint32_t st = base + at * W::stage;
-        const float* const vec = reinterpret_cast<const float*>(smem + at * W::stage + W::vec);
         if (16 * w >= cols) continue;   // a warp without columns
         if (a.states != nullptr) {
             if (lane == 0) bulk_wait_read();
@@ -361,8 +353,8 @@ __global__ void __launch_bounds__(BV * 2) gdr_walk_kernel(const __grid_constant_
 #pragma unroll
                 for (int t = 0; t < NS; ++t) stsm4(keep + t * (16 * DKP * 2) + state_at(L.rA, 2 * kt + L.uA), s[t]);
             }
-            products<NS, XT, NS, false, 4>(r, s, W::kTile, [&](int np) { return st + W::K + tile_at<DKP>(16 * np + L.rB, 2 * kt + L.uB); });
-            products<NS, XT, NS, false, 4>(o, s, W::kTile, [&](int np) { return st + W::Q + tile_at<DKP>(16 * np + L.rB, 2 * kt + L.uB); });
+            products<NS, NS, NS, false, 4>(r, s, W::kTile, [&](int np) { return base + W::K + tile_at<DKP>(16 * np + L.rB, 2 * kt + L.uB); });
+            products<NS, NS, NS, false, 4>(o, s, W::kTile, [&](int np) { return base + W::Q + tile_at<DKP>(16 * np + L.rB, 2 * kt + L.uB); });
         }
         if (a.states != nullptr) {   // the state before the block, for the backward
             async_fence();
@@ -375,9 +367,9 @@ __global__ void __launch_bounds__(BV * 2) gdr_walk_kernel(const __grid_constant_
         // r = beta (v - e^gam K S); o = e^gam Q S
 #pragma unroll
         for (int np = 0; np < 4; ++np) {
-            uint32_t f[XT][4];
+            uint32_t f[NS][4];
 #pragma unroll
-            for (int x = 0; x < XT; ++x) ldsm4t(f[x], st + W::V + x * W::kVal + tile_at<BV>(16 * np + L.rAt, 2 * w + L.uAt));
+            for (int x = 0; x < NS; ++x) ldsm4t(f[x], base + W::V + x * W::kVal + tile_at<BV>(16 * np + L.rAt, 2 * w + L.uAt));
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
                 const int nt = 2 * np + t;
@@ -387,7 +379,7 @@ __global__ void __launch_bounds__(BV * 2) gdr_walk_kernel(const __grid_constant_
                 for (int e = 0; e < 4; ++e) {
                     float v = 0.f;
 #pragma unroll
-                    for (int x = XT - 1; x >= 0; --x) {
+                    for (int x = NS - 1; x >= 0; --x) {
                         const uint32_t word = f[x][2 * t + (e >> 1)];
                         v += __uint_as_float(e & 1 ? word & 0xFFFF0000u : word << 16);
                     }
@@ -402,7 +394,7 @@ __global__ void __launch_bounds__(BV * 2) gdr_walk_kernel(const __grid_constant_
         for (int kt = 0; kt < 4; ++kt) {   // U = T r
             uint32_t f[NS][4];
             terms_of<NS>(r[2 * kt], r[2 * kt + 1], f);
-            products<NS, NS, NS, false, 4>(u, f, W::kPlane, [&](int np) { return st + W::T + tile_at<kC>(16 * np + L.rB, 2 * kt + L.uB); }, kt);
+            products<NS, NS, NS, false, 4>(u, f, W::kPlane, [&](int np) { return base + W::T + tile_at<kC>(16 * np + L.rB, 2 * kt + L.uB); }, kt);
         }
         const float last = vec[kC - 1];
 #pragma unroll
@@ -421,7 +413,7 @@ __global__ void __launch_bounds__(BV * 2) gdr_walk_kernel(const __grid_constant_
 #pragma unroll
                 for (int t = 0; t < NS; ++t) stsm4t(keep + t * (kC * 32) + rows_at(16 * kt + L.rAt, L.uAt), f[t]);
             }
-            products<NS, XT, NS, false, 4>(o, f, W::kPlane, [&](int np) { return st + W::A + tile_at<kC>(16 * np + L.rB, 2 * kt + L.uB); }, kt);
+            products<NS, NS, NS, false, 4>(o, f, W::kPlane, [&](int np) { return base + W::A + tile_at<kC>(16 * np + L.rB, 2 * kt + L.uB); }, kt);
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
                 const float2 c = *reinterpret_cast<const float2*>(vec + 2 * kC + 16 * kt + 8 * t + 2 * qd);
@@ -429,7 +421,7 @@ __global__ void __launch_bounds__(BV * 2) gdr_walk_kernel(const __grid_constant_
                 for (int e = 0; e < 4; ++e) u[2 * kt + t][e] *= e & 1 ? c.y : c.x;
             }
             terms_of<NS>(u[2 * kt], u[2 * kt + 1], f);
-            products<NS, XT, NS, true, KT>(S, f, W::kTile, [&](int np) { return st + W::K + tile_at<DKP>(16 * kt + L.rBt, 2 * np + L.uBt); });
+            products<NS, NS, NS, true, KT>(S, f, W::kTile, [&](int np) { return base + W::K + tile_at<DKP>(16 * kt + L.rBt, 2 * np + L.uBt); });
         }
         if (a.states != nullptr) {   // the writes, for the backward
             async_fence();
@@ -442,36 +434,13 @@ __global__ void __launch_bounds__(BV * 2) gdr_walk_kernel(const __grid_constant_
         // the rows' answers
         const int64_t r0 = b + j * kC;
         const int n = static_cast<int>(min(len - j * kC, int64_t(kC)));
-        if constexpr (sizeof(X) == 2) {
-            // turned in the tile of V, whose columns of this warp have been read
 #pragma unroll
-            for (int np = 0; np < 4; ++np) {
-                uint32_t f[4];
+        for (int nt = 0; nt < 8; ++nt)
 #pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    f[2 * t] = round2(o[2 * np + t][0] * a.scale, o[2 * np + t][1] * a.scale);
-                    f[2 * t + 1] = round2(o[2 * np + t][2] * a.scale, o[2 * np + t][3] * a.scale);
-                }
-                stsm4t(st + W::V + tile_at<BV>(16 * np + L.rAt, 2 * w + L.uAt), f);
+            for (int e = 0; e < 4; ++e) {
+                const int row = 8 * nt + 2 * qd + (e & 1), c = vc + (e >> 1) * 8;
+                if (row < n && c < a.dv) static_cast<float*>(a.y)[(r0 + row) * a.y_ld + h * a.dv + c] = o[nt][e] * a.scale;
             }
-            __syncwarp();
-#pragma unroll
-            for (int i = lane; i < kC * 2; i += 32) {
-                const int row = i >> 1, u8 = 2 * w + (i & 1);
-                if (row < n && u8 * 8 < cols) {
-                    const uint4 v = *reinterpret_cast<const uint4*>(smem + at * W::stage + W::V + tile_at<BV>(row, u8));
-                    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.y) + (r0 + row) * a.y_ld + h * a.dv + c0 + u8 * 8) = v;
-                }
-            }
-        } else {
-#pragma unroll
-            for (int nt = 0; nt < 8; ++nt)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int row = 8 * nt + 2 * qd + (e & 1), c = vc + (e >> 1) * 8;
-                    if (row < n && c < a.dv) static_cast<float*>(a.y)[(r0 + row) * a.y_ld + h * a.dv + c] = o[nt][e] * a.scale;
-                }
-        }
     }
     if (a.hT != nullptr && 16 * w < cols) {
         float* const hT = a.hT + (static_cast<int64_t>(p) * a.Hv + h) * a.dk * a.dv;
@@ -952,15 +921,14 @@ cudaError_t prepare(const Args& a, int64_t blocks, cudaStream_t cs) {
     return launch_dependent(k, dim3(static_cast<unsigned>(blocks * a.Hk)), dim3(128), bytes, cs, a);
 }
 
-template <int XT, int DKP, int BV>
+template <int DKP>
 cudaError_t walk(const Args& a, cudaStream_t cs) {
-    using X = std::conditional_t<XT == 1, __nv_bfloat16, float>;
-    using W = Walk<XT, DKP, BV>;
-    auto* const k = gdr_walk_kernel<XT, DKP, BV, X>;
+    using W = Walk<DKP>;
+    auto* const k = gdr_walk_kernel<DKP>;
     const int bytes = W::bytes(a.states != nullptr);
     const cudaError_t e = big_smem(k, bytes);
     if (e != cudaSuccess) return e;
-    const int64_t grid = static_cast<int64_t>(a.P) * a.Hv * ((a.dv + BV - 1) / BV);
+    const int64_t grid = static_cast<int64_t>(a.P) * a.Hv * ((a.dv + W::BV - 1) / W::BV);
     return launch_dependent(k, dim3(static_cast<unsigned>(grid)), dim3(W::threads), bytes, cs, a);
 }
 
@@ -1217,7 +1185,7 @@ extern "C" sdm_status sdm_gdr_forward(const sdm_gdr_shape* shape, const void* q,
             sg.ends = reinterpret_cast<int32_t*>(static_cast<unsigned char*>(ws) + l.ends);
         }
         if (shape->x_dtype == SDM_BF16) e = narrow ? walk_bf16<64>(a, sg, cs) : walk_bf16<128>(a, sg, cs);
-        else e = narrow ? walk<3, 64, 32>(a, cs) : walk<3, 128, 32>(a, cs);
+        else e = narrow ? walk<64>(a, cs) : walk<128>(a, cs);
     }
     return e == cudaSuccess ? SDM_OK : SDM_ERR_CUDA;
 }

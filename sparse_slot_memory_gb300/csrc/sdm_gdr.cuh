@@ -34,6 +34,7 @@ using namespace rows;
 constexpr int kC = SDM_GDR_CHUNK;   // rows of a block
 constexpr int kMaxD = 128;          // channels of a head at most
 constexpr int kVecs = 5;
+constexpr int kTerms = 3;           // of float32 rows, and of what is computed from them
 
 // A write strength below 2^-80 counts as 2^-80, so that the error v - e^g S^T k behind a write, which the strength's gradient
 // takes, can be had from the write. What a row of strength 0 writes is then 2^-80 of that error, which no other value feels.

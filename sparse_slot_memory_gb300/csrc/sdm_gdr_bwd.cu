@@ -21,21 +21,19 @@ namespace gdr {
 namespace {
 
 // ---- the walk from the end, float32 rows ------------------------------------------------------------------------------
-template <int XT, int DKP, int BV>
+template <int DKP>
 struct Back {
-    static constexpr int NS = XT == 1 ? 2 : 3;
+    static constexpr int BV = 32;
     static constexpr int kTile = kC * DKP * 2, kVal = kC * BV * 2, kPlane = kC * kC * 2;
-    static constexpr int K = 0, Q = K + XT * kTile, Y = Q + XT * kTile, T = Y + XT * kVal, A = T + NS * kPlane,
-                         vec = A + NS * kPlane, stage = vec + 3 * kC * 4, kKeep = NS * 16 * DKP * 2;
-    static constexpr int warps = BV / 16, threads = warps * 32;
-    static constexpr int stages = 2 * stage + warps * kKeep <= 227 * 1024 ? 2 : 1;
-    static constexpr int bytes = stages * stage + warps * kKeep;
+    static constexpr int K = 0, Q = K + kTerms * kTile, Y = Q + kTerms * kTile, T = Y + kTerms * kVal, A = T + kTerms * kPlane,
+                         vec = A + kTerms * kPlane, keep = vec + 3 * kC * 4, kKeep = kTerms * 16 * DKP * 2;
+    static constexpr int warps = BV / 16, threads = warps * 32, bytes = keep + warps * kKeep;
 };
 
-template <int XT, int DKP, int BV, typename X>
-__global__ void __launch_bounds__(BV * 2) gdr_back_kernel(const __grid_constant__ Args a) {
-    using W = Back<XT, DKP, BV>;
-    constexpr int KT = DKP / 16, NS = W::NS;
+template <int DKP>
+__global__ void __launch_bounds__(Back<DKP>::threads) gdr_back_kernel(const __grid_constant__ Args a) {
+    using W = Back<DKP>;
+    constexpr int KT = DKP / 16, NS = kTerms, BV = W::BV;
     extern __shared__ __align__(1024) unsigned char smem[];
     start_dependent();
     const int tid = threadIdx.x, w = tid >> 5, lane = tid & 31, g = lane >> 2, qd = lane & 3;
@@ -49,18 +47,17 @@ __global__ void __launch_bounds__(BV * 2) gdr_back_kernel(const __grid_constant_
     const uint32_t base = smem_of(smem);
     const int cols = min(BV, a.dv - c0), groups = (a.dv + 15) / 16;
 
-    auto load = [&](int64_t j, int s) {
-        const uint32_t st = base + s * W::stage;
+    auto load = [&](int64_t j) {
         const int n = static_cast<int>(min(len - j * kC, int64_t(kC)));
         const int64_t r0 = b + j * kC;
-        load_rows<DKP, W::threads>(st + W::K, a.k, XT, r0, n, kh * a.dk, a.dk, tid);
-        load_rows<DKP, W::threads>(st + W::Q, a.q, XT, r0, n, kh * a.dk, a.dk, tid);
-        load_rows<BV, W::threads>(st + W::Y, a.dy, XT, r0, n, h * a.dv + c0, cols, tid);
+        load_rows<DKP, W::threads>(base + W::K, a.k, NS, r0, n, kh * a.dk, a.dk, tid);
+        load_rows<DKP, W::threads>(base + W::Q, a.q, NS, r0, n, kh * a.dk, a.dk, tid);
+        load_rows<BV, W::threads>(base + W::Y, a.dy, NS, r0, n, h * a.dv + c0, cols, tid);
         const int64_t at = (id0 + j) * a.Hv + h;
         const __nv_bfloat16* const tri = a.tri + at * (2 * NS) * int64_t(kC * kC);
 #pragma unroll
-        for (int pl = 0; pl < 2 * NS; ++pl) load_tri<W::threads>(st + W::T + pl * W::kPlane, tri + pl * kC * kC, tid);
-        if (tid < 48) copy16(st + W::vec + tid * 16, a.vec + at * kVecs * kC + tid * 4, true);
+        for (int pl = 0; pl < 2 * NS; ++pl) load_tri<W::threads>(base + W::T + pl * W::kPlane, tri + pl * kC * kC, tid);
+        if (tid < 48) copy16(base + W::vec + tid * 16, a.vec + at * kVecs * kC + tid * 4, true);
         copies_commit();
     };
 
@@ -77,20 +74,14 @@ __global__ void __launch_bounds__(BV * 2) gdr_back_kernel(const __grid_constant_
                 S[t][e] = d != nullptr && i < a.dk && c < a.dv ? d[static_cast<int64_t>(i) * a.dv + c] : 0.f;
             }
     }
-    const uint32_t keep = base + W::stages * W::stage + w * W::kKeep;
-    if (blocks > 0 && W::stages == 2) load(blocks - 1, 0);
+    const uint32_t keep = base + W::keep + w * W::kKeep;
+    const float* const vec = reinterpret_cast<const float*>(smem + W::vec);
     for (int64_t it = 0; it < blocks; ++it) {
         const int64_t j = blocks - 1 - it;
-        const int at = W::stages == 2 ? static_cast<int>(it & 1) : 0;
-        if (W::stages == 1) {
-            __syncthreads();
-            load(j, 0);
-        }
+        __syncthreads();
+        load(j);
         copies_wait<0>();
         __syncthreads();
-        if (W::stages == 2 && j > 0) load(j - 1, at ^ 1);
-        const uint32_t st = base + at * W::stage;
-        const float* const vec = reinterpret_cast<const float*>(smem + at * W::stage + W::vec);
         if (16 * w >= cols) continue;
         if (lane == 0) bulk_wait_read();
         __syncwarp();
@@ -102,7 +93,7 @@ __global__ void __launch_bounds__(BV * 2) gdr_back_kernel(const __grid_constant_
             terms_of<NS>(S[2 * kt], S[2 * kt + 1], s);
 #pragma unroll
             for (int t = 0; t < NS; ++t) stsm4(keep + t * (16 * DKP * 2) + state_at(L.rA, 2 * kt + L.uA), s[t]);
-            products<NS, XT, NS, false, 4>(x, s, W::kTile, [&](int np) { return st + W::K + tile_at<DKP>(16 * np + L.rB, 2 * kt + L.uB); });
+            products<NS, NS, NS, false, 4>(x, s, W::kTile, [&](int np) { return base + W::K + tile_at<DKP>(16 * np + L.rB, 2 * kt + L.uB); });
         }
         async_fence();
         __syncwarp();
@@ -118,10 +109,10 @@ __global__ void __launch_bounds__(BV * 2) gdr_back_kernel(const __grid_constant_
         float u[8][4] = {};
 #pragma unroll
         for (int kt = 0; kt < 4; ++kt) {   // A^T dY, and Q^T (scale e^gam dY)
-            uint32_t y[XT][4];
+            uint32_t y[NS][4];
 #pragma unroll
-            for (int t = 0; t < XT; ++t) ldsm4t(y[t], st + W::Y + t * W::kVal + tile_at<BV>(16 * kt + L.rAt, 2 * w + L.uAt));
-            products<XT, NS, NS, true, 4>(u, y, W::kPlane, [&](int np) { return st + W::A + tile_at<kC>(16 * kt + L.rBt, 2 * np + L.uBt); }, 0, kt + 1);
+            for (int t = 0; t < NS; ++t) ldsm4t(y[t], base + W::Y + t * W::kVal + tile_at<BV>(16 * kt + L.rAt, 2 * w + L.uAt));
+            products<NS, NS, NS, true, 4>(u, y, W::kPlane, [&](int np) { return base + W::A + tile_at<kC>(16 * kt + L.rBt, 2 * np + L.uBt); }, 0, kt + 1);
             // the operand's columns are rows: 16 kt + 2 qd + {0, 1}, and 8 on
             uint32_t f[NS][4];
 #pragma unroll
@@ -129,7 +120,7 @@ __global__ void __launch_bounds__(BV * 2) gdr_back_kernel(const __grid_constant_
                 const float2 eg = *reinterpret_cast<const float2*>(vec + 16 * kt + 8 * (i >> 1) + 2 * qd);
                 float v0 = 0.f, v1 = 0.f;
 #pragma unroll
-                for (int t = XT - 1; t >= 0; --t) {
+                for (int t = NS - 1; t >= 0; --t) {
                     v0 += __uint_as_float(y[t][i] << 16);
                     v1 += __uint_as_float(y[t][i] & 0xFFFF0000u);
                 }
@@ -138,7 +129,7 @@ __global__ void __launch_bounds__(BV * 2) gdr_back_kernel(const __grid_constant_
 #pragma unroll
                 for (int t = 0; t < NS; ++t) f[t][i] = o[t];
             }
-            products<NS, XT, NS, true, KT>(S, f, W::kTile, [&](int np) { return st + W::Q + tile_at<DKP>(16 * kt + L.rBt, 2 * np + L.uBt); });
+            products<NS, NS, NS, true, KT>(S, f, W::kTile, [&](int np) { return base + W::Q + tile_at<DKP>(16 * kt + L.rBt, 2 * np + L.uBt); });
         }
 #pragma unroll
         for (int nt = 0; nt < 8; ++nt) {
@@ -154,7 +145,7 @@ __global__ void __launch_bounds__(BV * 2) gdr_back_kernel(const __grid_constant_
         for (int kt = 0; kt < 4; ++kt) {   // W = T^T dU
             uint32_t f[NS][4];
             terms_of<NS>(u[2 * kt], u[2 * kt + 1], f);
-            products<NS, NS, NS, true, 4>(x, f, W::kPlane, [&](int np) { return st + W::T + tile_at<kC>(16 * kt + L.rBt, 2 * np + L.uBt); }, 0, kt + 1);
+            products<NS, NS, NS, true, 4>(x, f, W::kPlane, [&](int np) { return base + W::T + tile_at<kC>(16 * kt + L.rBt, 2 * np + L.uBt); }, 0, kt + 1);
         }
         if (lane == 0) bulk_wait_read();   // the state's tile has left long ago
         __syncwarp();
@@ -175,7 +166,7 @@ __global__ void __launch_bounds__(BV * 2) gdr_back_kernel(const __grid_constant_
                 }
             }
             terms_of<NS>(u[2 * kt], u[2 * kt + 1], o);
-            products<NS, XT, NS, true, KT>(S, o, W::kTile, [&](int np) { return st + W::K + tile_at<DKP>(16 * kt + L.rBt, 2 * np + L.uBt); });
+            products<NS, NS, NS, true, KT>(S, o, W::kTile, [&](int np) { return base + W::K + tile_at<DKP>(16 * kt + L.rBt, 2 * np + L.uBt); });
         }
         async_fence();
         __syncwarp();
@@ -185,35 +176,13 @@ __global__ void __launch_bounds__(BV * 2) gdr_back_kernel(const __grid_constant_
         }
         const int64_t r0 = b + j * kC;
         const int n = static_cast<int>(min(len - j * kC, int64_t(kC)));
-        if constexpr (sizeof(X) == 2) {   // dV, turned in the tile of dY
 #pragma unroll
-            for (int np = 0; np < 4; ++np) {
-                uint32_t f[4];
+        for (int nt = 0; nt < 8; ++nt)
 #pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    f[2 * t] = round2(x[2 * np + t][0], x[2 * np + t][1]);
-                    f[2 * t + 1] = round2(x[2 * np + t][2], x[2 * np + t][3]);
-                }
-                stsm4t(st + W::Y + tile_at<BV>(16 * np + L.rAt, 2 * w + L.uAt), f);
+            for (int e = 0; e < 4; ++e) {
+                const int row = 8 * nt + 2 * qd + (e & 1), c = vc + (e >> 1) * 8;
+                if (row < n && c < a.dv) static_cast<float*>(a.dv_out)[(r0 + row) * a.dv_ld + h * a.dv + c] = x[nt][e];
             }
-            __syncwarp();
-#pragma unroll
-            for (int i = lane; i < kC * 2; i += 32) {
-                const int row = i >> 1, u8 = 2 * w + (i & 1);
-                if (row < n && u8 * 8 < cols) {
-                    const uint4 v = *reinterpret_cast<const uint4*>(smem + at * W::stage + W::Y + tile_at<BV>(row, u8));
-                    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.dv_out) + (r0 + row) * a.dv_ld + h * a.dv + c0 + u8 * 8) = v;
-                }
-            }
-        } else {
-#pragma unroll
-            for (int nt = 0; nt < 8; ++nt)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int row = 8 * nt + 2 * qd + (e & 1), c = vc + (e >> 1) * 8;
-                    if (row < n && c < a.dv) static_cast<float*>(a.dv_out)[(r0 + row) * a.dv_ld + h * a.dv + c] = x[nt][e];
-                }
-        }
     }
     if (a.dh0 != nullptr && 16 * w < cols) {
         float* const d = a.dh0 + (static_cast<int64_t>(p) * a.Hv + h) * a.dk * a.dv;
@@ -465,27 +434,25 @@ __global__ void __launch_bounds__(BV * 4) gdr_back_tc_kernel(const __grid_consta
 // 16 warps: warp w has rows 16 (w % 4) .. of everything, and of each product's columns the (w / 4)-th part: 16 of the 64 columns
 // of M and N, a quarter of dk. A block walks the value columns in slices of SL, the next ones' states, writes and gradients on
 // their way; all operands come from shared memory as they were stored, so a slice needs one barrier.
-template <int XT, int DKP>
+template <int DKP>
 struct Grad {
-    static constexpr int NS = XT == 1 ? 2 : 3, NG = XT == 1 ? 1 : 3;   // NG: terms of what only rows' gradients take
-    static constexpr int SL = XT == 1 ? 32 : 16, stages = XT == 1 ? 3 : 2;
+    static constexpr int NS = kTerms, SL = 16, stages = 2;
     static constexpr int kTile = kC * DKP * 2, kPlane = kC * kC * 2, kVal = kC * SL * 2;
     static constexpr int kState = SL / 16 * NS * 16 * DKP * 2, kRows = SL / 16 * NS * kC * 32;
     // within a stage
-    static constexpr int S = 0, dS = kState, W = 2 * kState, U = W + kRows, Y = U + kRows, stage = Y + XT * kVal;
+    static constexpr int S = 0, dS = kState, W = 2 * kState, U = W + kRows, Y = U + kRows, stage = Y + NS * kVal;
     // the whole
-    static constexpr int K = 0, Q = XT * kTile, slices = 2 * XT * kTile, end = slices + stages * stage;
-    // over the slices when they are done: N o D and - M o D, the sums of dg, and the rows' gradients
-    static constexpr int ND = slices, XD = ND + NG * kPlane, Z = XD + NG * kPlane, last = Z + kC * 65 * 4;
+    static constexpr int K = 0, Q = NS * kTile, slices = 2 * NS * kTile, end = slices + stages * stage;
+    // over the slices when they are done: N o D and - M o D, and the sums of dg
+    static constexpr int ND = slices, XD = ND + NS * kPlane, Z = XD + NS * kPlane, last = Z + kC * 65 * 4;
     static constexpr int bytes = end > last ? end : last;
-    static_assert(ND + 2 * kTile <= bytes, "the rows' gradients leave through the place of the products");
     static constexpr int threads = 512;
 };
 
-template <int XT, int DKP, typename X>
+template <int DKP>
 __global__ void __launch_bounds__(512) gdr_grad_kernel(const __grid_constant__ Args a) {
-    using W = Grad<XT, DKP>;
-    constexpr int NS = W::NS, NG = W::NG, SL = W::SL, KT = DKP / 16, DN = DKP / 64;   // DN: tiles of 16 columns of dk of a warp
+    using W = Grad<DKP>;
+    constexpr int NS = W::NS, SL = W::SL, KT = DKP / 16, DN = DKP / 64;   // DN: tiles of 16 columns of dk of a warp
     extern __shared__ __align__(1024) unsigned char smem[];
     __shared__ __align__(16) float vec[kVecs * kC];
     __shared__ float sums[2][4][kC];   // a, e by quarters
@@ -524,12 +491,12 @@ __global__ void __launch_bounds__(512) gdr_grad_kernel(const __grid_constant__ A
                 copy16(st + W::W + i * 16, there ? wp + i * 8 : wp, there);
                 copy16(st + W::U + i * 16, there ? up + i * 8 : up, there);
             }
-            load_rows<SL, W::threads>(st + W::Y, a.dy, XT, b, n, h * a.dv + c0, cols, tid);
+            load_rows<SL, W::threads>(st + W::Y, a.dy, NS, b, n, h * a.dv + c0, cols, tid);
         }
         copies_commit();
     };
-    load_rows<DKP, W::threads>(base + W::K, a.k, XT, b, n, kh * a.dk, a.dk, tid);
-    load_rows<DKP, W::threads>(base + W::Q, a.q, XT, b, n, kh * a.dk, a.dk, tid);
+    load_rows<DKP, W::threads>(base + W::K, a.k, NS, b, n, kh * a.dk, a.dk, tid);
+    load_rows<DKP, W::threads>(base + W::Q, a.q, NS, b, n, kh * a.dk, a.dk, tid);
 #pragma unroll
     for (int s = 0; s + 1 < W::stages; ++s) load(s);
     for (int i = tid; i < kVecs * kC; i += W::threads) vec[i] = a.vec[unit * kVecs * kC + i];
@@ -548,23 +515,23 @@ __global__ void __launch_bounds__(512) gdr_grad_kernel(const __grid_constant__ A
         for (int kt = 0; kt < SL / 16; ++kt) {
             const uint32_t Sg = st + W::S + kt * (NS * 16 * DKP * 2), Dg = st + W::dS + kt * (NS * 16 * DKP * 2);
             const uint32_t Ug = st + W::U + kt * (NS * kC * 32);
-            uint32_t wa[NS][4], ya[XT][4], ua[NS][4];
+            uint32_t wa[NS][4], ya[NS][4], ua[NS][4];
 #pragma unroll
             for (int t = 0; t < NS; ++t) {
                 ldsm4(wa[t], st + W::W + kt * (NS * kC * 32) + t * (kC * 32) + rows_at(16 * mi + L.rA, L.uA));
                 ldsm4(ua[t], Ug + t * (kC * 32) + rows_at(16 * mi + L.rA, L.uA));
             }
 #pragma unroll
-            for (int t = 0; t < XT; ++t) ldsm4(ya[t], st + W::Y + t * W::kVal + tile_at<SL>(16 * mi + L.rA, 2 * kt + L.uA));
+            for (int t = 0; t < NS; ++t) ldsm4(ya[t], st + W::Y + t * W::kVal + tile_at<SL>(16 * mi + L.rA, 2 * kt + L.uA));
             if (qf <= mi) {   // W U^T and dY U^T
                 auto at = [&](int) { return Ug + rows_at(16 * qf + L.rB, L.uB); };
                 products<NS, NS, NS, false, 1>(m, wa, kC * 32, at);
-                products<XT, NS, NS, false, 1>(nn, ya, kC * 32, at);
+                products<NS, NS, NS, false, 1>(nn, ya, kC * 32, at);
             }
             // dY S^T, W S^T, U dS'^T
             auto sa = [&](int np) { return Sg + state_at(L.rBt, 2 * (DN * qf + np) + L.uBt); };
             auto da = [&](int np) { return Dg + state_at(L.rBt, 2 * (DN * qf + np) + L.uBt); };
-            products<XT, NS, NS, true, DN>(dq, ya, 16 * DKP * 2, sa);
+            products<NS, NS, NS, true, DN>(dq, ya, 16 * DKP * 2, sa);
             products<NS, NS, NS, true, DN>(k2, wa, 16 * DKP * 2, sa);
             products<NS, NS, NS, true, DN>(k3, ua, 16 * DKP * 2, da);
         }
@@ -595,15 +562,15 @@ __global__ void __launch_bounds__(512) gdr_grad_kernel(const __grid_constant__ A
     if (qf <= mi) {
 #pragma unroll
         for (int kt = 0; kt < KT; ++kt) {
-            uint32_t ka[XT][4], qa[XT][4];
+            uint32_t ka[NS][4], qa[NS][4];
 #pragma unroll
-            for (int t = 0; t < XT; ++t) {
+            for (int t = 0; t < NS; ++t) {
                 ldsm4(ka[t], base + W::K + t * W::kTile + tile_at<DKP>(16 * mi + L.rA, 2 * kt + L.uA));
                 ldsm4(qa[t], base + W::Q + t * W::kTile + tile_at<DKP>(16 * mi + L.rA, 2 * kt + L.uA));
             }
             auto at = [&](int) { return base + W::K + tile_at<DKP>(16 * qf + L.rB, 2 * kt + L.uB); };
-            products<XT, XT, XT, false, 1>(kk, ka, W::kTile, at);
-            products<XT, XT, XT, false, 1>(qk, qa, W::kTile, at);
+            products<NS, NS, NS, false, 1>(kk, ka, W::kTile, at);
+            products<NS, NS, NS, false, 1>(qk, qa, W::kTile, at);
         }
     }
     __syncthreads();   // every slice is done: their place is free
@@ -617,20 +584,20 @@ __global__ void __launch_bounds__(512) gdr_grad_kernel(const __grid_constant__ A
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
                 float d = 0.f;
-                if (j + c <= i) d = decay<XT>((vec[3 * kC + i] - vec[3 * kC + j + c]) + (vec[4 * kC + i] - vec[4 * kC + j + c]));
+                if (j + c <= i) d = decay<kTerms>((vec[3 * kC + i] - vec[3 * kC + j + c]) + (vec[4 * kC + i] - vec[4 * kC + j + c]));
                 const float N = a.scale * nn[t][2 * e + c], M = vec[kC + i] * m[t][2 * e + c];
                 if (j + c == i) diag[i] = m[t][2 * e + c];
                 x[c] = j + c <= i ? d * N : 0.f;
                 y[c] = j + c < i ? -d * M : 0.f;
                 Z[i * 65 + j + c] = j + c < i ? fmaf(x[c], qk[t][2 * e + c], y[c] * kk[t][2 * e + c]) : 0.f;
             }
-            uint32_t o[NG];
-            split2<NG>(x[0], x[1], o);
+            uint32_t o[NS];
+            split2<NS>(x[0], x[1], o);
 #pragma unroll
-            for (int p = 0; p < NG; ++p) st_word(base + W::ND + p * W::kPlane + tile_at<kC>(i, j >> 3) + qd * 4, o[p]);
-            split2<NG>(y[0], y[1], o);
+            for (int p = 0; p < NS; ++p) st_word(base + W::ND + p * W::kPlane + tile_at<kC>(i, j >> 3) + qd * 4, o[p]);
+            split2<NS>(y[0], y[1], o);
 #pragma unroll
-            for (int p = 0; p < NG; ++p) st_word(base + W::XD + p * W::kPlane + tile_at<kC>(i, j >> 3) + qd * 4, o[p]);
+            for (int p = 0; p < NS; ++p) st_word(base + W::XD + p * W::kPlane + tile_at<kC>(i, j >> 3) + qd * 4, o[p]);
         }
     // the rows' scalars: a = e^gam (scale q . (S dY) - beta k . (S W)), e = e^(gam_last - gam) k . (dS' u)
 #pragma unroll
@@ -642,7 +609,7 @@ __global__ void __launch_bounds__(512) gdr_grad_kernel(const __grid_constant__ A
             const uint32_t at = tile_at<DKP>(r, 2 * DN * qf + t) + qd * 4;
             float q[2] = {}, k[2] = {};
 #pragma unroll
-            for (int p = XT - 1; p >= 0; --p) {
+            for (int p = NS - 1; p >= 0; --p) {
                 const uint32_t x = *reinterpret_cast<const uint32_t*>(smem + W::Q + p * W::kTile + at);
                 const uint32_t y = *reinterpret_cast<const uint32_t*>(smem + W::K + p * W::kTile + at);
                 q[0] += __uint_as_float(x << 16);
@@ -683,22 +650,22 @@ __global__ void __launch_bounds__(512) gdr_grad_kernel(const __grid_constant__ A
     for (int kt = 0; kt < 4; ++kt) {
         auto ka = [&](int np) { return base + W::K + tile_at<DKP>(16 * kt + L.rBt, 2 * (DN * qf + np) + L.uBt); };
         auto qa = [&](int np) { return base + W::Q + tile_at<DKP>(16 * kt + L.rBt, 2 * (DN * qf + np) + L.uBt); };
-        uint32_t f[NG][4];
+        uint32_t f[NS][4];
         if (kt <= mi) {
 #pragma unroll
-            for (int p = 0; p < NG; ++p) ldsm4(f[p], base + W::ND + p * W::kPlane + tile_at<kC>(16 * mi + L.rA, 2 * kt + L.uA));
-            products<NG, XT, NG, true, DN>(dq, f, W::kTile, ka);
+            for (int p = 0; p < NS; ++p) ldsm4(f[p], base + W::ND + p * W::kPlane + tile_at<kC>(16 * mi + L.rA, 2 * kt + L.uA));
+            products<NS, NS, NS, true, DN>(dq, f, W::kTile, ka);
 #pragma unroll
-            for (int p = 0; p < NG; ++p) ldsm4(f[p], base + W::XD + p * W::kPlane + tile_at<kC>(16 * mi + L.rA, 2 * kt + L.uA));
-            products<NG, XT, NG, true, DN>(k3, f, W::kTile, ka);
+            for (int p = 0; p < NS; ++p) ldsm4(f[p], base + W::XD + p * W::kPlane + tile_at<kC>(16 * mi + L.rA, 2 * kt + L.uA));
+            products<NS, NS, NS, true, DN>(k3, f, W::kTile, ka);
         }
         if (kt >= mi) {
 #pragma unroll
-            for (int p = 0; p < NG; ++p) ldsm4t(f[p], base + W::XD + p * W::kPlane + tile_at<kC>(16 * kt + L.rAt, 2 * mi + L.uAt));
-            products<NG, XT, NG, true, DN>(k3, f, W::kTile, ka);
+            for (int p = 0; p < NS; ++p) ldsm4t(f[p], base + W::XD + p * W::kPlane + tile_at<kC>(16 * kt + L.rAt, 2 * mi + L.uAt));
+            products<NS, NS, NS, true, DN>(k3, f, W::kTile, ka);
 #pragma unroll
-            for (int p = 0; p < NG; ++p) ldsm4t(f[p], base + W::ND + p * W::kPlane + tile_at<kC>(16 * kt + L.rAt, 2 * mi + L.uAt));
-            products<NG, XT, NG, true, DN>(k3, f, W::kTile, qa);
+            for (int p = 0; p < NS; ++p) ldsm4t(f[p], base + W::ND + p * W::kPlane + tile_at<kC>(16 * kt + L.rAt, 2 * mi + L.uAt));
+            products<NS, NS, NS, true, DN>(k3, f, W::kTile, qa);
         }
     }
     // dg. Column by column sums from the bottom (8 rows a thread, then what lies below them), then row by row up to the diagonal.
@@ -748,33 +715,6 @@ __global__ void __launch_bounds__(512) gdr_grad_kernel(const __grid_constant__ A
         }
     }
     // the rows' gradients: of a head's own queries and keys, or a value head's share of them in float32
-    if (a.part == nullptr && sizeof(X) == 2) {
-        __syncthreads();   // the sums of dg have been read
-#pragma unroll
-        for (int np = 0; np < DN; ++np) {
-            uint32_t f[4], k[4];
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                f[2 * t] = round2(dq[2 * np + t][0], dq[2 * np + t][1]);
-                f[2 * t + 1] = round2(dq[2 * np + t][2], dq[2 * np + t][3]);
-                k[2 * t] = round2(k3[2 * np + t][0], k3[2 * np + t][1]);
-                k[2 * t + 1] = round2(k3[2 * np + t][2], k3[2 * np + t][3]);
-            }
-            const uint32_t at = tile_at<DKP>(16 * mi + L.rA, 2 * (DN * qf + np) + L.uA);
-            stsm4(base + W::ND + at, f);
-            stsm4(base + W::ND + W::kTile + at, k);
-        }
-        __syncthreads();
-        for (int i = tid; i < kC * (DKP / 8); i += W::threads) {
-            const int r = i / (DKP / 8), u = i % (DKP / 8);
-            if (r >= n || u * 8 >= a.dk) continue;
-            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.dq) + (b + r) * a.dq_ld + kh * a.dk + u * 8) =
-                *reinterpret_cast<const uint4*>(smem + W::ND + tile_at<DKP>(r, u));
-            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.dk_out) + (b + r) * a.dk_ld + kh * a.dk + u * 8) =
-                *reinterpret_cast<const uint4*>(smem + W::ND + W::kTile + tile_at<DKP>(r, u));
-        }
-        return;
-    }
     const int64_t HD = static_cast<int64_t>(a.Hv) * a.dk;
 #pragma unroll
     for (int t = 0; t < 2 * DN; ++t)
@@ -1286,14 +1226,13 @@ cudaError_t big_smem(K kernel, int bytes) {
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
 }
 
-template <int XT, int DKP, int BV>
+template <int DKP>
 cudaError_t back(const Args& a, cudaStream_t cs) {
-    using X = std::conditional_t<XT == 1, __nv_bfloat16, float>;
-    using W = Back<XT, DKP, BV>;
-    auto* const k = gdr_back_kernel<XT, DKP, BV, X>;
+    using W = Back<DKP>;
+    auto* const k = gdr_back_kernel<DKP>;
     const cudaError_t e = big_smem(k, W::bytes);
     if (e != cudaSuccess) return e;
-    const int64_t grid = static_cast<int64_t>(a.P) * a.Hv * ((a.dv + BV - 1) / BV);
+    const int64_t grid = static_cast<int64_t>(a.P) * a.Hv * ((a.dv + W::BV - 1) / W::BV);
     return launch_dependent(k, dim3(static_cast<unsigned>(grid)), dim3(W::threads), W::bytes, cs, a);
 }
 
@@ -1309,11 +1248,10 @@ cudaError_t grad_tc(const Args& a, int64_t blocks, cudaStream_t cs) {
     return launch_dependent(k, dim3(static_cast<unsigned>(std::min<int64_t>(blocks * a.Hv, 152))), dim3(W::threads), W::bytes, cs, a, m);
 }
 
-template <int XT, int DKP>
+template <int DKP>
 cudaError_t grad(const Args& a, int64_t blocks, cudaStream_t cs) {
-    using X = std::conditional_t<XT == 1, __nv_bfloat16, float>;
-    using W = Grad<XT, DKP>;
-    auto* const k = gdr_grad_kernel<XT, DKP, X>;
+    using W = Grad<DKP>;
+    auto* const k = gdr_grad_kernel<DKP>;
     const cudaError_t e = big_smem(k, W::bytes);
     if (e != cudaSuccess) return e;
     return launch_dependent(k, dim3(static_cast<unsigned>(blocks * a.Hv)), dim3(W::threads), W::bytes, cs, a);
@@ -1391,11 +1329,11 @@ extern "C" sdm_status sdm_gdr_backward(const sdm_gdr_shape* shape, const void* q
     }
     const bool narrow = padded(shape->dk) == 64, bf16 = shape->x_dtype == SDM_BF16;
     if (e == cudaSuccess)
-        e = bf16 ? (narrow ? back_bf16<64>(a, cs) : back_bf16<128>(a, cs)) : (narrow ? back<3, 64, 32>(a, cs) : back<3, 128, 32>(a, cs));
+        e = bf16 ? (narrow ? back_bf16<64>(a, cs) : back_bf16<128>(a, cs)) : (narrow ? back<64>(a, cs) : back<128>(a, cs));
     const int64_t blocks = blocks_of(shape);
     if (e == cudaSuccess && shape->rows > 0)
         e = bf16 ? (narrow ? grad_tc<64>(a, blocks, cs) : grad_tc<128>(a, blocks, cs))
-                 : (narrow ? grad<3, 64>(a, blocks, cs) : grad<3, 128>(a, blocks, cs));
+                 : (narrow ? grad<64>(a, blocks, cs) : grad<128>(a, blocks, cs));
     if (e == cudaSuccess && shape->rows > 0 && a.part != nullptr) {
         const int64_t grid = std::min<int64_t>((shape->rows * (kn / 4) * 2 + 255) / 256, 152 * 16);
         e = launch_dependent(bf16 ? gdr_join_kernel<__nv_bfloat16> : gdr_join_kernel<float>, dim3(static_cast<unsigned>(grid)), dim3(256), 0,

@@ -495,7 +495,8 @@ int pow2(int n) {
     return p;
 }
 
-// The threads of a group, U and the rows of a block: the U that leaves the fewest places idle, 4 where it makes no difference.
+// The threads of a group, U and the rows of a block: the U that leaves the fewest places idle, 4 where it makes no difference; 8 where a
+// row's threads fit a block no other way, of which more than 256 are left.
 // 0: a row's threads do not fit a block.
 int geometry(const sdm_norm_shape* s, NormArgs* a) {
     memset(a, 0, sizeof(*a));
@@ -579,7 +580,7 @@ extern "C" sdm_status sdm_block_norm(const sdm_norm_shape* shape, const void* o,
     const int64_t blocks = std::min<int64_t>((a.rows + a.rows_block - 1) / a.rows_block, 152 * (2048 / threads));
     const cudaError_t e = by_type(shape, U, [&](auto t, auto u, auto gate) {
         constexpr int N = decltype(u)::value, G = decltype(gate)::value;
-        return launch_dependent(threads <= 256 ? norm_fwd_kernel<decltype(t), N, G, 256> : norm_fwd_kernel<decltype(t), N, G, kNormThreads>, dim3(static_cast<unsigned>(blocks)), dim3(threads), 0,
+        return launch_dependent(threads <= 256 ? norm_fwd_kernel<decltype(t), N, G, N == 8 ? kNormThreads : 256> : norm_fwd_kernel<decltype(t), N, G, kNormThreads>, dim3(static_cast<unsigned>(blocks)), dim3(threads), 0,
                                 reinterpret_cast<cudaStream_t>(stream), a);
     });
     return e == cudaSuccess ? SDM_OK : SDM_ERR_CUDA;
@@ -625,7 +626,7 @@ extern "C" sdm_status sdm_block_norm_backward(const sdm_norm_shape* shape, const
     if (shape->rows > 0)
         e = by_type(shape, U, [&](auto t, auto u, auto gate) {
             constexpr int N = decltype(u)::value, G = decltype(gate)::value;
-            auto* const k = threads <= 256 ? norm_bwd_kernel<decltype(t), N, G, 256> : norm_bwd_kernel<decltype(t), N, G, kNormThreads>;
+            auto* const k = threads <= 256 ? norm_bwd_kernel<decltype(t), N, G, N == 8 ? kNormThreads : 256> : norm_bwd_kernel<decltype(t), N, G, kNormThreads>;
             if (smem > 47 * 1024) {
                 const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
                 if (e != cudaSuccess) return e;
