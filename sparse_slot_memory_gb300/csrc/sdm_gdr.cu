@@ -66,17 +66,21 @@ __global__ void __launch_bounds__(128, XT == 1 ? 4 : 2) gdr_prepare_kernel(const
 #pragma unroll
         for (int np = 0; np < 4; ++np) {
             if (np > w) continue;
+            uint32_t f[XT][4];
 #pragma unroll
-            for (int x = 0; x < XT; ++x) {
-                uint32_t f[4];
-                ldsm4(f, K + x * kTile + tile_at<DKP>(16 * np + L.rB, 2 * kt + L.uB));
+            for (int x = 0; x < XT; ++x) ldsm4(f[x], K + x * kTile + tile_at<DKP>(16 * np + L.rB, 2 * kt + L.uB));
 #pragma unroll
-                for (int y = 0; y < XT - x; ++y) {
-                    mma(kk[2 * np], ka[y], f[0], f[1]);
-                    mma(kk[2 * np + 1], ka[y], f[2], f[3]);
-                    mma(qk[2 * np], qa[y], f[0], f[1]);
-                    mma(qk[2 * np + 1], qa[y], f[2], f[3]);
-                }
+            for (int e = 0; e < 2; ++e) {
+                auto step = [&](float (&sum)[4], const uint32_t (&a)[XT][4]) {
+                    add_step<XT>(sum, [&](float (&t)[4]) {
+#pragma unroll
+                        for (int x = XT - 1; x >= 0; --x)
+#pragma unroll
+                            for (int y = XT - 1 - x; y >= 0; --y) mma(t, a[y], f[x][2 * e], f[x][2 * e + 1]);
+                    });
+                };
+                step(kk[2 * np + e], ka);
+                step(qk[2 * np + e], qa);
             }
         }
     }
@@ -187,15 +191,20 @@ __global__ void __launch_bounds__(128, XT == 1 ? 4 : 2) gdr_prepare_kernel(const
 #pragma unroll
                 for (int p = 0; p < NS; ++p) ldsm4t(t[p], T + p * kPlane + tile_at<kC>(c0 + 16 * kt + L.rBt, c / 8));
 #pragma unroll
-                for (int m = 0; m < M; ++m) {
+                for (int m = 0; m < M; ++m)
+                    add_step<NS>(y[m], [&](float (&sum)[4]) {
 #pragma unroll
-                    for (int p = 0; p < NS; ++p) {
-                        uint32_t f[4];
-                        ldsm4(f, N + p * kPlane + tile_at<kC>(r0 + 16 * m + L.rA, c0 / 8 + 2 * kt + L.uA));
+                        for (int x = 0; x < NS; ++x) {
+                            const int p = NS == 3 ? NS - 1 - x : x;
+                            uint32_t f[4];
+                            ldsm4(f, N + p * kPlane + tile_at<kC>(r0 + 16 * m + L.rA, c0 / 8 + 2 * kt + L.uA));
 #pragma unroll
-                        for (int q = 0; q < NS - p; ++q) mma(y[m], f, t[q][0], t[q][1]);
-                    }
-                }
+                            for (int z = 0; z < NS - p; ++z) {
+                                const int q = NS == 3 ? NS - 1 - p - z : z;
+                                mma(sum, f, t[q][0], t[q][1]);
+                            }
+                        }
+                    });
             }
             uint32_t yt[M][2][NS];
 #pragma unroll
@@ -210,15 +219,20 @@ __global__ void __launch_bounds__(128, XT == 1 ? 4 : 2) gdr_prepare_kernel(const
             for (int m = 0; m < M; ++m) {
                 float o[4] = {};
 #pragma unroll
-                for (int kt = 0; kt <= m; ++kt) {
+                for (int kt = 0; kt <= m; ++kt)
+                    add_step<NS>(o, [&](float (&sum)[4]) {
 #pragma unroll
-                    for (int p = 0; p < NS; ++p) {
-                        uint32_t f[4];
-                        ldsm4(f, T + p * kPlane + tile_at<kC>(r0 + 16 * m + L.rA, r0 / 8 + 2 * kt + L.uA));
+                        for (int x = 0; x < NS; ++x) {
+                            const int p = NS == 3 ? NS - 1 - x : x;
+                            uint32_t f[4];
+                            ldsm4(f, T + p * kPlane + tile_at<kC>(r0 + 16 * m + L.rA, r0 / 8 + 2 * kt + L.uA));
 #pragma unroll
-                        for (int q = 0; q < NS - p; ++q) mma(o, f, yt[kt][0][q], yt[kt][1][q]);
-                    }
-                }
+                            for (int z = 0; z < NS - p; ++z) {
+                                const int q = NS == 3 ? NS - 1 - p - z : z;
+                                mma(sum, f, yt[kt][0][q], yt[kt][1][q]);
+                            }
+                        }
+                    });
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     uint32_t t[NS];
