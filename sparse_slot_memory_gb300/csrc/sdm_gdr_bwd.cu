@@ -743,15 +743,23 @@ __global__ void __launch_bounds__(512) gdr_grad_kernel(const __grid_constant__ A
 // cycles, in which shared memory is read all the time) and <dS', S>; the decays; then the gates' gradients beside the rows'. A
 // block's sums fill tensor memory, so the next block's products wait until these are taken in. Left out one at a time, <dS', S> was
 // worth 36 us of 725, the sums with queries and keys 19, the slices' products 50; the gates' gradients 118 and the rows' 147 before
-// half of the warps took each and the rows left through shared memory (630).
+// half of the warps took each and the rows left through shared memory (630). M o D and N o D enter D5 and D6 as two terms like all
+// that is computed, so that the rows' gradients have their rounding's error alone (0.0017; one term: 0.0021, and 18 us less).
 template <int DKP>
 struct GradTc {
     // a slice: U's two terms, [W; dY], [W's rests; 0], S's and dS's two terms, all in units of 8 value columns
     static constexpr int kUnit = DKP * 16, kTerm = 4 * kUnit, kStates = 2 * kTerm;
     static constexpr int U = 0, WY = 8192, S = WY + 16384, dS = S + kStates, stage = dS + kStates;
     static constexpr int kKQ = 2 * kC * DKP * 2;             // [K; Q], two of them: tiles of 128 rows for 64 columns
-    static constexpr int slices = 2 * kKQ, XN = slices + 2 * stage, Z = XN + 16384, bytes = Z + kC * 65 * 4;
+    // [-(M o D); N o D] in two terms (as an operand of 128 columns its transpose is read 16 KB beyond either), the slices, the terms of dg
+    static constexpr int XN = 2 * kKQ, slices = XN + 2 * 16384, Z = slices + 2 * stage, bytes = Z + 16 * (17 + 33 + 49 + 65) * 4;
+    static_assert(2 * stage >= 16384, "the operand's end");
     static constexpr int threads = 512;
+    // The place of row i of dg's terms: rows of block b of 16 have the 16 b + 16 columns up to their diagonal block's end
+    __device__ static __forceinline__ int row(int i) {
+        const int b = i >> 4;
+        return 128 * b * (b + 1) + 16 * b + (i & 15) * (16 * b + 17);
+    }
 };
 
 template <int DKP>
@@ -1007,15 +1015,20 @@ __global__ void __launch_bounds__(512, 1) gdr_grad_tc_kernel(const __grid_consta
             }
             __syncwarp();
 #pragma unroll
-            for (int q = 0; q < 2; ++q)
-                *reinterpret_cast<uint4*>(smem + W::XN + stacked_at(r, 2 * quarter + q)) =
-                    make_uint4(round2(x[8 * q], x[8 * q + 1]), round2(x[8 * q + 2], x[8 * q + 3]), round2(x[8 * q + 4], x[8 * q + 5]),
-                               round2(x[8 * q + 6], x[8 * q + 7]));
+            for (int q = 0; q < 2; ++q) {
+                uint32_t hi[4], lo[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) terms2(pack2(x[8 * q + 2 * e], x[8 * q + 2 * e + 1]), hi[e], lo[e]);
+                unsigned char* const to = smem + W::XN + stacked_at(r, 2 * quarter + q);
+                *reinterpret_cast<uint4*>(to) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                *reinterpret_cast<uint4*>(to + 16384) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            }
             async_fence();
             tensor::fence_before();
-            if (key) {
+            float* const mine_z = Z + W::row(i) + 16 * quarter;
+            if (key && quarter <= own) {
 #pragma unroll
-                for (int c = 0; c < 16; ++c) Z[i * 65 + 16 * quarter + c] = y[c];
+                for (int c = 0; c < 16; ++c) mine_z[c] = y[c];
             }
             __syncthreads();
             if (w == 0 && tensor::elect()) {
@@ -1024,16 +1037,18 @@ __global__ void __launch_bounds__(512, 1) gdr_grad_tc_kernel(const __grid_consta
                 const uint64_t k = tensor::swizzled(KQ, 16384), q = k + 8192 / 16, X = tensor::operand(base + W::XN, 2048, 128);
                 const uint64_t Xt = tensor::operand(base + W::XN, 128, 2048);
 #pragma unroll
-                for (int ks = 0; ks < 4; ++ks) {
-                    tensor::mma(D5, X + ks * 256, k + ks * 128, out5, ks > 0);
-                    tensor::mma(D6, Xt + 64 + ks * 16, q + ks * 128, out6, ks > 0);
-                    tensor::mma(D6, Xt + ks * 16, k + ks * 128, out6, true);
-                }
+                for (int t = 0; t < 2; ++t)
+#pragma unroll
+                    for (int ks = 0; ks < 4; ++ks) {
+                        tensor::mma(D5, X + t * 1024 + ks * 256, k + ks * 128, out5, t + ks > 0);
+                        tensor::mma(D6, Xt + t * 1024 + 64 + ks * 16, q + ks * 128, out6, t + ks > 0);
+                        tensor::mma(D6, Xt + t * 1024 + ks * 16, k + ks * 128, out6, true);
+                    }
                 tensor::commit(bar + 16);
             }
-            if (!key) {
+            if (!key && quarter <= own) {
 #pragma unroll
-                for (int c = 0; c < 16; ++c) Z[i * 65 + 16 * quarter + c] += y[c];
+                for (int c = 0; c < 16; ++c) mine_z[c] += y[c];
             }
         }
         // the rows' products with their own queries and keys
@@ -1075,7 +1090,10 @@ __global__ void __launch_bounds__(512, 1) gdr_grad_tc_kernel(const __grid_consta
         // Half of the warps write dg and dbeta, the others meanwhile the rows' gradients.
         if (quarter >= 2) {
             const int g = tid - 256;
-            auto sync = [&]() { asm volatile("bar.sync 1, 256;" ::: "memory"); };
+            auto sync = [&]() {
+                __syncwarp();
+                asm volatile("bar.sync 1, 256;" ::: "memory");
+            };
             if (g < kC) {
                 const float eg = vec[g];
                 auto four = [&](int x) { return (sums[x][0][g] + sums[x][1][g]) + (sums[x][2][g] + sums[x][3][g]); };
@@ -1084,26 +1102,33 @@ __global__ void __launch_bounds__(512, 1) gdr_grad_tc_kernel(const __grid_consta
             }
             // Column by column sums from the bottom (16 rows a thread, then what lies below them), then row by row up to the diagonal.
             const int j = g & 63, part = g >> 6;
+            float* const column = Z + W::row(16 * part) + j;
+            const int pitch = 16 * part + 17;
+            float (*const parts)[68] = far;   // whose decays have been taken
             float run = 0.f, z[16];
+            if (j >> 4 <= part) {
 #pragma unroll
-            for (int x = 15; x >= 0; --x) {
-                run += Z[(16 * part + x) * 65 + j];
-                z[x] = run;
+                for (int x = 15; x >= 0; --x) {
+                    run += column[x * pitch];
+                    z[x] = run;
+                }
             }
-            Z[16 * part * 65 + j] = run;   // a part's sum where its first row was
+            parts[part][j] = run;
             sync();
-            float below = 0.f;
-            for (int q = 3; q > part; --q) below += Z[16 * q * 65 + j];
-            sync();
+            if (j >> 4 <= part) {
+                float below = 0.f;
+                for (int q = 3; q > part; --q) below += parts[q][j];
 #pragma unroll
-            for (int x = 0; x < 16; ++x) Z[(16 * part + x) * 65 + j] = z[x] + below;
+                for (int x = 0; x < 16; ++x) column[x * pitch] = z[x] + below;
+            }
             sync();
             const int t = g >> 2, fourth = g & 3;
+            const float* const row = Z + W::row(t);
             float x = 0.f;
 #pragma unroll
             for (int e = 0; e < 16; ++e) {
                 const int c = 4 * e + fourth;   // a column before row t, its end's share, and a row from t on
-                x += c < t ? Z[t * 65 + c] + share[1][c] : share[0][c];
+                x += c < t ? row[c] + share[1][c] : share[0][c];
             }
             x += __shfl_xor_sync(kFull, x, 1);
             x += __shfl_xor_sync(kFull, x, 2);
