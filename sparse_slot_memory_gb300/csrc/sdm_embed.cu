@@ -8,6 +8,7 @@
 // a part of 16 where an id has more, the frequent words; their parts' sums wait in the workspace and are joined in order by a
 // last kernel. No sum depends on timing. Bound by HBM: the table's gradient is written once (float32, 131072 x 2048: 1.07 GB),
 // the tokens' rows are read once. Measured: that step's 278 us of 238; the zeros alone run at 6.0 TB/s, the sort (38 us) beside them.
+// The gradient alone of 16384, 32768, 65536, 131072 and 262144 tokens takes 209, 240, 295, 393 and 648 us of 168, 178, 198, 238 and 317.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -312,7 +313,7 @@ __device__ __forceinline__ void put_row(const EmbedArgs& a, int v, int c, int n,
 template <typename TT, typename T>
 __global__ void __launch_bounds__(kThreads, 4) embed_bwd_kernel(const __grid_constant__ EmbedArgs a) {
     start_dependent();
-    constexpr int F = sizeof(T) == 2 ? 4 : 2;   // tokens of 512 columns on their way: what 64 registers hold
+    constexpr int F = sizeof(T) == 2 ? 4 : 2;   // tokens of 512 columns on their way: what 64 registers hold but for 80 bytes a thread, which bfloat16 rows spill
     const int lane = threadIdx.x & 31, slices = (a.D + kSlice - 1) / kSlice;
     const int32_t* const tok = a.tok[(a.passes + 1) & 1];
     const int64_t units = static_cast<int64_t>(a.count[0]) * slices, stride = static_cast<int64_t>(gridDim.x) * kWarps;

@@ -31,7 +31,7 @@ __global__ void __launch_bounds__(256) gdr_split_kernel(const float* x, int64_t 
 // A block of 4 warps for each block of rows and key head; warp w holds rows 16 w .. of K K^T and Q K^T, and for each value head of
 // the key head weighs them by its decays. T is built from its 16 x 16 blocks: those on the diagonal row by row in float32 (a
 // column a lane), those below by T_21 = -T_22 (N_21 T_11), first for 32 rows, then for 64, in products of terms. Bound by the waits of
-// this chain at four blocks an SM (41 % of the issue slots): 8320 blocks of a head of 128 in 183 us; the bytes would take 80.
+// this chain at four blocks an SM (41 % of the issue slots): 8320 blocks of a head of 128 in 185 us; the bytes would take 80.
 template <int XT, int DKP>
 __global__ void __launch_bounds__(128, XT == 1 ? 4 : 2) gdr_prepare_kernel(const __grid_constant__ Args a) {
     constexpr int kTile = kC * DKP * 2, kPlane = kC * kC * 2, NS = XT == 1 ? 2 : 3;
@@ -291,7 +291,8 @@ __global__ void __launch_bounds__(128, XT == 1 ? 4 : 2) gdr_prepare_kernel(const
 // ---- the walk, float32 rows ---------------------------------------------------------------------------------------
 // A warp owns 16 of a head's value columns and keeps its part of the state transposed, S^T [16 x dk], in the accumulators of its
 // matrix instructions (mma.sync): an accumulator's layout is an operand's too, so the chain S -> R -> U -> S' never leaves the
-// warp's registers. Three terms would not fit beside one another as operands in shared memory, as the tensor core above them wants.
+// warp's registers. A block of rows takes 17 us (a sequence of 21 of them in both directions 815), which is this one chain: two warps a
+// block, a stage of 160 KB, of which the tensor core's operands in three terms would leave room for no second one either.
 template <int DKP>
 struct Walk {
     static constexpr int BV = 32;   // value columns of a block
@@ -477,7 +478,7 @@ __global__ void __launch_bounds__(Walk<DKP>::threads) gdr_walk_kernel(const __gr
 // write without conflicts. What bounds it is this chain: with 128 columns 2300 cycles of products, then 4 turns of a barrier,
 // loads from tensor memory and the cut into terms. Tiles of K and Q arrive a block ahead, V and T while the state is brought up
 // to date, in boxes of a tensor map and bulk copies; saved states leave in bulk copies of their operands. Measured, 8 x 4096 rows of 16
-// heads of 128: 288 us with what is saved for the backward (1.6 GB: 5.5 TB/s).
+// heads of 128: 290 us with what is saved for the backward (1.6 GB: 5.5 TB/s).
 //
 // Where the walks are few and long, every sequence is cut into segments that are walked side by side, twice. A segment makes
 // M S + B of the state S before it: the first time (FIRST) blocks start from zeros for B, and others, without V, from the identity
@@ -809,7 +810,7 @@ __global__ void __launch_bounds__(256) gdr_chain_kernel(const __grid_constant__ 
 // ---- one token of every request -----------------------------------------------------------------------------------
 // y = scale (e^g S^T q + (k.q) u), so one look at the state gives S^T k and S^T q together; it stays in registers until
 // u is known, and is written once. Bound by HBM: 8 bytes an element of the state. 32 requests of 16 heads of 128 x 128: 11.0 us in a
-// graph (6.1 TB/s), 15.4 with the host's call.
+// graph (6.1 TB/s), 15.7 with the host's call.
 struct StepArgs {
     const void* q;
     const void* k;

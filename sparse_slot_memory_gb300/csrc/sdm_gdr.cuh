@@ -482,8 +482,9 @@ inline int padded(int d) { return d <= 64 ? 64 : 128; }
 inline int64_t blocks_of(const sdm_gdr_shape* s) { return s->rows / kC + s->P; }
 
 // Value columns of a block of a walk of bfloat16 rows, of `heads` walks of dv (and dk, for a segment's move) columns. A block of rows
-// took 1.8 us with 32, 2.1 with 64 and 3.6 with 128 columns (keys of 64), and the SMs hold one block each: the fewest rounds of the
-// grid times that (`time`, in 0.36 us a block of rows). 12 prompts of 16 heads of 128 took 294 us with 64 and 402 with 128, 8 of 4096 rows 380 with 64 and 349 with 128,
+// took 1.8 us with 32, 2.1 with 64 and 3.6 with 128 columns (keys of 64) on an SM of its own, and the rule takes the SMs to hold one
+// block each: the fewest rounds of the grid times that (`time`, in 0.36 us a block of rows). With keys of 64 two blocks of 32 columns, or
+// of 64 in segments' first walk, do fit an SM, which the rule leaves out: it then counts rounds that run side by side. 12 prompts of 16 heads of 128 took 294 us with 64 and 402 with 128, 8 of 4096 rows 380 with 64 and 349 with 128,
 // one of 8 heads 952 with 32 and 1143 with 64.
 inline int columns(int64_t heads, int dv, int dk = 0, int64_t* time = nullptr) {
     int best = 32;

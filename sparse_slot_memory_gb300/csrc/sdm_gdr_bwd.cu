@@ -201,7 +201,7 @@ __global__ void __launch_bounds__(Back<DKP>::threads) gdr_back_kernel(const __gr
 // As the forward's walk (sdm_gdr.cu), with dS in the threads' registers: per block of rows
 //   K dS'  ->  x = e^(gam_last - gam) o K dS'  ->  W = T^T x + (scale A T)^T dY  ->  dS = e^gam_last dS' + Q^T (scale e^gam o dY) - K^T (e^gam o beta o W).
 // What dY gives by itself is multiplied beside the chain; its scaled rows take the place of the state's terms while those are not needed.
-// Measured, 8 x 4096 rows of 16 heads of 128: 345 us (1.6 GB: 4.6 TB/s). dV leaves in 16 bytes a thread, which the forward's answers
+// Measured, 8 x 4096 rows of 16 heads of 128: 344 us (1.6 GB: 4.6 TB/s). dV leaves in 16 bytes a thread, which the forward's answers
 // do not: no place in shared memory is free for whole rows at that point.
 template <int DKP, int BV>
 __global__ void __launch_bounds__(BV * 4) gdr_back_tc_kernel(const __grid_constant__ Args a, const __grid_constant__ Maps maps) {
@@ -739,7 +739,7 @@ __global__ void __launch_bounds__(512) gdr_grad_kernel(const __grid_constant__ A
 // so a thread that has row r of tensor memory has row r of the key's side (r < 64) or row r - 64 of the query's, and a quarter of its
 // columns. Resident blocks take (block of rows, head) after (block, head); the next ones' rows and states arrive, two slices of 32
 // value columns ahead, while these are finished. Its floor is HBM: 272 KB a block of a head of 128, of which the states are 128 (6.7
-// us on each of 152 SMs; measured 11.5). What bounds it is the chain of a block's phases: four slices of copies, products (1400
+// us on each of 152 SMs; measured 12.0). What bounds it is the chain of a block's phases: four slices of copies, products (1400
 // cycles, in which shared memory is read all the time) and <dS', S>; the decays; then the gates' gradients beside the rows'. A
 // block's sums fill tensor memory, so the next block's products wait until these are taken in. Left out one at a time, <dS', S> was
 // worth 36 us of 725, the sums with queries and keys 19, the slices' products 50; the gates' gradients 118 and the rows' 147 before

@@ -9,10 +9,13 @@
 //
 // Layout. A group's columns lie on `lanes` threads (a power of two), U units of 4 columns each, a row's groups on neighbouring
 // threads, so a row is read once and stays in registers through both norms; sums go through shuffles and, beyond a warp, one
-// barrier. Resident blocks walk the rows; the weights' gradients grow in shared memory, where every place has one thread, to
+// barrier. Blocks walk the rows, of the backward as many as reside, of the forward 2048 threads an SM, of which registers let a quarter
+// (float32) to three eighths reside, so that its last blocks come late. The weights' gradients grow in shared memory, where every place has one thread, to
 // a row of partial sums for each block, which a second kernel adds in order. The floor is HBM. Measured: 16384 x 4096 bf16 with every
-// part, both directions, 454 us of 198 (the backward issues in 57 % of the cycles, 60 instructions an element at 25 % of the warps, which its
-// rows' registers leave; 3.1 TB/s under the profiler); 16001 x 16 heads of 120, 171 us of 54 (8 of a head's 32 lanes have no columns).
+// part, both directions, 454 us of 198 (the backward issues in 57 % of the cycles, 60 instructions an element, among them 8-byte loads and
+// stores, weights read for every row and sums in shared memory, at 25 % of the warps, which its rows' registers leave; 3.1 TB/s under the
+// profiler); 16001 x 16 heads of 120, 171 us of 54 (instructions too: of a head's 32 places of 4 columns 2 are idle). float32 rows' backward
+// with four places a thread and a gate spills 100 to 116 bytes, with eight places both directions spill up to 204.
 #include <cuda_bf16.h>
 
 #include <algorithm>
@@ -580,8 +583,8 @@ extern "C" sdm_status sdm_block_norm(const sdm_norm_shape* shape, const void* o,
     const int64_t blocks = std::min<int64_t>((a.rows + a.rows_block - 1) / a.rows_block, 152 * (2048 / threads));
     const cudaError_t e = by_type(shape, U, [&](auto t, auto u, auto gate) {
         constexpr int N = decltype(u)::value, G = decltype(gate)::value;
-        return launch_dependent(threads <= 256 ? norm_fwd_kernel<decltype(t), N, G, N == 8 ? kNormThreads : 256> : norm_fwd_kernel<decltype(t), N, G, kNormThreads>, dim3(static_cast<unsigned>(blocks)), dim3(threads), 0,
-                                reinterpret_cast<cudaStream_t>(stream), a);
+        auto* const k = threads <= 256 ? norm_fwd_kernel<decltype(t), N, G, N == 8 ? kNormThreads : 256> : norm_fwd_kernel<decltype(t), N, G, kNormThreads>;
+        return launch_dependent(k, dim3(static_cast<unsigned>(blocks)), dim3(threads), 0, reinterpret_cast<cudaStream_t>(stream), a);
     });
     return e == cudaSuccess ? SDM_OK : SDM_ERR_CUDA;
 }

@@ -1,5 +1,5 @@
-// sdm_operators.cuh -- what the kernels of the operators around the memory share (sdm_glr.cu, sdm_rope.cu, sdm_logprob.cu):
-// their launches, plain loads, pairs of float32 and the parts of a cluster. The memory's own kernels include none of it, so
+// sdm_operators.cuh -- what the kernels of the operators around the memory share (sdm_glr.cu, sdm_rope.cu, sdm_logprob.cu, sdm_gdr.cu,
+// sdm_gdr_bwd.cu, sdm_norm.cu, sdm_embed.cu): their launches, plain loads, pairs of float32 and the parts of a cluster. The memory's own kernels include none of it, so
 // that captured figures of theirs stay tied to their sources alone.
 #pragma once
 
